@@ -13,6 +13,13 @@ CUDA kernels; there is no CPU path. If the shared library has not been built
     o, lse = fa_decode(q_new, k_cache, v_cache, scale)   # q_new: [B,H,Nq<=16,d]
     o, lse = fa_fwd(q, k, v, causal=True)            # causal self-attention
     o, lse = fa_fwd_varlen(q, k, v, cu_seqlens, max_seqlen)   # packed [total,H,d]
+
+Serving from a paged cache (k_pages, v_pages: [pages, Hkv, page_size, d]):
+
+    cos, sin = fa_rope_tables(max_positions, rot_dim, device="cuda")
+    q = fa_kv_append(k, v, k_pages, v_pages, block_tables, seq_lens, cu_seqlens, q=q, cos=cos, sin=sin)
+    o, lse = fa_decode_paged(q, k_pages, v_pages, block_tables, seq_lens)       # q: [B,Hq,Nq,d]
+    o, lse = fa_decode_shared(q, k_pages, v_pages, prefix_pages, prefix_len, block_tables, seq_lens)
 """
 from __future__ import annotations
 
@@ -27,6 +34,8 @@ __all__ = [
     "fa_fwd", "fa_bwd", "fa_bwd_stage", "fa_bwd_plan", "fa_fwd_varlen", "fa_bwd_varlen",
     "fa_bwd_varlen_workspace_bytes", "FA_CAUSAL", "fa_bwd_workspace_bytes", "fa_softmax_rows", "fa_decode",
     "fa_decode_workspace_bytes", "fa_decode_plan", "fa_check_device_status",
+    "fa_rope_tables", "fa_kv_append", "fa_decode_paged", "fa_decode_paged_workspace_bytes",
+    "fa_decode_shared", "fa_decode_shared_workspace_bytes",
     "fa_debug_timeout_probe", "fa_status_string", "fa_version", "library_path", "load_library",
     "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "FA_ERR_TIMEOUT",
     "FA_F32", "FA_BF16", "FAError", "FA_BWD_PREPROCESS", "FA_BWD_MAIN", "FA_BWD_DQ_CONVERT",
@@ -36,6 +45,7 @@ FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = ran
 FA_F32, FA_BF16 = 0, 1
 FA_BWD_PREPROCESS, FA_BWD_MAIN, FA_BWD_DQ_CONVERT = 0, 1, 2
 FA_CAUSAL = 1
+FA_ROPE_INTERLEAVED = 2
 _STAGE_FLAGS = {FA_BWD_PREPROCESS: 1 << 8, FA_BWD_MAIN: 2 << 8, FA_BWD_DQ_CONVERT: 4 << 8}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -43,6 +53,17 @@ _LIB_PATH = os.path.join(_HERE, "libfa_gb300.so")
 _lib = None
 
 _vp, _ci, _cf, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_ll = ctypes.c_longlong
+
+
+class _PagedKV(ctypes.Structure):
+    """fa_paged_kv of include/fa.h."""
+    _fields_ = [("k", _vp), ("v", _vp), ("num_pages", _ci), ("kv_heads", _ci), ("page_size", _ci),
+                ("d", _ci), ("k_page_stride", _ll), ("k_head_stride", _ll), ("k_row_stride", _ll),
+                ("v_page_stride", _ll), ("v_head_stride", _ll), ("v_row_stride", _ll)]
+
+
+_pkv, _strides = ctypes.POINTER(_PagedKV), ctypes.POINTER(_ll)
 _SIGNATURES = {
     "fa_fwd": (_ci, [_vp, _vp, _vp, _vp, _vp, _ci, _ci, _ci, _ci, _cf, _ci, _vp]),
     "fa_fwd_ex": (_ci, [_vp, _vp, _vp, _vp, _vp, _ci, _ci, _ci, _ci, _cf, _ci, _ci, _vp]),
@@ -62,6 +83,14 @@ _SIGNATURES = {
     "fa_decode": (_ci, [_vp] * 6 + [_sz, _ci, _ci, _ci, _ci, _ci, _cf, _ci, _vp]),
     "fa_decode_workspace_bytes": (_sz, [_ci, _ci, _ci, _ci, _ci, _ci]),
     "fa_decode_plan": (_ci, [_ci, _ci, _ci, _ci, _ci, _ci, ctypes.POINTER(_ci), ctypes.POINTER(_ci)]),
+    "fa_kv_append": (_ci, [_vp, _vp, _ll, _ll, _vp, _vp, _ll, _ll, _ci, _pkv, _vp, _ci, _vp, _vp, _ci, _ci,
+                           _vp, _vp, _ci, _ci, _vp, _ci, _ci, _vp]),
+    "fa_decode_paged": (_ci, [_vp, _strides, _pkv, _vp, _ci, _vp, _vp, _strides, _vp, _vp, _sz, _ci, _ci, _ci,
+                              _cf, _ci, _vp]),
+    "fa_decode_paged_workspace_bytes": (_sz, [_ci, _ci, _ci, _ci, _ci, _ci]),
+    "fa_decode_shared": (_ci, [_vp, _strides, _pkv, _vp, _ci, _vp, _ci, _vp, _vp, _strides, _vp, _vp, _sz, _ci,
+                               _ci, _ci, _cf, _ci, _vp]),
+    "fa_decode_shared_workspace_bytes": (_sz, [_ci, _ci, _ci, _ci, _ci, _ci, _ci]),
     "fa_check_device_status": (_ci, [_vp]),
     "fa_debug_timeout_probe": (_ci, [ctypes.c_longlong, _vp]),
     "fa_debug_fwd_skip_load": (_ci, [_vp] * 5 + [_ci, _ci, _ci, _ci, _cf, _ci, ctypes.c_longlong, _vp]),
@@ -386,6 +415,201 @@ def fa_decode(q, k, v, scale: float | None = None, out=None, lse=None, workspace
                            B, H, Nq, Nk, d, scale, _dtype_code(q), _stream_ptr(q.device))
     _raise(rc, "fa_decode")
     return o, lse
+
+
+def fa_rope_tables(max_positions: int, rot_dim: int, base: float = 10000.0, device=None):
+    """Cosines and sines (float32 [max_positions, rot_dim / 2]) of the angles
+    p * base^(-2i / rot_dim), computed in float64 (far positions) and rounded once."""
+    if rot_dim < 2 or rot_dim % 2 != 0 or max_positions < 1:
+        raise ValueError("rot_dim must be even and positive, max_positions positive")
+    f = float(base) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    a = torch.arange(max_positions, dtype=torch.float64, device=device)[:, None] * f
+    return a.cos().float(), a.sin().float()
+
+
+def _check_on(t, name: str, device, dtype):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (this library has no CPU path)")
+    if t.device != device or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} on {device}")
+
+
+def _paged_cache(k_pages, v_pages, block_tables, seq_lens):
+    """Checks a paged cache and its tables; returns (struct, B, max_pages, Hkv, d, device)."""
+    if not isinstance(k_pages, torch.Tensor):
+        raise TypeError("k_pages must be a torch.Tensor")
+    dev = k_pages.device
+    _check_on(k_pages, "k_pages", dev, torch.bfloat16)
+    _check_on(v_pages, "v_pages", dev, torch.bfloat16)
+    _check_on(block_tables, "block_tables", dev, torch.int32)
+    _check_on(seq_lens, "seq_lens", dev, torch.int32)
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must both be [pages, Hkv, page_size, d]")
+    ks, vs = k_pages.stride(), v_pages.stride()
+    if ks[3] != 1 or vs[3] != 1:
+        raise ValueError("the last dimension of k_pages and v_pages must be contiguous")
+    if block_tables.dim() != 2 or not block_tables.is_contiguous():
+        raise ValueError("block_tables must be a contiguous int32 [B, max_pages]")
+    if seq_lens.dim() != 1 or not seq_lens.is_contiguous() or seq_lens.shape[0] != block_tables.shape[0]:
+        raise ValueError("seq_lens must be a contiguous int32 [B]")
+    pages, hkv, page, d = k_pages.shape
+    c = _PagedKV(k_pages.data_ptr(), v_pages.data_ptr(), pages, hkv, page, d, ks[0], ks[1], ks[2], vs[0], vs[1],
+                 vs[2])
+    return c, block_tables.shape[0], block_tables.shape[1], hkv, d, dev
+
+
+def _token_stride(t, name: str, heads: int | None, d: int, dev):
+    """Checks packed tokens [total, heads, d] (heads of a token contiguous); returns their stride."""
+    _check_on(t, name, dev, torch.bfloat16)
+    if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [total, heads, {d}] with the cache's head count and size")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return t.stride(0)
+
+
+def fa_kv_append(k, v, k_pages, v_pages, block_tables, seq_lens, cu_seqlens=None, q=None, cos=None, sin=None,
+                 interleaved: bool = False, positions=None, q_out=None):
+    """Append new keys and values to a paged cache, rotating the keys (and q) by their position.
+
+    k, v: [total, Hkv, d] bf16 packed new tokens (a slice of a fused projection
+    will do); q: [total, Hq, d] or None. cu_seqlens: int32 [B+1] offsets of the
+    sequences' new tokens (None: total / B tokens each). seq_lens: int32 [B]
+    lengths after this append. cos, sin: float32 [max_positions, rot_dim / 2]
+    (None: no rotation). positions: int32 [total] rotary positions (None: the
+    key's index in the cache). k_pages and v_pages are written in place.
+    Returns the rotated queries (``q_out``, dense unless given), or None without q.
+    """
+    lib = load_library()
+    cache, B, max_pages, hkv, d, dev = _paged_cache(k_pages, v_pages, block_tables, seq_lens)
+    ks, vs = _token_stride(k, "k", hkv, d, dev), _token_stride(v, "v", hkv, d, dev)
+    total = k.shape[0]
+    if v.shape[0] != total:
+        raise ValueError("k and v must hold the same tokens")
+    hq = qs = os_ = 0
+    if q is not None:
+        hq, qs = q.shape[1] if q.dim() == 3 else 0, _token_stride(q, "q", None, d, dev)
+        if q.shape[0] != total:
+            raise ValueError("q and k must hold the same tokens")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        os_ = _token_stride(q_out, "q_out", hq, d, dev)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+    elif q_out is not None:
+        raise ValueError("q_out given without q")
+    if cu_seqlens is not None:
+        _check_on(cu_seqlens, "cu_seqlens", dev, torch.int32)
+        if cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() or cu_seqlens.shape[0] != B + 1:
+            raise ValueError("cu_seqlens must be a contiguous int32 [B+1]")
+    rot = max_pos = 0
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    if cos is not None:
+        for t, n in ((cos, "cos"), (sin, "sin")):
+            _check_on(t, n, dev, torch.float32)
+            if t.dim() != 2 or not t.is_contiguous() or t.shape != cos.shape:
+                raise ValueError(f"{n} must be a contiguous float32 [max_positions, rot_dim / 2]")
+        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+    if positions is not None:
+        _check_on(positions, "positions", dev, torch.int32)
+        if positions.dim() != 1 or not positions.is_contiguous() or positions.shape[0] != total:
+            raise ValueError("positions must be a contiguous int32 [total]")
+    if total == 0:
+        return q_out
+    ptr = lambda t: None if t is None else t.data_ptr()
+    with torch.cuda.device(dev):
+        rc = lib.fa_kv_append(k.data_ptr(), v.data_ptr(), ks, vs, ptr(q), ptr(q_out), qs, os_, hq,
+                              ctypes.byref(cache), block_tables.data_ptr(), max_pages, seq_lens.data_ptr(),
+                              ptr(cu_seqlens), B, total, ptr(cos), ptr(sin), rot, max_pos, ptr(positions),
+                              FA_ROPE_INTERLEAVED if interleaved else 0, FA_BF16, _stream_ptr(dev))
+    _raise(rc, "fa_kv_append")
+    return q_out
+
+
+def fa_decode_paged_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, d: int) -> int:
+    """Scratch bytes fa_decode_paged needs on the current device."""
+    return int(load_library().fa_decode_paged_workspace_bytes(B, Hq, Hkv, Nq, d, FA_BF16))
+
+
+def fa_decode_shared_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, prefix_len: int, d: int) -> int:
+    """Scratch bytes fa_decode_shared needs on the current device."""
+    return int(load_library().fa_decode_shared_workspace_bytes(B, Hq, Hkv, Nq, prefix_len, d, FA_BF16))
+
+
+def _decode_cache(where, q, k_pages, v_pages, prefix_pages, prefix_len, block_tables, seq_lens, scale, out, lse,
+                  workspace):
+    lib = load_library()
+    cache, B, max_pages, hkv, d, dev = _paged_cache(k_pages, v_pages, block_tables, seq_lens)
+    _check_on(q, "q", dev, torch.bfloat16)
+    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != d or q.shape[1] % hkv != 0 or q.stride(3) != 1:
+        raise ValueError("q must be [B, Hq, Nq, d] with the tables' B, the cache's d, Hq a multiple of its heads, "
+                         "and d contiguous")
+    _, hq, nq, _ = q.shape
+    o = torch.empty(q.shape, dtype=q.dtype, device=dev) if out is None else out
+    if out is not None:
+        _check_on(o, "out", dev, torch.bfloat16)
+        if o.shape != q.shape or o.stride(3) != 1:
+            raise ValueError("out must match q in shape, with d contiguous")
+    if lse is None:
+        lse = torch.empty((B, hq, nq), dtype=torch.float32, device=dev)
+    else:
+        _check_on(lse, "lse", dev, torch.float32)
+        if lse.shape != (B, hq, nq) or not lse.is_contiguous():
+            raise ValueError("lse must be contiguous float32 [B, Hq, Nq]")
+    if prefix_pages is not None:
+        _check_on(prefix_pages, "prefix_pages", dev, torch.int32)
+        if prefix_pages.dim() != 1 or not prefix_pages.is_contiguous():
+            raise ValueError("prefix_pages must be a contiguous int32 [pages]")
+        if prefix_pages.shape[0] * k_pages.shape[2] < prefix_len:
+            raise ValueError("prefix_pages holds fewer than prefix_len keys")
+    with torch.cuda.device(dev):
+        if workspace is None:
+            n = lib.fa_decode_shared_workspace_bytes(B, hq, hkv, nq, prefix_len, d, FA_BF16)
+            workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+        elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on q's device")
+        rc = lib.fa_decode_shared(q.data_ptr(), (_ll * 3)(*q.stride()[:3]), ctypes.byref(cache),
+                                  prefix_pages.data_ptr() if prefix_len > 0 else None, prefix_len,
+                                  block_tables.data_ptr(), max_pages, seq_lens.data_ptr(), o.data_ptr(),
+                                  (_ll * 3)(*o.stride()[:3]), lse.data_ptr(), workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), B, hq, nq, scale, FA_BF16,
+                                  _stream_ptr(dev))
+    _raise(rc, where)
+    return o, lse
+
+
+def fa_decode_paged(q, k_pages, v_pages, block_tables, seq_lens, scale: float | None = None, out=None, lse=None,
+                    workspace=None):
+    """Decode against a paged cache: the Nq newest tokens of each sequence over its seq_lens[b] keys.
+
+    q: [B, Hq, Nq, d] bf16, any strides with d contiguous (Hq / Hkv * Nq <= 64);
+    k_pages, v_pages: [pages, Hkv, page_size, d] bf16, any strides with d
+    contiguous; block_tables int32 [B, max_pages]; seq_lens int32 [B]. Query i
+    sees keys j < seq_lens[b] - Nq + 1 + i; one that sees none gets O = 0 and
+    LSE = -inf. Returns (O like q, LSE [B, Hq, Nq] float32).
+    """
+    scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else float(scale)
+    return _decode_cache("fa_decode_paged", q, k_pages, v_pages, None, 0, block_tables, seq_lens, scale, out, lse,
+                         workspace)
+
+
+def fa_decode_shared(q, k_pages, v_pages, prefix_pages, prefix_len: int, block_tables, seq_lens,
+                     scale: float | None = None, out=None, lse=None, workspace=None):
+    """``fa_decode_paged`` for a batch whose sequences all continue one prefix.
+
+    prefix_pages: int32 [ceil(prefix_len / page_size)] pages of the prefix, read
+    once for the whole batch; block_tables and seq_lens describe the sequences'
+    own keys, which follow the prefix. Returns (O like q, LSE [B, Hq, Nq] float32).
+    """
+    scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else float(scale)
+    prefix_len = int(prefix_len)
+    if prefix_len > 0 and prefix_pages is None:
+        raise ValueError("prefix_pages is missing")
+    return _decode_cache("fa_decode_shared", q, k_pages, v_pages, prefix_pages, prefix_len, block_tables, seq_lens,
+                         scale, out, lse, workspace)
 
 
 def fa_check_device_status(device=None) -> int:

@@ -32,6 +32,9 @@ SOURCES = [
     ("fa_noalloc.cu", []),
     ("softmax_rows.cu", []),
     ("decode_splitkv.cu", []),
+    ("fa_paged_api.cu", []),
+    ("paged_append.cu", []),
+    ("paged_decode.cu", []),
 ]
 
 

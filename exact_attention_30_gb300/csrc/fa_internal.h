@@ -191,6 +191,53 @@ DecodePlan plan_decode_for_slots(int BH, int Nk, int slots, int tile);
 int decode_tile_keys(int Nq);
 cudaError_t launch_decode_bf16(const DecodeArgs& a, int d, cudaStream_t st);
 
+// ---- paged key/value cache (paged_append.cu, paged_decode.cu) ----
+// The pool of include/fa.h's fa_paged_kv, strides in elements.
+struct PagedPool {
+  void* k;
+  void* v;
+  long long k_page, k_head, k_row;
+  long long v_page, v_head, v_row;
+  int num_pages, kv_heads, page_size;
+};
+
+struct AppendArgs {
+  const void* K;
+  const void* V;
+  const void* Q;   // nullptr: keys and values only
+  void* Qout;
+  long long k_stride, v_stride, q_stride, qout_stride;  // elements between tokens
+  PagedPool pool;
+  const int* block_tables;  // [B, max_pages]
+  const int* seq_lens;      // [B], after the append
+  const int* cu_seqlens;    // [B + 1] or nullptr: total / B tokens each
+  const float* cos;         // [max_positions, rot_dim / 2]
+  const float* sin;
+  const int* positions;     // [total] or nullptr: the key index
+  int B, Hq, total, max_pages, rot_dim, max_positions;
+  int interleaved;
+  int* status;
+};
+cudaError_t launch_append_bf16(const AppendArgs& a, int d, cudaStream_t st);
+
+struct PagedDecodeArgs {
+  const void* Q;                   // bf16, element strides of batch, head, row below
+  void* O;
+  long long q_b, q_h, q_r, o_b, o_h, o_r;
+  float* LSE;                      // [B, Hq, Nq], natural log
+  PagedPool pool;
+  const int* block_tables;         // [B, max_pages]
+  const int* seq_lens;             // [B] own keys of each sequence
+  const int* prefix_pages;         // pages every sequence's keys begin with
+  int prefix_len;                  // keys of the shared prefix (0: none)
+  int B, G, Nq, max_pages;         // G query heads per K/V head
+  float scale_log2;                // scale * log2(e)
+  int* status;
+  unsigned long long wait_limit_ns;
+};
+constexpr int kPagedMaxRows = 64;  // G * Nq
+cudaError_t launch_decode_paged_bf16(const PagedDecodeArgs& a, int d, cudaStream_t st);
+
 // Causal grids: (heads of a group, blocks, groups). Within a group of heads
 // the CTAs run longest first; groups run one after the other, each small
 // enough that what its heads' CTAs all stream stays in L2 (bytes_per_head;

@@ -1,0 +1,206 @@
+// fa_paged_api.cu -- the C ABI of the paged key/value cache operators
+// (fa_kv_append, fa_decode_paged, fa_decode_shared): argument validation and
+// launch. Host code only.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/fa.h"
+#include "fa_internal.h"
+
+using namespace fa;
+
+namespace {
+
+constexpr int kMaxPageSize = 65536;
+constexpr int kMaxKeys = 1 << 30;
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// A stride of an axis of `extent` entries: a multiple of 8 elements (16-byte
+// vectors) of at least `min` elements. An axis of one entry has no stride.
+bool stride_ok(long long stride, int extent, long long min) {
+  return extent == 1 || (stride >= min && stride % 8 == 0 && stride <= (1ll << 38));
+}
+
+fa_status check_pool(const fa_paged_kv* c, fa_dtype dt, PagedPool* out) {
+  if (!c || !c->k || !c->v) return FA_ERR_INVALID_ARG;
+  if (dt != FA_F32 && dt != FA_BF16) return FA_ERR_INVALID_ARG;
+  if (c->num_pages < 1 || c->kv_heads < 1 || c->page_size < 1 || c->d < 1) return FA_ERR_INVALID_ARG;
+  if (dt != FA_BF16 || (c->d != 64 && c->d != 128)) return FA_ERR_UNSUPPORTED;
+  if (c->page_size % 8 != 0 || c->page_size > kMaxPageSize) return FA_ERR_UNSUPPORTED;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16)) return FA_ERR_INVALID_ARG;
+  if (!stride_ok(c->k_page_stride, c->num_pages, c->d) || !stride_ok(c->k_head_stride, c->kv_heads, c->d) ||
+      !stride_ok(c->k_row_stride, c->page_size, c->d) || !stride_ok(c->v_page_stride, c->num_pages, c->d) ||
+      !stride_ok(c->v_head_stride, c->kv_heads, c->d) || !stride_ok(c->v_row_stride, c->page_size, c->d))
+    return FA_ERR_INVALID_ARG;
+  // an axis of one entry gets a stride that a tensor map accepts
+  auto st = [&](long long s, int extent) { return extent == 1 ? (long long)c->d : s; };
+  PagedPool p{};
+  p.k = c->k;
+  p.v = c->v;
+  p.k_page = st(c->k_page_stride, c->num_pages);
+  p.k_head = st(c->k_head_stride, c->kv_heads);
+  p.k_row = c->k_row_stride;
+  p.v_page = st(c->v_page_stride, c->num_pages);
+  p.v_head = st(c->v_head_stride, c->kv_heads);
+  p.v_row = c->v_row_stride;
+  p.num_pages = c->num_pages;
+  p.kv_heads = c->kv_heads;
+  p.page_size = c->page_size;
+  *out = p;
+  return FA_OK;
+}
+
+fa_status check_decode(int B, int Hq, int Hkv, int Nq, int d, fa_dtype dt) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Nq < 1 || d < 1 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
+  if (dt != FA_F32 && dt != FA_BF16) return FA_ERR_INVALID_ARG;
+  if (dt != FA_BF16 || (d != 64 && d != 128)) return FA_ERR_UNSUPPORTED;
+  if ((long long)(Hq / Hkv) * Nq > kPagedMaxRows) return FA_ERR_UNSUPPORTED;
+  if ((long long)B * Hkv > (1 << 24)) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+// Strides of a [B, H, N, d] view (NULL: dense).
+bool view_strides(const long long* s, int B, int H, int N, int d, long long* sb, long long* sh, long long* sr) {
+  if (!s) {
+    *sr = d;
+    *sh = (long long)N * d;
+    *sb = (long long)H * N * d;
+    return true;
+  }
+  if (!stride_ok(s[0], B, d) || !stride_ok(s[1], H, d) || !stride_ok(s[2], N, d)) return false;
+  *sb = B == 1 ? 0 : s[0];
+  *sh = H == 1 ? 0 : s[1];
+  *sr = N == 1 ? 0 : s[2];
+  return true;
+}
+
+fa_status decode_impl(const void* Q, const long long* q_strides, const fa_paged_kv* cache,
+                      const int* prefix_pages, int prefix_len, const int* block_tables, int max_pages,
+                      const int* seq_lens, void* O, const long long* o_strides, float* LSE,
+                      void* workspace, size_t workspace_bytes, int B, int Hq, int Nq, float scale,
+                      fa_dtype dt, void* stream) {
+  PagedDecodeArgs a;
+  std::memset(&a, 0, sizeof(a));
+  fa_status s = check_pool(cache, dt, &a.pool);
+  if (s != FA_OK) return s;
+  s = check_decode(B, Hq, cache->kv_heads, Nq, cache->d, dt);
+  if (s != FA_OK) return s;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
+  if (!Q || !O || !LSE || !block_tables || !seq_lens || !workspace || max_pages < 1) return FA_ERR_INVALID_ARG;
+  if (prefix_len < 0 || prefix_len > kMaxKeys || (prefix_len > 0 && !prefix_pages)) return FA_ERR_INVALID_ARG;
+  if (!aligned(Q, 16) || !aligned(O, 16) || !aligned(LSE, 4) || !aligned(block_tables, 4) ||
+      !aligned(seq_lens, 4) || !aligned(prefix_pages, 4) || !aligned(workspace, 256))
+    return FA_ERR_INVALID_ARG;
+  if (!view_strides(q_strides, B, Hq, Nq, cache->d, &a.q_b, &a.q_h, &a.q_r) ||
+      !view_strides(o_strides, B, Hq, Nq, cache->d, &a.o_b, &a.o_h, &a.o_r))
+    return FA_ERR_INVALID_ARG;
+  if (workspace_bytes < fa_decode_shared_workspace_bytes(B, Hq, cache->kv_heads, Nq, prefix_len, cache->d, dt))
+    return FA_ERR_INVALID_ARG;
+  a.status = device_status_ptr();
+  if (!a.status) return FA_ERR_CUDA;
+  a.Q = Q;
+  a.O = O;
+  a.LSE = LSE;
+  a.block_tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.prefix_pages = prefix_pages;
+  a.prefix_len = prefix_len;
+  a.B = B;
+  a.G = Hq / cache->kv_heads;
+  a.Nq = Nq;
+  a.max_pages = max_pages;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.wait_limit_ns = kDefaultWaitLimitNs;
+  return launch_decode_paged_bf16(a, cache->d, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK
+                                                                                                  : FA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_kv_append(const void* K, const void* V, long long k_stride, long long v_stride, const void* Q,
+                       void* Qout, long long q_stride, long long qout_stride, int Hq,
+                       const fa_paged_kv* cache, const int* block_tables, int max_pages,
+                       const int* seq_lens, const int* cu_seqlens, int B, int total, const float* cos,
+                       const float* sin, int rot_dim, int max_positions, const int* positions, int flags,
+                       fa_dtype dt, void* stream) {
+  AppendArgs a;
+  std::memset(&a, 0, sizeof(a));
+  const fa_status s = check_pool(cache, dt, &a.pool);
+  if (s != FA_OK) return s;
+  const int d = cache->d;
+  if (flags & ~FA_ROPE_INTERLEAVED) return FA_ERR_INVALID_ARG;
+  if (B < 1 || total < 1 || max_pages < 1 || Hq < 0 || (Q == nullptr) != (Hq == 0) ||
+      (Qout == nullptr) != (Hq == 0))
+    return FA_ERR_INVALID_ARG;
+  if (!K || !V || !block_tables || !seq_lens || (!cu_seqlens && total % B != 0)) return FA_ERR_INVALID_ARG;
+  if (rot_dim < 0 || rot_dim > d) return FA_ERR_INVALID_ARG;
+  if (rot_dim % 16 != 0) return FA_ERR_UNSUPPORTED;
+  if (rot_dim > 0 && (!cos || !sin || max_positions < 1)) return FA_ERR_INVALID_ARG;
+  if (!aligned(K, 16) || !aligned(V, 16) || !aligned(Q, 16) || !aligned(Qout, 16) ||
+      !aligned(cos, 16) || !aligned(sin, 16) || !aligned(block_tables, 4) || !aligned(seq_lens, 4) ||
+      !aligned(cu_seqlens, 4) || !aligned(positions, 4))
+    return FA_ERR_INVALID_ARG;
+  const long long kv_row = (long long)cache->kv_heads * d, q_row = (long long)Hq * d;
+  if (!stride_ok(k_stride, total, kv_row) || !stride_ok(v_stride, total, kv_row)) return FA_ERR_INVALID_ARG;
+  if (Hq > 0 && (!stride_ok(q_stride, total, q_row) || !stride_ok(qout_stride, total, q_row)))
+    return FA_ERR_INVALID_ARG;
+  if (Q != nullptr && Q == Qout && total > 1 && q_stride != qout_stride) return FA_ERR_INVALID_ARG;
+  a.status = device_status_ptr();
+  if (!a.status) return FA_ERR_CUDA;
+  a.K = K;
+  a.V = V;
+  a.Q = Q;
+  a.Qout = Qout;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_stride = q_stride;
+  a.qout_stride = qout_stride;
+  a.block_tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.cu_seqlens = cu_seqlens;
+  a.cos = cos;
+  a.sin = sin;
+  a.positions = positions;
+  a.B = B;
+  a.Hq = Hq;
+  a.total = total;
+  a.max_pages = max_pages;
+  a.rot_dim = rot_dim;
+  a.max_positions = max_positions;
+  a.interleaved = (flags & FA_ROPE_INTERLEAVED) != 0;
+  return launch_append_bf16(a, d, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int Nq, int prefix_len, int d, fa_dtype dt) {
+  if (check_decode(B, Hq, Hkv, Nq, d, dt) != FA_OK || prefix_len < 0 || prefix_len > kMaxKeys) return 0;
+  return 256;
+}
+
+size_t fa_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, fa_dtype dt) {
+  return fa_decode_shared_workspace_bytes(B, Hq, Hkv, Nq, 0, d, dt);
+}
+
+fa_status fa_decode_paged(const void* Q, const long long* q_strides, const fa_paged_kv* cache,
+                          const int* block_tables, int max_pages, const int* seq_lens, void* O,
+                          const long long* o_strides, float* LSE, void* workspace, size_t workspace_bytes,
+                          int B, int Hq, int Nq, float scale, fa_dtype dt, void* stream) {
+  return decode_impl(Q, q_strides, cache, nullptr, 0, block_tables, max_pages, seq_lens, O, o_strides, LSE,
+                     workspace, workspace_bytes, B, Hq, Nq, scale, dt, stream);
+}
+
+fa_status fa_decode_shared(const void* Q, const long long* q_strides, const fa_paged_kv* cache,
+                           const int* prefix_pages, int prefix_len, const int* block_tables, int max_pages,
+                           const int* seq_lens, void* O, const long long* o_strides, float* LSE,
+                           void* workspace, size_t workspace_bytes, int B, int Hq, int Nq, float scale,
+                           fa_dtype dt, void* stream) {
+  return decode_impl(Q, q_strides, cache, prefix_pages, prefix_len, block_tables, max_pages, seq_lens, O,
+                     o_strides, LSE, workspace, workspace_bytes, B, Hq, Nq, scale, dt, stream);
+}
+
+}  // extern "C"

@@ -310,6 +310,143 @@ fa_status fa_decode_plan(int B, int H, int Nq, int Nk, int d, int resident_ctas,
                          int* keys_per_split);
 
 /*
+ * Paged key/value cache: a pool of pages, each holding `page_size` keys (and
+ * values) of every K/V head. Element e of row r of head h of page p of the
+ * keys is k[p * k_page_stride + h * k_head_stride + r * k_row_stride + e],
+ * the values likewise, so both orders of a page (heads of rows, rows of
+ * heads) and views of a larger tensor are covered. The struct lives on the
+ * host and is read during the call only.
+ *   k, v      : DEVICE bf16, 16-byte aligned, not aliased with each other.
+ *   page_size : a multiple of 8 in [8, 65536].
+ *   d         : 64 or 128, contiguous.
+ *   strides   : in elements, multiples of 8, >= d (of an axis of extent 1:
+ *               ignored); distinct (page, head, row) must not overlap.
+ * A sequence b owns the pages block_tables[b * max_pages ..]: its key j is row
+ * j mod page_size of page block_tables[b * max_pages + j / page_size]. Entries
+ * past a sequence's last page are never read. block_tables and seq_lens are
+ * DEVICE int32 arrays, so that a captured graph follows their contents. The
+ * kernels check what they read there: a sequence with a negative length, a
+ * length beyond max_pages pages, or a page outside [0, num_pages) makes
+ * fa_check_device_status return FA_ERR_INVALID_ARG; nothing outside the pool
+ * is read or written, and that sequence's results are undefined.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  int num_pages, kv_heads, page_size, d;
+  long long k_page_stride, k_head_stride, k_row_stride;
+  long long v_page_stride, v_head_stride, v_row_stride;
+} fa_paged_kv;
+
+/* Flag of fa_kv_append: rotate the pairs (2i, 2i+1) instead of (i, i + rot_dim/2). */
+#define FA_ROPE_INTERLEAVED 2
+
+/*
+ * Append the new tokens of a batch to a paged cache, the keys (and, if given,
+ * the queries) rotated by their position on the way. A rotated pair (a, b) at
+ * position p becomes
+ *     (a cos[p][i] - b sin[p][i],  a sin[p][i] + b cos[p][i])
+ * for the pairs i < rot_dim / 2 of each head; elements from rot_dim on, and
+ * all values, are copied. The arithmetic is fp32, rounded once to bf16.
+ *   K, V      : new keys and values, packed tokens [total, Hkv, d] bf16, the
+ *               heads of a token contiguous, tokens k_stride / v_stride
+ *               elements apart (a slice of a fused projection will do).
+ *   Q, Qout   : queries [total, Hq, d] (tokens q_stride apart) and their
+ *               rotated copy (tokens qout_stride apart; may be Q itself with
+ *               the same stride); both NULL and Hq = 0: keys and values only.
+ *   cu_seqlens: DEVICE int32 [B+1]: sequence b's new tokens are the packed
+ *               tokens cu_seqlens[b] .. cu_seqlens[b+1]-1. Packed tokens from
+ *               cu_seqlens[B] on are padding: nothing of them is read or
+ *               written. NULL: every sequence has total / B (exactly) tokens.
+ *   seq_lens  : the sequences' lengths AFTER this append (what the attention
+ *               calls then take): new token i of n goes to key
+ *               seq_lens[b] - n + i. seq_lens[b] = 0 marks a padding
+ *               sequence: its tokens are skipped.
+ *   cos, sin  : DEVICE fp32 [max_positions, rot_dim / 2]; rot_dim = 0 (and
+ *               NULL): no rotation, Qout is a copy of Q.
+ *   positions : DEVICE int32 [total] rotary positions of the packed tokens;
+ *               NULL: the token's key index in the cache.
+ *   rot_dim   : a multiple of 16, 0 <= rot_dim <= d.
+ * No two new tokens may name the same (page, row); which of them such a row
+ * would hold, element by element, is undefined. K, V, Q, Qout 16-byte
+ * aligned; strides multiples of 8 and >= heads * d; cos, sin 16-byte aligned.
+ * On the device: a token whose key index is negative or past max_pages pages,
+ * whose page is outside the pool or whose position is outside
+ * [0, max_positions) is skipped (its Qout row too) and reported like a bad
+ * length above; so are inconsistent cu_seqlens (a sequence's offsets not
+ * within 0 <= cu[b] <= cu[b+1] <= total).
+ * Errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED (FA_F32, d, rot_dim,
+ * page_size), FA_ERR_CUDA.
+ */
+fa_status fa_kv_append(const void* K, const void* V, long long k_stride, long long v_stride,
+                       const void* Q, void* Qout, long long q_stride, long long qout_stride, int Hq,
+                       const fa_paged_kv* cache, const int* block_tables, int max_pages,
+                       const int* seq_lens, const int* cu_seqlens, int B, int total,
+                       const float* cos, const float* sin, int rot_dim, int max_positions,
+                       const int* positions, int flags, fa_dtype dt, void* stream);
+
+/*
+ * Decode against a paged cache: attention of the Nq newest tokens of each
+ * sequence, whose keys are already in the cache (fa_kv_append), over that
+ * sequence's seq_lens[b] keys. Query i of the Nq sees the keys
+ * j < seq_lens[b] - Nq + 1 + i: its own and all before it (Nq = 1: all).
+ * A query that sees no key (seq_lens[b] = 0, or fewer keys than new tokens)
+ * gets O = 0 and LSE = -inf. What stands in the pages behind a sequence's
+ * last key, NaN included, and in keys and values a query does not see has no
+ * influence on its row.
+ * The query heads h * Hq/Hkv .. (h + 1) * Hq/Hkv - 1 share K/V head h, which
+ * is read once for all of them: G * Nq <= 64 rows, G = Hq / Hkv.
+ *   Q   : [B,Hq,Nq,d] bf16; q_strides: NULL (dense) or 3 HOST values, the
+ *         element strides of batch, head and row, multiples of 8 (of an axis
+ *         of extent 1: ignored); 16-byte aligned.
+ *   O   : as Q, o_strides likewise; must not overlap Q or the cache.
+ *   LSE : [B,Hq,Nq] float32, dense (natural log, as fa_fwd).
+ *   workspace : device scratch of >= fa_decode_paged_workspace_bytes() bytes,
+ *         256-byte aligned, contents on entry irrelevant, not used by another
+ *         call in flight.
+ * The keys of all sequences and heads are laid end to end and cut into equal
+ * shares, one per resident CTA, on the device: lengths may change between
+ * replays of a captured graph. Sums in fp32; results are the same on every
+ * run. 1 <= B * Hkv <= 2^24, seq_lens[b] <= 2^30.
+ * Errors: FA_ERR_INVALID_ARG (pointers, sizes, Hq not a multiple of Hkv,
+ * strides, scale, small workspace), FA_ERR_UNSUPPORTED (FA_F32, d,
+ * page_size, G * Nq > 64), FA_ERR_CUDA.
+ */
+fa_status fa_decode_paged(const void* Q, const long long* q_strides, const fa_paged_kv* cache,
+                          const int* block_tables, int max_pages, const int* seq_lens, void* O,
+                          const long long* o_strides, float* LSE, void* workspace,
+                          size_t workspace_bytes, int B, int Hq, int Nq, float scale, fa_dtype dt,
+                          void* stream);
+
+/* Scratch bytes fa_decode_paged needs on the CURRENT device; 0 on invalid arguments. */
+size_t fa_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, fa_dtype dt);
+
+/*
+ * fa_decode_paged for a batch whose sequences all continue one prefix (a
+ * system prompt, a document, the prompt of many samples): every query sees
+ * the prefix_len keys of the pages prefix_pages[0 .. ceil(prefix_len /
+ * page_size) - 1] (DEVICE int32), then its own sequence's keys as in
+ * fa_decode_paged. block_tables and seq_lens describe the sequences' OWN keys
+ * only (their key 0 follows the prefix; a prefix may end inside a page, the
+ * rest of which is not read). The prefix is read once for the whole batch and
+ * its partial result is merged with the own keys' by maximum and sum.
+ *   prefix_len : HOST value, 0 <= prefix_len <= 2^30 (0: fa_decode_paged).
+ *   workspace  : >= fa_decode_shared_workspace_bytes() bytes, as above.
+ * Limits and errors: as fa_decode_paged, plus FA_ERR_INVALID_ARG for a
+ * negative prefix_len or missing prefix_pages. A prefix page outside the pool
+ * is reported by fa_check_device_status; every row is then undefined.
+ */
+fa_status fa_decode_shared(const void* Q, const long long* q_strides, const fa_paged_kv* cache,
+                           const int* prefix_pages, int prefix_len, const int* block_tables,
+                           int max_pages, const int* seq_lens, void* O, const long long* o_strides,
+                           float* LSE, void* workspace, size_t workspace_bytes, int B, int Hq, int Nq,
+                           float scale, fa_dtype dt, void* stream);
+
+/* Scratch bytes fa_decode_shared needs on the CURRENT device; 0 on invalid arguments. */
+size_t fa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int Nq, int prefix_len, int d,
+                                        fa_dtype dt);
+
+/*
  * fa_bwd without a caller-provided workspace, for callers that cannot
  * allocate device memory (for example code running inside a host application
  * that owns all device memory through its own pool, or a serving path where
