@@ -197,6 +197,20 @@ unsigned flag_stages(int flags) {
 
 }  // namespace
 
+bool encode_pool_bf16(CUtensorMap* m, const PagedPool& pool, bool values, int d, int box_rows) {
+  if (!get_encode_fn()) return false;
+  const long long page = values ? pool.v_page : pool.k_page, head = values ? pool.v_head : pool.k_head,
+                  row = values ? pool.v_row : pool.k_row;
+  cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)pool.page_size, (cuuint64_t)pool.kv_heads,
+                        (cuuint64_t)pool.num_pages};
+  cuuint64_t strides[3] = {(cuuint64_t)row * 2, (cuuint64_t)head * 2, (cuuint64_t)page * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, values ? pool.v : pool.k, dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int* device_status_ptr() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;

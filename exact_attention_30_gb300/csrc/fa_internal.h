@@ -220,7 +220,12 @@ struct AppendArgs {
 };
 cudaError_t launch_append_bf16(const AppendArgs& a, int d, cudaStream_t st);
 
+// 4-D tensor map (d, rows, heads, pages) over the pool's keys or values:
+// boxes of 64 columns x box_rows rows of one page, 128-byte swizzle.
+bool encode_pool_bf16(CUtensorMap* m, const PagedPool& pool, bool values, int d, int box_rows);
+
 struct PagedDecodeArgs {
+  CUtensorMap tmK, tmV;
   const void* Q;                   // bf16, element strides of batch, head, row below
   void* O;
   long long q_b, q_h, q_r, o_b, o_h, o_r;
@@ -231,11 +236,28 @@ struct PagedDecodeArgs {
   const int* prefix_pages;         // pages every sequence's keys begin with
   int prefix_len;                  // keys of the shared prefix (0: none)
   int B, G, Nq, max_pages;         // G query heads per K/V head
+  int box_rows;                    // rows per TMA box: divides page_size and 64
+  // schedule and scratch (paged_layout)
+  int ctas;                        // grid; shares of the keys
+  int n_seq;                       // B and, behind them, the prefix once per slot_rows of its rows
+  int slot_rows;                   // rows of a partial result's slot
+  float* Opart;                    // fp32 [slots][slot_rows][d], normalised
+  float* Lpart;                    // fp32 [slots][slot_rows], base-2 log-sum-exp
+  int2* unit_ctas;                 // [n_seq * Hkv] first and last CTA of a unit
+  long long* begun;                // [ctas] the unit that a CTA begins and does not end, or -1
   float scale_log2;                // scale * log2(e)
   int* status;
   unsigned long long wait_limit_ns;
 };
 constexpr int kPagedMaxRows = 64;  // G * Nq
+constexpr int kPagedMaxKeys = 1 << 30;
+// Grid and scratch of a decode on the current device (ctas = 0 on failure);
+// rows = G * Nq. Offsets in bytes; the partial outputs come first.
+struct PagedLayout {
+  int ctas, n_seq, slot_rows;
+  size_t lpart, unit_ctas, begun, total;
+};
+PagedLayout paged_layout(int B, int Hkv, int rows, int prefix_len, int d);
 cudaError_t launch_decode_paged_bf16(const PagedDecodeArgs& a, int d, cudaStream_t st);
 
 // Causal grids: (heads of a group, blocks, groups). Within a group of heads

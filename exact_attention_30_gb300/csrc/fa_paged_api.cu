@@ -15,7 +15,6 @@ using namespace fa;
 namespace {
 
 constexpr int kMaxPageSize = 65536;
-constexpr int kMaxKeys = 1 << 30;
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -91,17 +90,32 @@ fa_status decode_impl(const void* Q, const long long* q_strides, const fa_paged_
   if (s != FA_OK) return s;
   if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
   if (!Q || !O || !LSE || !block_tables || !seq_lens || !workspace || max_pages < 1) return FA_ERR_INVALID_ARG;
-  if (prefix_len < 0 || prefix_len > kMaxKeys || (prefix_len > 0 && !prefix_pages)) return FA_ERR_INVALID_ARG;
+  if (prefix_len < 0 || prefix_len > kPagedMaxKeys || (prefix_len > 0 && !prefix_pages)) return FA_ERR_INVALID_ARG;
   if (!aligned(Q, 16) || !aligned(O, 16) || !aligned(LSE, 4) || !aligned(block_tables, 4) ||
       !aligned(seq_lens, 4) || !aligned(prefix_pages, 4) || !aligned(workspace, 256))
     return FA_ERR_INVALID_ARG;
   if (!view_strides(q_strides, B, Hq, Nq, cache->d, &a.q_b, &a.q_h, &a.q_r) ||
       !view_strides(o_strides, B, Hq, Nq, cache->d, &a.o_b, &a.o_h, &a.o_r))
     return FA_ERR_INVALID_ARG;
-  if (workspace_bytes < fa_decode_shared_workspace_bytes(B, Hq, cache->kv_heads, Nq, prefix_len, cache->d, dt))
-    return FA_ERR_INVALID_ARG;
+  const PagedLayout L = paged_layout(B, cache->kv_heads, Hq / cache->kv_heads * Nq, prefix_len, cache->d);
+  if (L.ctas < 1) return FA_ERR_CUDA;
+  if (workspace_bytes < L.total) return FA_ERR_INVALID_ARG;
   a.status = device_status_ptr();
   if (!a.status) return FA_ERR_CUDA;
+  // boxes never cross a page's end: the largest power of two (>= 8) in the page size, up to a tile
+  a.box_rows = cache->page_size & -cache->page_size;
+  if (a.box_rows > 64) a.box_rows = 64;
+  if (!encode_pool_bf16(&a.tmK, a.pool, false, cache->d, a.box_rows) ||
+      !encode_pool_bf16(&a.tmV, a.pool, true, cache->d, a.box_rows))
+    return FA_ERR_CUDA;
+  char* ws = static_cast<char*>(workspace);
+  a.ctas = L.ctas;
+  a.n_seq = L.n_seq;
+  a.slot_rows = L.slot_rows;
+  a.Opart = reinterpret_cast<float*>(ws);
+  a.Lpart = reinterpret_cast<float*>(ws + L.lpart);
+  a.unit_ctas = reinterpret_cast<int2*>(ws + L.unit_ctas);
+  a.begun = reinterpret_cast<long long*>(ws + L.begun);
   a.Q = Q;
   a.O = O;
   a.LSE = LSE;
@@ -178,8 +192,8 @@ fa_status fa_kv_append(const void* K, const void* V, long long k_stride, long lo
 }
 
 size_t fa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int Nq, int prefix_len, int d, fa_dtype dt) {
-  if (check_decode(B, Hq, Hkv, Nq, d, dt) != FA_OK || prefix_len < 0 || prefix_len > kMaxKeys) return 0;
-  return 256;
+  if (check_decode(B, Hq, Hkv, Nq, d, dt) != FA_OK || prefix_len < 0 || prefix_len > kPagedMaxKeys) return 0;
+  return paged_layout(B, Hkv, Hq / Hkv * Nq, prefix_len, d).total;
 }
 
 size_t fa_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, fa_dtype dt) {
