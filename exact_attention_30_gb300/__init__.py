@@ -27,6 +27,7 @@ import ctypes
 import math
 import os
 import re
+import struct
 
 import torch
 
@@ -56,14 +57,13 @@ _vp, _ci, _cf, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_siz
 _ll = ctypes.c_longlong
 
 
-class _PagedKV(ctypes.Structure):
-    """fa_paged_kv of include/fa.h."""
-    _fields_ = [("k", _vp), ("v", _vp), ("num_pages", _ci), ("kv_heads", _ci), ("page_size", _ci),
-                ("d", _ci), ("k_page_stride", _ll), ("k_head_stride", _ll), ("k_row_stride", _ll),
-                ("v_page_stride", _ll), ("v_head_stride", _ll), ("v_row_stride", _ll)]
+# fa_paged_kv of include/fa.h and the three strides of a [B, H, N, d] view. They
+# are passed as the packed bytes: for a decode step of one short sequence, what
+# the host does per call is most of the time, and a ctypes structure costs more.
+_get_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_pack_pool = struct.Struct("@PPiiii6q").pack
+_pack_strides = struct.Struct("@3q").pack
 
-
-_pkv, _strides = ctypes.POINTER(_PagedKV), ctypes.POINTER(_ll)
 _SIGNATURES = {
     "fa_fwd": (_ci, [_vp, _vp, _vp, _vp, _vp, _ci, _ci, _ci, _ci, _cf, _ci, _vp]),
     "fa_fwd_ex": (_ci, [_vp, _vp, _vp, _vp, _vp, _ci, _ci, _ci, _ci, _cf, _ci, _ci, _vp]),
@@ -83,12 +83,12 @@ _SIGNATURES = {
     "fa_decode": (_ci, [_vp] * 6 + [_sz, _ci, _ci, _ci, _ci, _ci, _cf, _ci, _vp]),
     "fa_decode_workspace_bytes": (_sz, [_ci, _ci, _ci, _ci, _ci, _ci]),
     "fa_decode_plan": (_ci, [_ci, _ci, _ci, _ci, _ci, _ci, ctypes.POINTER(_ci), ctypes.POINTER(_ci)]),
-    "fa_kv_append": (_ci, [_vp, _vp, _ll, _ll, _vp, _vp, _ll, _ll, _ci, _pkv, _vp, _ci, _vp, _vp, _ci, _ci,
+    "fa_kv_append": (_ci, [_vp, _vp, _ll, _ll, _vp, _vp, _ll, _ll, _ci, _vp, _vp, _ci, _vp, _vp, _ci, _ci,
                            _vp, _vp, _ci, _ci, _vp, _ci, _ci, _vp]),
-    "fa_decode_paged": (_ci, [_vp, _strides, _pkv, _vp, _ci, _vp, _vp, _strides, _vp, _vp, _sz, _ci, _ci, _ci,
+    "fa_decode_paged": (_ci, [_vp, _vp, _vp, _vp, _ci, _vp, _vp, _vp, _vp, _vp, _sz, _ci, _ci, _ci,
                               _cf, _ci, _vp]),
     "fa_decode_paged_workspace_bytes": (_sz, [_ci, _ci, _ci, _ci, _ci, _ci]),
-    "fa_decode_shared": (_ci, [_vp, _strides, _pkv, _vp, _ci, _vp, _ci, _vp, _vp, _strides, _vp, _vp, _sz, _ci,
+    "fa_decode_shared": (_ci, [_vp, _vp, _vp, _vp, _ci, _vp, _ci, _vp, _vp, _vp, _vp, _vp, _sz, _ci,
                                _ci, _ci, _cf, _ci, _vp]),
     "fa_decode_shared_workspace_bytes": (_sz, [_ci, _ci, _ci, _ci, _ci, _ci, _ci]),
     "fa_check_device_status": (_ci, [_vp]),
@@ -167,6 +167,11 @@ def _check(t: torch.Tensor, name: str, like: torch.Tensor | None = None):
 
 def _stream_ptr(device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
+
+
+def _raw_stream(index: int) -> int:
+    """The current stream of device ``index``, without building a Stream object where torch allows."""
+    return _get_raw_stream(index) if _get_raw_stream is not None else _stream_ptr(index)
 
 
 def _raise(code: int, where: str):
@@ -427,47 +432,59 @@ def fa_rope_tables(max_positions: int, rot_dim: int, base: float = 10000.0, devi
     return a.cos().float(), a.sin().float()
 
 
-def _check_on(t, name: str, device, dtype):
+def _check_on(t, name: str, index: int, dtype):
+    """Checks that t is a tensor of ``dtype`` on CUDA device ``index`` (-1: on any) and returns its device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
+    i = t.get_device()
+    if i < 0:
         raise ValueError(f"{name} must be a CUDA tensor (this library has no CPU path)")
-    if t.device != device or t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype} on {device}")
+    if t.dtype is not dtype or (i != index and index >= 0):
+        raise ValueError(f"{name} must be {dtype} and on the same device as the other tensors")
+    return i
 
 
 def _paged_cache(k_pages, v_pages, block_tables, seq_lens):
-    """Checks a paged cache and its tables; returns (struct, B, max_pages, Hkv, d, device)."""
-    if not isinstance(k_pages, torch.Tensor):
-        raise TypeError("k_pages must be a torch.Tensor")
-    dev = k_pages.device
-    _check_on(k_pages, "k_pages", dev, torch.bfloat16)
+    """Checks a paged cache and its tables; returns (fa_paged_kv, its shape, B, max_pages, device index)."""
+    dev = _check_on(k_pages, "k_pages", -1, torch.bfloat16)
     _check_on(v_pages, "v_pages", dev, torch.bfloat16)
     _check_on(block_tables, "block_tables", dev, torch.int32)
     _check_on(seq_lens, "seq_lens", dev, torch.int32)
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+    shape = k_pages.shape
+    if len(shape) != 4 or v_pages.shape != shape:
         raise ValueError("k_pages and v_pages must both be [pages, Hkv, page_size, d]")
-    ks, vs = k_pages.stride(), v_pages.stride()
-    if ks[3] != 1 or vs[3] != 1:
+    k0, k1, k2, k3 = k_pages.stride()
+    v0, v1, v2, v3 = v_pages.stride()
+    if k3 != 1 or v3 != 1:
         raise ValueError("the last dimension of k_pages and v_pages must be contiguous")
     if block_tables.dim() != 2 or not block_tables.is_contiguous():
         raise ValueError("block_tables must be a contiguous int32 [B, max_pages]")
-    if seq_lens.dim() != 1 or not seq_lens.is_contiguous() or seq_lens.shape[0] != block_tables.shape[0]:
+    B, max_pages = block_tables.shape
+    if seq_lens.dim() != 1 or not seq_lens.is_contiguous() or seq_lens.shape[0] != B:
         raise ValueError("seq_lens must be a contiguous int32 [B]")
-    pages, hkv, page, d = k_pages.shape
-    c = _PagedKV(k_pages.data_ptr(), v_pages.data_ptr(), pages, hkv, page, d, ks[0], ks[1], ks[2], vs[0], vs[1],
-                 vs[2])
-    return c, block_tables.shape[0], block_tables.shape[1], hkv, d, dev
+    pool = _pack_pool(k_pages.data_ptr(), v_pages.data_ptr(), *shape, k0, k1, k2, v0, v1, v2)
+    return pool, shape, B, max_pages, dev
 
 
-def _token_stride(t, name: str, heads: int | None, d: int, dev):
+def _on_device(dev: int, fn, *args):
+    """fn(*args, current stream of device dev), with dev as the current device."""
+    if dev == torch.cuda.current_device():
+        return fn(*args, _raw_stream(dev))
+    with torch.cuda.device(dev):
+        return fn(*args, _raw_stream(dev))
+
+
+def _token_stride(t, name: str, total, heads, d: int, dev: int):
     """Checks packed tokens [total, heads, d] (heads of a token contiguous); returns their stride."""
     _check_on(t, name, dev, torch.bfloat16)
-    if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [total, heads, {d}] with the cache's head count and size")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != d or (heads is not None and shape[1] != heads) or \
+            (total is not None and shape[0] != total):
+        raise ValueError(f"{name} must be [total, heads, {d}] with the other tensors' tokens and heads")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != d and shape[1] > 1):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return t.stride(0)
+    return s0
 
 
 def fa_kv_append(k, v, k_pages, v_pages, block_tables, seq_lens, cu_seqlens=None, q=None, cos=None, sin=None,
@@ -483,49 +500,51 @@ def fa_kv_append(k, v, k_pages, v_pages, block_tables, seq_lens, cu_seqlens=None
     Returns the rotated queries (``q_out``, dense unless given), or None without q.
     """
     lib = load_library()
-    cache, B, max_pages, hkv, d, dev = _paged_cache(k_pages, v_pages, block_tables, seq_lens)
-    ks, vs = _token_stride(k, "k", hkv, d, dev), _token_stride(v, "v", hkv, d, dev)
+    pool, (_, hkv, page, d), B, max_pages, dev = _paged_cache(k_pages, v_pages, block_tables, seq_lens)
+    ks = _token_stride(k, "k", None, hkv, d, dev)
     total = k.shape[0]
-    if v.shape[0] != total:
-        raise ValueError("k and v must hold the same tokens")
+    vs = _token_stride(v, "v", total, hkv, d, dev)
     hq = qs = os_ = 0
+    q_ptr = out_ptr = cu_ptr = cos_ptr = sin_ptr = pos_ptr = None
     if q is not None:
-        hq, qs = q.shape[1] if q.dim() == 3 else 0, _token_stride(q, "q", None, d, dev)
-        if q.shape[0] != total:
-            raise ValueError("q and k must hold the same tokens")
+        qs = _token_stride(q, "q", total, None, d, dev)
+        hq = q.shape[1]
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        os_ = _token_stride(q_out, "q_out", hq, d, dev)
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            os_ = hq * d
+        else:
+            os_ = _token_stride(q_out, "q_out", total, hq, d, dev)
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out given without q")
     if cu_seqlens is not None:
         _check_on(cu_seqlens, "cu_seqlens", dev, torch.int32)
         if cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() or cu_seqlens.shape[0] != B + 1:
             raise ValueError("cu_seqlens must be a contiguous int32 [B+1]")
+        cu_ptr = cu_seqlens.data_ptr()
     rot = max_pos = 0
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
     if cos is not None:
-        for t, n in ((cos, "cos"), (sin, "sin")):
-            _check_on(t, n, dev, torch.float32)
-            if t.dim() != 2 or not t.is_contiguous() or t.shape != cos.shape:
-                raise ValueError(f"{n} must be a contiguous float32 [max_positions, rot_dim / 2]")
-        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        _check_on(cos, "cos", dev, torch.float32)
+        _check_on(sin, "sin", dev, torch.float32)
+        if cos.dim() != 2 or sin.shape != cos.shape or not cos.is_contiguous() or not sin.is_contiguous():
+            raise ValueError("cos and sin must be contiguous float32 [max_positions, rot_dim / 2]")
+        max_pos, rot = cos.shape
+        rot *= 2
+        cos_ptr, sin_ptr = cos.data_ptr(), sin.data_ptr()
     if positions is not None:
         _check_on(positions, "positions", dev, torch.int32)
         if positions.dim() != 1 or not positions.is_contiguous() or positions.shape[0] != total:
             raise ValueError("positions must be a contiguous int32 [total]")
+        pos_ptr = positions.data_ptr()
     if total == 0:
         return q_out
-    ptr = lambda t: None if t is None else t.data_ptr()
-    with torch.cuda.device(dev):
-        rc = lib.fa_kv_append(k.data_ptr(), v.data_ptr(), ks, vs, ptr(q), ptr(q_out), qs, os_, hq,
-                              ctypes.byref(cache), block_tables.data_ptr(), max_pages, seq_lens.data_ptr(),
-                              ptr(cu_seqlens), B, total, ptr(cos), ptr(sin), rot, max_pos, ptr(positions),
-                              FA_ROPE_INTERLEAVED if interleaved else 0, FA_BF16, _stream_ptr(dev))
-    _raise(rc, "fa_kv_append")
+    rc = _on_device(dev, lib.fa_kv_append, k.data_ptr(), v.data_ptr(), ks, vs, q_ptr, out_ptr, qs, os_, hq, pool,
+                    block_tables.data_ptr(), max_pages, seq_lens.data_ptr(), cu_ptr, B, total, cos_ptr, sin_ptr, rot,
+                    max_pos, pos_ptr, FA_ROPE_INTERLEAVED if interleaved else 0, FA_BF16)
+    if rc != FA_OK:
+        _raise(rc, "fa_kv_append")
     return q_out
 
 
@@ -539,46 +558,65 @@ def fa_decode_shared_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, prefix_
     return int(load_library().fa_decode_shared_workspace_bytes(B, Hq, Hkv, Nq, prefix_len, d, FA_BF16))
 
 
+_decode_ws_bytes: dict = {}  # (device, sizes) -> bytes: what the library answered
+
+
 def _decode_cache(where, q, k_pages, v_pages, prefix_pages, prefix_len, block_tables, seq_lens, scale, out, lse,
                   workspace):
     lib = load_library()
-    cache, B, max_pages, hkv, d, dev = _paged_cache(k_pages, v_pages, block_tables, seq_lens)
+    pool, (_, hkv, page, d), B, max_pages, dev = _paged_cache(k_pages, v_pages, block_tables, seq_lens)
     _check_on(q, "q", dev, torch.bfloat16)
-    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != d or q.shape[1] % hkv != 0 or q.stride(3) != 1:
-        raise ValueError("q must be [B, Hq, Nq, d] with the tables' B, the cache's d, Hq a multiple of its heads, "
-                         "and d contiguous")
-    _, hq, nq, _ = q.shape
-    o = torch.empty(q.shape, dtype=q.dtype, device=dev) if out is None else out
-    if out is not None:
-        _check_on(o, "out", dev, torch.bfloat16)
-        if o.shape != q.shape or o.stride(3) != 1:
-            raise ValueError("out must match q in shape, with d contiguous")
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != B or shape[3] != d or shape[1] % hkv != 0:
+        raise ValueError("q must be [B, Hq, Nq, d] with the tables' B, the cache's d and Hq a multiple of its heads")
+    _, hq, nq, _ = shape
+    q0, q1, q2, q3 = q.stride()
+    device = q.device
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        o_strides, o3 = None, 1
+    else:
+        _check_on(out, "out", dev, torch.bfloat16)
+        if out.shape != shape:
+            raise ValueError("out must match q in shape")
+        o0, o1, o2, o3 = out.stride()
+        o_strides = _pack_strides(o0, o1, o2)
+    if q3 != 1 or o3 != 1:
+        raise ValueError("the last dimension of q and out must be contiguous")
     if lse is None:
-        lse = torch.empty((B, hq, nq), dtype=torch.float32, device=dev)
+        lse = torch.empty((B, hq, nq), dtype=torch.float32, device=device)
     else:
         _check_on(lse, "lse", dev, torch.float32)
         if lse.shape != (B, hq, nq) or not lse.is_contiguous():
             raise ValueError("lse must be contiguous float32 [B, Hq, Nq]")
-    if prefix_pages is not None:
+    prefix_ptr = None
+    if prefix_len > 0:
         _check_on(prefix_pages, "prefix_pages", dev, torch.int32)
         if prefix_pages.dim() != 1 or not prefix_pages.is_contiguous():
             raise ValueError("prefix_pages must be a contiguous int32 [pages]")
-        if prefix_pages.shape[0] * k_pages.shape[2] < prefix_len:
+        if prefix_pages.shape[0] * page < prefix_len:
             raise ValueError("prefix_pages holds fewer than prefix_len keys")
-    with torch.cuda.device(dev):
-        if workspace is None:
-            n = lib.fa_decode_shared_workspace_bytes(B, hq, hkv, nq, prefix_len, d, FA_BF16)
-            workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
-        elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+        prefix_ptr = prefix_pages.data_ptr()
+    if workspace is None:
+        key = (dev, B, hq, hkv, nq, prefix_len, d)
+        n = _decode_ws_bytes.get(key)
+        if n is None:
+            with torch.cuda.device(dev):
+                n = lib.fa_decode_shared_workspace_bytes(B, hq, hkv, nq, prefix_len, d, FA_BF16)
+            if len(_decode_ws_bytes) >= 4096:
+                _decode_ws_bytes.clear()
+            _decode_ws_bytes[key] = n
+        workspace = torch.empty(n, dtype=torch.uint8, device=device)
+    else:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on q's device")
-        rc = lib.fa_decode_shared(q.data_ptr(), (_ll * 3)(*q.stride()[:3]), ctypes.byref(cache),
-                                  prefix_pages.data_ptr() if prefix_len > 0 else None, prefix_len,
-                                  block_tables.data_ptr(), max_pages, seq_lens.data_ptr(), o.data_ptr(),
-                                  (_ll * 3)(*o.stride()[:3]), lse.data_ptr(), workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), B, hq, nq, scale, FA_BF16,
-                                  _stream_ptr(dev))
-    _raise(rc, where)
-    return o, lse
+        n = workspace.numel() * workspace.element_size()
+    rc = _on_device(dev, lib.fa_decode_shared, q.data_ptr(), _pack_strides(q0, q1, q2), pool, prefix_ptr, prefix_len,
+                    block_tables.data_ptr(), max_pages, seq_lens.data_ptr(), out.data_ptr(), o_strides,
+                    lse.data_ptr(), workspace.data_ptr(), n, B, hq, nq, scale, FA_BF16)
+    if rc != FA_OK:
+        _raise(rc, where)
+    return out, lse
 
 
 def fa_decode_paged(q, k_pages, v_pages, block_tables, seq_lens, scale: float | None = None, out=None, lse=None,

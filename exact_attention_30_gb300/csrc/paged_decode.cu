@@ -698,11 +698,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const __
 template <int D, int MT>
 cudaError_t launch(const PagedDecodeArgs& a, unsigned merge_blocks, cudaStream_t st) {
   using C = Cfg<D, MT>;
-  cudaError_t e = cudaFuncSetAttribute(decode_paged_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       C::SMEM_ALLOC);
-  if (e != cudaSuccess) return e;
   decode_paged_kernel<D, MT><<<(unsigned)a.ctas, C::THREADS, C::SMEM_ALLOC, st>>>(a);
-  e = cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // set up while the main kernel runs (programmatic dependent launch)
   cudaLaunchAttribute attr{};
@@ -717,6 +714,8 @@ cudaError_t launch(const PagedDecodeArgs& a, unsigned merge_blocks, cudaStream_t
   return cudaLaunchKernelEx(&cfg, decode_merge_kernel<D>, a);
 }
 
+// Also allows the kernel its shared memory on the current device; every launch
+// follows a paged_layout() on the same device.
 template <int D, int MT>
 int ctas_per_sm() {
   using C = Cfg<D, MT>;

@@ -1,12 +1,12 @@
 """Host-side refusals of the paged-cache entry points: they return from validation before any CUDA call."""
 import ctypes
 import os
+import struct
 
 import pytest
 import torch
 
 import exact_attention_30_gb300 as fa
-from exact_attention_30_gb300 import _PagedKV
 from exact_attention_30_gb300 import build as fa_build
 
 FAKE = 0x10000  # an aligned non-null value: never dereferenced, validation fails first
@@ -23,7 +23,7 @@ def _cache(**kw):
     c = dict(k=FAKE, v=FAKE, num_pages=10, kv_heads=4, page_size=16, d=128, k_page_stride=8192, k_head_stride=2048,
              k_row_stride=128, v_page_stride=8192, v_head_stride=2048, v_row_stride=128)
     c.update(kw)
-    return _PagedKV(**c)
+    return struct.pack("@PPiiii6q", *c.values())  # fa_paged_kv
 
 
 BAD_POOLS = [
@@ -42,7 +42,7 @@ def _append(lib, cache=None, K=FAKE, V=FAKE, ks=512, vs=512, Q=FAKE, Qo=FAKE + 6
             tables=FAKE, max_pages=4, lens=FAKE, cu=FAKE, B=2, total=6, cos=FAKE, sin=FAKE, rot=128, max_pos=64,
             positions=None, flags=0, dt=fa.FA_BF16):
     cache = _cache() if cache is None else cache
-    return lib.fa_kv_append(K, V, ks, vs, Q, Qo, qs, qos, Hq, ctypes.byref(cache), tables, max_pages, lens, cu, B,
+    return lib.fa_kv_append(K, V, ks, vs, Q, Qo, qs, qos, Hq, cache, tables, max_pages, lens, cu, B,
                             total, cos, sin, rot, max_pos, positions, flags, dt, None)
 
 
@@ -52,9 +52,9 @@ def _decode(lib, cache=None, Q=FAKE, qs=None, tables=FAKE, max_pages=4, lens=FAK
     cache = _cache() if cache is None else cache
     st = lambda s: None if s is None else (ctypes.c_longlong * 3)(*s)
     if shared:
-        return lib.fa_decode_shared(Q, st(qs), ctypes.byref(cache), prefix, prefix_len, tables, max_pages, lens, O,
+        return lib.fa_decode_shared(Q, st(qs), cache, prefix, prefix_len, tables, max_pages, lens, O,
                                     st(os_), LSE, ws, ws_bytes, B, Hq, Nq, scale, dt, None)
-    return lib.fa_decode_paged(Q, st(qs), ctypes.byref(cache), tables, max_pages, lens, O, st(os_), LSE, ws, ws_bytes,
+    return lib.fa_decode_paged(Q, st(qs), cache, tables, max_pages, lens, O, st(os_), LSE, ws, ws_bytes,
                                B, Hq, Nq, scale, dt, None)
 
 
