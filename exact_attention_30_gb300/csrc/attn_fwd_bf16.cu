@@ -47,6 +47,13 @@
 // tiles first (longest-processing-time order), so the short ones fill the
 // last wave.
 //
+// Shared prefix of a paged cache (Args = PrefixArgs): the rows of a K/V head
+// are the queries of every sequence of a batch, gathered by the softmax warps
+// (one row per thread) into the Q tiles; the keys are the prefix's pages, one
+// TMA box per page and lane of the producer warp. Every unit is split into key
+// ranges as above, also into one, and leaves partial results, which
+// decode_merge_kernel combines with those of the sequences' own keys.
+//
 // Every mbarrier wait is bounded; on expiry the kernel records a timeout in
 // the status word, drains its in-flight TMA loads and MMAs, frees TMEM and
 // exits.
@@ -55,6 +62,7 @@
 #include <cuda_runtime.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "fa_internal.h"
 #include "ptx.cuh"
@@ -159,9 +167,10 @@ __device__ __forceinline__ bool softmax_pass_own_p(uint32_t s_addr, uint32_t p_a
   return true;
 }
 
-template <int D>
-__global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) fwd_bf16_kernel(const __grid_constant__ FwdArgs a) {
+template <int D, class Args>
+__global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) fwd_bf16_kernel(const __grid_constant__ Args a) {
   using C = FwdCfg<D>;
+  constexpr bool PREFIX = std::is_same_v<Args, PrefixArgs>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -181,7 +190,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) fwd_bf16_kernel(const _
 
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool causal = a.seq.causal != 0;
+  const bool causal = !PREFIX && a.seq.causal != 0;
   int bh, qblk;
   int tail_unit = -1, part = 0;  // split units: index among them, key part
   if (causal) {
@@ -192,7 +201,9 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) fwd_bf16_kernel(const _
   } else {
     // one CTA per unit (head, 256-row block), head-major; the units from
     // n_full on are split into a.splits key ranges, one CTA each
-    const int qblocks = (a.seq.N + C::BM * C::QT - 1) / (C::BM * C::QT);
+    int n_rows = a.seq.N;
+    if constexpr (PREFIX) n_rows = a.rows;
+    const int qblocks = (n_rows + C::BM * C::QT - 1) / (C::BM * C::QT);
     int u = (int)blockIdx.x;
     if (u >= a.n_full) {
       const int r = u - a.n_full;
@@ -207,7 +218,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) fwd_bf16_kernel(const _
   const SeqView sv = seq_view(a.seq, bh, a.status);
   const int N = sv.len;  // queries = keys of this sequence
   const int q0 = qblk * (C::BM * C::QT);
-  if (q0 >= N) return;  // the whole CTA: nothing of this sequence here
+  if (!PREFIX && q0 >= N) return;  // the whole CTA: nothing of this sequence here
   const int n_kv = (N + C::BN - 1) / C::BN;
   // key tiles kt0 + j, j < n_t0 (query tile 0) or n_t1 (tile 1): all of
   // them, up to the diagonal (causal), or this CTA's part of a split unit
@@ -218,13 +229,17 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) fwd_bf16_kernel(const _
   }
   const int qt0 = q0 / C::BM;
   const int n_t0 = causal ? min(qt0 + 1, n_kv) : kt_end - kt0;
-  const int n_t1 = causal ? min(qt0 + 2, n_kv) : kt_end - kt0;  // >= n_t0
-  const int n_max = n_t1;
+  int n_t1 = causal ? min(qt0 + 2, n_kv) : kt_end - kt0;  // >= n_t0, or 0: a prefix's block without a second tile
+  if constexpr (PREFIX) {
+    if (q0 + C::BM >= a.rows) n_t1 = 0;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the own keys' kernel may fill idle SMs
+  }
+  const int n_max = PREFIX ? n_t0 : n_t1;
   const int y0 = sv.start;  // first row of the sequence in the TMA views
   const int plane = sv.plane;
 
   if (threadIdx.x == 0) {
-    for (int t = 0; t < C::QT; ++t) mbar_init(BAR(B_QFULL + t), 1);
+    for (int t = 0; t < C::QT; ++t) mbar_init(BAR(B_QFULL + t), PREFIX ? 4 : 1);
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(BAR(B_KFULL + s), 1);
       mbar_init(BAR(B_VFULL + s), 1);
@@ -247,7 +262,64 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) fwd_bf16_kernel(const _
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 0) {
+  if (PREFIX && warp == 0) {
+    // ------------------------------------------- producer of a prefix's pages
+    if constexpr (PREFIX) {
+      // lane: one box of one 64-column chunk of a tile
+      const int nbox = C::BN / a.box_rows;
+      const bool mine = lane < nbox * C::CH;
+      const int box = lane % nbox, chunk = lane / nbox;
+      const uint32_t dst0 = sbase + chunk * C::CHUNK_BYTES + box * a.box_rows * 128;
+      auto look_up = [&](int tile, int& page, int& row) {
+        const int key = tile * C::BN + box * a.box_rows;
+        page = -1;
+        row = 0;
+        if (mine && key < N) {
+          const int pi = key / a.pool.page_size;
+          row = key - pi * a.pool.page_size;
+          page = __ldg(a.prefix_pages + pi);
+          if (page < 0 || page >= a.pool.num_pages) {
+            report_status(a.status, kStatusBadSeqlens);
+            page = a.pool.num_pages;  // outside the tensor: reads as zeros
+          }
+        }
+      };
+      int last_j = -1, page, row;
+      bool k_only = false;  // the last tile's keys were loaded, its values not
+      look_up(kt0, page, row);
+      for (int j = 0; j < n_max; ++j) {
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+        const int s = j % C::STAGES;
+        const uint32_t ph = (j / C::STAGES) & 1;
+        int next_page = -1, next_row = 0;
+        if (j + 1 < n_max) look_up(kt0 + j + 1, next_page, next_row);
+        const int left = N - (kt0 + j) * C::BN;
+        const int boxes = left >= C::BN ? nbox : (left + a.box_rows - 1) / a.box_rows;
+        const uint32_t bytes = (uint32_t)(boxes * a.box_rows * 128 * C::CH);
+        if (!mbar_wait_warp(BAR(B_KEMPTY + s), ph ^ 1, a.status, a.wait_limit_ns)) { *abort_flag = 1; break; }
+        if (lane == 0) mbar_arrive_expect_tx(BAR(B_KFULL + s), bytes);
+        __syncwarp();
+        if (page >= 0)
+          tma_load_4d(dst0 + C::OFF_K + s * C::TILE_BYTES, &a.tmK, BAR(B_KFULL + s), chunk * 64, row, bh, page);
+        last_j = j;
+        k_only = true;
+        if (!mbar_wait_warp(BAR(B_VEMPTY + s), ph ^ 1, a.status, a.wait_limit_ns)) { *abort_flag = 1; break; }
+        if (lane == 0) mbar_arrive_expect_tx(BAR(B_VFULL + s), bytes);
+        __syncwarp();
+        if (page >= 0)
+          tma_load_4d(dst0 + C::OFF_V + s * C::TILE_BYTES, &a.tmV, BAR(B_VFULL + s), chunk * 64, row, bh, page);
+        k_only = false;
+        page = next_page;
+        row = next_row;
+      }
+      // drain: the last load issued into each slot must have landed before exit
+      for (int j = max(0, last_j - C::STAGES + 1); j <= last_j; ++j) {
+        const uint32_t ph = (j / C::STAGES) & 1;
+        mbar_wait_warp(BAR(B_KFULL + j % C::STAGES), ph, a.status, a.wait_limit_ns);
+        if (j < last_j || !k_only) mbar_wait_warp(BAR(B_VFULL + j % C::STAGES), ph, a.status, a.wait_limit_ns);
+      }
+    }
+  } else if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       tma_prefetch_desc(&a.tmQ);
@@ -321,19 +393,39 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) fwd_bf16_kernel(const _
           mma_ss(dcol, qa + off, kb + off, idesc_s, kk > 0 ? 1u : 0u, leader);
         }
       };
-      auto issue_pv = [&](int t, int s, bool acc) {
+      // `keys`: those of the tile (a prefix's last tile: V has no rows past them)
+      auto issue_pv = [&](int t, int s, bool acc, int keys) {
         const uint64_t vb = dV0 + (uint64_t)((s * C::TILE_BYTES) >> 4);
         const uint32_t dcol = tmem + C::O_COL(t), acol = tmem + C::P_COL(t);
 #pragma unroll
         for (int kk = 0; kk < C::BN / 16; ++kk)
           mma_ts(dcol, acol + kk * 8, vb + (uint64_t)((kk * 2048) >> 4), idesc_o,
-                 (acc || kk > 0) ? 1u : 0u, leader);
+                 (acc || kk > 0) ? 1u : 0u, PREFIX && 16 * kk >= keys ? 0u : leader);
+      };
+      // V_j has landed in slot s. What stands behind a prefix's last key in
+      // its page may be anything, NaN included: the rows that the last 16-key
+      // step would read there become zero.
+      auto clean_v = [&](int j, int s) {
+        if constexpr (PREFIX) {
+          const int keys = N - (kt0 + j) * C::BN;
+          if (keys < C::BN && (keys & 15) != 0) {
+            const int n_rows = 16 - (keys & 15);
+            for (int e = lane; e < n_rows * C::CH * 8; e += 32) {
+              const int r = keys + e / (C::CH * 8), u = e % (C::CH * 8);
+              *reinterpret_cast<uint4*>(smem + C::OFF_V + s * C::TILE_BYTES + (u >> 3) * C::CHUNK_BYTES + r * 128 +
+                                        (u & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
       };
       auto wait = [&](int b, uint32_t parity) {
         return mbar_wait_warp(BAR(b), parity, a.status, a.wait_limit_ns);
       };
       bool ok = wait(B_QFULL + 0, 0) && wait(B_KFULL + 0, 0);
       for (int t = 0; ok && t < C::QT; ++t) {
+        if (PREFIX && t > 0 && n_t1 == 0) break;
         if (t > 0 && !wait(B_QFULL + t, 0)) { ok = false; break; }
         tc_fence_after();
         issue_s(t, 0);
@@ -365,17 +457,19 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) fwd_bf16_kernel(const _
             }
             if (!wait(B_PFULL + t, j & 1)) { ok = false; break; }
             if (!v_here && !wait(B_VFULL + s, ph)) { ok = false; break; }
+            if (!v_here) clean_v(j, s);
             v_here = true;
             tc_fence_after();
-            issue_pv(t, s, j > 0);
+            issue_pv(t, s, j > 0, N - (kt0 + j) * C::BN);
             mma_commit(BAR(B_ODONE + t), leader);
           } else {
             // P overwrites S: P_j V_j must be issued before S_{j+1}.
             if (!v_here && !wait(B_VFULL + s, ph)) { ok = false; break; }
+            if (!v_here) clean_v(j, s);
             v_here = true;
             if (!wait(B_PFULL + t, j & 1)) { ok = false; break; }
             tc_fence_after();
-            issue_pv(t, s, j > 0);
+            issue_pv(t, s, j > 0, N - (kt0 + j) * C::BN);
             mma_commit(BAR(B_ODONE + t), leader);
             if (j + 1 < n_own) {
               if (!k_next && !wait(B_KFULL + s1, ph1)) { ok = false; break; }
@@ -408,6 +502,22 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) fwd_bf16_kernel(const _
     const float c2 = a.scale_log2;
     float m_ref = -INFINITY, l = 0.f;
     bool ok = true;
+    if constexpr (PREFIX) {
+      // this thread's row of the batch: sequence, query head, new token
+      if (n_own > 0) {
+        const int R = a.G * a.Nq, b = row / R, i = (row - b * R) % a.Nq, hq = bh * a.G + (row - b * R) / a.Nq;
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.Qrows) + b * a.q_b + hq * a.q_h + i * a.q_r);
+        uint8_t* dst = smem + C::OFF_Q + t * C::TILE_BYTES + row_in_tile * 128;
+#pragma unroll
+        for (int u = 0; u < D / 8; ++u) {
+          const uint4 v = row < a.rows ? __ldg(src + u) : make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(dst + (u >> 3) * C::CHUNK_BYTES + (((u & 7) ^ (row_in_tile & 7)) << 4)) = v;
+        }
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(B_QFULL + t));
+    }
     for (int j = 0; j < n_own; ++j) {
       if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
       bool w = mbar_wait(BAR(B_SFULL + t), j & 1, a.status, a.wait_limit_ns);
@@ -556,11 +666,11 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) fwd_bf16_kernel(const _
     // warp that gave up must not leave the others waiting at a barrier it
     // never reaches. Split units: both tiles' warps (they stage into shared
     // memory the other tile may still read); otherwise the tile's own four.
-    if (tail_unit >= 0) ok = named_bar_and<1>(256, ok);
+    if (PREFIX || tail_unit >= 0) ok = named_bar_and<1>(256, ok);
     else if (t == 0) ok = named_bar_and<2>(128, ok);
     else ok = named_bar_and<3>(128, ok);
     if (!ok) *abort_flag = 1;
-    if (tail_unit >= 0) {
+    if (PREFIX || tail_unit >= 0) {
       // One key part of a split unit: its normalised partial O (fp32) and
       // base-2 LSE go to the workspace; fwd_tail_merge_kernel, launched after
       // this kernel, combines the parts. Both tiles' products are complete
@@ -751,7 +861,7 @@ cudaError_t launch_fwd_d(const FwdArgs& a, int BH, cudaStream_t st) {
   using C = FwdCfg<D>;
   static_assert(C::SMEM_ALLOC <= 227 * 1024, "shared memory budget");
   static_assert(C::QT * D * 512 <= C::OFF_BAR - C::OFF_Q, "split-part staging fits the tile buffers");
-  cudaError_t e = cudaFuncSetAttribute(fwd_bf16_kernel<D>,
+  cudaError_t e = cudaFuncSetAttribute(fwd_bf16_kernel<D, FwdArgs>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
   if (e != cudaSuccess) return e;
   const unsigned qblocks = (unsigned)((a.seq.N + C::BM * C::QT - 1) / (C::BM * C::QT));
@@ -766,7 +876,7 @@ cudaError_t launch_fwd_d(const FwdArgs& a, int BH, cudaStream_t st) {
     const int hpg = causal_heads_per_group(BH, 4ll * a.seq.N * D, 96ll << 20);
     grid = dim3((unsigned)hpg, qblocks, (unsigned)((BH + hpg - 1) / hpg));
   }
-  fwd_bf16_kernel<D><<<grid, C::THREADS, C::SMEM_ALLOC, st>>>(a);
+  fwd_bf16_kernel<D, FwdArgs><<<grid, C::THREADS, C::SMEM_ALLOC, st>>>(a);
   cudaError_t e2 = cudaGetLastError();
   if (e2 != cudaSuccess || a.splits == 1) return e2;
   const long long merge_rows = (long long)a.n_tail * C::BM * C::QT;
@@ -776,6 +886,21 @@ cudaError_t launch_fwd_d(const FwdArgs& a, int BH, cudaStream_t st) {
   if (a.splits == 2) fwd_tail_merge_kernel<D, 2><<<blocks(8), 256, 0, st>>>(a);
   else if (a.splits == 3) fwd_tail_merge_kernel<D, 3><<<blocks(5), 256, 0, st>>>(a);
   else fwd_tail_merge_kernel<D, 4><<<blocks(4), 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_prefix_d(const PrefixArgs& a, cudaStream_t st) {
+  using C = FwdCfg<D>;
+  const long long qblocks = ((long long)a.rows + C::BM * C::QT - 1) / (C::BM * C::QT);
+  const long long units = qblocks * a.pool.kv_heads;
+  if (a.rows < 1 || a.seq.N < 1 || a.splits < 1 || a.splits > (a.seq.N + C::BN - 1) / C::BN || a.n_full != 0 ||
+      a.n_tail != units || units * a.splits > 0x7fffffffll)
+    return cudaErrorInvalidValue;
+  const cudaError_t e = cudaFuncSetAttribute(fwd_bf16_kernel<D, PrefixArgs>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
+  if (e != cudaSuccess) return e;
+  fwd_bf16_kernel<D, PrefixArgs><<<(unsigned)(units * a.splits), C::THREADS, C::SMEM_ALLOC, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -818,6 +943,29 @@ int fwd_slots() {
     g_slots[dev] = sms;  // one forward CTA per SM (all of TMEM, most of shared memory)
   }
   return g_slots[dev];
+}
+
+int plan_prefix_splits(long long units, int n_kv, int slots) {
+  if (units < 1 || n_kv < 1 || slots < 1) return 0;
+  // Waves times the longest range, each range with a start-up (Q, the first
+  // K/V tiles, the epilogue) of about three tiles; ties to the fewer parts.
+  long long best = -1;
+  int splits = 1;
+  for (int s = 1; s <= n_kv && s <= kPrefixMaxSplits; ++s) {
+    const long long waves = (units * s + slots - 1) / slots;
+    const long long cost = waves * ((n_kv + s - 1) / s + 3);
+    if (best < 0 || cost < best) {
+      best = cost;
+      splits = s;
+    }
+  }
+  return splits;
+}
+
+cudaError_t launch_prefix_bf16(const PrefixArgs& a, int d, cudaStream_t st) {
+  if (d == 128) return launch_prefix_d<128>(a, st);
+  if (d == 64) return launch_prefix_d<64>(a, st);
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_fwd_bf16(const FwdArgs& a, int BH, int d, cudaStream_t st) {

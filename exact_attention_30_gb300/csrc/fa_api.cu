@@ -84,19 +84,6 @@ bool encode_acc_f32(CUtensorMap* m, void* ptr, long long rows, int d) {
   return r == CUDA_SUCCESS;
 }
 
-// Partial O of the forward's split units: fp32 [rows, d] as 2-D (d, rows),
-// boxes of 32 columns (128 bytes) x 128 rows in the 128-byte swizzle.
-bool encode_part_f32(CUtensorMap* m, void* ptr, long long rows, int d) {
-  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)d * 4};
-  cuuint32_t box[2] = {32, 128};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, ptr, dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 fa_status check_dtype_d(int d, fa_dtype dt) {
@@ -197,6 +184,20 @@ unsigned flag_stages(int flags) {
 
 }  // namespace
 
+// Partial O of the forward's split units: fp32 [rows, d] as 2-D (d, rows),
+// boxes of 32 columns (128 bytes) x 128 rows in the 128-byte swizzle.
+bool encode_part_f32(CUtensorMap* m, void* ptr, long long rows, int d) {
+  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)d * 4};
+  cuuint32_t box[2] = {32, 128};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, ptr, dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// The pool's keys or values, 4-D (d, rows of a page, heads, pages).
 bool encode_pool_bf16(CUtensorMap* m, const PagedPool& pool, bool values, int d, int box_rows) {
   if (!get_encode_fn()) return false;
   const long long page = values ? pool.v_page : pool.k_page, head = values ? pool.v_head : pool.k_head,

@@ -220,6 +220,26 @@ struct AppendArgs {
 };
 cudaError_t launch_append_bf16(const AppendArgs& a, int d, cudaStream_t st);
 
+// The forward over a prefix that a batch shares (attn_fwd_bf16.cu): the rows of
+// K/V head h are the query rows of all sequences, row b * G * Nq + g * Nq + i
+// being new token i of query head h * G + g of sequence b, against the
+// seq.N keys of the prefix's pages. n_full = 0, n_tail = heads * ceil(rows /
+// 256) units of `splits` >= 1 key ranges, partial results in Opart and Lpart.
+struct PrefixArgs : FwdArgs {  // tmK, tmV: the pool (encode_pool_bf16), boxes of box_rows rows
+  PagedPool pool;
+  const void* Qrows;  // bf16; element strides of batch, head, row:
+  long long q_b, q_h, q_r;
+  const int* prefix_pages;
+  int rows;           // B * G * Nq
+  int G, Nq, box_rows;
+};
+cudaError_t launch_prefix_bf16(const PrefixArgs& a, int d, cudaStream_t st);
+constexpr int kPrefixMaxSplits = 64;
+// Key ranges per unit for `units` units of n_kv 128-key tiles on a GPU that
+// runs `slots` forward CTAs at once (0 on bad sizes).
+int plan_prefix_splits(long long units, int n_kv, int slots);
+bool encode_part_f32(CUtensorMap* m, void* ptr, long long rows, int d);
+
 // 4-D tensor map (d, rows, heads, pages) over the pool's keys or values:
 // boxes of 64 columns x box_rows rows of one page, 128-byte swizzle.
 bool encode_pool_bf16(CUtensorMap* m, const PagedPool& pool, bool values, int d, int box_rows);
@@ -239,12 +259,17 @@ struct PagedDecodeArgs {
   int box_rows;                    // rows per TMA box: divides page_size and 64
   // schedule and scratch (paged_layout)
   int ctas;                        // grid; shares of the keys
-  int n_seq;                       // B and, behind them, the prefix once per slot_rows of its rows
+  int n_seq;                       // B, or B + 1: the prefix is the last sequence
   int slot_rows;                   // rows of a partial result's slot
   float* Opart;                    // fp32 [slots][slot_rows][d], normalised
   float* Lpart;                    // fp32 [slots][slot_rows], base-2 log-sum-exp
   int2* unit_ctas;                 // [n_seq * Hkv] first and last CTA of a unit
   long long* begun;                // [ctas] the unit that a CTA begins and does not end, or -1
+  // A prefix of many rows runs as a kernel of its own (launch_prefix_bf16),
+  // whose pre_splits partial results per row lie here; 0: it is part of n_seq.
+  int pre_splits;
+  const float* pre_Opart;
+  const float* pre_Lpart;
   float scale_log2;                // scale * log2(e)
   int* status;
   unsigned long long wait_limit_ns;
@@ -254,8 +279,8 @@ constexpr int kPagedMaxKeys = 1 << 30;
 // Grid and scratch of a decode on the current device (ctas = 0 on failure);
 // rows = G * Nq. Offsets in bytes; the partial outputs come first.
 struct PagedLayout {
-  int ctas, n_seq, slot_rows;
-  size_t lpart, unit_ctas, begun, total;
+  int ctas, n_seq, slot_rows, pre_splits;
+  size_t lpart, unit_ctas, begun, pre_opart, pre_lpart, total;
 };
 PagedLayout paged_layout(int B, int Hkv, int rows, int prefix_len, int d);
 cudaError_t launch_decode_paged_bf16(const PagedDecodeArgs& a, int d, cudaStream_t st);

@@ -129,6 +129,42 @@ fa_status decode_impl(const void* Q, const long long* q_strides, const fa_paged_
   a.max_pages = max_pages;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_limit_ns = kDefaultWaitLimitNs;
+  if (L.pre_splits > 0) {
+    PrefixArgs p;
+    std::memset(static_cast<void*>(&p), 0, sizeof(p));
+    p.pool = a.pool;
+    p.box_rows = cache->page_size & -cache->page_size;
+    if (p.box_rows > 128) p.box_rows = 128;
+    p.rows = B * a.G * Nq;
+    const long long units = ((long long)p.rows + 255) / 256 * cache->kv_heads;
+    p.Opart = reinterpret_cast<float*>(ws + L.pre_opart);
+    p.Lpart = reinterpret_cast<float*>(ws + L.pre_lpart);
+    if (!encode_pool_bf16(&p.tmK, a.pool, false, cache->d, p.box_rows) ||
+        !encode_pool_bf16(&p.tmV, a.pool, true, cache->d, p.box_rows) ||
+        !encode_part_f32(&p.tmOpart, p.Opart, units * L.pre_splits * 256, cache->d))
+      return FA_ERR_CUDA;
+    p.seq.H = cache->kv_heads;
+    p.seq.N = prefix_len;
+    p.seq.total = prefix_len;
+    p.BH = cache->kv_heads;
+    p.scale_log2 = a.scale_log2;
+    p.status = a.status;
+    p.wait_limit_ns = a.wait_limit_ns;
+    p.n_tail = (int)units;
+    p.splits = L.pre_splits;
+    p.debug_skip_kv = -1;
+    p.Qrows = Q;
+    p.q_b = a.q_b;
+    p.q_h = a.q_h;
+    p.q_r = a.q_r;
+    p.prefix_pages = prefix_pages;
+    p.G = a.G;
+    p.Nq = Nq;
+    if (launch_prefix_bf16(p, cache->d, static_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_CUDA;
+    a.pre_splits = L.pre_splits;
+    a.pre_Opart = p.Opart;
+    a.pre_Lpart = p.Lpart;
+  }
   return launch_decode_paged_bf16(a, cache->d, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK
                                                                                                   : FA_ERR_CUDA;
 }

@@ -19,8 +19,10 @@
 // fixed order (results do not depend on timing). A unit that lies in one share
 // is written out directly.
 //
-// A shared prefix is one more sequence of the same grid per block of slot_rows
-// rows (those of every sequence, B * R per K/V head), read once for each block.
+// A shared prefix with no more rows than fit a unit (those of every sequence,
+// B * R <= 64 per K/V head) is one more sequence of the same grid. With more
+// rows it is a matrix product of its own (launch_prefix_bf16), and only its
+// partial results meet the own keys' here.
 //
 // CTA: one producer warp and 4 consumer warps per 16 query rows. The producer
 // reads page numbers a tile ahead and lets each lane issue one TMA box (64
@@ -96,14 +98,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y,
-                                            int z, int w) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-      : "memory");
 }
 __device__ __forceinline__ void named_bar(int id, int count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
@@ -266,7 +260,10 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
       if (seq_keys(a, s) == 0) empty_rows<D>(a, s);
     __syncthreads();  // begun[] may be written again below, by another thread
   }
-  if (share.left <= 0) return;
+  if (share.left <= 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // as at the end
+    return;
+  }
   Walk wk;
   wk.begin(a, share, C::BK);
 
@@ -349,14 +346,13 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
   while (wk.sh.left > 0 && wk.piece() > 0) {
     const int n = wk.piece(), first = wk.sh.tile, seq = wk.sh.seq, head = wk.sh.head, len = wk.len;
     const bool pre = seq >= a.B;
-    const int pre_row = pre ? (seq - a.B) * a.slot_rows : 0;  // first of this block of the prefix's rows
-    const int rows = pre ? min(a.slot_rows, a.B * R - pre_row) : R;
+    const int rows = pre ? a.B * R : R;
     // row r of this unit: batch entry, query head, new token
     auto row_at = [&](int r, int& b, int& hq, int& i) {
       b = seq;
       if (pre) {
-        b = (pre_row + r) / R;
-        r += pre_row - b * R;
+        b = r / R;
+        r -= b * R;
       }
       i = r % a.Nq;
       hq = head * a.G + r / a.Nq;
@@ -604,6 +600,8 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
     }
     wk.advance(a, n, C::BK);
   }
+  // a prefix's kernel ends before this one does, so the merge sees both
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Rows of units that were not written out directly: partial results of the
@@ -629,9 +627,13 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const __
     own_n = c.y - c.x + 1;
   }
   int pre_first = 0, pre_n = 0;
-  const int pre_block = (b * R + r) / a.slot_rows;
-  const long long pre_unit = (long long)(a.B + pre_block) * Hkv + head;
-  if (a.prefix_len > 0) {
+  const long long pre_unit = (long long)a.B * Hkv + head;
+  long long pre_row = 0;  // kernel of its own: row of the first part, parts 256 rows apart
+  if (a.pre_splits > 0) {
+    const int rr = b * R + r, qblocks = (a.B * R + 255) / 256;
+    pre_n = a.pre_splits;
+    pre_row = ((long long)head * qblocks + rr / 256) * a.pre_splits * 256 + rr % 256;
+  } else if (a.prefix_len > 0) {
     const int2 c = a.unit_ctas[pre_unit];
     pre_first = c.x;
     pre_n = c.y - c.x + 1;
@@ -643,11 +645,20 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const __
   for (int p = warp; p < own_n + pre_n; p += kMergeWarps) {
     const bool own = p < own_n;
     const int i = own ? p : p - own_n;
-    const long long slot = part_slot(a, (own ? own_first : pre_first) + i, i == 0, i + 1 == (own ? own_n : pre_n), own ? unit : pre_unit);
-    const long long row = slot * a.slot_rows + (own ? r : b * R + r - pre_block * a.slot_rows);
-    const float L = a.Lpart[row];
+    const float* O = a.Opart;
+    const float* Ls = a.Lpart;
+    long long row;
+    if (own || a.pre_splits == 0) {
+      const long long slot = part_slot(a, (own ? own_first : pre_first) + i, i == 0, i + 1 == (own ? own_n : pre_n), own ? unit : pre_unit);
+      row = slot * a.slot_rows + (own ? r : b * R + r);
+    } else {
+      O = a.pre_Opart;
+      Ls = a.pre_Lpart;
+      row = pre_row + 256ll * i;
+    }
+    const float L = Ls[row];
     float x[E];
-    const float* src = a.Opart + row * D + lane * E;
+    const float* src = O + row * D + lane * E;
     if constexpr (E == 4) {
       const float4 v = *reinterpret_cast<const float4*>(src);
       x[0] = v.x; x[1] = v.y; x[2 % E] = v.z; x[3 % E] = v.w;
@@ -698,19 +709,25 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const __
 template <int D, int MT>
 cudaError_t launch(const PagedDecodeArgs& a, unsigned merge_blocks, cudaStream_t st) {
   using C = Cfg<D, MT>;
-  decode_paged_kernel<D, MT><<<(unsigned)a.ctas, C::THREADS, C::SMEM_ALLOC, st>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  // set up while the main kernel runs (programmatic dependent launch)
+  // programmatic dependent launches: the own keys' kernel takes the SMs that a
+  // prefix's kernel leaves idle (and waits for that kernel's end before its
+  // own), the merge is set up while the main kernel runs
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(merge_blocks);
-  cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.stream = st;
   cfg.attrs = &attr;
+  cfg.numAttrs = a.pre_splits > 0 ? 1 : 0;
+  cfg.gridDim = dim3((unsigned)a.ctas);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM_ALLOC;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_paged_kernel<D, MT>, a);
+  if (e != cudaSuccess) return e;
   cfg.numAttrs = 1;
+  cfg.gridDim = dim3(merge_blocks);
+  cfg.blockDim = dim3(32 * kMergeWarps);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, decode_merge_kernel<D>, a);
 }
 
@@ -755,19 +772,30 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 PagedLayout paged_layout(int B, int Hkv, int rows, int prefix_len, int d) {
   PagedLayout L{};
   const long long pre_rows = prefix_len > 0 ? (long long)B * rows : 0;
-  const long long most = pre_rows > rows ? pre_rows : rows;
+  const bool own_kernel = pre_rows > kPagedMaxRows;
+  const long long most = pre_rows > rows && !own_kernel ? pre_rows : rows;
   const int mt = most <= 16 ? 1 : most <= 32 ? 2 : 4;
   L.ctas = resident_ctas(d, mt);
   if (L.ctas <= 0) return L;
   L.slot_rows = 16 * mt;
-  const long long blocks = (pre_rows + L.slot_rows - 1) / L.slot_rows;
-  L.n_seq = (int)(B + blocks);
+  L.n_seq = B + (pre_rows > 0 && !own_kernel ? 1 : 0);
   const size_t units = (size_t)L.n_seq * Hkv;
   const size_t slots = 2 * (size_t)L.ctas + (prefix_len > 0 ? units : 0);
   L.lpart = up256(slots * L.slot_rows * d * sizeof(float));
   L.unit_ctas = L.lpart + up256(slots * L.slot_rows * sizeof(float));
   L.begun = L.unit_ctas + up256(units * sizeof(int2));
-  L.total = L.begun + up256((size_t)L.ctas * sizeof(long long));
+  L.total = L.pre_opart = L.begun + up256((size_t)L.ctas * sizeof(long long));
+  if (own_kernel) {
+    const long long pre_units = (pre_rows + 255) / 256 * Hkv;
+    L.pre_splits = plan_prefix_splits(pre_units, (int)(((long long)prefix_len + 127) / 128), fwd_slots());
+    if (L.pre_splits < 1) {
+      L.ctas = 0;
+      return L;
+    }
+    const size_t parts = (size_t)pre_units * L.pre_splits * 256;
+    L.pre_lpart = L.pre_opart + up256(parts * d * sizeof(float));
+    L.total = L.pre_lpart + up256(parts * sizeof(float));
+  }
   return L;
 }
 
