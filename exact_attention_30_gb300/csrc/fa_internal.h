@@ -244,6 +244,22 @@ bool encode_part_f32(CUtensorMap* m, void* ptr, long long rows, int d);
 // boxes of 64 columns x box_rows rows of one page, 128-byte swizzle.
 bool encode_pool_bf16(CUtensorMap* m, const PagedPool& pool, bool values, int d, int box_rows);
 
+// n / d for 0 <= n < 2^31 by a multiplication (the round-up method: mul =
+// floor(2^32 (2^shift - d) / d) + 1, shift = ceil(log2 d)).
+struct FastDiv {
+  unsigned mul, shift;
+#ifdef __CUDACC__
+  __device__ __forceinline__ int operator()(int n) const {
+    return (int)((__umulhi((unsigned)n, mul) + (unsigned)n) >> shift);
+  }
+#endif
+};
+inline FastDiv fast_div(unsigned d) {
+  unsigned shift = 0;
+  while ((1ull << shift) < d) ++shift;
+  return FastDiv{(unsigned)(((1ull << 32) * ((1ull << shift) - d)) / d + 1), shift};
+}
+
 struct PagedDecodeArgs {
   CUtensorMap tmK, tmV;
   const void* Q;                   // bf16, element strides of batch, head, row below
@@ -256,15 +272,16 @@ struct PagedDecodeArgs {
   const int* prefix_pages;         // pages every sequence's keys begin with
   int prefix_len;                  // keys of the shared prefix (0: none)
   int B, G, Nq, max_pages;         // G query heads per K/V head
-  int box_rows;                    // rows per TMA box: divides page_size and 64
+  int box_shift;                   // log2 of the rows per TMA box, which divide page_size and 64
+  FastDiv page_div, nq_div, rows_div, ctas_div;  // by page_size, Nq, G * Nq, ctas
   // schedule and scratch (paged_layout)
   int ctas;                        // grid; shares of the keys
   int n_seq;                       // B, or B + 1: the prefix is the last sequence
   int slot_rows;                   // rows of a partial result's slot
   float* Opart;                    // fp32 [slots][slot_rows][d], normalised
   float* Lpart;                    // fp32 [slots][slot_rows], base-2 log-sum-exp
-  int2* unit_ctas;                 // [n_seq * Hkv] first and last CTA of a unit
-  long long* begun;                // [ctas] the unit that a CTA begins and does not end, or -1
+  int2* unit_ctas;                 // [n_seq * Hkv] with a prefix: first and last CTA of a unit
+  int2* begun;                     // [ctas] no prefix: the unit that a CTA begins and does not end, or -1; its last CTA
   // A prefix of many rows runs as a kernel of its own (launch_prefix_bf16),
   // whose pre_splits partial results per row lie here; 0: it is part of n_seq.
   int pre_splits;

@@ -103,19 +103,22 @@ fa_status decode_impl(const void* Q, const long long* q_strides, const fa_paged_
   a.status = device_status_ptr();
   if (!a.status) return FA_ERR_CUDA;
   // boxes never cross a page's end: the largest power of two (>= 8) in the page size, up to a tile
-  a.box_rows = cache->page_size & -cache->page_size;
-  if (a.box_rows > 64) a.box_rows = 64;
-  if (!encode_pool_bf16(&a.tmK, a.pool, false, cache->d, a.box_rows) ||
-      !encode_pool_bf16(&a.tmV, a.pool, true, cache->d, a.box_rows))
+  while (a.box_shift < 6 && cache->page_size % (2 << a.box_shift) == 0) ++a.box_shift;
+  if (!encode_pool_bf16(&a.tmK, a.pool, false, cache->d, 1 << a.box_shift) ||
+      !encode_pool_bf16(&a.tmV, a.pool, true, cache->d, 1 << a.box_shift))
     return FA_ERR_CUDA;
   char* ws = static_cast<char*>(workspace);
   a.ctas = L.ctas;
+  a.page_div = fast_div((unsigned)cache->page_size);
+  a.nq_div = fast_div((unsigned)Nq);
+  a.rows_div = fast_div((unsigned)(Hq / cache->kv_heads * Nq));
+  a.ctas_div = fast_div((unsigned)L.ctas);
   a.n_seq = L.n_seq;
   a.slot_rows = L.slot_rows;
   a.Opart = reinterpret_cast<float*>(ws);
   a.Lpart = reinterpret_cast<float*>(ws + L.lpart);
   a.unit_ctas = reinterpret_cast<int2*>(ws + L.unit_ctas);
-  a.begun = reinterpret_cast<long long*>(ws + L.begun);
+  a.begun = reinterpret_cast<int2*>(ws + L.begun);
   a.Q = Q;
   a.O = O;
   a.LSE = LSE;

@@ -12,7 +12,7 @@
 // against its keys, in tiles of 64. All units' tiles are laid end to end and
 // cut into equal shares, one per resident CTA, so a batch of very different
 // lengths fills the GPU evenly and one long sequence is spread over all of it.
-// The lengths live on the device, so each CTA finds its share itself (a block
+// The lengths live on the device, so each CTA finds its share itself (a warp's
 // scan over the lengths). A share may end inside a unit; such a unit's pieces
 // leave normalised fp32 partial results and base-2 log-sum-exps in the
 // workspace, at most two per CTA, and decode_merge_kernel combines them in a
@@ -47,6 +47,8 @@ namespace fa {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
+// What beginning and ending a unit costs, in tiles, when the keys are shared out
+constexpr int kUnitSteps = 2;
 // tolerated growth of a row's maximum (log2 units) before its output is rescaled
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kLn2 = 0.69314718055994531f;
@@ -68,11 +70,18 @@ struct Cfg {
   // share an SM, one loading while the other one merges. More rows: one CTA.
   static constexpr bool MERGE_IN_STAGE = MT == 1;
   static constexpr int CTAS = MT == 1 ? 2 : 1;
-  static constexpr int STAGES = (MT == 1 ? 3 : MT == 2 ? 5 : 4) * (D == 128 ? 1 : 2);
+  static constexpr int STAGES = (MT == 2 ? 4 : 3) * (D == 128 ? 1 : 2);
+  // Four groups of 16 rows leave 96 registers per thread: their queries stay
+  // in shared memory, and key and value fragments are loaded one at a time
+  // (else four).
+  static constexpr bool LEAN = MT == 4;
+  static constexpr int QBUF = 16 * MT * D * 2;  // a unit's queries; two, one being filled for the next unit
   static constexpr int OFF_MERGE = STAGES * STAGE;
-  static constexpr int OFF_ML = OFF_MERGE + (MERGE_IN_STAGE ? 0 : MT * MERGE);  // fp32 m, l [MT][4][16]
-  static constexpr int OFF_SCAN = OFF_ML + MT * 4 * 16 * 8;  // int64 [32] warp sums, share start
-  static constexpr int OFF_BAR = OFF_SCAN + 48 * 8;
+  static constexpr int OFF_Q = OFF_MERGE + (MERGE_IN_STAGE ? 0 : MT * MERGE);
+  static constexpr int OFF_ML = OFF_Q + 2 * QBUF;               // fp32 m, l [MT][4][16]
+  static constexpr int OFF_ROWS = OFF_ML + MT * 4 * 16 * 8;     // RowInfo [2][16 MT]: own keys, prefix
+  static constexpr int OFF_SHARE = OFF_ROWS + 2 * 16 * MT * 24;  // the CTA's Share
+  static constexpr int OFF_BAR = OFF_SHARE + 48;
   static constexpr int SMEM = OFF_BAR + 2 * STAGES * 8;
   static constexpr int SMEM_ALLOC = SMEM + 1024;  // base rounded up to 1024 (swizzle atom)
   static_assert(!MERGE_IN_STAGE || MERGE <= STAGE, "merge space");
@@ -94,11 +103,15 @@ __device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], uint32_t addr) {
 // c[16 rows x 8] += a[16 x 16] b[16 x 8], bf16 in, fp32 out. Lane 4g + q holds
 // c rows g (0, 1) and g + 8 (2, 3), columns 2q, 2q + 1.
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// 16 bytes global -> shared by this thread's copy groups; zeros unless `valid`.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void named_bar(int id, int count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
@@ -115,71 +128,93 @@ __device__ __forceinline__ int seq_keys(const PagedDecodeArgs& a, int s) {
   return n;
 }
 
-// The share of CTA w: tiles [t0, t1) of all units' tiles laid end to end,
-// and where t0 lies.
-struct Share {
-  long long left;  // tiles
-  int seq;         // sequence of the first tile
-  int head, tile;  // K/V head and tile within the unit
+// Where row r of a unit lies: offsets of its query and output from those of
+// the unit's first batch entry and head, and how many of the newest keys it
+// does not see. Row r is new token r mod Nq of the unit's query head r / Nq; a
+// prefix's rows are those of sequence 0, 1, ...
+struct RowInfo {
+  long long q, o;
+  int hidden;
 };
 
+// CTA w of W takes steps [begin(w), begin(w + 1)) of T: T / W each, the first
+// T mod W one more.
+struct Cut {
+  long long per, extra;
+  __device__ __forceinline__ Cut(const PagedDecodeArgs& a, long long T) {
+    if (T < (1ll << 31)) per = a.ctas_div((int)T);  // always, but for caches of terabytes
+    else per = T / a.ctas;
+    extra = T - per * a.ctas;
+  }
+  __device__ __forceinline__ long long begin(long long w) const { return w * per + (w < extra ? w : extra); }
+  // the CTA that has step t
+  __device__ __forceinline__ int owner(long long t) const {
+    const long long longer = extra * (per + 1);
+    if (t < longer) return t < (1ll << 31) ? (int)t / (int)(per + 1) : (int)(t / (per + 1));
+    t -= longer;
+    return (int)extra + (t < (1ll << 31) ? (int)t / (int)per : (int)(t / per));
+  }
+};
+
+// A unit's steps: one per tile and kUnitSteps for what it costs to begin and
+// end one (queries, merge, output); its tiles are its last steps.
+__device__ __forceinline__ int unit_steps(int keys, int bk) { return keys > 0 ? (keys + bk - 1) / bk + kUnitSteps : 0; }
+
+// The share of a CTA, and where its first step lies.
+struct Share {
+  long long left;  // steps
+  long long at;    // first step among all
+  long long T;     // all steps
+  int seq;         // sequence of the first step
+  int head, step;  // K/V head and step within the unit
+};
+
+// Found by one warp: each lane adds up the steps of a run of sequences.
 template <class C>
-__device__ __forceinline__ Share find_share(const PagedDecodeArgs& a, uint8_t* smem) {
-  long long* warp_sum = reinterpret_cast<long long*>(smem + C::OFF_SCAN);  // [32]
-  int* start = reinterpret_cast<int*>(smem + C::OFF_SCAN + 32 * 8);        // seq, head, tile
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int WARPS = C::THREADS / 32;
-  const int chunk = (a.n_seq + C::THREADS - 1) / C::THREADS;
-  const int s0 = min(tid * chunk, a.n_seq), s1 = min(s0 + chunk, a.n_seq);
+__device__ __forceinline__ Share find_share(const PagedDecodeArgs& a, int lane) {
+  const int chunk = (a.n_seq + 31) >> 5;
+  const int s0 = min(lane * chunk, a.n_seq), s1 = min(s0 + chunk, a.n_seq);
   long long sum = 0;
-  for (int s = s0; s < s1; ++s) sum += (seq_keys(a, s) + C::BK - 1) / C::BK;
+  for (int s = s0; s < s1; ++s) sum += unit_steps(seq_keys(a, s), C::BK);
   long long incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long v = __shfl_up_sync(kFull, incl, o);
     if (lane >= o) incl += v;
   }
-  if (lane == 31) warp_sum[warp] = incl;
-  __syncthreads();
-  long long before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
-    const long long v = warp_sum[w];
-    before += w < warp ? v : 0;
-    total += v;
-  }
   const int Hkv = a.pool.kv_heads;
-  const long long T = total * Hkv;
-  const long long W = T < (long long)gridDim.x ? T : (long long)gridDim.x;  // CTAs with work
-  const long long w = blockIdx.x;
-  Share sh{0, 0, 0, 0};
-  if (w < W) {
-    const long long t0 = T * w / W;
-    sh.left = T * (w + 1) / W - t0;
-    const long long hi = (before + incl) * Hkv, lo = hi - sum * Hkv;
-    if (lo <= t0 && t0 < hi) {  // t0 lies in this thread's chunk of sequences
-      long long at = t0 - lo;
-      for (int s = s0; s < s1; ++s) {
-        const long long n = (seq_keys(a, s) + C::BK - 1) / C::BK;
-        if (at < n * Hkv) {
-          start[0] = s;
-          start[1] = (int)(at / n);
-          start[2] = (int)(at - at / n * n);
-          break;
-        }
-        at -= n * Hkv;
+  Share sh;
+  sh.T = __shfl_sync(kFull, incl, 31) * Hkv;
+  const Cut cut(a, sh.T);
+  sh.at = cut.begin(blockIdx.x);
+  sh.left = cut.begin(blockIdx.x + 1) - sh.at;
+  const long long hi = incl * Hkv, lo = hi - sum * Hkv;
+  const bool here = lo <= sh.at && sh.at < hi;  // the first step lies in this lane's sequences
+  int seq = 0, head = 0, step = 0;
+  if (here) {
+    long long at = sh.at - lo;
+    for (int s = s0; s < s1; ++s) {
+      const int n = unit_steps(seq_keys(a, s), C::BK);
+      const long long all = (long long)n * Hkv;
+      if (at < all) {
+        head = all < (1ll << 31) ? (int)at / n : (int)(at / n);
+        step = (int)(at - (long long)head * n);
+        seq = s;
+        break;
       }
+      at -= all;
     }
   }
-  __syncthreads();
-  sh.seq = start[0];
-  sh.head = start[1];
-  sh.tile = start[2];
+  const unsigned who = __ballot_sync(kFull, here);
+  const int src = who ? __ffs(who) - 1 : 0;
+  sh.seq = __shfl_sync(kFull, seq, src);
+  sh.head = __shfl_sync(kFull, head, src);
+  sh.step = __shfl_sync(kFull, step, src);
   return sh;
 }
 
-// Walks a share piece by piece (a piece: a unit's tiles within the share);
-// producer and consumers walk the same way.
+// Walks a share unit by unit; the producer and the consumers walk alike. A
+// piece may hold no tile (a share that ends before a unit's first one).
 struct Walk {
   Share sh;
   int len, tiles, next_len;
@@ -188,29 +223,43 @@ struct Walk {
     tiles = (len + bk - 1) / bk;
     next_len = sh.seq + 1 < a.n_seq ? seq_keys(a, sh.seq + 1) : 0;  // on its way while this one is worked on
   }
-  __device__ __forceinline__ void begin(const PagedDecodeArgs& a, const Share& s, int bk) {
+  // false: nothing to do
+  __device__ __forceinline__ bool begin(const PagedDecodeArgs& a, const Share& s, int bk) {
     sh = s;
-    len = s.left > 0 ? seq_keys(a, s.seq) : 0;
+    if (sh.left <= 0) return false;
+    len = seq_keys(a, s.seq);
     load(a, bk);
+    return tile_count() > 0 || advance(a, bk);
   }
-  __device__ __forceinline__ int piece() const {
-    const int n = tiles - sh.tile;
-    return sh.left < n ? (int)sh.left : n;
+  __device__ __forceinline__ int first_tile() const { return max(0, sh.step - kUnitSteps); }
+  __device__ __forceinline__ int tile_count() const {
+    const long long end = sh.left < tiles + kUnitSteps - sh.step ? sh.step + sh.left : tiles + kUnitSteps;
+    return max(0, (int)end - kUnitSteps) - first_tile();
   }
-  __device__ __forceinline__ void advance(const PagedDecodeArgs& a, int n, int bk) {
-    sh.left -= n;
-    sh.tile = 0;
-    if (sh.left <= 0 || ++sh.head < a.pool.kv_heads) return;
-    sh.head = 0;
+  // first step of this unit among all
+  __device__ __forceinline__ long long unit_at() const { return sh.at - sh.step; }
+  // to the next piece with a tile; false at the share's end
+  __device__ __forceinline__ bool advance(const PagedDecodeArgs& a, int bk) {
     do {
-      ++sh.seq;
-      len = next_len;
-      load(a, bk);
-    } while (len == 0 && sh.seq + 1 < a.n_seq);
+      const int n = tiles + kUnitSteps - sh.step;
+      sh.left -= n;
+      sh.at += n;
+      sh.step = 0;
+      if (sh.left <= 0) return false;
+      if (++sh.head >= a.pool.kv_heads) {
+        sh.head = 0;
+        do {
+          if (++sh.seq >= a.n_seq) return false;
+          len = next_len;
+          load(a, bk);
+        } while (len == 0);
+      }
+    } while (tile_count() <= 0);
+    return true;
   }
 };
 
-// Partial result of unit u's piece in CTA w. A piece that begins its unit and
+// Slot of the partial result of a unit's piece in CTA w. A piece that begins its unit and
 // does not end it: the CTA's second slot; one that continues a unit: the
 // first. Units of one piece that still need a merge (with a prefix's part)
 // have slots of their own behind those.
@@ -221,9 +270,9 @@ __device__ __forceinline__ long long part_slot(const PagedDecodeArgs& a, int w, 
 
 // All rows of sequence s: no key, so O = 0 and LSE = -inf.
 template <int D>
-__device__ void empty_rows(const PagedDecodeArgs& a, int s) {
+__device__ __noinline__ void empty_rows(const PagedDecodeArgs& a, int s, int thread, int threads) {
   const int Hq = a.pool.kv_heads * a.G, rows = Hq * a.Nq;
-  for (long long e = threadIdx.x; e < (long long)rows * (D / 8); e += blockDim.x) {
+  for (long long e = thread; e < (long long)rows * (D / 8); e += threads) {
     const int row = (int)(e / (D / 8)), c = (int)(e - (long long)row * (D / 8)) * 8;
     const int hq = row / a.Nq, i = row - hq * a.Nq;
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.O) + s * a.o_b + hq * a.o_h + i * a.o_r + c) = make_uint4(0u, 0u, 0u, 0u);
@@ -252,80 +301,95 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
   }
   // the merge kernel may be set up meanwhile; it waits for this grid's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const Share share = find_share<C>(a, smem);
-  if (a.prefix_len == 0) {
-    if (threadIdx.x == 0) a.begun[blockIdx.x] = -1;
-    // rows of sequences without keys
-    for (int s = blockIdx.x; s < a.B; s += gridDim.x)
-      if (seq_keys(a, s) == 0) empty_rows<D>(a, s);
-    __syncthreads();  // begun[] may be written again below, by another thread
+  const int Hkv = a.pool.kv_heads, R = a.G * a.Nq;
+  RowInfo* row_info = reinterpret_cast<RowInfo*>(smem + C::OFF_ROWS);
+  Share* shared_share = reinterpret_cast<Share*>(smem + C::OFF_SHARE);
+  if (warp == 0) {
+    const Share found = find_share<C>(a, lane);
+    if (lane == 0) *shared_share = found;
+  } else {
+    for (int e = threadIdx.x - 32; e < (a.prefix_len > 0 ? 2 : 1) * 16 * MT; e += C::THREADS - 32) {
+      const int p = e & (16 * MT - 1);
+      const int b = e < 16 * MT ? 0 : a.rows_div(p), r = p - b * R, g = a.nq_div(r), i = r - g * a.Nq;
+      row_info[e] = RowInfo{b * a.q_b + g * a.q_h + i * a.q_r, b * a.o_b + g * a.o_h + i * a.o_r,
+                            e < 16 * MT ? a.Nq - 1 - i : 0};
+    }
   }
-  if (share.left <= 0) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // as at the end
-    return;
-  }
+  __syncthreads();
   Walk wk;
-  wk.begin(a, share, C::BK);
+  const bool any = wk.begin(a, *shared_share, C::BK);
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    const int nbox = C::BK / a.box_rows;      // boxes of a chunk's 64 rows
+    if (lane == 0 && a.prefix_len == 0) a.begun[blockIdx.x] = make_int2(-1, 0);
+    if (!any) return;
+    const int nbox = C::BK >> a.box_shift;    // boxes of a chunk's 64 rows
     const bool mine = lane < nbox * 2 * C::CH;
-    const int box = lane % nbox, col = lane / nbox;  // this lane's box; keys' chunks, then values'
+    const int box = lane & (nbox - 1), col = lane >> (6 - a.box_shift);  // this lane's box; keys' chunks, then values'
     const bool is_v = col >= C::CH;
     const int chunk = is_v ? col - C::CH : col;
     const CUtensorMap* map = is_v ? &a.tmV : &a.tmK;
-    const uint32_t dst0 = sbase + (is_v ? C::KV : 0) + chunk * C::CHUNK + box * a.box_rows * 128;
+    const uint32_t dst0 = sbase + (is_v ? C::KV : 0) + chunk * C::CHUNK + ((box * 128) << a.box_shift);
     if (lane == 0) {
       tma_prefetch_desc(&a.tmK);
       tma_prefetch_desc(&a.tmV);
     }
-    const int ps = a.pool.page_size;
-    int it = 0;
-    bool ok = true;
-    while (ok && wk.sh.left > 0 && wk.piece() > 0) {
-      const int n = wk.piece(), len = wk.len, head = wk.sh.head, first = wk.sh.tile;
-      const int* table = wk.sh.seq < a.B ? a.block_tables + (long long)wk.sh.seq * a.max_pages : a.prefix_pages;
-      // page and row of this lane's box, a tile ahead
-      auto look_up = [&](int tile, int& page, int& row) {
-        const int key = tile * C::BK + box * a.box_rows;
-        page = -1;
-        row = 0;
-        if (mine && key < len) {
-          const int pi = key / ps;
-          row = key - pi * ps;
-          page = __ldg(table + pi);
-        }
-      };
-      int page, row;
-      look_up(first, page, row);
-      for (int j = 0; j < n; ++j, ++it) {
-        const int s = it % C::STAGES;
-        const int left = len - (first + j) * C::BK;  // keys from this tile on
-        const int boxes = left >= C::BK ? nbox : (left + a.box_rows - 1) / a.box_rows;
-        int next_page = -1, next_row = 0;
-        if (j + 1 < n) look_up(first + j + 1, next_page, next_row);
-        if (!mbar_wait_warp(EMPTY(s), ((it / C::STAGES) & 1) ^ 1, a.status, a.wait_limit_ns)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) mbar_arrive_expect_tx(FULL(s), (uint32_t)(boxes * a.box_rows * 128 * 2 * C::CH));
-        __syncwarp();
-        if (mine && box < boxes) {
-          if (page < 0 || page >= a.pool.num_pages) {
-            report_status(a.status, kStatusBadSeqlens);
-            page = a.pool.num_pages;  // outside the tensor: reads as zeros
-          }
-          tma_load_4d(dst0 + s * C::STAGE, map, FULL(s), chunk * 64, row, head, page);
-        }
-        page = next_page;
-        row = next_row;
+    const Cut cut(a, wk.sh.T);
+    // a tile's boxes, and page, row and head of this lane's; looked up one
+    // tile ahead, across units too
+    struct Tile {
+      int boxes, page, row, head;
+    };
+    auto look_up = [&](int tile) {
+      Tile t;
+      const int key0 = tile * C::BK, left = wk.len - key0;
+      t.boxes = left >= C::BK ? nbox : (left + (1 << a.box_shift) - 1) >> a.box_shift;
+      t.page = -1;
+      t.row = 0;
+      t.head = wk.sh.head;
+      if (mine && box < t.boxes) {
+        const int* table = wk.sh.seq < a.B ? a.block_tables + (long long)wk.sh.seq * a.max_pages : a.prefix_pages;
+        const int key = key0 + (box << a.box_shift), pi = a.page_div(key);
+        t.row = key - pi * a.pool.page_size;
+        t.page = __ldg(table + pi);
       }
-      wk.advance(a, n, C::BK);
+      return t;
+    };
+    int tile = wk.first_tile(), tile_end = tile + wk.tile_count(), it = 0;
+    Tile t = look_up(tile);
+    for (bool more = true; more; ++it) {
+      if (tile == 0 && lane == 0) {
+        // this CTA begins the unit; the one that has its last step ends it
+        const long long end = wk.unit_at() + kUnitSteps + wk.tiles;
+        const bool whole = end <= wk.sh.at + wk.sh.left;
+        if (a.prefix_len > 0 || !whole) {
+          const int unit = wk.sh.seq * Hkv + wk.sh.head, last = whole ? (int)blockIdx.x : cut.owner(end - 1);
+          if (a.prefix_len > 0) a.unit_ctas[unit] = make_int2(blockIdx.x, last);
+          else a.begun[blockIdx.x] = make_int2(unit, last);
+        }
+      }
+      if (++tile == tile_end) {
+        more = wk.advance(a, C::BK);
+        tile = wk.first_tile();
+        tile_end = tile + wk.tile_count();
+      }
+      const Tile next = more ? look_up(tile) : t;
+      const int s = it % C::STAGES;
+      if (!mbar_wait_warp(EMPTY(s), ((it / C::STAGES) & 1) ^ 1, a.status, a.wait_limit_ns)) break;
+      if (lane == 0) mbar_arrive_expect_tx(FULL(s), (uint32_t)((t.boxes * 128 * 2 * C::CH) << a.box_shift));
+      __syncwarp();
+      if (mine && box < t.boxes) {
+        if (t.page < 0 || t.page >= a.pool.num_pages) {
+          report_status(a.status, kStatusBadSeqlens);
+          t.page = a.pool.num_pages;  // outside the tensor: reads as zeros
+        }
+        tma_load_4d(dst0 + s * C::STAGE, map, FULL(s), chunk * 64, t.row, t.head, t.page);
+      }
+      t = next;
     }
     // copies in flight land before the CTA ends, also when a wait ran out
-    for (int t = it - C::STAGES < 0 ? 0 : it - C::STAGES; t < it; ++t)
-      mbar_wait_warp(FULL(t % C::STAGES), (t / C::STAGES) & 1, a.status, a.wait_limit_ns);
+    for (int u = it - C::STAGES < 0 ? 0 : it - C::STAGES; u < it; ++u)
+      mbar_wait_warp(FULL(u % C::STAGES), (u / C::STAGES) & 1, a.status, a.wait_limit_ns);
     return;
   }
 
@@ -334,56 +398,53 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
   // it still reaches every barrier; the status word tells.
   const int cw = warp - 1, mt = cw >> 2, kw = cw & 3;
   const int g = lane >> 2, q = lane & 3;
-  const int Hkv = a.pool.kv_heads, Hq = Hkv * a.G, R = a.G * a.Nq;
+  const int ct = kw * 32 + lane;  // thread of the 16 rows' 128
   const float c2 = a.scale_log2;
   const int ra = mt * 16 + g, rb = ra + 8;  // this lane's query rows
   float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML) + mt * 64;  // [4][16]
   const uint32_t k_off = (uint32_t)((kw * 16 + (lane >> 4) * 8 + (lane & 7)) * 128);
   const uint32_t v_off = (uint32_t)(C::KV + (kw * 16 + ((lane >> 3) & 1) * 8 + (lane & 7)) * 128);
   const uint32_t k_u = (lane >> 3) & 1, v_u = lane >> 4, sw = lane & 7;
-  bool ok = true;
-  int it = 0;
-  while (wk.sh.left > 0 && wk.piece() > 0) {
-    const int n = wk.piece(), first = wk.sh.tile, seq = wk.sh.seq, head = wk.sh.head, len = wk.len;
+  // A unit's 16 query rows, D / 8 vectors each, vector u of row r at u ^ (r & 7)
+  const uint32_t q_buf = sbase + C::OFF_Q + mt * 16 * D * 2;
+  const uint32_t q_off = (uint32_t)((((lane >> 3) & 1) * 8 + (lane & 7)) * D * 2), q_u = lane >> 4;
+  auto fetch_q = [&](int seq, int head, int buf) {
     const bool pre = seq >= a.B;
     const int rows = pre ? a.B * R : R;
-    // row r of this unit: batch entry, query head, new token
-    auto row_at = [&](int r, int& b, int& hq, int& i) {
-      b = seq;
-      if (pre) {
-        b = r / R;
-        r -= b * R;
-      }
-      i = r % a.Nq;
-      hq = head * a.G + r / a.Nq;
-    };
-    uint32_t qf[D / 16][4];
-    int lim_a = len, lim_b = len;  // keys that rows ra and rb see
-    {
-      int b, hq, i;
-      const uint32_t* qa = nullptr;
-      const uint32_t* qb = nullptr;
-      const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(a.Q);
-      if (ra < rows) {
-        row_at(ra, b, hq, i);
-        qa = reinterpret_cast<const uint32_t*>(Q + b * a.q_b + hq * a.q_h + i * a.q_r) + q;
-        if (!pre) lim_a = len - a.Nq + 1 + i;
-      }
-      if (rb < rows) {
-        row_at(rb, b, hq, i);
-        qb = reinterpret_cast<const uint32_t*>(Q + b * a.q_b + hq * a.q_h + i * a.q_r) + q;
-        if (!pre) lim_b = len - a.Nq + 1 + i;
-      }
+    const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(a.Q) + (pre ? 0 : seq * a.q_b) + (long long)head * a.G * a.q_h;
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        qf[ks][0] = qa ? __ldg(qa + ks * 8) : 0u;
-        qf[ks][1] = qb ? __ldg(qb + ks * 8) : 0u;
-        qf[ks][2] = qa ? __ldg(qa + ks * 8 + 4) : 0u;
-        qf[ks][3] = qb ? __ldg(qb + ks * 8 + 4) : 0u;
-      }
+    for (int e = ct; e < 16 * (D / 8); e += 128) {
+      const int r = e / (D / 8), u = e - r * (D / 8);
+      const bool valid = mt * 16 + r < rows;
+      const __nv_bfloat16* src = base + (valid ? row_info[(pre ? 16 * MT : 0) + mt * 16 + r].q + u * 8 : 0);
+      copy16(q_buf + buf * C::QBUF + r * (D * 2) + ((u ^ (r & 7)) << 4), src, valid);
     }
+  };
+  if (any) fetch_q(wk.sh.seq, wk.sh.head, 0);
+  if (a.prefix_len == 0) {
+    // rows of sequences without keys
+    for (int s = blockIdx.x; s < a.B; s += gridDim.x)
+      if (seq_keys(a, s) == 0) empty_rows<D>(a, s, threadIdx.x - 32, C::THREADS - 32);
+  }
+  bool ok = true;
+  int it = 0, qb = 0;
+  for (bool more = any; more; qb ^= 1) {
+    const int n = wk.tile_count(), first = wk.first_tile(), seq = wk.sh.seq, head = wk.sh.head, len = wk.len;
+    const bool begins = first == 0, ends = first + n == wk.tiles;
+    const bool pre = seq >= a.B;
+    const int rows = pre ? a.B * R : R;
+    const RowInfo* info = row_info + (pre ? 16 * MT : 0);
     const int seen = pre ? len : max(0, len - a.Nq + 1);  // keys that every row sees
     const bool active = mt * 16 < rows;                   // else these warps only keep step
+    copies_done();
+    named_bar(1 + mt, 128);  // this unit's queries are there; the other buffer has been read
+    uint32_t qf[C::LEAN ? 1 : D / 16][4];
+    if constexpr (!C::LEAN) {
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) ldmatrix4(qf[ks], q_buf + qb * C::QBUF + q_off + (((2 * ks + q_u) ^ sw) << 4));
+    }
+    more = wk.advance(a, C::BK);
+    if (more) fetch_q(wk.sh.seq, wk.sh.head, qb ^ 1);
     float acc[D / 8][4];
 #pragma unroll
     for (int nn = 0; nn < D / 8; ++nn) acc[nn][0] = acc[nn][1] = acc[nn][2] = acc[nn][3] = 0.f;
@@ -394,18 +455,40 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
       const int k0 = (first + j) * C::BK + kw * 16;  // this warp's keys
       if (ok && active && k0 < len) {
         const uint32_t st = sbase + s * C::STAGE;
-        float x[2][4];
+        // scores in two chains of products, each half of the head
+        float x[2][4], y[2][4];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.f;
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          uint32_t kf[4];
-          ldmatrix4(kf, st + k_off + (ks >> 2) * C::CHUNK + ((((2 * ks + k_u) & 7) ^ sw) << 4));
-          mma16816(x[0], qf[ks], kf[0], kf[1]);
-          mma16816(x[1], qf[ks], kf[2], kf[3]);
+          for (int c = 0; c < 4; ++c) x[t][c] = y[t][c] = 0.f;
+        auto k_at = [&](int ks) { return st + k_off + (ks >> 2) * C::CHUNK + ((((2 * ks + k_u) & 7) ^ sw) << 4); };
+        auto v_at = [&](int np) { return st + v_off + (np >> 2) * C::CHUNK + ((((2 * np + v_u) & 7) ^ sw) << 4); };
+        constexpr int FB = C::LEAN ? 1 : 4;  // fragments loaded at a time
+        uint32_t f[FB][4];                   // of K, then of V
+#pragma unroll
+        for (int k1 = 0; k1 < D / 16; k1 += FB) {
+#pragma unroll
+          for (int i = 0; i < FB; ++i) ldmatrix4(f[i], k_at(k1 + i));
+          if constexpr (C::LEAN) ldmatrix4(qf[0], q_buf + qb * C::QBUF + q_off + (((2 * k1 + q_u) ^ sw) << 4));
+#pragma unroll
+          for (int i = 0; i < FB; ++i) {
+            const uint32_t(&qk)[4] = qf[C::LEAN ? 0 : k1 + i];
+            mma16816(i & 1 ? y[0] : x[0], qk, f[i][0], f[i][1]);
+            mma16816(i & 1 ? y[1] : x[1], qk, f[i][2], f[i][3]);
+          }
         }
+        // the first values are on their way while the weights are computed
+#pragma unroll
+        for (int i = 0; i < FB; ++i) ldmatrix4_t(f[i], v_at(i));
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[t][c] += y[t][c];
         const bool edge = k0 + 16 > seen;  // some key of this warp is hidden from some row
+        int lim_a = len, lim_b = len;      // keys that rows ra and rb see
         if (edge) {
+          lim_a -= ra < rows ? info[ra].hidden : 0;
+          lim_b -= rb < rows ? info[rb].hidden : 0;
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -456,17 +539,22 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
           keep1 = keep(k0 + 8 + 2 * q);
         }
 #pragma unroll
-        for (int np = 0; np < D / 16; ++np) {
-          uint32_t vf[4];
-          ldmatrix4_t(vf, st + v_off + (np >> 2) * C::CHUNK + ((((2 * np + v_u) & 7) ^ sw) << 4));
-          if (edge) {
-            vf[0] &= keep0;
-            vf[1] &= keep1;
-            vf[2] &= keep0;
-            vf[3] &= keep1;
+        for (int n1 = 0; n1 < D / 16; n1 += FB) {
+          if (n1 > 0) {
+#pragma unroll
+            for (int i = 0; i < FB; ++i) ldmatrix4_t(f[i], v_at(n1 + i));
           }
-          mma16816(acc[2 * np], pf, vf[0], vf[1]);
-          mma16816(acc[2 * np + 1], pf, vf[2], vf[3]);
+#pragma unroll
+          for (int i = 0; i < FB; ++i) {
+            if (edge) {
+              f[i][0] &= keep0;
+              f[i][1] &= keep1;
+              f[i][2] &= keep0;
+              f[i][3] &= keep1;
+            }
+            mma16816(acc[2 * (n1 + i)], pf, f[i][0], f[i][1]);
+            mma16816(acc[2 * (n1 + i) + 1], pf, f[i][2], f[i][3]);
+          }
         }
         if (edge && len > seen) {
           // the newest keys, seen by some rows only: added row by row
@@ -497,10 +585,7 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
       if (lane == 0 && !(C::MERGE_IN_STAGE && j + 1 == n)) mbar_arrive(EMPTY(s));
     }
 
-    if (!active) {
-      wk.advance(a, n, C::BK);
-      continue;
-    }
+    if (!active) continue;
     // the four warps of each 16 rows meet: common maximum, then the sum of
     // their outputs, each already scaled by its share of the total
     l_a += __shfl_xor_sync(kFull, l_a, 1);
@@ -514,51 +599,50 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
     named_bar(1 + mt, 128);  // also: every warp has read its keys of the last stage
     float f_a, f_b, lse_a, lse_b;
     auto combine = [&](int r, float m_own, float& f, float& lse) {
-      float mm = -INFINITY, ll = 0.f;
+      float2 t[4];
 #pragma unroll
-      for (int w = 0; w < 4; ++w) mm = fmaxf(mm, ml[w * 16 + r].x);
+      for (int w = 0; w < 4; ++w) t[w] = ml[w * 16 + r];
+      const float mm = fmaxf(fmaxf(t[0].x, t[1].x), fmaxf(t[2].x, t[3].x));
       const float mu = mm == -INFINITY ? 0.f : mm;
+      float ll = 0.f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float2 t = ml[w * 16 + r];
-        ll = fmaf(t.y, ex2_approx(t.x - mu), ll);
-      }
-      f = ll == 0.f ? 0.f : ex2_approx(m_own - mu) / ll;
+      for (int w = 0; w < 4; ++w) ll = fmaf(t[w].y, ex2_approx(t[w].x - mu), ll);
+      f = ll == 0.f ? 0.f : __fdividef(ex2_approx(m_own - mu), ll);
       lse = ll == 0.f ? -INFINITY : mm + __log2f(ll);
     };
     combine(g, m_a, f_a, lse_a);
     combine(g + 8, m_b, f_b, lse_b);
     const int last_stage = (it - 1) % C::STAGES;
     float* om = reinterpret_cast<float*>(smem + (C::MERGE_IN_STAGE ? last_stage * C::STAGE : C::OFF_MERGE + mt * C::MERGE));
-    const bool begins = first == 0, ends = first + n == wk.tiles;
     const long long unit = (long long)seq * Hkv + head;
     const bool direct = begins && ends && a.prefix_len == 0;
-    const long long slot = part_slot(a, blockIdx.x, begins, ends, unit);
-    const int ct = kw * 32 + lane;  // thread of the 16 rows' 128
-    if (mt == 0 && ct == 0) {
-      if (begins) a.unit_ctas[unit].x = blockIdx.x;
-      if (ends) a.unit_ctas[unit].y = blockIdx.x;
-      if (begins && !ends) a.begun[blockIdx.x] = unit;
-    }
+    const long long part_row = part_slot(a, blockIdx.x, begins, ends, unit) * a.slot_rows;
+    const long long o_unit = (pre ? 0 : seq * a.o_b) + (long long)head * a.G * a.o_h;
     // row r's column c lies at c ^ 8 (r & 7): the eight rows of a store differ in banks
     constexpr int DW = C::DW;
     const int sg = (8 * g) & (DW - 1);
+    const int group_rows = min(16, rows - mt * 16);
 #pragma unroll
     for (int d0 = 0; d0 < D; d0 += DW) {
       if (d0 > 0) named_bar(1 + mt, 128);  // the columns before these have been read
+      if (g < group_rows) {
 #pragma unroll
-      for (int nn = 0; nn < DW / 8; ++nn) {
-        const float* x = acc[d0 / 8 + nn];
-        const int c = (8 * nn + 2 * q) ^ sg;
-        *reinterpret_cast<float2*>(om + (kw * 16 + g) * DW + c) = make_float2(x[0] * f_a, x[1] * f_a);
-        *reinterpret_cast<float2*>(om + (kw * 16 + g + 8) * DW + c) = make_float2(x[2] * f_b, x[3] * f_b);
+        for (int nn = 0; nn < DW / 8; ++nn) {
+          const float* x = acc[d0 / 8 + nn];
+          *reinterpret_cast<float2*>(om + (kw * 16 + g) * DW + ((8 * nn + 2 * q) ^ sg)) = make_float2(x[0] * f_a, x[1] * f_a);
+        }
+      }
+      if (g + 8 < group_rows) {
+#pragma unroll
+        for (int nn = 0; nn < DW / 8; ++nn) {
+          const float* x = acc[d0 / 8 + nn];
+          *reinterpret_cast<float2*>(om + (kw * 16 + g + 8) * DW + ((8 * nn + 2 * q) ^ sg)) = make_float2(x[2] * f_b, x[3] * f_b);
+        }
       }
       named_bar(1 + mt, 128);
-#pragma unroll
-      for (int e = ct; e < 16 * (DW / 4); e += 128) {
+      for (int e = ct; e < group_rows * (DW / 4); e += 128) {
         const int r = e / (DW / 4), c = (e - r * (DW / 4)) * 4;
         const int rr = mt * 16 + r;
-        if (rr >= rows) continue;
         const float* p = om + r * DW + (c ^ ((8 * r) & 56 & (DW - 1)));
         float4 y = *reinterpret_cast<const float4*>(p);
 #pragma unroll
@@ -570,25 +654,18 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
           y.w += z.w;
         }
         if (direct) {
-          int b, hq, i;
-          row_at(rr, b, hq, i);
-          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.O) + b * a.o_b + hq * a.o_h + i * a.o_r + d0 + c;
+          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.O) + o_unit + info[rr].o + d0 + c;
           *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
         } else {
-          *reinterpret_cast<float4*>(a.Opart + (slot * a.slot_rows + rr) * D + d0 + c) = y;
+          *reinterpret_cast<float4*>(a.Opart + (part_row + rr) * D + d0 + c) = y;
         }
       }
     }
     if (kw == 0 && q == 0) {
       auto put = [&](int r, float lse) {
         if (r >= rows) return;
-        if (direct) {
-          int b, hq, i;
-          row_at(r, b, hq, i);
-          a.LSE[((long long)b * Hq + hq) * a.Nq + i] = lse * kLn2;
-        } else {
-          a.Lpart[slot * a.slot_rows + r] = lse;
-        }
+        if (direct) a.LSE[unit * R + r] = lse * kLn2;
+        else a.Lpart[part_row + r] = lse;
       };
       put(ra, lse_a);
       put(rb, lse_b);
@@ -598,7 +675,6 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
       __syncwarp();
       if (lane == 0) mbar_arrive(EMPTY(last_stage));
     }
-    wk.advance(a, n, C::BK);
   }
   // a prefix's kernel ends before this one does, so the merge sees both
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -606,108 +682,142 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
 
 // Rows of units that were not written out directly: partial results of the
 // own keys (and of the prefix) merged by maximum and sum, in order of the
-// CTAs. One block per query row, one warp per partial result at a time.
+// CTAs. WPR warps share a row, each taking every WPR-th partial result, and
+// meet in shared memory: without a prefix few rows have parts, but a long
+// sequence has one from each of many CTAs (WPR = 4); with one every row has
+// parts, about as many as the prefix has key ranges (WPR = 1).
 constexpr int kMergeWarps = 4;
-template <int D>
+template <int D, int WPR>
 __global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const __grid_constant__ PagedDecodeArgs a) {
   constexpr int E = D / 32;
+  constexpr int AHEAD = 4;  // partial results in flight per warp
   __shared__ float sm[kMergeWarps], sl[kMergeWarps], so[kMergeWarps][D];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % WPR;
   const int Hkv = a.pool.kv_heads, R = a.G * a.Nq;
-  const int r = (int)(blockIdx.x % R);
-  // without a prefix only the units that a share's end cuts have parts
-  const long long unit = a.prefix_len == 0 ? a.begun[blockIdx.x / R] : blockIdx.x / R;
-  if (unit < 0) return;
-  const int b = (int)(unit / Hkv), head = (int)(unit - (long long)b * Hkv);
-  int own_first = 0, own_n = 0;
-  if (seq_keys(a, b) > 0) {
-    const int2 c = a.unit_ctas[unit];
+  const unsigned item = blockIdx.x * (kMergeWarps / WPR) + warp / WPR;
+  const unsigned group = item / (unsigned)R;
+  const int r = (int)(item - group * (unsigned)R);
+  int unit, own_first, own_n, pre_first = 0, pre_n = 0;
+  long long pre_row = 0;  // a prefix's kernel of its own: row of the first part, parts 256 rows apart
+  int b, head;
+  if (WPR > 1) {
+    // without a prefix only the units that a share's end cuts have parts
+    const int2 c = a.begun[group];
+    if (c.x < 0) return;  // the whole block
+    unit = c.x;
+    own_first = (int)group;
+    own_n = c.y - own_first + 1;
+    b = unit / Hkv;
+    head = unit - b * Hkv;
+  } else {
+    if (item >= (unsigned)(a.B * Hkv) * (unsigned)R) return;
+    unit = (int)group;
+    b = unit / Hkv;
+    head = unit - b * Hkv;
+    const int2 c = a.unit_ctas[unit];  // not written for a sequence without keys
     own_first = c.x;
-    own_n = c.y - c.x + 1;
-  }
-  int pre_first = 0, pre_n = 0;
-  const long long pre_unit = (long long)a.B * Hkv + head;
-  long long pre_row = 0;  // kernel of its own: row of the first part, parts 256 rows apart
-  if (a.pre_splits > 0) {
-    const int rr = b * R + r, qblocks = (a.B * R + 255) / 256;
-    pre_n = a.pre_splits;
-    pre_row = ((long long)head * qblocks + rr / 256) * a.pre_splits * 256 + rr % 256;
-  } else if (a.prefix_len > 0) {
-    const int2 c = a.unit_ctas[pre_unit];
-    pre_first = c.x;
-    pre_n = c.y - c.x + 1;
+    own_n = seq_keys(a, b) > 0 ? c.y - c.x + 1 : 0;
+    if (a.pre_splits > 0) {
+      const int rr = b * R + r, qblocks = (a.B * R + 255) / 256;
+      pre_n = a.pre_splits;
+      pre_row = ((long long)head * qblocks + rr / 256) * a.pre_splits * 256 + rr % 256;
+    } else {
+      const int2 cp = a.unit_ctas[a.B * Hkv + head];
+      pre_first = cp.x;
+      pre_n = cp.y - cp.x + 1;
+    }
   }
   float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int p = warp; p < own_n + pre_n; p += kMergeWarps) {
-    const bool own = p < own_n;
-    const int i = own ? p : p - own_n;
-    const float* O = a.Opart;
-    const float* Ls = a.Lpart;
-    long long row;
-    if (own || a.pre_splits == 0) {
-      const long long slot = part_slot(a, (own ? own_first : pre_first) + i, i == 0, i + 1 == (own ? own_n : pre_n), own ? unit : pre_unit);
-      row = slot * a.slot_rows + (own ? r : b * R + r);
-    } else {
-      O = a.pre_Opart;
-      Ls = a.pre_Lpart;
-      row = pre_row + 256ll * i;
+  const int n = own_n + pre_n;
+  for (int p0 = part; p0 < n; p0 += AHEAD * WPR) {
+    float L[AHEAD], x[AHEAD][E];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int p = p0 + k * WPR;
+      L[k] = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[k][e] = 0.f;
+      if (p >= n) continue;
+      const bool own = p < own_n;
+      const int i = own ? p : p - own_n;
+      const float* O = a.Opart;
+      const float* Ls = a.Lpart;
+      long long row;
+      if (own || a.pre_splits == 0) {
+        const int u = own ? unit : a.B * Hkv + head;
+        const long long slot = part_slot(a, (own ? own_first : pre_first) + i, i == 0, i + 1 == (own ? own_n : pre_n), u);
+        row = slot * a.slot_rows + (own ? r : b * R + r);
+      } else {
+        O = a.pre_Opart;
+        Ls = a.pre_Lpart;
+        row = pre_row + 256ll * i;
+      }
+      L[k] = Ls[row];
+      const float* src = O + row * D + lane * E;
+      if constexpr (E == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        x[k][0] = v.x; x[k][1] = v.y; x[k][2 % E] = v.z; x[k][3 % E] = v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        x[k][0] = v.x; x[k][1] = v.y;
+      }
     }
-    const float L = Ls[row];
-    float x[E];
-    const float* src = O + row * D + lane * E;
-    if constexpr (E == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(src);
-      x[0] = v.x; x[1] = v.y; x[2 % E] = v.z; x[3 % E] = v.w;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(src);
-      x[0] = v.x; x[1] = v.y;
-    }
-    const float mn = fmaxf(m, L), mu = mn == -INFINITY ? 0.f : mn;
-    const float f = ex2_approx(m - mu), w = ex2_approx(L - mu);
+    float mn = m;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) mn = fmaxf(mn, L[k]);
+    const float mu = mn == -INFINITY ? 0.f : mn;
+    const float f = ex2_approx(m - mu);
     m = mn;
-    l = fmaf(l, f, w);
+    l *= f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], f, w * x[e]);
+    for (int e = 0; e < E; ++e) acc[e] *= f;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const float w = ex2_approx(L[k] - mu);
+      l += w;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(w, x[k][e], acc[e]);
+    }
   }
+  if constexpr (WPR > 1) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) so[warp][lane * E + e] = acc[e];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
+    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = acc[e];
+    if (lane == 0) {
+      sm[warp] = m;
+      sl[warp] = l;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) m = fmaxf(m, sm[w]);
+    const float mu = m == -INFINITY ? 0.f : m;
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) {
+      const float f = ex2_approx(sm[w] - mu);
+      l = fmaf(sl[w], f, l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(so[w][lane * E + e], f, acc[e]);
+    }
   }
-  __syncthreads();
-  if (warp != 0) return;
-  float mm = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) mm = fmaxf(mm, sm[w]);
-  const float mu = mm == -INFINITY ? 0.f : mm;
-  float ll = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) {
-    const float f = ex2_approx(sm[w] - mu);
-    ll = fmaf(sl[w], f, ll);
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(so[w][lane * E + e], f, acc[e]);
-  }
-  const float inv = ll == 0.f ? 0.f : 1.f / ll;
-  const int i = r % a.Nq, hq = head * a.G + r / a.Nq;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int g = r / a.Nq, i = r - g * a.Nq, hq = head * a.G + g;
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.O) + b * a.o_b + hq * a.o_h + i * a.o_r + lane * E;
   if constexpr (E == 4)
     *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2 % E] * inv, acc[3 % E] * inv));
   else
     *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-  if (lane == 0)
-    a.LSE[((long long)b * Hkv * a.G + hq) * a.Nq + i] = ll == 0.f ? -INFINITY : (mm + __log2f(ll)) * kLn2;
+  if (lane == 0) a.LSE[(long long)unit * R + r] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
 template <int D, int MT>
-cudaError_t launch(const PagedDecodeArgs& a, unsigned merge_blocks, cudaStream_t st) {
+cudaError_t launch(const PagedDecodeArgs& a, cudaStream_t st) {
   using C = Cfg<D, MT>;
   // programmatic dependent launches: the own keys' kernel takes the SMs that a
   // prefix's kernel leaves idle (and waits for that kernel's end before its
@@ -725,10 +835,15 @@ cudaError_t launch(const PagedDecodeArgs& a, unsigned merge_blocks, cudaStream_t
   const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_paged_kernel<D, MT>, a);
   if (e != cudaSuccess) return e;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(merge_blocks);
   cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, decode_merge_kernel<D>, a);
+  const unsigned rows = (unsigned)(a.G * a.Nq);
+  if (a.prefix_len == 0) {
+    cfg.gridDim = dim3((unsigned)a.ctas * rows);
+    return cudaLaunchKernelEx(&cfg, decode_merge_kernel<D, kMergeWarps>, a);
+  }
+  cfg.gridDim = dim3(((unsigned)(a.B * a.pool.kv_heads) * rows + kMergeWarps - 1) / kMergeWarps);
+  return cudaLaunchKernelEx(&cfg, decode_merge_kernel<D, 1>, a);
 }
 
 // Also allows the kernel its shared memory on the current device; every launch
@@ -784,7 +899,7 @@ PagedLayout paged_layout(int B, int Hkv, int rows, int prefix_len, int d) {
   L.lpart = up256(slots * L.slot_rows * d * sizeof(float));
   L.unit_ctas = L.lpart + up256(slots * L.slot_rows * sizeof(float));
   L.begun = L.unit_ctas + up256(units * sizeof(int2));
-  L.total = L.pre_opart = L.begun + up256((size_t)L.ctas * sizeof(long long));
+  L.total = L.pre_opart = L.begun + up256((size_t)L.ctas * sizeof(int2));
   if (own_kernel) {
     const long long pre_units = (pre_rows + 255) / 256 * Hkv;
     L.pre_splits = plan_prefix_splits(pre_units, (int)(((long long)prefix_len + 127) / 128), fwd_slots());
@@ -800,18 +915,16 @@ PagedLayout paged_layout(int B, int Hkv, int rows, int prefix_len, int d) {
 }
 
 cudaError_t launch_decode_paged_bf16(const PagedDecodeArgs& a, int d, cudaStream_t st) {
-  const long long rows = a.prefix_len > 0 ? (long long)a.B * a.pool.kv_heads * a.G * a.Nq : (long long)a.ctas * a.G * a.Nq;
-  if (rows > 0x7fffffffll || a.ctas < 1) return cudaErrorInvalidValue;
-  const unsigned blocks = (unsigned)rows;
+  if (a.ctas < 1) return cudaErrorInvalidValue;
   if (d == 128) {
-    if (a.slot_rows == 16) return launch<128, 1>(a, blocks, st);
-    if (a.slot_rows == 32) return launch<128, 2>(a, blocks, st);
-    return launch<128, 4>(a, blocks, st);
+    if (a.slot_rows == 16) return launch<128, 1>(a, st);
+    if (a.slot_rows == 32) return launch<128, 2>(a, st);
+    return launch<128, 4>(a, st);
   }
   if (d == 64) {
-    if (a.slot_rows == 16) return launch<64, 1>(a, blocks, st);
-    if (a.slot_rows == 32) return launch<64, 2>(a, blocks, st);
-    return launch<64, 4>(a, blocks, st);
+    if (a.slot_rows == 16) return launch<64, 1>(a, st);
+    if (a.slot_rows == 32) return launch<64, 2>(a, st);
+    return launch<64, 4>(a, st);
   }
   return cudaErrorInvalidValue;
 }
