@@ -432,36 +432,41 @@ def fa_rope_tables(max_positions: int, rot_dim: int, base: float = 10000.0, devi
     return a.cos().float(), a.sin().float()
 
 
-def _check_on(t, name: str, index: int, dtype):
-    """Checks that t is a tensor of ``dtype`` on CUDA device ``index`` (-1: on any) and returns its device."""
-    if not isinstance(t, torch.Tensor):
+_BF16, _F32, _I32, _Tensor = torch.bfloat16, torch.float32, torch.int32, torch.Tensor
+
+
+def _refuse(t, name: str, device: int, dtype, what: str):
+    """Raises for argument ``name``, which is not what the caller's test asks for."""
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    i = t.get_device()
-    if i < 0:
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (this library has no CPU path)")
-    if t.dtype is not dtype or (i != index and index >= 0):
-        raise ValueError(f"{name} must be {dtype} and on the same device as the other tensors")
-    return i
+    raise ValueError(f"{name} must be {what}, {dtype}, on the other tensors' device (cuda:{device}); "
+                     f"it is {tuple(t.shape)}, {t.dtype}, on {t.device}")
+
+
+def _is(t, dtype, device: int) -> bool:
+    """Whether t is a tensor of ``dtype`` on CUDA device ``device``."""
+    return isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == device
 
 
 def _paged_cache(k_pages, v_pages, block_tables, seq_lens):
     """Checks a paged cache and its tables; returns (fa_paged_kv, its shape, B, max_pages, device index)."""
-    dev = _check_on(k_pages, "k_pages", -1, torch.bfloat16)
-    _check_on(v_pages, "v_pages", dev, torch.bfloat16)
-    _check_on(block_tables, "block_tables", dev, torch.int32)
-    _check_on(seq_lens, "seq_lens", dev, torch.int32)
+    dev = k_pages.get_device() if isinstance(k_pages, _Tensor) else -1
+    if dev < 0 or not _is(k_pages, _BF16, dev) or k_pages.dim() != 4:
+        _refuse(k_pages, "k_pages", dev, _BF16, "[pages, Hkv, page_size, d]")
     shape = k_pages.shape
-    if len(shape) != 4 or v_pages.shape != shape:
-        raise ValueError("k_pages and v_pages must both be [pages, Hkv, page_size, d]")
+    if not _is(v_pages, _BF16, dev) or v_pages.shape != shape:
+        _refuse(v_pages, "v_pages", dev, _BF16, "of k_pages' shape")
+    if not _is(block_tables, _I32, dev) or block_tables.dim() != 2 or not block_tables.is_contiguous():
+        _refuse(block_tables, "block_tables", dev, _I32, "a contiguous [B, max_pages]")
+    B, max_pages = block_tables.shape
+    if not _is(seq_lens, _I32, dev) or seq_lens.shape != (B,) or not seq_lens.is_contiguous():
+        _refuse(seq_lens, "seq_lens", dev, _I32, "a contiguous [B]")
     k0, k1, k2, k3 = k_pages.stride()
     v0, v1, v2, v3 = v_pages.stride()
     if k3 != 1 or v3 != 1:
         raise ValueError("the last dimension of k_pages and v_pages must be contiguous")
-    if block_tables.dim() != 2 or not block_tables.is_contiguous():
-        raise ValueError("block_tables must be a contiguous int32 [B, max_pages]")
-    B, max_pages = block_tables.shape
-    if seq_lens.dim() != 1 or not seq_lens.is_contiguous() or seq_lens.shape[0] != B:
-        raise ValueError("seq_lens must be a contiguous int32 [B]")
     pool = _pack_pool(k_pages.data_ptr(), v_pages.data_ptr(), *shape, k0, k1, k2, v0, v1, v2)
     return pool, shape, B, max_pages, dev
 
@@ -476,13 +481,13 @@ def _on_device(dev: int, fn, *args):
 
 def _token_stride(t, name: str, total, heads, d: int, dev: int):
     """Checks packed tokens [total, heads, d] (heads of a token contiguous); returns their stride."""
-    _check_on(t, name, dev, torch.bfloat16)
-    shape = t.shape
-    if len(shape) != 3 or shape[2] != d or (heads is not None and shape[1] != heads) or \
-            (total is not None and shape[0] != total):
-        raise ValueError(f"{name} must be [total, heads, {d}] with the other tensors' tokens and heads")
+    if not _is(t, _BF16, dev) or t.dim() != 3:
+        _refuse(t, name, dev, _BF16, f"[total, heads, {d}]")
+    n, h, e = t.shape
     s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != d and shape[1] > 1):
+    if e != d or (heads is not None and h != heads) or (total is not None and n != total):
+        raise ValueError(f"{name} must be [total, heads, {d}] with the other tensors' tokens and heads")
+    if s2 != 1 or (s1 != d and h > 1):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
     return s0
 
@@ -499,7 +504,6 @@ def fa_kv_append(k, v, k_pages, v_pages, block_tables, seq_lens, cu_seqlens=None
     key's index in the cache). k_pages and v_pages are written in place.
     Returns the rotated queries (``q_out``, dense unless given), or None without q.
     """
-    lib = load_library()
     pool, (_, hkv, page, d), B, max_pages, dev = _paged_cache(k_pages, v_pages, block_tables, seq_lens)
     ks = _token_stride(k, "k", None, hkv, d, dev)
     total = k.shape[0]
@@ -510,7 +514,7 @@ def fa_kv_append(k, v, k_pages, v_pages, block_tables, seq_lens, cu_seqlens=None
         qs = _token_stride(q, "q", total, None, d, dev)
         hq = q.shape[1]
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            q_out = torch.empty((total, hq, d), dtype=_BF16, device=q.device)
             os_ = hq * d
         else:
             os_ = _token_stride(q_out, "q_out", total, hq, d, dev)
@@ -518,31 +522,29 @@ def fa_kv_append(k, v, k_pages, v_pages, block_tables, seq_lens, cu_seqlens=None
     elif q_out is not None:
         raise ValueError("q_out given without q")
     if cu_seqlens is not None:
-        _check_on(cu_seqlens, "cu_seqlens", dev, torch.int32)
-        if cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() or cu_seqlens.shape[0] != B + 1:
-            raise ValueError("cu_seqlens must be a contiguous int32 [B+1]")
+        if not _is(cu_seqlens, _I32, dev) or cu_seqlens.shape != (B + 1,) or not cu_seqlens.is_contiguous():
+            _refuse(cu_seqlens, "cu_seqlens", dev, _I32, "a contiguous [B+1]")
         cu_ptr = cu_seqlens.data_ptr()
     rot = max_pos = 0
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
     if cos is not None:
-        _check_on(cos, "cos", dev, torch.float32)
-        _check_on(sin, "sin", dev, torch.float32)
-        if cos.dim() != 2 or sin.shape != cos.shape or not cos.is_contiguous() or not sin.is_contiguous():
-            raise ValueError("cos and sin must be contiguous float32 [max_positions, rot_dim / 2]")
+        if not _is(cos, _F32, dev) or cos.dim() != 2 or not cos.is_contiguous():
+            _refuse(cos, "cos", dev, _F32, "a contiguous [max_positions, rot_dim / 2]")
         max_pos, rot = cos.shape
+        if not _is(sin, _F32, dev) or sin.shape != (max_pos, rot) or not sin.is_contiguous():
+            _refuse(sin, "sin", dev, _F32, "contiguous and of cos' shape")
         rot *= 2
         cos_ptr, sin_ptr = cos.data_ptr(), sin.data_ptr()
     if positions is not None:
-        _check_on(positions, "positions", dev, torch.int32)
-        if positions.dim() != 1 or not positions.is_contiguous() or positions.shape[0] != total:
-            raise ValueError("positions must be a contiguous int32 [total]")
+        if not _is(positions, _I32, dev) or positions.shape != (total,) or not positions.is_contiguous():
+            _refuse(positions, "positions", dev, _I32, "a contiguous [total]")
         pos_ptr = positions.data_ptr()
     if total == 0:
         return q_out
-    rc = _on_device(dev, lib.fa_kv_append, k.data_ptr(), v.data_ptr(), ks, vs, q_ptr, out_ptr, qs, os_, hq, pool,
-                    block_tables.data_ptr(), max_pages, seq_lens.data_ptr(), cu_ptr, B, total, cos_ptr, sin_ptr, rot,
-                    max_pos, pos_ptr, FA_ROPE_INTERLEAVED if interleaved else 0, FA_BF16)
+    rc = _on_device(dev, load_library().fa_kv_append, k.data_ptr(), v.data_ptr(), ks, vs, q_ptr, out_ptr, qs, os_, hq,
+                    pool, block_tables.data_ptr(), max_pages, seq_lens.data_ptr(), cu_ptr, B, total, cos_ptr, sin_ptr,
+                    rot, max_pos, pos_ptr, FA_ROPE_INTERLEAVED if interleaved else 0, FA_BF16)
     if rc != FA_OK:
         _raise(rc, "fa_kv_append")
     return q_out
@@ -561,39 +563,46 @@ def fa_decode_shared_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, prefix_
 _decode_ws_bytes: dict = {}  # (device, sizes) -> bytes: what the library answered
 
 
+def _decode_workspace_size(lib, key):
+    dev, B, hq, hkv, nq, prefix_len, d = key
+    with torch.cuda.device(dev):
+        n = lib.fa_decode_shared_workspace_bytes(B, hq, hkv, nq, prefix_len, d, FA_BF16)
+    if len(_decode_ws_bytes) >= 4096:
+        _decode_ws_bytes.clear()
+    _decode_ws_bytes[key] = n
+    return n
+
+
 def _decode_cache(where, q, k_pages, v_pages, prefix_pages, prefix_len, block_tables, seq_lens, scale, out, lse,
                   workspace):
     lib = load_library()
     pool, (_, hkv, page, d), B, max_pages, dev = _paged_cache(k_pages, v_pages, block_tables, seq_lens)
-    _check_on(q, "q", dev, torch.bfloat16)
+    if not _is(q, _BF16, dev) or q.dim() != 4:
+        _refuse(q, "q", dev, _BF16, "[B, Hq, Nq, d]")
     shape = q.shape
-    if len(shape) != 4 or shape[0] != B or shape[3] != d or shape[1] % hkv != 0:
+    b, hq, nq, e = shape
+    if b != B or e != d or hq % hkv != 0:
         raise ValueError("q must be [B, Hq, Nq, d] with the tables' B, the cache's d and Hq a multiple of its heads")
-    _, hq, nq, _ = shape
     q0, q1, q2, q3 = q.stride()
     device = q.device
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        out = torch.empty(shape, dtype=_BF16, device=device)
         o_strides, o3 = None, 1
     else:
-        _check_on(out, "out", dev, torch.bfloat16)
-        if out.shape != shape:
-            raise ValueError("out must match q in shape")
+        if not _is(out, _BF16, dev) or out.shape != shape:
+            _refuse(out, "out", dev, _BF16, "of q's shape")
         o0, o1, o2, o3 = out.stride()
         o_strides = _pack_strides(o0, o1, o2)
     if q3 != 1 or o3 != 1:
         raise ValueError("the last dimension of q and out must be contiguous")
     if lse is None:
-        lse = torch.empty((B, hq, nq), dtype=torch.float32, device=device)
-    else:
-        _check_on(lse, "lse", dev, torch.float32)
-        if lse.shape != (B, hq, nq) or not lse.is_contiguous():
-            raise ValueError("lse must be contiguous float32 [B, Hq, Nq]")
+        lse = torch.empty((B, hq, nq), dtype=_F32, device=device)
+    elif not _is(lse, _F32, dev) or lse.shape != (B, hq, nq) or not lse.is_contiguous():
+        _refuse(lse, "lse", dev, _F32, "a contiguous [B, Hq, Nq]")
     prefix_ptr = None
     if prefix_len > 0:
-        _check_on(prefix_pages, "prefix_pages", dev, torch.int32)
-        if prefix_pages.dim() != 1 or not prefix_pages.is_contiguous():
-            raise ValueError("prefix_pages must be a contiguous int32 [pages]")
+        if not _is(prefix_pages, _I32, dev) or prefix_pages.dim() != 1 or not prefix_pages.is_contiguous():
+            _refuse(prefix_pages, "prefix_pages", dev, _I32, "a contiguous [pages]")
         if prefix_pages.shape[0] * page < prefix_len:
             raise ValueError("prefix_pages holds fewer than prefix_len keys")
         prefix_ptr = prefix_pages.data_ptr()
@@ -601,14 +610,10 @@ def _decode_cache(where, q, k_pages, v_pages, prefix_pages, prefix_len, block_ta
         key = (dev, B, hq, hkv, nq, prefix_len, d)
         n = _decode_ws_bytes.get(key)
         if n is None:
-            with torch.cuda.device(dev):
-                n = lib.fa_decode_shared_workspace_bytes(B, hq, hkv, nq, prefix_len, d, FA_BF16)
-            if len(_decode_ws_bytes) >= 4096:
-                _decode_ws_bytes.clear()
-            _decode_ws_bytes[key] = n
+            n = _decode_workspace_size(lib, key)
         workspace = torch.empty(n, dtype=torch.uint8, device=device)
     else:
-        if workspace.get_device() != dev or not workspace.is_contiguous():
+        if not isinstance(workspace, _Tensor) or workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on q's device")
         n = workspace.numel() * workspace.element_size()
     rc = _on_device(dev, lib.fa_decode_shared, q.data_ptr(), _pack_strides(q0, q1, q2), pool, prefix_ptr, prefix_len,
