@@ -285,6 +285,8 @@ struct PagedDecodeArgs {
   // A prefix of many rows runs as a kernel of its own (launch_prefix_bf16),
   // whose pre_splits partial results per row lie here; 0: it is part of n_seq.
   int pre_splits;
+  int early_ctas, early_steps;     // CTAs that run beside that kernel, and the steps they take in its time
+  FastDiv early_div;               // by early_ctas
   const float* pre_Opart;
   const float* pre_Lpart;
   float scale_log2;                // scale * log2(e)
@@ -299,6 +301,16 @@ struct PagedLayout {
   int ctas, n_seq, slot_rows, pre_splits;
   size_t lpart, unit_ctas, begun, pre_opart, pre_lpart, total;
 };
+// How a prefix's kernel and the own keys' kernel share the GPU: key ranges per
+// unit of the former (at most max_splits, which the scratch is laid out for),
+// and the CTAs of the latter that find an SM meanwhile, with the steps they take
+// in that time. rows = G * Nq; own_keys: an estimate of a sequence's own keys
+// (the lengths are on the device).
+struct PrefixPlan {
+  int splits, early_ctas, early_steps;
+};
+PrefixPlan plan_prefix_beside(int B, int rows, int Hkv, int prefix_len, int d, int max_splits, int ctas, int sms,
+                              int own_keys);
 PagedLayout paged_layout(int B, int Hkv, int rows, int prefix_len, int d);
 cudaError_t launch_decode_paged_bf16(const PagedDecodeArgs& a, int d, cudaStream_t st);
 

@@ -139,12 +139,17 @@ fa_status decode_impl(const void* Q, const long long* q_strides, const fa_paged_
     p.box_rows = cache->page_size & -cache->page_size;
     if (p.box_rows > 128) p.box_rows = 128;
     p.rows = B * a.G * Nq;
+    // a table is as wide as its longest sequence may get; a quarter of that is
+    // taken for what the sequences hold on average
+    const long long most = (long long)max_pages * cache->page_size;
+    const PrefixPlan plan = plan_prefix_beside(B, a.G * Nq, cache->kv_heads, prefix_len, cache->d, L.pre_splits, L.ctas,
+                                               fwd_slots(), (int)(most < kPagedMaxKeys ? most : kPagedMaxKeys) / 4);
     const long long units = ((long long)p.rows + 255) / 256 * cache->kv_heads;
     p.Opart = reinterpret_cast<float*>(ws + L.pre_opart);
     p.Lpart = reinterpret_cast<float*>(ws + L.pre_lpart);
     if (!encode_pool_bf16(&p.tmK, a.pool, false, cache->d, p.box_rows) ||
         !encode_pool_bf16(&p.tmV, a.pool, true, cache->d, p.box_rows) ||
-        !encode_part_f32(&p.tmOpart, p.Opart, units * L.pre_splits * 256, cache->d))
+        !encode_part_f32(&p.tmOpart, p.Opart, units * plan.splits * 256, cache->d))
       return FA_ERR_CUDA;
     p.seq.H = cache->kv_heads;
     p.seq.N = prefix_len;
@@ -154,7 +159,7 @@ fa_status decode_impl(const void* Q, const long long* q_strides, const fa_paged_
     p.status = a.status;
     p.wait_limit_ns = a.wait_limit_ns;
     p.n_tail = (int)units;
-    p.splits = L.pre_splits;
+    p.splits = plan.splits;
     p.debug_skip_kv = -1;
     p.Qrows = Q;
     p.q_b = a.q_b;
@@ -164,7 +169,10 @@ fa_status decode_impl(const void* Q, const long long* q_strides, const fa_paged_
     p.G = a.G;
     p.Nq = Nq;
     if (launch_prefix_bf16(p, cache->d, static_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_CUDA;
-    a.pre_splits = L.pre_splits;
+    a.pre_splits = plan.splits;
+    a.early_ctas = plan.early_ctas;
+    a.early_steps = plan.early_steps;
+    a.early_div = fast_div((unsigned)(plan.early_ctas > 0 ? plan.early_ctas : 1));
     a.pre_Opart = p.Opart;
     a.pre_Lpart = p.Lpart;
   }

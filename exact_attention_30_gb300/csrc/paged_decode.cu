@@ -137,22 +137,43 @@ struct RowInfo {
   int hidden;
 };
 
-// CTA w of W takes steps [begin(w), begin(w + 1)) of T: T / W each, the first
-// T mod W one more.
+// Steps that an early CTA rather takes on top than leaves to CTAs that start
+// after the prefix's kernel (about their start-up time)
+constexpr int kEarlySlack = 6;
+
+// CTA w of W takes steps [begin(w), begin(w + 1)) of T. The first `early` CTAs
+// run beside a prefix's kernel and take `more` steps each in that time; the
+// rest is shared equally by all (the first `extra` CTAs take one more). Few
+// more steps than that: the early ones share them all.
 struct Cut {
-  long long per, extra;
-  __device__ __forceinline__ Cut(const PagedDecodeArgs& a, long long T) {
-    if (T < (1ll << 31)) per = a.ctas_div((int)T);  // always, but for caches of terabytes
-    else per = T / a.ctas;
-    extra = T - per * a.ctas;
+  long long per, extra, more;
+  int early, ctas;
+  __device__ __forceinline__ Cut(const PagedDecodeArgs& a, long long T) : more(a.early_steps), early(a.early_ctas), ctas(a.ctas) {
+    long long rest = T - early * more;
+    FastDiv div = a.ctas_div;
+    if (early > 0 && rest < (long long)early * kEarlySlack) {
+      rest = T;
+      more = 0;
+      ctas = early;
+      div = a.early_div;
+    }
+    if (rest < (1ll << 31)) per = div((int)rest);  // always, but for caches of terabytes
+    else per = rest / ctas;
+    extra = rest - per * ctas;
   }
-  __device__ __forceinline__ long long begin(long long w) const { return w * per + (w < extra ? w : extra); }
-  // the CTA that has step t
-  __device__ __forceinline__ int owner(long long t) const {
-    const long long longer = extra * (per + 1);
-    if (t < longer) return t < (1ll << 31) ? (int)t / (int)(per + 1) : (int)(t / (per + 1));
-    t -= longer;
-    return (int)extra + (t < (1ll << 31) ? (int)t / (int)per : (int)(t / per));
+  __device__ __forceinline__ long long begin(int w) const {
+    const int c = min(w, ctas);
+    return c * per + min((long long)c, extra) + min(w, early) * more;
+  }
+  // the CTA from w on that has step t
+  __device__ __forceinline__ int owner(int w, long long t) const {
+    int lo = w, hi = ctas;  // begin(lo) <= t < begin(hi)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (begin(mid) <= t) lo = mid;
+      else hi = mid;
+    }
+    return lo;
   }
 };
 
@@ -363,7 +384,7 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
         const long long end = wk.unit_at() + kUnitSteps + wk.tiles;
         const bool whole = end <= wk.sh.at + wk.sh.left;
         if (a.prefix_len > 0 || !whole) {
-          const int unit = wk.sh.seq * Hkv + wk.sh.head, last = whole ? (int)blockIdx.x : cut.owner(end - 1);
+          const int unit = wk.sh.seq * Hkv + wk.sh.head, last = whole ? (int)blockIdx.x : cut.owner(blockIdx.x, end - 1);
           if (a.prefix_len > 0) a.unit_ctas[unit] = make_int2(blockIdx.x, last);
           else a.begun[blockIdx.x] = make_int2(unit, last);
         }
@@ -676,8 +697,9 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
       if (lane == 0) mbar_arrive(EMPTY(last_stage));
     }
   }
-  // a prefix's kernel ends before this one does, so the merge sees both
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // a prefix's kernel ends before this one does, so the merge sees both; one
+  // CTA waits for that, the others make room
+  if (blockIdx.x + 1 == gridDim.x) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Rows of units that were not written out directly: partial results of the
@@ -912,6 +934,41 @@ PagedLayout paged_layout(int B, int Hkv, int rows, int prefix_len, int d) {
     L.total = L.pre_lpart + up256(parts * sizeof(float));
   }
   return L;
+}
+
+PrefixPlan plan_prefix_beside(int B, int rows, int Hkv, int prefix_len, int d, int max_splits, int ctas, int sms,
+                              int own_keys) {
+  // Times in us, measured on a GB300: a prefix's CTA takes kStart and, per tile
+  // of 128 keys, 1.76 (two tiles of query rows) or 1.05 (one), two thirds of
+  // that at d = 64. An own keys' CTA beside it takes kOwnStart and 0.75 per
+  // step of 32 KB, or what all such CTAs' bytes take at 6 GB/ms; one that finds
+  // its SM only after the prefix's costs kLate before the rest goes on.
+  constexpr double kStart = 11.0, kOwnStart = 2.0, kStep = 0.75, kLate = 4.0, kStepAll = 32768.0 / 6e6;
+  const int n_kv = (int)(((long long)prefix_len + 127) / 128);
+  const long long units = ((long long)B * rows + 255) / 256 * Hkv;
+  const double tile = ((long long)B * rows > 128 ? 1.76 : 1.05) * (d == 128 ? 1.0 : 0.67);
+  const double steps = (double)B * Hkv * (own_keys * (double)d / 8192.0 + kUnitSteps + 0.5);
+  PrefixPlan best{max_splits, 0, 0};
+  double best_us = -1;
+  for (int s = 1; s <= max_splits; ++s) {
+    const long long waves = (units * s + sms - 1) / sms;
+    const double pre_us = kStart + (double)waves * ((n_kv + s - 1) / s) * tile;
+    const int early = waves == 1 ? (sms - (int)(units * s)) * (ctas / sms) : 0;
+    const double step = early * kStepAll > kStep ? early * kStepAll : kStep;
+    const int more = early > 0 && pre_us > kOwnStart ? (int)((pre_us - kOwnStart) / step) : 0;
+    double us = pre_us;
+    if (early > 0 && steps <= early * (double)(more + kEarlySlack)) {
+      const double own_us = kOwnStart + steps / early * step;
+      us = own_us > us ? own_us : us;
+    } else {
+      us += kLate + (steps - early * (double)more) * kStepAll;
+    }
+    if (best_us < 0 || us < best_us) {
+      best_us = us;
+      best = PrefixPlan{s, early, more};
+    }
+  }
+  return best;
 }
 
 cudaError_t launch_decode_paged_bf16(const PagedDecodeArgs& a, int d, cudaStream_t st) {
