@@ -74,6 +74,8 @@ template <int D, int PASSES>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a, int chunks) {
   constexpr int U = D / 16;    // lanes of a head
   constexpr int HPP = 32 / U;  // heads of a pass
+  // a decode behind this kernel may be set up meanwhile; it waits for the end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const long long gw = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const long long warps = (long long)gridDim.x * (kThreads / 32);
