@@ -66,8 +66,9 @@ struct Cfg {
   // warps meet, DW columns at a time
   static constexpr int DW = MT == 1 ? D : D / 2;
   static constexpr int MERGE = 4 * 16 * DW * 4;
-  // One 16-row group: its merge fits the piece's last stage, and two CTAs
-  // share an SM, one loading while the other one merges. More rows: one CTA.
+  // One 16-row group: each warp's output fits the place of its keys and values
+  // in the piece's last stage, and two CTAs share an SM, one loading while the
+  // other one merges. More rows: space of its own, one CTA.
   static constexpr bool MERGE_IN_STAGE = MT == 1;
   static constexpr int CTAS = MT == 1 ? 2 : 1;
   static constexpr int STAGES = (MT == 2 ? 4 : 3) * (D == 128 ? 1 : 2);
@@ -85,7 +86,7 @@ struct Cfg {
   static constexpr int OFF_BAR = OFF_SHARE + 48;
   static constexpr int SMEM = OFF_BAR + 2 * STAGES * 8;
   static constexpr int SMEM_ALLOC = SMEM + 1024;  // base rounded up to 1024 (swizzle atom)
-  static_assert(!MERGE_IN_STAGE || MERGE <= STAGE, "merge space");
+  static_assert(!MERGE_IN_STAGE || MERGE == STAGE, "merge space");
   static_assert(CTAS * (SMEM_ALLOC + 1024) <= 228 * 1024, "shared memory budget");
 };
 
@@ -624,8 +625,8 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
     }
 
     if (!active) continue;
-    // the four warps of each 16 rows meet: common maximum, then the sum of
-    // their outputs, each already scaled by its share of the total
+    // the four warps of each 16 rows meet in shared memory: maxima, sums and
+    // outputs as they are, weighted and added by whoever writes them out
     l_a += __shfl_xor_sync(kFull, l_a, 1);
     l_b += __shfl_xor_sync(kFull, l_b, 1);
     l_a += __shfl_xor_sync(kFull, l_a, 2);
@@ -634,31 +635,21 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
       ml[kw * 16 + g] = make_float2(m_a, l_a);
       ml[kw * 16 + g + 8] = make_float2(m_b, l_b);
     }
-    named_bar(1 + mt, 128);  // also: every warp has read its keys of the last stage
-    float f_a, f_b, lse_a, lse_b;
-    auto combine = [&](int r, float m_own, float& f, float& lse) {
-      float2 t[4];
-#pragma unroll
-      for (int w = 0; w < 4; ++w) t[w] = ml[w * 16 + r];
-      const float mm = fmaxf(fmaxf(t[0].x, t[1].x), fmaxf(t[2].x, t[3].x));
-      const float mu = mm == -INFINITY ? 0.f : mm;
-      float ll = 0.f;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) ll = fmaf(t[w].y, ex2_approx(t[w].x - mu), ll);
-      f = ll == 0.f ? 0.f : __fdividef(ex2_approx(m_own - mu), ll);
-      lse = ll == 0.f ? -INFINITY : mm + __log2f(ll);
-    };
-    combine(g, m_a, f_a, lse_a);
-    combine(g + 8, m_b, f_b, lse_b);
     const int last_stage = (it - 1) % C::STAGES;
-    float* om = reinterpret_cast<float*>(smem + (C::MERGE_IN_STAGE ? last_stage * C::STAGE : C::OFF_MERGE + mt * C::MERGE));
+    uint8_t* om = smem + (C::MERGE_IN_STAGE ? last_stage * C::STAGE : C::OFF_MERGE + mt * C::MERGE);
+    // Column c of row r of warp w. In the stage a warp takes the place of its
+    // own 16 keys and values (nobody else reads those): 32 columns per chunk.
+    // 16-byte (32-byte) units permuted by the row, so that the eight rows of a
+    // store differ in banks.
+    auto om_at = [&](int w, int r, int c) {
+      if (C::MERGE_IN_STAGE) return om + (c >> 5) * C::CHUNK + w * 2048 + r * 128 + (((c & 31) * 4) ^ ((r & 7) << 4));
+      return om + ((w * 16 + r) * C::DW + (c ^ ((8 * r) & 56 & (C::DW - 1)))) * 4;
+    };
     const long long unit = (long long)seq * Hkv + head;
     const bool direct = begins && ends && a.prefix_len == 0;
     const long long part_row = part_slot(a, blockIdx.x, begins, ends, unit) * a.slot_rows;
     const long long o_unit = (pre ? 0 : seq * a.o_b) + (long long)head * a.G * a.o_h;
-    // row r's column c lies at c ^ 8 (r & 7): the eight rows of a store differ in banks
     constexpr int DW = C::DW;
-    const int sg = (8 * g) & (DW - 1);
     const int group_rows = min(16, rows - mt * 16);
 #pragma unroll
     for (int d0 = 0; d0 < D; d0 += DW) {
@@ -667,46 +658,52 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
 #pragma unroll
         for (int nn = 0; nn < DW / 8; ++nn) {
           const float* x = acc[d0 / 8 + nn];
-          *reinterpret_cast<float2*>(om + (kw * 16 + g) * DW + ((8 * nn + 2 * q) ^ sg)) = make_float2(x[0] * f_a, x[1] * f_a);
+          *reinterpret_cast<float2*>(om_at(kw, g, 8 * nn + 2 * q)) = make_float2(x[0], x[1]);
         }
       }
       if (g + 8 < group_rows) {
 #pragma unroll
         for (int nn = 0; nn < DW / 8; ++nn) {
           const float* x = acc[d0 / 8 + nn];
-          *reinterpret_cast<float2*>(om + (kw * 16 + g + 8) * DW + ((8 * nn + 2 * q) ^ sg)) = make_float2(x[2] * f_b, x[3] * f_b);
+          *reinterpret_cast<float2*>(om_at(kw, g + 8, 8 * nn + 2 * q)) = make_float2(x[2], x[3]);
         }
       }
       named_bar(1 + mt, 128);
       for (int e = ct; e < group_rows * (DW / 4); e += 128) {
         const int r = e / (DW / 4), c = (e - r * (DW / 4)) * 4;
         const int rr = mt * 16 + r;
-        const float* p = om + r * DW + (c ^ ((8 * r) & 56 & (DW - 1)));
-        float4 y = *reinterpret_cast<const float4*>(p);
+        float2 t[4];
 #pragma unroll
-        for (int w = 1; w < 4; ++w) {
-          const float4 z = *reinterpret_cast<const float4*>(p + w * 16 * DW);
-          y.x += z.x;
-          y.y += z.y;
-          y.z += z.z;
-          y.w += z.w;
+        for (int w = 0; w < 4; ++w) t[w] = ml[w * 16 + r];
+        const float mm = fmaxf(fmaxf(t[0].x, t[1].x), fmaxf(t[2].x, t[3].x));
+        const float mu = mm == -INFINITY ? 0.f : mm;
+        float ll = 0.f;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float f = ex2_approx(t[w].x - mu);
+          const float4 z = *reinterpret_cast<const float4*>(om_at(w, r, c));
+          ll = fmaf(t[w].y, f, ll);
+          y.x = fmaf(z.x, f, y.x);
+          y.y = fmaf(z.y, f, y.y);
+          y.z = fmaf(z.z, f, y.z);
+          y.w = fmaf(z.w, f, y.w);
         }
+        const float inv = ll == 0.f ? 0.f : __fdividef(1.f, ll);
+        y.x *= inv;
+        y.y *= inv;
+        y.z *= inv;
+        y.w *= inv;
+        const float lse = ll == 0.f ? -INFINITY : mm + __log2f(ll);
         if (direct) {
           __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.O) + o_unit + info[rr].o + d0 + c;
           *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+          if (d0 + c == 0) a.LSE[unit * R + rr] = lse * kLn2;
         } else {
           *reinterpret_cast<float4*>(a.Opart + (part_row + rr) * D + d0 + c) = y;
+          if (d0 + c == 0) a.Lpart[part_row + rr] = lse;
         }
       }
-    }
-    if (kw == 0 && q == 0) {
-      auto put = [&](int r, float lse) {
-        if (r >= rows) return;
-        if (direct) a.LSE[unit * R + r] = lse * kLn2;
-        else a.Lpart[part_row + r] = lse;
-      };
-      put(ra, lse_a);
-      put(rb, lse_b);
     }
     if (C::MERGE_IN_STAGE) {
       fence_proxy_async_smem();  // the stage's next writer is the TMA
@@ -723,16 +720,16 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
 // own keys (and of the prefix) merged by maximum and sum, in order of the
 // CTAs. WPR warps share a row, each taking every WPR-th partial result, and
 // meet in shared memory: without a prefix few rows have parts, but a long
-// sequence has one from each of many CTAs (WPR = 4); with one every row has
-// parts, about as many as the prefix has key ranges (WPR = 1).
-constexpr int kMergeWarps = 4;
-template <int D, int WPR>
+// sequence has one from each of many CTAs (WPR = 8); with one every row has
+// parts, as many as the prefix has key ranges (WPR = 1 up to 16, else 8).
+constexpr int kMergeWarps = 8;
+template <int D, int WPR, bool PREFIX>
 __global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const __grid_constant__ PagedDecodeArgs a) {
   constexpr int E = D / 32;
   constexpr int AHEAD = 4;  // partial results in flight per warp
   __shared__ float sm[kMergeWarps], sl[kMergeWarps], so[kMergeWarps][D];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (WPR > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!PREFIX) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % WPR;
   const int Hkv = a.pool.kv_heads, R = a.G * a.Nq;
   const unsigned item = blockIdx.x * (kMergeWarps / WPR) + warp / WPR;
@@ -741,7 +738,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const __
   int unit, own_first, own_n, pre_first = 0, pre_n = 0;
   long long pre_row = 0;  // a prefix's kernel of its own: row of the first part, parts 256 rows apart
   int b, head;
-  if (WPR > 1) {
+  if (!PREFIX) {
     // without a prefix only the units that a share's end cuts have parts
     const int2 c = a.begun[group];
     if (c.x < 0) return;  // the whole block
@@ -751,7 +748,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const __
     b = unit / Hkv;
     head = unit - b * Hkv;
   } else {
-    if (item >= (unsigned)(a.B * Hkv) * (unsigned)R) return;
+    if (item >= (unsigned)(a.B * Hkv) * (unsigned)R) return;  // the whole block, if its warps share a row
     unit = (int)group;
     b = unit / Hkv;
     head = unit - b * Hkv;
@@ -882,10 +879,17 @@ cudaError_t launch(const PagedDecodeArgs& a, cudaStream_t st) {
   const unsigned rows = (unsigned)(a.G * a.Nq);
   if (a.prefix_len == 0) {
     cfg.gridDim = dim3((unsigned)a.ctas * rows);
-    return cudaLaunchKernelEx(&cfg, decode_merge_kernel<D, kMergeWarps>, a);
+    return cudaLaunchKernelEx(&cfg, decode_merge_kernel<D, kMergeWarps, false>, a);
   }
-  cfg.gridDim = dim3(((unsigned)(a.B * a.pool.kv_heads) * rows + kMergeWarps - 1) / kMergeWarps);
-  return cudaLaunchKernelEx(&cfg, decode_merge_kernel<D, 1>, a);
+  const unsigned all = (unsigned)(a.B * a.pool.kv_heads) * rows;
+  // parts of a prefix that is part of the grid: about one per CTA and head
+  const int parts = a.pre_splits > 0 ? a.pre_splits : a.ctas / a.pool.kv_heads;
+  if (parts > 16) {
+    cfg.gridDim = dim3(all);
+    return cudaLaunchKernelEx(&cfg, decode_merge_kernel<D, kMergeWarps, true>, a);
+  }
+  cfg.gridDim = dim3((all + kMergeWarps - 1) / kMergeWarps);
+  return cudaLaunchKernelEx(&cfg, decode_merge_kernel<D, 1, true>, a);
 }
 
 // Also allows the kernel its shared memory on the current device; every launch
