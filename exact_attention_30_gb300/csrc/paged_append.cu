@@ -8,14 +8,19 @@
 // and v element is read once and written once, and a token's row of cosines
 // and sines once.
 //
-// A warp owns one token and a chunk of its heads (q, then k, then v heads). A
-// lane owns two 16-byte vectors of a head: the two halves of eight rotated
-// pairs, so that both partners of a pair meet in one lane's registers and the
-// same cosines serve every head of the chunk. The chunk is four passes long
-// (eight 16-byte loads in flight per lane) unless that would leave SMs idle,
-// as for the single tokens of a decode step, where each pass is a warp of its
-// own: then only latency counts, and the loads of the token are issued before
-// the chain of dependent look-ups (sequence, length, page) starts.
+// A warp works on one token, on a chunk of its heads (q, then k, then v heads)
+// at a time. A lane owns two 16-byte vectors of a head: the two halves of eight
+// rotated pairs, so that both partners of a pair meet in one lane's registers
+// and the same cosines serve every head. The loads of the first chunk are
+// issued before the chain of dependent look-ups (sequence and length, page)
+// starts. Three shapes of the same work, in us for 256 / 1024 / 4096 / 32768
+// tokens of 32 + 16 heads of 128 (a plain copy of the bytes takes 0.9 / 3.8 /
+// 15.2 / 121):
+//   a warp per pass over 4 heads              3.27 / 6.42 / 20.7 / 152
+//   a warp per four passes                    3.30 / 5.08 / 18.4 / 128
+//   a warp per token, two passes at a time    5.54 / 7.79 / 16.6 / 123
+// The first spreads the few tokens of a decode step over the SMs (one token:
+// 2.4 against 5.4 us), the last looks a token's place up once.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -26,22 +31,33 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kFewWarps = 512;
+constexpr int kManyTokens = 2048;
 constexpr unsigned kFull = 0xffffffffu;
 
-// Sequence of packed token t: the largest b with cu[b] <= t, by a 32-way
-// search (two rounds of loads for up to 1024 sequences). -1: cu[0] > t.
-__device__ __forceinline__ int find_sequence(const int* cu, int B, int t, int lane) {
-  int lo = 0, hi = B;
-  bool any = true;
-  while (hi - lo > 1 && any) {
+// Where packed token t belongs: the largest b with cu[b] <= t, its last new
+// token and its length. A 32-way search; its final round, over at most 32
+// sequences, brings all three at once (one round trip to memory for up to 32
+// sequences, two for up to 1024).
+struct Place {
+  int b, last, len;  // b = -1: cu[0] > t
+};
+__device__ __forceinline__ Place find_place(const AppendArgs& a, int t, int lane) {
+  int lo = 0, hi = a.B;
+  while (hi - lo > 32) {
     const int step = (hi - lo + 31) >> 5;
     const int i = lo + step * lane;
-    const unsigned m = __ballot_sync(kFull, i < hi && __ldg(cu + i) <= t);
-    any = m != 0;
-    lo += any ? step * (31 - __clz(m)) : 0;
+    const unsigned m = __ballot_sync(kFull, i < hi && __ldg(a.cu_seqlens + i) <= t);
+    if (m == 0) return Place{-1, 0, 0};
+    lo += step * (31 - __clz(m));
     hi = min(lo + step, hi);
   }
-  return any ? lo : -1;
+  const int i = min(lo + lane, hi - 1);
+  const int begin = __ldg(a.cu_seqlens + i), end = __ldg(a.cu_seqlens + i + 1), len = __ldg(a.seq_lens + i);
+  const unsigned m = __ballot_sync(kFull, lo + lane < hi && begin <= t);
+  if (m == 0) return Place{-1, 0, 0};
+  const int src = 31 - __clz(m);
+  return Place{lo + src, __shfl_sync(kFull, end, src), __shfl_sync(kFull, len, src)};
 }
 
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
@@ -70,8 +86,8 @@ __device__ __forceinline__ void rotate_neighbours(uint4& x, uint4& y, const floa
   }
 }
 
-template <int D, int PASSES>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a, int chunks) {
+template <int D, int PASSES, bool LOOP>
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a, int chunks, int per_token) {
   constexpr int U = D / 16;    // lanes of a head
   constexpr int HPP = 32 / U;  // heads of a pass
   // a decode behind this kernel may be set up meanwhile; it waits for the end
@@ -86,8 +102,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       if (c0 < 0 || c1 < c0 || c1 > a.total) report_status(a.status, kStatusBadSeqlens);
     }
   }
-  if (gw >= (long long)a.total * chunks) return;
-  const int t = (int)(gw / chunks), chunk = (int)(gw - (long long)t * chunks);
+  // per_token warps share a token's chunks of heads
+  if (gw >= (long long)a.total * per_token) return;
+  const int t = (int)(gw / per_token);
+  int chunk = (int)(gw - (long long)t * per_token);
   const int u = lane % U, hl = lane / U;
   const int Hkv = a.pool.kv_heads, heads = a.Hq + 2 * Hkv;
   const int rot = a.rot_dim;
@@ -105,31 +123,36 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.K);
   const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.V);
   uint4 x[PASSES], y[PASSES];
+  auto load = [&]() {
 #pragma unroll
-  for (int p = 0; p < PASSES; ++p) {
-    const int h = (chunk * PASSES + p) * HPP + hl;
-    x[p] = y[p] = make_uint4(0u, 0u, 0u, 0u);
-    if (h < heads) {
-      const __nv_bfloat16* src = h < a.Hq         ? q + t * a.q_stride + (long long)h * D
-                                 : h < a.Hq + Hkv ? k + t * a.k_stride + (long long)(h - a.Hq) * D
-                                                  : v + t * a.v_stride + (long long)(h - a.Hq - Hkv) * D;
-      x[p] = *reinterpret_cast<const uint4*>(src + e0);
-      y[p] = *reinterpret_cast<const uint4*>(src + e1);
+    for (int p = 0; p < PASSES; ++p) {
+      const int h = (chunk * PASSES + p) * HPP + hl;
+      x[p] = y[p] = make_uint4(0u, 0u, 0u, 0u);
+      if (h < heads) {
+        const __nv_bfloat16* src = h < a.Hq         ? q + t * a.q_stride + (long long)h * D
+                                   : h < a.Hq + Hkv ? k + t * a.k_stride + (long long)(h - a.Hq) * D
+                                                    : v + t * a.v_stride + (long long)(h - a.Hq - Hkv) * D;
+        x[p] = *reinterpret_cast<const uint4*>(src + e0);
+        y[p] = *reinterpret_cast<const uint4*>(src + e1);
+      }
     }
-  }
+  };
+  load();
   // where the token goes
-  int b, last;  // its sequence, and the first packed token after that
+  int b, last, len;  // its sequence, the first packed token after that, the length
   if (a.cu_seqlens == nullptr) {
     const int n = a.total / a.B;
     b = t / n;
     last = (b + 1) * n;
+    len = __ldg(a.seq_lens + b);
   } else {
-    b = find_sequence(a.cu_seqlens, a.B, t, lane);
-    if (b < 0) return;  // before the first sequence: reported above
-    last = __ldg(a.cu_seqlens + b + 1);
+    const Place p = find_place(a, t, lane);
+    b = p.b;
+    last = p.last;
+    len = p.len;
+    if (b < 0) return;      // before the first sequence: reported above
     if (t >= last) return;  // behind the last sequence: padding
   }
-  const int len = __ldg(a.seq_lens + b);
   if (len == 0) return;  // a padding sequence
   const long long pos = (long long)len - last + t;
   const int ps = a.pool.page_size;
@@ -163,41 +186,45 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   __nv_bfloat16* kd = static_cast<__nv_bfloat16*>(a.pool.k) + (long long)page * a.pool.k_page + (long long)row * a.pool.k_row;
   __nv_bfloat16* vd = static_cast<__nv_bfloat16*>(a.pool.v) + (long long)page * a.pool.v_page + (long long)row * a.pool.v_row;
   __nv_bfloat16* qd = static_cast<__nv_bfloat16*>(a.Qout) + t * a.qout_stride;
+  do {
 #pragma unroll
-  for (int p = 0; p < PASSES; ++p) {
-    const int h = (chunk * PASSES + p) * HPP + hl;
-    if (h >= heads) continue;
-    if (rotated && h < a.Hq + Hkv) {
-      if (a.interleaved) rotate_neighbours(x[p], y[p], c, s);
-      else rotate_halves(x[p], y[p], c, s);
+    for (int p = 0; p < PASSES; ++p) {
+      const int h = (chunk * PASSES + p) * HPP + hl;
+      if (h >= heads) continue;
+      if (rotated && h < a.Hq + Hkv) {
+        if (a.interleaved) rotate_neighbours(x[p], y[p], c, s);
+        else rotate_halves(x[p], y[p], c, s);
+      }
+      __nv_bfloat16* dst = h < a.Hq         ? qd + (long long)h * D
+                           : h < a.Hq + Hkv ? kd + (h - a.Hq) * a.pool.k_head
+                                            : vd + (h - a.Hq - Hkv) * a.pool.v_head;
+      *reinterpret_cast<uint4*>(dst + e0) = x[p];
+      *reinterpret_cast<uint4*>(dst + e1) = y[p];
     }
-    __nv_bfloat16* dst = h < a.Hq         ? qd + (long long)h * D
-                         : h < a.Hq + Hkv ? kd + (h - a.Hq) * a.pool.k_head
-                                          : vd + (h - a.Hq - Hkv) * a.pool.v_head;
-    *reinterpret_cast<uint4*>(dst + e0) = x[p];
-    *reinterpret_cast<uint4*>(dst + e1) = y[p];
-  }
+    chunk += per_token;
+    if (LOOP && chunk < chunks) load();
+  } while (LOOP && chunk < chunks);
 }
 
-template <int D, int PASSES>
+template <int D, int PASSES, bool LOOP>
 cudaError_t launch_passes(const AppendArgs& a, cudaStream_t st) {
   constexpr int HPP = 32 / (D / 16);
   const int heads = a.Hq + 2 * a.pool.kv_heads;
-  const int chunks = (heads + HPP * PASSES - 1) / (HPP * PASSES);
-  const long long warps = (long long)a.total * chunks;
+  const int chunks = (heads + HPP * PASSES - 1) / (HPP * PASSES), per_token = LOOP ? 1 : chunks;
+  const long long warps = (long long)a.total * per_token;
   const long long blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  append_kernel<D, PASSES><<<(unsigned)blocks, kThreads, 0, st>>>(a, chunks);
+  append_kernel<D, PASSES, LOOP><<<(unsigned)blocks, kThreads, 0, st>>>(a, chunks, per_token);
   return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch_d(const AppendArgs& a, cudaStream_t st) {
-  // four passes per warp once that still gives every SM several blocks
   constexpr int HPP = 32 / (D / 16);
   const int heads = a.Hq + 2 * a.pool.kv_heads;
   const long long warps4 = (long long)a.total * ((heads + 4 * HPP - 1) / (4 * HPP));
-  return warps4 >= 4096 ? launch_passes<D, 4>(a, st) : launch_passes<D, 1>(a, st);
+  if (a.total >= kManyTokens) return launch_passes<D, 2, true>(a, st);
+  return warps4 < kFewWarps ? launch_passes<D, 1, false>(a, st) : launch_passes<D, 4, false>(a, st);
 }
 
 }  // namespace

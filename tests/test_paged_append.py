@@ -66,6 +66,20 @@ def test_append_against_the_definition(lens, new, page, hq, hkv, d, rot, inter, 
     _check(c, bk, bv, new, cu[:-1], q, k, v, out, cos, sin, inter)
 
 
+@pytest.mark.parametrize("lens,hq,hkv,d,rot,inter", [((1500, 900, 77), 5, 3, 64, 64, False), ((2100,), 6, 1, 128, 96, True)])
+def test_a_warp_for_every_token(lens, hq, hkv, d, rot, inter):
+    """More than 2048 new tokens: a token's heads in one warp, the last pass of it partly idle."""
+    c = Cache(lens, hkv, 64, d, seed=d)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    q, k, v = _tokens(int(cu[-1]), hq, hkv, d, seed=d + 1)
+    cos, sin = fa.fa_rope_tables(max(lens), rot, device="cuda")
+    bk, bv = c.k.clone(), c.v.clone()
+    out = fa.fa_kv_append(k, v, c.k, c.v, c.tables, c.seq_lens, torch.tensor(cu, dtype=torch.int32).cuda(), q=q,
+                          cos=cos, sin=sin, interleaved=inter)
+    assert fa.fa_check_device_status() == fa.FA_OK
+    _check(c, bk, bv, lens, cu[:-1], q, k, v, out, cos, sin, inter)
+
+
 def test_equal_counts_without_offsets_keys_only_and_positions():
     lens, new, hkv, d = (20, 33, 3), (3, 3, 3), 2, 128
     c = Cache(lens, hkv, 16, d, seed=1, one_tensor=True)
