@@ -32,6 +32,14 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
 EncodeTiledFn g_encode = nullptr;
 
 bool get_encode_fn() {
+  // The driver's encoder wants a context on the calling thread; a thread whose
+  // first CUDA call this is has none yet.
+  static thread_local bool bound = false;
+  if (!bound) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return false;
+    bound = true;
+  }
   std::lock_guard<std::mutex> lk(g_mu);
   if (g_encode) return true;
   void* fn = nullptr;

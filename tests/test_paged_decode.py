@@ -238,6 +238,33 @@ def test_two_streams_at_once(prefix):
             assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])
 
 
+def test_first_cuda_call_of_a_thread():
+    """A thread that has made no CUDA call yet, on tensors and scratch that are there already."""
+    import threading
+    c = Cache((90, 3), 2, 16, 64, seed=45)
+    q = _q(2, 4, 1, 64, 46)
+    out, lse = torch.empty_like(q), torch.empty((2, 4, 1), device="cuda")
+    ws = torch.empty(fa.fa_decode_paged_workspace_bytes(2, 4, 2, 1, 64), dtype=torch.uint8, device="cuda")
+    k = torch.randn((1, 1, 64, 64), device="cuda").to(torch.bfloat16)
+    o, l = torch.empty_like(k), torch.empty((1, 1, 64), device="cuda")
+    torch.cuda.synchronize()
+    codes = []
+
+    def first(fn):
+        try:
+            fn()
+            codes.append(fa.FA_OK)
+        except fa.FAError as e:
+            codes.append(e.code)
+    for fn in (lambda: fa.fa_decode_paged(q, c.k, c.v, c.tables, c.seq_lens, 0.125, out, lse, ws),
+               lambda: fa.fa_fwd(k, k, k, 0.125, out=o, lse=l)):
+        t = threading.Thread(target=first, args=(fn,))
+        t.start()
+        t.join()
+    assert codes == [fa.FA_OK, fa.FA_OK] and fa.fa_check_device_status() == fa.FA_OK
+    check_decode(c, q, out, lse, 0.125)
+
+
 def test_pool_offsets_beyond_32_bits():
     page, hkv, d = 256, 8, 128
     pages = (1 << 32) // (page * hkv * d) + 4
