@@ -238,6 +238,35 @@ def test_two_streams_at_once(prefix):
             assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])
 
 
+<<<<<<< Updated upstream
+=======
+def test_default_stream_scratch_is_shared_by_calls_of_all_sizes():
+    """Calls of different sizes and kinds, one after another on the default stream, and from two threads at once."""
+    import threading
+    cases = [Cache((900, 30), 2, 16, 128, seed=40), Cache((2000,) * 6, 4, 16, 64, seed=41, prefix=300),
+             Cache((5, 0, 9), 1, 16, 128, seed=42), Cache((100,) * 40, 2, 16, 64, seed=43, prefix=2500)]
+    qs = [_q(len(c.lens), 8, 1, c.d, 44 + i) for i, c in enumerate(cases)]
+    first = [_call(c, q) for c, q in zip(cases, qs)]
+    for c, q, (o, l) in zip(cases, qs, first):
+        check_decode(c, q, o, l, 1 / math.sqrt(c.d))
+    got, errors = {}, []
+
+    def work(k):
+        try:
+            got[k] = [[_call(c, q) for c, q in zip(cases, qs)] for _ in range(20)]
+        except Exception as e:  # pragma: no cover
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not errors and fa.fa_check_device_status() == fa.FA_OK
+    for k in got:
+        for round_ in got[k]:
+            for (o, l), (o0, l0) in zip(round_, first):
+                assert torch.equal(o, o0) and torch.equal(l, l0)
+
+
+>>>>>>> Stashed changes
 def test_first_cuda_call_of_a_thread():
     """A thread that has made no CUDA call yet, on tensors and scratch that are there already."""
     import threading
