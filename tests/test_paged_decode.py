@@ -238,8 +238,6 @@ def test_two_streams_at_once(prefix):
             assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])
 
 
-<<<<<<< Updated upstream
-=======
 def test_default_stream_scratch_is_shared_by_calls_of_all_sizes():
     """Calls of different sizes and kinds, one after another on the default stream, and from two threads at once."""
     import threading
@@ -266,7 +264,6 @@ def test_default_stream_scratch_is_shared_by_calls_of_all_sizes():
                 assert torch.equal(o, o0) and torch.equal(l, l0)
 
 
->>>>>>> Stashed changes
 def test_first_cuda_call_of_a_thread():
     """A thread that has made no CUDA call yet, on tensors and scratch that are there already."""
     import threading
