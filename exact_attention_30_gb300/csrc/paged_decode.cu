@@ -39,6 +39,7 @@
 #include <cuda_runtime.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "fa_internal.h"
 #include "ptx.cuh"
@@ -53,8 +54,16 @@ constexpr int kUnitSteps = 2;
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kLn2 = 0.69314718055994531f;
 
-template <int D, int MT>
+// ROWS: query rows of a unit, 8, 16, 32 or 64 (fewer are padded). BESIDE: on
+// the few SMs that a prefix's kernel leaves, where the latency of units bounds
+// the own keys rather than memory: three CTAs per SM with two stages each
+// (8 rows, whose registers allow it; 128 samples 57.5 -> 54 us). Elsewhere two
+// with three stages: fewer parts to merge (48 ragged sequences 78.5 against
+// 79.6, 299 of 165 keys 18.3 against 20.2 us).
+template <int D_, int ROWS_, bool BESIDE>
 struct Cfg {
+  static constexpr int D = D_, ROWS = ROWS_;
+  static constexpr int MT = ROWS < 16 ? 1 : ROWS / 16;  // groups of rows, four consumer warps each
   static constexpr int BK = 64;              // keys per tile
   static constexpr int CH = D / 64;          // 128-byte column chunks of a row
   static constexpr int CHUNK = BK * 128;     // 64 rows x 128 bytes, swizzled
@@ -66,16 +75,17 @@ struct Cfg {
   // warps meet, DW columns at a time
   static constexpr int DW = MT == 1 ? D : D / 2;
   static constexpr int MERGE = 4 * 16 * DW * 4;
-  // One 16-row group: each warp's output fits the place of its keys and values
-  // in the piece's last stage, and two CTAs share an SM, one loading while the
-  // other one merges. More rows: space of its own, one CTA.
+  // One group of rows: each warp's output fits the place of its keys and
+  // values in the piece's last stage, and several CTAs share an SM, one loading
+  // while another one merges. More rows: space of its own, one CTA.
   static constexpr bool MERGE_IN_STAGE = MT == 1;
-  static constexpr int CTAS = MT == 1 ? 2 : 1;
-  static constexpr int STAGES = (MT == 2 ? 4 : 3) * (D == 128 ? 1 : 2);
+  static constexpr int CTAS = MT > 1 ? 1 : BESIDE ? 3 : 2;
+  static constexpr int STAGES = (MT == 2 ? 4 : BESIDE ? 2 : 3) * (D == 128 ? 1 : 2);
+  static_assert(!BESIDE || ROWS == 8, "registers");
   // Queries as fragments in registers, or read from shared memory per tile
-  // (one group: 1% faster than in registers, which then spill; four groups
+  // (16 rows: 1% faster than in registers, which then spill; four groups
   // leave 96 registers). FB: K or V fragments loaded at a time.
-  static constexpr bool Q_IN_SMEM = MT != 2;
+  static constexpr bool Q_IN_SMEM = ROWS == 16 || MT == 4;
   static constexpr int FB = MT == 4 ? 1 : 4;
   static constexpr int QBUF = 16 * MT * D * 2;  // a unit's queries; two, one being filled for the next unit
   static constexpr int OFF_MERGE = STAGES * STAGE;
@@ -101,6 +111,12 @@ __device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], uint32_t addr) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
+}
+// An 8 x 8 matrix of 16-bit elements, one pair per lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 // c[16 rows x 8] += a[16 x 16] b[16 x 8], bf16 in, fp32 out. Lane 4g + q holds
 // c rows g (0, 1) and g + 8 (2, 3), columns 2q, 2q + 1.
@@ -140,9 +156,14 @@ struct RowInfo {
   int hidden;
 };
 
+// Which of a pair of values, of keys k and k + 1, every row sees.
+__device__ __forceinline__ uint32_t keep_pair(int k, int seen) {
+  return (k < seen ? 0xffffu : 0u) | (k + 1 < seen ? 0xffff0000u : 0u);
+}
+
 // Steps that an early CTA rather takes on top than leaves to CTAs that start
 // after the prefix's kernel (about their start-up time)
-constexpr int kEarlySlack = 6;
+constexpr int kEarlySlack = 4;
 
 // CTA w of W takes steps [begin(w), begin(w + 1)) of T. The first `early` CTAs
 // run beside a prefix's kernel and take `more` steps each in that time; the
@@ -304,10 +325,384 @@ __device__ __noinline__ void empty_rows(const PagedDecodeArgs& a, int s, int thr
   }
 }
 
-template <int D, int MT>
-__global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
+// What a consumer warp holds of a unit while it works on its 16 keys of every
+// tile: running maximum, sum and unnormalised output of the unit's rows.
+// lane = 4 g + q throughout.
+//
+// Up to 16 rows: S = Q K^T and O = P V with the query rows on the products'
+// 16 rows; the scores leave the first product in the layout in which the
+// second one takes them.
+template <class C>
+struct WarpRows16 {
+  static constexpr int D = C::D, FB = C::FB;
+  static constexpr int ROWS = 16;
+  int g, q, kw, ra, rb;                    // ra, rb: this lane's rows of the unit
+  uint32_t k_off, v_off, k_u, v_u, sw, q_off, q_u, q_at;
+  uint32_t qf[C::Q_IN_SMEM ? FB : D / 16][4];
+  float acc[D / 8][4];
+  float m_a, m_b, l_a, l_b;
+
+  __device__ __forceinline__ void init(int lane, int kw_, int mt) {
+    g = lane >> 2;
+    q = lane & 3;
+    kw = kw_;
+    ra = mt * 16 + g;
+    rb = ra + 8;
+    k_off = (uint32_t)((kw * 16 + (lane >> 4) * 8 + (lane & 7)) * 128);
+    v_off = (uint32_t)(C::KV + (kw * 16 + ((lane >> 3) & 1) * 8 + (lane & 7)) * 128);
+    k_u = (lane >> 3) & 1;
+    v_u = lane >> 4;
+    sw = lane & 7;
+    q_off = (uint32_t)((((lane >> 3) & 1) * 8 + (lane & 7)) * D * 2);
+    q_u = lane >> 4;
+  }
+  __device__ __forceinline__ void load_q(uint32_t (&f)[4], int ks) { ldmatrix4(f, q_at + q_off + (((2 * ks + q_u) ^ sw) << 4)); }
+  __device__ __forceinline__ void begin(uint32_t q_smem) {
+    q_at = q_smem;
+    if constexpr (!C::Q_IN_SMEM) {
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) load_q(qf[ks], ks);
+    }
+#pragma unroll
+    for (int nn = 0; nn < D / 8; ++nn) acc[nn][0] = acc[nn][1] = acc[nn][2] = acc[nn][3] = 0.f;
+    m_a = m_b = -INFINITY;
+    l_a = l_b = 0.f;
+  }
+  // Keys k0 .. k0 + 15 of a unit of `len`, of which every row sees `seen`.
+  __device__ __forceinline__ void tile(uint32_t st, const uint8_t* stage, int k0, int len, int seen, const RowInfo* info, int rows,
+                                       float c2) {
+    // scores in two chains of products, each half of the head
+    float x[2][4], y[2][4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[t][c] = y[t][c] = 0.f;
+    auto k_at = [&](int ks) { return st + k_off + (ks >> 2) * C::CHUNK + ((((2 * ks + k_u) & 7) ^ sw) << 4); };
+    auto v_at = [&](int np) { return st + v_off + (np >> 2) * C::CHUNK + ((((2 * np + v_u) & 7) ^ sw) << 4); };
+    uint32_t f[FB][4];  // of K, then of V
+#pragma unroll
+    for (int k1 = 0; k1 < D / 16; k1 += FB) {
+#pragma unroll
+      for (int i = 0; i < FB; ++i) ldmatrix4(f[i], k_at(k1 + i));
+      if constexpr (C::Q_IN_SMEM) {
+#pragma unroll
+        for (int i = 0; i < FB; ++i) load_q(qf[i], k1 + i);
+      }
+#pragma unroll
+      for (int i = 0; i < FB; ++i) {
+        const uint32_t(&qk)[4] = qf[C::Q_IN_SMEM ? i : k1 + i];
+        mma16816((k1 + i) & 1 ? y[0] : x[0], qk, f[i][0], f[i][1]);
+        mma16816((k1 + i) & 1 ? y[1] : x[1], qk, f[i][2], f[i][3]);
+      }
+    }
+    // the first values are on their way while the weights are computed
+#pragma unroll
+    for (int i = 0; i < FB; ++i) ldmatrix4_t(f[i], v_at(i));
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[t][c] += y[t][c];
+    const bool edge = k0 + 16 > seen;  // some key of this warp is hidden from some row
+    int lim_a = len, lim_b = len;      // keys that rows ra and rb see
+    if (edge) {
+      lim_a -= ra < rows ? info[ra].hidden : 0;
+      lim_b -= rb < rows ? info[rb].hidden : 0;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (k0 + 8 * t + 2 * q + (c & 1) >= (c < 2 ? lim_a : lim_b)) x[t][c] = -INFINITY;
+    }
+    float t_a = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
+    float t_b = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
+    t_a = fmaxf(t_a, __shfl_xor_sync(kFull, t_a, 1));
+    t_b = fmaxf(t_b, __shfl_xor_sync(kFull, t_b, 1));
+    t_a = fmaxf(t_a, __shfl_xor_sync(kFull, t_a, 2)) * c2;
+    t_b = fmaxf(t_b, __shfl_xor_sync(kFull, t_b, 2)) * c2;
+    const bool up_a = t_a > m_a + kRescaleLog2, up_b = t_b > m_b + kRescaleLog2;
+    if (__any_sync(kFull, up_a || up_b)) {  // always at a row's first key
+      const float f_a = up_a ? ex2_approx(m_a - t_a) : 1.f, f_b = up_b ? ex2_approx(m_b - t_b) : 1.f;
+      m_a = up_a ? t_a : m_a;
+      m_b = up_b ? t_b : m_b;
+      l_a *= f_a;
+      l_b *= f_b;
+#pragma unroll
+      for (int nn = 0; nn < D / 8; ++nn) {
+        acc[nn][0] *= f_a;
+        acc[nn][1] *= f_a;
+        acc[nn][2] *= f_b;
+        acc[nn][3] *= f_b;
+      }
+    }
+    const float n_a = m_a == -INFINITY ? 0.f : -m_a, n_b = m_b == -INFINITY ? 0.f : -m_b;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      x[t][0] = ex2_approx(fmaf(x[t][0], c2, n_a));
+      x[t][1] = ex2_approx(fmaf(x[t][1], c2, n_a));
+      x[t][2] = ex2_approx(fmaf(x[t][2], c2, n_b));
+      x[t][3] = ex2_approx(fmaf(x[t][3], c2, n_b));
+      l_a += x[t][0] + x[t][1];
+      l_b += x[t][2] + x[t][3];
+    }
+    // P is rounded to bf16 for the product (half a step of each weight);
+    // the sums l keep the unrounded weights
+    const uint32_t pf[4] = {pack_bf16x2(x[0][0], x[0][1]), pack_bf16x2(x[0][2], x[0][3]),
+                            pack_bf16x2(x[1][0], x[1][1]), pack_bf16x2(x[1][2], x[1][3])};
+    // values of keys that some row does not see stay out of the product
+    // (0 times NaN); keys 2q, 2q + 1 and 8 + 2q, 8 + 2q + 1 are this lane's
+    const uint32_t keep0 = edge ? keep_pair(k0 + 2 * q, seen) : kFull, keep1 = edge ? keep_pair(k0 + 8 + 2 * q, seen) : kFull;
+#pragma unroll
+    for (int n1 = 0; n1 < D / 16; n1 += FB) {
+      if (n1 > 0) {
+#pragma unroll
+        for (int i = 0; i < FB; ++i) ldmatrix4_t(f[i], v_at(n1 + i));
+      }
+#pragma unroll
+      for (int i = 0; i < FB; ++i) {
+        if (edge) {
+          f[i][0] &= keep0;
+          f[i][1] &= keep1;
+          f[i][2] &= keep0;
+          f[i][3] &= keep1;
+        }
+        mma16816(acc[2 * (n1 + i)], pf, f[i][0], f[i][1]);
+        mma16816(acc[2 * (n1 + i) + 1], pf, f[i][2], f[i][3]);
+      }
+    }
+    if (edge && len > seen) {
+      // the newest keys, seen by some rows only: added row by row
+      for (int k = max(k0, seen); k < min(k0 + 16, len); ++k) {
+        const int c = k - k0, src = (g << 2) | ((c & 7) >> 1);
+        const float pa = (c & 8) ? ((c & 1) ? x[1][1] : x[1][0]) : ((c & 1) ? x[0][1] : x[0][0]);
+        const float pb = (c & 8) ? ((c & 1) ? x[1][3] : x[1][2]) : ((c & 1) ? x[0][3] : x[0][2]);
+        const float p_a = __shfl_sync(kFull, pa, src), p_b = __shfl_sync(kFull, pb, src);
+        const int r = kw * 16 + c;
+        const uint8_t* vr = stage + C::KV + r * 128 + q * 4;
+#pragma unroll
+        for (int nn = 0; nn < D / 8; ++nn) {
+          const uint32_t v2 = *reinterpret_cast<const uint32_t*>(vr + (nn >> 3) * C::CHUNK + (((nn & 7) ^ (r & 7)) << 4));
+          const float v0 = __uint_as_float(v2 << 16), v1 = __uint_as_float(v2 & 0xffff0000u);
+          if (k < lim_a) {
+            acc[nn][0] = fmaf(p_a, v0, acc[nn][0]);
+            acc[nn][1] = fmaf(p_a, v1, acc[nn][1]);
+          }
+          if (k < lim_b) {
+            acc[nn][2] = fmaf(p_b, v0, acc[nn][2]);
+            acc[nn][3] = fmaf(p_b, v1, acc[nn][3]);
+          }
+        }
+      }
+    }
+  }
+  // Maxima and sums of the rows, [4 warps][16].
+  __device__ __forceinline__ void put_sums(float2* ml) {
+    l_a += __shfl_xor_sync(kFull, l_a, 1);
+    l_b += __shfl_xor_sync(kFull, l_b, 1);
+    l_a += __shfl_xor_sync(kFull, l_a, 2);
+    l_b += __shfl_xor_sync(kFull, l_b, 2);
+    if (q == 0) {
+      ml[kw * 16 + g] = make_float2(m_a, l_a);
+      ml[kw * 16 + g + 8] = make_float2(m_b, l_b);
+    }
+  }
+  // Column c of row r of warp w's output. In the stage a warp takes the place
+  // of its own 16 keys and values (nobody else reads those): 32 columns per
+  // chunk. 16-byte (32-byte) units permuted by the row, so that the eight rows
+  // of a store differ in banks.
+  static __device__ __forceinline__ uint8_t* om_at(uint8_t* om, int w, int r, int c) {
+    if (C::MERGE_IN_STAGE) return om + (c >> 5) * C::CHUNK + w * 2048 + r * 128 + (((c & 31) * 4) ^ ((r & 7) << 4));
+    return om + ((w * 16 + r) * C::DW + (c ^ ((8 * r) & 56 & (C::DW - 1)))) * 4;
+  }
+  // Columns d0 .. d0 + DW - 1 of the group's first n rows.
+  __device__ __forceinline__ void put_out(uint8_t* om, int d0, int n) {
+#pragma unroll
+    for (int nn = 0; nn < C::DW / 8; ++nn) {
+      // (d0 is a constant in the unrolled caller)
+      const float* x = acc[d0 / 8 + nn];
+      if (g < n) *reinterpret_cast<float2*>(om_at(om, kw, g, 8 * nn + 2 * q)) = make_float2(x[0], x[1]);
+      if (g + 8 < n) *reinterpret_cast<float2*>(om_at(om, kw, g + 8, 8 * nn + 2 * q)) = make_float2(x[2], x[3]);
+    }
+  }
+};
+
+// Up to 8 rows (one new token of up to 8 query heads): S^T = K Q^T and
+// O^T = V^T P^T, keys and columns on the products' 16 rows and the query rows
+// on their 8 columns, half the products, exponentials and registers of the
+// form above. P^T changes layout by a transposition of its 8 x 8 halves.
+template <class C>
+struct WarpRows8 {
+  static constexpr int D = C::D, FB = C::FB;
+  static constexpr int ROWS = 8;
+  int g, q, kw;                  // this lane's rows: 2q, 2q + 1; its keys of the warp's 16: g, g + 8
+  uint32_t k_off, v_off, u_k, u_v, sw, q_off;
+  uint32_t qf[D / 32][4];
+  float acc[D / 16][4];          // columns 16 i + g (+ 8) of rows 2q, 2q + 1
+  float m0, m1, l0, l1;
+
+  __device__ __forceinline__ void init(int lane, int kw_, int) {
+    g = lane >> 2;
+    q = lane & 3;
+    kw = kw_;
+    k_off = (uint32_t)((kw * 16 + ((lane >> 3) & 1) * 8 + (lane & 7)) * 128);
+    u_k = lane >> 4;
+    v_off = (uint32_t)(C::KV + (kw * 16 + (lane >> 4) * 8 + (lane & 7)) * 128);
+    u_v = (lane >> 3) & 1;
+    sw = lane & 7;
+    q_off = (uint32_t)((lane & 7) * D * 2) + 0u;
+  }
+  __device__ __forceinline__ void begin(uint32_t q_smem) {
+    const uint32_t u = (uint32_t)((threadIdx.x & 31) >> 3);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) ldmatrix4(qf[i], q_smem + q_off + (((4 * i + u) ^ sw) << 4));
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    m0 = m1 = -INFINITY;
+    l0 = l1 = 0.f;
+  }
+  __device__ __forceinline__ void tile(uint32_t st, const uint8_t* stage, int k0, int len, int seen, const RowInfo* info, int rows,
+                                       float c2) {
+    float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};  // two chains of products
+    auto k_at = [&](int ks) { return st + k_off + (ks >> 2) * C::CHUNK + ((((2 * ks + u_k) & 7) ^ sw) << 4); };
+    auto v_at = [&](int np) { return st + v_off + (np >> 2) * C::CHUNK + ((((2 * np + u_v) & 7) ^ sw) << 4); };
+    uint32_t f[FB][4];  // of K, then of V
+#pragma unroll
+    for (int k1 = 0; k1 < D / 16; k1 += FB) {
+#pragma unroll
+      for (int i = 0; i < FB; ++i) ldmatrix4(f[i], k_at(k1 + i));
+#pragma unroll
+      for (int i = 0; i < FB; ++i) {
+        const int ks = k1 + i;
+        mma16816(ks & 1 ? y : x, f[i], qf[ks >> 1][2 * (ks & 1)], qf[ks >> 1][2 * (ks & 1) + 1]);
+      }
+    }
+    // the first values are on their way while the weights are computed
+#pragma unroll
+    for (int i = 0; i < FB; ++i) ldmatrix4_t(f[i], v_at(i));
+#pragma unroll
+    for (int c = 0; c < 4; ++c) x[c] += y[c];
+    const bool edge = k0 + 16 > seen;  // some key of this warp is hidden from some row
+    int lim0 = len, lim1 = len;        // keys that rows 2q and 2q + 1 see
+    if (edge) {
+      lim0 -= 2 * q < rows ? info[2 * q].hidden : 0;
+      lim1 -= 2 * q + 1 < rows ? info[2 * q + 1].hidden : 0;
+      if (k0 + g >= lim0) x[0] = -INFINITY;
+      if (k0 + g >= lim1) x[1] = -INFINITY;
+      if (k0 + g + 8 >= lim0) x[2] = -INFINITY;
+      if (k0 + g + 8 >= lim1) x[3] = -INFINITY;
+    }
+    float t0 = fmaxf(x[0], x[2]), t1 = fmaxf(x[1], x[3]);
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      t0 = fmaxf(t0, __shfl_xor_sync(kFull, t0, o));
+      t1 = fmaxf(t1, __shfl_xor_sync(kFull, t1, o));
+    }
+    t0 *= c2;
+    t1 *= c2;
+    const bool up0 = t0 > m0 + kRescaleLog2, up1 = t1 > m1 + kRescaleLog2;
+    if (__any_sync(kFull, up0 || up1)) {  // always at a row's first key
+      const float f0 = up0 ? ex2_approx(m0 - t0) : 1.f, f1 = up1 ? ex2_approx(m1 - t1) : 1.f;
+      m0 = up0 ? t0 : m0;
+      m1 = up1 ? t1 : m1;
+      l0 *= f0;
+      l1 *= f1;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        acc[i][0] *= f0;
+        acc[i][1] *= f1;
+        acc[i][2] *= f0;
+        acc[i][3] *= f1;
+      }
+    }
+    const float n0 = m0 == -INFINITY ? 0.f : -m0, n1 = m1 == -INFINITY ? 0.f : -m1;
+    x[0] = ex2_approx(fmaf(x[0], c2, n0));
+    x[1] = ex2_approx(fmaf(x[1], c2, n1));
+    x[2] = ex2_approx(fmaf(x[2], c2, n0));
+    x[3] = ex2_approx(fmaf(x[3], c2, n1));
+    l0 += x[0] + x[2];
+    l1 += x[1] + x[3];
+    // P is rounded to bf16 for the product (half a step of each weight);
+    // the sums l keep the unrounded weights
+    const uint32_t b0 = transpose8(pack_bf16x2(x[0], x[1])), b1 = transpose8(pack_bf16x2(x[2], x[3]));
+    // values of keys that some row does not see stay out of the product
+    // (0 times NaN); keys 2q, 2q + 1 and 8 + 2q, 8 + 2q + 1 are this lane's
+    const uint32_t keep0 = edge ? keep_pair(k0 + 2 * q, seen) : kFull, keep1 = edge ? keep_pair(k0 + 8 + 2 * q, seen) : kFull;
+#pragma unroll
+    for (int i1 = 0; i1 < D / 16; i1 += FB) {
+      if (i1 > 0) {
+#pragma unroll
+        for (int i = 0; i < FB; ++i) ldmatrix4_t(f[i], v_at(i1 + i));
+      }
+#pragma unroll
+      for (int i = 0; i < FB; ++i) {
+        if (edge) {
+          f[i][0] &= keep0;
+          f[i][1] &= keep0;
+          f[i][2] &= keep1;
+          f[i][3] &= keep1;
+        }
+        mma16816(acc[i1 + i], f[i], b0, b1);
+      }
+    }
+    if (edge && len > seen) {
+      // the newest keys, seen by some rows only: added row by row
+      for (int k = max(k0, seen); k < min(k0 + 16, len); ++k) {
+        const int c = k - k0, src = ((c & 7) << 2) | q;
+        const float p0 = __shfl_sync(kFull, (c & 8) ? x[2] : x[0], src), p1 = __shfl_sync(kFull, (c & 8) ? x[3] : x[1], src);
+        const int r = kw * 16 + c;
+        const uint8_t* vr = stage + C::KV + r * 128 + g * 2;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint8_t* p = vr + (i >> 2) * C::CHUNK;
+          const float v0 = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(p + (((2 * i & 7) ^ (r & 7)) << 4)) << 16);
+          const float v1 = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(p + ((((2 * i + 1) & 7) ^ (r & 7)) << 4)) << 16);
+          if (k < lim0) {
+            acc[i][0] = fmaf(p0, v0, acc[i][0]);
+            acc[i][2] = fmaf(p0, v1, acc[i][2]);
+          }
+          if (k < lim1) {
+            acc[i][1] = fmaf(p1, v0, acc[i][1]);
+            acc[i][3] = fmaf(p1, v1, acc[i][3]);
+          }
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void put_sums(float2* ml) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      l0 += __shfl_xor_sync(kFull, l0, o);
+      l1 += __shfl_xor_sync(kFull, l1, o);
+    }
+    if (g == 0) {
+      ml[kw * 16 + 2 * q] = make_float2(m0, l0);
+      ml[kw * 16 + 2 * q + 1] = make_float2(m1, l1);
+    }
+  }
+  // In the stage, the place of the warp's own 16 keys: 64 columns of 8 rows
+  // per chunk, 32-byte units permuted by the pair of rows (a store's four).
+  static __device__ __forceinline__ uint8_t* om_at(uint8_t* om, int w, int r, int c) {
+    return om + (c >> 6) * C::CHUNK + w * 2048 + r * 256 + ((c & 63) ^ ((r >> 1) << 3)) * 4;
+  }
+  __device__ __forceinline__ void put_out(uint8_t* om, int, int n) {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      if (2 * q < n) {
+        *reinterpret_cast<float*>(om_at(om, kw, 2 * q, 16 * i + g)) = acc[i][0];
+        *reinterpret_cast<float*>(om_at(om, kw, 2 * q, 16 * i + g + 8)) = acc[i][2];
+      }
+      if (2 * q + 1 < n) {
+        *reinterpret_cast<float*>(om_at(om, kw, 2 * q + 1, 16 * i + g)) = acc[i][1];
+        *reinterpret_cast<float*>(om_at(om, kw, 2 * q + 1, 16 * i + g + 8)) = acc[i][3];
+      }
+    }
+  }
+};
+
+template <int D, int ROWS, bool BESIDE>
+__global__ void __launch_bounds__(Cfg<D, ROWS, BESIDE>::THREADS, Cfg<D, ROWS, BESIDE>::CTAS)
     decode_paged_kernel(const __grid_constant__ PagedDecodeArgs a) {
-  using C = Cfg<D, MT>;
+  using C = Cfg<D, ROWS, BESIDE>;
+  constexpr int MT = C::MT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -433,23 +828,20 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
   // After a wait ran out a warp goes on without waiting or computing, so that
   // it still reaches every barrier; the status word tells.
   const int cw = warp - 1, mt = cw >> 2, kw = cw & 3;
-  const int g = lane >> 2, q = lane & 3;
-  const int ct = kw * 32 + lane;  // thread of the 16 rows' 128
+  const int ct = kw * 32 + lane;  // thread of the group's 128
   const float c2 = a.scale_log2;
-  const int ra = mt * 16 + g, rb = ra + 8;  // this lane's query rows
   float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML) + mt * 64;  // [4][16]
-  const uint32_t k_off = (uint32_t)((kw * 16 + (lane >> 4) * 8 + (lane & 7)) * 128);
-  const uint32_t v_off = (uint32_t)(C::KV + (kw * 16 + ((lane >> 3) & 1) * 8 + (lane & 7)) * 128);
-  const uint32_t k_u = (lane >> 3) & 1, v_u = lane >> 4, sw = lane & 7;
   // A unit's 16 query rows, D / 8 vectors each, vector u of row r at u ^ (r & 7)
   const uint32_t q_buf = sbase + C::OFF_Q + mt * 16 * D * 2;
-  const uint32_t q_off = (uint32_t)((((lane >> 3) & 1) * 8 + (lane & 7)) * D * 2), q_u = lane >> 4;
+  using Warp = std::conditional_t<ROWS == 8, WarpRows8<C>, WarpRows16<C>>;
+  Warp st;
+  st.init(lane, kw, mt);
   auto fetch_q = [&](int seq, int head, int buf) {
     const bool pre = seq >= a.B;
     const int rows = pre ? a.B * R : R;
     const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(a.Q) + (pre ? 0 : seq * a.q_b) + (long long)head * a.G * a.q_h;
 #pragma unroll
-    for (int e = ct; e < 16 * (D / 8); e += 128) {
+    for (int e = ct; e < Warp::ROWS * (D / 8); e += 128) {
       const int r = e / (D / 8), u = e - r * (D / 8);
       const bool valid = mt * 16 + r < rows;
       const __nv_bfloat16* src = base + (valid ? row_info[(pre ? 16 * MT : 0) + mt * 16 + r].q + u * 8 : 0);
@@ -474,177 +866,24 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
     const bool active = mt * 16 < rows;                   // else these warps only keep step
     copies_done();
     named_bar(1 + mt, 128);  // this unit's queries are there; the other buffer has been read
-    uint32_t qf[C::Q_IN_SMEM ? C::FB : D / 16][4];
-    if constexpr (!C::Q_IN_SMEM) {
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) ldmatrix4(qf[ks], q_buf + qb * C::QBUF + q_off + (((2 * ks + q_u) ^ sw) << 4));
-    }
+    st.begin(q_buf + qb * C::QBUF);
     more = wk.advance(a, C::BK);
     if (more) fetch_q(wk.sh.seq, wk.sh.head, qb ^ 1);
-    float acc[D / 8][4];
-#pragma unroll
-    for (int nn = 0; nn < D / 8; ++nn) acc[nn][0] = acc[nn][1] = acc[nn][2] = acc[nn][3] = 0.f;
-    float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;
     for (int j = 0; j < n; ++j, ++it) {
       const int s = it % C::STAGES;
       if (ok) ok = mbar_wait_warp(FULL(s), (it / C::STAGES) & 1, a.status, a.wait_limit_ns);
       const int k0 = (first + j) * C::BK + kw * 16;  // this warp's keys
-      if (ok && active && k0 < len) {
-        const uint32_t st = sbase + s * C::STAGE;
-        // scores in two chains of products, each half of the head
-        float x[2][4], y[2][4];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) x[t][c] = y[t][c] = 0.f;
-        auto k_at = [&](int ks) { return st + k_off + (ks >> 2) * C::CHUNK + ((((2 * ks + k_u) & 7) ^ sw) << 4); };
-        auto v_at = [&](int np) { return st + v_off + (np >> 2) * C::CHUNK + ((((2 * np + v_u) & 7) ^ sw) << 4); };
-        constexpr int FB = C::FB;  // fragments loaded at a time
-        uint32_t f[FB][4];         // of K, then of V
-#pragma unroll
-        for (int k1 = 0; k1 < D / 16; k1 += FB) {
-#pragma unroll
-          for (int i = 0; i < FB; ++i) ldmatrix4(f[i], k_at(k1 + i));
-          if constexpr (C::Q_IN_SMEM) {
-#pragma unroll
-            for (int i = 0; i < FB; ++i) ldmatrix4(qf[i], q_buf + qb * C::QBUF + q_off + (((2 * (k1 + i) + q_u) ^ sw) << 4));
-          }
-#pragma unroll
-          for (int i = 0; i < FB; ++i) {
-            const uint32_t(&qk)[4] = qf[C::Q_IN_SMEM ? i : k1 + i];
-            mma16816((k1 + i) & 1 ? y[0] : x[0], qk, f[i][0], f[i][1]);
-            mma16816((k1 + i) & 1 ? y[1] : x[1], qk, f[i][2], f[i][3]);
-          }
-        }
-        // the first values are on their way while the weights are computed
-#pragma unroll
-        for (int i = 0; i < FB; ++i) ldmatrix4_t(f[i], v_at(i));
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) x[t][c] += y[t][c];
-        const bool edge = k0 + 16 > seen;  // some key of this warp is hidden from some row
-        int lim_a = len, lim_b = len;      // keys that rows ra and rb see
-        if (edge) {
-          lim_a -= ra < rows ? info[ra].hidden : 0;
-          lim_b -= rb < rows ? info[rb].hidden : 0;
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (k0 + 8 * t + 2 * q + (c & 1) >= (c < 2 ? lim_a : lim_b)) x[t][c] = -INFINITY;
-        }
-        float t_a = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
-        float t_b = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
-        t_a = fmaxf(t_a, __shfl_xor_sync(kFull, t_a, 1));
-        t_b = fmaxf(t_b, __shfl_xor_sync(kFull, t_b, 1));
-        t_a = fmaxf(t_a, __shfl_xor_sync(kFull, t_a, 2)) * c2;
-        t_b = fmaxf(t_b, __shfl_xor_sync(kFull, t_b, 2)) * c2;
-        const bool up_a = t_a > m_a + kRescaleLog2, up_b = t_b > m_b + kRescaleLog2;
-        if (__any_sync(kFull, up_a || up_b)) {  // always at a row's first key
-          const float f_a = up_a ? ex2_approx(m_a - t_a) : 1.f, f_b = up_b ? ex2_approx(m_b - t_b) : 1.f;
-          m_a = up_a ? t_a : m_a;
-          m_b = up_b ? t_b : m_b;
-          l_a *= f_a;
-          l_b *= f_b;
-#pragma unroll
-          for (int nn = 0; nn < D / 8; ++nn) {
-            acc[nn][0] *= f_a;
-            acc[nn][1] *= f_a;
-            acc[nn][2] *= f_b;
-            acc[nn][3] *= f_b;
-          }
-        }
-        const float n_a = m_a == -INFINITY ? 0.f : -m_a, n_b = m_b == -INFINITY ? 0.f : -m_b;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          x[t][0] = ex2_approx(fmaf(x[t][0], c2, n_a));
-          x[t][1] = ex2_approx(fmaf(x[t][1], c2, n_a));
-          x[t][2] = ex2_approx(fmaf(x[t][2], c2, n_b));
-          x[t][3] = ex2_approx(fmaf(x[t][3], c2, n_b));
-          l_a += x[t][0] + x[t][1];
-          l_b += x[t][2] + x[t][3];
-        }
-        // P is rounded to bf16 for the product (half a step of each weight);
-        // the sums l keep the unrounded weights
-        const uint32_t pf[4] = {pack_bf16x2(x[0][0], x[0][1]), pack_bf16x2(x[0][2], x[0][3]),
-                                pack_bf16x2(x[1][0], x[1][1]), pack_bf16x2(x[1][2], x[1][3])};
-        // values of keys that some row does not see stay out of the product
-        // (0 times NaN); keys 2q, 2q + 1 and 8 + 2q, 8 + 2q + 1 are this lane's
-        uint32_t keep0 = kFull, keep1 = kFull;
-        if (edge) {
-          auto keep = [&](int k) { return (k < seen ? 0xffffu : 0u) | (k + 1 < seen ? 0xffff0000u : 0u); };
-          keep0 = keep(k0 + 2 * q);
-          keep1 = keep(k0 + 8 + 2 * q);
-        }
-#pragma unroll
-        for (int n1 = 0; n1 < D / 16; n1 += FB) {
-          if (n1 > 0) {
-#pragma unroll
-            for (int i = 0; i < FB; ++i) ldmatrix4_t(f[i], v_at(n1 + i));
-          }
-#pragma unroll
-          for (int i = 0; i < FB; ++i) {
-            if (edge) {
-              f[i][0] &= keep0;
-              f[i][1] &= keep1;
-              f[i][2] &= keep0;
-              f[i][3] &= keep1;
-            }
-            mma16816(acc[2 * (n1 + i)], pf, f[i][0], f[i][1]);
-            mma16816(acc[2 * (n1 + i) + 1], pf, f[i][2], f[i][3]);
-          }
-        }
-        if (edge && len > seen) {
-          // the newest keys, seen by some rows only: added row by row
-          for (int k = max(k0, seen); k < min(k0 + 16, len); ++k) {
-            const int c = k - k0, src = (lane & 28) | ((c & 7) >> 1);
-            const float pa = (c & 8) ? ((c & 1) ? x[1][1] : x[1][0]) : ((c & 1) ? x[0][1] : x[0][0]);
-            const float pb = (c & 8) ? ((c & 1) ? x[1][3] : x[1][2]) : ((c & 1) ? x[0][3] : x[0][2]);
-            const float p_a = __shfl_sync(kFull, pa, src), p_b = __shfl_sync(kFull, pb, src);
-            const int r = kw * 16 + c;
-            const uint8_t* vr = smem + s * C::STAGE + C::KV + r * 128 + q * 4;
-#pragma unroll
-            for (int nn = 0; nn < D / 8; ++nn) {
-              const uint32_t v2 = *reinterpret_cast<const uint32_t*>(vr + (nn >> 3) * C::CHUNK + (((nn & 7) ^ (r & 7)) << 4));
-              const float v0 = __uint_as_float(v2 << 16), v1 = __uint_as_float(v2 & 0xffff0000u);
-              if (k < lim_a) {
-                acc[nn][0] = fmaf(p_a, v0, acc[nn][0]);
-                acc[nn][1] = fmaf(p_a, v1, acc[nn][1]);
-              }
-              if (k < lim_b) {
-                acc[nn][2] = fmaf(p_b, v0, acc[nn][2]);
-                acc[nn][3] = fmaf(p_b, v1, acc[nn][3]);
-              }
-            }
-          }
-        }
-      }
+      if (ok && active && k0 < len) st.tile(sbase + s * C::STAGE, smem + s * C::STAGE, k0, len, seen, info, rows, c2);
       __syncwarp();
       if (lane == 0 && !(C::MERGE_IN_STAGE && j + 1 == n)) mbar_arrive(EMPTY(s));
     }
 
     if (!active) continue;
-    // the four warps of each 16 rows meet in shared memory: maxima, sums and
-    // outputs as they are, weighted and added by whoever writes them out
-    l_a += __shfl_xor_sync(kFull, l_a, 1);
-    l_b += __shfl_xor_sync(kFull, l_b, 1);
-    l_a += __shfl_xor_sync(kFull, l_a, 2);
-    l_b += __shfl_xor_sync(kFull, l_b, 2);
-    if (q == 0) {
-      ml[kw * 16 + g] = make_float2(m_a, l_a);
-      ml[kw * 16 + g + 8] = make_float2(m_b, l_b);
-    }
+    // the four warps of a group of rows meet in shared memory: maxima, sums
+    // and outputs as they are, weighted and added by whoever writes them out
+    st.put_sums(ml);
     const int last_stage = (it - 1) % C::STAGES;
     uint8_t* om = smem + (C::MERGE_IN_STAGE ? last_stage * C::STAGE : C::OFF_MERGE + mt * C::MERGE);
-    // Column c of row r of warp w. In the stage a warp takes the place of its
-    // own 16 keys and values (nobody else reads those): 32 columns per chunk.
-    // 16-byte (32-byte) units permuted by the row, so that the eight rows of a
-    // store differ in banks.
-    auto om_at = [&](int w, int r, int c) {
-      if (C::MERGE_IN_STAGE) return om + (c >> 5) * C::CHUNK + w * 2048 + r * 128 + (((c & 31) * 4) ^ ((r & 7) << 4));
-      return om + ((w * 16 + r) * C::DW + (c ^ ((8 * r) & 56 & (C::DW - 1)))) * 4;
-    };
     const long long unit = (long long)seq * Hkv + head;
     const bool direct = begins && ends && a.prefix_len == 0;
     const long long part_row = part_slot(a, blockIdx.x, begins, ends, unit) * a.slot_rows;
@@ -654,20 +893,7 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
 #pragma unroll
     for (int d0 = 0; d0 < D; d0 += DW) {
       if (d0 > 0) named_bar(1 + mt, 128);  // the columns before these have been read
-      if (g < group_rows) {
-#pragma unroll
-        for (int nn = 0; nn < DW / 8; ++nn) {
-          const float* x = acc[d0 / 8 + nn];
-          *reinterpret_cast<float2*>(om_at(kw, g, 8 * nn + 2 * q)) = make_float2(x[0], x[1]);
-        }
-      }
-      if (g + 8 < group_rows) {
-#pragma unroll
-        for (int nn = 0; nn < DW / 8; ++nn) {
-          const float* x = acc[d0 / 8 + nn];
-          *reinterpret_cast<float2*>(om_at(kw, g + 8, 8 * nn + 2 * q)) = make_float2(x[2], x[3]);
-        }
-      }
+      st.put_out(om, d0, group_rows);
       named_bar(1 + mt, 128);
       for (int e = ct; e < group_rows * (DW / 4); e += 128) {
         const int r = e / (DW / 4), c = (e - r * (DW / 4)) * 4;
@@ -682,7 +908,7 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           const float f = ex2_approx(t[w].x - mu);
-          const float4 z = *reinterpret_cast<const float4*>(om_at(w, r, c));
+          const float4 z = *reinterpret_cast<const float4*>(Warp::om_at(om, w, r, c));
           ll = fmaf(t[w].y, f, ll);
           y.x = fmaf(z.x, f, y.x);
           y.y = fmaf(z.y, f, y.y);
@@ -853,9 +1079,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const __
   if (lane == 0) a.LSE[(long long)unit * R + r] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
-template <int D, int MT>
+template <int D, int ROWS, bool BESIDE>
 cudaError_t launch(const PagedDecodeArgs& a, cudaStream_t st) {
-  using C = Cfg<D, MT>;
+  using C = Cfg<D, ROWS, BESIDE>;
   // programmatic dependent launches: each kernel is set up while the one
   // before it runs; the own keys' kernel takes the SMs that a prefix's kernel
   // leaves idle (and waits for that kernel's end before its own). The first
@@ -871,7 +1097,7 @@ cudaError_t launch(const PagedDecodeArgs& a, cudaStream_t st) {
   cfg.gridDim = dim3((unsigned)a.ctas);
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM_ALLOC;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_paged_kernel<D, MT>, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_paged_kernel<D, ROWS, BESIDE>, a);
   if (e != cudaSuccess) return e;
   cfg.numAttrs = 1;
   cfg.blockDim = dim3(32 * kMergeWarps);
@@ -894,14 +1120,14 @@ cudaError_t launch(const PagedDecodeArgs& a, cudaStream_t st) {
 
 // Also allows the kernel its shared memory on the current device; every launch
 // follows a paged_layout() on the same device.
-template <int D, int MT>
+template <int D, int ROWS, bool BESIDE>
 int ctas_per_sm() {
-  using C = Cfg<D, MT>;
-  if (cudaFuncSetAttribute(decode_paged_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC) !=
+  using C = Cfg<D, ROWS, BESIDE>;
+  if (cudaFuncSetAttribute(decode_paged_kernel<D, ROWS, BESIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC) !=
       cudaSuccess)
     return 0;
   int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_paged_kernel<D, MT>, C::THREADS, C::SMEM_ALLOC) !=
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_paged_kernel<D, ROWS, BESIDE>, C::THREADS, C::SMEM_ALLOC) !=
       cudaSuccess)
     return 0;
   return n;
@@ -909,21 +1135,37 @@ int ctas_per_sm() {
 
 constexpr int kMaxDevices = 64;
 std::mutex g_slots_mu;
-int g_slots[kMaxDevices][2][3] = {};  // [device][d == 128][16, 32, 64 rows] -> resident CTAs
+int g_slots[kMaxDevices][2][5] = {};  // [device][d == 128][8, 16, 32, 64 rows, 8 beside a prefix] -> resident CTAs
 
-int resident_ctas(int d, int mt) {
+template <int D>
+int ctas_per_sm(int rows, bool beside) {
+  return rows == 8    ? (beside ? ctas_per_sm<D, 8, true>() : ctas_per_sm<D, 8, false>())
+         : rows == 16 ? ctas_per_sm<D, 16, false>()
+         : rows == 32 ? ctas_per_sm<D, 32, false>()
+                      : ctas_per_sm<D, 64, false>();
+}
+
+int resident_ctas(int d, int rows, bool beside) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
   std::lock_guard<std::mutex> lk(g_slots_mu);
-  int& slot = g_slots[dev][d == 128][mt >> 1];
+  int& slot = g_slots[dev][d == 128][rows == 8 ? (beside ? 4 : 0) : rows == 16 ? 1 : rows == 32 ? 2 : 3];
   if (slot == 0) {
     int sms = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    const int n = d == 128 ? (mt == 1 ? ctas_per_sm<128, 1>() : mt == 2 ? ctas_per_sm<128, 2>() : ctas_per_sm<128, 4>())
-                           : (mt == 1 ? ctas_per_sm<64, 1>() : mt == 2 ? ctas_per_sm<64, 2>() : ctas_per_sm<64, 4>());
-    slot = sms * n;
+    slot = sms * (d == 128 ? ctas_per_sm<128>(rows, beside) : ctas_per_sm<64>(rows, beside));
   }
   return slot;
+}
+
+template <int D>
+cudaError_t launch_d(const PagedDecodeArgs& a, cudaStream_t st) {
+  switch (a.slot_rows) {
+    case 8: return a.pre_splits > 0 ? launch<D, 8, true>(a, st) : launch<D, 8, false>(a, st);
+    case 16: return launch<D, 16, false>(a, st);
+    case 32: return launch<D, 32, false>(a, st);
+    default: return launch<D, 64, false>(a, st);
+  }
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -935,10 +1177,9 @@ PagedLayout paged_layout(int B, int Hkv, int rows, int prefix_len, int d) {
   const long long pre_rows = prefix_len > 0 ? (long long)B * rows : 0;
   const bool own_kernel = pre_rows > kPagedMaxRows;
   const long long most = pre_rows > rows && !own_kernel ? pre_rows : rows;
-  const int mt = most <= 16 ? 1 : most <= 32 ? 2 : 4;
-  L.ctas = resident_ctas(d, mt);
+  L.slot_rows = most <= 8 ? 8 : most <= 16 ? 16 : most <= 32 ? 32 : 64;
+  L.ctas = resident_ctas(d, L.slot_rows, own_kernel);
   if (L.ctas <= 0) return L;
-  L.slot_rows = 16 * mt;
   L.n_seq = B + (pre_rows > 0 && !own_kernel ? 1 : 0);
   const size_t units = (size_t)L.n_seq * Hkv;
   const size_t slots = 2 * (size_t)L.ctas + (prefix_len > 0 ? units : 0);
@@ -997,17 +1238,7 @@ PrefixPlan plan_prefix_beside(int B, int rows, int Hkv, int prefix_len, int d, i
 
 cudaError_t launch_decode_paged_bf16(const PagedDecodeArgs& a, int d, cudaStream_t st) {
   if (a.ctas < 1) return cudaErrorInvalidValue;
-  if (d == 128) {
-    if (a.slot_rows == 16) return launch<128, 1>(a, st);
-    if (a.slot_rows == 32) return launch<128, 2>(a, st);
-    return launch<128, 4>(a, st);
-  }
-  if (d == 64) {
-    if (a.slot_rows == 16) return launch<64, 1>(a, st);
-    if (a.slot_rows == 32) return launch<64, 2>(a, st);
-    return launch<64, 4>(a, st);
-  }
-  return cudaErrorInvalidValue;
+  return d == 128 ? launch_d<128>(a, st) : d == 64 ? launch_d<64>(a, st) : cudaErrorInvalidValue;
 }
 
 }  // namespace fa
