@@ -24,16 +24,30 @@
 // rows it is a matrix product of its own (launch_prefix_bf16), and only its
 // partial results meet the own keys' here.
 //
-// CTA: one producer warp and 4 consumer warps per 16 query rows. The producer
-// reads page numbers a tile ahead and lets each lane issue one TMA box (64
-// columns of up to 64 rows of one page) into a ring of tiles. Consumer warp
+// CTA: one producer warp and four consumer warps per 16 (or 8) query rows. The
+// producer reads page numbers a tile ahead and lets each lane issue one TMA box
+// (64 columns of up to 64 rows of one page) into a ring of tiles. Consumer warp
 // kw owns keys 16 kw .. 16 kw + 15 of every tile and keeps its own running
 // maximum, sum and output in registers: no exchange between warps until the
-// piece ends. Bytes bound this kernel (4 d bytes per key against 4 d R flops);
-// with keys split over warps the warp-level mma.sync needs no barrier, no
-// tensor-memory round trip and no transposed copy of P per tile, which is what
-// a short cache's latency consists of, and its rate is far from the limit up
-// to 32 rows.
+// piece ends. Bytes bound this kernel (4 d bytes per key against 4 d R flops):
+// with keys split over warps the warp-level mma.sync needs no barrier and no
+// tensor-memory round trip per tile, which is what a short cache's latency
+// consists of, and its rate is far from the limit up to 32 rows. Two CTAs share
+// an SM (up to 16 rows), one loading while the other one merges.
+//
+// Measured on a GB300, GPU time of a call: 8 sequences of 32768 keys (8 heads,
+// 8 queries each, d = 128) 163-165 us, 6.5-6.6 TB/s, 96-97% of a copy's rate; 48 of
+// 100 to 9000 keys (8 heads, 4 queries each) 78 us, 6.1 TB/s. The same kernel
+// that loads and does not compute takes 162 and 77: loads, not products, bound
+// long caches. 20 sequences of 333 to 4097 keys (16 heads, 4 new tokens,
+// d = 64) 27 us against 18 for the bytes, and one of 701 keys 7.4 us: about 4 us
+// of the chain length - page - keys and 2 us of merge.
+//
+// Tried and slower: tiles of 128 keys at d = 64 (27 -> 32 us); the merge done
+// by the last CTA of a unit, by a ticket (one sequence 7.7 -> 13 us); 32 keys
+// per warp, pairs of warps on alternate tiles (long 164 -> 178 us); a ring and
+// a share for every warp (long 165 -> 192 us: the TMA takes over 100 cycles per
+// box, and consumers that issue wait for it).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -139,7 +153,7 @@ __device__ __forceinline__ void named_bar(int id, int count) {
 // counts as zero.
 __device__ __forceinline__ int seq_keys(const PagedDecodeArgs& a, int s) {
   if (s >= a.B) return a.prefix_len;
-  const int n = __ldg(a.seq_lens + s);
+  const int n = a.seq_lens[s];
   if (n < 0 || n > kPagedMaxKeys || n > (long long)a.max_pages * a.pool.page_size) {
     report_status(a.status, kStatusBadSeqlens);
     return 0;
@@ -304,9 +318,9 @@ struct Walk {
   }
 };
 
-// Slot of the partial result of a unit's piece in CTA w. A piece that begins its unit and
-// does not end it: the CTA's second slot; one that continues a unit: the
-// first. Units of one piece that still need a merge (with a prefix's part)
+// Slot of the partial result of a unit's piece in CTA w. A piece that begins its
+// unit and does not end it: the CTA's second slot; one that continues a unit:
+// the first. Units of one piece that still need a merge (with a prefix's part)
 // have slots of their own behind those.
 __device__ __forceinline__ long long part_slot(const PagedDecodeArgs& a, int w, bool begins, bool ends, long long unit) {
   if (begins && ends) return 2ll * a.ctas + unit;
@@ -548,7 +562,7 @@ struct WarpRows8 {
     v_off = (uint32_t)(C::KV + (kw * 16 + (lane >> 4) * 8 + (lane & 7)) * 128);
     u_v = (lane >> 3) & 1;
     sw = lane & 7;
-    q_off = (uint32_t)((lane & 7) * D * 2) + 0u;
+    q_off = (uint32_t)((lane & 7) * D * 2);
   }
   __device__ __forceinline__ void begin(uint32_t q_smem) {
     const uint32_t u = (uint32_t)((threadIdx.x & 31) >> 3);
@@ -721,8 +735,9 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, BESIDE>::THREADS, Cfg<D, ROWS, BE
   // Launched while the kernel before it may still run: nothing of global
   // memory is read or written before that one's end (a prefix's kernel of its
   // own has waited for it), but the tables may come into L2: length, page and
-  // keys are three dependent look-ups. The merge kernel is set up in the same
-  // way meanwhile.
+  // keys are three dependent look-ups. (They are then read by plain loads: a
+  // read-only load might be moved above the wait.) The merge kernel is set up
+  // in the same way meanwhile.
   {
     const long long line = (long long)blockIdx.x * C::THREADS + threadIdx.x;
     const char* const lens = reinterpret_cast<const char*>(a.seq_lens);
@@ -756,7 +771,7 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, BESIDE>::THREADS, Cfg<D, ROWS, BE
     if (!any) return;
     const int nbox = C::BK >> a.box_shift;    // boxes of a chunk's 64 rows
     const bool mine = lane < nbox * 2 * C::CH;
-    const int box = lane & (nbox - 1), col = lane >> (6 - a.box_shift);  // this lane's box; keys' chunks, then values'
+    const int box = lane & (nbox - 1), col = lane >> (6 - a.box_shift);  // this lane's box; the keys' chunks, then the values'
     const bool is_v = col >= C::CH;
     const int chunk = is_v ? col - C::CH : col;
     const CUtensorMap* map = is_v ? &a.tmV : &a.tmK;
@@ -782,7 +797,7 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, BESIDE>::THREADS, Cfg<D, ROWS, BE
         const int* table = wk.sh.seq < a.B ? a.block_tables + (long long)wk.sh.seq * a.max_pages : a.prefix_pages;
         const int key = key0 + (box << a.box_shift), pi = a.page_div(key);
         t.row = key - pi * a.pool.page_size;
-        t.page = __ldg(table + pi);
+        t.page = table[pi];
       }
       return t;
     };
@@ -961,6 +976,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const __
   const unsigned item = blockIdx.x * (kMergeWarps / WPR) + warp / WPR;
   const unsigned group = item / (unsigned)R;
   const int r = (int)(item - group * (unsigned)R);
+  // a unit whose CTA gave up on a wait has no entry: what stands there is
+  // taken for some CTAs of the grid
+  auto in_grid = [&](int w) { return min(max(w, 0), a.ctas - 1); };
   int unit, own_first, own_n, pre_first = 0, pre_n = 0;
   long long pre_row = 0;  // a prefix's kernel of its own: row of the first part, parts 256 rows apart
   int b, head;
@@ -979,16 +997,16 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const __
     b = unit / Hkv;
     head = unit - b * Hkv;
     const int2 c = a.unit_ctas[unit];  // not written for a sequence without keys
-    own_first = c.x;
-    own_n = seq_keys(a, b) > 0 ? c.y - c.x + 1 : 0;
+    own_first = in_grid(c.x);
+    own_n = seq_keys(a, b) > 0 ? in_grid(c.y) - own_first + 1 : 0;
     if (a.pre_splits > 0) {
       const int rr = b * R + r, qblocks = (a.B * R + 255) / 256;
       pre_n = a.pre_splits;
       pre_row = ((long long)head * qblocks + rr / 256) * a.pre_splits * 256 + rr % 256;
     } else {
       const int2 cp = a.unit_ctas[a.B * Hkv + head];
-      pre_first = cp.x;
-      pre_n = cp.y - cp.x + 1;
+      pre_first = in_grid(cp.x);
+      pre_n = in_grid(cp.y) - pre_first + 1;
     }
   }
   float m = -INFINITY, l = 0.f, acc[E];

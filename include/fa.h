@@ -356,8 +356,9 @@ typedef struct {
  *               the same stride); both NULL and Hq = 0: keys and values only.
  *   cu_seqlens: DEVICE int32 [B+1]: sequence b's new tokens are the packed
  *               tokens cu_seqlens[b] .. cu_seqlens[b+1]-1. Packed tokens from
- *               cu_seqlens[B] on are padding: nothing of them is read or
- *               written. NULL: every sequence has total / B (exactly) tokens.
+ *               cu_seqlens[B] on are padding: what they hold does not
+ *               matter, and nothing is written for them (nor their rows of
+ *               Qout). NULL: every sequence has total / B (exactly) tokens.
  *   seq_lens  : the sequences' lengths AFTER this append (what the attention
  *               calls then take): new token i of n goes to key
  *               seq_lens[b] - n + i. seq_lens[b] = 0 marks a padding
@@ -472,7 +473,8 @@ fa_status fa_bwd_noalloc(const void* Q, const void* K, const void* V, const void
  * word on the current device. Returns FA_ERR_TIMEOUT if any kernel launched
  * since the last check abandoned a bounded wait (its outputs are then
  * undefined), FA_ERR_INVALID_ARG if a variable-length call met inconsistent
- * cu_seqlens (the sequences concerned were skipped), FA_ERR_CUDA if the
+ * cu_seqlens (the sequences concerned were skipped) or a call on a paged cache
+ * a length, a page or a position out of range (see there), FA_ERR_CUDA if the
  * stream reports an error, FA_OK otherwise.
  */
 fa_status fa_check_device_status(void* stream);
