@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) fwd_bf16_kernel(const _
     if constexpr (PREFIX) {
       // lane: one box of one 64-column chunk of a tile
       const int nbox = C::BN / a.box_rows;
-      const bool mine = lane < nbox * C::CH;
+      const bool mine = lane < nbox * C::CH && a.debug_skip_kv < 0;  // the test hook: nothing is loaded
       const int box = lane % nbox, chunk = lane / nbox;
       const uint32_t dst0 = sbase + chunk * C::CHUNK_BYTES + box * a.box_rows * 128;
       auto look_up = [&](int tile, int& page, int& row) {

@@ -260,13 +260,6 @@ using namespace fa;
 
 namespace {
 
-// Bounded-wait limit of the test hooks, clamped to [1 us, 2 s].
-unsigned long long clamp_limit(long long limit_ns) {
-  if (limit_ns < 1000) limit_ns = 1000;
-  if (limit_ns > 2000000000ll) limit_ns = 2000000000ll;
-  return (unsigned long long)limit_ns;
-}
-
 // The bf16 forward at d = 64 runs on the four-query-tile kernel (one CTA per
 // batch*head and 512-row block) when the problem is fixed-length (causal or
 // not) and its grid fills at least three quarters of the GPU's resident CTAs

@@ -292,6 +292,7 @@ struct PagedDecodeArgs {
   float scale_log2;                // scale * log2(e)
   int* status;
   unsigned long long wait_limit_ns;
+  int debug_skip_tile;             // test hook (fa_debug_decode_skip_load): -1, or the tile of a CTA that is not loaded
 };
 constexpr int kPagedMaxRows = 64;  // G * Nq
 constexpr int kPagedMaxKeys = 1 << 30;
@@ -325,6 +326,13 @@ inline int causal_heads_per_group(int BH, long long bytes_per_head, long long bu
   if (g >= BH) return BH;
   const long long groups = (BH + g - 1) / g;
   return (int)((BH + groups - 1) / groups);
+}
+
+// Bounded-wait limit of the test hooks, clamped to [1 us, 2 s].
+inline unsigned long long clamp_limit(long long limit_ns) {
+  if (limit_ns < 1000) limit_ns = 1000;
+  if (limit_ns > 2000000000ll) limit_ns = 2000000000ll;
+  return (unsigned long long)limit_ns;
 }
 
 // Bounded-wait probe (fa_debug_timeout_probe).

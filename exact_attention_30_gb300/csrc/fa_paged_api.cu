@@ -81,7 +81,8 @@ fa_status decode_impl(const void* Q, const long long* q_strides, const fa_paged_
                       const int* prefix_pages, int prefix_len, const int* block_tables, int max_pages,
                       const int* seq_lens, void* O, const long long* o_strides, float* LSE,
                       void* workspace, size_t workspace_bytes, int B, int Hq, int Nq, float scale,
-                      fa_dtype dt, void* stream) {
+                      fa_dtype dt, void* stream, int debug_skip = -1,
+                      unsigned long long limit_ns = kDefaultWaitLimitNs) {
   PagedDecodeArgs a;
   std::memset(&a, 0, sizeof(a));
   fa_status s = check_pool(cache, dt, &a.pool);
@@ -134,7 +135,8 @@ fa_status decode_impl(const void* Q, const long long* q_strides, const fa_paged_
   a.Nq = Nq;
   a.max_pages = max_pages;
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.wait_limit_ns = kDefaultWaitLimitNs;
+  a.wait_limit_ns = limit_ns;
+  a.debug_skip_tile = debug_skip;
   if (L.pre_splits > 0) {
     PrefixArgs p;
     std::memset(static_cast<void*>(&p), 0, sizeof(p));
@@ -163,7 +165,7 @@ fa_status decode_impl(const void* Q, const long long* q_strides, const fa_paged_
     p.wait_limit_ns = a.wait_limit_ns;
     p.n_tail = (int)units;
     p.splits = plan.splits;
-    p.debug_skip_kv = -1;
+    p.debug_skip_kv = debug_skip;
     p.Qrows = Q;
     p.q_b = a.q_b;
     p.q_h = a.q_h;
@@ -265,6 +267,17 @@ fa_status fa_decode_shared(const void* Q, const long long* q_strides, const fa_p
                            fa_dtype dt, void* stream) {
   return decode_impl(Q, q_strides, cache, prefix_pages, prefix_len, block_tables, max_pages, seq_lens, O,
                      o_strides, LSE, workspace, workspace_bytes, B, Hq, Nq, scale, dt, stream);
+}
+
+fa_status fa_debug_decode_skip_load(const void* Q, const long long* q_strides, const fa_paged_kv* cache,
+                                    const int* prefix_pages, int prefix_len, const int* block_tables,
+                                    int max_pages, const int* seq_lens, void* O, const long long* o_strides,
+                                    float* LSE, void* workspace, size_t workspace_bytes, int B, int Hq, int Nq,
+                                    float scale, int skip_tile, long long limit_ns, void* stream) {
+  if (skip_tile < 1) return FA_ERR_INVALID_ARG;
+  return decode_impl(Q, q_strides, cache, prefix_pages, prefix_len, block_tables, max_pages, seq_lens, O,
+                     o_strides, LSE, workspace, workspace_bytes, B, Hq, Nq, scale, FA_BF16, stream, skip_tile,
+                     clamp_limit(limit_ns));
 }
 
 }  // extern "C"

@@ -822,9 +822,10 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, BESIDE>::THREADS, Cfg<D, ROWS, BE
       const Tile next = more ? look_up(tile) : t;
       const int s = it % C::STAGES;
       if (!mbar_wait_warp(EMPTY(s), ((it / C::STAGES) & 1) ^ 1, a.status, a.wait_limit_ns)) break;
-      if (lane == 0) mbar_arrive_expect_tx(FULL(s), (uint32_t)((t.boxes * 128 * 2 * C::CH) << a.box_shift));
+      const bool load = it != a.debug_skip_tile;
+      if (load && lane == 0) mbar_arrive_expect_tx(FULL(s), (uint32_t)((t.boxes * 128 * 2 * C::CH) << a.box_shift));
       __syncwarp();
-      if (mine && box < t.boxes) {
+      if (load && mine && box < t.boxes) {
         if (t.page < 0 || t.page >= a.pool.num_pages) {
           report_status(a.status, kStatusBadSeqlens);
           t.page = a.pool.num_pages;  // outside the tensor: reads as zeros
@@ -841,7 +842,9 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, BESIDE>::THREADS, Cfg<D, ROWS, BE
 
   // -------------------------------------------------------------- consumers
   // After a wait ran out a warp goes on without waiting or computing, so that
-  // it still reaches every barrier; the status word tells.
+  // it still reaches every barrier, and frees no stage any more: the producer
+  // then stops by a wait of its own, before a stage's barrier is used again
+  // whose copies are still in flight. The status word tells.
   const int cw = warp - 1, mt = cw >> 2, kw = cw & 3;
   const int ct = kw * 32 + lane;  // thread of the group's 128
   const float c2 = a.scale_log2;
@@ -890,7 +893,7 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, BESIDE>::THREADS, Cfg<D, ROWS, BE
       const int k0 = (first + j) * C::BK + kw * 16;  // this warp's keys
       if (ok && active && k0 < len) st.tile(sbase + s * C::STAGE, smem + s * C::STAGE, k0, len, seen, info, rows, c2);
       __syncwarp();
-      if (lane == 0 && !(C::MERGE_IN_STAGE && j + 1 == n)) mbar_arrive(EMPTY(s));
+      if (ok && lane == 0 && !(C::MERGE_IN_STAGE && j + 1 == n)) mbar_arrive(EMPTY(s));
     }
 
     if (!active) continue;
@@ -949,7 +952,7 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, BESIDE>::THREADS, Cfg<D, ROWS, BE
     if (C::MERGE_IN_STAGE) {
       fence_proxy_async_smem();  // the stage's next writer is the TMA
       __syncwarp();
-      if (lane == 0) mbar_arrive(EMPTY(last_stage));
+      if (ok && lane == 0) mbar_arrive(EMPTY(last_stage));
     }
   }
   // a prefix's kernel ends before this one does, so the merge sees both; one
@@ -976,9 +979,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const __
   const unsigned item = blockIdx.x * (kMergeWarps / WPR) + warp / WPR;
   const unsigned group = item / (unsigned)R;
   const int r = (int)(item - group * (unsigned)R);
-  // a unit whose CTA gave up on a wait has no entry: what stands there is
-  // taken for some CTAs of the grid
-  auto in_grid = [&](int w) { return min(max(w, 0), a.ctas - 1); };
+  // a unit whose CTA gave up on a wait may have no entry, and then no result
+  auto in_grid = [&](int2 c) { return (unsigned)c.x <= (unsigned)c.y && (unsigned)c.y < (unsigned)a.ctas; };
   int unit, own_first, own_n, pre_first = 0, pre_n = 0;
   long long pre_row = 0;  // a prefix's kernel of its own: row of the first part, parts 256 rows apart
   int b, head;
@@ -997,17 +999,19 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const __
     b = unit / Hkv;
     head = unit - b * Hkv;
     const int2 c = a.unit_ctas[unit];  // not written for a sequence without keys
-    own_first = in_grid(c.x);
-    own_n = seq_keys(a, b) > 0 ? in_grid(c.y) - own_first + 1 : 0;
+    own_first = c.x;
+    own_n = seq_keys(a, b) > 0 ? c.y - own_first + 1 : 0;
     if (a.pre_splits > 0) {
       const int rr = b * R + r, qblocks = (a.B * R + 255) / 256;
       pre_n = a.pre_splits;
       pre_row = ((long long)head * qblocks + rr / 256) * a.pre_splits * 256 + rr % 256;
     } else {
       const int2 cp = a.unit_ctas[a.B * Hkv + head];
-      pre_first = in_grid(cp.x);
-      pre_n = in_grid(cp.y) - pre_first + 1;
+      pre_first = cp.x;
+      pre_n = cp.y - pre_first + 1;
+      if (!in_grid(cp)) return;
     }
+    if (own_n != 0 && !in_grid(c)) return;
   }
   float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll

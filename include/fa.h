@@ -518,6 +518,18 @@ fa_status fa_debug_bwd_skip_load(const void* Q, const void* K, const void* V, co
                                  int d, float scale, int skip_tile, long long limit_ns,
                                  void* stream);
 /*
+ * The same for the decode over a paged cache: arguments of fa_decode_shared
+ * (dtype bf16). No CTA loads the tile `skip_tile` >= 1 of its walk (one with
+ * fewer tiles works as usual), and a kernel of the prefix's own loads nothing.
+ */
+fa_status fa_debug_decode_skip_load(const void* Q, const long long* q_strides,
+                                    const fa_paged_kv* cache, const int* prefix_pages,
+                                    int prefix_len, const int* block_tables, int max_pages,
+                                    const int* seq_lens, void* O, const long long* o_strides,
+                                    float* LSE, void* workspace, size_t workspace_bytes, int B,
+                                    int Hq, int Nq, float scale, int skip_tile, long long limit_ns,
+                                    void* stream);
+/*
  * fa_debug_bwd_skip_load with flags: FA_CAUSAL runs the causal backward,
  * whose persistent CTAs take their units from the device counter and pass
  * them on through the shared-memory item ring (the ring's bounded waits then
