@@ -52,7 +52,7 @@
 // (one row per thread) into the Q tiles; the keys are the prefix's pages, one
 // TMA box per page and lane of the producer warp. Every unit is split into key
 // ranges as above, also into one, and leaves partial results, which
-// decode_merge_kernel combines with those of the sequences' own keys. Measured:
+// merge_prefix_kernel combines with those of the sequences' own keys. Measured:
 // 11 us to begin and end (launch, pages, queries, first tiles, partial rows)
 // and 1.76 us per 256 rows x 128 keys (1.05 with one query tile) at d = 128,
 // 9.5 TFLOP/s per SM, the forward's own rate; 512 rows x 32768 keys x 8 heads

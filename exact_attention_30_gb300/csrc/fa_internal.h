@@ -277,10 +277,11 @@ struct PagedDecodeArgs {
   // schedule and scratch (paged_layout)
   int ctas;                        // grid; shares of the keys
   int n_seq;                       // B, or B + 1: the prefix is the last sequence
-  int slot_rows;                   // rows of a partial result's slot
+  int slot_rows;                   // rows of a partial result's slot, and of a unit at most
+  int group_shift;                 // 1 << group_shift units of slot_rows rows per sequence and K/V head
   float* Opart;                    // fp32 [slots][slot_rows][d], normalised
   float* Lpart;                    // fp32 [slots][slot_rows], base-2 log-sum-exp
-  int2* unit_ctas;                 // [n_seq * Hkv] with a prefix: first and last CTA of a unit
+  int2* unit_ctas;                 // [units] with a prefix: first and last CTA of a unit
   int2* begun;                     // [ctas] no prefix: the unit that a CTA begins and does not end, or -1; its last CTA
   // A prefix of many rows runs as a kernel of its own (launch_prefix_bf16),
   // whose pre_splits partial results per row lie here; 0: it is part of n_seq.
@@ -299,7 +300,7 @@ constexpr int kPagedMaxKeys = 1 << 30;
 // Grid and scratch of a decode on the current device (ctas = 0 on failure);
 // rows = G * Nq. Offsets in bytes; the partial outputs come first.
 struct PagedLayout {
-  int ctas, n_seq, slot_rows, pre_splits;
+  int ctas, n_seq, slot_rows, group_shift, pre_splits;
   size_t lpart, unit_ctas, begun, pre_opart, pre_lpart, total;
 };
 // How a prefix's kernel and the own keys' kernel share the GPU: key ranges per

@@ -119,6 +119,7 @@ fa_status decode_impl(const void* Q, const long long* q_strides, const fa_paged_
   a.ctas_div = fast_div((unsigned)L.ctas);
   a.n_seq = L.n_seq;
   a.slot_rows = L.slot_rows;
+  a.group_shift = L.group_shift;
   a.Opart = reinterpret_cast<float*>(ws);
   a.Lpart = reinterpret_cast<float*>(ws + L.lpart);
   a.unit_ctas = reinterpret_cast<int2*>(ws + L.unit_ctas);

@@ -15,7 +15,7 @@
 // The lengths live on the device, so each CTA finds its share itself (a warp's
 // scan over the lengths). A share may end inside a unit; such a unit's pieces
 // leave normalised fp32 partial results and base-2 log-sum-exps in the
-// workspace, at most two per CTA, and decode_merge_kernel combines them in a
+// workspace, at most two per CTA, and a second kernel combines them in a
 // fixed order (results do not depend on timing). A unit that lies in one share
 // is written out directly.
 //
@@ -68,7 +68,7 @@ constexpr int kUnitSteps = 2;
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kLn2 = 0.69314718055994531f;
 
-// ROWS: query rows of a unit, 8, 16, 32 or 64 (fewer are padded). BESIDE: on
+// ROWS: query rows of a unit, 8, 16 or 32 (fewer are padded). BESIDE: on
 // the few SMs that a prefix's kernel leaves, where the latency of units bounds
 // the own keys rather than memory: three CTAs per SM with two stages each
 // (8 rows, whose registers allow it; 128 samples 57.5 -> 54 us). Elsewhere two
@@ -78,6 +78,7 @@ template <int D_, int ROWS_, bool BESIDE>
 struct Cfg {
   static constexpr int D = D_, ROWS = ROWS_;
   static constexpr int MT = ROWS < 16 ? 1 : ROWS / 16;  // groups of rows, four consumer warps each
+  static constexpr int OWN_ROWS = ROWS == 32 ? kPagedMaxRows : 16;  // query rows of a K/V head
   static constexpr int BK = 64;              // keys per tile
   static constexpr int CH = D / 64;          // 128-byte column chunks of a row
   static constexpr int CHUNK = BK * 128;     // 64 rows x 128 bytes, swizzled
@@ -99,14 +100,14 @@ struct Cfg {
   // Queries as fragments in registers, or read from shared memory per tile
   // (16 rows: 1% faster than in registers, which then spill; four groups
   // leave 96 registers). FB: K or V fragments loaded at a time.
-  static constexpr bool Q_IN_SMEM = ROWS == 16 || MT == 4;
-  static constexpr int FB = MT == 4 ? 1 : 4;
+  static constexpr bool Q_IN_SMEM = ROWS == 16;
+  static constexpr int FB = 4;
   static constexpr int QBUF = 16 * MT * D * 2;  // a unit's queries; two, one being filled for the next unit
   static constexpr int OFF_MERGE = STAGES * STAGE;
   static constexpr int OFF_Q = OFF_MERGE + (MERGE_IN_STAGE ? 0 : MT * MERGE);
   static constexpr int OFF_ML = OFF_Q + 2 * QBUF;               // fp32 m, l [MT][4][16]
-  static constexpr int OFF_ROWS = OFF_ML + MT * 4 * 16 * 8;     // RowInfo [2][16 MT]: own keys, prefix
-  static constexpr int OFF_SHARE = OFF_ROWS + 2 * 16 * MT * 24;  // the CTA's Share
+  static constexpr int OFF_ROWS = OFF_ML + MT * 4 * 16 * 8;     // RowInfo [OWN_ROWS], prefix's [16 MT]
+  static constexpr int OFF_SHARE = OFF_ROWS + (OWN_ROWS + 16 * MT) * 24;  // the CTA's Share
   static constexpr int OFF_BAR = OFF_SHARE + 48;
   static constexpr int SMEM = OFF_BAR + 2 * STAGES * 8;
   static constexpr int SMEM_ALLOC = SMEM + 1024;  // base rounded up to 1024 (swizzle atom)
@@ -215,6 +216,17 @@ struct Cut {
   }
 };
 
+// Units of a sequence. More than 32 rows of a K/V head are several groups, which
+// follow one another, so that the second one finds the head's keys in L2.
+template <class C>
+__device__ __forceinline__ int group_shift(const PagedDecodeArgs& a) {
+  return C::ROWS == 32 ? a.group_shift : 0;
+}
+template <class C>
+__device__ __forceinline__ int unit_heads(const PagedDecodeArgs& a) {
+  return a.pool.kv_heads << group_shift<C>(a);
+}
+
 // A unit's steps: one per tile and kUnitSteps for what it costs to begin and
 // end one (queries, merge, output); its tiles are its last steps.
 __device__ __forceinline__ int unit_steps(int keys, int bk) { return keys > 0 ? (keys + bk - 1) / bk + kUnitSteps : 0; }
@@ -225,7 +237,8 @@ struct Share {
   long long at;    // first step among all
   long long T;     // all steps
   int seq;         // sequence of the first step
-  int head, step;  // K/V head and step within the unit
+  int head, step;  // unit of the sequence, and step within it
+  int empty;       // whether some sequence has no keys
 };
 
 // Found by one warp: each lane adds up the steps of a run of sequences.
@@ -234,27 +247,32 @@ __device__ __forceinline__ Share find_share(const PagedDecodeArgs& a, int lane) 
   const int chunk = (a.n_seq + 31) >> 5;
   const int s0 = min(lane * chunk, a.n_seq), s1 = min(s0 + chunk, a.n_seq);
   long long sum = 0;
-  for (int s = s0; s < s1; ++s) sum += unit_steps(seq_keys(a, s), C::BK);
+  bool empty = false;
+  for (int s = s0; s < s1; ++s) {
+    const int n = unit_steps(seq_keys(a, s), C::BK);
+    sum += n;
+    empty |= n == 0;
+  }
   long long incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long v = __shfl_up_sync(kFull, incl, o);
     if (lane >= o) incl += v;
   }
-  const int Hkv = a.pool.kv_heads;
+  const int heads = unit_heads<C>(a);
   Share sh;
-  sh.T = __shfl_sync(kFull, incl, 31) * Hkv;
+  sh.T = __shfl_sync(kFull, incl, 31) * heads;
   const Cut cut(a, sh.T);
   sh.at = cut.begin(blockIdx.x);
   sh.left = cut.begin(blockIdx.x + 1) - sh.at;
-  const long long hi = incl * Hkv, lo = hi - sum * Hkv;
+  const long long hi = incl * heads, lo = hi - sum * heads;
   const bool here = lo <= sh.at && sh.at < hi;  // the first step lies in this lane's sequences
   int seq = 0, head = 0, step = 0;
   if (here) {
     long long at = sh.at - lo;
     for (int s = s0; s < s1; ++s) {
       const int n = unit_steps(seq_keys(a, s), C::BK);
-      const long long all = (long long)n * Hkv;
+      const long long all = (long long)n * heads;
       if (at < all) {
         head = all < (1ll << 31) ? (int)at / n : (int)(at / n);
         step = (int)(at - (long long)head * n);
@@ -269,26 +287,28 @@ __device__ __forceinline__ Share find_share(const PagedDecodeArgs& a, int lane) 
   sh.seq = __shfl_sync(kFull, seq, src);
   sh.head = __shfl_sync(kFull, head, src);
   sh.step = __shfl_sync(kFull, step, src);
+  sh.empty = __any_sync(kFull, empty);
   return sh;
 }
 
 // Walks a share unit by unit; the producer and the consumers walk alike. A
 // piece may hold no tile (a share that ends before a unit's first one).
+template <class C>
 struct Walk {
   Share sh;
   int len, tiles, next_len;
 
-  __device__ __forceinline__ void load(const PagedDecodeArgs& a, int bk) {
-    tiles = (len + bk - 1) / bk;
+  __device__ __forceinline__ void load(const PagedDecodeArgs& a) {
+    tiles = (len + C::BK - 1) / C::BK;
     next_len = sh.seq + 1 < a.n_seq ? seq_keys(a, sh.seq + 1) : 0;  // on its way while this one is worked on
   }
   // false: nothing to do
-  __device__ __forceinline__ bool begin(const PagedDecodeArgs& a, const Share& s, int bk) {
+  __device__ __forceinline__ bool begin(const PagedDecodeArgs& a, const Share& s) {
     sh = s;
     if (sh.left <= 0) return false;
     len = seq_keys(a, s.seq);
-    load(a, bk);
-    return tile_count() > 0 || advance(a, bk);
+    load(a);
+    return tile_count() > 0 || advance(a);
   }
   __device__ __forceinline__ int first_tile() const { return max(0, sh.step - kUnitSteps); }
   __device__ __forceinline__ int tile_count() const {
@@ -298,19 +318,19 @@ struct Walk {
   // first step of this unit among all
   __device__ __forceinline__ long long unit_at() const { return sh.at - sh.step; }
   // to the next piece with a tile; false at the share's end
-  __device__ __forceinline__ bool advance(const PagedDecodeArgs& a, int bk) {
+  __device__ __forceinline__ bool advance(const PagedDecodeArgs& a) {
     do {
       const int n = tiles + kUnitSteps - sh.step;
       sh.left -= n;
       sh.at += n;
       sh.step = 0;
       if (sh.left <= 0) return false;
-      if (++sh.head >= a.pool.kv_heads) {
+      if (++sh.head >= unit_heads<C>(a)) {
         sh.head = 0;
         do {
           if (++sh.seq >= a.n_seq) return false;
           len = next_len;
-          load(a, bk);
+          load(a);
         } while (len == 0);
       }
     } while (tile_count() <= 0);
@@ -327,15 +347,21 @@ __device__ __forceinline__ long long part_slot(const PagedDecodeArgs& a, int w, 
   return 2ll * w + (begins ? 1 : 0);
 }
 
-// All rows of sequence s: no key, so O = 0 and LSE = -inf.
+// Rows of sequences without keys: O = 0, LSE = -inf. Warp w of n writes those
+// of every n-th (sequence, K/V head).
 template <int D>
-__device__ __noinline__ void empty_rows(const PagedDecodeArgs& a, int s, int thread, int threads) {
-  const int Hq = a.pool.kv_heads * a.G, rows = Hq * a.Nq;
-  for (long long e = thread; e < (long long)rows * (D / 8); e += threads) {
-    const int row = (int)(e / (D / 8)), c = (int)(e - (long long)row * (D / 8)) * 8;
-    const int hq = row / a.Nq, i = row - hq * a.Nq;
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.O) + s * a.o_b + hq * a.o_h + i * a.o_r + c) = make_uint4(0u, 0u, 0u, 0u);
-    if (c == 0) a.LSE[(long long)s * rows + row] = -INFINITY;
+__device__ __noinline__ void empty_rows(const PagedDecodeArgs& a, int w, int n) {
+  const int Hkv = a.pool.kv_heads, R = a.G * a.Nq, lane = threadIdx.x & 31;
+  constexpr int U = D / 8;  // lanes of a row
+  for (int unit = w; unit < a.B * Hkv; unit += n) {
+    const int b = unit / Hkv, head = unit - b * Hkv;
+    if (seq_keys(a, b) != 0) continue;
+    for (int r = lane / U; r < R; r += 32 / U) {
+      const int g = a.nq_div(r), i = r - g * a.Nq;
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.O) + b * a.o_b + (long long)(head * a.G + g) * a.o_h + i * a.o_r +
+                                (lane & (U - 1)) * 8) = make_uint4(0u, 0u, 0u, 0u);
+      if ((lane & (U - 1)) == 0) a.LSE[(long long)unit * R + r] = -INFINITY;
+    }
   }
 }
 
@@ -747,23 +773,23 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, BESIDE>::THREADS, Cfg<D, ROWS, BE
   }
   if (a.pre_splits == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int Hkv = a.pool.kv_heads, R = a.G * a.Nq;
+  const int R = a.G * a.Nq, shift = group_shift<C>(a);
   RowInfo* row_info = reinterpret_cast<RowInfo*>(smem + C::OFF_ROWS);
   Share* shared_share = reinterpret_cast<Share*>(smem + C::OFF_SHARE);
   if (warp == 0) {
     const Share found = find_share<C>(a, lane);
     if (lane == 0) *shared_share = found;
   } else {
-    for (int e = threadIdx.x - 32; e < (a.prefix_len > 0 ? 2 : 1) * 16 * MT; e += C::THREADS - 32) {
-      const int p = e & (16 * MT - 1);
-      const int b = e < 16 * MT ? 0 : a.rows_div(p), r = p - b * R, g = a.nq_div(r), i = r - g * a.Nq;
-      row_info[e] = RowInfo{b * a.q_b + g * a.q_h + i * a.q_r, b * a.o_b + g * a.o_h + i * a.o_r,
-                            e < 16 * MT ? a.Nq - 1 - i : 0};
+    for (int e = threadIdx.x - 32; e < C::OWN_ROWS + (a.prefix_len > 0 ? 16 * MT : 0); e += C::THREADS - 32) {
+      const bool own = e < C::OWN_ROWS;
+      const int p = own ? e : e - C::OWN_ROWS;
+      const int b = own ? 0 : a.rows_div(p), r = p - b * R, g = a.nq_div(r), i = r - g * a.Nq;
+      row_info[e] = RowInfo{b * a.q_b + g * a.q_h + i * a.q_r, b * a.o_b + g * a.o_h + i * a.o_r, own ? a.Nq - 1 - i : 0};
     }
   }
   __syncthreads();
-  Walk wk;
-  const bool any = wk.begin(a, *shared_share, C::BK);
+  Walk<C> wk;
+  const bool any = wk.begin(a, *shared_share);
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -792,7 +818,7 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, BESIDE>::THREADS, Cfg<D, ROWS, BE
       t.boxes = left >= C::BK ? nbox : (left + (1 << a.box_shift) - 1) >> a.box_shift;
       t.page = -1;
       t.row = 0;
-      t.head = wk.sh.head;
+      t.head = wk.sh.head >> shift;
       if (mine && box < t.boxes) {
         const int* table = wk.sh.seq < a.B ? a.block_tables + (long long)wk.sh.seq * a.max_pages : a.prefix_pages;
         const int key = key0 + (box << a.box_shift), pi = a.page_div(key);
@@ -809,13 +835,13 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, BESIDE>::THREADS, Cfg<D, ROWS, BE
         const long long end = wk.unit_at() + kUnitSteps + wk.tiles;
         const bool whole = end <= wk.sh.at + wk.sh.left;
         if (a.prefix_len > 0 || !whole) {
-          const int unit = wk.sh.seq * Hkv + wk.sh.head, last = whole ? (int)blockIdx.x : cut.owner(blockIdx.x, end - 1);
+          const int unit = wk.sh.seq * unit_heads<C>(a) + wk.sh.head, last = whole ? (int)blockIdx.x : cut.owner(blockIdx.x, end - 1);
           if (a.prefix_len > 0) a.unit_ctas[unit] = make_int2(blockIdx.x, last);
           else a.begun[blockIdx.x] = make_int2(unit, last);
         }
       }
       if (++tile == tile_end) {
-        more = wk.advance(a, C::BK);
+        more = wk.advance(a);
         tile = wk.first_tile();
         tile_end = tile + wk.tile_count();
       }
@@ -854,38 +880,37 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, BESIDE>::THREADS, Cfg<D, ROWS, BE
   using Warp = std::conditional_t<ROWS == 8, WarpRows8<C>, WarpRows16<C>>;
   Warp st;
   st.init(lane, kw, mt);
-  auto fetch_q = [&](int seq, int head, int buf) {
+  auto fetch_q = [&](int seq, int unit_head, int buf) {
     const bool pre = seq >= a.B;
-    const int rows = pre ? a.B * R : R;
+    const int head = unit_head >> shift, r0 = (unit_head - (head << shift)) * ROWS;
+    const int rows = pre ? a.B * R : R - r0;
+    const RowInfo* info = row_info + (pre ? C::OWN_ROWS : r0) + mt * 16;
     const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(a.Q) + (pre ? 0 : seq * a.q_b) + (long long)head * a.G * a.q_h;
 #pragma unroll
     for (int e = ct; e < Warp::ROWS * (D / 8); e += 128) {
       const int r = e / (D / 8), u = e - r * (D / 8);
       const bool valid = mt * 16 + r < rows;
-      const __nv_bfloat16* src = base + (valid ? row_info[(pre ? 16 * MT : 0) + mt * 16 + r].q + u * 8 : 0);
+      const __nv_bfloat16* src = base + (valid ? info[r].q + u * 8 : 0);
       copy16(q_buf + buf * C::QBUF + r * (D * 2) + ((u ^ (r & 7)) << 4), src, valid);
     }
   };
   if (any) fetch_q(wk.sh.seq, wk.sh.head, 0);
-  if (a.prefix_len == 0) {
-    // rows of sequences without keys
-    for (int s = blockIdx.x; s < a.B; s += gridDim.x)
-      if (seq_keys(a, s) == 0) empty_rows<D>(a, s, threadIdx.x - 32, C::THREADS - 32);
-  }
+  if (a.prefix_len == 0 && shared_share->empty) empty_rows<D>(a, blockIdx.x * C::CONSUMERS + cw, gridDim.x * C::CONSUMERS);
   bool ok = true;
   int it = 0, qb = 0;
   for (bool more = any; more; qb ^= 1) {
-    const int n = wk.tile_count(), first = wk.first_tile(), seq = wk.sh.seq, head = wk.sh.head, len = wk.len;
+    const int n = wk.tile_count(), first = wk.first_tile(), seq = wk.sh.seq, unit_head = wk.sh.head, len = wk.len;
+    const int head = unit_head >> shift, r0 = (unit_head - (head << shift)) * ROWS;
     const bool begins = first == 0, ends = first + n == wk.tiles;
     const bool pre = seq >= a.B;
-    const int rows = pre ? a.B * R : R;
-    const RowInfo* info = row_info + (pre ? 16 * MT : 0);
+    const int rows = pre ? a.B * R : min(ROWS, R - r0);
+    const RowInfo* info = row_info + (pre ? C::OWN_ROWS : r0);
     const int seen = pre ? len : max(0, len - a.Nq + 1);  // keys that every row sees
     const bool active = mt * 16 < rows;                   // else these warps only keep step
     copies_done();
     named_bar(1 + mt, 128);  // this unit's queries are there; the other buffer has been read
     st.begin(q_buf + qb * C::QBUF);
-    more = wk.advance(a, C::BK);
+    more = wk.advance(a);
     if (more) fetch_q(wk.sh.seq, wk.sh.head, qb ^ 1);
     for (int j = 0; j < n; ++j, ++it) {
       const int s = it % C::STAGES;
@@ -902,7 +927,7 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, BESIDE>::THREADS, Cfg<D, ROWS, BE
     st.put_sums(ml);
     const int last_stage = (it - 1) % C::STAGES;
     uint8_t* om = smem + (C::MERGE_IN_STAGE ? last_stage * C::STAGE : C::OFF_MERGE + mt * C::MERGE);
-    const long long unit = (long long)seq * Hkv + head;
+    const long long unit = (long long)seq * unit_heads<C>(a) + unit_head;
     const bool direct = begins && ends && a.prefix_len == 0;
     const long long part_row = part_slot(a, blockIdx.x, begins, ends, unit) * a.slot_rows;
     const long long o_unit = (pre ? 0 : seq * a.o_b) + (long long)head * a.G * a.o_h;
@@ -942,7 +967,7 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, BESIDE>::THREADS, Cfg<D, ROWS, BE
         if (direct) {
           __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.O) + o_unit + info[rr].o + d0 + c;
           *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-          if (d0 + c == 0) a.LSE[unit * R + rr] = lse * kLn2;
+          if (d0 + c == 0) a.LSE[(unit >> shift) * R + r0 + rr] = lse * kLn2;
         } else {
           *reinterpret_cast<float4*>(a.Opart + (part_row + rr) * D + d0 + c) = y;
           if (d0 + c == 0) a.Lpart[part_row + rr] = lse;
@@ -961,113 +986,82 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, BESIDE>::THREADS, Cfg<D, ROWS, BE
 }
 
 // Rows of units that were not written out directly: partial results of the
-// own keys (and of the prefix) merged by maximum and sum, in order of the
-// CTAs. WPR warps share a row, each taking every WPR-th partial result, and
-// meet in shared memory: without a prefix few rows have parts, but a long
-// sequence has one from each of many CTAs (WPR = 8); with one every row has
-// parts, as many as the prefix has key ranges (WPR = 1 up to 16, else 8).
+// own keys (and of the prefix) merged by maximum and sum, in order of the CTAs.
 constexpr int kMergeWarps = 8;
-template <int D, int WPR, bool PREFIX>
-__global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const __grid_constant__ PagedDecodeArgs a) {
-  constexpr int E = D / 32;
-  constexpr int AHEAD = 4;  // partial results in flight per warp
-  __shared__ float sm[kMergeWarps], sl[kMergeWarps], so[kMergeWarps][D];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!PREFIX) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % WPR;
-  const int Hkv = a.pool.kv_heads, R = a.G * a.Nq;
-  const unsigned item = blockIdx.x * (kMergeWarps / WPR) + warp / WPR;
-  const unsigned group = item / (unsigned)R;
-  const int r = (int)(item - group * (unsigned)R);
-  // a unit whose CTA gave up on a wait may have no entry, and then no result
-  auto in_grid = [&](int2 c) { return (unsigned)c.x <= (unsigned)c.y && (unsigned)c.y < (unsigned)a.ctas; };
-  int unit, own_first, own_n, pre_first = 0, pre_n = 0;
-  long long pre_row = 0;  // a prefix's kernel of its own: row of the first part, parts 256 rows apart
-  int b, head;
-  if (!PREFIX) {
-    // without a prefix only the units that a share's end cuts have parts
-    const int2 c = a.begun[group];
-    if (c.x < 0) return;  // the whole block
-    unit = c.x;
-    own_first = (int)group;
-    own_n = c.y - own_first + 1;
-    b = unit / Hkv;
-    head = unit - b * Hkv;
-  } else {
-    if (item >= (unsigned)(a.B * Hkv) * (unsigned)R) return;  // the whole block, if its warps share a row
-    unit = (int)group;
-    b = unit / Hkv;
-    head = unit - b * Hkv;
-    const int2 c = a.unit_ctas[unit];  // not written for a sequence without keys
-    own_first = c.x;
-    own_n = seq_keys(a, b) > 0 ? c.y - own_first + 1 : 0;
-    if (a.pre_splits > 0) {
-      const int rr = b * R + r, qblocks = (a.B * R + 255) / 256;
-      pre_n = a.pre_splits;
-      pre_row = ((long long)head * qblocks + rr / 256) * a.pre_splits * 256 + rr % 256;
-    } else {
-      const int2 cp = a.unit_ctas[a.B * Hkv + head];
-      pre_first = cp.x;
-      pre_n = cp.y - pre_first + 1;
-      if (!in_grid(cp)) return;
-    }
-    if (own_n != 0 && !in_grid(c)) return;
-  }
+
+// The parts of a row: those of the CTAs that share its unit, then the prefix's.
+struct Parts {
+  int unit, slot_row;     // unit, and the row in its slots
+  int own_first, own_n;   // CTAs
+  int pre_unit, pre_slot_row, pre_first, pre_n;  // the same of a prefix that is part of the grid
+  long long pre_row;      // a prefix's kernel of its own: row of the first part, parts 256 rows apart
+};
+
+// A warp's share of a row: every step-th part from `part` on; a lane has D / 32 columns.
+template <int D, bool PREFIX>
+struct RowSum {
+  static constexpr int E = D / 32;
+  static constexpr int AHEAD = 4;  // partial results in flight per warp
   float m = -INFINITY, l = 0.f, acc[E];
+
+  __device__ __forceinline__ void add(const PagedDecodeArgs& a, const Parts& P, int part, int step, int lane) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  const int n = own_n + pre_n;
-  for (int p0 = part; p0 < n; p0 += AHEAD * WPR) {
-    float L[AHEAD], x[AHEAD][E];
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    const int n = P.own_n + P.pre_n;
+    for (int p0 = part; p0 < n; p0 += AHEAD * step) {
+      float L[AHEAD], x[AHEAD][E];
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) {
-      const int p = p0 + k * WPR;
-      L[k] = -INFINITY;
+      for (int k = 0; k < AHEAD; ++k) {
+        const int p = p0 + k * step;
+        L[k] = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[k][e] = 0.f;
-      if (p >= n) continue;
-      const bool own = p < own_n;
-      const int i = own ? p : p - own_n;
-      const float* O = a.Opart;
-      const float* Ls = a.Lpart;
-      long long row;
-      if (own || a.pre_splits == 0) {
-        const int u = own ? unit : a.B * Hkv + head;
-        const long long slot = part_slot(a, (own ? own_first : pre_first) + i, i == 0, i + 1 == (own ? own_n : pre_n), u);
-        row = slot * a.slot_rows + (own ? r : b * R + r);
-      } else {
-        O = a.pre_Opart;
-        Ls = a.pre_Lpart;
-        row = pre_row + 256ll * i;
+        for (int e = 0; e < E; ++e) x[k][e] = 0.f;
+        if (p >= n) continue;
+        const bool own = !PREFIX || p < P.own_n;
+        const int i = own ? p : p - P.own_n;
+        const float* O = a.Opart;
+        const float* Ls = a.Lpart;
+        long long row;
+        if (own) {
+          row = part_slot(a, P.own_first + i, i == 0, i + 1 == P.own_n, P.unit) * a.slot_rows + P.slot_row;
+        } else if (a.pre_splits == 0) {
+          row = part_slot(a, P.pre_first + i, i == 0, i + 1 == P.pre_n, P.pre_unit) * a.slot_rows + P.pre_slot_row;
+        } else {
+          O = a.pre_Opart;
+          Ls = a.pre_Lpart;
+          row = P.pre_row + 256ll * i;
+        }
+        L[k] = Ls[row];
+        const float* src = O + row * D + lane * E;
+        if constexpr (E == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          x[k][0] = v.x; x[k][1] = v.y; x[k][2 % E] = v.z; x[k][3 % E] = v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          x[k][0] = v.x; x[k][1] = v.y;
+        }
       }
-      L[k] = Ls[row];
-      const float* src = O + row * D + lane * E;
-      if constexpr (E == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        x[k][0] = v.x; x[k][1] = v.y; x[k][2 % E] = v.z; x[k][3 % E] = v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        x[k][0] = v.x; x[k][1] = v.y;
+      float mn = m;
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) mn = fmaxf(mn, L[k]);
+      const float mu = mn == -INFINITY ? 0.f : mn;
+      const float f = ex2_approx(m - mu);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= f;
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        const float w = ex2_approx(L[k] - mu);
+        l += w;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(w, x[k][e], acc[e]);
       }
-    }
-    float mn = m;
-#pragma unroll
-    for (int k = 0; k < AHEAD; ++k) mn = fmaxf(mn, L[k]);
-    const float mu = mn == -INFINITY ? 0.f : mn;
-    const float f = ex2_approx(m - mu);
-    m = mn;
-    l *= f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= f;
-#pragma unroll
-    for (int k = 0; k < AHEAD; ++k) {
-      const float w = ex2_approx(L[k] - mu);
-      l += w;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(w, x[k][e], acc[e]);
     }
   }
-  if constexpr (WPR > 1) {
+  // Groups of `step` warps meet; the first of each has the row's sum afterwards.
+  __device__ __forceinline__ void meet(int warp, int step, int lane) {
+    __shared__ float sm[kMergeWarps], sl[kMergeWarps], so[kMergeWarps][D];
 #pragma unroll
     for (int e = 0; e < E; ++e) so[warp][lane * E + e] = acc[e];
     if (lane == 0) {
@@ -1075,30 +1069,126 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const __
       sl[warp] = l;
     }
     __syncthreads();
-    if (warp != 0) return;
-    m = -INFINITY;
+    if ((warp & (step - 1)) == 0) {
+      float ms[kMergeWarps];  // of the other slots: no part
 #pragma unroll
-    for (int w = 0; w < WPR; ++w) m = fmaxf(m, sm[w]);
-    const float mu = m == -INFINITY ? 0.f : m;
-    l = 0.f;
+      for (int w = 0; w < kMergeWarps; ++w) ms[w] = w < step ? sm[warp + (w & (step - 1))] : -INFINITY;
+      m = -INFINITY;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+      for (int w = 0; w < kMergeWarps; ++w) m = fmaxf(m, ms[w]);
+      const float mu = m == -INFINITY ? 0.f : m;
+      l = 0.f;
 #pragma unroll
-    for (int w = 0; w < WPR; ++w) {
-      const float f = ex2_approx(sm[w] - mu);
-      l = fmaf(sl[w], f, l);
+      for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(so[w][lane * E + e], f, acc[e]);
+      for (int w = 0; w < kMergeWarps; ++w) {
+        const int from = warp + (w & (step - 1));
+        const float f = ex2_approx(ms[w] - mu);
+        l = fmaf(sl[from], f, l);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(so[from][lane * E + e], f, acc[e]);
+      }
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int g = r / a.Nq, i = r - g * a.Nq, hq = head * a.G + g;
-  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.O) + b * a.o_b + hq * a.o_h + i * a.o_r + lane * E;
-  if constexpr (E == 4)
-    *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2 % E] * inv, acc[3 % E] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-  if (lane == 0) a.LSE[(long long)unit * R + r] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+  // Row r of sequence b and K/V head `head`
+  __device__ __forceinline__ void store(const PagedDecodeArgs& a, int b, int head, int r, int lane) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int g = a.nq_div(r), i = r - g * a.Nq, hq = head * a.G + g;
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.O) + b * a.o_b + hq * a.o_h + i * a.o_r + lane * E;
+    if constexpr (E == 4)
+      *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2 % E] * inv, acc[3 % E] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+    if (lane == 0)
+      a.LSE[((long long)b * a.pool.kv_heads + head) * a.G * a.Nq + r] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+  }
+};
+
+// Without a prefix only the units that a share's end cuts have parts. Items are
+// (CTA that begins such a unit, row of the unit); a block looks at every
+// gridDim.x-th of them at once, one per lane, as many are none, and shares its
+// warps out among those that are: eight to a single row (a long sequence has
+// parts of many CTAs), one to each of many.
+template <int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_cut_kernel(const __grid_constant__ PagedDecodeArgs a, int rows) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned mine = blockIdx.x + lane * gridDim.x;  // at most 32 per block
+  const bool there = mine < (unsigned)(a.ctas * rows);
+  const int cta = there ? (rows < a.slot_rows ? a.rows_div((int)mine) : (int)(mine / (unsigned)rows)) : 0;
+  const int row = (int)mine - cta * rows;
+  const int2 c = there ? a.begun[cta] : make_int2(-1, 0);
+  const int n = c.y - cta + 1;
+  unsigned rest = __ballot_sync(kFull, c.x >= 0);
+  // the next kMergeWarps / STEP of the items, STEP warps each
+  auto merge = [&](auto STEP) {
+    unsigned from = rest;
+#pragma unroll
+    for (int k = 0; k < kMergeWarps / STEP; ++k) {
+      if (k < warp / STEP) from &= from - 1;
+      rest &= rest - 1;
+    }
+    const int at = __ffs(from) - 1;  // this warp's item, or -1
+    Parts P{};
+    P.unit = __shfl_sync(kFull, c.x, at & 31);
+    P.slot_row = __shfl_sync(kFull, row, at & 31);
+    P.own_first = __shfl_sync(kFull, cta, at & 31);
+    P.own_n = at < 0 ? 0 : __shfl_sync(kFull, n, at & 31);
+    RowSum<D, false> sum;
+    sum.add(a, P, warp % STEP, STEP, lane);
+    if (STEP > 1) sum.meet(warp, STEP, lane);
+    if (at >= 0 && warp % STEP == 0) {
+      const int heads = a.pool.kv_heads << a.group_shift, b = P.unit / heads, h = P.unit - b * heads, head = h >> a.group_shift;
+      const int r = (h - (head << a.group_shift)) * a.slot_rows + P.slot_row;
+      if (r < a.G * a.Nq) sum.store(a, b, head, r, lane);  // the unit may have fewer rows than others
+    }
+  };
+  while (rest != 0) {
+    const int items = __popc(rest);
+    if (items == 1) merge(std::integral_constant<int, 8>{});
+    else if (items <= 4) merge(std::integral_constant<int, 2>{});
+    else merge(std::integral_constant<int, 1>{});
+    if (rest != 0) __syncthreads();
+  }
+}
+
+// With a prefix every row has parts, as many as the prefix has key ranges: a
+// warp per row for up to 16 of those (WPR = 1), else a block (WPR = 8).
+template <int D, int WPR>
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_prefix_kernel(const __grid_constant__ PagedDecodeArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int Hkv = a.pool.kv_heads, R = a.G * a.Nq;
+  const unsigned item = blockIdx.x * (kMergeWarps / WPR) + warp / WPR;
+  if (item >= (unsigned)(a.B * Hkv) * (unsigned)R) return;  // the whole block, if its warps share a row
+  const int group = (int)(item / (unsigned)R), r = (int)(item - group * (unsigned)R);
+  const int b = group / Hkv, head = group - b * Hkv, rg = a.group_shift == 0 ? 0 : r / 32;
+  // a unit whose CTA gave up on a wait may have no entry, and then no result
+  auto in_grid = [&](int2 c) { return (unsigned)c.x <= (unsigned)c.y && (unsigned)c.y < (unsigned)a.ctas; };
+  Parts P{};
+  P.unit = (group << a.group_shift) + rg;
+  P.slot_row = r - rg * 32;
+  const int2 c = a.unit_ctas[P.unit];  // not written for a sequence without keys
+  P.own_first = c.x;
+  P.own_n = seq_keys(a, b) > 0 ? c.y - c.x + 1 : 0;
+  if (a.pre_splits > 0) {
+    const int rr = b * R + r, qblocks = (a.B * R + 255) / 256;
+    P.pre_n = a.pre_splits;
+    P.pre_row = ((long long)head * qblocks + rr / 256) * a.pre_splits * 256 + rr % 256;
+  } else {
+    P.pre_unit = a.B * Hkv + head;
+    P.pre_slot_row = b * R + r;
+    const int2 cp = a.unit_ctas[P.pre_unit];
+    P.pre_first = cp.x;
+    P.pre_n = cp.y - cp.x + 1;
+    if (!in_grid(cp)) return;
+  }
+  if (P.own_n != 0 && !in_grid(c)) return;
+  RowSum<D, true> sum;
+  sum.add(a, P, warp % WPR, WPR, lane);
+  if constexpr (WPR > 1) sum.meet(warp, WPR, lane);
+  if (WPR == 1 || warp == 0) sum.store(a, b, head, r, lane);
 }
 
 template <int D, int ROWS, bool BESIDE>
@@ -1124,20 +1214,22 @@ cudaError_t launch(const PagedDecodeArgs& a, cudaStream_t st) {
   cfg.numAttrs = 1;
   cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.dynamicSmemBytes = 0;
-  const unsigned rows = (unsigned)(a.G * a.Nq);
+  const int rows = a.G * a.Nq;
   if (a.prefix_len == 0) {
-    cfg.gridDim = dim3((unsigned)a.ctas * rows);
-    return cudaLaunchKernelEx(&cfg, decode_merge_kernel<D, kMergeWarps, false>, a);
+    // as many blocks as find room at once, each for several (CTA, row) items
+    const int unit_rows = rows < a.slot_rows ? rows : a.slot_rows, most = a.slot_rows == 32 ? 4 : 2;
+    cfg.gridDim = dim3((unsigned)(a.ctas * (unit_rows < most ? unit_rows : most)));
+    return cudaLaunchKernelEx(&cfg, merge_cut_kernel<D>, a, unit_rows);
   }
-  const unsigned all = (unsigned)(a.B * a.pool.kv_heads) * rows;
+  const unsigned all = (unsigned)(a.B * a.pool.kv_heads) * (unsigned)rows;
   // parts of a prefix that is part of the grid: about one per CTA and head
   const int parts = a.pre_splits > 0 ? a.pre_splits : a.ctas / a.pool.kv_heads;
   if (parts > 16) {
     cfg.gridDim = dim3(all);
-    return cudaLaunchKernelEx(&cfg, decode_merge_kernel<D, kMergeWarps, true>, a);
+    return cudaLaunchKernelEx(&cfg, merge_prefix_kernel<D, kMergeWarps>, a);
   }
   cfg.gridDim = dim3((all + kMergeWarps - 1) / kMergeWarps);
-  return cudaLaunchKernelEx(&cfg, decode_merge_kernel<D, 1, true>, a);
+  return cudaLaunchKernelEx(&cfg, merge_prefix_kernel<D, 1>, a);
 }
 
 // Also allows the kernel its shared memory on the current device; every launch
@@ -1155,23 +1247,25 @@ int ctas_per_sm() {
   return n;
 }
 
+// Rows of a K/V head up to which a prefix is one more sequence of the grid
+constexpr int kGridPrefixRows = 32;
+
 constexpr int kMaxDevices = 64;
 std::mutex g_slots_mu;
-int g_slots[kMaxDevices][2][5] = {};  // [device][d == 128][8, 16, 32, 64 rows, 8 beside a prefix] -> resident CTAs
+int g_slots[kMaxDevices][2][4] = {};  // [device][d == 128][8, 16, 32 rows, 8 beside a prefix] -> resident CTAs
 
 template <int D>
 int ctas_per_sm(int rows, bool beside) {
   return rows == 8    ? (beside ? ctas_per_sm<D, 8, true>() : ctas_per_sm<D, 8, false>())
          : rows == 16 ? ctas_per_sm<D, 16, false>()
-         : rows == 32 ? ctas_per_sm<D, 32, false>()
-                      : ctas_per_sm<D, 64, false>();
+                      : ctas_per_sm<D, 32, false>();
 }
 
 int resident_ctas(int d, int rows, bool beside) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
   std::lock_guard<std::mutex> lk(g_slots_mu);
-  int& slot = g_slots[dev][d == 128][rows == 8 ? (beside ? 4 : 0) : rows == 16 ? 1 : rows == 32 ? 2 : 3];
+  int& slot = g_slots[dev][d == 128][rows == 8 ? (beside ? 3 : 0) : rows == 16 ? 1 : 2];
   if (slot == 0) {
     int sms = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
@@ -1185,8 +1279,7 @@ cudaError_t launch_d(const PagedDecodeArgs& a, cudaStream_t st) {
   switch (a.slot_rows) {
     case 8: return a.pre_splits > 0 ? launch<D, 8, true>(a, st) : launch<D, 8, false>(a, st);
     case 16: return launch<D, 16, false>(a, st);
-    case 32: return launch<D, 32, false>(a, st);
-    default: return launch<D, 64, false>(a, st);
+    default: return launch<D, 32, false>(a, st);
   }
 }
 
@@ -1197,13 +1290,14 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 PagedLayout paged_layout(int B, int Hkv, int rows, int prefix_len, int d) {
   PagedLayout L{};
   const long long pre_rows = prefix_len > 0 ? (long long)B * rows : 0;
-  const bool own_kernel = pre_rows > kPagedMaxRows;
+  const bool own_kernel = pre_rows > kGridPrefixRows;
   const long long most = pre_rows > rows && !own_kernel ? pre_rows : rows;
-  L.slot_rows = most <= 8 ? 8 : most <= 16 ? 16 : most <= 32 ? 32 : 64;
+  L.slot_rows = most <= 8 ? 8 : most <= 16 ? 16 : 32;
+  while ((L.slot_rows << L.group_shift) < rows) ++L.group_shift;
   L.ctas = resident_ctas(d, L.slot_rows, own_kernel);
   if (L.ctas <= 0) return L;
   L.n_seq = B + (pre_rows > 0 && !own_kernel ? 1 : 0);
-  const size_t units = (size_t)L.n_seq * Hkv;
+  const size_t units = (size_t)L.n_seq * Hkv << L.group_shift;
   const size_t slots = 2 * (size_t)L.ctas + (prefix_len > 0 ? units : 0);
   L.lpart = up256(slots * L.slot_rows * d * sizeof(float));
   L.unit_ctas = L.lpart + up256(slots * L.slot_rows * sizeof(float));
@@ -1234,7 +1328,7 @@ PrefixPlan plan_prefix_beside(int B, int rows, int Hkv, int prefix_len, int d, i
   const int n_kv = (int)(((long long)prefix_len + 127) / 128);
   const long long units = ((long long)B * rows + 255) / 256 * Hkv;
   const double tile = ((long long)B * rows > 128 ? 1.76 : 1.05) * (d == 128 ? 1.0 : 0.67);
-  const double steps = (double)B * Hkv * (own_keys * (double)d / 8192.0 + kUnitSteps + 0.5);
+  const double steps = (double)B * Hkv * (rows > 32 ? 2 : 1) * (own_keys * (double)d / 8192.0 + kUnitSteps + 0.5);
   PrefixPlan best{max_splits, 0, 0};
   double best_us = -1;
   for (int s = 1; s <= max_splits; ++s) {

@@ -70,6 +70,43 @@ def test_rows_that_share_a_prefix(B, g, nq, prefix, page, d):
     _run(c, 2 * g, nq, seed=B)
 
 
+@pytest.mark.parametrize("g,nq", [(1, 1), (2, 1), (3, 1), (4, 1), (8, 1), (5, 3), (8, 2), (8, 4), (33, 1), (5, 8), (8, 8)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_of_units_cut_between_ctas(g, nq, d):
+    """A long sequence whose keys many CTAs share, short ones, empty ones: rows of one to many parts to merge."""
+    c = Cache((6000, 0, 5, 129, 900, 0), 3, 64, d, seed=g + nq)
+    c.poison()
+    q = _q(6, 3 * g, nq, d, seed=nq)
+    o, lse = _call(c, q)
+    assert fa.fa_check_device_status() == fa.FA_OK
+    check_decode(c, q, o, lse, 1 / math.sqrt(d), heads=[0, 2])
+
+
+@pytest.mark.parametrize("g,nq", [(6, 2), (8, 4), (9, 5)])
+def test_many_cut_units(g, nq):
+    """More units than CTAs, of lengths that leave nearly every CTA with a cut one."""
+    rng = np.random.default_rng(g)
+    lens = rng.integers(1, 400, 150).tolist()
+    c = Cache(lens, 3, 16, 64, seed=g)
+    q = _q(150, 3 * g, nq, 64, seed=g)
+    o, lse = _call(c, q)
+    assert fa.fa_check_device_status() == fa.FA_OK
+    check_decode(c, q, o, lse, 1 / 8, heads=[1], seqs=range(0, 150, 7))
+
+
+@pytest.mark.parametrize("B,g,nq,prefix", [(5, 8, 1, 700), (12, 1, 5, 300), (20, 33, 1, 500), (3, 8, 8, 1500)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_more_than_32_rows_with_a_prefix(B, g, nq, prefix, d):
+    """33 to 64 rows of the batch, and of one sequence."""
+    lens = np.random.default_rng(B).integers(0, 500, B).tolist()
+    c = Cache(lens, 2, 32, d, seed=B + d, prefix=prefix)
+    c.poison()
+    q = _q(B, 2 * g, nq, d, seed=B)
+    o, lse = _call(c, q)
+    assert fa.fa_check_device_status() == fa.FA_OK
+    check_decode(c, q, o, lse, 1 / math.sqrt(d), seqs=sorted({0, 1, B // 2, B - 1}))
+
+
 def test_one_long_sequence_among_short_ones():
     c = Cache((5, 20000, 1, 300, 64), 2, 64, 128, seed=1)
     _run(c, 8, 1, seed=2)
