@@ -1068,7 +1068,7 @@ struct RowSum {
       sm[warp] = m;
       sl[warp] = l;
     }
-    __syncthreads();
+    named_bar(1 + warp / step, 32 * step);
     if ((warp & (step - 1)) == 0) {
       float ms[kMergeWarps];  // of the other slots: no part
 #pragma unroll
@@ -1153,15 +1153,15 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_cut_kernel(const __gri
   }
 }
 
-// With a prefix every row has parts, as many as the prefix has key ranges: a
-// warp per row for up to 16 of those (WPR = 1), else a block (WPR = 8).
+// With a prefix every row has parts, as many as the prefix has key ranges. WPR
+// warps share a row.
 template <int D, int WPR>
 __global__ void __launch_bounds__(32 * kMergeWarps) merge_prefix_kernel(const __grid_constant__ PagedDecodeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int Hkv = a.pool.kv_heads, R = a.G * a.Nq;
   const unsigned item = blockIdx.x * (kMergeWarps / WPR) + warp / WPR;
-  if (item >= (unsigned)(a.B * Hkv) * (unsigned)R) return;  // the whole block, if its warps share a row
+  if (item >= (unsigned)(a.B * Hkv) * (unsigned)R) return;  // all warps of a row alike, here and below
   const int group = (int)(item / (unsigned)R), r = (int)(item - group * (unsigned)R);
   const int b = group / Hkv, head = group - b * Hkv, rg = a.group_shift == 0 ? 0 : r / 32;
   // a unit whose CTA gave up on a wait may have no entry, and then no result
@@ -1188,7 +1188,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_prefix_kernel(const __
   RowSum<D, true> sum;
   sum.add(a, P, warp % WPR, WPR, lane);
   if constexpr (WPR > 1) sum.meet(warp, WPR, lane);
-  if (WPR == 1 || warp == 0) sum.store(a, b, head, r, lane);
+  if (warp % WPR == 0) sum.store(a, b, head, r, lane);
 }
 
 template <int D, int ROWS, bool BESIDE>
@@ -1224,12 +1224,16 @@ cudaError_t launch(const PagedDecodeArgs& a, cudaStream_t st) {
   const unsigned all = (unsigned)(a.B * a.pool.kv_heads) * (unsigned)rows;
   // parts of a prefix that is part of the grid: about one per CTA and head
   const int parts = a.pre_splits > 0 ? a.pre_splits : a.ctas / a.pool.kv_heads;
-  if (parts > 16) {
-    cfg.gridDim = dim3(all);
-    return cudaLaunchKernelEx(&cfg, merge_prefix_kernel<D, kMergeWarps>, a);
-  }
-  cfg.gridDim = dim3((all + kMergeWarps - 1) / kMergeWarps);
-  return cudaLaunchKernelEx(&cfg, merge_prefix_kernel<D, 1>, a);
+  // Up to four parts of a row are one round of loads, more take several: more
+  // warps for a row while all rows find room at once, and beyond 16 parts anyway
+  // (768 rows of 12 parts: 16.6 -> 15.0 us of the call)
+  int wpr = 1;
+  while (wpr < kMergeWarps && (parts > 16 * wpr || (parts > 4 * wpr && all * wpr <= 3000))) wpr *= 2;
+  cfg.gridDim = dim3((all * wpr + kMergeWarps - 1) / kMergeWarps);
+  return cudaLaunchKernelEx(&cfg, wpr == 8   ? merge_prefix_kernel<D, 8>
+                                  : wpr == 4 ? merge_prefix_kernel<D, 4>
+                                  : wpr == 2 ? merge_prefix_kernel<D, 2>
+                                             : merge_prefix_kernel<D, 1>, a);
 }
 
 // Also allows the kernel its shared memory on the current device; every launch
@@ -1322,13 +1326,19 @@ PrefixPlan plan_prefix_beside(int B, int rows, int Hkv, int prefix_len, int d, i
   // Times in us, measured on a GB300: a prefix's CTA takes kStart and, per tile
   // of 128 keys, 1.76 (two tiles of query rows) or 1.05 (one), two thirds of
   // that at d = 64. An own keys' CTA beside it takes kOwnStart and 0.75 per
-  // step of 32 KB, or what all such CTAs' bytes take at 6 GB/ms; one that finds
-  // its SM only after the prefix's costs kLate before the rest goes on.
-  constexpr double kStart = 11.0, kOwnStart = 2.0, kStep = 0.75, kLate = 4.0, kStepAll = 32768.0 / 6e6;
+  // step of 32 KB (1.1, and 1.5 steps more per unit, with more than 16 rows at d
+  // = 128), or what all such CTAs' bytes take at 6 GB/ms; one that finds its SM
+  // only after the prefix's costs kLate before the rest goes on. Each key range
+  // is a partial result per row, written once and read once (9 sequences of 25
+  // rows, 32 heads, 953 keys: 33.6 -> 25.9 us with two ranges for three).
+  constexpr double kStart = 11.0, kOwnStart = 2.0, kLate = 4.0, kStepAll = 32768.0 / 6e6, kPartBytes = 6e6;
+  const bool wide = rows > 16 && d == 128;
+  const double kStep = wide ? 1.1 : 0.75;
   const int n_kv = (int)(((long long)prefix_len + 127) / 128);
   const long long units = ((long long)B * rows + 255) / 256 * Hkv;
   const double tile = ((long long)B * rows > 128 ? 1.76 : 1.05) * (d == 128 ? 1.0 : 0.67);
-  const double steps = (double)B * Hkv * (rows > 32 ? 2 : 1) * (own_keys * (double)d / 8192.0 + kUnitSteps + 0.5);
+  const double steps = (double)B * Hkv * (rows > 32 ? 2 : 1) * (own_keys * (double)d / 8192.0 + kUnitSteps + (wide ? 2.0 : 0.5));
+  const double part_us = (double)B * rows * Hkv * d * 8.0 / kPartBytes;
   PrefixPlan best{max_splits, 0, 0};
   double best_us = -1;
   for (int s = 1; s <= max_splits; ++s) {
@@ -1344,6 +1354,7 @@ PrefixPlan plan_prefix_beside(int B, int rows, int Hkv, int prefix_len, int d, i
     } else {
       us += kLate + (steps - early * (double)more) * kStepAll;
     }
+    us += s * part_us;
     if (best_us < 0 || us < best_us) {
       best_us = us;
       best = PrefixPlan{s, early, more};
