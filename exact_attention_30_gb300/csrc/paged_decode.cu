@@ -52,6 +52,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <mutex>
 #include <type_traits>
 
@@ -71,12 +72,14 @@ constexpr float kLn2 = 0.69314718055994531f;
 // ROWS: query rows of a unit, 8, 16 or 32 (fewer are padded). BESIDE: on
 // the few SMs that a prefix's kernel leaves, where the latency of units bounds
 // the own keys rather than memory: three CTAs per SM with two stages each
-// (8 rows, whose registers allow it; 128 samples 57.5 -> 54 us). Elsewhere two
-// with three stages: fewer parts to merge (48 ragged sequences 78.5 against
-// 79.6, 299 of 165 keys 18.3 against 20.2 us).
-template <int D_, int ROWS_, bool BESIDE>
+// (8 rows, whose registers allow it; 128 samples 57.5 -> 54 us): 1 for one new
+// token, 2 for several (keys that only some rows see cost registers, which
+// spill: 56.8 us). 0, elsewhere: two with three stages, fewer parts to merge (48
+// ragged sequences 78.5 against 79.6, 299 of 165 keys 18.3 against 20.2 us).
+template <int D_, int ROWS_, int BESIDE>
 struct Cfg {
   static constexpr int D = D_, ROWS = ROWS_;
+  static constexpr bool MANY_NEW = BESIDE != 1;  // more than one new token: keys that only some rows see
   static constexpr int MT = ROWS < 16 ? 1 : ROWS / 16;  // groups of rows, four consumer warps each
   static constexpr int OWN_ROWS = ROWS == 32 ? kPagedMaxRows : 16;  // query rows of a K/V head
   static constexpr int BK = 64;              // keys per tile
@@ -171,9 +174,32 @@ struct RowInfo {
   int hidden;
 };
 
-// Which of a pair of values, of keys k and k + 1, every row sees.
-__device__ __forceinline__ uint32_t keep_pair(int k, int seen) {
-  return (k < seen ? 0xffffu : 0u) | (k + 1 < seen ? 0xffff0000u : 0u);
+// Which of a pair of values, of keys k and k + 1, are of the first n keys.
+__device__ __forceinline__ uint32_t keep_pair(int k, int n) { return (k < n ? 0xffffu : 0u) | (k + 1 < n ? 0xffff0000u : 0u); }
+
+// Top bits of those halves of a pair of bf16 that are infinite or NaN.
+__device__ __forceinline__ uint32_t non_finite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+
+// The newest keys (seen .. len - 1) are hidden from some rows, whose weights
+// there are zero. Their values go through the product like all others, but
+// what is not finite (0 times it is NaN) is taken out of the fragments f, of
+// which first and second say what belongs to such keys (each register is a pair
+// of keys: of the first eight at even places, or in the first half of four).
+// True if there was any in the warp.
+template <int FB, bool ODD_IS_SECOND>
+__device__ __forceinline__ bool take_out(uint32_t (&f)[FB][4], uint32_t first, uint32_t second) {
+  uint32_t hit = 0;
+#pragma unroll
+  for (int i = 0; i < FB; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) hit |= non_finite(f[i][e]) & ((ODD_IS_SECOND ? e & 1 : e >> 1) ? second : first);
+  if (!__any_sync(kFull, hit != 0)) return false;
+#pragma unroll
+  for (int i = 0; i < FB; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      f[i][e] &= ~(((non_finite(f[i][e]) >> 15) * 0xffffu) & ((ODD_IS_SECOND ? e & 1 : e >> 1) ? second : first));
+  return true;
 }
 
 // Steps that an early CTA rather takes on top than leaves to CTAs that start
@@ -488,9 +514,13 @@ struct WarpRows16 {
     // the sums l keep the unrounded weights
     const uint32_t pf[4] = {pack_bf16x2(x[0][0], x[0][1]), pack_bf16x2(x[0][2], x[0][3]),
                             pack_bf16x2(x[1][0], x[1][1]), pack_bf16x2(x[1][2], x[1][3])};
-    // values of keys that some row does not see stay out of the product
-    // (0 times NaN); keys 2q, 2q + 1 and 8 + 2q, 8 + 2q + 1 are this lane's
-    const uint32_t keep0 = edge ? keep_pair(k0 + 2 * q, seen) : kFull, keep1 = edge ? keep_pair(k0 + 8 + 2 * q, seen) : kFull;
+    // values behind the last key stay out of the product (0 times NaN); keys
+    // 2q, 2q + 1 and 8 + 2q, 8 + 2q + 1 are this lane's
+    const uint32_t keep0 = edge ? keep_pair(k0 + 2 * q, len) : kFull, keep1 = edge ? keep_pair(k0 + 8 + 2 * q, len) : kFull;
+    if (C::MANY_NEW && edge && len > seen) {
+      newest(stage, k0, len, seen, lim_a, lim_b, keep0, keep1, x, pf, v_at);
+      return;
+    }
 #pragma unroll
     for (int n1 = 0; n1 < D / 16; n1 += FB) {
       if (n1 > 0) {
@@ -509,8 +539,28 @@ struct WarpRows16 {
         mma16816(acc[2 * (n1 + i) + 1], pf, f[i][2], f[i][3]);
       }
     }
-    if (edge && len > seen) {
-      // the newest keys, seen by some rows only: added row by row
+  }
+  // P V for keys of which some are hidden from some row (more than one new
+  // token): apart from the rest, which must not hold its registers.
+  template <class At>
+  __device__ __forceinline__ void newest(const uint8_t* stage, int k0, int len, int seen, int lim_a, int lim_b, uint32_t keep0, uint32_t keep1,
+                                         const float (&x)[2][4], const uint32_t (&pf)[4], const At& v_at) {
+    const uint32_t some0 = ~keep_pair(k0 + 2 * q, seen), some1 = ~keep_pair(k0 + 8 + 2 * q, seen);
+    bool taken = false;
+#pragma unroll
+    for (int n = 0; n < D / 16; ++n) {
+      uint32_t f[1][4];
+      ldmatrix4_t(f[0], v_at(n));
+      f[0][0] &= keep0;
+      f[0][1] &= keep1;
+      f[0][2] &= keep0;
+      f[0][3] &= keep1;
+      taken |= take_out<1, true>(f, some0, some1);
+      mma16816(acc[2 * n], pf, f[0][0], f[0][1]);
+      mma16816(acc[2 * n + 1], pf, f[0][2], f[0][3]);
+    }
+    if (taken) {
+      // what was taken out goes to the rows that see it
       for (int k = max(k0, seen); k < min(k0 + 16, len); ++k) {
         const int c = k - k0, src = (g << 2) | ((c & 7) >> 1);
         const float pa = (c & 8) ? ((c & 1) ? x[1][1] : x[1][0]) : ((c & 1) ? x[0][1] : x[0][0]);
@@ -522,13 +572,13 @@ struct WarpRows16 {
         for (int nn = 0; nn < D / 8; ++nn) {
           const uint32_t v2 = *reinterpret_cast<const uint32_t*>(vr + (nn >> 3) * C::CHUNK + (((nn & 7) ^ (r & 7)) << 4));
           const float v0 = __uint_as_float(v2 << 16), v1 = __uint_as_float(v2 & 0xffff0000u);
-          if (k < lim_a) {
-            acc[nn][0] = fmaf(p_a, v0, acc[nn][0]);
-            acc[nn][1] = fmaf(p_a, v1, acc[nn][1]);
+          if (!isfinite(v0)) {
+            if (k < lim_a) acc[nn][0] = fmaf(p_a, v0, acc[nn][0]);
+            if (k < lim_b) acc[nn][2] = fmaf(p_b, v0, acc[nn][2]);
           }
-          if (k < lim_b) {
-            acc[nn][2] = fmaf(p_b, v0, acc[nn][2]);
-            acc[nn][3] = fmaf(p_b, v1, acc[nn][3]);
+          if (!isfinite(v1)) {
+            if (k < lim_a) acc[nn][1] = fmaf(p_a, v1, acc[nn][1]);
+            if (k < lim_b) acc[nn][3] = fmaf(p_b, v1, acc[nn][3]);
           }
         }
       }
@@ -623,8 +673,10 @@ struct WarpRows8 {
     const bool edge = k0 + 16 > seen;  // some key of this warp is hidden from some row
     int lim0 = len, lim1 = len;        // keys that rows 2q and 2q + 1 see
     if (edge) {
-      lim0 -= 2 * q < rows ? info[2 * q].hidden : 0;
-      lim1 -= 2 * q + 1 < rows ? info[2 * q + 1].hidden : 0;
+      if (C::MANY_NEW) {
+        lim0 -= 2 * q < rows ? info[2 * q].hidden : 0;
+        lim1 -= 2 * q + 1 < rows ? info[2 * q + 1].hidden : 0;
+      }
       if (k0 + g >= lim0) x[0] = -INFINITY;
       if (k0 + g >= lim1) x[1] = -INFINITY;
       if (k0 + g + 8 >= lim0) x[2] = -INFINITY;
@@ -663,9 +715,13 @@ struct WarpRows8 {
     // P is rounded to bf16 for the product (half a step of each weight);
     // the sums l keep the unrounded weights
     const uint32_t b0 = transpose8(pack_bf16x2(x[0], x[1])), b1 = transpose8(pack_bf16x2(x[2], x[3]));
-    // values of keys that some row does not see stay out of the product
-    // (0 times NaN); keys 2q, 2q + 1 and 8 + 2q, 8 + 2q + 1 are this lane's
-    const uint32_t keep0 = edge ? keep_pair(k0 + 2 * q, seen) : kFull, keep1 = edge ? keep_pair(k0 + 8 + 2 * q, seen) : kFull;
+    // values behind the last key stay out of the product (0 times NaN); keys
+    // 2q, 2q + 1 and 8 + 2q, 8 + 2q + 1 are this lane's
+    const uint32_t keep0 = edge ? keep_pair(k0 + 2 * q, len) : kFull, keep1 = edge ? keep_pair(k0 + 8 + 2 * q, len) : kFull;
+    if (C::MANY_NEW && edge && len > seen) {
+      newest(stage, k0, len, seen, lim0, lim1, keep0, keep1, x, b0, b1, v_at);
+      return;
+    }
 #pragma unroll
     for (int i1 = 0; i1 < D / 16; i1 += FB) {
       if (i1 > 0) {
@@ -683,8 +739,27 @@ struct WarpRows8 {
         mma16816(acc[i1 + i], f[i], b0, b1);
       }
     }
-    if (edge && len > seen) {
-      // the newest keys, seen by some rows only: added row by row
+  }
+  // P V for keys of which some are hidden from some row (more than one new
+  // token): apart from the rest, which must not hold its registers.
+  template <class At>
+  __device__ __forceinline__ void newest(const uint8_t* stage, int k0, int len, int seen, int lim0, int lim1, uint32_t keep0, uint32_t keep1,
+                                         const float (&x)[4], uint32_t b0, uint32_t b1, const At& v_at) {
+    const uint32_t some0 = ~keep_pair(k0 + 2 * q, seen), some1 = ~keep_pair(k0 + 8 + 2 * q, seen);
+    bool taken = false;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      uint32_t f[1][4];
+      ldmatrix4_t(f[0], v_at(i));
+      f[0][0] &= keep0;
+      f[0][1] &= keep0;
+      f[0][2] &= keep1;
+      f[0][3] &= keep1;
+      taken |= take_out<1, false>(f, some0, some1);
+      mma16816(acc[i], f[0], b0, b1);
+    }
+    if (taken) {
+      // what was taken out goes to the rows that see it
       for (int k = max(k0, seen); k < min(k0 + 16, len); ++k) {
         const int c = k - k0, src = ((c & 7) << 2) | q;
         const float p0 = __shfl_sync(kFull, (c & 8) ? x[2] : x[0], src), p1 = __shfl_sync(kFull, (c & 8) ? x[3] : x[1], src);
@@ -695,13 +770,13 @@ struct WarpRows8 {
           const uint8_t* p = vr + (i >> 2) * C::CHUNK;
           const float v0 = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(p + (((2 * i & 7) ^ (r & 7)) << 4)) << 16);
           const float v1 = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(p + ((((2 * i + 1) & 7) ^ (r & 7)) << 4)) << 16);
-          if (k < lim0) {
-            acc[i][0] = fmaf(p0, v0, acc[i][0]);
-            acc[i][2] = fmaf(p0, v1, acc[i][2]);
+          if (!isfinite(v0)) {
+            if (k < lim0) acc[i][0] = fmaf(p0, v0, acc[i][0]);
+            if (k < lim1) acc[i][1] = fmaf(p1, v0, acc[i][1]);
           }
-          if (k < lim1) {
-            acc[i][1] = fmaf(p1, v0, acc[i][1]);
-            acc[i][3] = fmaf(p1, v1, acc[i][3]);
+          if (!isfinite(v1)) {
+            if (k < lim0) acc[i][2] = fmaf(p0, v1, acc[i][2]);
+            if (k < lim1) acc[i][3] = fmaf(p1, v1, acc[i][3]);
           }
         }
       }
@@ -738,7 +813,7 @@ struct WarpRows8 {
   }
 };
 
-template <int D, int ROWS, bool BESIDE>
+template <int D, int ROWS, int BESIDE>
 __global__ void __launch_bounds__(Cfg<D, ROWS, BESIDE>::THREADS, Cfg<D, ROWS, BESIDE>::CTAS)
     decode_paged_kernel(const __grid_constant__ PagedDecodeArgs a) {
   using C = Cfg<D, ROWS, BESIDE>;
@@ -1191,7 +1266,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_prefix_kernel(const __
   if (warp % WPR == 0) sum.store(a, b, head, r, lane);
 }
 
-template <int D, int ROWS, bool BESIDE>
+template <int D, int ROWS, int BESIDE>
 cudaError_t launch(const PagedDecodeArgs& a, cudaStream_t st) {
   using C = Cfg<D, ROWS, BESIDE>;
   // programmatic dependent launches: each kernel is set up while the one
@@ -1238,7 +1313,7 @@ cudaError_t launch(const PagedDecodeArgs& a, cudaStream_t st) {
 
 // Also allows the kernel its shared memory on the current device; every launch
 // follows a paged_layout() on the same device.
-template <int D, int ROWS, bool BESIDE>
+template <int D, int ROWS, int BESIDE>
 int ctas_per_sm() {
   using C = Cfg<D, ROWS, BESIDE>;
   if (cudaFuncSetAttribute(decode_paged_kernel<D, ROWS, BESIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC) !=
@@ -1260,9 +1335,9 @@ int g_slots[kMaxDevices][2][4] = {};  // [device][d == 128][8, 16, 32 rows, 8 be
 
 template <int D>
 int ctas_per_sm(int rows, bool beside) {
-  return rows == 8    ? (beside ? ctas_per_sm<D, 8, true>() : ctas_per_sm<D, 8, false>())
-         : rows == 16 ? ctas_per_sm<D, 16, false>()
-                      : ctas_per_sm<D, 32, false>();
+  return rows == 8    ? (beside ? std::min(ctas_per_sm<D, 8, 1>(), ctas_per_sm<D, 8, 2>()) : ctas_per_sm<D, 8, 0>())
+         : rows == 16 ? ctas_per_sm<D, 16, 0>()
+                      : ctas_per_sm<D, 32, 0>();
 }
 
 int resident_ctas(int d, int rows, bool beside) {
@@ -1281,9 +1356,9 @@ int resident_ctas(int d, int rows, bool beside) {
 template <int D>
 cudaError_t launch_d(const PagedDecodeArgs& a, cudaStream_t st) {
   switch (a.slot_rows) {
-    case 8: return a.pre_splits > 0 ? launch<D, 8, true>(a, st) : launch<D, 8, false>(a, st);
-    case 16: return launch<D, 16, false>(a, st);
-    default: return launch<D, 32, false>(a, st);
+    case 8: return a.pre_splits == 0 ? launch<D, 8, 0>(a, st) : a.Nq == 1 ? launch<D, 8, 1>(a, st) : launch<D, 8, 2>(a, st);
+    case 16: return launch<D, 16, 0>(a, st);
+    default: return launch<D, 32, 0>(a, st);
   }
 }
 

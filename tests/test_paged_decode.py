@@ -161,6 +161,34 @@ def test_unseen_new_tokens_may_hold_anything(prefix):
     assert torch.isnan(lse[:, :, nq - 1]).all()
 
 
+@pytest.mark.parametrize("B,g,nq,prefix", [(3, 1, 5, 0), (3, 2, 7, 0), (3, 4, 8, 0), (3, 3, 20, 0), (3, 1, 5, 100), (30, 1, 5, 700)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_of_newer_tokens_may_hold_anything(B, g, nq, prefix, d):
+    """Infinities and NaN in single values of the last new tokens: rows that do not see those tokens stay as they
+    are, bit by bit; rows that do get what a sum with such a term gives, in that column only."""
+    lens = [150, 64 + nq, 3 * nq] + [90] * (B - 3)
+    c = Cache(lens, 2, 16, d, seed=nq + d, prefix=prefix)
+    q = _q(B, 2 * g, nq, d, 12)
+    clean_o, clean_l = _call(c, q)
+    check_decode(c, q, clean_o, clean_l, 1 / math.sqrt(d), seqs=[0, 1, 2])
+    bad = {nq // 2: (3, math.inf), nq - 1: (d - 2, math.nan)}  # new token: column, value
+    for b, n in enumerate(lens):
+        for i, (col, x) in bad.items():
+            j = n - nq + i
+            c.v[int(c.tables[b, j // 16]), :, j % 16, col] = x
+    o, lse = _call(c, q)
+    assert fa.fa_check_device_status() == fa.FA_OK
+    assert torch.equal(lse, clean_l)
+    for i in range(nq):
+        same = torch.ones(d, dtype=torch.bool)
+        for first, (col, x) in bad.items():
+            if i >= first:
+                same[col] = False
+                got = o[:, :, i, col]
+                assert bool((torch.isnan(got) if math.isnan(x) else torch.isnan(got) | (got == x)).all()), (i, col)
+        assert torch.equal(o[:, :, i, same], clean_o[:, :, i, same]), i
+
+
 @pytest.mark.parametrize("prefix", [0, 333, 5000])
 def test_strided_queries_and_outputs(prefix):
     """Token-major views of queries and outputs; what lies between the rows of the output stays."""
