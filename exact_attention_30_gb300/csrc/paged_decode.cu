@@ -20,7 +20,7 @@
 // is written out directly.
 //
 // A shared prefix with no more rows than fit a unit (those of every sequence,
-// B * R <= 64 per K/V head) is one more sequence of the same grid. With more
+// B * R <= 32 per K/V head) is one more sequence of the same grid. With more
 // rows it is a matrix product of its own (launch_prefix_bf16), and only its
 // partial results meet the own keys' here.
 //
@@ -36,14 +36,18 @@
 // an SM (up to 16 rows), one loading while the other one merges.
 //
 // Measured on a GB300, GPU time of a call: 8 sequences of 32768 keys (8 heads,
-// 8 queries each, d = 128) 163-165 us, 6.5-6.6 TB/s, 96-97% of a copy's rate; 48 of
-// 100 to 9000 keys (8 heads, 4 queries each) 78 us, 6.1 TB/s. The same kernel
+// 8 queries each, d = 128) 163 us, 6.6 TB/s, 97% of a copy's rate; 48 of 100
+// to 9000 keys (8 heads, 4 queries each) 77 us, 6.1 TB/s. The same kernel
 // that loads and does not compute takes 162 and 77: loads, not products, bound
 // long caches. 20 sequences of 333 to 4097 keys (16 heads, 4 new tokens,
-// d = 64) 27 us against 18 for the bytes, and one of 701 keys 7.4 us: about 4 us
+// d = 64) 27 us against 18 for the bytes, and one of 701 keys 7.6 us: about 4 us
 // of the chain length - page - keys and 2 us of merge.
 //
-// Tried and slower: tiles of 128 keys at d = 64 (27 -> 32 us); the merge done
+// More than 32 rows are two units, the second of which finds the keys in L2: 32
+// units of 16384 keys 95 us with 64 rows, 54 with 32, 51 with 16, 47 with 4.
+//
+// Tried and slower: 64 rows in one unit (16 consumer warps of 112 registers, 211
+// us for those); tiles of 128 keys at d = 64 (27 -> 32 us); the merge done
 // by the last CTA of a unit, by a ticket (one sequence 7.7 -> 13 us); 32 keys
 // per warp, pairs of warps on alternate tiles (long 164 -> 178 us); a ring and
 // a share for every warp (long 165 -> 192 us: the TMA takes over 100 cycles per
