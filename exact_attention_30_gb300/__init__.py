@@ -62,6 +62,7 @@ _ll = ctypes.c_longlong
 # are passed as the packed bytes: for a decode step of one short sequence, what
 # the host does per call is most of the time, and a ctypes structure costs more.
 _get_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _pack_pool = struct.Struct("@PPiiii6q").pack
 _pack_strides = struct.Struct("@3q").pack
 
@@ -476,7 +477,7 @@ def _paged_cache(k_pages, v_pages, block_tables, seq_lens):
 
 def _on_device(dev: int, fn, *args):
     """fn(*args, current stream of device dev), with dev as the current device."""
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():  # a CUDA tensor is there, so CUDA is initialised
         return fn(*args, _raw_stream(dev))
     with torch.cuda.device(dev):
         return fn(*args, _raw_stream(dev))

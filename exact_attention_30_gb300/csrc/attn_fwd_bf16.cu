@@ -893,6 +893,10 @@ cudaError_t launch_fwd_d(const FwdArgs& a, int BH, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+std::mutex g_slots_mu;
+int g_slots[16] = {};
+bool g_prefix_set[16][2] = {};  // the prefix kernel's shared memory has been asked for: a call of 1 us
+
 template <int D>
 cudaError_t launch_prefix_d(const PrefixArgs& a, cudaStream_t st) {
   using C = FwdCfg<D>;
@@ -901,15 +905,21 @@ cudaError_t launch_prefix_d(const PrefixArgs& a, cudaStream_t st) {
   if (a.rows < 1 || a.seq.N < 1 || a.splits < 1 || a.splits > (a.seq.N + C::BN - 1) / C::BN || a.n_full != 0 ||
       a.n_tail != units || units * a.splits > 0x7fffffffll)
     return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(fwd_bf16_kernel<D, PrefixArgs>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 16) return cudaErrorInvalidValue;
+  {
+    std::lock_guard<std::mutex> lk(g_slots_mu);
+    if (!g_prefix_set[dev][D == 128]) {
+      e = cudaFuncSetAttribute(fwd_bf16_kernel<D, PrefixArgs>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
+      if (e != cudaSuccess) return e;
+      g_prefix_set[dev][D == 128] = true;
+    }
+  }
   fwd_bf16_kernel<D, PrefixArgs><<<(unsigned)(units * a.splits), C::THREADS, C::SMEM_ALLOC, st>>>(a);
   return cudaGetLastError();
 }
-
-std::mutex g_slots_mu;
-int g_slots[16] = {};
 
 }  // namespace
 

@@ -77,6 +77,36 @@ bool view_strides(const long long* s, int B, int H, int N, int d, long long* sb,
   return true;
 }
 
+// Layout and plan of a decode, functions of its sizes and the device alone. A
+// decoding loop asks for the same ones again and again, and trying all numbers
+// of key ranges costs the host 2 us: each thread keeps its last.
+struct Schedule {
+  int dev, B, Hkv, rows, prefix_len, d, own_keys;
+  PagedLayout layout;
+  PrefixPlan plan;
+};
+const Schedule* schedule(int B, int Hkv, int rows, int prefix_len, int d, int own_keys) {
+  thread_local Schedule last = {-1, 0, 0, 0, 0, 0, 0, {}, {}};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+  if (last.dev == dev && last.B == B && last.Hkv == Hkv && last.rows == rows && last.prefix_len == prefix_len &&
+      last.d == d && last.own_keys == own_keys)
+    return &last;
+  last.dev = -1;
+  last.layout = paged_layout(B, Hkv, rows, prefix_len, d);
+  if (last.layout.ctas < 1) return nullptr;
+  if (last.layout.pre_splits > 0)
+    last.plan = plan_prefix_beside(B, rows, Hkv, prefix_len, d, last.layout.pre_splits, last.layout.ctas, fwd_slots(), own_keys);
+  last.B = B;
+  last.Hkv = Hkv;
+  last.rows = rows;
+  last.prefix_len = prefix_len;
+  last.d = d;
+  last.own_keys = own_keys;
+  last.dev = dev;
+  return &last;
+}
+
 fa_status decode_impl(const void* Q, const long long* q_strides, const fa_paged_kv* cache,
                       const int* prefix_pages, int prefix_len, const int* block_tables, int max_pages,
                       const int* seq_lens, void* O, const long long* o_strides, float* LSE,
@@ -98,15 +128,20 @@ fa_status decode_impl(const void* Q, const long long* q_strides, const fa_paged_
   if (!view_strides(q_strides, B, Hq, Nq, cache->d, &a.q_b, &a.q_h, &a.q_r) ||
       !view_strides(o_strides, B, Hq, Nq, cache->d, &a.o_b, &a.o_h, &a.o_r))
     return FA_ERR_INVALID_ARG;
-  const PagedLayout L = paged_layout(B, cache->kv_heads, Hq / cache->kv_heads * Nq, prefix_len, cache->d);
-  if (L.ctas < 1) return FA_ERR_CUDA;
+  // a table is as wide as its longest sequence may get; a quarter of that is
+  // taken for what the sequences hold on average
+  const long long most = (long long)max_pages * cache->page_size;
+  const int own_keys = (int)(most < kPagedMaxKeys ? most : kPagedMaxKeys) / 4;
+  const Schedule* sched = schedule(B, cache->kv_heads, Hq / cache->kv_heads * Nq, prefix_len, cache->d, own_keys);
+  if (!sched) return FA_ERR_CUDA;
+  const PagedLayout& L = sched->layout;
   if (workspace_bytes < L.total) return FA_ERR_INVALID_ARG;
   a.status = device_status_ptr();
   if (!a.status) return FA_ERR_CUDA;
   // boxes never cross a page's end, and a sequence's last one is loaded whole:
   // short sequences (up to 512 keys by their table) get boxes of up to 16 rows
   // (4 to 7% faster), others of up to 64 (3% faster than 16)
-  const int most_shift = (long long)max_pages * cache->page_size <= 512 ? 4 : 6;
+  const int most_shift = most <= 512 ? 4 : 6;
   while (a.box_shift < most_shift && cache->page_size % (2 << a.box_shift) == 0) ++a.box_shift;
   if (!encode_pool_bf16(&a.tmK, a.pool, false, cache->d, 1 << a.box_shift) ||
       !encode_pool_bf16(&a.tmV, a.pool, true, cache->d, 1 << a.box_shift))
@@ -145,11 +180,7 @@ fa_status decode_impl(const void* Q, const long long* q_strides, const fa_paged_
     p.box_rows = cache->page_size & -cache->page_size;
     if (p.box_rows > 128) p.box_rows = 128;
     p.rows = B * a.G * Nq;
-    // a table is as wide as its longest sequence may get; a quarter of that is
-    // taken for what the sequences hold on average
-    const long long most = (long long)max_pages * cache->page_size;
-    const PrefixPlan plan = plan_prefix_beside(B, a.G * Nq, cache->kv_heads, prefix_len, cache->d, L.pre_splits, L.ctas,
-                                               fwd_slots(), (int)(most < kPagedMaxKeys ? most : kPagedMaxKeys) / 4);
+    const PrefixPlan& plan = sched->plan;
     const long long units = ((long long)p.rows + 255) / 256 * cache->kv_heads;
     p.Opart = reinterpret_cast<float*>(ws + L.pre_opart);
     p.Lpart = reinterpret_cast<float*>(ws + L.pre_lpart);
