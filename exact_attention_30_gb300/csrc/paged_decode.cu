@@ -1270,6 +1270,16 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_prefix_kernel(const __
   if (warp % WPR == 0) sum.store(a, b, head, r, lane);
 }
 
+// Warps per row of merge_prefix_kernel. Up to four parts of a row are one round
+// of loads, more take several: more warps for a row while all rows find room at
+// once, and beyond 16 parts anyway (768 rows of 12 parts: 16.3 -> 14.2 us of the
+// call).
+int merge_warps(long long rows, int parts) {
+  int n = 1;
+  while (n < kMergeWarps && (parts > 16 * n || (parts > 4 * n && rows * n <= 3000))) n *= 2;
+  return n;
+}
+
 template <int D, int ROWS, int BESIDE>
 cudaError_t launch(const PagedDecodeArgs& a, cudaStream_t st) {
   using C = Cfg<D, ROWS, BESIDE>;
@@ -1303,11 +1313,7 @@ cudaError_t launch(const PagedDecodeArgs& a, cudaStream_t st) {
   const unsigned all = (unsigned)(a.B * a.pool.kv_heads) * (unsigned)rows;
   // parts of a prefix that is part of the grid: about one per CTA and head
   const int parts = a.pre_splits > 0 ? a.pre_splits : a.ctas / a.pool.kv_heads;
-  // Up to four parts of a row are one round of loads, more take several: more
-  // warps for a row while all rows find room at once, and beyond 16 parts anyway
-  // (768 rows of 12 parts: 16.6 -> 15.0 us of the call)
-  int wpr = 1;
-  while (wpr < kMergeWarps && (parts > 16 * wpr || (parts > 4 * wpr && all * wpr <= 3000))) wpr *= 2;
+  const int wpr = merge_warps(all, parts);
   cfg.gridDim = dim3((all * wpr + kMergeWarps - 1) / kMergeWarps);
   return cudaLaunchKernelEx(&cfg, wpr == 8   ? merge_prefix_kernel<D, 8>
                                   : wpr == 4 ? merge_prefix_kernel<D, 4>
@@ -1402,22 +1408,23 @@ PagedLayout paged_layout(int B, int Hkv, int rows, int prefix_len, int d) {
 
 PrefixPlan plan_prefix_beside(int B, int rows, int Hkv, int prefix_len, int d, int max_splits, int ctas, int sms,
                               int own_keys) {
-  // Times in us, measured on a GB300: a prefix's CTA takes kStart and, per tile
+  // Times in us, measured on a GB300. A prefix's CTA takes kStart and, per tile
   // of 128 keys, 1.76 (two tiles of query rows) or 1.05 (one), two thirds of
-  // that at d = 64. An own keys' CTA beside it takes kOwnStart and 0.75 per
-  // step of 32 KB (1.1, and 1.5 steps more per unit, with more than 16 rows at d
-  // = 128), or what all such CTAs' bytes take at 6 GB/ms; one that finds its SM
-  // only after the prefix's costs kLate before the rest goes on. Each key range
-  // is a partial result per row, written once and read once (9 sequences of 25
-  // rows, 32 heads, 953 keys: 33.6 -> 25.9 us with two ranges for three).
-  constexpr double kStart = 11.0, kOwnStart = 2.0, kLate = 4.0, kStepAll = 32768.0 / 6e6, kPartBytes = 6e6;
+  // that at d = 64. An own keys' CTA beside it takes kOwnStart and per step (64
+  // keys) 0.75, 0.6 at d = 64, 1.1 and 1.5 steps more per unit with more than 16
+  // rows at d = 128, or what all such CTAs' bytes take at 6 GB/ms; one that finds
+  // its SM only after the prefix's costs kLate, in which the others go on. Each
+  // key range is a partial result per row, written once and read once, four of
+  // them in a round of the merge. The own keys are a guess: the plan is the one
+  // with the least time for half, all and twice of them together.
+  constexpr double kStart = 11.0, kOwnStart = 2.0, kLate = 3.0, kPartBytes = 4e6, kRound = 1.0;
   const bool wide = rows > 16 && d == 128;
-  const double kStep = wide ? 1.1 : 0.75;
+  const double kStep = wide ? 1.1 : d == 128 ? 0.75 : 0.6, kStepAll = 256.0 * d / 6e6;
   const int n_kv = (int)(((long long)prefix_len + 127) / 128);
-  const long long units = ((long long)B * rows + 255) / 256 * Hkv;
-  const double tile = ((long long)B * rows > 128 ? 1.76 : 1.05) * (d == 128 ? 1.0 : 0.67);
-  const double steps = (double)B * Hkv * (rows > 32 ? 2 : 1) * (own_keys * (double)d / 8192.0 + kUnitSteps + (wide ? 2.0 : 0.5));
-  const double part_us = (double)B * rows * Hkv * d * 8.0 / kPartBytes;
+  const long long all_rows = (long long)B * rows, units = (all_rows + 255) / 256 * Hkv;
+  const double tile = (all_rows > 128 ? 1.76 : 1.05) * (d == 128 ? 1.0 : 0.67);
+  const double own_units = (double)B * Hkv * (rows > 32 ? 2 : 1);
+  const double part_us = (double)all_rows * Hkv * d * 8.0 / kPartBytes;
   PrefixPlan best{max_splits, 0, 0};
   double best_us = -1;
   for (int s = 1; s <= max_splits; ++s) {
@@ -1425,15 +1432,16 @@ PrefixPlan plan_prefix_beside(int B, int rows, int Hkv, int prefix_len, int d, i
     const double pre_us = kStart + (double)waves * ((n_kv + s - 1) / s) * tile;
     const int early = waves == 1 ? (sms - (int)(units * s)) * (ctas / sms) : 0;
     const double step = early * kStepAll > kStep ? early * kStepAll : kStep;
-    const int more = early > 0 && pre_us > kOwnStart ? (int)((pre_us - kOwnStart) / step) : 0;
-    double us = pre_us;
-    if (early > 0 && steps <= early * (double)(more + kEarlySlack)) {
-      const double own_us = kOwnStart + steps / early * step;
-      us = own_us > us ? own_us : us;
-    } else {
-      us += kLate + (steps - early * (double)more) * kStepAll;
+    const int more = early > 0 ? (int)((pre_us + kLate - kOwnStart) / step) : 0;
+    const int per_round = 4 * merge_warps(all_rows * Hkv, s);
+    double us = 3 * (s * part_us + (s + per_round) / per_round * kRound);
+    for (double guess = 0.5; guess <= 2; guess *= 2) {
+      const double steps = own_units * (guess * own_keys / 64.0 + kUnitSteps + (wide ? 2.0 : 0.5));
+      if (early > 0 && steps <= early * (double)more)
+        us += std::max(pre_us, kOwnStart + steps / early * step);
+      else
+        us += pre_us + kLate + (steps - early * (double)more) * kStepAll;
     }
-    us += s * part_us;
     if (best_us < 0 || us < best_us) {
       best_us = us;
       best = PrefixPlan{s, early, more};
