@@ -307,12 +307,12 @@ struct PagedLayout {
 // unit of the former (at most max_splits, which the scratch is laid out for),
 // and the CTAs of the latter that find an SM meanwhile, with the steps they take
 // in that time. rows = G * Nq; own_keys: an estimate of a sequence's own keys
-// (the lengths are on the device).
+// (the lengths are on the device); narrow: boxes of 8 rows, which load slower.
 struct PrefixPlan {
   int splits, early_ctas, early_steps;
 };
 PrefixPlan plan_prefix_beside(int B, int rows, int Hkv, int prefix_len, int d, int max_splits, int ctas, int sms,
-                              int own_keys);
+                              int own_keys, bool narrow);
 PagedLayout paged_layout(int B, int Hkv, int rows, int prefix_len, int d);
 cudaError_t launch_decode_paged_bf16(const PagedDecodeArgs& a, int d, cudaStream_t st);
 

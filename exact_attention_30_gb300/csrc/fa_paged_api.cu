@@ -82,27 +82,30 @@ bool view_strides(const long long* s, int B, int H, int N, int d, long long* sb,
 // of key ranges costs the host 2 us: each thread keeps its last.
 struct Schedule {
   int dev, B, Hkv, rows, prefix_len, d, own_keys;
+  bool narrow;
   PagedLayout layout;
   PrefixPlan plan;
 };
-const Schedule* schedule(int B, int Hkv, int rows, int prefix_len, int d, int own_keys) {
-  thread_local Schedule last = {-1, 0, 0, 0, 0, 0, 0, {}, {}};
+const Schedule* schedule(int B, int Hkv, int rows, int prefix_len, int d, int own_keys, bool narrow) {
+  thread_local Schedule last = {-1, 0, 0, 0, 0, 0, 0, false, {}, {}};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
   if (last.dev == dev && last.B == B && last.Hkv == Hkv && last.rows == rows && last.prefix_len == prefix_len &&
-      last.d == d && last.own_keys == own_keys)
+      last.d == d && last.own_keys == own_keys && last.narrow == narrow)
     return &last;
   last.dev = -1;
   last.layout = paged_layout(B, Hkv, rows, prefix_len, d);
   if (last.layout.ctas < 1) return nullptr;
   if (last.layout.pre_splits > 0)
-    last.plan = plan_prefix_beside(B, rows, Hkv, prefix_len, d, last.layout.pre_splits, last.layout.ctas, fwd_slots(), own_keys);
+    last.plan = plan_prefix_beside(B, rows, Hkv, prefix_len, d, last.layout.pre_splits, last.layout.ctas, fwd_slots(), own_keys,
+                                   narrow);
   last.B = B;
   last.Hkv = Hkv;
   last.rows = rows;
   last.prefix_len = prefix_len;
   last.d = d;
   last.own_keys = own_keys;
+  last.narrow = narrow;
   last.dev = dev;
   return &last;
 }
@@ -132,7 +135,8 @@ fa_status decode_impl(const void* Q, const long long* q_strides, const fa_paged_
   // taken for what the sequences hold on average
   const long long most = (long long)max_pages * cache->page_size;
   const int own_keys = (int)(most < kPagedMaxKeys ? most : kPagedMaxKeys) / 4;
-  const Schedule* sched = schedule(B, cache->kv_heads, Hq / cache->kv_heads * Nq, prefix_len, cache->d, own_keys);
+  const Schedule* sched = schedule(B, cache->kv_heads, Hq / cache->kv_heads * Nq, prefix_len, cache->d, own_keys,
+                                   cache->page_size % 16 != 0);
   if (!sched) return FA_ERR_CUDA;
   const PagedLayout& L = sched->layout;
   if (workspace_bytes < L.total) return FA_ERR_INVALID_ARG;

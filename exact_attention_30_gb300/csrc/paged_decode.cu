@@ -1407,22 +1407,23 @@ PagedLayout paged_layout(int B, int Hkv, int rows, int prefix_len, int d) {
 }
 
 PrefixPlan plan_prefix_beside(int B, int rows, int Hkv, int prefix_len, int d, int max_splits, int ctas, int sms,
-                              int own_keys) {
+                              int own_keys, bool narrow) {
   // Times in us, measured on a GB300. A prefix's CTA takes kStart and, per tile
   // of 128 keys, 1.76 (two tiles of query rows) or 1.05 (one), two thirds of
   // that at d = 64. An own keys' CTA beside it takes kOwnStart and per step (64
   // keys) 0.75, 0.6 at d = 64, 1.1 and 1.5 steps more per unit with more than 16
   // rows at d = 128, or what all such CTAs' bytes take at 6 GB/ms; one that finds
-  // its SM only after the prefix's costs kLate, in which the others go on. Each
+  // its SM only after the prefix's costs kLate, in which the others go on. Boxes
+  // of 8 rows: a third more per tile, twice as much per step. Each
   // key range is a partial result per row, written once and read once, four of
   // them in a round of the merge. The own keys are a guess: the plan is the one
   // with the least time for half, all and twice of them together.
   constexpr double kStart = 11.0, kOwnStart = 2.0, kLate = 3.0, kPartBytes = 4e6, kRound = 1.0;
   const bool wide = rows > 16 && d == 128;
-  const double kStep = wide ? 1.1 : d == 128 ? 0.75 : 0.6, kStepAll = 256.0 * d / 6e6;
+  const double kStep = (wide ? 1.1 : d == 128 ? 0.75 : 0.6) * (narrow ? 2 : 1), kStepAll = 256.0 * d / 6e6;
   const int n_kv = (int)(((long long)prefix_len + 127) / 128);
   const long long all_rows = (long long)B * rows, units = (all_rows + 255) / 256 * Hkv;
-  const double tile = (all_rows > 128 ? 1.76 : 1.05) * (d == 128 ? 1.0 : 0.67);
+  const double tile = (all_rows > 128 ? 1.76 : 1.05) * (d == 128 ? 1.0 : 0.67) * (narrow ? 1.33 : 1.0);
   const double own_units = (double)B * Hkv * (rows > 32 ? 2 : 1);
   const double part_us = (double)all_rows * Hkv * d * 8.0 / kPartBytes;
   PrefixPlan best{max_splits, 0, 0};
