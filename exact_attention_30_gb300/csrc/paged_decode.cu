@@ -1138,8 +1138,9 @@ struct RowSum {
       }
     }
   }
-  // Groups of `step` warps meet; the first of each has the row's sum afterwards.
-  __device__ __forceinline__ void meet(int warp, int step, int lane) {
+  // Groups of STEP warps meet; the first of each has the row's sum afterwards.
+  template <int STEP>
+  __device__ __forceinline__ void meet(int warp, int lane) {
     __shared__ float sm[kMergeWarps], sl[kMergeWarps], so[kMergeWarps][D];
 #pragma unroll
     for (int e = 0; e < E; ++e) so[warp][lane * E + e] = acc[e];
@@ -1147,25 +1148,21 @@ struct RowSum {
       sm[warp] = m;
       sl[warp] = l;
     }
-    named_bar(1 + warp / step, 32 * step);
-    if ((warp & (step - 1)) == 0) {
-      float ms[kMergeWarps];  // of the other slots: no part
-#pragma unroll
-      for (int w = 0; w < kMergeWarps; ++w) ms[w] = w < step ? sm[warp + (w & (step - 1))] : -INFINITY;
+    named_bar(1 + warp / STEP, 32 * STEP);
+    if (warp % STEP == 0) {
       m = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kMergeWarps; ++w) m = fmaxf(m, ms[w]);
+      for (int w = 0; w < STEP; ++w) m = fmaxf(m, sm[warp + w]);
       const float mu = m == -INFINITY ? 0.f : m;
       l = 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll
-      for (int w = 0; w < kMergeWarps; ++w) {
-        const int from = warp + (w & (step - 1));
-        const float f = ex2_approx(ms[w] - mu);
-        l = fmaf(sl[from], f, l);
+      for (int w = 0; w < STEP; ++w) {
+        const float f = ex2_approx(sm[warp + w] - mu);
+        l = fmaf(sl[warp + w], f, l);
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(so[from][lane * E + e], f, acc[e]);
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(so[warp + w][lane * E + e], f, acc[e]);
       }
     }
   }
@@ -1216,7 +1213,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_cut_kernel(const __gri
     P.own_n = at < 0 ? 0 : __shfl_sync(kFull, n, at & 31);
     RowSum<D, false> sum;
     sum.add(a, P, warp % STEP, STEP, lane);
-    if (STEP > 1) sum.meet(warp, STEP, lane);
+    if constexpr (decltype(STEP)::value > 1) sum.template meet<decltype(STEP)::value>(warp, lane);
     if (at >= 0 && warp % STEP == 0) {
       const int heads = a.pool.kv_heads << a.group_shift, b = P.unit / heads, h = P.unit - b * heads, head = h >> a.group_shift;
       const int r = (h - (head << a.group_shift)) * a.slot_rows + P.slot_row;
@@ -1266,7 +1263,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_prefix_kernel(const __
   if (P.own_n != 0 && !in_grid(c)) return;
   RowSum<D, true> sum;
   sum.add(a, P, warp % WPR, WPR, lane);
-  if constexpr (WPR > 1) sum.meet(warp, WPR, lane);
+  if constexpr (WPR > 1) sum.template meet<WPR>(warp, lane);
   if (warp % WPR == 0) sum.store(a, b, head, r, lane);
 }
 

@@ -381,6 +381,20 @@ def test_same_page_named_twice():
     _run(c, 4, 1, seed=31)
 
 
+@pytest.mark.parametrize("lens,g,prefix", [([9000, 40], 1, 0), ([3000] * 12, 8, 0), ([300] * 20, 4, 2000), ([200, 100], 4, 900)])
+def test_an_infinite_value_stays_infinite(lens, g, prefix):
+    """One infinite value among equal scores makes its column infinite, not NaN, whatever parts the row is merged of."""
+    c = Cache(lens, 2, 16, 128, seed=21, prefix=prefix)
+    q = torch.zeros((len(lens), 2 * g, 1, 128), dtype=torch.bfloat16, device="cuda")
+    for b, n in enumerate(lens):
+        c.v[int(c.tables[b, n // 2 // 16]), :, n // 2 % 16, 5] = -math.inf
+    o, lse = _call(c, q)
+    assert fa.fa_check_device_status() == fa.FA_OK
+    assert bool((o[..., 5] == -math.inf).all())
+    assert bool(torch.isfinite(o[..., :5]).all()) and bool(torch.isfinite(o[..., 6:]).all()) and bool(torch.isfinite(lse).all())
+
+
+
 def test_matches_the_dense_decode():
     B, H, nq, nk, d = 2, 3, 4, 500, 128
     c = Cache((nk,) * B, H, 16, d, seed=32)
