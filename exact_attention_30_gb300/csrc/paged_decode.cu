@@ -104,10 +104,10 @@ struct Cfg {
   static constexpr int CTAS = MT > 1 ? 1 : BESIDE ? 3 : 2;
   static constexpr int STAGES = (MT == 2 ? 4 : BESIDE ? 2 : 3) * (D == 128 ? 1 : 2);
   static_assert(!BESIDE || ROWS == 8, "registers");
-  // Queries as fragments in registers, or read from shared memory per tile
-  // (16 rows: 1% faster than in registers, which then spill; four groups
-  // leave 96 registers). FB: K or V fragments loaded at a time.
-  static constexpr bool Q_IN_SMEM = ROWS == 16;
+  // Queries as fragments in registers, or read from shared memory per tile (16
+  // rows, 32 at d = 128: 1 to 4% faster than in registers, which then spill).
+  // FB: K or V fragments loaded at a time.
+  static constexpr bool Q_IN_SMEM = ROWS == 16 || (ROWS == 32 && D == 128);
   static constexpr int FB = 4;
   static constexpr int QBUF = 16 * MT * D * 2;  // a unit's queries; two, one being filled for the next unit
   static constexpr int OFF_MERGE = STAGES * STAGE;
