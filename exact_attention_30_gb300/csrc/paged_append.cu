@@ -35,13 +35,16 @@ constexpr int kFewWarps = 512;
 constexpr int kManyTokens = 2048;
 constexpr unsigned kFull = 0xffffffffu;
 
-// Where packed token t belongs: the largest b with cu[b] <= t, its last new
-// token and its length. A 32-way search; its final round, over at most 32
-// sequences, brings all three at once (one round trip to memory for up to 32
-// sequences, two for up to 1024).
+// Where packed token t belongs: the largest b with cu[b] <= t, the first packed
+// token after its new ones and its length. A 32-way search; its final round,
+// over at most 32 sequences, brings all three at once (one round trip to memory
+// for up to 32 sequences, two for up to 1024). Where a sequence's offsets do not
+// lie within the tokens, none of these is its own (kNone): a wrong end would
+// move them over keys that are in the cache already.
 struct Place {
   int b, last, len;  // b = -1: cu[0] > t
 };
+constexpr int kNone = -1;  // as `last`: before every token
 __device__ __forceinline__ Place find_place(const AppendArgs& a, int t, int lane) {
   int lo = 0, hi = a.B;
   while (hi - lo > 32) {
@@ -57,7 +60,8 @@ __device__ __forceinline__ Place find_place(const AppendArgs& a, int t, int lane
   const unsigned m = __ballot_sync(kFull, lo + lane < hi && begin <= t);
   if (m == 0) return Place{-1, 0, 0};
   const int src = 31 - __clz(m);
-  return Place{lo + src, __shfl_sync(kFull, end, src), __shfl_sync(kFull, len, src)};
+  const int last = begin >= 0 && end <= a.total ? end : kNone;
+  return Place{lo + src, __shfl_sync(kFull, last, src), __shfl_sync(kFull, len, src)};
 }
 
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
@@ -150,8 +154,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     b = p.b;
     last = p.last;
     len = p.len;
-    if (b < 0) return;      // before the first sequence: reported above
-    if (t >= last) return;  // behind the last sequence: padding
+    if (b < 0) return;      // before the first sequence: padding
+    if (t >= last) return;  // behind the last sequence: padding; or its offsets are wrong, as reported above
   }
   if (len == 0) return;  // a padding sequence
   const long long pos = (long long)len - last + t;

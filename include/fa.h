@@ -374,8 +374,10 @@ typedef struct {
  * On the device: a token whose key index is negative or past max_pages pages,
  * whose page is outside the pool or whose position is outside
  * [0, max_positions) is skipped (its Qout row too) and reported like a bad
- * length above; so are inconsistent cu_seqlens (a sequence's offsets not
- * within 0 <= cu[b] <= cu[b+1] <= total).
+ * length above; so are all tokens of a sequence whose offsets are not within
+ * 0 <= cu_seqlens[b] <= cu_seqlens[b+1] <= total. (Where offsets decrease,
+ * tokens of other sequences may be left out as well; none is stored but at the
+ * key that its own sequence's offsets give it.)
  * Errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED (FA_F32, d, rot_dim,
  * page_size), FA_ERR_CUDA.
  */

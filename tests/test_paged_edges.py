@@ -1,0 +1,50 @@
+"""Paged-cache calls at the edge of what the header allows: offsets that do not fit the tokens."""
+import pytest
+import torch
+
+import exact_attention_30_gb300 as fa
+from paged_utils import Cache
+
+pytestmark = pytest.mark.gpu
+
+
+def _ends_behind(n, last_end):
+    """n sequences of one new token each, the last one's end moved."""
+    cu = list(range(n + 1))
+    cu[-1] = last_end
+    return cu
+
+
+@pytest.mark.parametrize("cu,total,lens", [
+    ([0, 2, 4, 7], 6, (30, 20, 10)),          # the last end behind the tokens: its keys would move by one
+    ([0, 2, 9, 9], 6, (30, 20, 10)),          # a sequence from the tokens to behind them, an empty one there
+    ([-1, 2, 4, 6], 6, (30, 20, 10)),         # a begin before the tokens
+    ([0, 2, 2, 1], 6, (30, 20, 10)),          # an end before its begin
+    (_ends_behind(40, 43), 40, (17,) * 40),   # more sequences than one round of the search
+    (_ends_behind(1100, 1101), 1100, (9,) * 1100),
+    ([0, 1500, 2401], 2400, (1501, 1000)),    # a warp for every token
+])
+def test_tokens_of_inconsistent_offsets_are_not_stored(cu, total, lens):
+    """A sequence whose offsets do not lie within the tokens is reported, and its cache and its rows of the queries
+    stay; the other sequences' tokens are stored where they belong."""
+    hq, hkv, d, page = 4, 2, 64, 16
+    c = Cache(lens, hkv, page, d, seed=len(lens), width_extra=1)
+    x = torch.randn((total, hq + 2 * hkv, d), generator=torch.Generator().manual_seed(total)).to(torch.bfloat16).cuda()
+    q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+    want_k, want_v = c.k.clone(), c.v.clone()
+    out = torch.full((total, hq, d), 3.0, dtype=torch.bfloat16, device="cuda")
+    want_q = out.clone()
+    tables = c.tables.cpu()
+    for b, n in enumerate(lens):
+        if not 0 <= cu[b] <= cu[b + 1] <= total:
+            continue
+        t = torch.arange(cu[b], cu[b + 1])
+        pos = n - cu[b + 1] + t
+        pages, rows = tables[b, pos // page].long().cuda(), (pos % page).cuda()
+        t = t.cuda()
+        want_k[pages, :, rows], want_v[pages, :, rows], want_q[t] = k[t], v[t], q[t]
+    fa.fa_kv_append(k, v, c.k, c.v, c.tables, c.seq_lens, torch.tensor(cu, dtype=torch.int32).cuda(), q=q, q_out=out)
+    assert fa.fa_check_device_status() == fa.FA_ERR_INVALID_ARG
+    assert fa.fa_check_device_status() == fa.FA_OK  # cleared
+    assert torch.equal(out, want_q)
+    assert torch.equal(c.k, want_k) and torch.equal(c.v, want_v)
