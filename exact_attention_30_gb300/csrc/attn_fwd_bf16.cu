@@ -171,6 +171,14 @@ __device__ __forceinline__ bool softmax_pass_own_p(uint32_t s_addr, uint32_t p_a
   return true;
 }
 
+// -m, what is added to the scaled scores of a row of maximum m. A prefix's rows
+// may have met nothing but scores of -inf yet (infinite keys): those have weight
+// zero, where -inf + inf would be NaN.
+template <bool PREFIX>
+__device__ __forceinline__ float minus_max(float m) {
+  return PREFIX && m == -INFINITY ? 0.f : -m;
+}
+
 template <int D, class Args>
 __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) fwd_bf16_kernel(const __grid_constant__ Args a) {
   using C = FwdCfg<D>;
@@ -568,7 +576,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) fwd_bf16_kernel(const _
         // S_j was issued before P_{j-1} V_{j-1}, which must have finished
         // reading P's columns before the first store.
         const uint32_t p_addr = lane_addr + C::P_COL(t);
-        const float neg_m = (j > 0) ? -m_ref : 0.f;
+        const float neg_m = (j > 0) ? minus_max<PREFIX>(m_ref) : 0.f;
         if (!softmax_pass_own_p<true>(s_addr, p_addr, mask_tile, valid, c22, f2_pack(neg_m, neg_m),
                                       mx, sm2, j > 0, BAR(B_ODONE + t), (uint32_t)(j - 1) & 1u,
                                       a.status, a.wait_limit_ns)) {
@@ -583,7 +591,8 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) fwd_bf16_kernel(const _
 #pragma unroll
           for (int u = 0; u < 4; ++u) sm2[u] = 0ull;
           tmem_st_wait();  // the speculative P is overwritten below
-          softmax_pass_own_p<false>(s_addr, p_addr, mask_tile, valid, c22, f2_pack(-m_new, -m_new),
+          const float neg_new = minus_max<PREFIX>(m_new);
+          softmax_pass_own_p<false>(s_addr, p_addr, mask_tile, valid, c22, f2_pack(neg_new, neg_new),
                                     mx, sm2, false, 0u, 0u, a.status, a.wait_limit_ns);
           m_ref = m_new;
         }
@@ -594,7 +603,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) fwd_bf16_kernel(const _
       } else {
         uint32_t pk[64];
         {
-          const float neg_m = (j > 0) ? -m_ref : 0.f;
+          const float neg_m = (j > 0) ? minus_max<PREFIX>(m_ref) : 0.f;
           const uint64_t nm2 = f2_pack(neg_m, neg_m);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -617,7 +626,8 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) fwd_bf16_kernel(const _
           // same values)
           const float m_new = need ? mt : m_ref;
           alpha = need ? ex2_approx(m_ref - m_new) : 1.f;
-          const uint64_t nm2 = f2_pack(-m_new, -m_new);
+          const float neg_new = minus_max<PREFIX>(m_new);
+          const uint64_t nm2 = f2_pack(neg_new, neg_new);
 #pragma unroll
           for (int u = 0; u < 4; ++u) sm2[u] = 0ull;
 #pragma unroll
@@ -685,7 +695,9 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) fwd_bf16_kernel(const _
       const int prow0 = (tail_unit * a.splits + part) * rows_unit + t * C::BM;  // tile's first workspace row
       if (ok) {
         tc_fence_after();
-        const float inv_l = 1.f / l;
+        // a key range whose scores are all -inf: output 0 (or what an infinite
+        // value times 0 is), log-sum-exp -inf
+        const float inv_l = PREFIX && l == 0.f ? 0.f : 1.f / l;
         uint8_t* stage = smem + C::OFF_Q + t * (D * 512);
 #pragma unroll
         for (int q = 0; q < D / 32; ++q) {

@@ -1,11 +1,20 @@
-"""Paged-cache calls at the edge of what the header allows: offsets that do not fit the tokens."""
+"""Paged-cache calls at the edge of what the header allows: offsets that do not fit the tokens, scores of -inf."""
+import math
+
+import numpy as np
 import pytest
 import torch
 
 import exact_attention_30_gb300 as fa
-from paged_utils import Cache
+from paged_utils import Cache, check_decode
 
 pytestmark = pytest.mark.gpu
+
+
+def _call(c, q):
+    if c.prefix:
+        return fa.fa_decode_shared(q, c.k, c.v, c.prefix_pages, c.prefix, c.tables, c.seq_lens)
+    return fa.fa_decode_paged(q, c.k, c.v, c.tables, c.seq_lens)
 
 
 def _ends_behind(n, last_end):
@@ -48,3 +57,47 @@ def test_tokens_of_inconsistent_offsets_are_not_stored(cu, total, lens):
     assert fa.fa_check_device_status() == fa.FA_OK  # cleared
     assert torch.equal(out, want_q)
     assert torch.equal(c.k, want_k) and torch.equal(c.v, want_v)
+
+
+class _WithoutInfiniteKeys(Cache):
+    """What is left of the keys where a row's score of every infinite one is -inf: their weights are zero."""
+
+    def keys_values(self, b, h):
+        k, v = super().keys_values(b, h)
+        finite = np.isfinite(k).all(1)
+        return k[finite], v[finite]
+
+    def spoil(self, table, first, last):
+        for j in range(first, last):
+            self.k[int(table[j // self.page]), :, j % self.page, 1] = math.inf
+
+
+@pytest.mark.parametrize("lens,g,prefix,spoiled,own_spoiled", [
+    # a prefix's kernel of its own, 80 rows a head: the only key of the last tile (and key range), the first
+    # tile, one between, several ranges, all of the prefix
+    ((60,) * 20, 4, 129, (128, 129), (0, 0)),
+    ((60,) * 20, 4, 300, (0, 128), (0, 0)),
+    ((60,) * 20, 4, 300, (128, 256), (0, 0)),
+    ((60,) * 20, 4, 1500, (100, 1100), (0, 0)),
+    ((60,) * 20, 4, 200, (0, 200), (0, 0)),
+    ((300,) * 40, 8, 1000, (0, 900), (0, 200)),  # 320 rows, and own keys
+    # the prefix as one more sequence, and none; rows of 8, 16, 32 and two units
+    ((200, 70), 4, 500, (0, 300), (0, 64)),
+    ((9000, 40), 4, 0, (0, 0), (0, 39)),
+    ((9000, 70), 12, 0, (0, 0), (3, 69)),
+    ((3000, 400), 24, 0, (0, 0), (0, 390)),
+    ((3000, 400), 40, 0, (0, 0), (0, 390)),
+])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_of_minus_infinity_have_no_weight(lens, g, prefix, spoiled, own_spoiled, d):
+    """Infinite keys whose scores are -inf in every row count as absent, also where a whole tile, a CTA's share or a
+    key range holds nothing else."""
+    c = _WithoutInfiniteKeys(lens, 2, 16, d, seed=d + prefix, prefix=prefix)
+    q = torch.randn((len(lens), 2 * g, 1, d), generator=torch.Generator().manual_seed(g)).to(torch.bfloat16).cuda()
+    q[..., 1] = -q[..., 1].abs() - 0.5
+    c.spoil(c.prefix_pages, *spoiled)
+    for b in range(len(lens)):
+        c.spoil(c.tables[b], *own_spoiled)
+    o, lse = _call(c, q)
+    assert fa.fa_check_device_status() == fa.FA_OK
+    check_decode(c, q, o, lse, 1 / math.sqrt(d), seqs=sorted({0, 1, len(lens) - 1}))
