@@ -37,7 +37,7 @@ __all__ = [
     "fa_bwd_varlen_workspace_bytes", "FA_CAUSAL", "fa_bwd_workspace_bytes", "fa_softmax_rows", "fa_decode",
     "fa_decode_workspace_bytes", "fa_decode_plan", "fa_check_device_status",
     "fa_rope_tables", "fa_kv_append", "fa_decode_paged", "fa_decode_paged_workspace_bytes",
-    "fa_decode_shared", "fa_decode_shared_workspace_bytes",
+    "fa_decode_shared", "fa_decode_shared_workspace_bytes", "fa_decode_shared_plan",
     "fa_debug_timeout_probe", "fa_status_string", "fa_version", "library_path", "load_library",
     "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "FA_ERR_TIMEOUT",
     "FA_F32", "FA_BF16", "FAError", "FA_BWD_PREPROCESS", "FA_BWD_MAIN", "FA_BWD_DQ_CONVERT",
@@ -93,6 +93,7 @@ _SIGNATURES = {
     "fa_decode_shared": (_ci, [_vp, _vp, _vp, _vp, _ci, _vp, _ci, _vp, _vp, _vp, _vp, _vp, _sz, _ci,
                                _ci, _ci, _cf, _ci, _vp]),
     "fa_decode_shared_workspace_bytes": (_sz, [_ci, _ci, _ci, _ci, _ci, _ci, _ci]),
+    "fa_decode_shared_plan": (_ci, [_ci] * 9 + [ctypes.POINTER(_ci)] * 2),
     "fa_check_device_status": (_ci, [_vp]),
     "fa_debug_timeout_probe": (_ci, [ctypes.c_longlong, _vp]),
     "fa_debug_fwd_skip_load": (_ci, [_vp] * 5 + [_ci, _ci, _ci, _ci, _cf, _ci, ctypes.c_longlong, _vp]),
@@ -562,6 +563,15 @@ def fa_decode_paged_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, d: int) 
 def fa_decode_shared_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, prefix_len: int, d: int) -> int:
     """Scratch bytes fa_decode_shared needs on the current device."""
     return int(load_library().fa_decode_shared_workspace_bytes(B, Hq, Hkv, Nq, prefix_len, d, FA_BF16))
+
+
+def fa_decode_shared_plan(B: int, Hq: int, Hkv: int, Nq: int, prefix_len: int, d: int, page_size: int, max_pages: int,
+                          sms: int = 0):
+    """(key ranges, CTAs) of the prefix's kernel in fa_decode_shared, (0, 0) if it has none; sms > 0 plans without a device."""
+    ranges, ctas = ctypes.c_int(0), ctypes.c_int(0)
+    _raise(load_library().fa_decode_shared_plan(B, Hq, Hkv, Nq, int(prefix_len), d, page_size, max_pages, int(sms),
+                                                ctypes.byref(ranges), ctypes.byref(ctas)), "fa_decode_shared_plan")
+    return ranges.value, ctas.value
 
 
 _decode_ws_bytes: dict = {}  # (device, sizes) -> bytes: what the library answered

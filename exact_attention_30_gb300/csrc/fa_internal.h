@@ -306,14 +306,17 @@ struct PagedLayout {
 // How a prefix's kernel and the own keys' kernel share the GPU: key ranges per
 // unit of the former (at most max_splits, which the scratch is laid out for),
 // and the CTAs of the latter that find an SM meanwhile, with the steps they take
-// in that time. rows = G * Nq; own_keys: an estimate of a sequence's own keys
-// (the lengths are on the device); narrow: boxes of 8 rows, which load slower.
+// in that time. rows = G * Nq; most_keys: own keys that a sequence's table can
+// hold (the lengths are on the device); narrow: boxes of 8 rows, which load slower.
 struct PrefixPlan {
   int splits, early_ctas, early_steps;
 };
 PrefixPlan plan_prefix_beside(int B, int rows, int Hkv, int prefix_len, int d, int max_splits, int ctas, int sms,
-                              int own_keys, bool narrow);
+                              int most_keys, bool narrow);
 PagedLayout paged_layout(int B, int Hkv, int rows, int prefix_len, int d);
+// The plan of a call (splits = 0: no kernel of the prefix's own; -1: the device
+// query failed) for a GPU of `sms` SMs, or the current one (0).
+PrefixPlan plan_shared(int B, int rows, int Hkv, int prefix_len, int d, int sms, int most_keys, bool narrow);
 cudaError_t launch_decode_paged_bf16(const PagedDecodeArgs& a, int d, cudaStream_t st);
 
 // Causal grids: (heads of a group, blocks, groups). Within a group of heads

@@ -77,34 +77,40 @@ bool view_strides(const long long* s, int B, int H, int N, int d, long long* sb,
   return true;
 }
 
+// Keys that a table of max_pages pages can hold.
+int most_keys(int max_pages, int page_size) {
+  const long long n = (long long)max_pages * page_size;
+  return n < kPagedMaxKeys ? (int)n : kPagedMaxKeys;
+}
+
 // Layout and plan of a decode, functions of its sizes and the device alone. A
 // decoding loop asks for the same ones again and again, and trying all numbers
 // of key ranges costs the host 2 us: each thread keeps its last.
 struct Schedule {
-  int dev, B, Hkv, rows, prefix_len, d, own_keys;
+  int dev, B, Hkv, rows, prefix_len, d, most;
   bool narrow;
   PagedLayout layout;
   PrefixPlan plan;
 };
-const Schedule* schedule(int B, int Hkv, int rows, int prefix_len, int d, int own_keys, bool narrow) {
+const Schedule* schedule(int B, int Hkv, int rows, int prefix_len, int d, int most, bool narrow) {
   thread_local Schedule last = {-1, 0, 0, 0, 0, 0, 0, false, {}, {}};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
   if (last.dev == dev && last.B == B && last.Hkv == Hkv && last.rows == rows && last.prefix_len == prefix_len &&
-      last.d == d && last.own_keys == own_keys && last.narrow == narrow)
+      last.d == d && last.most == most && last.narrow == narrow)
     return &last;
   last.dev = -1;
   last.layout = paged_layout(B, Hkv, rows, prefix_len, d);
   if (last.layout.ctas < 1) return nullptr;
   if (last.layout.pre_splits > 0)
-    last.plan = plan_prefix_beside(B, rows, Hkv, prefix_len, d, last.layout.pre_splits, last.layout.ctas, fwd_slots(), own_keys,
+    last.plan = plan_prefix_beside(B, rows, Hkv, prefix_len, d, last.layout.pre_splits, last.layout.ctas, fwd_slots(), most,
                                    narrow);
   last.B = B;
   last.Hkv = Hkv;
   last.rows = rows;
   last.prefix_len = prefix_len;
   last.d = d;
-  last.own_keys = own_keys;
+  last.most = most;
   last.narrow = narrow;
   last.dev = dev;
   return &last;
@@ -131,11 +137,8 @@ fa_status decode_impl(const void* Q, const long long* q_strides, const fa_paged_
   if (!view_strides(q_strides, B, Hq, Nq, cache->d, &a.q_b, &a.q_h, &a.q_r) ||
       !view_strides(o_strides, B, Hq, Nq, cache->d, &a.o_b, &a.o_h, &a.o_r))
     return FA_ERR_INVALID_ARG;
-  // a table is as wide as its longest sequence may get; a quarter of that is
-  // taken for what the sequences hold on average
-  const long long most = (long long)max_pages * cache->page_size;
-  const int own_keys = (int)(most < kPagedMaxKeys ? most : kPagedMaxKeys) / 4;
-  const Schedule* sched = schedule(B, cache->kv_heads, Hq / cache->kv_heads * Nq, prefix_len, cache->d, own_keys,
+  const int most = most_keys(max_pages, cache->page_size);
+  const Schedule* sched = schedule(B, cache->kv_heads, Hq / cache->kv_heads * Nq, prefix_len, cache->d, most,
                                    cache->page_size % 16 != 0);
   if (!sched) return FA_ERR_CUDA;
   const PagedLayout& L = sched->layout;
@@ -143,8 +146,8 @@ fa_status decode_impl(const void* Q, const long long* q_strides, const fa_paged_
   a.status = device_status_ptr();
   if (!a.status) return FA_ERR_CUDA;
   // boxes never cross a page's end, and a sequence's last one is loaded whole:
-  // short sequences (up to 512 keys by their table) get boxes of up to 16 rows
-  // (4 to 7% faster), others of up to 64 (3% faster than 16)
+  // sequences that their table keeps short (up to 512 keys) get boxes of up to 16
+  // rows (4 to 7% faster), others, which may be long, of up to 64 (3% faster than 16)
   const int most_shift = most <= 512 ? 4 : 6;
   while (a.box_shift < most_shift && cache->page_size % (2 << a.box_shift) == 0) ++a.box_shift;
   if (!encode_pool_bf16(&a.tmK, a.pool, false, cache->d, 1 << a.box_shift) ||
@@ -286,6 +289,21 @@ size_t fa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int Nq, int pref
 
 size_t fa_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, fa_dtype dt) {
   return fa_decode_shared_workspace_bytes(B, Hq, Hkv, Nq, 0, d, dt);
+}
+
+fa_status fa_decode_shared_plan(int B, int Hq, int Hkv, int Nq, int prefix_len, int d, int page_size, int max_pages,
+                                int sms, int* key_ranges, int* prefix_ctas) {
+  if (!key_ranges || !prefix_ctas || sms < 0 || page_size < 1 || max_pages < 1) return FA_ERR_INVALID_ARG;
+  const fa_status s = check_decode(B, Hq, Hkv, Nq, d, FA_BF16);
+  if (s != FA_OK) return s;
+  if (prefix_len < 0 || prefix_len > kPagedMaxKeys) return FA_ERR_INVALID_ARG;
+  if (page_size % 8 != 0 || page_size > kMaxPageSize) return FA_ERR_UNSUPPORTED;
+  const PrefixPlan p = plan_shared(B, Hq / Hkv * Nq, Hkv, prefix_len, d, sms, most_keys(max_pages, page_size),
+                                   page_size % 16 != 0);
+  if (p.splits < 0) return FA_ERR_CUDA;
+  *key_ranges = p.splits;
+  *prefix_ctas = (int)(((long long)B * (Hq / Hkv) * Nq + 255) / 256 * Hkv * p.splits);
+  return FA_OK;
 }
 
 fa_status fa_decode_paged(const void* Q, const long long* q_strides, const fa_paged_kv* cache,

@@ -1404,7 +1404,7 @@ PagedLayout paged_layout(int B, int Hkv, int rows, int prefix_len, int d) {
 }
 
 PrefixPlan plan_prefix_beside(int B, int rows, int Hkv, int prefix_len, int d, int max_splits, int ctas, int sms,
-                              int own_keys, bool narrow) {
+                              int most_keys, bool narrow) {
   // Times in us, measured on a GB300. A prefix's CTA takes kStart and, per tile
   // of 128 keys, 1.76 (two tiles of query rows) or 1.05 (one), two thirds of
   // that at d = 64. An own keys' CTA beside it takes kOwnStart and per step (64
@@ -1413,8 +1413,17 @@ PrefixPlan plan_prefix_beside(int B, int rows, int Hkv, int prefix_len, int d, i
   // its SM only after the prefix's costs kLate, in which the others go on. Boxes
   // of 8 rows: a third more per tile, twice as much per step. Each
   // key range is a partial result per row, written once and read once, four of
-  // them in a round of the merge. The own keys are a guess: the plan is the one
-  // with the least time for half, all and twice of them together.
+  // them in a round of the merge.
+  //
+  // How many own keys the sequences have is not known here, and the width of
+  // their table says little: it is the longest context a server allows, and a
+  // captured graph keeps its plan while they grow. So the plan is the one that
+  // loses least against each length's own best plan, over lengths from 32 to 2048
+  // keys as far as the table can hold them. (A quarter of the table's width taken
+  // for the length: 64 questions, 100 to 700 own keys, 75 us in a table of 768
+  // keys and 477 in one of 131072; now 75 in both. By the times above the loss
+  // is 2 to 4% in the mean over shapes, whatever the length.)
+  constexpr int kLengths[] = {32, 128, 512, 2048}, kMost = 4;
   constexpr double kStart = 11.0, kOwnStart = 2.0, kLate = 3.0, kPartBytes = 4e6, kRound = 1.0;
   const bool wide = rows > 16 && d == 128;
   const double kStep = (wide ? 1.1 : d == 128 ? 0.75 : 0.6) * (narrow ? 2 : 1), kStepAll = 256.0 * d / 6e6;
@@ -1423,8 +1432,13 @@ PrefixPlan plan_prefix_beside(int B, int rows, int Hkv, int prefix_len, int d, i
   const double tile = (all_rows > 128 ? 1.76 : 1.05) * (d == 128 ? 1.0 : 0.67) * (narrow ? 1.33 : 1.0);
   const double own_units = (double)B * Hkv * (rows > 32 ? 2 : 1);
   const double part_us = (double)all_rows * Hkv * d * 8.0 / kPartBytes;
-  PrefixPlan best{max_splits, 0, 0};
-  double best_us = -1;
+  int lengths[kMost], n_lengths = 0;
+  while (n_lengths < kMost && (n_lengths == 0 || kLengths[n_lengths] <= most_keys)) {
+    lengths[n_lengths] = std::min(kLengths[n_lengths], most_keys);
+    ++n_lengths;
+  }
+  PrefixPlan plans[kPrefixMaxSplits];
+  double us[kPrefixMaxSplits][kMost], least[kMost];
   for (int s = 1; s <= max_splits; ++s) {
     const long long waves = (units * s + sms - 1) / sms;
     const double pre_us = kStart + (double)waves * ((n_kv + s - 1) / s) * tile;
@@ -1432,20 +1446,48 @@ PrefixPlan plan_prefix_beside(int B, int rows, int Hkv, int prefix_len, int d, i
     const double step = early * kStepAll > kStep ? early * kStepAll : kStep;
     const int more = early > 0 ? (int)((pre_us + kLate - kOwnStart) / step) : 0;
     const int per_round = 4 * merge_warps(all_rows * Hkv, s);
-    double us = 3 * (s * part_us + (s + per_round) / per_round * kRound);
-    for (double guess = 0.5; guess <= 2; guess *= 2) {
-      const double steps = own_units * (guess * own_keys / 64.0 + kUnitSteps + (wide ? 2.0 : 0.5));
+    plans[s - 1] = PrefixPlan{s, early, more};
+    for (int i = 0; i < n_lengths; ++i) {
+      const double steps = own_units * (lengths[i] / 64.0 + kUnitSteps + (wide ? 2.0 : 0.5));
+      double& t = us[s - 1][i];
+      t = s * part_us + (s + per_round) / per_round * kRound;
       if (early > 0 && steps <= early * (double)more)
-        us += std::max(pre_us, kOwnStart + steps / early * step);
+        t += std::max(pre_us, kOwnStart + steps / early * step);
       else
-        us += pre_us + kLate + (steps - early * (double)more) * kStepAll;
-    }
-    if (best_us < 0 || us < best_us) {
-      best_us = us;
-      best = PrefixPlan{s, early, more};
+        t += pre_us + kLate + (steps - early * (double)more) * kStepAll;
+      least[i] = s == 1 ? t : std::min(least[i], t);
     }
   }
-  return best;
+  int best = 0;
+  double best_loss = -1;
+  for (int s = 0; s < max_splits; ++s) {
+    double loss = 0;
+    for (int i = 0; i < n_lengths; ++i) loss += us[s][i] / least[i];
+    if (best_loss < 0 || loss < best_loss) {
+      best_loss = loss;
+      best = s;
+    }
+  }
+  return plans[best];
+}
+
+PrefixPlan plan_shared(int B, int rows, int Hkv, int prefix_len, int d, int sms, int most_keys, bool narrow) {
+  int max_splits, ctas;
+  if (sms == 0) {
+    const PagedLayout L = paged_layout(B, Hkv, rows, prefix_len, d);
+    if (L.ctas < 1) return PrefixPlan{-1, 0, 0};
+    max_splits = L.pre_splits;
+    ctas = L.ctas;
+    sms = fwd_slots();
+  } else {
+    const long long all_rows = (long long)B * rows;
+    max_splits = prefix_len > 0 && all_rows > kGridPrefixRows
+                     ? plan_prefix_splits((all_rows + 255) / 256 * Hkv, (int)(((long long)prefix_len + 127) / 128), sms)
+                     : 0;
+    ctas = sms * (rows <= 8 ? Cfg<128, 8, 1>::CTAS : rows <= 16 ? Cfg<128, 16, 0>::CTAS : Cfg<128, 32, 0>::CTAS);
+  }
+  if (max_splits < 1) return PrefixPlan{0, 0, 0};
+  return plan_prefix_beside(B, rows, Hkv, prefix_len, d, max_splits, ctas, sms, most_keys, narrow);
 }
 
 cudaError_t launch_decode_paged_bf16(const PagedDecodeArgs& a, int d, cudaStream_t st) {

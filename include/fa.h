@@ -450,6 +450,21 @@ size_t fa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int Nq, int pref
                                         fa_dtype dt);
 
 /*
+ * How fa_decode_shared shares a GPU between the prefix and the own keys: a
+ * prefix of more than 32 rows (B * G * Nq) runs as a kernel of its own, of
+ * *prefix_ctas CTAs (one per SM), its keys cut into *key_ranges ranges; the own
+ * keys take the other SMs meanwhile, and all SMs afterwards. 0 and 0 without
+ * such a kernel. The own keys' lengths are on the device, so this choice, which
+ * a captured graph keeps, is made for any of them: of the table's size it only
+ * uses that sequences cannot be longer (from 2048 keys on, nothing). sms > 0
+ * plans for a GPU of that many SMs (no device access); sms == 0: the current
+ * device. FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED as fa_decode_shared;
+ * FA_ERR_CUDA if the device query fails.
+ */
+fa_status fa_decode_shared_plan(int B, int Hq, int Hkv, int Nq, int prefix_len, int d, int page_size,
+                                int max_pages, int sms, int* key_ranges, int* prefix_ctas);
+
+/*
  * fa_bwd without a caller-provided workspace, for callers that cannot
  * allocate device memory (for example code running inside a host application
  * that owns all device memory through its own pool, or a serving path where

@@ -1,4 +1,4 @@
-"""Paged-cache calls at the edge of what the header allows: offsets that do not fit the tokens, scores of -inf."""
+"""Paged-cache calls at the edge of what the header allows: offsets that do not fit the tokens, scores of -inf, wide tables."""
 import math
 
 import numpy as np
@@ -101,3 +101,30 @@ def test_scores_of_minus_infinity_have_no_weight(lens, g, prefix, spoiled, own_s
     o, lse = _call(c, q)
     assert fa.fa_check_device_status() == fa.FA_OK
     check_decode(c, q, o, lse, 1 / math.sqrt(d), seqs=sorted({0, 1, len(lens) - 1}))
+
+
+@pytest.mark.parametrize("lens,g,nq,prefix", [((5, 0, 300), 4, 1, 0), ((5, 0, 300), 4, 2, 90), ((90, 0, 700) * 10, 4, 1, 2500),
+                                              ((40,) * 33, 8, 1, 700)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_tables_far_wider_than_the_sequences(lens, g, nq, prefix, d):
+    """Tables as wide as a server's longest context, eager and captured, one sequence grown past the others since."""
+    c = Cache(lens, 2, 16, d, seed=d + len(lens), prefix=prefix, width_extra=8192)
+    c.poison()
+    q = torch.randn((len(lens), 2 * g, nq, d), generator=torch.Generator().manual_seed(g)).to(torch.bfloat16).cuda()
+    seqs = sorted({0, 1, 2, len(lens) - 1})
+    o, lse = _call(c, q)
+    assert fa.fa_check_device_status() == fa.FA_OK
+    check_decode(c, q, o, lse, 1 / math.sqrt(d), seqs=seqs)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = _call(c, q)
+    # sequence 1 now names the pages of sequence 2, twice over
+    n = -(-c.lens[2] // c.page)
+    c.tables[1, :n] = c.tables[2, :n]
+    c.tables[1, n:2 * n] = c.tables[2, :n]
+    c.lens[1] = c.lens[2] // c.page * c.page
+    c.seq_lens[1] = c.lens[1]
+    graph.replay()
+    assert fa.fa_check_device_status() == fa.FA_OK
+    check_decode(c, q, o, lse, 1 / math.sqrt(d), seqs=seqs)
