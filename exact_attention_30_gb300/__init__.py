@@ -450,6 +450,13 @@ def _refuse(t, name: str, device: int, dtype, what: str):
                      f"it is {tuple(t.shape)}, {t.dtype}, on {t.device}")
 
 
+def _int32(n: int, name: str) -> int:
+    """n, which the library takes as a C int; ctypes would cut it to 32 bits without a word."""
+    if not -(1 << 31) <= n < 1 << 31:
+        raise ValueError(f"{name} = {n} does not fit 32 bits")
+    return n
+
+
 def _is(t, dtype, device: int) -> bool:
     """Whether t is a tensor of ``dtype`` on CUDA device ``device``."""
     return isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == device
@@ -466,6 +473,7 @@ def _paged_cache(k_pages, v_pages, block_tables, seq_lens):
     if not _is(block_tables, _I32, dev) or block_tables.dim() != 2 or not block_tables.is_contiguous():
         _refuse(block_tables, "block_tables", dev, _I32, "a contiguous [B, max_pages]")
     B, max_pages = block_tables.shape
+    _int32(max_pages, "the width of block_tables")
     if not _is(seq_lens, _I32, dev) or seq_lens.shape != (B,) or not seq_lens.is_contiguous():
         _refuse(seq_lens, "seq_lens", dev, _I32, "a contiguous [B]")
     k0, k1, k2, k3 = k_pages.stride()
@@ -562,6 +570,7 @@ def fa_decode_paged_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, d: int) 
 
 def fa_decode_shared_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, prefix_len: int, d: int) -> int:
     """Scratch bytes fa_decode_shared needs on the current device."""
+    prefix_len = _int32(int(prefix_len), "prefix_len")
     return int(load_library().fa_decode_shared_workspace_bytes(B, Hq, Hkv, Nq, prefix_len, d, FA_BF16))
 
 
@@ -569,7 +578,8 @@ def fa_decode_shared_plan(B: int, Hq: int, Hkv: int, Nq: int, prefix_len: int, d
                           sms: int = 0):
     """(key ranges, CTAs) of the prefix's kernel in fa_decode_shared, (0, 0) if it has none; sms > 0 plans without a device."""
     ranges, ctas = ctypes.c_int(0), ctypes.c_int(0)
-    _raise(load_library().fa_decode_shared_plan(B, Hq, Hkv, Nq, int(prefix_len), d, page_size, max_pages, int(sms),
+    prefix_len, max_pages = _int32(int(prefix_len), "prefix_len"), _int32(max_pages, "max_pages")
+    _raise(load_library().fa_decode_shared_plan(B, Hq, Hkv, Nq, prefix_len, d, page_size, max_pages, int(sms),
                                                 ctypes.byref(ranges), ctypes.byref(ctas)), "fa_decode_shared_plan")
     return ranges.value, ctas.value
 
@@ -677,7 +687,7 @@ def fa_decode_shared(q, k_pages, v_pages, prefix_pages, prefix_len: int, block_t
     own keys, which follow the prefix. Returns (O like q, LSE [B, Hq, Nq] float32).
     """
     scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else float(scale)
-    prefix_len = int(prefix_len)
+    prefix_len = _int32(int(prefix_len), "prefix_len")
     if prefix_len > 0 and prefix_pages is None:
         raise ValueError("prefix_pages is missing")
     return _decode_cache("fa_decode_shared", q, k_pages, v_pages, prefix_pages, prefix_len, block_tables, seq_lens,

@@ -1,4 +1,5 @@
-"""Paged-cache calls at the edge of what the header allows: offsets that do not fit the tokens, scores of -inf, wide tables."""
+"""Paged-cache calls at the edge of what the header allows: offsets that do not fit the tokens, scores of -inf, wide tables, sizes
+past 32 bits."""
 import math
 
 import numpy as np
@@ -128,3 +129,22 @@ def test_tables_far_wider_than_the_sequences(lens, g, nq, prefix, d):
     graph.replay()
     assert fa.fa_check_device_status() == fa.FA_OK
     check_decode(c, q, o, lse, 1 / math.sqrt(d), seqs=seqs)
+
+
+def test_sizes_past_32_bits_are_refused():
+    """A prefix length and a table's width that 32 bits would cut to small ones of the same call (2^32 + 20, 2^32 + 1)."""
+    c = Cache((20, 5), 2, 16, 64, seed=34, prefix=20)
+    q = torch.randn((2, 4, 1, 64), device="cuda").to(torch.bfloat16)
+    pages = torch.zeros((1 << 16) + 1, dtype=torch.int32, device="cuda")
+    pool = torch.zeros((1, 2, 1 << 16, 64), dtype=torch.bfloat16, device="cuda")
+    for n in ((1 << 32) + 20, 1 << 31):
+        with pytest.raises(ValueError, match="32 bits"):
+            fa.fa_decode_shared(q, pool, pool.clone(), pages, n, c.tables, c.seq_lens)
+    with pytest.raises(fa.FAError):  # within 32 bits, past what the library takes
+        fa.fa_decode_shared(q, pool, pool.clone(), pages, (1 << 30) + 1, c.tables, c.seq_lens)
+    wide = torch.empty((1, (1 << 32) + 1), dtype=torch.int32, device="cuda")
+    k = torch.zeros((1, 2, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="32 bits"):
+        fa.fa_decode_paged(q[:1], c.k, c.v, wide, c.seq_lens[:1])
+    with pytest.raises(ValueError, match="32 bits"):
+        fa.fa_kv_append(k, k, c.k, c.v, wide, c.seq_lens[:1])

@@ -71,3 +71,10 @@ def test_plan_refusals(kw, code):
     with pytest.raises(fa.FAError) as e:
         _plan(**{**dict(B=4, hq=8, hkv=4, nq=1, prefix=500, d=128, table_keys=100), **kw})
     assert e.value.code == code
+
+
+def test_lengths_past_32_bits_are_refused():
+    with pytest.raises(ValueError, match="32 bits"):
+        _plan(4, 8, 4, 1, (1 << 32) + 500, 128, 100)
+    with pytest.raises(ValueError, match="32 bits"):
+        fa.fa_decode_shared_workspace_bytes(4, 8, 4, 1, (1 << 32) + 500, 128)
