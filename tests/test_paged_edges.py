@@ -1,5 +1,5 @@
 """Paged-cache calls at the edge of what the header allows: offsets that do not fit the tokens, scores of -inf, wide tables, sizes
-past 32 bits."""
+past 32 bits, small boxes, the plain entry of the library, padding in front, captured branches."""
 import math
 
 import numpy as np
@@ -148,3 +148,96 @@ def test_sizes_past_32_bits_are_refused():
         fa.fa_decode_paged(q[:1], c.k, c.v, wide, c.seq_lens[:1])
     with pytest.raises(ValueError, match="32 bits"):
         fa.fa_kv_append(k, k, c.k, c.v, wide, c.seq_lens[:1])
+
+
+
+
+
+@pytest.mark.parametrize("page", [8, 24, 40, 200])
+@pytest.mark.parametrize("B,g,nq,prefix", [(20, 4, 1, 700), (40, 8, 2, 333), (9, 5, 3, 1000)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefix_of_many_rows_in_pages_of_odd_multiples_of_8(B, g, nq, prefix, page, d):
+    """Boxes of 8 rows in the prefix's kernel."""
+    lens = np.random.default_rng(page + B).integers(0, 90, B).tolist()
+    c = Cache(lens, 2, page, d, seed=B + page, prefix=prefix, rows_first=page == 24)
+    c.poison()
+    q = torch.randn((B, 2 * g, nq, d), generator=torch.Generator().manual_seed(page)).to(torch.bfloat16).cuda()
+    o, lse = _call(c, q)
+    assert fa.fa_check_device_status() == fa.FA_OK
+    check_decode(c, q, o, lse, 1 / math.sqrt(d), seqs=sorted({0, 1, B // 2, B - 1}))
+
+
+
+@pytest.mark.parametrize("lens,g,nq", [((70, 0, 300), 4, 1), ((900, 33), 5, 3), ((200, 65), 16, 4)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_entry_without_a_prefix(lens, g, nq, d):
+    """fa_decode_paged of the library itself, dense and strided, gives the bits of fa_decode_shared without a prefix."""
+    lib = fa.load_library()
+    hkv, B, hq = 2, len(lens), 2 * g
+    c = Cache(lens, hkv, 16, d, seed=nq + d)
+    q = torch.randn((B, hq, nq, d), generator=torch.Generator().manual_seed(g)).to(torch.bfloat16).cuda()
+    want, want_lse = fa.fa_decode_shared(q, c.k, c.v, None, 0, c.tables, c.seq_lens, scale=0.1)
+    pool = fa._pack_pool(c.k.data_ptr(), c.v.data_ptr(), c.pages, hkv, c.page, d, *c.k.stride()[:3], *c.v.stride()[:3])
+    n = fa.fa_decode_paged_workspace_bytes(B, hq, hkv, nq, d)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    q_rows = torch.zeros((B, nq, hq + 3, d), dtype=torch.bfloat16, device="cuda")
+    q_rows[:, :, :hq] = q.transpose(1, 2)
+    o_rows = torch.full_like(q_rows, 7.0)
+    strides = lambda t: fa._pack_strides(t.stride(0), t.stride(2), t.stride(1))
+    o = torch.empty_like(q)
+    for query, q_strides, out, o_strides in ((q, None, o, None), (q_rows, strides(q_rows), o_rows, strides(o_rows))):
+        lse = torch.empty((B, hq, nq), dtype=torch.float32, device="cuda")
+        assert lib.fa_decode_paged(query.data_ptr(), q_strides, pool, c.tables.data_ptr(), c.tables.shape[1],
+                                   c.seq_lens.data_ptr(), out.data_ptr(), o_strides, lse.data_ptr(), ws.data_ptr(), n,
+                                   B, hq, nq, 0.1, fa.FA_BF16, torch.cuda.current_stream().cuda_stream) == fa.FA_OK
+        assert fa.fa_check_device_status() == fa.FA_OK
+        assert torch.equal(lse, want_lse)
+    assert torch.equal(o, want)
+    assert torch.equal(o_rows[:, :, :hq].transpose(1, 2), want) and bool((o_rows[:, :, hq:] == 7.0).all())
+
+
+
+def test_tokens_before_the_first_offset_are_padding():
+    """Offsets that begin past the first packed token: what stands before them is left alone, like what stands behind."""
+    lens, hq, hkv, d = (20, 9), 4, 2, 64
+    c = Cache(lens, hkv, 16, d, seed=3)
+    x = torch.randn((9, hq + 2 * hkv, d), generator=torch.Generator().manual_seed(4)).to(torch.bfloat16).cuda()
+    q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+    want_k, want_v = c.k.clone(), c.v.clone()
+    out = torch.full((9, hq, d), 3.0, dtype=torch.bfloat16, device="cuda")
+    for t, b, pos in ((2, 0, 17), (3, 0, 18), (4, 0, 19), (5, 1, 7), (6, 1, 8)):
+        page = int(c.tables[b, pos // 16])
+        want_k[page, :, pos % 16], want_v[page, :, pos % 16] = k[t], v[t]
+    fa.fa_kv_append(k, v, c.k, c.v, c.tables, c.seq_lens, torch.tensor([2, 5, 7], dtype=torch.int32).cuda(), q=q, q_out=out)
+    assert fa.fa_check_device_status() == fa.FA_OK
+    assert torch.equal(out[2:7], q[2:7]) and bool((out[:2] == 3.0).all()) and bool((out[7:] == 3.0).all())
+    assert torch.equal(c.k, want_k) and torch.equal(c.v, want_v)
+
+
+@pytest.mark.parametrize("prefix", [0, 900])
+def test_captured_branches_and_copies(prefix):
+    """Calls captured behind a copy of their lengths, in two branches at once, and behind both branches."""
+    lens = (100, 33, 70) * 10
+    c = Cache(lens, 2, 16, 64, seed=50 + prefix, prefix=prefix)
+    q = torch.randn((30, 8, 1, 64), generator=torch.Generator().manual_seed(51)).to(torch.bfloat16).cuda()
+    want, want_lse = _call(c, q)
+    check_decode(c, q, want, want_lse, 1 / 8, seqs=(0, 1, 29))
+    right, side = c.seq_lens.clone(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph, got = torch.cuda.CUDAGraph(), []
+    with torch.cuda.graph(graph):
+        c.seq_lens.copy_(right)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            got += [_call(c, q), _call(c, q)]
+        got += [_call(c, q), _call(c, q)]
+        torch.cuda.current_stream().wait_stream(side)
+        got.append(_call(c, q))
+    for _ in range(3):
+        c.seq_lens.fill_(1)
+        for o, lse in got:
+            o.fill_(9.0)
+        graph.replay()
+        assert fa.fa_check_device_status() == fa.FA_OK
+        for o, lse in got:
+            assert torch.equal(o, want) and torch.equal(lse, want_lse)
