@@ -511,8 +511,8 @@ def fa_kv_append(k, v, k_pages, v_pages, block_tables, seq_lens, cu_seqlens=None
 
     k, v: [total, Hkv, d] bf16 packed new tokens (a slice of a fused projection
     will do); q: [total, Hq, d] or None. cu_seqlens: int32 [B+1] offsets of the
-    sequences' new tokens (None: total / B tokens each). seq_lens: int32 [B]
-    lengths after this append. cos, sin: float32 [max_positions, rot_dim / 2]
+    sequences' new tokens (None: total / B tokens each); tokens outside all of
+    them are padding. seq_lens: int32 [B] lengths after this append. cos, sin: float32 [max_positions, rot_dim / 2]
     (None: no rotation). positions: int32 [total] rotary positions (None: the
     key's index in the cache). k_pages and v_pages are written in place.
     Returns the rotated queries (``q_out``, dense unless given), or None without q.
@@ -592,8 +592,8 @@ _SCRATCH_KEPT_BYTES = 64 << 20
 def _decode_workspace(lib, key, device, stream: int):
     """Scratch for one call. Calls on the default stream (which is never
     captured and runs one after another) reuse one tensor per thread and device:
-    allocating and freeing it took 5 of a call's 23 us. Other streams, and calls
-    that need much, get their own."""
+    allocating and freeing it took 5 of a call's 23 us. It is given back when the
+    thread ends. Other streams, and calls that need more than 64 MB, get their own."""
     n = _decode_ws_bytes.get(key)
     if n is None:
         n = _decode_workspace_size(lib, key)
@@ -682,8 +682,8 @@ def fa_decode_shared(q, k_pages, v_pages, prefix_pages, prefix_len: int, block_t
                      scale: float | None = None, out=None, lse=None, workspace=None):
     """``fa_decode_paged`` for a batch whose sequences all continue one prefix.
 
-    prefix_pages: int32 [ceil(prefix_len / page_size)] pages of the prefix, read
-    once for the whole batch; block_tables and seq_lens describe the sequences'
+    prefix_pages: int32 [ceil(prefix_len / page_size)] pages of the prefix, loaded
+    once per 256 query rows of a K/V head; block_tables and seq_lens describe the sequences'
     own keys, which follow the prefix. Returns (O like q, LSE [B, Hq, Nq] float32).
     """
     scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else float(scale)

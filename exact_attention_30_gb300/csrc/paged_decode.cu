@@ -32,16 +32,18 @@
 // piece ends. Bytes bound this kernel (4 d bytes per key against 4 d R flops):
 // with keys split over warps the warp-level mma.sync needs no barrier and no
 // tensor-memory round trip per tile, which is what a short cache's latency
-// consists of, and its rate is far from the limit up to 32 rows. Two CTAs share
-// an SM (up to 16 rows), one loading while the other one merges.
+// consists of. Up to 16 rows its rate is far from the limit, and two CTAs share an
+// SM, one loading while the other one merges; with 17 to 32 a tile's products take
+// 1.0 us against 0.73 for its bytes, and they bound the kernel.
 //
 // Measured on a GB300, GPU time of a call: 8 sequences of 32768 keys (8 heads,
 // 8 queries each, d = 128) 163 us, 6.6 TB/s, 97% of a copy's rate; 48 of 100
 // to 9000 keys (8 heads, 4 queries each) 77 us, 6.1 TB/s. The same kernel
 // that loads and does not compute takes 162 and 77: loads, not products, bound
 // long caches. 20 sequences of 333 to 4097 keys (16 heads, 4 new tokens,
-// d = 64) 27 us against 18 for the bytes, and one of 701 keys 7.6 us: about 4 us
-// of the chain length - page - keys and 2 us of merge.
+// d = 64) 26 us against 18 for the bytes; without arithmetic as well, so it is the
+// loading that is slow there (4.7 TB/s). One sequence of 701 keys 7.4 us: about
+// 4 us of the chain length - page - keys and 2 us of merge.
 //
 // More than 32 rows are two units, the second of which finds the keys in L2: 32
 // units of 16384 keys 95 us with 64 rows, 54 with 32, 51 with 16, 47 with 4.

@@ -355,10 +355,10 @@ typedef struct {
  *               rotated copy (tokens qout_stride apart; may be Q itself with
  *               the same stride); both NULL and Hq = 0: keys and values only.
  *   cu_seqlens: DEVICE int32 [B+1]: sequence b's new tokens are the packed
- *               tokens cu_seqlens[b] .. cu_seqlens[b+1]-1. Packed tokens from
- *               cu_seqlens[B] on are padding: what they hold does not
- *               matter, and nothing is written for them (nor their rows of
- *               Qout). NULL: every sequence has total / B (exactly) tokens.
+ *               tokens cu_seqlens[b] .. cu_seqlens[b+1]-1. Packed tokens
+ *               before cu_seqlens[0] and from cu_seqlens[B] on are padding:
+ *               what they hold does not matter, and nothing is written for
+ *               them (nor their rows of Qout). NULL: every sequence has total / B (exactly) tokens.
  *   seq_lens  : the sequences' lengths AFTER this append (what the attention
  *               calls then take): new token i of n goes to key
  *               seq_lens[b] - n + i. seq_lens[b] = 0 marks a padding
@@ -397,11 +397,14 @@ fa_status fa_kv_append(const void* K, const void* V, long long k_stride, long lo
  * gets O = 0 and LSE = -inf. What stands in the pages behind a sequence's
  * last key, NaN included, and in keys and values a query does not see has no
  * influence on its row.
- * The query heads h * Hq/Hkv .. (h + 1) * Hq/Hkv - 1 share K/V head h, which
- * is read once for all of them: G * Nq <= 64 rows, G = Hq / Hkv.
+ * The query heads h * Hq/Hkv .. (h + 1) * Hq/Hkv - 1 share K/V head h, whose
+ * keys and values are loaded once for up to 32 rows (query heads times new
+ * tokens), twice for more, the second time mostly from L2: G * Nq <= 64 rows,
+ * G = Hq / Hkv.
+ * A key whose score is -inf has weight zero, also where a row sees no other.
  *   Q   : [B,Hq,Nq,d] bf16; q_strides: NULL (dense) or 3 HOST values, the
- *         element strides of batch, head and row, multiples of 8 (of an axis
- *         of extent 1: ignored); 16-byte aligned.
+ *         element strides of batch, head and row, multiples of 8 and >= d (of
+ *         an axis of extent 1: ignored); 16-byte aligned.
  *   O   : as Q, o_strides likewise; must not overlap Q or the cache.
  *   LSE : [B,Hq,Nq] float32, dense (natural log, as fa_fwd).
  *   workspace : device scratch of >= fa_decode_paged_workspace_bytes() bytes,
@@ -409,8 +412,9 @@ fa_status fa_kv_append(const void* K, const void* V, long long k_stride, long lo
  *         call in flight.
  * The keys of all sequences and heads are laid end to end and cut into equal
  * shares, one per resident CTA, on the device: lengths may change between
- * replays of a captured graph. Sums in fp32; results are the same on every
- * run. 1 <= B * Hkv <= 2^24, seq_lens[b] <= 2^30.
+ * replays of a captured graph. Scores, maxima and sums in fp32; each weight is
+ * rounded to bf16 once for its product with the values (the sum of weights takes
+ * it unrounded), O once at the end. Results are the same on every run. 1 <= B * Hkv <= 2^24, seq_lens[b] <= 2^30.
  * Errors: FA_ERR_INVALID_ARG (pointers, sizes, Hq not a multiple of Hkv,
  * strides, scale, small workspace), FA_ERR_UNSUPPORTED (FA_F32, d,
  * page_size, G * Nq > 64), FA_ERR_CUDA.
@@ -431,8 +435,9 @@ size_t fa_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, fa
  * page_size) - 1] (DEVICE int32), then its own sequence's keys as in
  * fa_decode_paged. block_tables and seq_lens describe the sequences' OWN keys
  * only (their key 0 follows the prefix; a prefix may end inside a page, the
- * rest of which is not read). The prefix is read once for the whole batch and
- * its partial result is merged with the own keys' by maximum and sum.
+ * rest of which is not read). The prefix is loaded once per K/V head and 256
+ * query rows of the batch (B * G * Nq; further blocks of 256 mostly find it in
+ * L2), and its partial result is merged with the own keys' by maximum and sum.
  *   prefix_len : HOST value, 0 <= prefix_len <= 2^30 (0: fa_decode_paged).
  *   workspace  : >= fa_decode_shared_workspace_bytes() bytes, as above.
  * Limits and errors: as fa_decode_paged, plus FA_ERR_INVALID_ARG for a
