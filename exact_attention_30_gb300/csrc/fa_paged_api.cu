@@ -293,7 +293,7 @@ size_t fa_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, fa
 
 fa_status fa_decode_shared_plan(int B, int Hq, int Hkv, int Nq, int prefix_len, int d, int page_size, int max_pages,
                                 int sms, int* key_ranges, int* prefix_ctas) {
-  if (!key_ranges || !prefix_ctas || sms < 0 || page_size < 1 || max_pages < 1) return FA_ERR_INVALID_ARG;
+  if (!key_ranges || !prefix_ctas || sms < 0 || sms > 65536 || page_size < 1 || max_pages < 1) return FA_ERR_INVALID_ARG;
   const fa_status s = check_decode(B, Hq, Hkv, Nq, d, FA_BF16);
   if (s != FA_OK) return s;
   if (prefix_len < 0 || prefix_len > kPagedMaxKeys) return FA_ERR_INVALID_ARG;

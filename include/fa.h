@@ -462,8 +462,8 @@ size_t fa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int Nq, int pref
  * such a kernel. The own keys' lengths are on the device, so this choice, which
  * a captured graph keeps, is made for any of them: of the table's size it only
  * uses that sequences cannot be longer (from 2048 keys on, nothing). sms > 0
- * plans for a GPU of that many SMs (no device access); sms == 0: the current
- * device. FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED as fa_decode_shared;
+ * plans for a GPU of that many SMs, 65536 at most (no device access); sms == 0:
+ * the current device. FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED as fa_decode_shared;
  * FA_ERR_CUDA if the device query fails.
  */
 fa_status fa_decode_shared_plan(int B, int Hq, int Hkv, int Nq, int prefix_len, int d, int page_size,

@@ -73,6 +73,16 @@ def test_plan_refusals(kw, code):
     assert e.value.code == code
 
 
+def test_a_gpu_of_too_many_sms_is_refused():
+    """The plan counts three CTAs on each SM in 32 bits."""
+    ranges, ctas = _plan(40, 8, 4, 1, 5000, 128, 100, sms=65536)  # 80 rows: one block of 256 for each of 4 heads
+    assert 1 <= ranges <= 40 and ctas == 4 * ranges
+    with pytest.raises(fa.FAError):
+        _plan(40, 8, 4, 1, 5000, 128, 100, sms=65537)
+    with pytest.raises(fa.FAError):
+        _plan(40, 8, 4, 1, 5000, 128, 100, sms=(1 << 31) - 1)
+
+
 def test_lengths_past_32_bits_are_refused():
     with pytest.raises(ValueError, match="32 bits"):
         _plan(4, 8, 4, 1, (1 << 32) + 500, 128, 100)
