@@ -38,6 +38,7 @@ __all__ = [
     "fa_decode_workspace_bytes", "fa_decode_plan", "fa_check_device_status",
     "fa_rope_tables", "fa_kv_append", "fa_decode_paged", "fa_decode_paged_workspace_bytes",
     "fa_decode_shared", "fa_decode_shared_workspace_bytes", "fa_decode_shared_plan",
+    "fa_prompt_fwd", "fa_prompt_paged", "fa_prompt_fwd_workspace_bytes",
     "fa_debug_timeout_probe", "fa_status_string", "fa_version", "library_path", "load_library",
     "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "FA_ERR_TIMEOUT",
     "FA_F32", "FA_BF16", "FAError", "FA_BWD_PREPROCESS", "FA_BWD_MAIN", "FA_BWD_DQ_CONVERT",
@@ -94,6 +95,11 @@ _SIGNATURES = {
                                _ci, _ci, _cf, _ci, _vp]),
     "fa_decode_shared_workspace_bytes": (_sz, [_ci, _ci, _ci, _ci, _ci, _ci, _ci]),
     "fa_decode_shared_plan": (_ci, [_ci] * 9 + [ctypes.POINTER(_ci)] * 2),
+    "fa_prompt_fwd": (_ci, [_vp, _vp, _vp, _ll, _ll, _ll, _vp, _ll, _vp, _vp, _vp] + [_ci] * 7 +
+                      [_vp, _sz, _ci, _cf, _ci, _vp]),
+    "fa_prompt_fwd_workspace_bytes": (_sz, [_ci] * 8),
+    "fa_prompt_paged": (_ci, [_vp, _ll, _vp, _vp, _ci, _vp, _vp, _ll, _vp, _vp, _ci, _ci, _ci, _ci, _vp, _sz, _cf, _ci,
+                              _vp]),
     "fa_check_device_status": (_ci, [_vp]),
     "fa_debug_timeout_probe": (_ci, [ctypes.c_longlong, _vp]),
     "fa_debug_fwd_skip_load": (_ci, [_vp] * 5 + [_ci, _ci, _ci, _ci, _cf, _ci, ctypes.c_longlong, _vp]),
@@ -692,6 +698,130 @@ def fa_decode_shared(q, k_pages, v_pages, prefix_pages, prefix_len: int, block_t
         raise ValueError("prefix_pages is missing")
     return _decode_cache("fa_decode_shared", q, k_pages, v_pages, prefix_pages, prefix_len, block_tables, seq_lens,
                          scale, out, lse, workspace)
+
+
+def _offsets(t, name: str, B, dev: int):
+    """Checks int32 offsets [B+1] on device ``dev``; returns B."""
+    if not _is(t, _I32, dev) or t.dim() != 1 or not t.is_contiguous() or (B is not None and t.shape[0] != B + 1) or \
+            t.shape[0] < 2:
+        _refuse(t, name, dev, _I32, "a contiguous [B+1]")
+    return t.shape[0] - 1
+
+
+def _packed_queries(q, dev: int, d: int, hkv: int):
+    """Checks packed queries [total, Hq, d]; returns (their stride, total, Hq)."""
+    stride = _token_stride(q, "q", None, None, d, dev)
+    total, hq, _ = q.shape
+    if hkv < 1 or hq % hkv != 0:
+        raise ValueError("q's heads must be a multiple of the keys' heads")
+    return stride, total, hq
+
+
+def _prompt_outputs(q, out, lse, total: int, hq: int, d: int, dev: int):
+    """The outputs of a prompt's attention, allocated unless given; returns (out, its stride, lse)."""
+    if out is None:
+        out, stride = torch.empty((total, hq, d), dtype=_BF16, device=q.device), hq * d
+    else:
+        stride = _token_stride(out, "out", total, hq, d, dev)
+    if lse is None:
+        lse = torch.empty((hq, total), dtype=_F32, device=q.device)
+    elif not _is(lse, _F32, dev) or lse.shape != (hq, total) or not lse.is_contiguous():
+        _refuse(lse, "lse", dev, _F32, "a contiguous [Hq, total]")
+    return out, stride, lse
+
+
+def _scratch(workspace, need, device, dev: int):
+    """(pointer, bytes, tensor) of the caller's scratch, or of a new one of need() bytes (None for 0)."""
+    if workspace is None:
+        n = need()
+        if n == 0:
+            return None, 0, None
+        workspace = torch.empty(n, dtype=torch.uint8, device=device)
+    elif not isinstance(workspace, _Tensor) or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on q's device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def fa_prompt_fwd_workspace_bytes(B: int, Hq: int, Hkv: int, total_q: int, max_seqlen_q: int, max_seqlen_k: int,
+                                  d: int) -> int:
+    """Scratch bytes with which fa_prompt_fwd and fa_prompt_paged split this problem on the current device (0: not split)."""
+    return int(load_library().fa_prompt_fwd_workspace_bytes(B, Hq, Hkv, total_q, max_seqlen_q, max_seqlen_k, d, FA_BF16))
+
+
+def fa_prompt_fwd(q, k, v, cu_seqlens_q, max_seqlen_q: int, cu_seqlens_k=None, max_seqlen_k: int | None = None,
+                  scale: float | None = None, out=None, lse=None, workspace=None):
+    """Causal attention of packed prompts with grouped heads.
+
+    q: [total_q, Hq, d], k, v: [total_k, Hkv, d] bf16, the heads of a token
+    contiguous (a slice of a fused projection will do); cu_seqlens_q and
+    cu_seqlens_k: int32 [B+1] offsets of the sequences' tokens and keys (None:
+    the same). Of a sequence's n tokens and m keys, token i sees keys
+    j <= m - n + i; one that sees none gets O = 0 and LSE = -inf. Rows of tokens
+    outside all sequences are not written.
+    Returns (O [total_q, Hq, d], LSE [Hq, total_q] float32).
+    """
+    dev = q.get_device() if isinstance(q, _Tensor) else -1
+    if dev < 0 or not _is(q, _BF16, dev) or q.dim() != 3:
+        _refuse(q, "q", dev, _BF16, "[total, Hq, d]")
+    d = q.shape[2]
+    if not _is(k, _BF16, dev) or k.dim() != 3:
+        _refuse(k, "k", dev, _BF16, "[total, Hkv, d]")
+    total_k, hkv, _ = k.shape
+    ks = _token_stride(k, "k", None, hkv, d, dev)
+    vs = _token_stride(v, "v", total_k, hkv, d, dev)
+    qs, total, hq = _packed_queries(q, dev, d, hkv)
+    B = _offsets(cu_seqlens_q, "cu_seqlens_q", None, dev)
+    if cu_seqlens_k is None:
+        cu_seqlens_k, max_seqlen_k = cu_seqlens_q, max_seqlen_q if max_seqlen_k is None else max_seqlen_k
+    else:
+        _offsets(cu_seqlens_k, "cu_seqlens_k", B, dev)
+        if max_seqlen_k is None:
+            raise ValueError("max_seqlen_k is missing")
+    mq, mk = _int32(int(max_seqlen_q), "max_seqlen_q"), _int32(int(max_seqlen_k), "max_seqlen_k")
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    out, os_, lse = _prompt_outputs(q, out, lse, total, hq, d, dev)
+    if total == 0:
+        return out, lse
+    if total_k == 0:  # no sequence has a key; a tensor map wants one row
+        k = v = torch.zeros((1, hkv, d), dtype=_BF16, device=q.device)
+        total_k = mk = 1
+    lib = load_library()
+    with torch.cuda.device(dev):
+        ws, n, workspace = _scratch(
+            workspace, lambda: lib.fa_prompt_fwd_workspace_bytes(B, hq, hkv, total, mq, mk, d, FA_BF16), q.device, dev)
+        rc = lib.fa_prompt_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, out.data_ptr(), os_, lse.data_ptr(),
+                               cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, hq, hkv, total, total_k, mq, mk, ws,
+                               n, d, scale, FA_BF16, _raw_stream(dev))
+    _raise(rc, "fa_prompt_fwd")
+    return out, lse
+
+
+def fa_prompt_paged(q, k_pages, v_pages, block_tables, seq_lens, cu_seqlens_q, max_seqlen_q: int,
+                    scale: float | None = None, out=None, lse=None, workspace=None):
+    """``fa_prompt_fwd`` over a paged cache that already holds the tokens' own keys and those of earlier turns.
+
+    q: [total_q, Hq, d] bf16 packed new tokens, cu_seqlens_q int32 [B+1];
+    k_pages, v_pages, block_tables, seq_lens as in ``fa_decode_paged`` (lengths
+    after the append). Returns (O [total_q, Hq, d], LSE [Hq, total_q] float32).
+    """
+    pool, (_, hkv, page, d), B, max_pages, dev = _paged_cache(k_pages, v_pages, block_tables, seq_lens)
+    qs, total, hq = _packed_queries(q, dev, d, hkv)
+    _offsets(cu_seqlens_q, "cu_seqlens_q", B, dev)
+    mq = _int32(int(max_seqlen_q), "max_seqlen_q")
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    out, os_, lse = _prompt_outputs(q, out, lse, total, hq, d, dev)
+    if total == 0:
+        return out, lse
+    lib = load_library()
+    most = min(max_pages * page, 1 << 30)
+    with torch.cuda.device(dev):
+        ws, n, workspace = _scratch(
+            workspace, lambda: lib.fa_prompt_fwd_workspace_bytes(B, hq, hkv, total, mq, most, d, FA_BF16), q.device, dev)
+        rc = lib.fa_prompt_paged(q.data_ptr(), qs, pool, block_tables.data_ptr(), max_pages, seq_lens.data_ptr(),
+                                 out.data_ptr(), os_, lse.data_ptr(), cu_seqlens_q.data_ptr(), B, hq, total, mq, ws, n,
+                                 scale, FA_BF16, _raw_stream(dev))
+    _raise(rc, "fa_prompt_paged")
+    return out, lse
 
 
 def fa_check_device_status(device=None) -> int:

@@ -35,6 +35,8 @@ SOURCES = [
     ("fa_paged_api.cu", []),
     ("paged_append.cu", []),
     ("paged_decode.cu", []),
+    ("fa_prompt_api.cu", []),
+    ("prompt_fwd.cu", []),
 ]
 
 

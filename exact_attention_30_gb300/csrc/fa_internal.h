@@ -191,6 +191,22 @@ DecodePlan plan_decode_for_slots(int BH, int Nk, int slots, int tile);
 int decode_tile_keys(int Nq);
 cudaError_t launch_decode_bf16(const DecodeArgs& a, int d, cudaStream_t st);
 
+// n / d for 0 <= n < 2^31 by a multiplication (the round-up method: mul =
+// floor(2^32 (2^shift - d) / d) + 1, shift = ceil(log2 d)).
+struct FastDiv {
+  unsigned mul, shift;
+#ifdef __CUDACC__
+  __device__ __forceinline__ int operator()(int n) const {
+    return (int)((__umulhi((unsigned)n, mul) + (unsigned)n) >> shift);
+  }
+#endif
+};
+inline FastDiv fast_div(unsigned d) {
+  unsigned shift = 0;
+  while ((1ull << shift) < d) ++shift;
+  return FastDiv{(unsigned)(((1ull << 32) * ((1ull << shift) - d)) / d + 1), shift};
+}
+
 // ---- paged key/value cache (paged_append.cu, paged_decode.cu) ----
 // The pool of include/fa.h's fa_paged_kv, strides in elements.
 struct PagedPool {
@@ -244,21 +260,61 @@ bool encode_part_f32(CUtensorMap* m, void* ptr, long long rows, int d);
 // boxes of 64 columns x box_rows rows of one page, 128-byte swizzle.
 bool encode_pool_bf16(CUtensorMap* m, const PagedPool& pool, bool values, int d, int box_rows);
 
-// n / d for 0 <= n < 2^31 by a multiplication (the round-up method: mul =
-// floor(2^32 (2^shift - d) / d) + 1, shift = ceil(log2 d)).
-struct FastDiv {
-  unsigned mul, shift;
-#ifdef __CUDACC__
-  __device__ __forceinline__ int operator()(int n) const {
-    return (int)((__umulhi((unsigned)n, mul) + (unsigned)n) >> shift);
-  }
-#endif
+// ---- causal attention of packed prompts with grouped heads (prompt_*.cu) ----
+// B sequences; sequence b has the packed query tokens cu_q[b] .. cu_q[b + 1] - 1
+// and the keys cu_k[b] .. cu_k[b + 1] - 1 (packed) or the first seq_lens[b] keys
+// of its pages (cu_k == nullptr; total_k = max_k = what a table can hold).
+struct PromptSeqs {
+  const int* cu_q;
+  const int* cu_k;
+  const int* seq_lens;
+  int B, total_q, total_k, max_q, max_k;
 };
-inline FastDiv fast_div(unsigned d) {
-  unsigned shift = 0;
-  while ((1ull << shift) < d) ++shift;
-  return FastDiv{(unsigned)(((1ull << 32) * ((1ull << shift) - d)) / d + 1), shift};
+
+// The G query heads of a K/V head are rows of one problem: row r of a query
+// tile is head r mod G of token r / G, TP = floor(128 / G) tokens to a tile, so
+// a K/V head's keys are loaded once for all of them, dK and dV add up in place,
+// and a short prompt fills its tiles.
+constexpr int kPromptMaxGroup = 128;
+constexpr int kPromptMaxTokens = 1 << 30;
+inline int prompt_tile_tokens(int G) { return 128 / G; }
+
+struct PromptFwdArgs {
+  CUtensorMap tmQ, tmO;  // 4-D (d, head of the group, token, K/V head), boxes 64 x G x TP x 1
+  CUtensorMap tmK, tmV;  // packed: 3-D (d, token, head), boxes 64 x 128 x 1; paged: the pool (encode_pool_bf16)
+  CUtensorMap tmOpart;   // Opart as 2-D (d, rows), 32 x 128 boxes, 128-byte swizzle
+  PromptSeqs seqs;
+  PagedPool pool;            // paged only
+  const int* block_tables;   // paged only: [B, max_pages]
+  int max_pages, box_rows;
+  void* O;
+  long long o_stride;        // elements between the tokens of O
+  float* LSE;                // [Hkv * G, total_q]
+  int Hkv, G, tile_tokens;
+  FastDiv g_div;             // by G
+  int heads_per_group;       // K/V heads whose blocks are listed together (their keys stay in L2)
+  long long max_blocks;      // at least as many blocks of 2 * tile_tokens tokens as all sequences have
+  int splits;                // key ranges per block
+  float* Opart;              // splits > 1: fp32 [Hkv * max_blocks][splits][256][d], normalised
+  float* Lpart;              // and base-2 log-sum-exps
+  float scale_log2;
+  int* status;
+  unsigned long long wait_limit_ns;
+  int debug_skip_kv;
+};
+cudaError_t launch_prompt_fwd(const PromptFwdArgs& a, int d, cudaStream_t st);
+// Key ranges per block for `units` blocks (of all heads) that see up to
+// key_tiles 128-key tiles, on a GPU that runs `slots` CTAs at once.
+int plan_prompt_splits(long long units, int key_tiles, int slots);
+// Rows of a TMA box of a page: a power of two that divides page_size (a multiple of 8), at most `most`.
+inline int pool_box_rows(int page_size, int most) {
+  const int p = page_size & -page_size;
+  return p < most ? p : most;
 }
+// Tensor map of bf16 elements, 64-element inner boxes with the 128-byte swizzle;
+// dims and box from the innermost axis, strides in elements from the second.
+bool encode_bf16(CUtensorMap* m, const void* ptr, int rank, const long long* dims, const long long* strides,
+                 const int* box);
 
 struct PagedDecodeArgs {
   CUtensorMap tmK, tmV;

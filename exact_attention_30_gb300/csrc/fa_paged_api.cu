@@ -8,6 +8,7 @@
 #include <cstring>
 
 #include "../../include/fa.h"
+#include "fa_checks.h"
 #include "fa_internal.h"
 
 using namespace fa;
@@ -22,35 +23,6 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 // vectors) of at least `min` elements. An axis of one entry has no stride.
 bool stride_ok(long long stride, int extent, long long min) {
   return extent == 1 || (stride >= min && stride % 8 == 0 && stride <= (1ll << 38));
-}
-
-fa_status check_pool(const fa_paged_kv* c, fa_dtype dt, PagedPool* out) {
-  if (!c || !c->k || !c->v) return FA_ERR_INVALID_ARG;
-  if (dt != FA_F32 && dt != FA_BF16) return FA_ERR_INVALID_ARG;
-  if (c->num_pages < 1 || c->kv_heads < 1 || c->page_size < 1 || c->d < 1) return FA_ERR_INVALID_ARG;
-  if (dt != FA_BF16 || (c->d != 64 && c->d != 128)) return FA_ERR_UNSUPPORTED;
-  if (c->page_size % 8 != 0 || c->page_size > kMaxPageSize) return FA_ERR_UNSUPPORTED;
-  if (!aligned(c->k, 16) || !aligned(c->v, 16)) return FA_ERR_INVALID_ARG;
-  if (!stride_ok(c->k_page_stride, c->num_pages, c->d) || !stride_ok(c->k_head_stride, c->kv_heads, c->d) ||
-      !stride_ok(c->k_row_stride, c->page_size, c->d) || !stride_ok(c->v_page_stride, c->num_pages, c->d) ||
-      !stride_ok(c->v_head_stride, c->kv_heads, c->d) || !stride_ok(c->v_row_stride, c->page_size, c->d))
-    return FA_ERR_INVALID_ARG;
-  // an axis of one entry gets a stride that a tensor map accepts
-  auto st = [&](long long s, int extent) { return extent == 1 ? (long long)c->d : s; };
-  PagedPool p{};
-  p.k = c->k;
-  p.v = c->v;
-  p.k_page = st(c->k_page_stride, c->num_pages);
-  p.k_head = st(c->k_head_stride, c->kv_heads);
-  p.k_row = c->k_row_stride;
-  p.v_page = st(c->v_page_stride, c->num_pages);
-  p.v_head = st(c->v_head_stride, c->kv_heads);
-  p.v_row = c->v_row_stride;
-  p.num_pages = c->num_pages;
-  p.kv_heads = c->kv_heads;
-  p.page_size = c->page_size;
-  *out = p;
-  return FA_OK;
 }
 
 fa_status check_decode(int B, int Hq, int Hkv, int Nq, int d, fa_dtype dt) {
@@ -124,7 +96,7 @@ fa_status decode_impl(const void* Q, const long long* q_strides, const fa_paged_
                       unsigned long long limit_ns = kDefaultWaitLimitNs) {
   PagedDecodeArgs a;
   std::memset(&a, 0, sizeof(a));
-  fa_status s = check_pool(cache, dt, &a.pool);
+  fa_status s = check_paged_pool(cache, dt, &a.pool);
   if (s != FA_OK) return s;
   s = check_decode(B, Hq, cache->kv_heads, Nq, cache->d, dt);
   if (s != FA_OK) return s;
@@ -226,6 +198,39 @@ fa_status decode_impl(const void* Q, const long long* q_strides, const fa_paged_
 
 }  // namespace
 
+namespace fa {
+
+fa_status check_paged_pool(const fa_paged_kv* c, fa_dtype dt, PagedPool* out) {
+  if (!c || !c->k || !c->v) return FA_ERR_INVALID_ARG;
+  if (dt != FA_F32 && dt != FA_BF16) return FA_ERR_INVALID_ARG;
+  if (c->num_pages < 1 || c->kv_heads < 1 || c->page_size < 1 || c->d < 1) return FA_ERR_INVALID_ARG;
+  if (dt != FA_BF16 || (c->d != 64 && c->d != 128)) return FA_ERR_UNSUPPORTED;
+  if (c->page_size % 8 != 0 || c->page_size > kMaxPageSize) return FA_ERR_UNSUPPORTED;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16)) return FA_ERR_INVALID_ARG;
+  if (!stride_ok(c->k_page_stride, c->num_pages, c->d) || !stride_ok(c->k_head_stride, c->kv_heads, c->d) ||
+      !stride_ok(c->k_row_stride, c->page_size, c->d) || !stride_ok(c->v_page_stride, c->num_pages, c->d) ||
+      !stride_ok(c->v_head_stride, c->kv_heads, c->d) || !stride_ok(c->v_row_stride, c->page_size, c->d))
+    return FA_ERR_INVALID_ARG;
+  // an axis of one entry gets a stride that a tensor map accepts
+  auto st = [&](long long s, int extent) { return extent == 1 ? (long long)c->d : s; };
+  PagedPool p{};
+  p.k = c->k;
+  p.v = c->v;
+  p.k_page = st(c->k_page_stride, c->num_pages);
+  p.k_head = st(c->k_head_stride, c->kv_heads);
+  p.k_row = c->k_row_stride;
+  p.v_page = st(c->v_page_stride, c->num_pages);
+  p.v_head = st(c->v_head_stride, c->kv_heads);
+  p.v_row = c->v_row_stride;
+  p.num_pages = c->num_pages;
+  p.kv_heads = c->kv_heads;
+  p.page_size = c->page_size;
+  *out = p;
+  return FA_OK;
+}
+
+}  // namespace fa
+
 extern "C" {
 
 fa_status fa_kv_append(const void* K, const void* V, long long k_stride, long long v_stride, const void* Q,
@@ -236,7 +241,7 @@ fa_status fa_kv_append(const void* K, const void* V, long long k_stride, long lo
                        fa_dtype dt, void* stream) {
   AppendArgs a;
   std::memset(&a, 0, sizeof(a));
-  const fa_status s = check_pool(cache, dt, &a.pool);
+  const fa_status s = check_paged_pool(cache, dt, &a.pool);
   if (s != FA_OK) return s;
   const int d = cache->d;
   if (flags & ~FA_ROPE_INTERLEAVED) return FA_ERR_INVALID_ARG;

@@ -470,6 +470,69 @@ fa_status fa_decode_shared_plan(int B, int Hq, int Hkv, int Nq, int prefix_len, 
                                 int max_pages, int sms, int* key_ranges, int* prefix_ctas);
 
 /*
+ * Causal attention of packed prompts with grouped heads. Sequence b has the
+ * query tokens cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1 and the keys
+ * cu_seqlens_k[b] .. cu_seqlens_k[b+1]-1 of packed tensors; of its n tokens and
+ * m keys, token i sees the keys j <= m - n + i (the tokens are the newest of
+ * the sequence; n = m: a whole prompt, row r sees keys 0..r). A token that sees
+ * no key (m < n) gets O = 0 and LSE = -inf. Query heads h * Hq/Hkv ..
+ * (h + 1) * Hq/Hkv - 1 share K/V head h.
+ *   Q, O : [total_q, Hq, d] bf16, K, V: [total_k, Hkv, d] bf16: the heads of a
+ *          token contiguous, tokens *_stride elements apart (a slice of a fused
+ *          projection will do; of one token: ignored), multiples of 8 and >=
+ *          heads * d; 16-byte aligned. O must not overlap the inputs.
+ *   LSE  : [Hq, total_q] float32, dense (natural log, as fa_fwd_varlen).
+ *   cu_seqlens_q, cu_seqlens_k : DEVICE int32 [B+1], non-decreasing; they may
+ *          be one array. Tokens before the first offset and from the last one
+ *          on are padding: not read, and their rows of O and LSE are not
+ *          written. What stands outside a sequence's keys, NaN included, has no
+ *          influence on it; values that are not finite reach every row of
+ *          their own sequence whose tile reads them, as in a product with
+ *          weight zero.
+ *   max_seqlen_q, max_seqlen_k : HOST upper bounds of the sequences' tokens and
+ *          keys; with total_q they size the launch.
+ *   workspace : device scratch of >= fa_prompt_fwd_workspace_bytes() bytes,
+ *          256-byte aligned, contents on entry irrelevant, not used by another
+ *          call in flight; it lets few queries with many keys be split into key
+ *          ranges. NULL: they are not split.
+ * Scores, maxima and sums in fp32; each weight is rounded to bf16 once for its
+ * product with the values (the sum of weights takes it unrounded), O once at
+ * the end. Results are the same on every run.
+ * On the device: a sequence whose offsets do not lie within the tensors in
+ * order, or whose lengths exceed the given bounds, is left out (nothing of it
+ * is read or written) and fa_check_device_status returns FA_ERR_INVALID_ARG.
+ * Limits: bf16, d 64 or 128, Hq / Hkv <= 128, totals <= 2^30, B * Hkv <= 2^24.
+ * Errors: FA_ERR_INVALID_ARG (pointers, sizes, strides, scale, small
+ * workspace), FA_ERR_UNSUPPORTED (FA_F32, d, the limits), FA_ERR_CUDA.
+ */
+fa_status fa_prompt_fwd(const void* Q, const void* K, const void* V, long long q_stride, long long k_stride,
+                        long long v_stride, void* O, long long o_stride, float* LSE, const int* cu_seqlens_q,
+                        const int* cu_seqlens_k, int B, int Hq, int Hkv, int total_q, int total_k, int max_seqlen_q,
+                        int max_seqlen_k, void* workspace, size_t workspace_bytes, int d, float scale, fa_dtype dt,
+                        void* stream);
+
+/*
+ * Scratch bytes with which fa_prompt_fwd (or fa_prompt_paged, max_seqlen_k =
+ * max_pages * page_size) splits this problem on the CURRENT device; 0 when it
+ * does not (or on invalid arguments).
+ */
+size_t fa_prompt_fwd_workspace_bytes(int B, int Hq, int Hkv, int total_q, int max_seqlen_q, int max_seqlen_k, int d,
+                                     fa_dtype dt);
+
+/*
+ * fa_prompt_fwd over a paged cache, which already holds the tokens' own keys
+ * and values (fa_kv_append) and those of earlier turns: sequence b has the
+ * first seq_lens[b] keys of its pages (DEVICE int32 arrays, as in
+ * fa_decode_paged; a length or a page out of range is reported likewise, and
+ * that sequence's results are undefined). For more new tokens than
+ * fa_decode_paged takes. Arguments, limits and errors otherwise as there.
+ */
+fa_status fa_prompt_paged(const void* Q, long long q_stride, const fa_paged_kv* cache, const int* block_tables,
+                          int max_pages, const int* seq_lens, void* O, long long o_stride, float* LSE,
+                          const int* cu_seqlens_q, int B, int Hq, int total_q, int max_seqlen_q, void* workspace,
+                          size_t workspace_bytes, float scale, fa_dtype dt, void* stream);
+
+/*
  * fa_bwd without a caller-provided workspace, for callers that cannot
  * allocate device memory (for example code running inside a host application
  * that owns all device memory through its own pool, or a serving path where
