@@ -280,9 +280,8 @@ constexpr int kPromptMaxTokens = 1 << 30;
 inline int prompt_tile_tokens(int G) { return 128 / G; }
 
 struct PromptFwdArgs {
-  CUtensorMap tmQ, tmO;  // 4-D (d, head of the group, token, K/V head), boxes 64 x G x TP x 1
+  CUtensorMap tmQ;       // 4-D (d, head of the group, token, K/V head), boxes 64 x G x TP x 1
   CUtensorMap tmK, tmV;  // packed: 3-D (d, token, head), boxes 64 x 128 x 1; paged: the pool (encode_pool_bf16)
-  CUtensorMap tmOpart;   // Opart as 2-D (d, rows), 32 x 128 boxes, 128-byte swizzle
   PromptSeqs seqs;
   PagedPool pool;            // paged only
   const int* block_tables;   // paged only: [B, max_pages]

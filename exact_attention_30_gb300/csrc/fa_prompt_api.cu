@@ -117,10 +117,8 @@ fa_status fwd_launch(PromptFwdArgs& a, const void* Q, long long q_stride, void* 
     if (workspace_bytes < p.total) return FA_ERR_INVALID_ARG;
     a.Opart = static_cast<float*>(workspace);
     a.Lpart = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.lpart);
-    if (!encode_part_f32(&a.tmOpart, a.Opart, a.max_blocks * a.Hkv * a.splits * 256, d)) return FA_ERR_CUDA;
   }
-  if (!encode_grouped(&a.tmQ, Q, token_stride(q_stride, total_q, Hq, d), G, a.Hkv, total_q, a.tile_tokens, d) ||
-      !encode_grouped(&a.tmO, O, a.o_stride, G, a.Hkv, total_q, a.tile_tokens, d))
+  if (!encode_grouped(&a.tmQ, Q, token_stride(q_stride, total_q, Hq, d), G, a.Hkv, total_q, a.tile_tokens, d))
     return FA_ERR_CUDA;
   return launch_prompt_fwd(a, d, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
@@ -131,14 +129,17 @@ namespace fa {
 
 int plan_prompt_splits(long long units, int key_tiles, int slots) {
   if (units < 1 || key_tiles < 1 || slots < 1) return 1;
-  // Waves times the longest range, each range with a start-up of about three
-  // tiles; the partial results' second kernel costs about four.
-  long long best = -1;
+  // The longest range, or the blocks' work shared out evenly, whichever is
+  // more. Blocks differ (a prompt's first see few keys, sequences are ragged):
+  // on average they see half of key_tiles. A range begins and ends in about
+  // three tiles' time, the partial results' second kernel takes about four's.
+  float best = 0.f;
   int splits = 1;
   for (int s = 1; s <= key_tiles && s <= kPrefixMaxSplits; ++s) {
-    const long long waves = (units * s + slots - 1) / slots;
-    const long long cost = waves * ((key_tiles + s - 1) / s + 3) + (s > 1 ? 4 : 0);
-    if (best < 0 || cost < best) {
+    const float share = (float)units / (float)slots * (0.5f * (float)key_tiles + 3.f * (float)s);
+    const float longest = (float)((key_tiles + s - 1) / s + 3);
+    const float cost = std::max(share, longest) + (s > 1 ? 4.f : 0.f);
+    if (s == 1 || cost < best) {
       best = cost;
       splits = s;
     }

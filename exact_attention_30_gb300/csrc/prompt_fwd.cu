@@ -32,6 +32,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "fa_internal.h"
 #include "fwd_tile.cuh"
 #include "prompt.cuh"
@@ -39,6 +41,25 @@
 
 namespace fa {
 namespace {
+
+// mbar_wait in fewer instructions: the clock is read only after 64 tries.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, int* status, unsigned long long limit_ns) {
+  unsigned long long t0 = 0;
+#pragma unroll 1
+  for (unsigned i = 1; !mbar_try_wait(bar, parity); ++i) {
+    if ((i & 63u) != 0) continue;
+    const unsigned long long now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > limit_ns) {
+      report_status(status, kStatusTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int* status, unsigned long long limit_ns) {
+  return __all_sync(0xffffffffu, wait_phase(bar, parity, status, limit_ns));
+}
 
 struct PromptBlock {
   PromptView v;
@@ -50,7 +71,7 @@ struct PromptBlock {
 };
 
 // Whole warp: the block and key range of CTA `u`; false past the last one.
-__device__ __forceinline__ bool prompt_block(const PromptFwdArgs& a, long long u, int lane, bool report,
+__device__ __noinline__ bool prompt_block(const PromptFwdArgs& a, long long u, int lane, bool report,
                                              PromptBlock& k, int& part) {
   const int per = 2 * a.tile_tokens;
   bool bad = false;
@@ -85,47 +106,72 @@ __device__ __forceinline__ bool prompt_block(const PromptFwdArgs& a, long long u
   return true;
 }
 
+// Shared memory: that of the two-tile forward, a 4 KB staging buffer for each
+// softmax warp's rows of O, and a ring of published blocks.
+template <int D>
+struct PromptCfg : FwdCfg<D> {
+  using F = FwdCfg<D>;
+  static constexpr int STAGE_BYTES = 32 * 128;
+  static constexpr int OFF_STAGE = F::OFF_BAR;  // behind the K/V ring
+  static constexpr int IRING = 4;               // blocks published ahead
+  static constexpr int ITEM_INTS = 12;
+  static constexpr int OFF_BARS = OFF_STAGE + 8 * STAGE_BYTES;
+  // q_full[2], q_empty[2], k_full, v_full, k_empty, v_empty [STAGES each], s_full[2], p_full[2],
+  // o_done[2], s_free[2], item_full, item_empty [IRING each], cancel, drain
+  static constexpr int NBARS = 4 + 4 * F::STAGES + 8 + 2 * IRING + 2;
+  static constexpr int OFF_ITEMS = (OFF_BARS + NBARS * 8 + 15) / 16 * 16;
+  static constexpr int OFF_CANCEL = OFF_ITEMS + IRING * ITEM_INTS * 4;  // 16 bytes: the next CTA index
+  static constexpr int OFF_MISC = OFF_CANCEL + 16;                      // TMEM base, abort flag
+  static constexpr int BYTES = OFF_MISC + 8;
+  static constexpr int ALLOC = BYTES + 1024;  // slack for 1024-byte alignment
+};
+
+// A block as the MMA and softmax warps see it, in the ring.
+struct PromptItem {
+  int q0, n, m, head, tok0, kt0, n0, n1, part_row;  // n0 = -1: no more blocks
+
+  __device__ __forceinline__ int n_of(int t) const { return t == 0 ? n0 : n1; }
+};
+
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) prompt_fwd_kernel(const __grid_constant__ PromptFwdArgs a) {
-  using C = FwdCfg<D>;
+  using C = PromptCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
-  const uint32_t bar0 = sbase + C::OFF_BAR;
+  const uint32_t bar0 = sbase + C::OFF_BARS;
   auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
-  const int B_QFULL = 0;
-  const int B_KFULL = C::QT, B_VFULL = C::QT + C::STAGES, B_KEMPTY = C::QT + 2 * C::STAGES,
-            B_VEMPTY = C::QT + 3 * C::STAGES;
-  const int B_SFULL = C::QT + 4 * C::STAGES, B_PFULL = B_SFULL + C::QT, B_ODONE = B_PFULL + C::QT;
-  const int B_SFREE = B_ODONE + C::QT;  // S read by the softmax (own-P layout only)
-  const int B_DRAIN = B_SFREE + C::QT;
-  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_BAR + C::NBAR * 8);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + C::NBAR * 8 + 4);
+  const int B_QFULL = 0, B_QEMPTY = 2, B_KFULL = 4, B_VFULL = B_KFULL + C::STAGES, B_KEMPTY = B_VFULL + C::STAGES,
+            B_VEMPTY = B_KEMPTY + C::STAGES, B_SFULL = B_VEMPTY + C::STAGES, B_PFULL = B_SFULL + 2,
+            B_ODONE = B_PFULL + 2, B_SFREE = B_ODONE + 2, B_ITF = B_SFREE + 2, B_ITE = B_ITF + C::IRING,
+            B_CANCEL = B_ITE + C::IRING, B_DRAIN = B_CANCEL + 1;
+  volatile int* items = reinterpret_cast<volatile int*>(smem + C::OFF_ITEMS);
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  PromptBlock k;
-  int part;
-  if (!prompt_block(a, blockIdx.x, lane, blockIdx.x == 0 && warp == 0, k, part)) return;  // the whole CTA
-  const int n = k.v.n, m = k.v.m, past = m - n;
-  const int n_max = max(k.n0, k.n1);
-  const int kt0 = k.kt0;
-  auto n_of = [&](int t) { return t == 0 ? k.n0 : k.n1; };
   const int TP = a.tile_tokens, RT = TP * a.G;  // tokens and rows of a query tile
 
   if (threadIdx.x == 0) {
-    for (int t = 0; t < C::QT; ++t) mbar_init(BAR(B_QFULL + t), 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(BAR(B_QFULL + t), 1);
+      mbar_init(BAR(B_QEMPTY + t), 1);
+      mbar_init(BAR(B_SFULL + t), 1);
+      mbar_init(BAR(B_PFULL + t), 4);  // one arrival per softmax warp
+      mbar_init(BAR(B_ODONE + t), 1);
+      mbar_init(BAR(B_SFREE + t), 4);
+    }
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(BAR(B_KFULL + s), 1);
       mbar_init(BAR(B_VFULL + s), 1);
       mbar_init(BAR(B_KEMPTY + s), 1);
       mbar_init(BAR(B_VEMPTY + s), 1);
     }
-    for (int t = 0; t < C::QT; ++t) {
-      mbar_init(BAR(B_SFULL + t), 1);
-      mbar_init(BAR(B_PFULL + t), 4);  // one arrival per softmax warp
-      mbar_init(BAR(B_ODONE + t), 1);
-      mbar_init(BAR(B_SFREE + t), 4);
+    for (int s = 0; s < C::IRING; ++s) {
+      mbar_init(BAR(B_ITF + s), 1);  // the producer
+      mbar_init(BAR(B_ITE + s), 9);  // one arrival per consuming warp: MMA, 8 softmax
     }
+    mbar_init(BAR(B_CANCEL), 1);
     mbar_init(BAR(B_DRAIN), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -138,6 +184,19 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) prompt_fwd_kernel(const
   // The rows RT .. 127 of a query tile (G does not divide 128) hold whatever
   // shared memory held: rows are independent, and these are not written out.
 
+  // The i-th block of this CTA, for a consuming warp; false if the wait ran out.
+  auto get_item = [&](int i, PromptItem& it) {
+    const int s = i % C::IRING;
+    if (!wait_warp(BAR(B_ITF + s), (i / C::IRING) & 1, a.status, a.wait_limit_ns)) return false;
+    const volatile int* p = items + s * C::ITEM_INTS;
+    it = PromptItem{p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8]};
+    return true;
+  };
+  auto release_item = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(BAR(B_ITE + i % C::IRING));
+  };
+
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     // One lane issues the packed tensors' boxes; a paged cache's boxes have a
@@ -145,92 +204,147 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) prompt_fwd_kernel(const
     const int nbox = PAGED ? C::BN / a.box_rows : 1;
     const bool mine = PAGED ? lane < nbox * C::CH : lane == 0;
     const int box = PAGED ? lane % nbox : 0, chunk = PAGED ? lane / nbox : 0;
-    auto look_up = [&](int tile, int& page, int& row) {
-      page = -1;
-      row = 0;
-      if constexpr (PAGED) {
-        const int key = tile * C::BN + box * a.box_rows;
-        if (mine && key < m) {
-          const int pi = key / a.pool.page_size;
-          row = key - pi * a.pool.page_size;
-          page = __ldg(a.block_tables + (size_t)k.seq * a.max_pages + pi);
-          if (page < 0 || page >= a.pool.num_pages) {
-            report_status(a.status, kStatusBadSeqlens);
-            page = a.pool.num_pages;  // outside the tensor: reads as zeros
-          }
-        }
-      }
-    };
-    // bytes of a tile's boxes that hold keys of the sequence
-    auto tile_bytes = [&](int j) {
-      if constexpr (!PAGED) return (uint32_t)C::TILE_BYTES;
-      const int left = m - (kt0 + j) * C::BN;
-      const int boxes = left >= C::BN ? nbox : (left + a.box_rows - 1) / a.box_rows;
-      return (uint32_t)(boxes * a.box_rows * 128 * C::CH);
-    };
-    auto load = [&](const CUtensorMap* map, int off, int bar, int s, int j, int page, int row) {
-      const uint32_t dst = sbase + off + s * C::TILE_BYTES;
-      if constexpr (PAGED) {
-        if (page >= 0)
-          tma_load_4d(dst + chunk * C::CHUNK_BYTES + box * a.box_rows * 128, map, BAR(bar + s), chunk * 64, row, k.head, page);
-      } else if (lane == 0) {
-        for (int c = 0; c < C::CH; ++c)
-          tma_load_3d(dst + c * C::CHUNK_BYTES, map, BAR(bar + s), c * 64, k.v.k0 + (kt0 + j) * C::BN, k.head);
-      }
-    };
-    auto load_q = [&](int t) {
-      if (lane == 0 && n_of(t) > 0) {
-        mbar_arrive_expect_tx(BAR(B_QFULL + t), (uint32_t)(RT * 128 * C::CH));
-        for (int c = 0; c < C::CH; ++c)
-          tma_load_4d(sbase + C::OFF_Q + (t * C::CH + c) * C::CHUNK_BYTES, &a.tmQ, BAR(B_QFULL + t), c * 64, 0,
-                      k.v.q0 + k.tok0 + t * TP, k.head);
-      }
-    };
     if (lane == 0) {
       tma_prefetch_desc(&a.tmQ);
       tma_prefetch_desc(&a.tmK);
       tma_prefetch_desc(&a.tmV);
     }
-    load_q(0);
-    bool q1 = false;  // tile 1's queries are asked for after the first keys
-    int last_k = -1, last_v = -1;  // last tile whose load was issued
-    int skipped = -1;
-    int page, row;
-    look_up(kt0, page, row);
-    for (int j = 0; j < n_max; ++j) {
-      if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
-      const int s = j % C::STAGES;
-      const uint32_t ph = (j / C::STAGES) & 1;
-      int next_page = -1, next_row = 0;
-      if (j + 1 < n_max) look_up(kt0 + j + 1, next_page, next_row);
-      if (!mbar_wait_warp(BAR(B_KEMPTY + s), ph ^ 1, a.status, a.wait_limit_ns)) { *abort_flag = 1; break; }
-      if (j != a.debug_skip_kv) {
-        if (lane == 0) mbar_arrive_expect_tx(BAR(B_KFULL + s), tile_bytes(j));
-        __syncwarp();
-        load(&a.tmK, C::OFF_K, B_KFULL, s, j, page, row);
-      } else {
-        skipped = j;
+    PromptBlock k, next;
+    int part;
+    bool ok = true;
+    // Publishes block i of this CTA (or that there is none).
+    auto publish = [&](int i, bool there, const PromptBlock& b, int p) {
+      const int s = i % C::IRING;
+      if (i >= C::IRING && !wait_warp(BAR(B_ITE + s), ((i / C::IRING) - 1) & 1, a.status, a.wait_limit_ns)) return false;
+      if (lane == 0) {
+        volatile int* d = items + s * C::ITEM_INTS;
+        d[0] = b.v.q0;
+        d[1] = b.v.n;
+        d[2] = b.v.m;
+        d[3] = b.head;
+        d[4] = b.tok0;
+        d[5] = b.kt0;
+        d[6] = there ? b.n0 : -1;
+        d[7] = b.n1;
+        d[8] = b.unit * a.splits + p;
+        mbar_arrive(BAR(B_ITF + s));
       }
-      last_k = j;
-      if (j == 0) {
-        load_q(1);
-        q1 = true;
-      }
-      if (!mbar_wait_warp(BAR(B_VEMPTY + s), ph ^ 1, a.status, a.wait_limit_ns)) { *abort_flag = 1; break; }
-      if (lane == 0) mbar_arrive_expect_tx(BAR(B_VFULL + s), tile_bytes(j));
       __syncwarp();
-      load(&a.tmV, C::OFF_V, B_VFULL, s, j, page, row);
-      last_v = j;
-      page = next_page;
-      row = next_row;
+      return true;
+    };
+    bool there = prompt_block(a, blockIdx.x, lane, blockIdx.x == 0, k, part);
+    ok = publish(0, there, k, part);
+    int g0 = 0, q_used[2] = {0, 0};       // key tiles, and loads of each Q slot, before this block
+    int asked = 0, answered = 0;          // requests for a next CTA
+    int last_k = -1, last_v = -1, skipped = -1;  // last tiles whose loads were issued, by ring position
+    for (int i = 0; ok && there; ++i) {
+      // the CTA that would begin next gives its index to this one, if any is left
+      if (lane == 0) {
+        mbar_arrive_expect_tx(BAR(B_CANCEL), 16);
+        clc_try_cancel(sbase + C::OFF_CANCEL, BAR(B_CANCEL));
+      }
+      ++asked;
+      bool next_there = false;
+      int next_part = 0;
+      auto fetch_next = [&]() {
+        if (!wait_warp(BAR(B_CANCEL), i & 1, a.status, a.wait_limit_ns)) return false;
+        ++answered;
+        const int u = clc_next_cta(sbase + C::OFF_CANCEL);
+        fence_proxy_async_smem();  // read before the next answer is written there
+        __syncwarp();
+        next_there = u >= 0 && prompt_block(a, u, lane, false, next, next_part);
+        return publish(i + 1, next_there, next, next_part);
+      };
+      const int n_max = max(k.n0, k.n1), m = k.v.m, kt0 = k.kt0;
+      auto look_up = [&](int tile, int& page, int& row) {
+        page = -1;
+        row = 0;
+        if constexpr (PAGED) {
+          const int key = tile * C::BN + box * a.box_rows;
+          if (mine && key < m) {
+            const int pi = key / a.pool.page_size;
+            row = key - pi * a.pool.page_size;
+            page = __ldg(a.block_tables + (size_t)k.seq * a.max_pages + pi);
+            if (page < 0 || page >= a.pool.num_pages) {
+              report_status(a.status, kStatusBadSeqlens);
+              page = a.pool.num_pages;  // outside the tensor: reads as zeros
+            }
+          }
+        }
+      };
+      // bytes of a tile's boxes that hold keys of the sequence
+      auto tile_bytes = [&](int j) {
+        if constexpr (!PAGED) return (uint32_t)C::TILE_BYTES;
+        const int left = m - (kt0 + j) * C::BN;
+        const int boxes = left >= C::BN ? nbox : (left + a.box_rows - 1) / a.box_rows;
+        return (uint32_t)(boxes * a.box_rows * 128 * C::CH);
+      };
+      auto load = [&](const CUtensorMap* map, int off, int bar, int s, int j, int page, int row) {
+        const uint32_t dst = sbase + off + s * C::TILE_BYTES;
+        if constexpr (PAGED) {
+          if (page >= 0)
+            tma_load_4d(dst + chunk * C::CHUNK_BYTES + box * a.box_rows * 128, map, BAR(bar + s), chunk * 64, row, k.head, page);
+        } else if (lane == 0) {
+          for (int c = 0; c < C::CH; ++c)
+            tma_load_3d(dst + c * C::CHUNK_BYTES, map, BAR(bar + s), c * 64, k.v.k0 + (kt0 + j) * C::BN, k.head);
+        }
+      };
+      auto load_q = [&](int t) {  // once the block before has read the slot
+        if ((t == 0 ? k.n0 : k.n1) == 0) return true;
+        if (q_used[t] > 0 && !wait_warp(BAR(B_QEMPTY + t), (q_used[t] - 1) & 1, a.status, a.wait_limit_ns)) return false;
+        ++q_used[t];
+        if (lane == 0) {
+          mbar_arrive_expect_tx(BAR(B_QFULL + t), (uint32_t)(RT * 128 * C::CH));
+          for (int c = 0; c < C::CH; ++c)
+            tma_load_4d(sbase + C::OFF_Q + (t * C::CH + c) * C::CHUNK_BYTES, &a.tmQ, BAR(B_QFULL + t), c * 64, 0,
+                        k.v.q0 + k.tok0 + t * TP, k.head);
+        }
+        __syncwarp();
+        return true;
+      };
+      int page, row;
+      look_up(kt0, page, row);
+      for (int j = 0; ok && j < n_max; ++j) {
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
+        const int g = g0 + j, s = g % C::STAGES;
+        const uint32_t ph = (g / C::STAGES) & 1;
+        int next_page = -1, next_row = 0;
+        if (j + 1 < n_max) look_up(kt0 + j + 1, next_page, next_row);
+        if (!wait_warp(BAR(B_KEMPTY + s), ph ^ 1, a.status, a.wait_limit_ns)) { ok = false; break; }
+        if (g != a.debug_skip_kv) {
+          if (lane == 0) mbar_arrive_expect_tx(BAR(B_KFULL + s), tile_bytes(j));
+          __syncwarp();
+          load(&a.tmK, C::OFF_K, B_KFULL, s, j, page, row);
+        } else {
+          skipped = g;
+        }
+        last_k = g;
+        if (j == 0 && !(load_q(0) && load_q(1))) { ok = false; break; }
+        if (!wait_warp(BAR(B_VEMPTY + s), ph ^ 1, a.status, a.wait_limit_ns)) { ok = false; break; }
+        if (lane == 0) mbar_arrive_expect_tx(BAR(B_VFULL + s), tile_bytes(j));
+        __syncwarp();
+        load(&a.tmV, C::OFF_V, B_VFULL, s, j, page, row);
+        last_v = g;
+        page = next_page;
+        row = next_row;
+        if (j == min(1, n_max - 1)) ok = fetch_next();
+      }
+      if (!ok) break;
+      if (n_max == 0 && !fetch_next()) { ok = false; break; }
+      g0 += n_max;
+      there = next_there;
+      k = next;
+      part = next_part;
     }
-    // drain: the last load issued into each buffer must have landed before exit
-    if (k.n0 > 0) mbar_wait_warp(BAR(B_QFULL + 0), 0, a.status, a.wait_limit_ns);
-    if (q1 && k.n1 > 0) mbar_wait_warp(BAR(B_QFULL + 1), 0, a.status, a.wait_limit_ns);
-    for (int j = max(0, last_k - C::STAGES + 1); j <= last_k; ++j)
-      if (j != skipped) mbar_wait_warp(BAR(B_KFULL + j % C::STAGES), (j / C::STAGES) & 1, a.status, a.wait_limit_ns);
-    for (int j = max(0, last_v - C::STAGES + 1); j <= last_v; ++j)
-      mbar_wait_warp(BAR(B_VFULL + j % C::STAGES), (j / C::STAGES) & 1, a.status, a.wait_limit_ns);
+    if (!ok) *abort_flag = 1;
+    // drain: what was asked for last must have landed before exit
+    for (int t = 0; t < 2; ++t)
+      if (q_used[t] > 0) wait_warp(BAR(B_QFULL + t), (q_used[t] - 1) & 1, a.status, a.wait_limit_ns);
+    for (int g = max(0, last_k - C::STAGES + 1); g <= last_k; ++g)
+      if (g != skipped) wait_warp(BAR(B_KFULL + g % C::STAGES), (g / C::STAGES) & 1, a.status, a.wait_limit_ns);
+    for (int g = max(0, last_v - C::STAGES + 1); g <= last_v; ++g)
+      wait_warp(BAR(B_VFULL + g % C::STAGES), (g / C::STAGES) & 1, a.status, a.wait_limit_ns);
+    if (answered < asked) wait_warp(BAR(B_CANCEL), answered & 1, a.status, a.wait_limit_ns);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     const uint32_t leader = elect_one();
@@ -239,7 +353,9 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) prompt_fwd_kernel(const
     const uint64_t dQ0 = sdesc_sw128(sbase + C::OFF_Q, 16, 1024);
     const uint64_t dK0 = sdesc_sw128(sbase + C::OFF_K, 16, 1024);
     const uint64_t dV0 = sdesc_sw128(sbase + C::OFF_V, C::CHUNK_BYTES, 1024);
-    auto issue_s = [&](int t, int s) {
+    auto wait = [&](int b, uint32_t parity) { return wait_warp(BAR(b), parity, a.status, a.wait_limit_ns); };
+    // S of tile t against the keys in slot s; `last`: the block's last for this tile
+    auto issue_s = [&](int t, int s, bool last) {
       const uint64_t qa = dQ0 + (uint64_t)((t * C::TILE_BYTES) >> 4);
       const uint64_t kb = dK0 + (uint64_t)((s * C::TILE_BYTES) >> 4);
       const uint32_t dcol = tmem + C::S_COL(t);
@@ -249,22 +365,29 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) prompt_fwd_kernel(const
         mma_ss(dcol, qa + off, kb + off, idesc_s, kk > 0 ? 1u : 0u, leader);
       }
       mma_commit(BAR(B_SFULL + t), leader);
+      if (last) mma_commit(BAR(B_QEMPTY + t), leader);
     };
-    // P V over the keys that the tile's last query sees, in steps of 16
-    auto issue_pv = [&](int t, int s, int j) {
+    // P V over a whole tile, and over the first `keys` keys (those that the
+    // tile's last query sees) in steps of 16
+    auto issue_pv = [&](int t, int s, bool acc) {
       const uint64_t vb = dV0 + (uint64_t)((s * C::TILE_BYTES) >> 4);
       const uint32_t dcol = tmem + C::O_COL(t), acol = tmem + C::P_COL(t);
-      const int keys = past + min(n, k.tok0 + (t + 1) * TP) - (kt0 + j) * C::BN;
 #pragma unroll
       for (int kk = 0; kk < C::BN / 16; ++kk)
-        mma_ts(dcol, acol + kk * 8, vb + (uint64_t)((kk * 2048) >> 4), idesc_o, (j > 0 || kk > 0) ? 1u : 0u,
-               16 * kk >= keys ? 0u : leader);
+        mma_ts(dcol, acol + kk * 8, vb + (uint64_t)((kk * 2048) >> 4), idesc_o, (acc || kk > 0) ? 1u : 0u, leader);
       mma_commit(BAR(B_ODONE + t), leader);
     };
-    // V_j has landed in slot s: rows behind the last key that the last step
-    // would read become zero.
-    auto clean_v = [&](int j, int s) {
-      const int keys = m - (kt0 + j) * C::BN;
+    auto issue_pv_keys = [&](int t, int s, bool acc, int keys) {
+      const uint64_t vb = dV0 + (uint64_t)((s * C::TILE_BYTES) >> 4);
+      const uint32_t dcol = tmem + C::O_COL(t), acol = tmem + C::P_COL(t);
+#pragma unroll 1
+      for (int kk = 0; kk < C::BN / 16 && 16 * kk < keys; ++kk)
+        mma_ts(dcol, acol + kk * 8, vb + (uint64_t)((kk * 2048) >> 4), idesc_o, (acc || kk > 0) ? 1u : 0u, leader);
+      mma_commit(BAR(B_ODONE + t), leader);
+    };
+    // V has landed in slot s with `keys` keys of the sequence: rows behind them
+    // that the last step would read become zero.
+    auto clean_v = [&](int s, int keys) {
       if (keys < C::BN && (keys & 15) != 0) {
         const int n_rows = 16 - (keys & 15);
         for (int e = lane; e < n_rows * C::CH * 8; e += 32) {
@@ -276,59 +399,149 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) prompt_fwd_kernel(const
         __syncwarp();
       }
     };
-    auto wait = [&](int b, uint32_t parity) { return mbar_wait_warp(BAR(b), parity, a.status, a.wait_limit_ns); };
-    bool ok = true;
-    if (n_max > 0) {
-      ok = wait(B_KFULL + 0, 0);
-      for (int t = 0; ok && t < C::QT; ++t) {
-        if (n_of(t) == 0) continue;
-        if (!wait(B_QFULL + t, 0)) { ok = false; break; }
-        tc_fence_after();
-        issue_s(t, 0);
-      }
-      if (ok) mma_commit(BAR(B_KEMPTY + 0), leader);
-    }
-    for (int j = 0; ok && j < n_max; ++j) {
-      if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
-      const int s = j % C::STAGES;
-      const uint32_t ph = (j / C::STAGES) & 1;
-      const int s1 = (j + 1) % C::STAGES;
-      const uint32_t ph1 = ((j + 1) / C::STAGES) & 1;
-      bool k_next = false, v_here = false;  // K_{j+1}, V_j have landed
-      auto need_v = [&]() {
-        if (!v_here) {
-          if (!wait(B_VFULL + s, ph)) return false;
-          clean_v(j, s);
-        }
-        return v_here = true;
-      };
-      auto next_s = [&](int t) {
-        if (!k_next && !wait(B_KFULL + s1, ph1)) return false;
-        k_next = true;
-        tc_fence_after();
-        issue_s(t, s1);
+    PromptItem it;
+    bool ok = get_item(0, it);
+    int g0 = 0;              // key tiles before this block
+    int c0 = 0, c1 = 0;      // key tiles of query tiles 0 and 1 before it
+    int q0_used = 0, q1_used = 0;  // blocks with such a tile before it
+    int s_done = 0;  // bit t: the block's first S of tile t has been issued
+    // The first S of tile t of block `b`, whose keys begin at ring position g
+    // (`now`: only if its operands are there).
+    auto first_s = [&](int t, const PromptItem& b, int g, int c, bool now) {
+      const int nt = b.n_of(t);
+      if (nt == 0 || (s_done >> t & 1)) return true;
+      const int s = g % C::STAGES;
+      const uint32_t pk = (g / C::STAGES) & 1, pq = (t == 0 ? q0_used : q1_used) & 1;
+      if (now && !__all_sync(0xffffffffu, mbar_test(BAR(B_KFULL + s), pk) && mbar_test(BAR(B_QFULL + t), pq)))
         return true;
-      };
-      for (int t = 0; ok && t < C::QT; ++t) {
-        if (j >= n_of(t)) continue;
-        const bool more = j + 1 < n_of(t);
-        if constexpr (C::P_OWN) {
-          // P has its own columns: S_{j+1} goes first, P_j V_j follows
-          if (more && !(wait(B_SFREE + t, j & 1) && next_s(t))) { ok = false; break; }
-          if (!wait(B_PFULL + t, j & 1) || !need_v()) { ok = false; break; }
-          tc_fence_after();
-          issue_pv(t, s, j);
-        } else {
-          // P overwrites S: P_j V_j must be issued before S_{j+1}
-          if (!need_v() || !wait(B_PFULL + t, j & 1)) { ok = false; break; }
-          tc_fence_after();
-          issue_pv(t, s, j);
-          if (more && !next_s(t)) { ok = false; break; }
+      if (!now && !(wait(B_KFULL + s, pk) && wait(B_QFULL + t, pq))) return false;
+      if (C::P_OWN && c > 0 && !wait(B_SFREE + t, (c - 1) & 1)) return false;
+      tc_fence_after();
+      issue_s(t, s, nt == 1);
+      if (t == 0) ++q0_used;
+      else ++q1_used;
+      s_done |= 1 << t;
+      return true;
+    };
+    for (int i = 0; ok && it.n0 >= 0; ++i) {
+      const int n_max = max(it.n0, it.n1), past = it.m - it.n;
+      PromptItem next;
+      next.n0 = -1;
+      bool fetched = false;
+#pragma unroll 1
+      for (int t = 0; ok && t < C::QT; ++t) ok = first_s(t, it, g0, t == 0 ? c0 : c1, false);
+      if (!ok) break;
+      s_done = 0;
+      if (n_max > 0) mma_commit(BAR(B_KEMPTY + g0 % C::STAGES), leader);
+      const int seen0 = past + min(it.n, it.tok0 + TP) - it.kt0 * C::BN;  // keys from kt0 on that tile 0's last query sees
+      const int seen1 = past + min(it.n, it.tok0 + 2 * TP) - it.kt0 * C::BN;
+      // The tiles that neither query tile ends near: whole keys, a next S for
+      // both. The loop is kept short (a wait and sixteen products per tile):
+      // what its warp does between two waits, and what it does to the
+      // instruction cache, is on the path from one softmax to the next
+      // (16384 tokens, 32 heads, d = 128: 1385 TFLOP/s with the last tiles'
+      // cases in it).
+      const int n_lean = min(it.n0, it.n1) - 2;
+      int j = 0;
+#pragma unroll 1
+      for (; j < n_lean; ++j) {
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
+        const int g = g0 + j, s = g % C::STAGES, s1 = (g + 1) % C::STAGES;
+        const uint32_t ph1 = ((g + 1) / C::STAGES) & 1;
+        if constexpr (!C::P_OWN) ok = wait(B_VFULL + s, (g / C::STAGES) & 1);
+#pragma unroll
+        for (int t = 0; t < C::QT; ++t) {
+          const uint32_t pt = (uint32_t)((t == 0 ? c0 : c1) + j) & 1u;
+          if constexpr (C::P_OWN) {
+            ok = ok && wait(B_SFREE + t, pt);
+            if (t == 0) ok = ok && wait(B_KFULL + s1, ph1);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(t, s1, false);
+            ok = wait(B_PFULL + t, pt);
+            if (t == 0) ok = ok && wait(B_VFULL + s, (g / C::STAGES) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(t, s, j > 0);
+          } else {
+            ok = ok && wait(B_PFULL + t, pt);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(t, s, j > 0);
+            if (t == 0) {
+              ok = wait(B_KFULL + s1, ph1);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            issue_s(t, s1, false);
+          }
         }
+        if (!ok) break;
+        mma_commit(BAR(B_VEMPTY + s), leader);
+        mma_commit(BAR(B_KEMPTY + s1), leader);
       }
       if (!ok) break;
-      mma_commit(BAR(B_VEMPTY + s), leader);
-      if (j + 1 < n_max) mma_commit(BAR(B_KEMPTY + s1), leader);
+#pragma unroll 1
+      for (; j < n_max; ++j) {
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
+        const int g = g0 + j, s = g % C::STAGES, s1 = (g + 1) % C::STAGES;
+        const uint32_t ph = (g / C::STAGES) & 1, ph1 = ((g + 1) / C::STAGES) & 1;
+        bool k_next = false, v_here = false;  // K_{j+1}, V_j have landed
+        auto need_v = [&]() {
+          if (!v_here) {
+            if (!wait(B_VFULL + s, ph)) return false;
+            clean_v(s, it.m - (it.kt0 + j) * C::BN);
+          }
+          return v_here = true;
+        };
+        auto next_s = [&](int t) {
+          if (!k_next && !wait(B_KFULL + s1, ph1)) return false;
+          k_next = true;
+          tc_fence_after();
+          issue_s(t, s1, j + 2 == it.n_of(t));
+          return true;
+        };
+#pragma unroll 1
+        for (int t = 0; t < C::QT; ++t) {
+          const uint32_t pt = (uint32_t)((t == 0 ? c0 : c1) + j) & 1u;
+          if (j < it.n_of(t)) {
+            const bool more = j + 1 < it.n_of(t);
+            const int keys = (t == 0 ? seen0 : seen1) - j * C::BN;
+            if constexpr (C::P_OWN) {
+              // P has its own columns: S_{j+1} goes first, P_j V_j follows
+              if (more && !(wait(B_SFREE + t, pt) && next_s(t))) { ok = false; break; }
+              if (!wait(B_PFULL + t, pt) || !need_v()) { ok = false; break; }
+              tc_fence_after();
+              issue_pv_keys(t, s, j > 0, keys);
+            } else {
+              // P overwrites S: P_j V_j must be issued before S_{j+1}
+              if (!need_v() || !wait(B_PFULL + t, pt)) { ok = false; break; }
+              tc_fence_after();
+              issue_pv_keys(t, s, j > 0, keys);
+              if (more && !next_s(t)) { ok = false; break; }
+            }
+          }
+          if (j + 1 == n_max) {
+            // this tile is done with the block: the next block's first S, if
+            // its operands are there already
+            if (!fetched && !get_item(i + 1, next)) { ok = false; break; }
+            fetched = true;
+            if (next.n0 >= 0 && !first_s(t, next, g0 + n_max, (t == 0 ? c0 : c1) + it.n_of(t), true)) {
+              ok = false;
+              break;
+            }
+          }
+        }
+        if (!ok) break;
+        mma_commit(BAR(B_VEMPTY + s), leader);
+        if (j + 1 < n_max) mma_commit(BAR(B_KEMPTY + s1), leader);
+      }
+      if (!ok || (!fetched && !get_item(i + 1, next))) { ok = false; break; }
+      release_item(i);
+      g0 += n_max;
+      c0 += it.n_of(0);
+      c1 += it.n_of(1);
+      it = next;
     }
     if (!ok && lane == 0) *abort_flag = 1;
     // drain every MMA issued before TMEM can be released
@@ -339,220 +552,210 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) prompt_fwd_kernel(const
     const int t = (warp - C::SW0) >> 2;  // query tile of this warpgroup
     const int wq = warp & 3;             // TMEM lane quarter
     const int row = wq * 32 + lane;      // row of the tile
-    const int tok_in = a.g_div(row), g = row - tok_in * a.G;
-    const int tok0 = k.tok0 + t * TP;    // first token of the tile
-    const int tok = tok0 + tok_in;
-    const bool live = row < RT && tok < n;
-    const int n_own = n_of(t);
     const uint32_t lane_addr = tmem + ((uint32_t)(wq * 32) << 16);
     const uint32_t s_addr = lane_addr + C::S_COL(t);
     const uint32_t o_addr = lane_addr + C::O_COL(t);
     const float c2 = a.scale_log2;
     const uint64_t c22 = f2_pack(c2, c2);
-    float m_ref = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int j = 0; j < n_own; ++j) {
-      if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
-      const bool w = mbar_wait(BAR(B_SFULL + t), j & 1, a.status, a.wait_limit_ns);
-      if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
-      tc_fence_after();
-      // keys of this tile that the row sees: the tile's first query's diagonal
-      // decides whether any row has masked columns here
-      const int key0 = (kt0 + j) * C::BN;
-      const bool mask_tile = past + tok0 + 1 - key0 < C::BN;
-      const int valid = min(past + tok + 1, m) - key0;
-      float mx[4];
-      uint64_t sm2[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) { mx[u] = -INFINITY; sm2[u] = 0ull; }
-      bool need;
-      float alpha = 1.f;
-      // a row that has met no key yet: what is added to its scores (-inf) is 0
-      const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
-      if constexpr (C::P_OWN) {
-        const uint32_t p_addr = lane_addr + C::P_COL(t);
-        if (!softmax_pass_own_p<true>(s_addr, p_addr, mask_tile, valid, c22, f2_pack(neg_m, neg_m), mx, sm2, j > 0,
-                                      BAR(B_ODONE + t), (uint32_t)(j - 1) & 1u, a.status, a.wait_limit_ns)) {
-          ok = false;
-          break;
-        }
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
-        need = mt > m_ref + kRescaleLog2;
-        if (__any_sync(0xffffffffu, need)) {
-          const float m_new = need ? mt : m_ref;
-          alpha = need ? ex2_approx(m_ref - m_new) : 1.f;
-#pragma unroll
-          for (int u = 0; u < 4; ++u) sm2[u] = 0ull;
-          tmem_st_wait();  // the speculative P is overwritten below
-          const float neg_new = m_new == -INFINITY ? 0.f : -m_new;
-          softmax_pass_own_p<false>(s_addr, p_addr, mask_tile, valid, c22, f2_pack(neg_new, neg_new), mx, sm2, false, 0u,
-                                    0u, a.status, a.wait_limit_ns);
-          m_ref = m_new;
-        }
-        // S_j has been read: S_{j+1} may be written over it
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(B_SFREE + t));
-      } else {
-        // The speculative pass against the reference max of the tiles before,
-        // the tile's own max alongside; a tile whose max exceeds it by more than
-        // kRescaleLog2 is done again. 64 columns of S are in registers at a time.
-        uint32_t pk[64];
-        auto pass = [&](auto with_max, float neg) {
-          const uint64_t nm2 = f2_pack(neg, neg);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t r[64];
-            tmem_ld32(s_addr + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
-            tmem_ld32(s_addr + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+    int c = 0;  // key tiles of this query tile before the block
+    for (int i = 0; ok; ++i) {
+      int n_own, sees, first;  // keys from kt0 on that this row and the tile's first row see
+      {
+        PromptItem it;
+        if (!get_item(i, it)) { ok = false; break; }
+        if (it.n0 < 0) break;
+        n_own = it.n_of(t);
+        first = it.m - it.n + it.tok0 + t * TP + 1 - it.kt0 * C::BN;
+        sees = min(first + a.g_div(row), it.m - it.kt0 * C::BN);
+      }
+      float m_ref = -INFINITY, l = 0.f;
+      for (int j = 0; j < n_own; ++j) {
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
+        const bool w = wait_phase(BAR(B_SFULL + t), (c + j) & 1, a.status, a.wait_limit_ns);
+        if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+        tc_fence_after();
+        // the diagonal of the tile's first query decides whether any row has
+        // masked columns here
+        const bool mask_tile = first - j * C::BN < C::BN;
+        const int valid = sees - j * C::BN;
+        if (mask_tile) {
+          // masked scores are replaced where they stand, a few tiles to a block:
+          // no mask in the pass below
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t r[32];
+            tmem_ld32(s_addr + 32 * q, r);
             tmem_ld_wait();
-            if (mask_tile) {
+            mask_cols32(r, 32 * q, valid);
+            tmem_st32(s_addr + 32 * q, r);
+          }
+          tmem_st_wait();
+        }
+        // The speculative pass against the reference max of the tiles before, the
+        // tile's own max alongside; a tile whose max exceeds it by more than
+        // kRescaleLog2 is done again (the first always is). A row that has met no
+        // key yet has m_ref = -inf: what is added to its scores, -inf, is 0.
+        float mx[4];
+        uint64_t sm2[4];
+        float alpha = 1.f;
+        bool moved = false;
+        uint32_t pk[C::P_OWN ? 1 : 64];
+#pragma unroll 1
+        while (true) {
 #pragma unroll
-              for (int i = 0; i < 64; ++i) r[i] = 64 * h + i >= valid ? __float_as_uint(-INFINITY) : r[i];
-            }
+          for (int u = 0; u < 4; ++u) { mx[u] = -INFINITY; sm2[u] = 0ull; }
+          const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+          const uint64_t nm2 = f2_pack(neg, neg);
+          if constexpr (C::P_OWN) {
+            ok = softmax_pass_own_p<true>(s_addr, lane_addr + C::P_COL(t), false, 0, c22, nm2, mx, sm2, j > 0 && !moved,
+                                          BAR(B_ODONE + t), (uint32_t)(c + j - 1) & 1u, a.status, a.wait_limit_ns);
+            if (!ok) break;
+          } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float s0 = __uint_as_float(r[2 * i]), s1 = __uint_as_float(r[2 * i + 1]);
-              if constexpr (with_max) mx[i & 3] = fmax3(mx[i & 3], s0, s1);
-              const float2 x = f2_unpack(ffma2(f2_pack(s0, s1), c22, nm2));
-              const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
-              sm2[i & 3] = fadd2(sm2[i & 3], f2_pack(p0, p1));
-              pk[32 * h + i] = pack_bf16x2(p0, p1);
+            for (int h = 0; h < 2; ++h) {
+              uint32_t r[64];  // 64 columns of S at a time
+              tmem_ld32(s_addr + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+              tmem_ld32(s_addr + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+              tmem_ld_wait();
+#pragma unroll
+              for (int u = 0; u < 32; ++u) {
+                const float x0 = __uint_as_float(r[2 * u]), x1 = __uint_as_float(r[2 * u + 1]);
+                mx[u & 3] = fmax3(mx[u & 3], x0, x1);
+                const float2 x = f2_unpack(ffma2(f2_pack(x0, x1), c22, nm2));
+                const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+                sm2[u & 3] = fadd2(sm2[u & 3], f2_pack(p0, p1));
+                pk[32 * h + u] = pack_bf16x2(p0, p1);
+              }
             }
           }
-        };
-        pass(std::true_type{}, neg_m);
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
-        need = mt > m_ref + kRescaleLog2;
-        if (__any_sync(0xffffffffu, need)) {
-          const float m_new = need ? mt : m_ref;
-          alpha = need ? ex2_approx(m_ref - m_new) : 1.f;
-#pragma unroll
-          for (int u = 0; u < 4; ++u) sm2[u] = 0ull;
-          pass(std::false_type{}, m_new == -INFINITY ? 0.f : -m_new);
-          m_ref = m_new;
+          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
+          const bool need = mt > m_ref + kRescaleLog2;
+          if (!__any_sync(0xffffffffu, need)) break;
+          if (need) {
+            alpha = ex2_approx(m_ref - mt);
+            m_ref = mt;
+          }
+          moved = true;
+          if constexpr (C::P_OWN) tmem_st_wait();  // the speculative P is overwritten
         }
-        tmem_st32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-        tmem_st32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
-      }
-      const float2 sa = f2_unpack(fadd2(fadd2(sm2[0], sm2[1]), fadd2(sm2[2], sm2[3])));
-      l = l * alpha + (sa.x + sa.y);
-      // P V of the tile before is complete here (attn_fwd_bf16.cu): O can be rescaled
-      if (j > 0 && __any_sync(0xffffffffu, need)) {
-#pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-          uint32_t o[32];
-          tmem_ld32(o_addr + 32 * q, o);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-          tmem_st32(o_addr + 32 * q, o);
+        if (!ok) break;
+        if constexpr (C::P_OWN) {
+          // S_j has been read: S_{j+1} may be written over it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(BAR(B_SFREE + t));
+        } else {
+          tmem_st32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+          tmem_st32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
         }
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(B_PFULL + t));
-    }
-    tmem_st_wait();  // no TMEM store may be in flight when the loop is left early
-    if (ok && n_own > 0) {
-      const bool w = mbar_wait(BAR(B_ODONE + t), (n_own - 1) & 1, a.status, a.wait_limit_ns);
-      ok = __all_sync(0xffffffffu, w);
-    }
-    const bool parts = a.splits > 1;
-    // every warp that shares an epilogue barrier takes the same decision (both
-    // tiles' warps where they stage over the other tile's buffers)
-    if (parts) ok = named_bar_and<1>(256, ok);
-    else if (t == 0) ok = named_bar_and<2>(128, ok);
-    else ok = named_bar_and<3>(128, ok);
-    if (!ok) *abort_flag = 1;
-    const float inv_l = l == 0.f ? 0.f : 1.f / l;
-    if (ok && tok0 < n) {
-      tc_fence_after();
-      // 32 columns of this row of O, normalised; zeros where the tile has no key
-      auto read_o = [&](int q, float (&x)[32]) {
-        uint32_t r[32];
-        if (n_own > 0) {
-          tmem_ld32(o_addr + 32 * q, r);
-          tmem_ld_wait();
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = n_own > 0 && l != 0.f ? __uint_as_float(r[i]) * inv_l : 0.f;
-      };
-      const float lse2 = m_ref + __log2f(l);  // -inf for a row without keys
-      if (parts) {
-        // fp32 rows of this key range; a range without keys leaves only its log-sum-exp
-        const long long prow0 = ((long long)k.unit * a.splits + part) * (2 * C::BM) + t * C::BM;
-        a.Lpart[prow0 + row] = lse2;
-        if (n_own > 0) {
-          uint8_t* stage = smem + C::OFF_Q + t * (D * 512);
+        const float2 sa = f2_unpack(fadd2(fadd2(sm2[0], sm2[1]), fadd2(sm2[2], sm2[3])));
+        l = l * alpha + (sa.x + sa.y);
+        // P V of the tile before is complete here (attn_fwd_bf16.cu): O can be rescaled
+        if (j > 0 && moved) {
 #pragma unroll
           for (int q = 0; q < D / 32; ++q) {
-            float x[32];
-            read_o(q, x);
-            uint8_t* b = stage + q * 16384 + row * 128;
+            uint32_t o[32];
+            tmem_ld32(o_addr + 32 * q, o);
+            tmem_ld_wait();
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-              *reinterpret_cast<float4*>(b + ((u ^ (row & 7)) << 4)) =
-                  make_float4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
-          }
-          fence_proxy_async_smem();
-          if (t == 0) named_bar_sync<2>(128);
-          else named_bar_sync<3>(128);
-          if (warp == C::SW0 + 4 * t && lane == 0) {
-#pragma unroll
-            for (int q = 0; q < D / 32; ++q)
-              tma_store_2d(&a.tmOpart, smem_u32(stage + q * 16384), q * 32, (int)prow0);
-            bulk_commit_group();
-            bulk_wait_group_read<0>();
+            for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
+            tmem_st32(o_addr + 32 * q, o);
           }
         }
-      } else {
-        // A tile whose tokens are all of its sequence leaves through the tile's
-        // Q slot by TMA; a sequence's last, partial tile row by row from there
-        // (16 lanes a 256-byte row).
-        uint8_t* stage = smem + C::OFF_Q + t * C::TILE_BYTES;
-#pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-          float x[32];
-          read_o(q, x);
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const int c0 = 32 * q + 8 * v, u = (c0 & 63) >> 3;
-            *reinterpret_cast<uint4*>(stage + (c0 >> 6) * C::CHUNK_BYTES + row * 128 + ((u ^ (row & 7)) << 4)) =
-                make_uint4(pack_bf16x2(x[8 * v], x[8 * v + 1]), pack_bf16x2(x[8 * v + 2], x[8 * v + 3]),
-                           pack_bf16x2(x[8 * v + 4], x[8 * v + 5]), pack_bf16x2(x[8 * v + 6], x[8 * v + 7]));
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_PFULL + t));
+      }
+      tmem_st_wait();  // no TMEM store may be in flight when the loop is left early
+      if (!ok) break;
+      c += n_own;
+      if (n_own > 0) {
+        const bool w = wait_phase(BAR(B_ODONE + t), (c - 1) & 1, a.status, a.wait_limit_ns);
+        if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+        tc_fence_after();
+      }
+      // The warp's 32 rows leave through its staging buffer, 128 bytes of each
+      // at a time in the swizzle that spreads them over the banks, read back so
+      // that a store instruction writes whole 128-byte rows. The next block's
+      // first P V comes after this warp's next p_full arrival, so the
+      // accumulator is safe until then.
+      PromptItem it;
+      get_item(i, it);  // again: keeps the loop's registers free
+      const int n = it.n, tok0 = it.tok0 + t * TP;  // tok0: first token of the tile
+      if (tok0 < n) {
+        uint8_t* stage = smem + C::OFF_STAGE + (warp - C::SW0) * C::STAGE_BYTES;  // [32 rows][128 bytes]
+        const float inv_l = l == 0.f ? 0.f : 1.f / l;
+        const float lse2 = m_ref + __log2f(l);  // -inf for a row without keys
+        const int rsub = lane >> 3, unit = lane & 7;
+        // one 32-column piece of this row of O, normalised; zeros without keys
+        auto read_o = [&](int q, float (&x)[32]) {
+          uint32_t r[32];
+          if (n_own > 0) {
+            tmem_ld32(o_addr + 32 * q, r);
+            tmem_ld_wait();
           }
-        }
-        if (tok0 + TP <= n) {
-          fence_proxy_async_smem();
-          if (t == 0) named_bar_sync<2>(128);
-          else named_bar_sync<3>(128);
-          if (warp == C::SW0 + 4 * t && lane == 0) {
 #pragma unroll
-            for (int c = 0; c < C::CH; ++c)
-              tma_store_4d(&a.tmO, smem_u32(stage + c * C::CHUNK_BYTES), c * 64, 0, k.v.q0 + tok0, k.head);
-            bulk_commit_group();
-            bulk_wait_group_read<0>();  // the slot read before the CTA exits
+          for (int u = 0; u < 32; ++u) x[u] = n_own > 0 && l != 0.f ? __uint_as_float(r[u]) * inv_l : 0.f;
+        };
+        if (a.splits > 1) {
+          // fp32 rows of this key range; a range without keys leaves only its log-sum-exp
+          const long long prow0 = (long long)it.part_row * (2 * C::BM) + t * C::BM + wq * 32;
+          a.Lpart[prow0 + lane] = lse2;
+          if (n_own > 0) {
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+              float x[32];
+              read_o(q, x);
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+                *reinterpret_cast<float4*>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) =
+                    make_float4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
+              __syncwarp();
+#pragma unroll
+              for (int u = 0; u < 8; ++u) {
+                const int r = 4 * u + rsub;
+                const float4 y = *reinterpret_cast<const float4*>(stage + r * 128 + ((unit ^ (r & 7)) << 4));
+                *reinterpret_cast<float4*>(a.Opart + (prow0 + r) * D + 32 * q + 4 * unit) = y;
+              }
+              __syncwarp();
+            }
           }
         } else {
-          __syncwarp();
-          constexpr int LPR = D / 8;  // lanes to a row
-#pragma unroll 4
-          for (int i = 0; i < 32; i += 32 / LPR) {
-            const int r = wq * 32 + i + lane / LPR, u = lane % LPR;
-            const int tk = a.g_div(r);
-            const uint4 x = *reinterpret_cast<const uint4*>(stage + (u >> 3) * C::CHUNK_BYTES + r * 128 +
-                                                            (((u & 7) ^ (r & 7)) << 4));
-            if (r < RT && tok0 + tk < n)
-              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.O) + (long long)(k.v.q0 + tok0 + tk) * a.o_stride +
-                                        (long long)(k.head * a.G + r - tk * a.G) * D + 8 * u) = x;
+#pragma unroll 1
+          for (int h = 0; h < D / 64; ++h) {
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              float x[32];
+              read_o(2 * h + hh, x);
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * hh + u) ^ (lane & 7)) << 4)) =
+                    make_uint4(pack_bf16x2(x[8 * u], x[8 * u + 1]), pack_bf16x2(x[8 * u + 2], x[8 * u + 3]),
+                               pack_bf16x2(x[8 * u + 4], x[8 * u + 5]), pack_bf16x2(x[8 * u + 6], x[8 * u + 7]));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const int r = 4 * u + rsub, tr = wq * 32 + r, tk = a.g_div(tr);
+              const uint4 y = *reinterpret_cast<const uint4*>(stage + r * 128 + ((unit ^ (r & 7)) << 4));
+              if (tr < RT && tok0 + tk < n)
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.O) + (long long)(it.q0 + tok0 + tk) * a.o_stride +
+                                          (long long)(it.head * a.G + tr - tk * a.G) * D + 64 * h + 8 * unit) = y;
+            }
+            __syncwarp();
           }
+          const int tok_in = a.g_div(row);
+          if (row < RT && tok0 + tok_in < n)
+            a.LSE[(size_t)(it.head * a.G + row - tok_in * a.G) * a.seqs.total_q + it.q0 + tok0 + tok_in] =
+                lse2 * 0.69314718055994531f;
         }
-        if (live)
-          a.LSE[(size_t)(k.head * a.G + g) * a.seqs.total_q + k.v.q0 + tok] = lse2 * 0.69314718055994531f;
       }
+      tc_fence_before();
+      release_item(i);
     }
+    if (!ok) *abort_flag = 1;
   }
 
   tc_fence_before();
@@ -621,16 +824,15 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const __grid_constant
 
 template <int D, bool PAGED>
 cudaError_t launch_d(const PromptFwdArgs& a, cudaStream_t st) {
-  using C = FwdCfg<D>;
-  static_assert(C::SMEM_ALLOC <= 227 * 1024, "shared memory budget");
-  static_assert(C::QT * D * 512 <= C::OFF_BAR - C::OFF_Q, "partial rows fit the tile buffers");
+  using C = PromptCfg<D>;
+  static_assert(C::ALLOC <= 227 * 1024, "shared memory budget");
   const long long ctas = a.max_blocks * a.Hkv * a.splits;
   if (a.splits < 1 || a.max_blocks < 1 || ctas > 0x7fffffffll || (a.splits > 1 && (!a.Opart || !a.Lpart)))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(prompt_fwd_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       C::SMEM_ALLOC);
+                                       C::ALLOC);
   if (e != cudaSuccess) return e;
-  prompt_fwd_kernel<D, PAGED><<<(unsigned)ctas, C::THREADS, C::SMEM_ALLOC, st>>>(a);
+  prompt_fwd_kernel<D, PAGED><<<(unsigned)ctas, C::THREADS, C::ALLOC, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.splits == 1) return e;
   prompt_merge_kernel<D><<<(unsigned)(a.max_blocks * a.Hkv * 8), 256, 0, st>>>(a);
