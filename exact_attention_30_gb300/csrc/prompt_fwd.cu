@@ -71,7 +71,7 @@ struct PromptBlock {
 };
 
 // Whole warp: the block and key range of CTA `u`; false past the last one.
-__device__ __noinline__ bool prompt_block(const PromptFwdArgs& a, long long u, int lane, bool report,
+__device__ __forceinline__ bool prompt_block(const PromptFwdArgs& a, long long u, int lane, bool report,
                                              PromptBlock& k, int& part) {
   const int per = 2 * a.tile_tokens;
   bool bad = false;
@@ -106,35 +106,43 @@ __device__ __noinline__ bool prompt_block(const PromptFwdArgs& a, long long u, i
   return true;
 }
 
-// Shared memory: that of the two-tile forward, a 4 KB staging buffer for each
-// softmax warp's rows of O, and a ring of published blocks.
+// Warps 0-3: producer, MMA issuer, scheduler, none; 4-7 and 8-11: softmax of
+// query tiles 0 and 1; 12-15: output. Shared memory: that of the two-tile
+// forward, a 4 KB staging buffer for each output warp, the rows' statistics on
+// their way to the output warps and a ring of published blocks.
 template <int D>
 struct PromptCfg : FwdCfg<D> {
   using F = FwdCfg<D>;
+  static constexpr int NTHREADS = 512;
   static constexpr int STAGE_BYTES = 32 * 128;
   static constexpr int OFF_STAGE = F::OFF_BAR;  // behind the K/V ring
-  static constexpr int IRING = 4;               // blocks published ahead
+  static constexpr int OFF_STAT = OFF_STAGE + 4 * STAGE_BYTES;  // float2 [2 blocks][2 tiles][128 rows]: maximum, sum
+  static constexpr int IRING = 2;  // blocks published: the one in work and the next
   static constexpr int ITEM_INTS = 12;
-  static constexpr int OFF_BARS = OFF_STAGE + 8 * STAGE_BYTES;
+  static constexpr int OFF_BARS = OFF_STAT + 2 * 2 * 128 * 8;
   // q_full[2], q_empty[2], k_full, v_full, k_empty, v_empty [STAGES each], s_full[2], p_full[2],
-  // o_done[2], s_free[2], item_full, item_empty [IRING each], cancel, drain
-  static constexpr int NBARS = 4 + 4 * F::STAGES + 8 + 2 * IRING + 2;
+  // o_done[2], s_free[2], o_free[2], l_full[2 tiles][2 blocks], item_full, item_empty [IRING each], cancel, drain
+  static constexpr int NBARS = 4 + 4 * F::STAGES + 14 + 2 * IRING + 2;
   static constexpr int OFF_ITEMS = (OFF_BARS + NBARS * 8 + 15) / 16 * 16;
   static constexpr int OFF_CANCEL = OFF_ITEMS + IRING * ITEM_INTS * 4;  // 16 bytes: the next CTA index
   static constexpr int OFF_MISC = OFF_CANCEL + 16;                      // TMEM base, abort flag
   static constexpr int BYTES = OFF_MISC + 8;
   static constexpr int ALLOC = BYTES + 1024;  // slack for 1024-byte alignment
+  // Registers per thread of the control, softmax and output warps: with the
+  // launch's 128 each, 128 * (56 + 2 * 176 + 104) = 512 * 128.
+  static constexpr int R_CONTROL = 56, R_SOFTMAX = 176, R_OUT = 104;
+  static_assert(128 * (R_CONTROL + 2 * R_SOFTMAX + R_OUT) <= NTHREADS * 128, "register split");
 };
 
-// A block as the MMA and softmax warps see it, in the ring.
-struct PromptItem {
-  int q0, n, m, head, tok0, kt0, n0, n1, part_row;  // n0 = -1: no more blocks
-
-  __device__ __forceinline__ int n_of(int t) const { return t == 0 ? n0 : n1; }
-};
+// What the ring holds of a block: its sequence's first packed token and tokens,
+// the K/V head, tile 0's first token, the first key tile, the key tiles of query
+// tiles 0 and 1 (-1: no more blocks), its rows among the partial results, the
+// sequence's first packed key and index, and of the keys from the first tile on,
+// those that tile 0's first row sees and those that there are.
+enum : int { kItQ0, kItN, kItHead, kItTok0, kItKt0, kItN0, kItN1, kItPart, kItK0, kItSeq, kItFirst, kItLeft };
 
 template <int D, bool PAGED>
-__global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) prompt_fwd_kernel(const __grid_constant__ PromptFwdArgs a) {
+__global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constant__ PromptFwdArgs a) {
   using C = PromptCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -143,8 +151,8 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) prompt_fwd_kernel(const
   auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   const int B_QFULL = 0, B_QEMPTY = 2, B_KFULL = 4, B_VFULL = B_KFULL + C::STAGES, B_KEMPTY = B_VFULL + C::STAGES,
             B_VEMPTY = B_KEMPTY + C::STAGES, B_SFULL = B_VEMPTY + C::STAGES, B_PFULL = B_SFULL + 2,
-            B_ODONE = B_PFULL + 2, B_SFREE = B_ODONE + 2, B_ITF = B_SFREE + 2, B_ITE = B_ITF + C::IRING,
-            B_CANCEL = B_ITE + C::IRING, B_DRAIN = B_CANCEL + 1;
+            B_ODONE = B_PFULL + 2, B_SFREE = B_ODONE + 2, B_OFREE = B_SFREE + 2, B_LFULL = B_OFREE + 2,
+            B_ITF = B_LFULL + 4, B_ITE = B_ITF + C::IRING, B_CANCEL = B_ITE + C::IRING, B_DRAIN = B_CANCEL + 1;
   volatile int* items = reinterpret_cast<volatile int*>(smem + C::OFF_ITEMS);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
@@ -160,6 +168,9 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) prompt_fwd_kernel(const
       mbar_init(BAR(B_PFULL + t), 4);  // one arrival per softmax warp
       mbar_init(BAR(B_ODONE + t), 1);
       mbar_init(BAR(B_SFREE + t), 4);
+      mbar_init(BAR(B_OFREE + t), 4);  // one arrival per output warp
+      mbar_init(BAR(B_LFULL + 2 * t), 4);  // a barrier for every other block: a tile without rows
+      mbar_init(BAR(B_LFULL + 2 * t + 1), 4);  // is done at once, and its waiter may be a block behind
     }
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(BAR(B_KFULL + s), 1);
@@ -168,8 +179,8 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) prompt_fwd_kernel(const
       mbar_init(BAR(B_VEMPTY + s), 1);
     }
     for (int s = 0; s < C::IRING; ++s) {
-      mbar_init(BAR(B_ITF + s), 1);  // the producer
-      mbar_init(BAR(B_ITE + s), 9);  // one arrival per consuming warp: MMA, 8 softmax
+      mbar_init(BAR(B_ITF + s), 1);   // the scheduler
+      mbar_init(BAR(B_ITE + s), 14);  // one arrival per consuming warp: producer, MMA, 8 softmax, 4 output
     }
     mbar_init(BAR(B_CANCEL), 1);
     mbar_init(BAR(B_DRAIN), 1);
@@ -184,372 +195,383 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) prompt_fwd_kernel(const
   // The rows RT .. 127 of a query tile (G does not divide 128) hold whatever
   // shared memory held: rows are independent, and these are not written out.
 
-  // The i-th block of this CTA, for a consuming warp; false if the wait ran out.
-  auto get_item = [&](int i, PromptItem& it) {
-    const int s = i % C::IRING;
-    if (!wait_warp(BAR(B_ITF + s), (i / C::IRING) & 1, a.status, a.wait_limit_ns)) return false;
-    const volatile int* p = items + s * C::ITEM_INTS;
-    it = PromptItem{p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8]};
-    return true;
+  auto wait = [&](int b, uint32_t parity) { return wait_warp(BAR(b), parity, a.status, a.wait_limit_ns); };
+  // Waits for the i-th block of this CTA (a consuming warp; false if the wait
+  // ran out), and reads of it, until release_item(i).
+  auto get_item = [&](int i) { return wait(B_ITF + i % C::IRING, (i / C::IRING) & 1); };
+  // (broadcast: the compiler keeps what is the same in all lanes, and what
+  // follows from it, in uniform registers, where the products' operands go)
+  auto item = [&](int i, int what) {
+    return __shfl_sync(0xffffffffu, (int)items[(i % C::IRING) * C::ITEM_INTS + what], 0);
   };
   auto release_item = [&](int i) {
     __syncwarp();
     if (lane == 0) mbar_arrive(BAR(B_ITE + i % C::IRING));
   };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    // One lane issues the packed tensors' boxes; a paged cache's boxes have a
-    // lane each (box `box` of the 64-column chunk `chunk` of a tile).
-    const int nbox = PAGED ? C::BN / a.box_rows : 1;
-    const bool mine = PAGED ? lane < nbox * C::CH : lane == 0;
-    const int box = PAGED ? lane % nbox : 0, chunk = PAGED ? lane / nbox : 0;
-    if (lane == 0) {
-      tma_prefetch_desc(&a.tmQ);
-      tma_prefetch_desc(&a.tmK);
-      tma_prefetch_desc(&a.tmV);
-    }
-    PromptBlock k, next;
-    int part;
-    bool ok = true;
-    // Publishes block i of this CTA (or that there is none).
-    auto publish = [&](int i, bool there, const PromptBlock& b, int p) {
-      const int s = i % C::IRING;
-      if (i >= C::IRING && !wait_warp(BAR(B_ITE + s), ((i / C::IRING) - 1) & 1, a.status, a.wait_limit_ns)) return false;
-      if (lane == 0) {
-        volatile int* d = items + s * C::ITEM_INTS;
-        d[0] = b.v.q0;
-        d[1] = b.v.n;
-        d[2] = b.v.m;
-        d[3] = b.head;
-        d[4] = b.tok0;
-        d[5] = b.kt0;
-        d[6] = there ? b.n0 : -1;
-        d[7] = b.n1;
-        d[8] = b.unit * a.splits + p;
-        mbar_arrive(BAR(B_ITF + s));
-      }
-      __syncwarp();
-      return true;
-    };
-    bool there = prompt_block(a, blockIdx.x, lane, blockIdx.x == 0, k, part);
-    ok = publish(0, there, k, part);
-    int g0 = 0, q_used[2] = {0, 0};       // key tiles, and loads of each Q slot, before this block
-    int asked = 0, answered = 0;          // requests for a next CTA
-    int last_k = -1, last_v = -1, skipped = -1;  // last tiles whose loads were issued, by ring position
-    for (int i = 0; ok && there; ++i) {
-      // the CTA that would begin next gives its index to this one, if any is left
-      if (lane == 0) {
-        mbar_arrive_expect_tx(BAR(B_CANCEL), 16);
-        clc_try_cancel(sbase + C::OFF_CANCEL, BAR(B_CANCEL));
-      }
-      ++asked;
-      bool next_there = false;
-      int next_part = 0;
-      auto fetch_next = [&]() {
-        if (!wait_warp(BAR(B_CANCEL), i & 1, a.status, a.wait_limit_ns)) return false;
-        ++answered;
-        const int u = clc_next_cta(sbase + C::OFF_CANCEL);
-        fence_proxy_async_smem();  // read before the next answer is written there
-        __syncwarp();
-        next_there = u >= 0 && prompt_block(a, u, lane, false, next, next_part);
-        return publish(i + 1, next_there, next, next_part);
-      };
-      const int n_max = max(k.n0, k.n1), m = k.v.m, kt0 = k.kt0;
-      auto look_up = [&](int tile, int& page, int& row) {
-        page = -1;
-        row = 0;
-        if constexpr (PAGED) {
-          const int key = tile * C::BN + box * a.box_rows;
-          if (mine && key < m) {
-            const int pi = key / a.pool.page_size;
-            row = key - pi * a.pool.page_size;
-            page = __ldg(a.block_tables + (size_t)k.seq * a.max_pages + pi);
-            if (page < 0 || page >= a.pool.num_pages) {
-              report_status(a.status, kStatusBadSeqlens);
-              page = a.pool.num_pages;  // outside the tensor: reads as zeros
-            }
+  if (warp < 4) {
+    set_max_registers_dec<C::R_CONTROL>();
+    if (warp == 2) {
+      // ---------------------------------------------------------- scheduler
+      bool ok = true;
+      long long u = blockIdx.x;
+      for (int i = 0; ok && u >= 0; ++i) {
+        const int s = i % C::IRING;
+        if (i >= C::IRING) ok = wait(B_ITE + s, ((i / C::IRING) - 1) & 1);
+        if (ok && i > 0) {
+          // the CTA that would begin next gives its index to this one, if any is left
+          if (lane == 0) {
+            mbar_arrive_expect_tx(BAR(B_CANCEL), 16);
+            clc_try_cancel(sbase + C::OFF_CANCEL, BAR(B_CANCEL));
           }
-        }
-      };
-      // bytes of a tile's boxes that hold keys of the sequence
-      auto tile_bytes = [&](int j) {
-        if constexpr (!PAGED) return (uint32_t)C::TILE_BYTES;
-        const int left = m - (kt0 + j) * C::BN;
-        const int boxes = left >= C::BN ? nbox : (left + a.box_rows - 1) / a.box_rows;
-        return (uint32_t)(boxes * a.box_rows * 128 * C::CH);
-      };
-      auto load = [&](const CUtensorMap* map, int off, int bar, int s, int j, int page, int row) {
-        const uint32_t dst = sbase + off + s * C::TILE_BYTES;
-        if constexpr (PAGED) {
-          if (page >= 0)
-            tma_load_4d(dst + chunk * C::CHUNK_BYTES + box * a.box_rows * 128, map, BAR(bar + s), chunk * 64, row, k.head, page);
-        } else if (lane == 0) {
-          for (int c = 0; c < C::CH; ++c)
-            tma_load_3d(dst + c * C::CHUNK_BYTES, map, BAR(bar + s), c * 64, k.v.k0 + (kt0 + j) * C::BN, k.head);
-        }
-      };
-      auto load_q = [&](int t) {  // once the block before has read the slot
-        if ((t == 0 ? k.n0 : k.n1) == 0) return true;
-        if (q_used[t] > 0 && !wait_warp(BAR(B_QEMPTY + t), (q_used[t] - 1) & 1, a.status, a.wait_limit_ns)) return false;
-        ++q_used[t];
-        if (lane == 0) {
-          mbar_arrive_expect_tx(BAR(B_QFULL + t), (uint32_t)(RT * 128 * C::CH));
-          for (int c = 0; c < C::CH; ++c)
-            tma_load_4d(sbase + C::OFF_Q + (t * C::CH + c) * C::CHUNK_BYTES, &a.tmQ, BAR(B_QFULL + t), c * 64, 0,
-                        k.v.q0 + k.tok0 + t * TP, k.head);
-        }
-        __syncwarp();
-        return true;
-      };
-      int page, row;
-      look_up(kt0, page, row);
-      for (int j = 0; ok && j < n_max; ++j) {
-        if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
-        const int g = g0 + j, s = g % C::STAGES;
-        const uint32_t ph = (g / C::STAGES) & 1;
-        int next_page = -1, next_row = 0;
-        if (j + 1 < n_max) look_up(kt0 + j + 1, next_page, next_row);
-        if (!wait_warp(BAR(B_KEMPTY + s), ph ^ 1, a.status, a.wait_limit_ns)) { ok = false; break; }
-        if (g != a.debug_skip_kv) {
-          if (lane == 0) mbar_arrive_expect_tx(BAR(B_KFULL + s), tile_bytes(j));
+          ok = wait(B_CANCEL, (i - 1) & 1);
+          if (ok) u = clc_next_cta(sbase + C::OFF_CANCEL);
+          fence_proxy_async_smem();  // read before the next answer is written there
           __syncwarp();
-          load(&a.tmK, C::OFF_K, B_KFULL, s, j, page, row);
-        } else {
-          skipped = g;
-        }
-        last_k = g;
-        if (j == 0 && !(load_q(0) && load_q(1))) { ok = false; break; }
-        if (!wait_warp(BAR(B_VEMPTY + s), ph ^ 1, a.status, a.wait_limit_ns)) { ok = false; break; }
-        if (lane == 0) mbar_arrive_expect_tx(BAR(B_VFULL + s), tile_bytes(j));
-        __syncwarp();
-        load(&a.tmV, C::OFF_V, B_VFULL, s, j, page, row);
-        last_v = g;
-        page = next_page;
-        row = next_row;
-        if (j == min(1, n_max - 1)) ok = fetch_next();
-      }
-      if (!ok) break;
-      if (n_max == 0 && !fetch_next()) { ok = false; break; }
-      g0 += n_max;
-      there = next_there;
-      k = next;
-      part = next_part;
-    }
-    if (!ok) *abort_flag = 1;
-    // drain: what was asked for last must have landed before exit
-    for (int t = 0; t < 2; ++t)
-      if (q_used[t] > 0) wait_warp(BAR(B_QFULL + t), (q_used[t] - 1) & 1, a.status, a.wait_limit_ns);
-    for (int g = max(0, last_k - C::STAGES + 1); g <= last_k; ++g)
-      if (g != skipped) wait_warp(BAR(B_KFULL + g % C::STAGES), (g / C::STAGES) & 1, a.status, a.wait_limit_ns);
-    for (int g = max(0, last_v - C::STAGES + 1); g <= last_v; ++g)
-      wait_warp(BAR(B_VFULL + g % C::STAGES), (g / C::STAGES) & 1, a.status, a.wait_limit_ns);
-    if (answered < asked) wait_warp(BAR(B_CANCEL), answered & 1, a.status, a.wait_limit_ns);
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    const uint32_t leader = elect_one();
-    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
-    constexpr uint32_t idesc_o = idesc_bf16_f32(128, D, false, true);
-    const uint64_t dQ0 = sdesc_sw128(sbase + C::OFF_Q, 16, 1024);
-    const uint64_t dK0 = sdesc_sw128(sbase + C::OFF_K, 16, 1024);
-    const uint64_t dV0 = sdesc_sw128(sbase + C::OFF_V, C::CHUNK_BYTES, 1024);
-    auto wait = [&](int b, uint32_t parity) { return wait_warp(BAR(b), parity, a.status, a.wait_limit_ns); };
-    // S of tile t against the keys in slot s; `last`: the block's last for this tile
-    auto issue_s = [&](int t, int s, bool last) {
-      const uint64_t qa = dQ0 + (uint64_t)((t * C::TILE_BYTES) >> 4);
-      const uint64_t kb = dK0 + (uint64_t)((s * C::TILE_BYTES) >> 4);
-      const uint32_t dcol = tmem + C::S_COL(t);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint64_t off = (uint64_t)(((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32) >> 4);
-        mma_ss(dcol, qa + off, kb + off, idesc_s, kk > 0 ? 1u : 0u, leader);
-      }
-      mma_commit(BAR(B_SFULL + t), leader);
-      if (last) mma_commit(BAR(B_QEMPTY + t), leader);
-    };
-    // P V over a whole tile, and over the first `keys` keys (those that the
-    // tile's last query sees) in steps of 16
-    auto issue_pv = [&](int t, int s, bool acc) {
-      const uint64_t vb = dV0 + (uint64_t)((s * C::TILE_BYTES) >> 4);
-      const uint32_t dcol = tmem + C::O_COL(t), acol = tmem + C::P_COL(t);
-#pragma unroll
-      for (int kk = 0; kk < C::BN / 16; ++kk)
-        mma_ts(dcol, acol + kk * 8, vb + (uint64_t)((kk * 2048) >> 4), idesc_o, (acc || kk > 0) ? 1u : 0u, leader);
-      mma_commit(BAR(B_ODONE + t), leader);
-    };
-    auto issue_pv_keys = [&](int t, int s, bool acc, int keys) {
-      const uint64_t vb = dV0 + (uint64_t)((s * C::TILE_BYTES) >> 4);
-      const uint32_t dcol = tmem + C::O_COL(t), acol = tmem + C::P_COL(t);
-#pragma unroll 1
-      for (int kk = 0; kk < C::BN / 16 && 16 * kk < keys; ++kk)
-        mma_ts(dcol, acol + kk * 8, vb + (uint64_t)((kk * 2048) >> 4), idesc_o, (acc || kk > 0) ? 1u : 0u, leader);
-      mma_commit(BAR(B_ODONE + t), leader);
-    };
-    // V has landed in slot s with `keys` keys of the sequence: rows behind them
-    // that the last step would read become zero.
-    auto clean_v = [&](int s, int keys) {
-      if (keys < C::BN && (keys & 15) != 0) {
-        const int n_rows = 16 - (keys & 15);
-        for (int e = lane; e < n_rows * C::CH * 8; e += 32) {
-          const int r = keys + e / (C::CH * 8), u = e % (C::CH * 8);
-          *reinterpret_cast<uint4*>(smem + C::OFF_V + s * C::TILE_BYTES + (u >> 3) * C::CHUNK_BYTES + r * 128 +
-                                    (u & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-    };
-    PromptItem it;
-    bool ok = get_item(0, it);
-    int g0 = 0;              // key tiles before this block
-    int c0 = 0, c1 = 0;      // key tiles of query tiles 0 and 1 before it
-    int q0_used = 0, q1_used = 0;  // blocks with such a tile before it
-    int s_done = 0;  // bit t: the block's first S of tile t has been issued
-    // The first S of tile t of block `b`, whose keys begin at ring position g
-    // (`now`: only if its operands are there).
-    auto first_s = [&](int t, const PromptItem& b, int g, int c, bool now) {
-      const int nt = b.n_of(t);
-      if (nt == 0 || (s_done >> t & 1)) return true;
-      const int s = g % C::STAGES;
-      const uint32_t pk = (g / C::STAGES) & 1, pq = (t == 0 ? q0_used : q1_used) & 1;
-      if (now && !__all_sync(0xffffffffu, mbar_test(BAR(B_KFULL + s), pk) && mbar_test(BAR(B_QFULL + t), pq)))
-        return true;
-      if (!now && !(wait(B_KFULL + s, pk) && wait(B_QFULL + t, pq))) return false;
-      if (C::P_OWN && c > 0 && !wait(B_SFREE + t, (c - 1) & 1)) return false;
-      tc_fence_after();
-      issue_s(t, s, nt == 1);
-      if (t == 0) ++q0_used;
-      else ++q1_used;
-      s_done |= 1 << t;
-      return true;
-    };
-    for (int i = 0; ok && it.n0 >= 0; ++i) {
-      const int n_max = max(it.n0, it.n1), past = it.m - it.n;
-      PromptItem next;
-      next.n0 = -1;
-      bool fetched = false;
-#pragma unroll 1
-      for (int t = 0; ok && t < C::QT; ++t) ok = first_s(t, it, g0, t == 0 ? c0 : c1, false);
-      if (!ok) break;
-      s_done = 0;
-      if (n_max > 0) mma_commit(BAR(B_KEMPTY + g0 % C::STAGES), leader);
-      const int seen0 = past + min(it.n, it.tok0 + TP) - it.kt0 * C::BN;  // keys from kt0 on that tile 0's last query sees
-      const int seen1 = past + min(it.n, it.tok0 + 2 * TP) - it.kt0 * C::BN;
-      // The tiles that neither query tile ends near: whole keys, a next S for
-      // both. The loop is kept short (a wait and sixteen products per tile):
-      // what its warp does between two waits, and what it does to the
-      // instruction cache, is on the path from one softmax to the next
-      // (16384 tokens, 32 heads, d = 128: 1385 TFLOP/s with the last tiles'
-      // cases in it).
-      const int n_lean = min(it.n0, it.n1) - 2;
-      int j = 0;
-#pragma unroll 1
-      for (; j < n_lean; ++j) {
-        if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
-        const int g = g0 + j, s = g % C::STAGES, s1 = (g + 1) % C::STAGES;
-        const uint32_t ph1 = ((g + 1) / C::STAGES) & 1;
-        if constexpr (!C::P_OWN) ok = wait(B_VFULL + s, (g / C::STAGES) & 1);
-#pragma unroll
-        for (int t = 0; t < C::QT; ++t) {
-          const uint32_t pt = (uint32_t)((t == 0 ? c0 : c1) + j) & 1u;
-          if constexpr (C::P_OWN) {
-            ok = ok && wait(B_SFREE + t, pt);
-            if (t == 0) ok = ok && wait(B_KFULL + s1, ph1);
-            if (!ok) break;
-            tc_fence_after();
-            issue_s(t, s1, false);
-            ok = wait(B_PFULL + t, pt);
-            if (t == 0) ok = ok && wait(B_VFULL + s, (g / C::STAGES) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv(t, s, j > 0);
-          } else {
-            ok = ok && wait(B_PFULL + t, pt);
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv(t, s, j > 0);
-            if (t == 0) {
-              ok = wait(B_KFULL + s1, ph1);
-              if (!ok) break;
-              tc_fence_after();
-            }
-            issue_s(t, s1, false);
-          }
         }
         if (!ok) break;
-        mma_commit(BAR(B_VEMPTY + s), leader);
-        mma_commit(BAR(B_KEMPTY + s1), leader);
+        PromptBlock b;
+        int part = 0;
+        if (u >= 0 && !prompt_block(a, u, lane, u == 0, b, part)) u = -1;
+        if (lane == 0) {
+          volatile int* d = items + s * C::ITEM_INTS;
+          d[kItQ0] = b.v.q0;
+          d[kItN] = b.v.n;
+          d[kItHead] = b.head;
+          d[kItTok0] = b.tok0;
+          d[kItKt0] = b.kt0;
+          d[kItN0] = u >= 0 ? b.n0 : -1;
+          d[kItN1] = b.n1;
+          d[kItPart] = b.unit * a.splits + part;
+          d[kItK0] = b.v.k0;
+          d[kItSeq] = b.seq;
+          d[kItFirst] = b.v.m - b.v.n + b.tok0 + 1 - b.kt0 * C::BN;
+          d[kItLeft] = b.v.m - b.kt0 * C::BN;
+          mbar_arrive(BAR(B_ITF + s));
+        }
+        __syncwarp();
       }
-      if (!ok) break;
-#pragma unroll 1
-      for (; j < n_max; ++j) {
-        if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
-        const int g = g0 + j, s = g % C::STAGES, s1 = (g + 1) % C::STAGES;
-        const uint32_t ph = (g / C::STAGES) & 1, ph1 = ((g + 1) / C::STAGES) & 1;
-        bool k_next = false, v_here = false;  // K_{j+1}, V_j have landed
-        auto need_v = [&]() {
-          if (!v_here) {
-            if (!wait(B_VFULL + s, ph)) return false;
-            clean_v(s, it.m - (it.kt0 + j) * C::BN);
+      if (!ok) *abort_flag = 1;
+    } else if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      // One lane issues the packed tensors' boxes; a paged cache's boxes have a
+      // lane each (box `box` of the 64-column chunk `chunk` of a tile).
+      const int nbox = PAGED ? C::BN / a.box_rows : 1;
+      const bool mine = PAGED ? lane < nbox * C::CH : lane == 0;
+      const int box = PAGED ? lane % nbox : 0, chunk = PAGED ? lane / nbox : 0;
+      if (lane == 0) {
+        tma_prefetch_desc(&a.tmQ);
+        tma_prefetch_desc(&a.tmK);
+        tma_prefetch_desc(&a.tmV);
+      }
+      bool ok = true;
+      int g0 = 0, q0_used = 0, q1_used = 0;        // key tiles, and loads of each Q slot, before this block
+      int last_k = -1, last_v = -1, skipped = -1;  // last tiles whose loads were issued, by ring position
+      for (int i = 0; ok; ++i) {
+        if (!get_item(i)) { ok = false; break; }
+        const int n0 = item(i, kItN0), n1 = item(i, kItN1), n_max = max(n0, n1);
+        if (n0 < 0) break;
+        const int kt0 = item(i, kItKt0), left = item(i, kItLeft), head = item(i, kItHead);
+        const int key0 = item(i, kItK0) + kt0 * C::BN, tok = item(i, kItQ0) + item(i, kItTok0);
+        const int* table = PAGED ? a.block_tables + (size_t)item(i, kItSeq) * a.max_pages : nullptr;
+        auto look_up = [&](int j, int& page, int& row) {
+          page = -1;
+          row = 0;
+          if constexpr (PAGED) {
+            const int key = j * C::BN + box * a.box_rows;  // from kt0 on
+            if (mine && key < left) {
+              const int at = kt0 * C::BN + key, pi = at / a.pool.page_size;
+              row = at - pi * a.pool.page_size;
+              page = __ldg(table + pi);
+              if (page < 0 || page >= a.pool.num_pages) {
+                report_status(a.status, kStatusBadSeqlens);
+                page = a.pool.num_pages;  // outside the tensor: reads as zeros
+              }
+            }
           }
-          return v_here = true;
         };
-        auto next_s = [&](int t) {
-          if (!k_next && !wait(B_KFULL + s1, ph1)) return false;
-          k_next = true;
-          tc_fence_after();
-          issue_s(t, s1, j + 2 == it.n_of(t));
+        // bytes of a tile's boxes that hold keys of the sequence
+        auto tile_bytes = [&](int j) {
+          if constexpr (!PAGED) return (uint32_t)C::TILE_BYTES;
+          const int keys = left - j * C::BN;
+          const int boxes = keys >= C::BN ? nbox : (keys + a.box_rows - 1) / a.box_rows;
+          return (uint32_t)(boxes * a.box_rows * 128 * C::CH);
+        };
+        auto load = [&](const CUtensorMap* map, int off, int bar, int s, int j, int page, int row) {
+          const uint32_t dst = sbase + off + s * C::TILE_BYTES;
+          if constexpr (PAGED) {
+            if (page >= 0)
+              tma_load_4d(dst + chunk * C::CHUNK_BYTES + box * a.box_rows * 128, map, BAR(bar + s), chunk * 64, row, head, page);
+          } else if (lane == 0) {
+            for (int c = 0; c < C::CH; ++c)
+              tma_load_3d(dst + c * C::CHUNK_BYTES, map, BAR(bar + s), c * 64, key0 + j * C::BN, head);
+          }
+        };
+        auto load_q = [&](int t, int& used) {  // once the block before has read the slot
+          if ((t == 0 ? n0 : n1) == 0) return true;
+          if (used > 0 && !wait(B_QEMPTY + t, (used - 1) & 1)) return false;
+          ++used;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(BAR(B_QFULL + t), (uint32_t)(RT * 128 * C::CH));
+            for (int c = 0; c < C::CH; ++c)
+              tma_load_4d(sbase + C::OFF_Q + (t * C::CH + c) * C::CHUNK_BYTES, &a.tmQ, BAR(B_QFULL + t), c * 64, 0,
+                          tok + t * TP, head);
+          }
+          __syncwarp();
           return true;
         };
-#pragma unroll 1
-        for (int t = 0; t < C::QT; ++t) {
-          const uint32_t pt = (uint32_t)((t == 0 ? c0 : c1) + j) & 1u;
-          if (j < it.n_of(t)) {
-            const bool more = j + 1 < it.n_of(t);
-            const int keys = (t == 0 ? seen0 : seen1) - j * C::BN;
-            if constexpr (C::P_OWN) {
-              // P has its own columns: S_{j+1} goes first, P_j V_j follows
-              if (more && !(wait(B_SFREE + t, pt) && next_s(t))) { ok = false; break; }
-              if (!wait(B_PFULL + t, pt) || !need_v()) { ok = false; break; }
-              tc_fence_after();
-              issue_pv_keys(t, s, j > 0, keys);
-            } else {
-              // P overwrites S: P_j V_j must be issued before S_{j+1}
-              if (!need_v() || !wait(B_PFULL + t, pt)) { ok = false; break; }
-              tc_fence_after();
-              issue_pv_keys(t, s, j > 0, keys);
-              if (more && !next_s(t)) { ok = false; break; }
-            }
+        int page, row;
+        look_up(0, page, row);
+        for (int j = 0; j < n_max; ++j) {
+          if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
+          const int g = g0 + j, s = g % C::STAGES;
+          const uint32_t ph = (g / C::STAGES) & 1;
+          int next_page = -1, next_row = 0;
+          if (j + 1 < n_max) look_up(j + 1, next_page, next_row);
+          if (!wait(B_KEMPTY + s, ph ^ 1)) { ok = false; break; }
+          if (g != a.debug_skip_kv) {
+            if (lane == 0) mbar_arrive_expect_tx(BAR(B_KFULL + s), tile_bytes(j));
+            __syncwarp();
+            load(&a.tmK, C::OFF_K, B_KFULL, s, j, page, row);
+          } else {
+            skipped = g;
           }
-          if (j + 1 == n_max) {
-            // this tile is done with the block: the next block's first S, if
-            // its operands are there already
-            if (!fetched && !get_item(i + 1, next)) { ok = false; break; }
-            fetched = true;
-            if (next.n0 >= 0 && !first_s(t, next, g0 + n_max, (t == 0 ? c0 : c1) + it.n_of(t), true)) {
-              ok = false;
-              break;
-            }
-          }
+          last_k = g;
+          if (j == 0 && !(load_q(0, q0_used) && load_q(1, q1_used))) { ok = false; break; }
+          if (!wait(B_VEMPTY + s, ph ^ 1)) { ok = false; break; }
+          if (lane == 0) mbar_arrive_expect_tx(BAR(B_VFULL + s), tile_bytes(j));
+          __syncwarp();
+          load(&a.tmV, C::OFF_V, B_VFULL, s, j, page, row);
+          last_v = g;
+          page = next_page;
+          row = next_row;
         }
         if (!ok) break;
-        mma_commit(BAR(B_VEMPTY + s), leader);
-        if (j + 1 < n_max) mma_commit(BAR(B_KEMPTY + s1), leader);
+        g0 += n_max;
+        release_item(i);
       }
-      if (!ok || (!fetched && !get_item(i + 1, next))) { ok = false; break; }
-      release_item(i);
-      g0 += n_max;
-      c0 += it.n_of(0);
-      c1 += it.n_of(1);
-      it = next;
+      if (!ok) *abort_flag = 1;
+      // drain: what was asked for last must have landed before exit
+      if (q0_used > 0) wait(B_QFULL + 0, (q0_used - 1) & 1);
+      if (q1_used > 0) wait(B_QFULL + 1, (q1_used - 1) & 1);
+      for (int g = max(0, last_k - C::STAGES + 1); g <= last_k; ++g)
+        if (g != skipped) wait(B_KFULL + g % C::STAGES, (g / C::STAGES) & 1);
+      for (int g = max(0, last_v - C::STAGES + 1); g <= last_v; ++g) wait(B_VFULL + g % C::STAGES, (g / C::STAGES) & 1);
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer
+      const uint32_t leader = elect_one();
+      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
+      constexpr uint32_t idesc_o = idesc_bf16_f32(128, D, false, true);
+      const uint64_t dQ0 = sdesc_sw128(sbase + C::OFF_Q, 16, 1024);
+      const uint64_t dK0 = sdesc_sw128(sbase + C::OFF_K, 16, 1024);
+      const uint64_t dV0 = sdesc_sw128(sbase + C::OFF_V, C::CHUNK_BYTES, 1024);
+      // S of tile t against the keys in slot s; `last`: the block's last for this tile
+      auto issue_s = [&](int t, int s, bool last) {
+        const uint64_t qa = dQ0 + (uint64_t)((t * C::TILE_BYTES) >> 4);
+        const uint64_t kb = dK0 + (uint64_t)((s * C::TILE_BYTES) >> 4);
+        const uint32_t dcol = tmem + C::S_COL(t);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t off = (uint64_t)(((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32) >> 4);
+          mma_ss(dcol, qa + off, kb + off, idesc_s, kk > 0 ? 1u : 0u, leader);
+        }
+        mma_commit(BAR(B_SFULL + t), leader);
+        if (last) mma_commit(BAR(B_QEMPTY + t), leader);
+      };
+      // P V over a whole tile, and over the first `keys` keys (those that the
+      // tile's last query sees) in steps of 16
+      auto issue_pv = [&](int t, int s, bool acc) {
+        const uint64_t vb = dV0 + (uint64_t)((s * C::TILE_BYTES) >> 4);
+        const uint32_t dcol = tmem + C::O_COL(t), acol = tmem + C::P_COL(t);
+#pragma unroll
+        for (int kk = 0; kk < C::BN / 16; ++kk)
+          mma_ts(dcol, acol + kk * 8, vb + (uint64_t)((kk * 2048) >> 4), idesc_o, (acc || kk > 0) ? 1u : 0u, leader);
+        mma_commit(BAR(B_ODONE + t), leader);
+      };
+      auto issue_pv_keys = [&](int t, int s, bool acc, int keys) {
+        const uint64_t vb = dV0 + (uint64_t)((s * C::TILE_BYTES) >> 4);
+        const uint32_t dcol = tmem + C::O_COL(t), acol = tmem + C::P_COL(t);
+#pragma unroll 1
+        for (int kk = 0; kk < C::BN / 16 && 16 * kk < keys; ++kk)
+          mma_ts(dcol, acol + kk * 8, vb + (uint64_t)((kk * 2048) >> 4), idesc_o, (acc || kk > 0) ? 1u : 0u, leader);
+        mma_commit(BAR(B_ODONE + t), leader);
+      };
+      // V has landed in slot s with `keys` keys of the sequence: rows behind them
+      // that the last step would read become zero.
+      auto clean_v = [&](int s, int keys) {
+        if (keys < C::BN && (keys & 15) != 0) {
+          const int n_rows = 16 - (keys & 15);
+          for (int e = lane; e < n_rows * C::CH * 8; e += 32) {
+            const int r = keys + e / (C::CH * 8), u = e % (C::CH * 8);
+            *reinterpret_cast<uint4*>(smem + C::OFF_V + s * C::TILE_BYTES + (u >> 3) * C::CHUNK_BYTES + r * 128 +
+                                      (u & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+      };
+      bool ok = get_item(0);
+      int n0 = item(0, kItN0), n1 = item(0, kItN1);  // key tiles of the block's query tiles
+      int g0 = 0;              // key tiles before this block
+      int c0 = 0, c1 = 0;      // key tiles of query tiles 0 and 1 before it
+      int q0_used = 0, q1_used = 0;  // blocks with such a tile before it
+      int s_done = 0;  // bit t: the block's first S of tile t has been issued
+      // The first S of tile t (of nt key tiles) of a block whose keys begin at ring position g
+      // (`now`: only if its operands are there).
+      auto first_s = [&](int t, int nt, int g, int c, bool now) {
+        if (nt == 0 || (s_done >> t & 1)) return true;
+        const int s = g % C::STAGES;
+        const uint32_t pk = (g / C::STAGES) & 1, pq = (t == 0 ? q0_used : q1_used) & 1;
+        if (now && !__all_sync(0xffffffffu, mbar_test(BAR(B_KFULL + s), pk) && mbar_test(BAR(B_QFULL + t), pq)))
+          return true;
+        if (!now && !(wait(B_KFULL + s, pk) && wait(B_QFULL + t, pq))) return false;
+        if (C::P_OWN && c > 0 && !wait(B_SFREE + t, (c - 1) & 1)) return false;
+        tc_fence_after();
+        issue_s(t, s, nt == 1);
+        if (t == 0) ++q0_used;
+        else ++q1_used;
+        s_done |= 1 << t;
+        return true;
+      };
+      for (int i = 0; ok && n0 >= 0; ++i) {
+        const int n_max = max(n0, n1);
+        int next0 = -1, next1 = 0;
+        bool fetched = false;
+        auto fetch = [&]() {
+          if (!fetched && !get_item(i + 1)) return false;
+          next0 = item(i + 1, kItN0);
+          next1 = item(i + 1, kItN1);
+          return fetched = true;
+        };
+#pragma unroll 1
+        for (int t = 0; ok && t < C::QT; ++t) ok = first_s(t, t == 0 ? n0 : n1, g0, t == 0 ? c0 : c1, false);
+        if (!ok) break;
+        s_done = 0;
+        // the accumulators have left tensor memory (the block's first P V is at
+        // least a softmax away)
+        if (n0 > 0 && q0_used > 1) ok = wait(B_OFREE + 0, q0_used & 1);
+        if (n1 > 0 && q1_used > 1) ok = ok && wait(B_OFREE + 1, q1_used & 1);
+        if (!ok) break;
+        if (n_max > 0) mma_commit(BAR(B_KEMPTY + g0 % C::STAGES), leader);
+        // The tiles that neither query tile ends near: whole keys, a next S for
+        // both. The loop is kept short (a wait and sixteen products per tile):
+        // what its warp does between two waits, and what it does to the
+        // instruction cache, is on the path from one softmax to the next
+        // (16384 tokens, 32 heads, d = 128: 1385 TFLOP/s with the last tiles'
+        // cases in it).
+        const int n_lean = min(n0, n1) - 2;
+        int j = 0;
+#pragma unroll 1
+        for (; j < n_lean; ++j) {
+          if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
+          const int g = g0 + j, s = g % C::STAGES, s1 = (g + 1) % C::STAGES;
+          const uint32_t ph1 = ((g + 1) / C::STAGES) & 1;
+          if constexpr (!C::P_OWN) ok = wait(B_VFULL + s, (g / C::STAGES) & 1);
+#pragma unroll
+          for (int t = 0; t < C::QT; ++t) {
+            const uint32_t pt = (uint32_t)((t == 0 ? c0 : c1) + j) & 1u;
+            if constexpr (C::P_OWN) {
+              ok = ok && wait(B_SFREE + t, pt);
+              if (t == 0) ok = ok && wait(B_KFULL + s1, ph1);
+              if (!ok) break;
+              tc_fence_after();
+              issue_s(t, s1, false);
+              ok = wait(B_PFULL + t, pt);
+              if (t == 0) ok = ok && wait(B_VFULL + s, (g / C::STAGES) & 1);
+              if (!ok) break;
+              tc_fence_after();
+              issue_pv(t, s, j > 0);
+            } else {
+              ok = ok && wait(B_PFULL + t, pt);
+              if (!ok) break;
+              tc_fence_after();
+              issue_pv(t, s, j > 0);
+              if (t == 0) {
+                ok = wait(B_KFULL + s1, ph1);
+                if (!ok) break;
+                tc_fence_after();
+              }
+              issue_s(t, s1, false);
+            }
+          }
+          if (!ok) break;
+          mma_commit(BAR(B_VEMPTY + s), leader);
+          mma_commit(BAR(B_KEMPTY + s1), leader);
+        }
+        if (!ok) break;
+#pragma unroll 1
+        for (; j < n_max; ++j) {
+          if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
+          const int g = g0 + j, s = g % C::STAGES, s1 = (g + 1) % C::STAGES;
+          const uint32_t ph = (g / C::STAGES) & 1, ph1 = ((g + 1) / C::STAGES) & 1;
+          bool k_next = false, v_here = false;  // K_{j+1}, V_j have landed
+          auto need_v = [&]() {
+            if (!v_here) {
+              if (!wait(B_VFULL + s, ph)) return false;
+              clean_v(s, item(i, kItLeft) - j * C::BN);
+            }
+            return v_here = true;
+          };
+          auto next_s = [&](int t) {
+            if (!k_next && !wait(B_KFULL + s1, ph1)) return false;
+            k_next = true;
+            tc_fence_after();
+            issue_s(t, s1, j + 2 == (t == 0 ? n0 : n1));
+            return true;
+          };
+#pragma unroll 1
+          for (int t = 0; t < C::QT; ++t) {
+            const uint32_t pt = (uint32_t)((t == 0 ? c0 : c1) + j) & 1u;
+            const int nt = t == 0 ? n0 : n1;
+            if (j < nt) {
+              const bool more = j + 1 < nt;
+              // keys of this tile that the query tile's last query sees
+              const int keys = min(item(i, kItFirst) - 1 + (t + 1) * TP, item(i, kItLeft)) - j * C::BN;
+              if constexpr (C::P_OWN) {
+                // P has its own columns: S_{j+1} goes first, P_j V_j follows
+                if (more && !(wait(B_SFREE + t, pt) && next_s(t))) { ok = false; break; }
+                if (!wait(B_PFULL + t, pt) || !need_v()) { ok = false; break; }
+                tc_fence_after();
+                issue_pv_keys(t, s, j > 0, keys);
+              } else {
+                // P overwrites S: P_j V_j must be issued before S_{j+1}
+                if (!need_v() || !wait(B_PFULL + t, pt)) { ok = false; break; }
+                tc_fence_after();
+                issue_pv_keys(t, s, j > 0, keys);
+                if (more && !next_s(t)) { ok = false; break; }
+              }
+            }
+            if (j + 1 == n_max) {
+              // this tile is done with the block: the next block's first S, if
+              // its operands are there already
+              if (!fetch()) { ok = false; break; }
+              if (next0 >= 0 && !first_s(t, t == 0 ? next0 : next1, g0 + n_max, (t == 0 ? c0 : c1) + nt, true)) {
+                ok = false;
+                break;
+              }
+            }
+          }
+          if (!ok) break;
+          mma_commit(BAR(B_VEMPTY + s), leader);
+          if (j + 1 < n_max) mma_commit(BAR(B_KEMPTY + s1), leader);
+        }
+        if (!ok || !fetch()) { ok = false; break; }
+        release_item(i);
+        g0 += n_max;
+        c0 += n0;
+        c1 += n1;
+        n0 = next0;
+        n1 = next1;
+      }
+      if (!ok && lane == 0) *abort_flag = 1;
+      // drain every MMA issued before TMEM can be released
+      mma_commit(BAR(B_DRAIN), leader);
+      wait(B_DRAIN, 0);
     }
-    if (!ok && lane == 0) *abort_flag = 1;
-    // drain every MMA issued before TMEM can be released
-    mma_commit(BAR(B_DRAIN), leader);
-    wait(B_DRAIN, 0);
-  } else {
-    // ------------------------------------------------------------ softmax
-    const int t = (warp - C::SW0) >> 2;  // query tile of this warpgroup
+  } else if (warp < 12) {
+    set_max_registers_inc<C::R_SOFTMAX>();
+    // -------------------------------------------------------------- softmax
+    const int t = (warp - 4) >> 2;  // query tile of this warpgroup
     const int wq = warp & 3;             // TMEM lane quarter
     const int row = wq * 32 + lane;      // row of the tile
     const uint32_t lane_addr = tmem + ((uint32_t)(wq * 32) << 16);
@@ -561,14 +583,11 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) prompt_fwd_kernel(const
     int c = 0;  // key tiles of this query tile before the block
     for (int i = 0; ok; ++i) {
       int n_own, sees, first;  // keys from kt0 on that this row and the tile's first row see
-      {
-        PromptItem it;
-        if (!get_item(i, it)) { ok = false; break; }
-        if (it.n0 < 0) break;
-        n_own = it.n_of(t);
-        first = it.m - it.n + it.tok0 + t * TP + 1 - it.kt0 * C::BN;
-        sees = min(first + a.g_div(row), it.m - it.kt0 * C::BN);
-      }
+      if (!get_item(i)) { ok = false; break; }
+      if (item(i, kItN0) < 0) break;
+      n_own = item(i, t == 0 ? kItN0 : kItN1);
+      first = item(i, kItFirst) + t * TP;
+      sees = min(first + a.g_div(row), item(i, kItLeft));
       float m_ref = -INFINITY, l = 0.f;
       for (int j = 0; j < n_own; ++j) {
         if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
@@ -579,23 +598,30 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) prompt_fwd_kernel(const
         // masked columns here
         const bool mask_tile = first - j * C::BN < C::BN;
         const int valid = sees - j * C::BN;
-        if (mask_tile) {
-          // masked scores are replaced where they stand, a few tiles to a block:
-          // no mask in the pass below
+        if (mask_tile || j == 0) {
+          // A few tiles to a block: masked scores are replaced where they stand
+          // (no mask in the pass below), and the first tile's maximum is the
+          // row's first reference.
+          float top = -INFINITY;
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             uint32_t r[32];
             tmem_ld32(s_addr + 32 * q, r);
             tmem_ld_wait();
-            mask_cols32(r, 32 * q, valid);
-            tmem_st32(s_addr + 32 * q, r);
+            if (mask_tile) {
+              mask_cols32(r, 32 * q, valid);
+              tmem_st32(s_addr + 32 * q, r);
+            }
+#pragma unroll
+            for (int u = 0; u < 16; ++u) top = fmax3(top, __uint_as_float(r[2 * u]), __uint_as_float(r[2 * u + 1]));
           }
-          tmem_st_wait();
+          if (j == 0) m_ref = top * c2;
+          if (mask_tile) tmem_st_wait();
         }
         // The speculative pass against the reference max of the tiles before, the
         // tile's own max alongside; a tile whose max exceeds it by more than
-        // kRescaleLog2 is done again (the first always is). A row that has met no
-        // key yet has m_ref = -inf: what is added to its scores, -inf, is 0.
+        // kRescaleLog2 is done again. A row that has met no key yet has m_ref =
+        // -inf: what is added to its scores, -inf, is 0.
         float mx[4];
         uint64_t sm2[4];
         float alpha = 1.f;
@@ -608,7 +634,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) prompt_fwd_kernel(const
           const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
           const uint64_t nm2 = f2_pack(neg, neg);
           if constexpr (C::P_OWN) {
-            ok = softmax_pass_own_p<true>(s_addr, lane_addr + C::P_COL(t), false, 0, c22, nm2, mx, sm2, j > 0 && !moved,
+            ok = softmax_pass_own_p<true>(s_addr, lane_addr + C::P_COL(t), false, 0, c22, nm2, mx, sm2, c + j > 0 && !moved,
                                           BAR(B_ODONE + t), (uint32_t)(c + j - 1) & 1u, a.status, a.wait_limit_ns);
             if (!ok) break;
           } else {
@@ -671,89 +697,122 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1) prompt_fwd_kernel(const
       tmem_st_wait();  // no TMEM store may be in flight when the loop is left early
       if (!ok) break;
       c += n_own;
-      if (n_own > 0) {
-        const bool w = wait_phase(BAR(B_ODONE + t), (c - 1) & 1, a.status, a.wait_limit_ns);
-        if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+      // the row's statistics, for the output warps
+      reinterpret_cast<float2*>(smem + C::OFF_STAT)[((i & 1) * 2 + t) * 128 + row] = make_float2(m_ref, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(B_LFULL + 2 * t + (i & 1)));
+      release_item(i);
+    }
+    if (!ok) *abort_flag = 1;
+  } else {
+    set_max_registers_dec<C::R_OUT>();
+    // -------------------------------------------------------------- output
+    // O of both tiles leaves tensor memory here, so that the softmax warps go on
+    // to the next block at once.
+    const int wq = warp & 3;
+    const uint32_t lane_addr = tmem + ((uint32_t)(wq * 32) << 16);
+    const int row = wq * 32 + lane;
+    uint8_t* stage = smem + C::OFF_STAGE + wq * C::STAGE_BYTES;  // [32 rows][128 bytes]
+    const int rsub = lane >> 3, unit = lane & 7;
+    bool ok = true;
+    int c0 = 0, c1 = 0;  // key tiles of query tiles 0 and 1 before the block
+    for (int i = 0; ok; ++i) {
+      if (!get_item(i)) { ok = false; break; }
+      const int n0 = item(i, kItN0), n1 = item(i, kItN1);
+      if (n0 < 0) break;
+      c0 += n0;
+      c1 += n1;
+      const int n = item(i, kItN);
+#pragma unroll 1
+      for (int t = 0; t < 2; ++t) {
+        const int n_own = t == 0 ? n0 : n1, tok0 = item(i, kItTok0) + t * TP;
+        // the row's statistics, then its last P V (in this order: the barrier
+        // of the latter can be a phase behind until the former are there)
+        if (!wait(B_LFULL + 2 * t + (i & 1), (i >> 1) & 1)) { ok = false; break; }
+        const float2 ml = reinterpret_cast<const float2*>(smem + C::OFF_STAT)[((i & 1) * 2 + t) * 128 + row];
+        if (n_own > 0 && !wait(B_ODONE + t, ((t == 0 ? c0 : c1) - 1) & 1)) { ok = false; break; }
         tc_fence_after();
-      }
-      // The warp's 32 rows leave through its staging buffer, 128 bytes of each
-      // at a time in the swizzle that spreads them over the banks, read back so
-      // that a store instruction writes whole 128-byte rows. The next block's
-      // first P V comes after this warp's next p_full arrival, so the
-      // accumulator is safe until then.
-      PromptItem it;
-      get_item(i, it);  // again: keeps the loop's registers free
-      const int n = it.n, tok0 = it.tok0 + t * TP;  // tok0: first token of the tile
-      if (tok0 < n) {
-        uint8_t* stage = smem + C::OFF_STAGE + (warp - C::SW0) * C::STAGE_BYTES;  // [32 rows][128 bytes]
-        const float inv_l = l == 0.f ? 0.f : 1.f / l;
-        const float lse2 = m_ref + __log2f(l);  // -inf for a row without keys
-        const int rsub = lane >> 3, unit = lane & 7;
-        // one 32-column piece of this row of O, normalised; zeros without keys
-        auto read_o = [&](int q, float (&x)[32]) {
-          uint32_t r[32];
-          if (n_own > 0) {
-            tmem_ld32(o_addr + 32 * q, r);
-            tmem_ld_wait();
-          }
-#pragma unroll
-          for (int u = 0; u < 32; ++u) x[u] = n_own > 0 && l != 0.f ? __uint_as_float(r[u]) * inv_l : 0.f;
+        const float l = ml.y, inv_l = l == 0.f ? 0.f : 1.f / l;
+        const float lse2 = ml.x + __log2f(l);  // -inf for a row without keys
+        const bool any = n_own > 0, some = any && l != 0.f;
+        const uint32_t o_addr = lane_addr + C::O_COL(t);
+        auto free_o = [&]() {  // the tensor memory has been read
+          tc_fence_before();
+          __syncwarp();
+          if (any && lane == 0) mbar_arrive(BAR(B_OFREE + t));
         };
         if (a.splits > 1) {
           // fp32 rows of this key range; a range without keys leaves only its log-sum-exp
-          const long long prow0 = (long long)it.part_row * (2 * C::BM) + t * C::BM + wq * 32;
-          a.Lpart[prow0 + lane] = lse2;
-          if (n_own > 0) {
+          const long long prow0 = (long long)item(i, kItPart) * (2 * C::BM) + t * C::BM + wq * 32;
+          if (tok0 < n) a.Lpart[prow0 + lane] = lse2;
+          if (any) {
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
-              float x[32];
-              read_o(q, x);
+              uint32_t r[32];
+              tmem_ld32(o_addr + 32 * q, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int u = 0; u < 32; ++u) r[u] = some ? __float_as_uint(__uint_as_float(r[u]) * inv_l) : 0u;
 #pragma unroll
               for (int u = 0; u < 8; ++u)
-                *reinterpret_cast<float4*>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) =
-                    make_float4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
+                *reinterpret_cast<uint4*>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) =
+                    make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
               __syncwarp();
 #pragma unroll
               for (int u = 0; u < 8; ++u) {
-                const int r = 4 * u + rsub;
-                const float4 y = *reinterpret_cast<const float4*>(stage + r * 128 + ((unit ^ (r & 7)) << 4));
-                *reinterpret_cast<float4*>(a.Opart + (prow0 + r) * D + 32 * q + 4 * unit) = y;
+                const int rr = 4 * u + rsub;
+                const float4 y = *reinterpret_cast<const float4*>(stage + rr * 128 + ((unit ^ (rr & 7)) << 4));
+                *reinterpret_cast<float4*>(a.Opart + (prow0 + rr) * D + 32 * q + 4 * unit) = y;
               }
               __syncwarp();
             }
           }
-        } else {
-#pragma unroll 1
-          for (int h = 0; h < D / 64; ++h) {
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              float x[32];
-              read_o(2 * h + hh, x);
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * hh + u) ^ (lane & 7)) << 4)) =
-                    make_uint4(pack_bf16x2(x[8 * u], x[8 * u + 1]), pack_bf16x2(x[8 * u + 2], x[8 * u + 3]),
-                               pack_bf16x2(x[8 * u + 4], x[8 * u + 5]), pack_bf16x2(x[8 * u + 6], x[8 * u + 7]));
-            }
-            __syncwarp();
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              const int r = 4 * u + rsub, tr = wq * 32 + r, tk = a.g_div(tr);
-              const uint4 y = *reinterpret_cast<const uint4*>(stage + r * 128 + ((unit ^ (r & 7)) << 4));
-              if (tr < RT && tok0 + tk < n)
-                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.O) + (long long)(it.q0 + tok0 + tk) * a.o_stride +
-                                          (long long)(it.head * a.G + tr - tk * a.G) * D + 64 * h + 8 * unit) = y;
-            }
-            __syncwarp();
-          }
-          const int tok_in = a.g_div(row);
-          if (row < RT && tok0 + tok_in < n)
-            a.LSE[(size_t)(it.head * a.G + row - tok_in * a.G) * a.seqs.total_q + it.q0 + tok0 + tok_in] =
-                lse2 * 0.69314718055994531f;
+          free_o();
+          continue;
         }
+        // 64 columns of a row as bf16 at a time; out through the staging buffer,
+        // 128 bytes of each of the warp's 32 rows in the swizzle that spreads
+        // them over the banks, read back so that a store instruction writes
+        // whole 128-byte rows.
+        const long long tok_q = item(i, kItQ0) + tok0;
+        const int hq0 = item(i, kItHead) * a.G;
+#pragma unroll 1
+        for (int h = 0; h < D / 64; ++h) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t r[32];
+            if (any) {
+              tmem_ld32(o_addr + 64 * h + 32 * q, r);
+              tmem_ld_wait();
+            }
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+              pk[16 * q + u] =
+                  some ? pack_bf16x2(__uint_as_float(r[2 * u]) * inv_l, __uint_as_float(r[2 * u + 1]) * inv_l) : 0u;
+          }
+          if (h + 1 == D / 64) free_o();
+          if (tok0 >= n) continue;  // no such tile
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) =
+                make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int rr = 4 * u + rsub, tr = wq * 32 + rr, tk = a.g_div(tr);
+            const uint4 y = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((unit ^ (rr & 7)) << 4));
+            if (tr < RT && tok0 + tk < n)
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.O) + (tok_q + tk) * a.o_stride +
+                                        (long long)(hq0 + tr - tk * a.G) * D + 64 * h + 8 * unit) = y;
+          }
+          __syncwarp();
+        }
+        const int tok_in = a.g_div(row);
+        if (row < RT && tok0 + tok_in < n)
+          a.LSE[(size_t)(hq0 + row - tok_in * a.G) * a.seqs.total_q + tok_q + tok_in] = lse2 * 0.69314718055994531f;
       }
-      tc_fence_before();
-      release_item(i);
+      if (ok) release_item(i);
     }
     if (!ok) *abort_flag = 1;
   }
@@ -832,7 +891,7 @@ cudaError_t launch_d(const PromptFwdArgs& a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(prompt_fwd_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::ALLOC);
   if (e != cudaSuccess) return e;
-  prompt_fwd_kernel<D, PAGED><<<(unsigned)ctas, C::THREADS, C::ALLOC, st>>>(a);
+  prompt_fwd_kernel<D, PAGED><<<(unsigned)ctas, C::NTHREADS, C::ALLOC, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.splits == 1) return e;
   prompt_merge_kernel<D><<<(unsigned)(a.max_blocks * a.Hkv * 8), 256, 0, st>>>(a);

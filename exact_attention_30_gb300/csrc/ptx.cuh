@@ -98,6 +98,16 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int* st
 
 // Make generic-proxy writes to shared memory visible to the async proxy
 // (TMA / tensor core operand reads).
+// Registers per thread of this warpgroup, fewer or more than at launch (all of
+// its warps; what the block's warpgroups ask for must add up to the launch's).
+template <int N>
+__device__ __forceinline__ void set_max_registers_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_max_registers_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 // Barrier ID (1..15) among `count` threads of the block (a multiple of 32).
 template <int ID>
 __device__ __forceinline__ void named_bar_sync(int count) {
