@@ -38,7 +38,8 @@ __all__ = [
     "fa_decode_workspace_bytes", "fa_decode_plan", "fa_check_device_status",
     "fa_rope_tables", "fa_kv_append", "fa_decode_paged", "fa_decode_paged_workspace_bytes",
     "fa_decode_shared", "fa_decode_shared_workspace_bytes", "fa_decode_shared_plan",
-    "fa_prompt_fwd", "fa_prompt_paged", "fa_prompt_fwd_workspace_bytes",
+    "fa_prompt_fwd", "fa_prompt_paged", "fa_prompt_fwd_workspace_bytes", "fa_prompt_bwd",
+    "fa_prompt_bwd_workspace_bytes",
     "fa_debug_timeout_probe", "fa_status_string", "fa_version", "library_path", "load_library",
     "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "FA_ERR_TIMEOUT",
     "FA_F32", "FA_BF16", "FAError", "FA_BWD_PREPROCESS", "FA_BWD_MAIN", "FA_BWD_DQ_CONVERT",
@@ -98,6 +99,9 @@ _SIGNATURES = {
     "fa_prompt_fwd": (_ci, [_vp, _vp, _vp, _ll, _ll, _ll, _vp, _ll, _vp, _vp, _vp] + [_ci] * 7 +
                       [_vp, _sz, _ci, _cf, _ci, _vp]),
     "fa_prompt_fwd_workspace_bytes": (_sz, [_ci] * 8),
+    "fa_prompt_bwd": (_ci, [_vp] * 5 + [_ll] * 5 + [_vp] * 4 + [_ll] * 3 + [_vp] * 3 + [_sz] + [_ci] * 8 +
+                      [_cf, _ci, _vp]),
+    "fa_prompt_bwd_workspace_bytes": (_sz, [_ci] * 6),
     "fa_prompt_paged": (_ci, [_vp, _ll, _vp, _vp, _ci, _vp, _vp, _ll, _vp, _vp, _ci, _ci, _ci, _ci, _vp, _sz, _cf, _ci,
                               _vp]),
     "fa_check_device_status": (_ci, [_vp]),
@@ -742,24 +746,8 @@ def _scratch(workspace, need, device, dev: int):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
-def fa_prompt_fwd_workspace_bytes(B: int, Hq: int, Hkv: int, total_q: int, max_seqlen_q: int, max_seqlen_k: int,
-                                  d: int) -> int:
-    """Scratch bytes with which fa_prompt_fwd and fa_prompt_paged split this problem on the current device (0: not split)."""
-    return int(load_library().fa_prompt_fwd_workspace_bytes(B, Hq, Hkv, total_q, max_seqlen_q, max_seqlen_k, d, FA_BF16))
-
-
-def fa_prompt_fwd(q, k, v, cu_seqlens_q, max_seqlen_q: int, cu_seqlens_k=None, max_seqlen_k: int | None = None,
-                  scale: float | None = None, out=None, lse=None, workspace=None):
-    """Causal attention of packed prompts with grouped heads.
-
-    q: [total_q, Hq, d], k, v: [total_k, Hkv, d] bf16, the heads of a token
-    contiguous (a slice of a fused projection will do); cu_seqlens_q and
-    cu_seqlens_k: int32 [B+1] offsets of the sequences' tokens and keys (None:
-    the same). Of a sequence's n tokens and m keys, token i sees keys
-    j <= m - n + i; one that sees none gets O = 0 and LSE = -inf. Rows of tokens
-    outside all sequences are not written.
-    Returns (O [total_q, Hq, d], LSE [Hq, total_q] float32).
-    """
+def _prompt_inputs(q, k, v, cu_seqlens_q, max_seqlen_q, cu_seqlens_k, max_seqlen_k):
+    """Checks packed queries, keys and values and their offsets; returns their sizes and strides."""
     dev = q.get_device() if isinstance(q, _Tensor) else -1
     if dev < 0 or not _is(q, _BF16, dev) or q.dim() != 3:
         _refuse(q, "q", dev, _BF16, "[total, Hq, d]")
@@ -778,6 +766,29 @@ def fa_prompt_fwd(q, k, v, cu_seqlens_q, max_seqlen_q: int, cu_seqlens_k=None, m
         if max_seqlen_k is None:
             raise ValueError("max_seqlen_k is missing")
     mq, mk = _int32(int(max_seqlen_q), "max_seqlen_q"), _int32(int(max_seqlen_k), "max_seqlen_k")
+    return dev, B, total, total_k, hq, hkv, d, qs, ks, vs, cu_seqlens_k, mq, mk
+
+
+def fa_prompt_fwd_workspace_bytes(B: int, Hq: int, Hkv: int, total_q: int, max_seqlen_q: int, max_seqlen_k: int,
+                                  d: int) -> int:
+    """Scratch bytes with which fa_prompt_fwd and fa_prompt_paged split this problem on the current device (0: not split)."""
+    return int(load_library().fa_prompt_fwd_workspace_bytes(B, Hq, Hkv, total_q, max_seqlen_q, max_seqlen_k, d, FA_BF16))
+
+
+def fa_prompt_fwd(q, k, v, cu_seqlens_q, max_seqlen_q: int, cu_seqlens_k=None, max_seqlen_k: int | None = None,
+                  scale: float | None = None, out=None, lse=None, workspace=None):
+    """Causal attention of packed prompts with grouped heads.
+
+    q: [total_q, Hq, d], k, v: [total_k, Hkv, d] bf16, the heads of a token
+    contiguous (a slice of a fused projection will do); cu_seqlens_q and
+    cu_seqlens_k: int32 [B+1] offsets of the sequences' tokens and keys (None:
+    the same). Of a sequence's n tokens and m keys, token i sees keys
+    j <= m - n + i; one that sees none gets O = 0 and LSE = -inf. Rows of tokens
+    outside all sequences are not written.
+    Returns (O [total_q, Hq, d], LSE [Hq, total_q] float32).
+    """
+    dev, B, total, total_k, hq, hkv, d, qs, ks, vs, cu_seqlens_k, mq, mk = _prompt_inputs(
+        q, k, v, cu_seqlens_q, max_seqlen_q, cu_seqlens_k, max_seqlen_k)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     out, os_, lse = _prompt_outputs(q, out, lse, total, hq, d, dev)
     if total == 0:
@@ -794,6 +805,57 @@ def fa_prompt_fwd(q, k, v, cu_seqlens_q, max_seqlen_q: int, cu_seqlens_k=None, m
                                n, d, scale, FA_BF16, _raw_stream(dev))
     _raise(rc, "fa_prompt_fwd")
     return out, lse
+
+
+def fa_prompt_bwd_workspace_bytes(B: int, Hq: int, Hkv: int, total_q: int, d: int) -> int:
+    """Scratch bytes fa_prompt_bwd needs."""
+    return int(load_library().fa_prompt_bwd_workspace_bytes(B, Hq, Hkv, total_q, d, FA_BF16))
+
+
+def fa_prompt_bwd(q, k, v, o, do, lse, cu_seqlens_q, max_seqlen_q: int, cu_seqlens_k=None,
+                  max_seqlen_k: int | None = None, scale: float | None = None, dq=None, dk=None, dv=None, workspace=None):
+    """Backward of ``fa_prompt_fwd``: returns (dQ like q, dK and dV like k, summed over the heads that share them).
+
+    Takes the arguments of the forward and its o and lse; do: [total_q, Hq, d].
+    dq, dk, dv may be given (slices of a fused projection's gradient will do);
+    rows outside all sequences are not written.
+    """
+    dev, B, total, total_k, hq, hkv, d, qs, ks, vs, cu_seqlens_k, mq, mk = _prompt_inputs(
+        q, k, v, cu_seqlens_q, max_seqlen_q, cu_seqlens_k, max_seqlen_k)
+    os_ = _token_stride(o, "o", total, hq, d, dev)
+    dos = _token_stride(do, "do", total, hq, d, dev)
+    if not _is(lse, _F32, dev) or lse.shape != (hq, total) or not lse.is_contiguous():
+        _refuse(lse, "lse", dev, _F32, "a contiguous [Hq, total]")
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    outs, strides = [], []
+    for t, name, n, heads in ((dq, "dq", total, hq), (dk, "dk", total_k, hkv), (dv, "dv", total_k, hkv)):
+        if t is None:
+            t, stride = torch.empty((n, heads, d), dtype=_BF16, device=q.device), heads * d
+        else:
+            stride = _token_stride(t, name, n, heads, d, dev)
+        outs.append(t)
+        strides.append(stride)
+    dq, dk, dv = outs
+    if total == 0 and total_k == 0:
+        return tuple(outs)
+    if total == 0:  # no sequence has a token; a tensor map wants one row
+        q = o = do = torch.zeros((1, hq, d), dtype=_BF16, device=q.device)
+        dq, lse = torch.empty_like(q), torch.zeros((hq, 1), dtype=_F32, device=q.device)
+        total = mq = 1
+    if total_k == 0:  # no sequence has a key
+        k = v = torch.zeros((1, hkv, d), dtype=_BF16, device=q.device)
+        dk = dv = torch.empty_like(k)
+        total_k = mk = 1
+    lib = load_library()
+    with torch.cuda.device(dev):
+        ws, n, workspace = _scratch(
+            workspace, lambda: lib.fa_prompt_bwd_workspace_bytes(B, hq, hkv, total, d, FA_BF16), q.device, dev)
+        rc = lib.fa_prompt_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), qs, ks, vs, os_, dos,
+                               lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *strides,
+                               cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), ws, n, B, hq, hkv, total, total_k, mq,
+                               mk, d, scale, FA_BF16, _raw_stream(dev))
+    _raise(rc, "fa_prompt_bwd")
+    return tuple(outs)
 
 
 def fa_prompt_paged(q, k_pages, v_pages, block_tables, seq_lens, cu_seqlens_q, max_seqlen_q: int,

@@ -44,11 +44,25 @@
 // visits only the query tiles at or after the key tile's diagonal and masks
 // the diagonal tile (key r, query q: P = 0 where r > q); the grid then lists
 // the key tiles with the most query tiles first.
+//
+// Prompts with grouped heads (Args = PromptBwdArgs): the G query heads of a K/V
+// head are rows of one problem, as in prompt_fwd.cu: a query tile holds TP =
+// floor(128 / G) tokens of all G heads, so dK and dV of the shared head add up
+// in their accumulators in fp32 and in a fixed order. Each query tile has 128
+// rows of its own in the workspace (statistics, dQ accumulator), whatever its
+// sequence's first token, so a sequence never touches another's. The diagonal
+// crosses several tiles; rows behind a sequence's last token or key have no
+// influence, NaN included: P and dS are set to zero there, the products over
+// queries and keys end at the last one in steps of 16, and the rows that the
+// last step still reads are zeroed in shared memory.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "fa_internal.h"
+#include "prompt.cuh"
 #include "ptx.cuh"
 #include "seq.cuh"
 
@@ -283,8 +297,9 @@ struct BwdCfg {
   static constexpr int IRING = 4;  // items published ahead by the producer
   static constexpr int NBAR = 1 + 2 * QSTAGES + 2 * DOSTAGES + 2 * STATSTAGES + 11 + 2 * IRING;
   // after the barriers: TMEM base, abort flag, 8 bytes free, the item ring
-  // (IRING published items, 8 ints each)
-  static constexpr int SMEM_BYTES = OFF_BAR + NBAR * 8 + 16 + 32 * IRING;
+  // (IRING published items, ITEM_INTS ints each)
+  static constexpr int ITEM_INTS = 12;
+  static constexpr int SMEM_BYTES = OFF_BAR + NBAR * 8 + 16 + 4 * ITEM_INTS * IRING;
   static constexpr int SMEM_MAX = 227 * 1024;
   // request 1 KB of alignment slack when it fits; the kernel checks alignment
   static constexpr int SMEM_ALLOC = (SMEM_BYTES + 1024 <= SMEM_MAX) ? SMEM_BYTES + 1024 : SMEM_MAX;
@@ -310,6 +325,10 @@ struct BwdItem {
   int n_it;       // query tiles
   int tail_unit;  // index among the split units, or -1
   int part;       // query range of a split unit
+  // prompts: of the first query tile, its first packed token, the tokens of the
+  // sequence from there on, the token (from there on) whose diagonal is key 0
+  // of the key tile, and its workspace row
+  int q_tok, q_left, diag0, ws_row;
 };
 
 // Item w of the 1-D item list of a fixed-length problem (non-causal: units
@@ -388,6 +407,51 @@ __device__ __noinline__ bool bwd_item(const BwdArgs& a, bool list, int w, BwdIte
   return it.n_it > 0;
 }
 
+// The same for prompts: the preprocess's list has (sequence, K/V head, key
+// tile), sequences with the most keys first; a sequence without queries has no
+// items.
+template <int BK>
+__device__ __noinline__ bool prompt_bwd_item(const PromptBwdArgs& a, int w, BwdItem& it) {
+  const int* order = a.item_counter + 2;
+  const int* prefix = order + a.nseq;
+  int lo = 0, hi = a.nseq;  // prefix[lo] <= w < prefix[hi]
+  if (w < 0 || w >= prefix[hi]) return false;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid] <= w) lo = mid;
+    else hi = mid;
+  }
+  const int b = order[lo], local = w - prefix[lo];
+  bool bad = false;
+  const PromptView v = prompt_view(a.seqs, b, bad);
+  const int kblocks = (v.m + BK - 1) / BK;
+  if (kblocks < 1 || v.n < 1) return false;
+  const int head = local / kblocks, TP = a.tile_tokens, past = v.m - v.n;
+  it.kb = local - head * kblocks;
+  it.sv.plane = head;
+  it.sv.start = v.k0;
+  it.sv.len = v.m;
+  // query tiles from that of the first token that sees the key tile's first key
+  const int t0 = it.kb * BK - past, i0 = t0 > 0 ? t0 / TP : 0;
+  it.i_begin = 0;
+  it.n_it = (v.n + TP - 1) / TP - i0;
+  it.tail_unit = -1;
+  it.part = 0;
+  it.q_tok = v.q0 + i0 * TP;
+  it.q_left = v.n - i0 * TP;
+  it.diag0 = t0 - i0 * TP;
+  it.ws_row = (head * a.slots + prompt_slot(v.q0, b, TP) + i0) * 128;
+  return it.n_it > 0;
+}
+template <int BK, int BQ>
+__device__ __forceinline__ bool decode_item(const BwdArgs& a, bool list, int w, BwdItem& it) {
+  return bwd_item<BK, BQ>(a, list, w, it);
+}
+template <int BK, int BQ>
+__device__ __forceinline__ bool decode_item(const PromptBwdArgs& a, bool, int w, BwdItem& it) {
+  return prompt_bwd_item<BK>(a, w, it);
+}
+
 // The main kernel runs as a persistent grid (a.items > 0): one CTA per SM
 // takes items from the list, its first one by block index and, fixed-length
 // non-causal (items of one length), every gridDim.x-th after it; causal and
@@ -406,9 +470,11 @@ __device__ __noinline__ bool bwd_item(const BwdArgs& a, bool list, int w, BwdIte
 // published decoded through the item ring; otherwise every role steps
 // through the items itself (list: by stride gridDim.x; grid: its one unit),
 // and no ring or counter code is compiled in.
-template <int D, bool DYN>
-__global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant__ BwdArgs a) {
+template <int D, bool DYN, class Args>
+__global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant__ Args a) {
   using C = BwdCfg<D>;
+  constexpr bool PROMPT = std::is_same_v<Args, PromptBwdArgs>;
+  static_assert(!PROMPT || DYN, "prompts run from the item counter");
   // Who writes an item's dV and dK: the dQ warps (the softmax warps go
   // straight on to the next item), except in the counter kernel (DYN) at
   // d = 128, where the softmax warps do (there the dQ warps' register budget
@@ -437,8 +503,24 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + C::NBAR * 8 + 4);
   volatile int* item_ring = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + C::NBAR * 8 + 16);
   auto ring_item = [&](int slot) {
-    const volatile int* p = item_ring + 8 * slot;
+    const volatile int* p = item_ring + C::ITEM_INTS * slot;
     BwdItem it;
+    if constexpr (PROMPT) {  // broadcast: uniform registers for what follows from it
+      auto f = [&](int i) { return __shfl_sync(0xffffffffu, (int)p[i], 0); };
+      it.sv.plane = f(0);
+      it.sv.start = f(1);
+      it.sv.len = f(2);
+      it.kb = f(3);
+      it.i_begin = 0;
+      it.n_it = f(5);
+      it.tail_unit = -1;
+      it.part = 0;
+      it.q_tok = f(6);
+      it.q_left = f(7);
+      it.diag0 = f(8);
+      it.ws_row = f(9);
+      return it;
+    }
     it.sv.plane = p[0];
     it.sv.start = p[1];
     it.sv.len = p[2];
@@ -455,11 +537,11 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
   const bool causal = a.seq.causal != 0;
   const bool list = a.items > 0;
   // item indices >= n_items end the walk (a packed batch's total is in its schedule)
-  const int n_items = !list ? 1 : (a.seq.cu_seqlens != nullptr ? a.item_counter[1] : a.items);
+  const int n_items = !list ? 1 : (PROMPT || a.seq.cu_seqlens != nullptr ? a.item_counter[1] : a.items);
   if (list && (int)blockIdx.x >= n_items) return;
   if (!list) {
     BwdItem it0;
-    if (!bwd_item<C::BK, C::BQ>(a, false, 0, it0)) return;  // no key of a sequence here
+    if (!decode_item<C::BK, C::BQ>(a, false, 0, it0)) return;  // no key of a sequence here
   }
 
   if (threadIdx.x == 0) {
@@ -495,6 +577,22 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(smem_u32((const void*)tmem_slot), C::TMEM_COLS);
+  // tokens and rows of a query tile (the rest of its slots' rows stay zero)
+  int TP = C::BQ, G = 1;
+  if constexpr (PROMPT) {
+    TP = a.tile_tokens;
+    G = a.G;
+  }
+  const int RT = TP * G;
+  if constexpr (PROMPT) {
+    const int per_slot = (C::BQ - RT) * C::CH * 8;  // 16-byte units
+    for (int e = threadIdx.x; e < (C::QSTAGES + C::DOSTAGES) * per_slot; e += C::THREADS) {
+      const int slot = e / per_slot, u = e - slot * per_slot, r = RT + u / (C::CH * 8), x = u % (C::CH * 8);
+      *reinterpret_cast<uint4*>(smem + C::OFF_Q + slot * C::TILE + (x >> 3) * C::ROW_CHUNK + r * 128 + (x & 7) * 16) =
+          make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -516,14 +614,21 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
     } else {
       const int w = list ? (int)blockIdx.x + n * (int)gridDim.x : n;
       if (w >= n_items) return 1;
-      return bwd_item<C::BK, C::BQ>(a, list, w, it) ? 0 : 2;
+      return decode_item<C::BK, C::BQ>(a, list, w, it) ? 0 : 2;
     }
   };
   // The n-th item again (the epilogues read it again: that keeps the tile
   // loops' registers free).
   auto reload_item = [&](int n, BwdItem& it) {
     if constexpr (DYN) it = ring_item(n % C::IRING);
-    else bwd_item<C::BK, C::BQ>(a, list, list ? (int)blockIdx.x + n * (int)gridDim.x : n, it);
+    else decode_item<C::BK, C::BQ>(a, list, list ? (int)blockIdx.x + n * (int)gridDim.x : n, it);
+  };
+  // Element offset of row `key` of dV (which = 0) or dK (1).
+  auto out_row = [&](const BwdItem& it, int key, int which) {
+    if constexpr (PROMPT)
+      return (size_t)(it.sv.start + key) * (size_t)(which == 0 ? a.dv_stride : a.dk_stride) + (size_t)it.sv.plane * D;
+    else
+      return seq_row_offset(a.seq, it.sv, key);
   };
   // DYN: this warp is done with the n-th item's ring slot.
   auto release_item = [&](int n) {
@@ -567,7 +672,7 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
         bool end = false;
         for (;;) {
           if (w >= n_items) { end = true; break; }
-          if (bwd_item<C::BK, C::BQ>(a, list, w, it)) break;
+          if (decode_item<C::BK, C::BQ>(a, list, w, it)) break;
           w = take_next();
         }
         if constexpr (DYN) {
@@ -578,15 +683,22 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
             ok = false;
             break;
           }
-          volatile int* p = item_ring + 8 * slot;
+          volatile int* p = item_ring + C::ITEM_INTS * slot;
           p[0] = it.sv.plane;
           p[1] = it.sv.start;
           p[2] = it.sv.len;
           p[3] = it.kb;
           p[4] = it.i_begin;
           p[5] = end ? 0 : it.n_it;
-          p[6] = it.tail_unit;
-          p[7] = it.part;
+          if constexpr (PROMPT) {
+            p[6] = it.q_tok;
+            p[7] = it.q_left;
+            p[8] = it.diag0;
+            p[9] = it.ws_row;
+          } else {
+            p[6] = it.tail_unit;
+            p[7] = it.part;
+          }
           mbar_arrive(BAR(B_ITF + slot));
         }
         if (end) break;
@@ -596,10 +708,14 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
           const int s = g % C::QSTAGES;
           if (!mbar_wait(BAR(B_QEMPTY + s), ((g / C::QSTAGES) & 1) ^ 1, a.status, a.wait_limit_ns)) return false;
           if (g != a.debug_skip_q) {
-            mbar_arrive_expect_tx(BAR(B_QFULL + s), C::TILE);
-            for (int c = 0; c < C::CH; ++c)
-              tma_load_3d(sbase + C::OFF_Q + s * C::TILE + c * C::ROW_CHUNK, &a.tmQ, BAR(B_QFULL + s),
-                          c * 64, qrow0 + i * C::BQ, plane);
+            mbar_arrive_expect_tx(BAR(B_QFULL + s), PROMPT ? (uint32_t)(RT * 128 * C::CH) : (uint32_t)C::TILE);
+            for (int c = 0; c < C::CH; ++c) {
+              const uint32_t dst = sbase + C::OFF_Q + s * C::TILE + c * C::ROW_CHUNK;
+              if constexpr (PROMPT)
+                tma_load_4d(dst, &a.tmQ, BAR(B_QFULL + s), c * 64, 0, it.q_tok + i * TP, plane);
+              else
+                tma_load_3d(dst, &a.tmQ, BAR(B_QFULL + s), c * 64, qrow0 + i * C::BQ, plane);
+            }
             last[s] = g;
           }
           return true;
@@ -628,7 +744,7 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
           // the next item's K and V into L2 now, a few tiles before this
           // item's last dQ releases the buffer they load into
           BwdItem nx;
-          if (bwd_item<C::BK, C::BQ>(a, list, w_next, nx))
+          if (decode_item<C::BK, C::BQ>(a, list, w_next, nx))
             for (int c = 0; c < C::CH; ++c) {
               tma_prefetch_l2_3d(&a.tmK, c * 64, nx.sv.start + nx.kb * C::BK, nx.sv.plane);
               tma_prefetch_l2_3d(&a.tmV, c * 64, nx.sv.start + nx.kb * C::BK, nx.sv.plane);
@@ -652,7 +768,7 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
     // may belong to the next sequence, the whole warp copies them with plain
     // loads (lane k: rows 4k..4k+3) and sets -LSE*log2e = -inf past the
     // sequence, so that P = 0 there. Lane 0 issues the dO tile loads.
-    const bool stat_bulk = a.seq.cu_seqlens == nullptr;  // rows 16-byte aligned, padded
+    const bool stat_bulk = PROMPT || a.seq.cu_seqlens == nullptr;  // rows 16-byte aligned, padded
     if (lane == 0) tma_prefetch_desc(&a.tmdO);
     int last = -1;       // lane 0: global tile index of the last dO tile issued
     int last_stat = -1;  // lane 0: last statistics tile issued by bulk copies
@@ -665,7 +781,8 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
       if (got == 1) break;
       if (got == 2) continue;
       const int N = it.sv.len, plane = it.sv.plane;
-      const size_t ws_row0 = (size_t)plane * a.ws_rows + (size_t)it.sv.start;  // workspace row of query 0
+      // workspace row of query 0 (prompts: of the item's first query tile)
+      const size_t ws_row0 = PROMPT ? (size_t)it.ws_row : (size_t)plane * a.ws_rows + (size_t)it.sv.start;
       for (int i = 0; i < it.n_it; ++i) {
         const int g = g0 + i;
         if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
@@ -708,10 +825,14 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
           if (!mbar_wait(BAR(B_DOEMPTY + s), ph ^ 1, a.status, a.wait_limit_ns)) {
             *abort_flag = 1;
           } else {
-            mbar_arrive_expect_tx(BAR(B_DOFULL + s), C::TILE);
-            for (int c = 0; c < C::CH; ++c)
-              tma_load_3d(sbase + C::OFF_DO + s * C::TILE + c * C::ROW_CHUNK, &a.tmdO,
-                          BAR(B_DOFULL + s), c * 64, it.sv.start + q_row, plane);
+            mbar_arrive_expect_tx(BAR(B_DOFULL + s), PROMPT ? (uint32_t)(RT * 128 * C::CH) : (uint32_t)C::TILE);
+            for (int c = 0; c < C::CH; ++c) {
+              const uint32_t dst = sbase + C::OFF_DO + s * C::TILE + c * C::ROW_CHUNK;
+              if constexpr (PROMPT)
+                tma_load_4d(dst, &a.tmdO, BAR(B_DOFULL + s), c * 64, 0, it.q_tok + i * TP, plane);
+              else
+                tma_load_3d(dst, &a.tmdO, BAR(B_DOFULL + s), c * 64, it.sv.start + q_row, plane);
+            }
             last = g;
           }
         }
@@ -769,7 +890,15 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
           mma_ss(tmem + C::COL_DP, dVk + koff(kk), dOk + soff(s) + koff(kk), id_s, kk > 0, leader);
       };
       // dV += P^T dO_i (P^T from TMEM), dK += dS^T Q_i (K-dimension = queries)
-      auto issue_dv = [&](int s, bool acc) {
+      // (prompts: `steps` of 16 queries or keys, fewer than 8 in the last tile)
+      auto issue_dv = [&](int s, bool acc, int steps) {
+        if (PROMPT && steps < C::BQ / 16) {
+#pragma unroll 1
+          for (int kk = 0; kk < steps; ++kk)
+            mma_ts(tmem + C::COL_DV, tmem + C::COL_S + 64 * (kk >> 2) + 8 * (kk & 3), dOmn + soff(s) + roff(kk), id_dv,
+                   (acc || kk > 0) ? 1u : 0u, leader);
+          return;
+        }
 #pragma unroll
         for (int kk = 0; kk < C::BQ / 16; ++kk)
           // P^T of queries 16kk..16kk+15: packed bf16 in the S^T columns of the
@@ -777,19 +906,46 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
           mma_ts(tmem + C::COL_DV, tmem + C::COL_S + 64 * (kk >> 2) + 8 * (kk & 3), dOmn + soff(s) + roff(kk), id_dv,
                  (acc || kk > 0) ? 1u : 0u, leader);
       };
-      auto issue_dk = [&](int s, bool acc) {
+      auto issue_dk = [&](int s, bool acc, int steps) {
+        if (PROMPT && steps < C::BQ / 16) {
+#pragma unroll 1
+          for (int kk = 0; kk < steps; ++kk)
+            mma_ss(tmem + C::COL_DK, dSk + koff(kk), dQmn + soff(s) + roff(kk), id_dk, (acc || kk > 0) ? 1u : 0u, leader);
+          return;
+        }
 #pragma unroll
         for (int kk = 0; kk < C::BQ / 16; ++kk)
           mma_ss(tmem + C::COL_DK, dSk + koff(kk), dQmn + soff(s) + roff(kk), id_dk,
                  (acc || kk > 0) ? 1u : 0u, leader);
       };
       // dQ_i (K-dimension = keys), into the dP^T columns; both operands MN-major
-      auto issue_dq = [&]() {
+      auto issue_dq = [&](int steps) {
+        if (PROMPT && steps < C::BK / 16) {
+#pragma unroll 1
+          for (int kk = 0; kk < steps; ++kk) {
+            if (C::DQ_T) mma_ss(tmem + C::COL_DP, dKmn + roff(kk), dSmn + roff(kk), id_dq, kk > 0, leader);
+            else mma_ss(tmem + C::COL_DP, dSmn + roff(kk), dKmn + roff(kk), id_dq, kk > 0, leader);
+          }
+          return;
+        }
 #pragma unroll
         for (int kk = 0; kk < C::BK / 16; ++kk) {
           if (C::DQ_T) mma_ss(tmem + C::COL_DP, dKmn + roff(kk), dSmn + roff(kk), id_dq, kk > 0, leader);
           else mma_ss(tmem + C::COL_DP, dSmn + roff(kk), dKmn + roff(kk), id_dq, kk > 0, leader);
         }
+      };
+      // Prompts: rows `live` .. up to the next multiple of 16 of a landed tile
+      // become zero (they belong to another sequence, and the last step of a
+      // product over rows reads them).
+      auto clean_rows = [&](int off, int live) {
+        if (live >= 128 || (live & 15) == 0) return;
+        for (int e = lane; e < (16 - (live & 15)) * C::CH * 8; e += 32) {
+          const int r = live + e / (C::CH * 8), x = e % (C::CH * 8);
+          *reinterpret_cast<uint4*>(smem + off + (x >> 3) * C::ROW_CHUNK + r * 128 + (x & 7) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
       };
       bool ok = true;
       int ui = 0, g0 = 0;  // items and query tiles before this item
@@ -800,12 +956,20 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
         if (got == 1) break;
         if (got == 2) continue;
         const int n_it = it.n_it;
+        // prompts: rows of the item's last query tile, live keys
+        const int q_last = PROMPT ? (it.q_left - (n_it - 1) * TP) * G : 128;
+        const int k_live = PROMPT ? min(128, it.sv.len - it.kb * C::BK) : 128;
+        const int k_steps = (k_live + 15) >> 4;
         {
           // the item's first S^T and dP^T (S^T overwrites P^T of the previous
           // item's last tile: ordered after the dV products that read it)
           const int s = g0 % C::QSTAGES, so = g0 % C::DOSTAGES;
           ok = wait(B_KV, ui & 1) && wait(B_QFULL + s, (g0 / C::QSTAGES) & 1);
           if (!ok) break;
+          if constexpr (PROMPT) {
+            clean_rows(C::OFF_K, k_live);
+            if (n_it == 1) clean_rows(C::OFF_Q + s * C::TILE, q_last);
+          }
           tc_fence_after();
           issue_s(s);
           mma_commit(BAR(B_SFULL), leader);
@@ -813,6 +977,9 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
           // previous tile's dQ
           ok = (g0 == 0 || wait(B_DQEMPTY, (g0 - 1) & 1)) && wait(B_DOFULL + so, (g0 / C::DOSTAGES) & 1);
           if (!ok) break;
+          if constexpr (PROMPT) {
+            if (n_it == 1) clean_rows(C::OFF_DO + so * C::TILE, q_last);
+          }
           tc_fence_after();
           issue_dp(so);
           mma_commit(BAR(B_DPFULL), leader);
@@ -822,6 +989,7 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
           const int g = g0 + i;
           const int s = g % C::QSTAGES, so = g % C::DOSTAGES;
           const bool more = i + 1 < n_it;
+          const int q_steps = PROMPT && !more ? min(8, (q_last + 15) >> 4) : 8;
           const int s1 = (g + 1) % C::QSTAGES, so1 = (g + 1) % C::DOSTAGES;
           const uint32_t ph1 = ((g + 1) / C::QSTAGES) & 1, pho1 = ((g + 1) / C::DOSTAGES) & 1;
           if (!wait(B_PTREADY, g & 1)) { ok = false; break; }
@@ -830,26 +998,32 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
           // (softmax-warp epilogue: their pt_ready arrivals follow it)
           if (EPI_DQ && i == 0 && ui > 0 && !wait(B_ACCEMPTY, (ui - 1) & 1)) { ok = false; break; }
           tc_fence_after();
-          issue_dv(so, i > 0);
+          issue_dv(so, i > 0, q_steps);
           mma_commit(BAR(B_DOEMPTY + so), leader);  // dO_i: last use was dV
           if (more) {
             if (!wait(B_QFULL + s1, ph1)) { ok = false; break; }
+            if constexpr (PROMPT) {
+              if (i + 2 == n_it) clean_rows(C::OFF_Q + s1 * C::TILE, q_last);
+            }
             tc_fence_after();
             issue_s(s1);  // overwrites P^T(i): ordered after the dV products that read it
             mma_commit(BAR(B_SFULL), leader);
           }
           if (!wait(B_DSREADY, g & 1)) { ok = false; break; }
           tc_fence_after();
-          issue_dq();  // the dP^T columns: dP^T(i) was consumed before ds_ready
+          issue_dq(k_steps);  // the dP^T columns: dP^T(i) was consumed before ds_ready
           mma_commit(BAR(B_DQFULL), leader);
           if (!more) mma_commit(BAR(B_KVEMPTY), leader);  // K, V: last uses were dQ and dP^T of this tile
-          issue_dk(s, i > 0);
+          issue_dk(s, i > 0, q_steps);
           mma_commit(BAR(B_QEMPTY + s), leader);  // Q_i: last use was dK
           mma_commit(BAR(B_DSEMPTY), leader);     // dS^T(i): last use was dQ/dK
           if (more) {
             // dP^T(i+1) reuses the dQ columns once the dQ warps have read dQ(i)
             if (!wait(B_DQEMPTY, g & 1) ||
                 !wait(B_DOFULL + so1, pho1)) { ok = false; break; }
+            if constexpr (PROMPT) {
+              if (i + 2 == n_it) clean_rows(C::OFF_DO + so1 * C::TILE, q_last);
+            }
             tc_fence_after();
             issue_dp(so1);
             mma_commit(BAR(B_DPFULL), leader);
@@ -881,6 +1055,8 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
     for (int n = 0; ok; ++n) {
       int n_it, diag_i;
       bool key_live;
+      int diag0 = 0, q_left = 0;  // prompts
+      bool part_keys = false;     // prompts: the key tile is the sequence's last and not full
       {
         BwdItem it;
         const int got = get_item(n, it);
@@ -890,6 +1066,11 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
         n_it = it.n_it;
         diag_i = causal ? it.kb - it.i_begin : -1;  // iteration of the diagonal tile
         key_live = it.kb * C::BK + r < it.sv.len;
+        if constexpr (PROMPT) {
+          diag0 = it.diag0;
+          q_left = it.q_left;
+          part_keys = (it.kb + 1) * C::BK > it.sv.len;
+        }
       }
       for (int i = 0; i < n_it; ++i) {
         if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
@@ -898,8 +1079,21 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
         // On the causal diagonal, P = 0 in the columns q < r (key r after query
         // q): column 32h + 4k4 + e of this group is masked when it is below
         // r - 64g. (Queries past the sequence have -LSE*log2e = -inf: P = 0.)
-        const bool diag = i == diag_i;
-        const int r_rel = r - qc0;
+        bool diag = i == diag_i;
+        int r_rel = r - qc0;
+        // Prompts: row c of the tile is token c / G, and sees key r when its
+        // token is not before r's diagonal: c >= G * (diag0 + r - i TP). Rows
+        // from c_end on are behind the sequence. Where P is zero in such a tile,
+        // dS is too, whatever dP is.
+        int c_end = 128;
+        if constexpr (PROMPT) {
+          const int first = diag0 - i * TP;
+          diag = first + 127 > 0;
+          r_rel = G * (first + r) - qc0;
+          c_end = (q_left - i * TP) * G - qc0;
+        }
+        const bool tail = PROMPT && c_end < 64;
+        const bool masked = PROMPT && (diag || tail || part_keys);
         bool w_ok = mbar_wait(BAR(B_SFULL), gt & 1, a.status, a.wait_limit_ns) &&
                     mbar_wait(BAR(B_STFULL + st), (gt / C::STATSTAGES) & 1, a.status, a.wait_limit_ns);
         if (!__all_sync(0xffffffffu, w_ok)) { ok = false; break; }
@@ -931,6 +1125,13 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
               p1 = c + 1 < r_rel ? 0.f : p1;
               p2 = c + 2 < r_rel ? 0.f : p2;
               p3 = c + 3 < r_rel ? 0.f : p3;
+            }
+            if (tail) {
+              const int c = 32 * h + 4 * k4;
+              p0 = c >= c_end ? 0.f : p0;
+              p1 = c + 1 >= c_end ? 0.f : p1;
+              p2 = c + 2 >= c_end ? 0.f : p2;
+              p3 = c + 3 >= c_end ? 0.f : p3;
             }
             pf[16 * h + 2 * k4] = f2_pack(p0, p1);
             pf[16 * h + 2 * k4 + 1] = f2_pack(p2, p3);
@@ -966,8 +1167,13 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
             const float4 nd = *reinterpret_cast<const float4*>(drow + 32 * h + 4 * k4);
             const uint64_t ta = fadd2(f2_pack(__uint_as_float(dr[4 * k4]), __uint_as_float(dr[4 * k4 + 1])), f2_pack(nd.x, nd.y));
             const uint64_t tb = fadd2(f2_pack(__uint_as_float(dr[4 * k4 + 2]), __uint_as_float(dr[4 * k4 + 3])), f2_pack(nd.z, nd.w));
-            const float2 ga = f2_unpack(fmul2(pf[16 * h + 2 * k4], ta));
-            const float2 gb = f2_unpack(fmul2(pf[16 * h + 2 * k4 + 1], tb));
+            float2 ga = f2_unpack(fmul2(pf[16 * h + 2 * k4], ta));
+            float2 gb = f2_unpack(fmul2(pf[16 * h + 2 * k4 + 1], tb));
+            if (masked) {
+              const float2 pa = f2_unpack(pf[16 * h + 2 * k4]), pb = f2_unpack(pf[16 * h + 2 * k4 + 1]);
+              ga = make_float2(pa.x == 0.f ? 0.f : ga.x, pa.y == 0.f ? 0.f : ga.y);
+              gb = make_float2(pb.x == 0.f ? 0.f : gb.x, pb.y == 0.f ? 0.f : gb.y);
+            }
             dk[2 * k4] = pack_bf16x2(ga.x, ga.y);
             dk[2 * k4 + 1] = pack_bf16x2(gb.x, gb.y);
           }
@@ -1027,7 +1233,7 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
           // (rows past N are clipped); packed batches read the rows back so
           // that each store instruction writes 4 whole 128-byte rows of this
           // sequence instead of 16 bytes of 32 rows.
-          const bool tma_out = a.seq.cu_seqlens == nullptr;
+          const bool tma_out = !PROMPT && a.seq.cu_seqlens == nullptr;
           const float f = g == 0 ? 1.f : a.scale;
           __nv_bfloat16* base = reinterpret_cast<__nv_bfloat16*>(g == 0 ? a.dV : a.dK);
           uint8_t* stg = smem + C::OFF_DS + g * C::ROW_CHUNK + wq * 32 * 128;  // [32 rows][128 B]
@@ -1065,7 +1271,7 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
                 const uint4 x = *reinterpret_cast<const uint4*>(stg + rr * 128 + ((unit ^ (rr & 7)) << 4));
                 const int key = k0 + wq * 32 + rr;
                 if (key < it.sv.len)
-                  *reinterpret_cast<uint4*>(base + seq_row_offset(a.seq, it.sv, key) + 64 * hc + 8 * unit) = x;
+                  *reinterpret_cast<uint4*>(base + out_row(it, key, g) + 64 * hc + 8 * unit) = x;
               }
               __syncwarp();  // the rows are read before the next pass (or phase 2) writes them
             }
@@ -1097,7 +1303,8 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
         if (got < 0) { ok = false; break; }
         if (got == 1) break;
         if (got == 2) continue;
-        row_first = (size_t)it.sv.plane * a.ws_rows + (size_t)it.sv.start + (size_t)it.i_begin * C::BQ;
+        row_first = PROMPT ? (size_t)it.ws_row
+                           : (size_t)it.sv.plane * a.ws_rows + (size_t)it.sv.start + (size_t)it.i_begin * C::BQ;
         n_it = it.n_it;
       }
       for (int i = 0; i < n_it; ++i) {
@@ -1212,7 +1419,7 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
         // of 16 bytes of 32 rows.
         if (lane == 0) bulk_wait_group_read<0>();
         __syncwarp();
-        const bool tma_out = a.seq.cu_seqlens == nullptr;
+        const bool tma_out = !PROMPT && a.seq.cu_seqlens == nullptr;
         const int rsub = lane >> 3, unit = lane & 7;  // read-back: row 4j + rsub, 16-byte unit
 #pragma unroll 1
         for (int g = 0; g < 2; ++g) {
@@ -1253,7 +1460,7 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
                 const uint4 x = *reinterpret_cast<const uint4*>(stg + rr * 128 + ((unit ^ (rr & 7)) << 4));
                 const int key = k0 + wq * 32 + rr;
                 if (key < it.sv.len)
-                  *reinterpret_cast<uint4*>(base + seq_row_offset(a.seq, it.sv, key) + 64 * hc + 8 * unit) = x;
+                  *reinterpret_cast<uint4*>(base + out_row(it, key, g) + 64 * hc + 8 * unit) = x;
               }
               __syncwarp();  // the rows are read before the next pass writes them
             }
@@ -1300,7 +1507,7 @@ cudaError_t launch_bwd_d(const BwdArgs& a, int BH, unsigned stages, cudaStream_t
   }
   if (stages & kStageMain) {
     const bool dyn = a.items > 0 && (a.seq.causal || a.seq.cu_seqlens != nullptr);
-    e = cudaFuncSetAttribute(dyn ? bwd_main_kernel<D, true> : bwd_main_kernel<D, false>,
+    e = cudaFuncSetAttribute(dyn ? bwd_main_kernel<D, true, BwdArgs> : bwd_main_kernel<D, false, BwdArgs>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
     if (e != cudaSuccess) return e;
     const unsigned kblocks = (unsigned)((a.seq.N + C::BK - 1) / C::BK);
@@ -1331,8 +1538,8 @@ cudaError_t launch_bwd_d(const BwdArgs& a, int BH, unsigned stages, cudaStream_t
       const int hpg = causal_heads_per_group(BH, 8ll * a.seq.N * D, 48ll << 20);
       grid = dim3((unsigned)hpg, kblocks, (unsigned)((BH + hpg - 1) / hpg));
     }
-    if (dyn) bwd_main_kernel<D, true><<<grid, C::THREADS, C::SMEM_ALLOC, st>>>(a);
-    else bwd_main_kernel<D, false><<<grid, C::THREADS, C::SMEM_ALLOC, st>>>(a);
+    if (dyn) bwd_main_kernel<D, true, BwdArgs><<<grid, C::THREADS, C::SMEM_ALLOC, st>>>(a);
+    else bwd_main_kernel<D, false, BwdArgs><<<grid, C::THREADS, C::SMEM_ALLOC, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -1345,6 +1552,201 @@ cudaError_t launch_bwd_d(const BwdArgs& a, int BH, unsigned stages, cudaStream_t
     e = cudaGetLastError();
   }
   return e;
+}
+
+// ----------------------------------------------------------------------------
+// prompts: preprocess and dQ convert, a block of threads per K/V head and
+// workspace slot (a query tile's 128 rows)
+// ----------------------------------------------------------------------------
+// The sequence whose slots hold `slot` (its first one is at most that: slots
+// begin in increasing order), and the query tile; false: an unused slot.
+__device__ __forceinline__ bool slot_tile(const PromptBwdArgs& a, int slot, PromptView& v, int& tile) {
+  int lo = 0, hi = a.seqs.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (prompt_slot(__ldg(a.seqs.cu_q + mid), mid, a.tile_tokens) <= slot) lo = mid;
+    else hi = mid;
+  }
+  bool bad = false;
+  v = prompt_view(a.seqs, lo, bad);
+  tile = slot - prompt_slot(v.q0, lo, a.tile_tokens);
+  return tile >= 0 && tile * a.tile_tokens < v.n;
+}
+
+// The main kernel's list: rank by keys (descending, then index; index order past
+// 1024 sequences), and per rank the prefix sum of its units. One block.
+__device__ void prompt_sched_block(const PromptBwdArgs& a) {
+  int* sched = a.item_counter;
+  const int B = a.nseq;
+  int* order = sched + 2;
+  int* prefix = order + B;
+  __shared__ int lens[1024];
+  __shared__ int part[256];
+  const int t = threadIdx.x;
+  bool bad = false;
+  auto keys_of = [&](int b) {
+    const PromptView v = prompt_view(a.seqs, b, bad);
+    return v.n > 0 ? v.m : 0;
+  };
+  if (B <= 1024) {
+    for (int b = t; b < B; b += 256) lens[b] = keys_of(b);
+    __syncthreads();
+    for (int b = t; b < B; b += 256) {
+      const int lb = lens[b];
+      int r = 0;
+      for (int b2 = 0; b2 < B; ++b2) r += (lens[b2] > lb) || (lens[b2] == lb && b2 < b);
+      order[r] = b;
+    }
+  } else {
+    for (int b = t; b < B; b += 256) order[b] = b;
+  }
+  __syncthreads();
+  const int per = (B + 255) / 256;
+  const int r0 = min(B, t * per), r1 = min(B, r0 + per);
+  int sum = 0;
+  for (int r = r0; r < r1; ++r) sum += a.Hkv * ((keys_of(order[r]) + 127) / 128);
+  part[t] = sum;
+  __syncthreads();
+  if (t == 0) {
+    int acc = 0;
+    for (int i = 0; i < 256; ++i) {
+      const int x = part[i];
+      part[i] = acc;
+      acc += x;
+    }
+    sched[0] = 0;
+    sched[1] = acc;
+    prefix[B] = acc;
+  }
+  __syncthreads();
+  int acc = part[t];
+  for (int r = r0; r < r1; ++r) {
+    prefix[r] = acc;
+    acc += a.Hkv * ((keys_of(order[r]) + 127) / 128);
+  }
+  if (bad) report_status(a.status, kStatusBadSeqlens);
+}
+
+// Keys that no query sees (their sequence has none): dK = dV = 0. Blocks
+// `block` of `blocks`.
+template <int D>
+__device__ void prompt_zero_block(const PromptBwdArgs& a, int block, int blocks) {
+  __shared__ int list[256];
+  __shared__ int count;
+  for (int b0 = 0; b0 < a.seqs.B; b0 += 256) {
+    if (threadIdx.x == 0) count = 0;
+    __syncthreads();
+    const int b = b0 + threadIdx.x;
+    if (b < a.seqs.B) {
+      bool bad = false;
+      const PromptView v = prompt_view(a.seqs, b, bad);
+      if (v.n == 0 && v.m > 0) list[atomicAdd(&count, 1)] = b;
+    }
+    __syncthreads();
+    const int found = count;
+    for (int i = 0; i < found; ++i) {
+      bool bad = false;
+      const PromptView v = prompt_view(a.seqs, list[i], bad);
+      const long long units = (long long)v.m * a.Hkv * (D / 8);
+      for (long long e = (long long)block * 256 + threadIdx.x; e < units; e += (long long)blocks * 256) {
+        const long long key = e / (a.Hkv * (D / 8)), x = e - key * (a.Hkv * (D / 8));
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dK) + (v.k0 + key) * a.dk_stride + 8 * x) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dV) + (v.k0 + key) * a.dv_stride + 8 * x) = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+constexpr int kPromptZeroBlocks = 32;
+
+template <int D>
+__global__ void __launch_bounds__(256) prompt_bwd_pre_kernel(const __grid_constant__ PromptBwdArgs a) {
+  const int extra = (int)blockIdx.x - a.slots;
+  if (extra >= 0) {
+    if (blockIdx.y != 0) return;
+    if (extra == 0) prompt_sched_block(a);
+    else prompt_zero_block<D>(a, extra - 1, kPromptZeroBlocks);
+    return;
+  }
+  constexpr int LPR = D / 8, RPB = 256 / LPR;  // lanes to a row, rows at a time
+  const int head = blockIdx.y, slot = blockIdx.x;
+  PromptView v;
+  int tile;
+  if (!slot_tile(a, slot, v, tile)) return;
+  const int sub = threadIdx.x / LPR, l = threadIdx.x % LPR;
+  const size_t row0 = ((size_t)head * a.slots + slot) * 128;
+#pragma unroll 4
+  for (int r0 = 0; r0 < 128; r0 += RPB) {
+    const int r = r0 + sub, tk = a.g_div(r), tok = tile * a.tile_tokens + tk, hq = head * a.G + r - tk * a.G;
+    const bool live = r < a.tile_tokens * a.G && tok < v.n;
+    float acc = 0.f;
+    if (live) {
+      const long long t = v.q0 + tok;
+      const uint4 uo = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.O) + t * a.o_stride + (long long)hq * D + 8 * l);
+      const uint4 ud = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.dO) + t * a.do_stride + (long long)hq * D + 8 * l);
+      const __nv_bfloat162* o2 = reinterpret_cast<const __nv_bfloat162*>(&uo);
+      const __nv_bfloat162* d2 = reinterpret_cast<const __nv_bfloat162*>(&ud);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 fo = __bfloat1622float2(o2[i]), fd = __bfloat1622float2(d2[i]);
+        acc = fmaf(fo.x, fd.x, acc);
+        acc = fmaf(fo.y, fd.y, acc);
+      }
+    }
+    float4* z = reinterpret_cast<float4*>(a.dQacc + (row0 + r) * D + 8 * l);
+    z[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+    z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    if (l == 0) {
+      // negated, as bwd_pre_kernel; a row without keys (LSE = -inf) has P = 0
+      const float lse = live ? a.LSE[(size_t)hq * a.seqs.total_q + v.q0 + tok] : -INFINITY;
+      a.Drow[row0 + r] = live ? -acc : 0.f;
+      a.lse2[row0 + r] = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) prompt_bwd_convert_kernel(const __grid_constant__ PromptBwdArgs a) {
+  constexpr int LPR = D / 8, RPB = 256 / LPR;
+  const int head = blockIdx.y, slot = blockIdx.x;
+  PromptView v;
+  int tile;
+  if (!slot_tile(a, slot, v, tile)) return;
+  const int sub = threadIdx.x / LPR, l = threadIdx.x % LPR;
+  const size_t row0 = ((size_t)head * a.slots + slot) * 128;
+  const float f = a.scale;
+#pragma unroll 4
+  for (int r0 = 0; r0 < 128; r0 += RPB) {
+    const int r = r0 + sub, tk = a.g_div(r), tok = tile * a.tile_tokens + tk, hq = head * a.G + r - tk * a.G;
+    if (r >= a.tile_tokens * a.G || tok >= v.n) continue;
+    const float4* src = reinterpret_cast<const float4*>(a.dQacc + (row0 + r) * D + 8 * l);
+    const float4 x = src[0], y = src[1];
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dQ) + (long long)(v.q0 + tok) * a.dq_stride + (long long)hq * D + 8 * l) =
+        make_uint4(pack_bf16x2(f * x.x, f * x.y), pack_bf16x2(f * x.z, f * x.w), pack_bf16x2(f * y.x, f * y.y),
+                   pack_bf16x2(f * y.z, f * y.w));
+  }
+}
+
+template <int D>
+cudaError_t launch_prompt_d(const PromptBwdArgs& a, cudaStream_t st) {
+  using C = BwdCfg<D>;
+  if (a.slots < 1 || a.nseq < 1 || a.items < 1 || a.splits != 1 || a.item_counter == nullptr || a.seq.causal != 1)
+    return cudaErrorInvalidValue;
+  prompt_bwd_pre_kernel<D><<<dim3((unsigned)(a.slots + 1 + kPromptZeroBlocks), (unsigned)a.Hkv), 256, 0, st>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(bwd_main_kernel<D, true, PromptBwdArgs>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
+  if (e != cudaSuccess) return e;
+  const int sms = fwd_slots();
+  bwd_main_kernel<D, true, PromptBwdArgs>
+      <<<(unsigned)(sms > 0 && sms < a.items ? sms : a.items), C::THREADS, C::SMEM_ALLOC, st>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  prompt_bwd_convert_kernel<D><<<dim3((unsigned)a.slots, (unsigned)a.Hkv), 256, 0, st>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -1372,6 +1774,12 @@ size_t bwd_tail_part_bytes(const BwdTailPlan& p, int d) {
 cudaError_t launch_bwd_bf16(const BwdArgs& a, int BH, int d, unsigned stages, cudaStream_t st) {
   if (d == 128) return launch_bwd_d<128>(a, BH, stages, st);
   if (d == 64) return launch_bwd_d<64>(a, BH, stages, st);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_prompt_bwd(const PromptBwdArgs& a, int d, cudaStream_t st) {
+  if (d == 128) return launch_prompt_d<128>(a, st);
+  if (d == 64) return launch_prompt_d<64>(a, st);
   return cudaErrorInvalidValue;
 }
 

@@ -310,6 +310,19 @@ inline int pool_box_rows(int page_size, int most) {
   const int p = page_size & -page_size;
   return p < most ? p : most;
 }
+// The backward of packed prompts with grouped heads (attn_bwd_bf16.cu): the main
+// kernel of the causal backward over rows of all heads of a group. Of BwdArgs:
+// tmQ, tmdO as tmQ above; tmK, tmV 3-D as above; tmDQacc over Hkv * slots * 128
+// rows; dQacc, lse2, Drow [Hkv][slots][128 rows]; the schedule ints, nseq, items.
+struct PromptBwdArgs : BwdArgs {
+  PromptSeqs seqs;
+  int Hkv, G, tile_tokens;
+  int slots;  // workspace slots per K/V head: total_q / tile_tokens + B + 1
+  FastDiv g_div;
+  long long o_stride, do_stride, dq_stride, dk_stride, dv_stride;  // elements between tokens
+};
+cudaError_t launch_prompt_bwd(const PromptBwdArgs& a, int d, cudaStream_t st);
+bool encode_acc_f32(CUtensorMap* m, void* ptr, long long rows, int d);
 // Tensor map of bf16 elements, 64-element inner boxes with the 128-byte swizzle;
 // dims and box from the innermost axis, strides in elements from the second.
 bool encode_bf16(CUtensorMap* m, const void* ptr, int rank, const long long* dims, const long long* strides,

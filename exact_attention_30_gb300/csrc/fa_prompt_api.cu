@@ -1,5 +1,5 @@
 // fa_prompt_api.cu -- the C ABI of the prompt operators (fa_prompt_fwd,
-// fa_prompt_paged): argument validation, tensor maps, plans and launch. Host
+// fa_prompt_paged, fa_prompt_bwd): argument validation, tensor maps, plans and launch. Host
 // code only.
 #include <cuda_runtime.h>
 
@@ -63,6 +63,23 @@ bool encode_keys(CUtensorMap* m, const void* p, long long stride, int Hkv, int t
   const long long dims[3] = {d, total, Hkv}, strides[2] = {stride, d};
   const int box[3] = {64, box_rows, 1};
   return encode_bf16(m, p, 3, dims, strides, box);
+}
+
+// Scratch of the backward: fp32 dQ accumulator, two statistics per row, and the
+// main kernel's schedule (item counter, total, sequence order, B + 1 prefix sums).
+struct BwdLayout {
+  long long slots, rows;  // workspace slots per K/V head, rows of 128 of all heads
+  size_t lse2, drow, sched, total;
+};
+BwdLayout bwd_layout(int B, int G, int Hkv, int total_q, int d) {
+  BwdLayout L{};
+  L.slots = (long long)total_q / prompt_tile_tokens(G) + B + 1;
+  L.rows = L.slots * Hkv * 128;
+  L.lse2 = align_up((size_t)L.rows * d * sizeof(float), 256);
+  L.drow = L.lse2 + align_up((size_t)L.rows * sizeof(float), 256);
+  L.sched = L.drow + align_up((size_t)L.rows * sizeof(float), 256);
+  L.total = L.sched + align_up(sizeof(int) * (3 + 2 * (size_t)B), 256);
+  return L;
 }
 
 struct FwdPlan {
@@ -209,6 +226,85 @@ fa_status fa_prompt_paged(const void* Q, long long q_stride, const fa_paged_kv* 
   const long long keys = std::min<long long>((long long)cache->num_pages * cache->page_size, B * most);
   return fwd_launch(a, Q, q_stride, O, o_stride, LSE, cu_seqlens_q, B, Hq, total_q, max_seqlen_q, 4 * keys * cache->d,
                     workspace, workspace_bytes, cache->d, scale, stream, -1, kDefaultWaitLimitNs);
+}
+
+size_t fa_prompt_bwd_workspace_bytes(int B, int Hq, int Hkv, int total_q, int d, fa_dtype dt) {
+  if (check_heads(B, Hq, Hkv, d, dt) != FA_OK || total_q < 1 || total_q > kPromptMaxTokens) return 0;
+  const BwdLayout L = bwd_layout(B, Hq / Hkv, Hkv, total_q, d);
+  return L.rows > 0x7fffffffll ? 0 : L.total;
+}
+
+fa_status fa_prompt_bwd(const void* Q, const void* K, const void* V, const void* O, const void* dO, long long q_stride,
+                        long long k_stride, long long v_stride, long long o_stride, long long do_stride,
+                        const float* LSE, void* dQ, void* dK, void* dV, long long dq_stride, long long dk_stride,
+                        long long dv_stride, const int* cu_seqlens_q, const int* cu_seqlens_k, void* workspace,
+                        size_t workspace_bytes, int B, int Hq, int Hkv, int total_q, int total_k, int max_seqlen_q,
+                        int max_seqlen_k, int d, float scale, fa_dtype dt, void* stream) {
+  const fa_status s = check_sizes(B, Hq, Hkv, total_q, total_k, max_seqlen_q, max_seqlen_k, d, scale, dt);
+  if (s != FA_OK) return s;
+  if (!Q || !K || !V || !O || !dO || !LSE || !dQ || !dK || !dV || !cu_seqlens_q || !cu_seqlens_k || !workspace)
+    return FA_ERR_INVALID_ARG;
+  if (!aligned(Q, 16) || !aligned(K, 16) || !aligned(V, 16) || !aligned(O, 16) || !aligned(dO, 16) || !aligned(dQ, 16) ||
+      !aligned(dK, 16) || !aligned(dV, 16) || !aligned(LSE, 4) || !aligned(cu_seqlens_q, 4) ||
+      !aligned(cu_seqlens_k, 4) || !aligned(workspace, 256))
+    return FA_ERR_INVALID_ARG;
+  if (!token_stride_ok(q_stride, total_q, Hq, d) || !token_stride_ok(o_stride, total_q, Hq, d) ||
+      !token_stride_ok(do_stride, total_q, Hq, d) || !token_stride_ok(dq_stride, total_q, Hq, d) ||
+      !token_stride_ok(k_stride, total_k, Hkv, d) || !token_stride_ok(v_stride, total_k, Hkv, d) ||
+      !token_stride_ok(dk_stride, total_k, Hkv, d) || !token_stride_ok(dv_stride, total_k, Hkv, d))
+    return FA_ERR_INVALID_ARG;
+  const int G = Hq / Hkv;
+  const BwdLayout L = bwd_layout(B, G, Hkv, total_q, d);
+  if (Hkv > 65535 || L.rows > 0x7fffffffll) return FA_ERR_UNSUPPORTED;
+  if (workspace_bytes < L.total) return FA_ERR_INVALID_ARG;
+  PromptBwdArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.seqs.cu_q = cu_seqlens_q;
+  a.seqs.cu_k = cu_seqlens_k;
+  a.seqs.B = B;
+  a.seqs.total_q = total_q;
+  a.seqs.total_k = total_k;
+  a.seqs.max_q = max_seqlen_q;
+  a.seqs.max_k = max_seqlen_k;
+  a.Hkv = Hkv;
+  a.G = G;
+  a.tile_tokens = prompt_tile_tokens(G);
+  a.g_div = fast_div((unsigned)G);
+  a.slots = (int)L.slots;
+  a.o_stride = token_stride(o_stride, total_q, Hq, d);
+  a.do_stride = token_stride(do_stride, total_q, Hq, d);
+  a.dq_stride = token_stride(dq_stride, total_q, Hq, d);
+  a.dk_stride = token_stride(dk_stride, total_k, Hkv, d);
+  a.dv_stride = token_stride(dv_stride, total_k, Hkv, d);
+  a.O = O;
+  a.dO = dO;
+  a.LSE = LSE;
+  a.dQ = dQ;
+  a.dK = dK;
+  a.dV = dV;
+  char* ws = static_cast<char*>(workspace);
+  a.dQacc = reinterpret_cast<float*>(ws);
+  a.lse2 = reinterpret_cast<float*>(ws + L.lse2);
+  a.Drow = reinterpret_cast<float*>(ws + L.drow);
+  a.item_counter = reinterpret_cast<int*>(ws + L.sched);
+  a.nseq = B;
+  a.items = (int)std::min<long long>(most_blocks(B, total_k, max_seqlen_k, 128) * Hkv, 1 << 30);
+  a.splits = 1;
+  a.seq.causal = 1;
+  a.seq.H = Hkv;
+  a.scale = scale;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.wait_limit_ns = kDefaultWaitLimitNs;
+  a.debug_skip_q = -1;
+  a.status = device_status_ptr();
+  if (!a.status) return FA_ERR_CUDA;
+  if (!encode_grouped(&a.tmQ, Q, token_stride(q_stride, total_q, Hq, d), G, Hkv, total_q, a.tile_tokens, d) ||
+      !encode_grouped(&a.tmdO, dO, a.do_stride, G, Hkv, total_q, a.tile_tokens, d) ||
+      !encode_keys(&a.tmK, K, token_stride(k_stride, total_k, Hkv, d), Hkv, total_k, 128, d) ||
+      !encode_keys(&a.tmV, V, token_stride(v_stride, total_k, Hkv, d), Hkv, total_k, 128, d) ||
+      !encode_acc_f32(&a.tmDQacc, a.dQacc, L.rows, d))
+    return FA_ERR_CUDA;
+  return launch_prompt_bwd(a, d, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // extern "C"

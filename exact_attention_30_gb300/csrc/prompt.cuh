@@ -35,6 +35,11 @@ __device__ __forceinline__ PromptView prompt_view(const PromptSeqs& s, int b, bo
   return v;
 }
 
+// The backward's workspace: first slot (128 rows) of sequence b whose first
+// packed token is q0. Slots of different sequences do not overlap: between two
+// of them ceil(n / tile_tokens) <= floor((q0 + n) / tile_tokens) + 1 - floor(q0 / tile_tokens).
+__device__ __forceinline__ int prompt_slot(int q0, int b, int tile_tokens) { return q0 / tile_tokens + b; }
+
 // The blocks of a batch by levels: sequence b has `count` blocks, on the levels
 // base .. base + count - 1, and a higher level is more work. Blocks are listed
 // from the highest level down (the longest first, so that the short ones fill

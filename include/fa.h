@@ -532,6 +532,34 @@ fa_status fa_prompt_paged(const void* Q, long long q_stride, const fa_paged_kv* 
                           const int* cu_seqlens_q, int B, int Hq, int total_q, int max_seqlen_q, void* workspace,
                           size_t workspace_bytes, float scale, fa_dtype dt, void* stream);
 
+/* Scratch bytes for fa_prompt_bwd (0 on invalid sizes, or sizes past its limits). */
+size_t fa_prompt_bwd_workspace_bytes(int B, int Hq, int Hkv, int total_q, int d, fa_dtype dt);
+
+/*
+ * Backward pass of fa_prompt_fwd: dQ like Q, dK and dV like K and V, the
+ * gradients of a K/V head summed over the query heads that share it (in fp32,
+ * in a fixed order; dQ is added up over the keys by the memory system, in an
+ * order that differs from run to run: up to a rounding of fp32 per addition
+ * before its one rounding to bf16). A token that sees no key has dQ = 0; keys
+ * that no token sees (their sequence has none) dK = dV = 0. Rows outside all
+ * sequences are not read, and not written in the outputs.
+ *   O, dO [total_q, Hq, d]; LSE [Hq, total_q] from fa_prompt_fwd; dQ, dK, dV:
+ *   strides between tokens as in fa_prompt_fwd, no overlap with each other (a
+ *   fused projection's gradient will do: three slices of one tensor) or the
+ *   inputs. workspace: >= fa_prompt_bwd_workspace_bytes() bytes, 256-byte
+ *   aligned, contents on entry irrelevant, not used by another call in flight.
+ * Where offsets are not in order, a sequence that is left out gets no
+ * gradients, and gradients of sequences that overlap others are undefined.
+ * Limits and errors as fa_prompt_fwd, plus Hkv <= 65535, and the workspace's
+ * rows, 128 Hkv (total_q / floor(128 / G) + B + 1), below 2^31.
+ */
+fa_status fa_prompt_bwd(const void* Q, const void* K, const void* V, const void* O, const void* dO, long long q_stride,
+                        long long k_stride, long long v_stride, long long o_stride, long long do_stride,
+                        const float* LSE, void* dQ, void* dK, void* dV, long long dq_stride, long long dk_stride,
+                        long long dv_stride, const int* cu_seqlens_q, const int* cu_seqlens_k, void* workspace,
+                        size_t workspace_bytes, int B, int Hq, int Hkv, int total_q, int total_k, int max_seqlen_q,
+                        int max_seqlen_k, int d, float scale, fa_dtype dt, void* stream);
+
 /*
  * fa_bwd without a caller-provided workspace, for callers that cannot
  * allocate device memory (for example code running inside a host application

@@ -5,6 +5,7 @@ import torch
 
 EPS_BF16 = 2.0 ** -8   # half a step of bf16, relative (rounding to nearest)
 EPS_F32 = 2.0 ** -24
+TINY = 2.0 ** -126
 
 
 def bf16_randn(shape, seed):
@@ -105,3 +106,50 @@ def check_forward(c, o, lse, scale, heads=None, seqs=None):
             assert ((got_l == -math.inf) == none).all(), (b, h)
             dl = torch.where(none, 0.0, (got_l - ref_l).abs())
             assert (dl <= e + torch.where(none, 0.0, ref_l.abs()) * 2.0 ** -22 + 2.0 ** -19).all(), (b, h, dl.max())
+
+
+def backward64(q, k, v, do, scale):
+    """dQ [g, n, d], dK, dV [m, d] (summed over g) in fp64, and what their tolerances count: P, dP - D, and
+    the sizes sum |dO| |O'| with O' the bound of O's own error per element."""
+    o, _, p = attention64(q, k, v, scale)
+    if k.shape[0] == 0:
+        return torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v), p, p, None
+    dp = do @ v.transpose(-1, -2)
+    t = torch.where(p > 0, dp - (do * o).sum(-1, keepdim=True), 0.0)
+    ds = p * t * scale
+    d_err = (do.abs() * (EPS_BF16 * o.abs() + 1.02 * EPS_BF16 * (p @ v.abs()))).sum(-1, keepdim=True)
+    return ds @ k, (ds.transpose(-1, -2) @ q).sum(0), (p.transpose(-1, -2) @ do).sum(0), p, t, d_err
+
+
+def check_backward(c, dq, dk, dv, scale, seqs=None):
+    """Every gradient against the formula. P and dS are rounded to bf16 once for their products, each
+    gradient once at the end (half a step each); O, rounded like that, enters through D = sum dO O; scores
+    and exponentials add e to P (score_error), products of d terms in fp32 (d + 8) 2^-24 of their sizes, and
+    sums over queries or keys 2^-18. A P below 2^-126, fp32's least normal number, becomes zero in the
+    exponential, which moves it by at most that, and so may a gradient below it."""
+    for b, rows, keys, n, m in c.seqs():
+        if seqs is not None and b not in seqs:
+            continue
+        for h in range(c.hkv):
+            q, k, v = c.head(b, rows, keys, h)
+            hs = slice(h * c.g, (h + 1) * c.g)
+            do = c.do[rows, hs].transpose(0, 1).cpu().double()
+            rq, rk, rv, p, t, d_err = backward64(q, k, v, do, scale)
+            got_q = dq[rows, hs].transpose(0, 1).cpu().double()
+            got_k, got_v = dk[keys, h].cpu().double(), dv[keys, h].cpu().double()
+            if m == 0 or n == 0:
+                assert (got_q == 0).all() and (got_k == 0).all() and (got_v == 0).all(), (b, h)
+                continue
+            r = 1.01 * EPS_BF16 + 2 * score_error(q, k, scale, c.d) + 2.0 ** -18
+            dp_err = (c.d + 8) * EPS_F32 * 2 * (do.abs() @ v.abs().transpose(-1, -2)) + d_err
+            t_all = (do @ v.transpose(-1, -2)).abs() + (do.abs() * (p @ v).abs()).sum(-1, keepdim=True)
+            ds_err = scale * (p * (t.abs() * r + dp_err * (1 + r)) + TINY * seen_mask(n, m) * (t_all + dp_err))
+            size_v = (p.transpose(-1, -2) @ do.abs()).sum(0)
+            tiny_v = TINY * (seen_mask(n, m).double().T @ do.abs()).sum(0)
+            for name, got, ref, tol in (("dq", got_q, rq, ds_err @ k.abs()),
+                                        ("dk", got_k, rk, (ds_err.transpose(-1, -2) @ q.abs()).sum(0)),
+                                        ("dv", got_v, rv, r * size_v + tiny_v)):
+                tol = tol + EPS_BF16 * 1.01 * ref.abs() + TINY
+                err = (got - ref).abs()
+                assert torch.isfinite(got).all(), (b, h, name)
+                assert (err <= tol).all(), (b, h, name, (err / tol.clamp(min=1e-30)).max(), (err > tol).sum())
