@@ -39,7 +39,8 @@ __all__ = [
     "fa_rope_tables", "fa_kv_append", "fa_decode_paged", "fa_decode_paged_workspace_bytes",
     "fa_decode_shared", "fa_decode_shared_workspace_bytes", "fa_decode_shared_plan",
     "fa_prompt_fwd", "fa_prompt_paged", "fa_prompt_fwd_workspace_bytes", "fa_prompt_bwd",
-    "fa_prompt_bwd_workspace_bytes",
+    "fa_prompt_bwd_workspace_bytes", "fa_prompt_key_weights", "fa_prompt_key_weights_paged", "fa_decode_key_weights",
+    "fa_kv_evict",
     "fa_debug_timeout_probe", "fa_status_string", "fa_version", "library_path", "load_library",
     "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "FA_ERR_TIMEOUT",
     "FA_F32", "FA_BF16", "FAError", "FA_BWD_PREPROCESS", "FA_BWD_MAIN", "FA_BWD_DQ_CONVERT",
@@ -50,6 +51,7 @@ FA_F32, FA_BF16 = 0, 1
 FA_BWD_PREPROCESS, FA_BWD_MAIN, FA_BWD_DQ_CONVERT = 0, 1, 2
 FA_CAUSAL = 1
 FA_ROPE_INTERLEAVED = 2
+FA_ACCUMULATE = 4
 _STAGE_FLAGS = {FA_BWD_PREPROCESS: 1 << 8, FA_BWD_MAIN: 2 << 8, FA_BWD_DQ_CONVERT: 4 << 8}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -102,6 +104,14 @@ _SIGNATURES = {
     "fa_prompt_bwd": (_ci, [_vp] * 5 + [_ll] * 5 + [_vp] * 4 + [_ll] * 3 + [_vp] * 3 + [_sz] + [_ci] * 8 +
                       [_cf, _ci, _vp]),
     "fa_prompt_bwd_workspace_bytes": (_sz, [_ci] * 6),
+    "fa_prompt_key_weights": (_ci, [_vp, _vp, _ll, _ll, _vp, _vp, _ll, _ll, _ci, _vp, _vp] + [_ci] * 9 +
+                              [_cf, _ci, _ci, _vp]),
+    "fa_prompt_key_weights_paged": (_ci, [_vp, _ll, _vp, _vp, _ci, _vp, _vp, _vp, _ll, _ll, _ci, _vp] + [_ci] * 5 +
+                                    [_cf, _ci, _ci, _vp]),
+    "fa_decode_key_weights": (_ci, [_vp, _vp, _vp, _vp, _ci, _vp, _vp, _vp, _ll, _ll, _ci, _ci, _ci, _ci, _cf, _ci, _ci,
+                                    _vp]),
+    "fa_kv_evict": (_ci, [_vp, _vp, _ci, _vp, _vp, _ci, _vp, _vp, _ll, _ll, _ci, _vp, _ll, _ll, _vp, _ci, _ci, _ci, _ci,
+                          _vp]),
     "fa_prompt_paged": (_ci, [_vp, _ll, _vp, _vp, _ci, _vp, _vp, _ll, _vp, _vp, _ci, _ci, _ci, _ci, _vp, _sz, _cf, _ci,
                               _vp]),
     "fa_check_device_status": (_ci, [_vp]),
@@ -884,6 +894,132 @@ def fa_prompt_paged(q, k_pages, v_pages, block_tables, seq_lens, cu_seqlens_q, m
                                  scale, FA_BF16, _raw_stream(dev))
     _raise(rc, "fa_prompt_paged")
     return out, lse
+
+
+def _key_weights(weights, name: str, B: int, hkv: int, dev: int):
+    """Checks weights [B, Hkv, keys] (keys contiguous); returns their strides and number of keys."""
+    if not _is(weights, _F32, dev) or weights.dim() != 3 or weights.shape[:2] != (B, hkv) or weights.shape[2] < 1:
+        _refuse(weights, name, dev, _F32, f"[{B}, {hkv}, keys]")
+    s0, s1, s2 = weights.stride()
+    if s2 != 1 and weights.shape[2] > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return s0, s1, _int32(weights.shape[2], f"the width of {name}")
+
+
+def _check_lse(lse, shape, what: str, dev: int):
+    if not _is(lse, _F32, dev) or lse.shape != shape or not lse.is_contiguous():
+        _refuse(lse, "lse", dev, _F32, f"a contiguous {what}")
+
+
+def fa_prompt_key_weights(q, k, lse, weights, cu_seqlens_q, max_seqlen_q: int, cu_seqlens_k=None,
+                          max_seqlen_k: int | None = None, window: int = 0, accumulate: bool = True,
+                          scale: float | None = None):
+    """The attention weight that each key of the prompts got, summed over the tokens and the query heads of its head.
+
+    After ``fa_prompt_fwd``: its q, k, offsets and lse. weights: float32
+    [B, Hkv, >= max_seqlen_k], written in place at a key's index in its sequence:
+    keys older than the tokens are added to (accumulate) or set, the tokens' own
+    are set. window: only the last so many tokens of a sequence count (0: all).
+    Returns weights.
+    """
+    dev, B, total, total_k, hq, hkv, d, qs, ks, _, cu_seqlens_k, mq, mk = _prompt_inputs(
+        q, k, k, cu_seqlens_q, max_seqlen_q, cu_seqlens_k, max_seqlen_k)
+    _check_lse(lse, (hq, total), "[Hq, total]", dev)
+    wb, wh, wk = _key_weights(weights, "weights", B, hkv, dev)
+    window = _int32(int(window), "window")
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    if total == 0 or total_k == 0:
+        return weights
+    rc = _on_device(dev, load_library().fa_prompt_key_weights, q.data_ptr(), k.data_ptr(), qs, ks, lse.data_ptr(),
+                    weights.data_ptr(), wb, wh, wk, cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, hq, hkv, total,
+                    total_k, mq, mk, window, d, scale, FA_ACCUMULATE if accumulate else 0, FA_BF16)
+    _raise(rc, "fa_prompt_key_weights")
+    return weights
+
+
+def fa_prompt_key_weights_paged(q, k_pages, block_tables, seq_lens, lse, weights, cu_seqlens_q, max_seqlen_q: int,
+                                window: int = 0, accumulate: bool = True, scale: float | None = None):
+    """``fa_prompt_key_weights`` after ``fa_prompt_paged``: keys in a paged cache. Returns weights."""
+    pool, (_, hkv, page, d), B, max_pages, dev = _paged_cache(k_pages, k_pages, block_tables, seq_lens)
+    qs, total, hq = _packed_queries(q, dev, d, hkv)
+    _offsets(cu_seqlens_q, "cu_seqlens_q", B, dev)
+    _check_lse(lse, (hq, total), "[Hq, total]", dev)
+    wb, wh, wk = _key_weights(weights, "weights", B, hkv, dev)
+    mq, window = _int32(int(max_seqlen_q), "max_seqlen_q"), _int32(int(window), "window")
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    if total == 0:
+        return weights
+    rc = _on_device(dev, load_library().fa_prompt_key_weights_paged, q.data_ptr(), qs, pool, block_tables.data_ptr(),
+                    max_pages, seq_lens.data_ptr(), lse.data_ptr(), weights.data_ptr(), wb, wh, wk,
+                    cu_seqlens_q.data_ptr(), B, hq, total, mq, window, scale, FA_ACCUMULATE if accumulate else 0, FA_BF16)
+    _raise(rc, "fa_prompt_key_weights_paged")
+    return weights
+
+
+def fa_decode_key_weights(q, k_pages, block_tables, seq_lens, lse, weights, accumulate: bool = True,
+                          scale: float | None = None):
+    """The attention weight that each cached key got from the Nq newest tokens, after ``fa_decode_paged``.
+
+    q: [B, Hq, Nq, d] and lse [B, Hq, Nq] of that call; weights: float32
+    [B, Hkv, keys], written in place: older keys are added to (accumulate) or set,
+    the Nq newest are set. Returns weights.
+    """
+    pool, (_, hkv, page, d), B, max_pages, dev = _paged_cache(k_pages, k_pages, block_tables, seq_lens)
+    if not _is(q, _BF16, dev) or q.dim() != 4:
+        _refuse(q, "q", dev, _BF16, "[B, Hq, Nq, d]")
+    b, hq, nq, e = q.shape
+    if b != B or e != d or hq % hkv != 0:
+        raise ValueError("q must be [B, Hq, Nq, d] with the tables' B, the cache's d and Hq a multiple of its heads")
+    q0, q1, q2, q3 = q.stride()
+    if q3 != 1:
+        raise ValueError("the last dimension of q must be contiguous")
+    _check_lse(lse, (B, hq, nq), "[B, Hq, Nq]", dev)
+    wb, wh, wk = _key_weights(weights, "weights", B, hkv, dev)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    rc = _on_device(dev, load_library().fa_decode_key_weights, q.data_ptr(), _pack_strides(q0, q1, q2), pool,
+                    block_tables.data_ptr(), max_pages, seq_lens.data_ptr(), lse.data_ptr(), weights.data_ptr(), wb, wh, wk,
+                    B, hq, nq, scale, FA_ACCUMULATE if accumulate else 0, FA_BF16)
+    if rc != FA_OK:
+        _raise(rc, "fa_decode_key_weights")
+    return weights
+
+
+def fa_kv_evict(k_pages, v_pages, block_tables, seq_lens, weights, budget: int, recent: int = 0, new_tables=None,
+                new_lens=None, new_weights=None, kept=None):
+    """Of each sequence and K/V head the ``recent`` newest keys and those with the largest weights stay, ``budget`` in all.
+
+    They keep their order and move together, with their values: into the pages of
+    new_tables (int32 [B, pages]; None: in place), their weights to the front of
+    new_weights' rows (None: of weights'). weights: float32 [B, Hkv, keys].
+    Returns (lengths after it, int32 [B] (``new_lens``; may be seq_lens), and
+    kept, int32 [B, Hkv, budget]: the index each key that stays had, -1 behind them).
+    """
+    pool, (_, hkv, page, d), B, max_pages, dev = _paged_cache(k_pages, v_pages, block_tables, seq_lens)
+    wb, wh, wk = _key_weights(weights, "weights", B, hkv, dev)
+    budget, recent = _int32(int(budget), "budget"), _int32(int(recent), "recent")
+    if new_tables is None:
+        new_tables = block_tables
+    elif not _is(new_tables, _I32, dev) or new_tables.dim() != 2 or new_tables.shape[0] != B or \
+            not new_tables.is_contiguous():
+        _refuse(new_tables, "new_tables", dev, _I32, "a contiguous [B, pages]")
+    if new_weights is None:
+        new_weights = weights
+    nb, nh, nk = _key_weights(new_weights, "new_weights", B, hkv, dev)
+    if nk < min(budget, wk, max_pages * page):
+        raise ValueError("the rows of new_weights are too short for what stays")
+    if new_lens is None:
+        new_lens = torch.empty_like(seq_lens)
+    elif not _is(new_lens, _I32, dev) or new_lens.shape != (B,) or not new_lens.is_contiguous():
+        _refuse(new_lens, "new_lens", dev, _I32, "a contiguous [B]")
+    if kept is None:
+        kept = torch.empty((B, hkv, max(budget, 0)), dtype=_I32, device=k_pages.device)
+    elif not _is(kept, _I32, dev) or kept.shape != (B, hkv, budget) or not kept.is_contiguous():
+        _refuse(kept, "kept", dev, _I32, "a contiguous [B, Hkv, budget]")
+    rc = _on_device(dev, load_library().fa_kv_evict, pool, block_tables.data_ptr(), max_pages, seq_lens.data_ptr(),
+                    new_tables.data_ptr(), new_tables.shape[1], new_lens.data_ptr(), weights.data_ptr(), wb, wh, wk,
+                    new_weights.data_ptr(), nb, nh, kept.data_ptr(), B, budget, recent, FA_BF16)
+    _raise(rc, "fa_kv_evict")
+    return new_lens, kept
 
 
 def fa_check_device_status(device=None) -> int:

@@ -37,6 +37,9 @@ SOURCES = [
     ("paged_decode.cu", []),
     ("fa_prompt_api.cu", []),
     ("prompt_fwd.cu", []),
+    ("prompt_weights.cu", []),
+    ("paged_weights.cu", []),
+    ("kv_evict.cu", []),
 ]
 
 

@@ -1089,8 +1089,8 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
         if constexpr (PROMPT) {
           const int first = diag0 - i * TP;
           diag = first + 127 > 0;
-          r_rel = G * (first + r) - qc0;
-          c_end = (q_left - i * TP) * G - qc0;
+          r_rel = G * max(first + r, 0) - qc0;
+          c_end = min(q_left - i * TP, 128) * G - qc0;
         }
         const bool tail = PROMPT && c_end < 64;
         const bool masked = PROMPT && (diag || tail || part_keys);

@@ -322,11 +322,71 @@ struct PromptBwdArgs : BwdArgs {
   long long o_stride, do_stride, dq_stride, dk_stride, dv_stride;  // elements between tokens
 };
 cudaError_t launch_prompt_bwd(const PromptBwdArgs& a, int d, cudaStream_t st);
+// The weight that each key got (prompt_weights.cu): W[seq * w_batch + head *
+// w_head + key], keys below w_keys.
+struct PromptWeightArgs {
+  CUtensorMap tmQ, tmK;      // as in PromptFwdArgs
+  PromptSeqs seqs;
+  PagedPool pool;            // paged only
+  const int* block_tables;
+  int max_pages, box_rows;
+  const float* LSE;          // [Hkv * G, total_q]
+  float* W;
+  long long w_batch, w_head;
+  int w_keys, window, accumulate;
+  int Hkv, G, tile_tokens;
+  FastDiv g_div;
+  int heads_per_group;
+  long long max_units;       // at least as many blocks of 256 keys as all sequences have
+  float scale_log2;
+  int* status;
+  unsigned long long wait_limit_ns;
+  int debug_skip_q;
+};
+cudaError_t launch_prompt_weights(const PromptWeightArgs& a, int d, cudaStream_t st);
 bool encode_acc_f32(CUtensorMap* m, void* ptr, long long rows, int d);
 // Tensor map of bf16 elements, 64-element inner boxes with the 128-byte swizzle;
 // dims and box from the innermost axis, strides in elements from the second.
 bool encode_bf16(CUtensorMap* m, const void* ptr, int rank, const long long* dims, const long long* strides,
                  const int* box);
+
+// The weight that each cached key got from the newest tokens (paged_weights.cu).
+struct PagedWeightArgs {
+  const void* Q;             // bf16, element strides of batch, head, row
+  long long q_b, q_h, q_r;
+  PagedPool pool;            // keys only
+  const int* block_tables;   // [B, max_pages]
+  const int* seq_lens;
+  const float* LSE;          // [B, Hkv * G, Nq]
+  float* W;                  // [b * w_batch + h * w_head + key], key < w_keys
+  long long w_batch, w_head;
+  int w_keys, most_keys, accumulate;
+  int B, Hkv, G, Nq, max_pages;
+  FastDiv page_div, nq_div;
+  float scale_log2;
+  int ctas;
+  int* status;
+};
+cudaError_t launch_paged_weights(const PagedWeightArgs& a, int d, cudaStream_t st);
+
+// Eviction by weight (kv_evict.cu).
+struct EvictArgs {
+  PagedPool pool;
+  const int* block_tables;   // [B, max_pages]
+  const int* new_tables;     // [B, new_pages]; may be block_tables
+  const int* seq_lens;
+  int* new_lens;             // may be seq_lens
+  const float* W;            // [b * w_batch + h * w_head + key], key < w_keys
+  float* Wout;               // likewise; may be W
+  long long w_batch, w_head, wout_batch, wout_head;
+  int* kept;                 // [B, Hkv, budget]
+  int B, Hkv, d, max_pages, new_pages, w_keys, most_keys, budget, recent;
+  int pieces;                // column pieces of a row in the move
+  FastDiv page_div;
+  int* status;
+};
+cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t st);
+int evict_pieces(int B, int Hkv, int d, int sms);
 
 struct PagedDecodeArgs {
   CUtensorMap tmK, tmV;

@@ -1,8 +1,10 @@
 // fa_paged_api.cu -- the C ABI of the paged key/value cache operators
-// (fa_kv_append, fa_decode_paged, fa_decode_shared): argument validation and
+// (fa_kv_append, fa_decode_paged, fa_decode_shared, fa_decode_key_weights,
+// fa_kv_evict): argument validation and
 // launch. Host code only.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -337,6 +339,98 @@ fa_status fa_debug_decode_skip_load(const void* Q, const long long* q_strides, c
   return decode_impl(Q, q_strides, cache, prefix_pages, prefix_len, block_tables, max_pages, seq_lens, O,
                      o_strides, LSE, workspace, workspace_bytes, B, Hq, Nq, scale, FA_BF16, stream, skip_tile,
                      clamp_limit(limit_ns));
+}
+
+fa_status fa_decode_key_weights(const void* Q, const long long* q_strides, const fa_paged_kv* cache,
+                                const int* block_tables, int max_pages, const int* seq_lens, const float* LSE, float* W,
+                                long long w_batch_stride, long long w_head_stride, int w_keys, int B, int Hq, int Nq,
+                                float scale, int flags, fa_dtype dt, void* stream) {
+  PagedWeightArgs a;
+  std::memset(&a, 0, sizeof(a));
+  fa_status s = check_paged_pool(cache, dt, &a.pool);
+  if (s != FA_OK) return s;
+  s = check_decode(B, Hq, cache->kv_heads, Nq, cache->d, dt);
+  if (s != FA_OK) return s;
+  if (!std::isfinite(scale) || !(scale > 0.f) || (flags & ~FA_ACCUMULATE)) return FA_ERR_INVALID_ARG;
+  if (!Q || !LSE || !W || !block_tables || !seq_lens || max_pages < 1) return FA_ERR_INVALID_ARG;
+  if (!aligned(Q, 16) || !aligned(LSE, 4) || !aligned(W, 4) || !aligned(block_tables, 4) || !aligned(seq_lens, 4))
+    return FA_ERR_INVALID_ARG;
+  if (!view_strides(q_strides, B, Hq, Nq, cache->d, &a.q_b, &a.q_h, &a.q_r) ||
+      !weight_strides_ok(w_batch_stride, w_head_stride, w_keys, B, cache->kv_heads))
+    return FA_ERR_INVALID_ARG;
+  a.Q = Q;
+  a.block_tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.LSE = LSE;
+  a.W = W;
+  a.w_batch = w_batch_stride;
+  a.w_head = w_head_stride;
+  a.w_keys = w_keys;
+  a.most_keys = most_keys(max_pages, cache->page_size);
+  a.accumulate = flags & FA_ACCUMULATE ? 1 : 0;
+  a.B = B;
+  a.Hkv = cache->kv_heads;
+  a.G = Hq / cache->kv_heads;
+  a.Nq = Nq;
+  a.max_pages = max_pages;
+  a.page_div = fast_div((unsigned)cache->page_size);
+  a.nq_div = fast_div((unsigned)Nq);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.status = device_status_ptr();
+  const int sms = fwd_slots();
+  if (!a.status || sms < 1) return FA_ERR_CUDA;
+  // two CTAs of eight warps per SM (their registers' limit; one from 17 rows on);
+  // no more than there can be tiles of 32 keys
+  const long long tiles = (long long)B * a.Hkv * ((std::min(a.most_keys, w_keys) + 31) / 32);
+  a.ctas = (int)std::min<long long>(a.G * Nq <= 16 ? 2ll * sms : sms, tiles);
+  return launch_paged_weights(a, cache->d, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_kv_evict(const fa_paged_kv* cache, const int* block_tables, int max_pages, const int* seq_lens,
+                      const int* new_tables, int new_pages, int* new_lens, const float* W, long long w_batch_stride,
+                      long long w_head_stride, int w_keys, float* new_W, long long new_w_batch_stride,
+                      long long new_w_head_stride, int* kept, int B, int budget, int recent, fa_dtype dt, void* stream) {
+  EvictArgs a;
+  std::memset(&a, 0, sizeof(a));
+  const fa_status s = check_paged_pool(cache, dt, &a.pool);
+  if (s != FA_OK) return s;
+  if (B < 1 || max_pages < 1 || new_pages < 1 || budget < 1 || recent < 0 || recent > budget) return FA_ERR_INVALID_ARG;
+  if (!block_tables || !seq_lens || !new_tables || !new_lens || !W || !new_W || !kept) return FA_ERR_INVALID_ARG;
+  if (!aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(new_tables, 4) || !aligned(new_lens, 4) ||
+      !aligned(W, 4) || !aligned(new_W, 4) || !aligned(kept, 4))
+    return FA_ERR_INVALID_ARG;
+  const int most = std::min(most_keys(max_pages, cache->page_size), w_keys), keep = std::min(most, budget);
+  if (!weight_strides_ok(w_batch_stride, w_head_stride, w_keys, B, cache->kv_heads) ||
+      !weight_strides_ok(new_w_batch_stride, new_w_head_stride, keep, B, cache->kv_heads))
+    return FA_ERR_INVALID_ARG;
+  if ((long long)new_pages * cache->page_size < keep) return FA_ERR_INVALID_ARG;  // no room for what stays
+  if (B > 65535 || cache->kv_heads > 65535 || budget > kPagedMaxKeys) return FA_ERR_UNSUPPORTED;
+  a.block_tables = block_tables;
+  a.new_tables = new_tables;
+  a.seq_lens = seq_lens;
+  a.new_lens = new_lens;
+  a.W = W;
+  a.Wout = new_W;
+  a.w_batch = w_batch_stride;
+  a.w_head = w_head_stride;
+  a.wout_batch = new_w_batch_stride;
+  a.wout_head = new_w_head_stride;
+  a.kept = kept;
+  a.B = B;
+  a.Hkv = cache->kv_heads;
+  a.d = cache->d;
+  a.max_pages = max_pages;
+  a.new_pages = new_pages;
+  a.w_keys = w_keys;
+  a.most_keys = most_keys(max_pages, cache->page_size);
+  a.budget = budget;
+  a.recent = recent;
+  a.page_div = fast_div((unsigned)cache->page_size);
+  a.status = device_status_ptr();
+  const int sms = fwd_slots();
+  if (!a.status || sms < 1) return FA_ERR_CUDA;
+  a.pieces = evict_pieces(B, a.Hkv, a.d, sms);
+  return launch_kv_evict(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // extern "C"

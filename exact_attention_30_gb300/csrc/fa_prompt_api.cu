@@ -1,5 +1,5 @@
 // fa_prompt_api.cu -- the C ABI of the prompt operators (fa_prompt_fwd,
-// fa_prompt_paged, fa_prompt_bwd): argument validation, tensor maps, plans and launch. Host
+// fa_prompt_paged, fa_prompt_bwd, fa_prompt_key_weights and its paged form): argument validation, tensor maps, plans and launch. Host
 // code only.
 #include <cuda_runtime.h>
 
@@ -138,6 +138,40 @@ fa_status fwd_launch(PromptFwdArgs& a, const void* Q, long long q_stride, void* 
   if (!encode_grouped(&a.tmQ, Q, token_stride(q_stride, total_q, Hq, d), G, a.Hkv, total_q, a.tile_tokens, d))
     return FA_ERR_CUDA;
   return launch_prompt_fwd(a, d, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+// What the two entry points of the keys' weights have in common.
+fa_status weights_launch(PromptWeightArgs& a, const void* Q, long long q_stride, const float* LSE, float* W,
+                         long long w_batch, long long w_head, int w_keys, const int* cu_q, int B, int Hq, int total_q,
+                         int max_q, int window, int d, float scale, int flags, void* stream) {
+  if (!Q || !LSE || !W || !cu_q || window < 0 || (flags & ~FA_ACCUMULATE)) return FA_ERR_INVALID_ARG;
+  if (!aligned(Q, 16) || !aligned(LSE, 4) || !aligned(W, 4) || !aligned(cu_q, 4)) return FA_ERR_INVALID_ARG;
+  if (!token_stride_ok(q_stride, total_q, Hq, d) || !weight_strides_ok(w_batch, w_head, w_keys, B, a.Hkv))
+    return FA_ERR_INVALID_ARG;
+  a.G = Hq / a.Hkv;
+  a.tile_tokens = prompt_tile_tokens(a.G);
+  a.g_div = fast_div((unsigned)a.G);
+  a.seqs.cu_q = cu_q;
+  a.seqs.B = B;
+  a.seqs.total_q = total_q;
+  a.seqs.max_q = max_q;
+  a.LSE = LSE;
+  a.W = W;
+  a.w_batch = w_batch;
+  a.w_head = w_head;
+  a.w_keys = w_keys;
+  a.window = window;
+  a.accumulate = flags & FA_ACCUMULATE ? 1 : 0;
+  a.heads_per_group = causal_heads_per_group(a.Hkv, 2ll * total_q * a.G * d, 96ll << 20);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.wait_limit_ns = kDefaultWaitLimitNs;
+  a.debug_skip_q = -1;
+  a.status = device_status_ptr();
+  if (!a.status) return FA_ERR_CUDA;
+  if (a.max_units * a.Hkv > 0x7fffffffll) return FA_ERR_UNSUPPORTED;
+  if (!encode_grouped(&a.tmQ, Q, token_stride(q_stride, total_q, Hq, d), a.G, a.Hkv, total_q, a.tile_tokens, d))
+    return FA_ERR_CUDA;
+  return launch_prompt_weights(a, d, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // namespace
@@ -305,6 +339,54 @@ fa_status fa_prompt_bwd(const void* Q, const void* K, const void* V, const void*
       !encode_acc_f32(&a.tmDQacc, a.dQacc, L.rows, d))
     return FA_ERR_CUDA;
   return launch_prompt_bwd(a, d, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_prompt_key_weights(const void* Q, const void* K, long long q_stride, long long k_stride, const float* LSE,
+                                float* W, long long w_batch_stride, long long w_head_stride, int w_keys,
+                                const int* cu_seqlens_q, const int* cu_seqlens_k, int B, int Hq, int Hkv, int total_q,
+                                int total_k, int max_seqlen_q, int max_seqlen_k, int window, int d, float scale,
+                                int flags, fa_dtype dt, void* stream) {
+  const fa_status s = check_sizes(B, Hq, Hkv, total_q, total_k, max_seqlen_q, max_seqlen_k, d, scale, dt);
+  if (s != FA_OK) return s;
+  if (!K || !cu_seqlens_k || !aligned(K, 16) || !aligned(cu_seqlens_k, 4) || !token_stride_ok(k_stride, total_k, Hkv, d))
+    return FA_ERR_INVALID_ARG;
+  PromptWeightArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.Hkv = Hkv;
+  a.seqs.cu_k = cu_seqlens_k;
+  a.seqs.total_k = total_k;
+  a.seqs.max_k = max_seqlen_k;
+  if (!encode_keys(&a.tmK, K, token_stride(k_stride, total_k, Hkv, d), Hkv, total_k, 128, d)) return FA_ERR_CUDA;
+  a.max_units = most_blocks(B, total_k, max_seqlen_k, 256);
+  return weights_launch(a, Q, q_stride, LSE, W, w_batch_stride, w_head_stride, w_keys, cu_seqlens_q, B, Hq, total_q,
+                        max_seqlen_q, window, d, scale, flags, stream);
+}
+
+fa_status fa_prompt_key_weights_paged(const void* Q, long long q_stride, const fa_paged_kv* cache,
+                                      const int* block_tables, int max_pages, const int* seq_lens, const float* LSE,
+                                      float* W, long long w_batch_stride, long long w_head_stride, int w_keys,
+                                      const int* cu_seqlens_q, int B, int Hq, int total_q, int max_seqlen_q, int window,
+                                      float scale, int flags, fa_dtype dt, void* stream) {
+  PromptWeightArgs a;
+  std::memset(&a, 0, sizeof(a));
+  fa_status s = check_paged_pool(cache, dt, &a.pool);
+  if (s != FA_OK) return s;
+  if (max_pages < 1) return FA_ERR_INVALID_ARG;
+  const long long most = std::min<long long>((long long)max_pages * cache->page_size, kPagedMaxKeys);
+  s = check_sizes(B, Hq, cache->kv_heads, total_q, (int)most, max_seqlen_q, (int)most, cache->d, scale, dt);
+  if (s != FA_OK) return s;
+  if (!block_tables || !seq_lens || !aligned(block_tables, 4) || !aligned(seq_lens, 4)) return FA_ERR_INVALID_ARG;
+  a.Hkv = cache->kv_heads;
+  a.seqs.seq_lens = seq_lens;
+  a.seqs.total_k = (int)most;
+  a.seqs.max_k = (int)most;
+  a.block_tables = block_tables;
+  a.max_pages = max_pages;
+  a.box_rows = pool_box_rows(cache->page_size, 128);
+  if (!encode_pool_bf16(&a.tmK, a.pool, false, cache->d, a.box_rows)) return FA_ERR_CUDA;
+  a.max_units = (long long)B * ((std::min<long long>(most, w_keys) + 255) / 256);
+  return weights_launch(a, Q, q_stride, LSE, W, w_batch_stride, w_head_stride, w_keys, cu_seqlens_q, B, Hq, total_q,
+                        max_seqlen_q, window, cache->d, scale, flags, stream);
 }
 
 }  // extern "C"

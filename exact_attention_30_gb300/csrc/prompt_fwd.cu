@@ -42,25 +42,6 @@
 namespace fa {
 namespace {
 
-// mbar_wait in fewer instructions: the clock is read only after 64 tries.
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, int* status, unsigned long long limit_ns) {
-  unsigned long long t0 = 0;
-#pragma unroll 1
-  for (unsigned i = 1; !mbar_try_wait(bar, parity); ++i) {
-    if ((i & 63u) != 0) continue;
-    const unsigned long long now = globaltimer_ns();
-    if (t0 == 0) t0 = now;
-    if (now - t0 > limit_ns) {
-      report_status(status, kStatusTimeout);
-      return false;
-    }
-  }
-  return true;
-}
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int* status, unsigned long long limit_ns) {
-  return __all_sync(0xffffffffu, wait_phase(bar, parity, status, limit_ns));
-}
-
 struct PromptBlock {
   PromptView v;
   int seq, head;

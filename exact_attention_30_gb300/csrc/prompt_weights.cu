@@ -1,0 +1,478 @@
+// prompt_weights.cu -- the attention weight that each key of a prompt got.
+//
+//   w_hj = sum over the query heads of K/V head h and the counted tokens i
+//          (the last `window` of a sequence, or all) that see key j of
+//          exp(scale * q_i . k_j - LSE_i),
+// from the forward's log-sum-exp, so one product and one exponential per score
+// and nothing else: P is summed where it is computed.
+//
+// Keys are the rows of the products (S^T = K Q^T, a TMEM lane per key), so that
+// a thread adds up its own key's weights over the query tiles and no thread
+// needs another's. A unit is 256 keys (two tiles) of a sequence and K/V head,
+// which stay in shared memory while the query tiles (128 rows: all heads of the
+// group, prompt_fwd.cu) that see them stream through a ring; the next unit's
+// keys load meanwhile. Two tiles of keys per query tile, because one product of
+// 512 cycles per 32 KB of queries would ask the L2 for 18 TB/s. S is double
+// buffered in tensor memory for each key tile (four buffers of 128 columns).
+// Bound by the products and the exponentials alike: 1024 cycles a unit and query
+// tile each (8192 FLOP and 32 exponentials per cycle and SM).
+//
+// Sums: 128 weights of a query tile in eight fp32 accumulators, the tiles' sums
+// with a compensation term (Kahan's), in a fixed order.
+//
+// Warps 0: producer, 1: MMA issuer, 2: scheduler, 3: statistics, 4-7 and 8-11:
+// weights of key tiles 0 and 1. Units are listed longest first and taken over
+// from CTAs that have not begun, as in prompt_fwd.cu. Every wait is bounded.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "fa_internal.h"
+#include "prompt.cuh"
+#include "ptx.cuh"
+
+namespace fa {
+namespace {
+
+template <int D>
+struct WCfg {
+  static constexpr int CH = D / 64;
+  static constexpr int CHUNK = 128 * 128;
+  static constexpr int TILE = CH * CHUNK;  // 128 rows x D bf16
+  static constexpr int QS = 3;             // query tiles in flight
+  static constexpr int OFF_K = 0;          // [2 units][2 tiles]
+  static constexpr int OFF_Q = OFF_K + 4 * TILE;
+  static constexpr int OFF_STAT = OFF_Q + QS * TILE;  // [QS][128] -LSE * log2(e)
+  static constexpr int IRING = 2, ITEM_INTS = 12;
+  static constexpr int OFF_BARS = OFF_STAT + QS * 512;
+  // k_full[2], k_empty[2], q_full[QS], q_empty[QS], st_full[QS], st_empty[QS], s_full[2][2], s_free[2][2],
+  // item_full[2], item_empty[2], cancel, drain
+  static constexpr int NBARS = 4 + 4 * QS + 8 + 2 * IRING + 2;
+  static constexpr int OFF_ITEMS = (OFF_BARS + NBARS * 8 + 15) / 16 * 16;
+  static constexpr int OFF_CANCEL = OFF_ITEMS + IRING * ITEM_INTS * 4;
+  static constexpr int OFF_MISC = OFF_CANCEL + 16;
+  static constexpr int BYTES = OFF_MISC + 8;
+  static constexpr int ALLOC = BYTES + 1024;
+  static constexpr int THREADS = 384;
+  static constexpr uint32_t S_COL(int t, int b) { return 256u * t + 128u * b; }
+};
+
+// A unit in the ring: K/V head, first packed key and its index in the sequence,
+// keys of the sequence from there on, query tiles, how many of them key tile 1
+// does not meet, first packed token of the first query tile, tokens of the
+// sequence from there on, the token (from there on) whose diagonal is the unit's
+// first key, sequence, index of its first new key. All -1: no more units.
+enum : int { kWHead, kWKey, kWKey0, kWLeft, kWTiles, kWSkip1, kWTok, kWTokens, kWDiag, kWSeq, kWNew, kWInts };
+
+struct WUnit {
+  int f[kWInts];
+};
+
+// Whole warp: unit `u` of the list; false past the last one.
+__device__ __forceinline__ bool weight_unit(const PromptWeightArgs& a, long long u, int lane, bool report, WUnit& k) {
+  bool bad = false;
+  auto span = [&](int b) {
+    const PromptView v = prompt_view(a.seqs, b, bad);
+    bad = bad || (v.n > 0 && v.m > a.w_keys);
+    const bool there = v.n > 0 && v.m <= a.w_keys;
+    return PromptSpan{0, there ? (v.m + 255) / 256 : 0};
+  };
+  PromptSpan first;
+  int top;
+  const int total = count_blocks(a.seqs.B, lane, span, first, top);
+  if (report && bad) report_status(a.status, kStatusBadSeqlens);
+  if (u >= (long long)total * a.Hkv) return false;
+  const int hpg = a.heads_per_group;
+  const int group = (int)(u / ((long long)total * hpg));
+  const int local = (int)(u - (long long)group * total * hpg);
+  const int heads = min(hpg, a.Hkv - group * hpg);
+  const int idx = local / heads;
+  int seq, block;
+  find_block(a.seqs.B, lane, span, first, top, idx, seq, block);
+  const PromptView v = prompt_view(a.seqs, seq, bad);
+  const int TP = a.tile_tokens, past = v.m - v.n;
+  const int kb = (v.m + 255) / 256 - 1 - block;  // the first keys are seen by the most tokens
+  const int key0 = kb * 256;
+  const int from = a.window > 0 && a.window < v.n ? v.n - a.window : 0;  // the first token that counts
+  // query tiles begin at multiples of TP from the first token that counts
+  auto first_tile = [&](int key) { return max(key - past - from, 0) / TP; };
+  const int tiles = (v.n - from + TP - 1) / TP, i0 = first_tile(key0);
+  const int tok = from + i0 * TP;
+  k.f[kWHead] = group * hpg + local - idx * heads;
+  k.f[kWKey] = v.k0 + key0;
+  k.f[kWKey0] = key0;
+  k.f[kWLeft] = v.m - key0;
+  k.f[kWTiles] = tiles - i0;
+  k.f[kWSkip1] = v.m > key0 + 128 ? first_tile(key0 + 128) - i0 : tiles - i0;
+  k.f[kWTok] = v.q0 + tok;
+  k.f[kWTokens] = v.n - tok;
+  k.f[kWDiag] = key0 - past - tok;
+  k.f[kWSeq] = seq;
+  k.f[kWNew] = past;
+  return true;
+}
+
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(384, 1) prompt_weights_kernel(const __grid_constant__ PromptWeightArgs a) {
+  using C = WCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + C::OFF_BARS;
+  auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+  const int B_KFULL = 0, B_KEMPTY = 2, B_QFULL = 4, B_QEMPTY = B_QFULL + C::QS, B_STFULL = B_QEMPTY + C::QS,
+            B_STEMPTY = B_STFULL + C::QS, B_SFULL = B_STEMPTY + C::QS, B_SFREE = B_SFULL + 4, B_ITF = B_SFREE + 4,
+            B_ITE = B_ITF + C::IRING, B_CANCEL = B_ITE + C::IRING, B_DRAIN = B_CANCEL + 1;
+  volatile int* items = reinterpret_cast<volatile int*>(smem + C::OFF_ITEMS);
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int TP = a.tile_tokens, RT = TP * a.G;
+
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(BAR(B_KFULL + b), 1);
+      mbar_init(BAR(B_KEMPTY + b), 1);
+    }
+    for (int s = 0; s < C::QS; ++s) {
+      mbar_init(BAR(B_QFULL + s), 1);
+      mbar_init(BAR(B_QEMPTY + s), 1);
+      mbar_init(BAR(B_STFULL + s), 1);
+      mbar_init(BAR(B_STEMPTY + s), 8);  // one arrival per weights warp
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(BAR(B_SFULL + i), 1);
+      mbar_init(BAR(B_SFREE + i), 4);
+    }
+    for (int s = 0; s < C::IRING; ++s) {
+      mbar_init(BAR(B_ITF + s), 1);
+      mbar_init(BAR(B_ITE + s), 11);  // producer, MMA, statistics, 8 weights warps
+    }
+    mbar_init(BAR(B_CANCEL), 1);
+    mbar_init(BAR(B_DRAIN), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(smem_u32((const void*)tmem_slot), 512);
+  {
+    // rows RT .. 127 of the query slots (G does not divide 128) stay zero
+    const int per_slot = (128 - RT) * C::CH * 8;
+    for (int e = threadIdx.x; e < C::QS * per_slot; e += C::THREADS) {
+      const int slot = e / per_slot, u = e - slot * per_slot, r = RT + u / (C::CH * 8), x = u % (C::CH * 8);
+      *reinterpret_cast<uint4*>(smem + C::OFF_Q + slot * C::TILE + (x >> 3) * C::CHUNK + r * 128 + (x & 7) * 16) =
+          make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  auto wait = [&](int b, uint32_t parity) { return wait_warp(BAR(b), parity, a.status, a.wait_limit_ns); };
+  auto get_item = [&](int i) { return wait(B_ITF + i % C::IRING, (i / C::IRING) & 1); };
+  auto item = [&](int i, int what) {
+    return __shfl_sync(0xffffffffu, (int)items[(i % C::IRING) * C::ITEM_INTS + what], 0);
+  };
+  auto release_item = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(BAR(B_ITE + i % C::IRING));
+  };
+  bool ok = true;
+
+  if (warp == 2) {
+    // ---------------------------------------------------------- scheduler
+    long long u = blockIdx.x;
+    for (int i = 0; ok && u >= 0; ++i) {
+      const int s = i % C::IRING;
+      if (i >= C::IRING) ok = wait(B_ITE + s, ((i / C::IRING) - 1) & 1);
+      if (ok && i > 0) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(BAR(B_CANCEL), 16);
+          clc_try_cancel(sbase + C::OFF_CANCEL, BAR(B_CANCEL));
+        }
+        ok = wait(B_CANCEL, (i - 1) & 1);
+        if (ok) u = clc_next_cta(sbase + C::OFF_CANCEL);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (!ok) break;
+      WUnit k;
+      if (u >= 0 && !weight_unit(a, u, lane, u == 0, k)) u = -1;
+      if (lane == 0) {
+        volatile int* d = items + s * C::ITEM_INTS;
+#pragma unroll
+        for (int e = 0; e < kWInts; ++e) d[e] = u >= 0 ? k.f[e] : -1;
+        mbar_arrive(BAR(B_ITF + s));
+      }
+      __syncwarp();
+    }
+  } else if (warp == 0) {
+    // ---------------------------------------------------------- producer
+    const int nbox = PAGED ? 128 / a.box_rows : 1;
+    const bool mine = PAGED ? lane < nbox * C::CH : lane == 0;
+    const int box = PAGED ? lane % nbox : 0, chunk = PAGED ? lane / nbox : 0;
+    if (lane == 0) {
+      tma_prefetch_desc(&a.tmQ);
+      tma_prefetch_desc(&a.tmK);
+    }
+    int g0 = 0, units = 0, last_q = -1, skipped = -1;
+    for (int i = 0; ok; ++i) {
+      if (!get_item(i)) { ok = false; break; }
+      const int left = item(i, kWLeft);
+      if (left < 0) break;
+      const int head = item(i, kWHead), tiles = item(i, kWTiles), tok = item(i, kWTok);
+      const int kbuf = i & 1;
+      if (i >= 2 && !wait(B_KEMPTY + kbuf, ((i >> 1) - 1) & 1)) { ok = false; break; }
+      units = i + 1;
+      if constexpr (PAGED) {
+        const int keys = min(left, 256);
+        const int boxes = (keys + a.box_rows - 1) / a.box_rows;
+        if (lane == 0) mbar_arrive_expect_tx(BAR(B_KFULL + kbuf), (uint32_t)(boxes * a.box_rows * 128 * C::CH));
+        __syncwarp();
+        const int* table = a.block_tables + (size_t)item(i, kWSeq) * a.max_pages;
+        const int key0 = item(i, kWKey0);
+#pragma unroll 1
+        for (int t = 0; t < 2; ++t) {
+          const int at = t * 128 + box * a.box_rows;
+          if (mine && at < keys) {
+            const int pi = (key0 + at) / a.pool.page_size;
+            int page = __ldg(table + pi);
+            if (page < 0 || page >= a.pool.num_pages) {
+              report_status(a.status, kStatusBadSeqlens);
+              page = a.pool.num_pages;  // outside the tensor: reads as zeros
+            }
+            tma_load_4d(sbase + C::OFF_K + (2 * kbuf + t) * C::TILE + chunk * C::CHUNK + box * a.box_rows * 128, &a.tmK,
+                        BAR(B_KFULL + kbuf), chunk * 64, key0 + at - pi * a.pool.page_size, head, page);
+          }
+        }
+      } else if (lane == 0) {
+        const int n_t = left > 128 ? 2 : 1, key = items[(i % C::IRING) * C::ITEM_INTS + kWKey];
+        mbar_arrive_expect_tx(BAR(B_KFULL + kbuf), (uint32_t)(n_t * C::TILE));
+        for (int t = 0; t < n_t; ++t)
+          for (int c = 0; c < C::CH; ++c)
+            tma_load_3d(sbase + C::OFF_K + (2 * kbuf + t) * C::TILE + c * C::CHUNK, &a.tmK, BAR(B_KFULL + kbuf), c * 64,
+                        key + 128 * t, head);
+      }
+      __syncwarp();
+      for (int j = 0; j < tiles; ++j) {
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
+        const int g = g0 + j, s = g % C::QS;
+        if (g >= C::QS && !wait(B_QEMPTY + s, ((g / C::QS) - 1) & 1)) { ok = false; break; }
+        if (g != a.debug_skip_q) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(BAR(B_QFULL + s), (uint32_t)(RT * 128 * C::CH));
+            for (int c = 0; c < C::CH; ++c)
+              tma_load_4d(sbase + C::OFF_Q + s * C::TILE + c * C::CHUNK, &a.tmQ, BAR(B_QFULL + s), c * 64, 0, tok + j * TP,
+                          head);
+          }
+          __syncwarp();
+        } else {
+          skipped = g;
+        }
+        last_q = g;
+      }
+      if (!ok) break;
+      g0 += tiles;
+      release_item(i);
+    }
+    if (!ok) *abort_flag = 1;
+    // drain: what was asked for last must have landed before exit
+    for (int i = max(0, units - 2); i < units; ++i) wait(B_KFULL + (i & 1), (i >> 1) & 1);
+    for (int g = max(0, last_q - C::QS + 1); g <= last_q; ++g)
+      if (g != skipped) wait(B_QFULL + g % C::QS, (g / C::QS) & 1);
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    const uint32_t leader = elect_one();
+    constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
+    const uint64_t dK0 = sdesc_sw128(sbase + C::OFF_K, 16, 1024), dQ0 = sdesc_sw128(sbase + C::OFF_Q, 16, 1024);
+    int g0 = 0, c0 = 0, c1 = 0;  // query tiles, and S tiles of each key tile, before this unit
+    for (int i = 0; ok; ++i) {
+      if (!get_item(i)) { ok = false; break; }
+      const int tiles = item(i, kWTiles), skip1 = item(i, kWSkip1);
+      if (tiles < 0) break;
+      if (!wait(B_KFULL + (i & 1), (i >> 1) & 1)) { ok = false; break; }
+#pragma unroll 1
+      for (int j = 0; j < tiles; ++j) {
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
+        const int g = g0 + j, s = g % C::QS;
+        if (!wait(B_QFULL + s, (g / C::QS) & 1)) { ok = false; break; }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (t == 1 && j < skip1) continue;
+          const int c = t == 0 ? c0 + j : c1 + j - skip1, b = c & 1;
+          if (c >= 2 && !wait(B_SFREE + 2 * t + b, ((c >> 1) - 1) & 1)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t ka = dK0 + (uint64_t)(((2 * (i & 1) + t) * C::TILE) >> 4);
+          const uint64_t qb = dQ0 + (uint64_t)((s * C::TILE) >> 4);
+          const uint32_t dcol = tmem + C::S_COL(t, 0) + 128u * (uint32_t)b;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = (uint64_t)(((kk >> 2) * C::CHUNK + (kk & 3) * 32) >> 4);
+            mma_ss(dcol, ka + off, qb + off, idesc, kk > 0 ? 1u : 0u, leader);
+          }
+          mma_commit(BAR(B_SFULL + 2 * t + b), leader);
+        }
+        if (!ok) break;
+        mma_commit(BAR(B_QEMPTY + s), leader);
+      }
+      if (!ok) break;
+      mma_commit(BAR(B_KEMPTY + (i & 1)), leader);
+      g0 += tiles;
+      c0 += tiles;
+      c1 += tiles - skip1;
+      release_item(i);
+    }
+    if (!ok) *abort_flag = 1;
+    mma_commit(BAR(B_DRAIN), leader);  // every product issued has finished before TMEM is released
+    wait(B_DRAIN, 0);
+  } else if (warp == 3) {
+    // ---------------------------------------------------------- statistics
+    // -LSE * log2(e) of a query tile's rows, lane l: rows 4 l .. 4 l + 3; -inf
+    // (weight zero) for rows past the sequence, and where the row saw no key
+    int g0 = 0;
+    for (int i = 0; ok; ++i) {
+      if (!get_item(i)) { ok = false; break; }
+      const int tiles = item(i, kWTiles);
+      if (tiles < 0) break;
+      const int tok = item(i, kWTok), tokens = item(i, kWTokens), hq0 = item(i, kWHead) * a.G;
+      auto row_stat = [&](int j, int r) {
+        const int tk = a.g_div(r), t = j * TP + tk;
+        if (r >= RT || t >= tokens) return -INFINITY;
+        const float x = __ldg(a.LSE + (size_t)(hq0 + r - tk * a.G) * a.seqs.total_q + tok + t);
+        return x == -INFINITY ? x : -x * 1.4426950408889634f;
+      };
+      float4 next = make_float4(row_stat(0, 4 * lane), row_stat(0, 4 * lane + 1), row_stat(0, 4 * lane + 2),
+                                row_stat(0, 4 * lane + 3));
+      for (int j = 0; j < tiles; ++j) {
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
+        const int g = g0 + j, s = g % C::QS;
+        const float4 x = next;
+        if (j + 1 < tiles)
+          next = make_float4(row_stat(j + 1, 4 * lane), row_stat(j + 1, 4 * lane + 1), row_stat(j + 1, 4 * lane + 2),
+                             row_stat(j + 1, 4 * lane + 3));
+        if (g >= C::QS && !wait(B_STEMPTY + s, ((g / C::QS) - 1) & 1)) { ok = false; break; }
+        reinterpret_cast<float4*>(smem + C::OFF_STAT + s * 512)[lane] = x;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_STFULL + s));
+      }
+      if (!ok) break;
+      g0 += tiles;
+      release_item(i);
+    }
+  } else {
+    // ---------------------------------------------------------- weights
+    const int t = (warp - 4) >> 2, wq = warp & 3;
+    const int row = wq * 32 + lane;  // key of the tile
+    const uint32_t lane_addr = tmem + ((uint32_t)(wq * 32) << 16) + C::S_COL(t, 0);
+    const uint64_t c22 = f2_pack(a.scale_log2, a.scale_log2);
+    int g0 = 0, c = 0;
+    for (int i = 0; ok; ++i) {
+      if (!get_item(i)) { ok = false; break; }
+      const int tiles = item(i, kWTiles);
+      if (tiles < 0) break;
+      const int skip = t == 0 ? 0 : item(i, kWSkip1);
+      const int diag0 = item(i, kWDiag) + 128 * t;  // the token (from the first tile's on) whose diagonal is the tile's first key
+      const int tokens = item(i, kWTokens);
+      float total = 0.f, lost = 0.f;
+      for (int j = 0; j < tiles; ++j) {
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
+        const int g = g0 + j, s = g % C::QS;
+        if (!wait(B_STFULL + s, (g / C::QS) & 1)) { ok = false; break; }
+        if (j >= skip) {
+          const int b = c & 1;
+          if (!wait(B_SFULL + 2 * t + b, (c >> 1) & 1)) { ok = false; break; }
+          tc_fence_after();
+          const float* nl = reinterpret_cast<const float*>(smem + C::OFF_STAT + s * 512);
+          // columns that this key's weight has a part in: from its diagonal on,
+          // up to the sequence's end (the others may hold anything)
+          const int first = diag0 - j * TP;
+          const int lo = a.G * max(first + row, 0), hi = a.G * min(tokens - j * TP, 128);
+          const bool masked = first + 127 > 0 || hi < 128;
+          uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+          const uint32_t s_addr = lane_addr + 128u * (uint32_t)b;
+          auto add = [&](const uint32_t (&r)[32], int q) {
+#pragma unroll
+            for (int k4 = 0; k4 < 8; ++k4) {
+              const float4 n4 = *reinterpret_cast<const float4*>(nl + 32 * q + 4 * k4);
+              const float2 xa = f2_unpack(ffma2(f2_pack(__uint_as_float(r[4 * k4]), __uint_as_float(r[4 * k4 + 1])), c22, f2_pack(n4.x, n4.y)));
+              const float2 xb = f2_unpack(ffma2(f2_pack(__uint_as_float(r[4 * k4 + 2]), __uint_as_float(r[4 * k4 + 3])), c22, f2_pack(n4.z, n4.w)));
+              float p0 = ex2_approx(xa.x), p1 = ex2_approx(xa.y), p2 = ex2_approx(xb.x), p3 = ex2_approx(xb.y);
+              if (masked) {
+                const int col = 32 * q + 4 * k4;
+                p0 = col < lo || col >= hi ? 0.f : p0;
+                p1 = col + 1 < lo || col + 1 >= hi ? 0.f : p1;
+                p2 = col + 2 < lo || col + 2 >= hi ? 0.f : p2;
+                p3 = col + 3 < lo || col + 3 >= hi ? 0.f : p3;
+              }
+              sum[k4 & 1] = fadd2(sum[k4 & 1], f2_pack(p0, p1));
+              sum[2 + (k4 & 1)] = fadd2(sum[2 + (k4 & 1)], f2_pack(p2, p3));
+            }
+          };
+          uint32_t ra[32], rb[32];
+          tmem_ld32(s_addr, ra);
+          tmem_ld_wait_dep(ra);
+          tmem_ld32(s_addr + 32, rb);
+          add(ra, 0);
+          tmem_ld_wait_dep(rb);
+          tmem_ld32(s_addr + 64, ra);
+          add(rb, 1);
+          tmem_ld_wait_dep(ra);
+          tmem_ld32(s_addr + 96, rb);
+          add(ra, 2);
+          tmem_ld_wait_dep(rb);
+          // all of S is in registers: its buffer takes the tile after next
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(BAR(B_SFREE + 2 * t + b));
+          add(rb, 3);
+          ++c;
+          const float2 sa = f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])));
+          const float y = __fsub_rn(__fadd_rn(sa.x, sa.y), lost), z = __fadd_rn(total, y);
+          lost = __fsub_rn(__fsub_rn(z, total), y);
+          total = z;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_STEMPTY + s));
+      }
+      if (!ok) break;
+      const int left = item(i, kWLeft), key = item(i, kWKey0) + 128 * t + row, fresh = item(i, kWNew);
+      float* w = a.W + (long long)item(i, kWSeq) * a.w_batch + (long long)item(i, kWHead) * a.w_head + key;
+      // keys that are new with these tokens have no weight yet
+      if (128 * t + row < left) *w = a.accumulate && key < fresh ? *w + total : total;
+      g0 += tiles;
+      release_item(i);
+    }
+  }
+  if (!ok) *abort_flag = 1;
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, bool PAGED>
+cudaError_t launch_d(const PromptWeightArgs& a, cudaStream_t st) {
+  using C = WCfg<D>;
+  static_assert(C::ALLOC <= 227 * 1024, "shared memory budget");
+  const long long ctas = a.max_units * a.Hkv;
+  if (a.max_units < 1 || ctas > 0x7fffffffll) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(prompt_weights_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ALLOC);
+  if (e != cudaSuccess) return e;
+  prompt_weights_kernel<D, PAGED><<<(unsigned)ctas, C::THREADS, C::ALLOC, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_weights(const PromptWeightArgs& a, int d, cudaStream_t st) {
+  const bool paged = a.seqs.cu_k == nullptr;
+  if (d == 128) return paged ? launch_d<128, true>(a, st) : launch_d<128, false>(a, st);
+  if (d == 64) return paged ? launch_d<64, true>(a, st) : launch_d<64, false>(a, st);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace fa

@@ -560,6 +560,83 @@ fa_status fa_prompt_bwd(const void* Q, const void* K, const void* V, const void*
                         size_t workspace_bytes, int B, int Hq, int Hkv, int total_q, int total_k, int max_seqlen_q,
                         int max_seqlen_k, int d, float scale, fa_dtype dt, void* stream);
 
+/* Flag of the calls below: older keys' weights are added to, not set. */
+#define FA_ACCUMULATE 4
+
+/*
+ * The attention weight that each key of a prompt got:
+ *     w[b][h][j] = sum over the Hq/Hkv query heads of K/V head h and the counted
+ *                  tokens i that see key j of exp(scale * q_i . k_j - LSE_i),
+ * after fa_prompt_fwd, whose arguments and LSE it takes. One number per key by
+ * which fa_kv_evict decides what stays in a cache.
+ *   W      : float32, W[b * w_batch_stride + h * w_head_stride + j], j < w_keys
+ *            (j: the key's index in its sequence, as in the cache); rows must not
+ *            overlap. Elements from a sequence's length on, and all of a sequence
+ *            without tokens, are left as they are.
+ *   window : only the last `window` tokens of a sequence count; 0: all.
+ *   flags  : FA_ACCUMULATE: the weights of keys that are older than the tokens
+ *            (j < m - n) are added to what W holds; the tokens' own keys have
+ *            none yet, and theirs are set. 0: all are set.
+ * Scores, exponentials and sums in fp32 (sums of sums with a compensation term),
+ * in a fixed order. Limits and errors as fa_prompt_fwd, plus FA_ERR_INVALID_ARG
+ * for window < 0, unknown flags and overlapping rows of W; a sequence longer than
+ * w_keys is left out and reported like one longer than max_seqlen_k.
+ */
+fa_status fa_prompt_key_weights(const void* Q, const void* K, long long q_stride, long long k_stride, const float* LSE,
+                                float* W, long long w_batch_stride, long long w_head_stride, int w_keys,
+                                const int* cu_seqlens_q, const int* cu_seqlens_k, int B, int Hq, int Hkv, int total_q,
+                                int total_k, int max_seqlen_q, int max_seqlen_k, int window, int d, float scale,
+                                int flags, fa_dtype dt, void* stream);
+
+/* The same after fa_prompt_paged: keys in a paged cache (its values are not read). */
+fa_status fa_prompt_key_weights_paged(const void* Q, long long q_stride, const fa_paged_kv* cache,
+                                      const int* block_tables, int max_pages, const int* seq_lens, const float* LSE,
+                                      float* W, long long w_batch_stride, long long w_head_stride, int w_keys,
+                                      const int* cu_seqlens_q, int B, int Hq, int total_q, int max_seqlen_q, int window,
+                                      float scale, int flags, fa_dtype dt, void* stream);
+
+/*
+ * The same for a decoding step, after fa_decode_paged: Q, strides, tables, lengths
+ * and limits as there, LSE [B, Hq, Nq] its result. Every key of seq_lens[b] gets
+ * the weight of the Nq newest tokens' query heads; W and FA_ACCUMULATE as above
+ * (the new keys are the last Nq). The keys are read once, the values not.
+ */
+fa_status fa_decode_key_weights(const void* Q, const long long* q_strides, const fa_paged_kv* cache,
+                                const int* block_tables, int max_pages, const int* seq_lens, const float* LSE, float* W,
+                                long long w_batch_stride, long long w_head_stride, int w_keys, int B, int Hq, int Nq,
+                                float scale, int flags, fa_dtype dt, void* stream);
+
+/*
+ * Eviction from a paged cache by weight. Of the first seq_lens[b] keys of each
+ * sequence and K/V head stay the `recent` newest ones and, of the others, those
+ * with the largest weights (of equal ones the older; NaN counts as the largest),
+ * min(seq_lens[b], budget) in all. They keep their order: the i-th that stays
+ * moves, with its value, to row i mod page_size of page new_tables[b * new_pages
+ * + i / page_size]. Keys keep the rotation they were stored with; give
+ * fa_kv_append `positions` afterwards.
+ *   new_tables : may be block_tables (in place: the pages behind the last key
+ *          that stays are free afterwards). Otherwise a page of it must be either
+ *          that of the sequence's own old table at the same place, then in no other
+ *          sequence's tables, or a page that no old table holds in use; pages of
+ *          different sequences differ.
+ *   new_lens   : DEVICE int32 [B], min(seq_lens[b], budget); may be seq_lens.
+ *   W          : float32 weights as above, read. new_W: the weights of what stays,
+ *          in its order, from element 0 of each row on (strides likewise; the rest
+ *          of a row is left as it is); may be W.
+ *   kept       : DEVICE int32 [B, Hkv, budget]: the index that each key that stays
+ *          had, -1 behind the last one.
+ *   budget     : HOST value >= 1; 0 <= recent <= budget.
+ * new_pages pages must hold min(budget, w_keys, max_pages pages) keys. B <= 65535. On
+ * the device: a sequence whose length is negative, past max_pages pages or past
+ * w_keys is left as it is (kept -1, new_lens as seq_lens), and, like a page outside
+ * the pool (whose rows are not moved), reported by fa_check_device_status.
+ * Errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED (FA_F32, d, page_size, B), FA_ERR_CUDA.
+ */
+fa_status fa_kv_evict(const fa_paged_kv* cache, const int* block_tables, int max_pages, const int* seq_lens,
+                      const int* new_tables, int new_pages, int* new_lens, const float* W, long long w_batch_stride,
+                      long long w_head_stride, int w_keys, float* new_W, long long new_w_batch_stride,
+                      long long new_w_head_stride, int* kept, int B, int budget, int recent, fa_dtype dt, void* stream);
+
 /*
  * fa_bwd without a caller-provided workspace, for callers that cannot
  * allocate device memory (for example code running inside a host application

@@ -56,6 +56,22 @@ class Prompts:
         return q, self.k[keys, h].cpu().double(), self.v[keys, h].cpu().double()
 
 
+class Paged(Prompts):
+    """Prompts whose keys are in a paged cache."""
+
+    def __init__(self, n, cache, hq, seed=0, pad=(0, 0)):
+        self.n, self.m, self.cache = list(n), cache.lens, cache
+        self.hq, self.hkv, self.d, self.g, self.pad = hq, cache.hkv, cache.d, hq // cache.hkv, pad
+        self.total = sum(n) + sum(pad)
+        self.q = bf16_randn((self.total, hq, cache.d), seed)
+        self.cu_q = offsets(self.n, pad[0])
+
+    def head(self, b, rows, keys, h):
+        q = self.q[rows, h * self.g:(h + 1) * self.g].transpose(0, 1).cpu().double()
+        k, v = self.cache.keys_values(b, h)
+        return q, torch.from_numpy(k), torch.from_numpy(v)
+
+
 def seen_mask(n, m):
     """[n, m] True where token i of n sees key j of m."""
     return torch.arange(m) <= torch.arange(n)[:, None] + (m - n)
@@ -153,3 +169,31 @@ def check_backward(c, dq, dk, dv, scale, seqs=None):
                 err = (got - ref).abs()
                 assert torch.isfinite(got).all(), (b, h, name)
                 assert (err <= tol).all(), (b, h, name, (err / tol.clamp(min=1e-30)).max(), (err > tol).sum())
+
+
+def check_weights(c, w, before, lse, scale, window=0, accumulate=True, seqs=None):
+    """Every key's weight against the definition, with the fp32 lse that the call had. Each weight of a query is off
+    by e (score_error, twice: it is an exponent) and 2^-17 relative (the exponential, the rounding of -LSE * log2(e)
+    and of its sum with a score, and the sums); what was there is added in fp32."""
+    for b, rows, keys, n, m in c.seqs():
+        if seqs is not None and b not in seqs:
+            continue
+        for h in range(c.hkv):
+            got, old = w[b, h].cpu().double(), before[b, h].cpu().double()
+            if n == 0:
+                assert torch.equal(got, old), (b, h)
+                continue
+            q, k, _ = c.head(b, rows, keys, h)
+            z = lse[h * c.g:(h + 1) * c.g, rows].cpu().double()
+            x = torch.where(seen_mask(n, m), q @ k.transpose(-1, -2) * scale, -math.inf)
+            p = torch.where(z[..., None] == -math.inf, 0.0, torch.exp(x - z[..., None]))
+            if window:
+                p[:, :max(0, n - window)] = 0
+            ref = p.sum((0, 1))
+            tol = ref * (2.2 * score_error(q, k, scale, c.d) + 2.0 ** -17) + TINY * c.g * n
+            if accumulate and m > n:
+                ref[:m - n] += old[:m - n]
+                tol[:m - n] += 2.0 ** -24 * ref[:m - n].abs()
+            assert torch.equal(got[m:], old[m:]), (b, h)
+            err = (got[:m] - ref).abs()
+            assert (err <= tol).all(), (b, h, (err / tol.clamp(min=1e-30)).max())

@@ -6,7 +6,7 @@ import torch
 
 import exact_attention_30_gb300 as fa
 from paged_utils import Cache
-from prompt_utils import Prompts, bf16_randn, check_forward, offsets
+from prompt_utils import Paged, Prompts, check_forward, offsets
 
 pytestmark = pytest.mark.gpu
 
@@ -126,22 +126,6 @@ def test_graph_follows_offsets_and_streams():
         torch.cuda.synchronize()
         c.n = c.m = list(lens)
         check_forward(c, out, lse, 1 / math.sqrt(128))
-
-
-class Paged(Prompts):
-    """Prompts whose keys are in a paged cache."""
-
-    def __init__(self, n, cache, hq, seed=0, pad=(0, 0)):
-        self.n, self.m, self.cache = list(n), cache.lens, cache
-        self.hq, self.hkv, self.d, self.g, self.pad = hq, cache.hkv, cache.d, hq // cache.hkv, pad
-        self.total = sum(n) + sum(pad)
-        self.q = bf16_randn((self.total, hq, cache.d), seed)
-        self.cu_q = offsets(self.n, pad[0])
-
-    def head(self, b, rows, keys, h):
-        q = self.q[rows, h * self.g:(h + 1) * self.g].transpose(0, 1).cpu().double()
-        k, v = self.cache.keys_values(b, h)
-        return q, torch.from_numpy(k), torch.from_numpy(v)
 
 
 @pytest.mark.parametrize("page", [8, 16, 24, 64, 128, 1000])
