@@ -17,11 +17,13 @@
 // Bound by the products and the exponentials alike: 1024 cycles a unit and query
 // tile each (8192 FLOP and 32 exponentials per cycle and SM).
 //
-// Sums: 128 weights of a query tile in eight fp32 accumulators, the tiles' sums
+// Sums: 64 weights of a query tile in eight fp32 accumulators, the tiles' sums
 // with a compensation term (Kahan's), in a fixed order.
 //
-// Warps 0: producer, 1: MMA issuer, 2: scheduler, 3: statistics, 4-7 and 8-11:
-// weights of key tiles 0 and 1. Units are listed longest first and taken over
+// Warps 0: producer, 1: MMA issuer, 2: scheduler, 3: statistics, 4-19: weights,
+// four warps to the first and to the second 64 queries of each key tile (with
+// eight warps, two to a scheduler, waits and latencies were not covered: 8192
+// tokens, 32 heads 398 us). Units are listed longest first and taken over
 // from CTAs that have not begun, as in prompt_fwd.cu. Every wait is bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -44,16 +46,19 @@ struct WCfg {
   static constexpr int OFF_Q = OFF_K + 4 * TILE;
   static constexpr int OFF_STAT = OFF_Q + QS * TILE;  // [QS][128] -LSE * log2(e)
   static constexpr int IRING = 2, ITEM_INTS = 12;
-  static constexpr int OFF_BARS = OFF_STAT + QS * 512;
+  static constexpr int OFF_PART = OFF_STAT + QS * 512;  // [2 tiles][128] sums of the second column halves
+  static constexpr int OFF_BARS = OFF_PART + 2 * 512;
   // k_full[2], k_empty[2], q_full[QS], q_empty[QS], st_full[QS], st_empty[QS], s_full[2][2], s_free[2][2],
-  // item_full[2], item_empty[2], cancel, drain
-  static constexpr int NBARS = 4 + 4 * QS + 8 + 2 * IRING + 2;
+  // part_full[2], part_free[2], item_full[2], item_empty[2], cancel, drain
+  static constexpr int NBARS = 4 + 4 * QS + 12 + 2 * IRING + 2;
   static constexpr int OFF_ITEMS = (OFF_BARS + NBARS * 8 + 15) / 16 * 16;
   static constexpr int OFF_CANCEL = OFF_ITEMS + IRING * ITEM_INTS * 4;
   static constexpr int OFF_MISC = OFF_CANCEL + 16;
   static constexpr int BYTES = OFF_MISC + 8;
-  static constexpr int ALLOC = BYTES + 1024;
-  static constexpr int THREADS = 384;
+  static constexpr int MOST = 227 * 1024;
+  // 1 KB of alignment slack where it fits; the kernel checks the alignment
+  static constexpr int ALLOC = BYTES + 1024 <= MOST ? BYTES + 1024 : MOST;
+  static constexpr int THREADS = 640;
   static constexpr uint32_t S_COL(int t, int b) { return 256u * t + 128u * b; }
 };
 
@@ -113,15 +118,21 @@ __device__ __forceinline__ bool weight_unit(const PromptWeightArgs& a, long long
 }
 
 template <int D, bool PAGED>
-__global__ void __launch_bounds__(384, 1) prompt_weights_kernel(const __grid_constant__ PromptWeightArgs a) {
+__global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_constant__ PromptWeightArgs a) {
   using C = WCfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t pad = ((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + pad;
   const uint32_t sbase = smem_u32(smem);
+  if (pad + C::BYTES > (uint32_t)C::ALLOC) {
+    // cannot place the swizzled tiles: report and leave before touching anything
+    if (threadIdx.x == 0) report_status(a.status, kStatusTimeout);
+    return;
+  }
   const uint32_t bar0 = sbase + C::OFF_BARS;
   auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   const int B_KFULL = 0, B_KEMPTY = 2, B_QFULL = 4, B_QEMPTY = B_QFULL + C::QS, B_STFULL = B_QEMPTY + C::QS,
-            B_STEMPTY = B_STFULL + C::QS, B_SFULL = B_STEMPTY + C::QS, B_SFREE = B_SFULL + 4, B_ITF = B_SFREE + 4,
+            B_STEMPTY = B_STFULL + C::QS, B_SFULL = B_STEMPTY + C::QS, B_SFREE = B_SFULL + 4, B_PART = B_SFREE + 4, B_ITF = B_PART + 4,
             B_ITE = B_ITF + C::IRING, B_CANCEL = B_ITE + C::IRING, B_DRAIN = B_CANCEL + 1;
   volatile int* items = reinterpret_cast<volatile int*>(smem + C::OFF_ITEMS);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
@@ -138,15 +149,16 @@ __global__ void __launch_bounds__(384, 1) prompt_weights_kernel(const __grid_con
       mbar_init(BAR(B_QFULL + s), 1);
       mbar_init(BAR(B_QEMPTY + s), 1);
       mbar_init(BAR(B_STFULL + s), 1);
-      mbar_init(BAR(B_STEMPTY + s), 8);  // one arrival per weights warp
+      mbar_init(BAR(B_STEMPTY + s), 16);  // one arrival per weights warp
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(BAR(B_SFULL + i), 1);
-      mbar_init(BAR(B_SFREE + i), 4);
+      mbar_init(BAR(B_SFREE + i), 8);
+      mbar_init(BAR(B_PART + i), 4);  // part_full[2], part_free[2]
     }
     for (int s = 0; s < C::IRING; ++s) {
       mbar_init(BAR(B_ITF + s), 1);
-      mbar_init(BAR(B_ITE + s), 11);  // producer, MMA, statistics, 8 weights warps
+      mbar_init(BAR(B_ITE + s), 19);  // producer, MMA, statistics, 16 weights warps
     }
     mbar_init(BAR(B_CANCEL), 1);
     mbar_init(BAR(B_DRAIN), 1);
@@ -342,15 +354,19 @@ __global__ void __launch_bounds__(384, 1) prompt_weights_kernel(const __grid_con
         const float x = __ldg(a.LSE + (size_t)(hq0 + r - tk * a.G) * a.seqs.total_q + tok + t);
         return x == -INFINITY ? x : -x * 1.4426950408889634f;
       };
-      float4 next = make_float4(row_stat(0, 4 * lane), row_stat(0, 4 * lane + 1), row_stat(0, 4 * lane + 2),
-                                row_stat(0, 4 * lane + 3));
+      auto tile_stat = [&](int j) {
+        return j < tiles ? make_float4(row_stat(j, 4 * lane), row_stat(j, 4 * lane + 1), row_stat(j, 4 * lane + 2),
+                                       row_stat(j, 4 * lane + 3))
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+      };
+      float4 ahead[3] = {tile_stat(0), tile_stat(1), tile_stat(2)};  // loads of three tiles in flight
       for (int j = 0; j < tiles; ++j) {
         if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
         const int g = g0 + j, s = g % C::QS;
-        const float4 x = next;
-        if (j + 1 < tiles)
-          next = make_float4(row_stat(j + 1, 4 * lane), row_stat(j + 1, 4 * lane + 1), row_stat(j + 1, 4 * lane + 2),
-                             row_stat(j + 1, 4 * lane + 3));
+        const float4 x = ahead[0];
+        ahead[0] = ahead[1];
+        ahead[1] = ahead[2];
+        ahead[2] = tile_stat(j + 3);
         if (g >= C::QS && !wait(B_STEMPTY + s, ((g / C::QS) - 1) & 1)) { ok = false; break; }
         reinterpret_cast<float4*>(smem + C::OFF_STAT + s * 512)[lane] = x;
         __syncwarp();
@@ -362,9 +378,9 @@ __global__ void __launch_bounds__(384, 1) prompt_weights_kernel(const __grid_con
     }
   } else {
     // ---------------------------------------------------------- weights
-    const int t = (warp - 4) >> 2, wq = warp & 3;
-    const int row = wq * 32 + lane;  // key of the tile
-    const uint32_t lane_addr = tmem + ((uint32_t)(wq * 32) << 16) + C::S_COL(t, 0);
+    const int t = (warp >> 2 & 1) ^ 1, half = warp >= 12, wq = warp & 3;  // key tile, columns 64 half ..
+    const int row = wq * 32 + lane;                                       // key of the tile
+    const uint32_t lane_addr = tmem + ((uint32_t)(wq * 32) << 16) + C::S_COL(t, 0) + 64u * half;
     const uint64_t c22 = f2_pack(a.scale_log2, a.scale_log2);
     int g0 = 0, c = 0;
     for (int i = 0; ok; ++i) {
@@ -383,7 +399,7 @@ __global__ void __launch_bounds__(384, 1) prompt_weights_kernel(const __grid_con
           const int b = c & 1;
           if (!wait(B_SFULL + 2 * t + b, (c >> 1) & 1)) { ok = false; break; }
           tc_fence_after();
-          const float* nl = reinterpret_cast<const float*>(smem + C::OFF_STAT + s * 512);
+          const float* nl = reinterpret_cast<const float*>(smem + C::OFF_STAT + s * 512) + 64 * half;
           // columns that this key's weight has a part in: from its diagonal on,
           // up to the sequence's end (the others may hold anything)
           const int first = diag0 - j * TP;
@@ -391,20 +407,28 @@ __global__ void __launch_bounds__(384, 1) prompt_weights_kernel(const __grid_con
           const bool masked = first + 127 > 0 || hi < 128;
           uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
           const uint32_t s_addr = lane_addr + 128u * (uint32_t)b;
+          if (masked) {
+            // a few tiles to a unit: the others' scores become -inf where they
+            // stand, and no mask is in the pass below
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {
+              uint32_t r[32];
+              tmem_ld32(s_addr + 32 * q, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int u = 0; u < 32; ++u)
+                r[u] = 64 * half + 32 * q + u < lo || 64 * half + 32 * q + u >= hi ? __float_as_uint(-INFINITY) : r[u];
+              tmem_st32(s_addr + 32 * q, r);
+            }
+            tmem_st_wait();
+          }
           auto add = [&](const uint32_t (&r)[32], int q) {
 #pragma unroll
             for (int k4 = 0; k4 < 8; ++k4) {
               const float4 n4 = *reinterpret_cast<const float4*>(nl + 32 * q + 4 * k4);
               const float2 xa = f2_unpack(ffma2(f2_pack(__uint_as_float(r[4 * k4]), __uint_as_float(r[4 * k4 + 1])), c22, f2_pack(n4.x, n4.y)));
               const float2 xb = f2_unpack(ffma2(f2_pack(__uint_as_float(r[4 * k4 + 2]), __uint_as_float(r[4 * k4 + 3])), c22, f2_pack(n4.z, n4.w)));
-              float p0 = ex2_approx(xa.x), p1 = ex2_approx(xa.y), p2 = ex2_approx(xb.x), p3 = ex2_approx(xb.y);
-              if (masked) {
-                const int col = 32 * q + 4 * k4;
-                p0 = col < lo || col >= hi ? 0.f : p0;
-                p1 = col + 1 < lo || col + 1 >= hi ? 0.f : p1;
-                p2 = col + 2 < lo || col + 2 >= hi ? 0.f : p2;
-                p3 = col + 3 < lo || col + 3 >= hi ? 0.f : p3;
-              }
+              const float p0 = ex2_approx(xa.x), p1 = ex2_approx(xa.y), p2 = ex2_approx(xb.x), p3 = ex2_approx(xb.y);
               sum[k4 & 1] = fadd2(sum[k4 & 1], f2_pack(p0, p1));
               sum[2 + (k4 & 1)] = fadd2(sum[2 + (k4 & 1)], f2_pack(p2, p3));
             }
@@ -415,17 +439,11 @@ __global__ void __launch_bounds__(384, 1) prompt_weights_kernel(const __grid_con
           tmem_ld32(s_addr + 32, rb);
           add(ra, 0);
           tmem_ld_wait_dep(rb);
-          tmem_ld32(s_addr + 64, ra);
-          add(rb, 1);
-          tmem_ld_wait_dep(ra);
-          tmem_ld32(s_addr + 96, rb);
-          add(ra, 2);
-          tmem_ld_wait_dep(rb);
           // all of S is in registers: its buffer takes the tile after next
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(BAR(B_SFREE + 2 * t + b));
-          add(rb, 3);
+          add(rb, 1);
           ++c;
           const float2 sa = f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])));
           const float y = __fsub_rn(__fadd_rn(sa.x, sa.y), lost), z = __fadd_rn(total, y);
@@ -436,11 +454,25 @@ __global__ void __launch_bounds__(384, 1) prompt_weights_kernel(const __grid_con
         if (lane == 0) mbar_arrive(BAR(B_STEMPTY + s));
       }
       if (!ok) break;
+      // the second half's sums go to the first's warps
+      volatile float* part = reinterpret_cast<float*>(smem + C::OFF_PART + t * 512) + row;
+      g0 += tiles;
+      if (half) {
+        if (i > 0 && !wait(B_PART + 2 + t, (i - 1) & 1)) { ok = false; break; }
+        *part = total;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_PART + t));
+        release_item(i);
+        continue;
+      }
+      if (!wait(B_PART + t, i & 1)) { ok = false; break; }
+      total += *part;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(B_PART + 2 + t));
       const int left = item(i, kWLeft), key = item(i, kWKey0) + 128 * t + row, fresh = item(i, kWNew);
       float* w = a.W + (long long)item(i, kWSeq) * a.w_batch + (long long)item(i, kWHead) * a.w_head + key;
       // keys that are new with these tokens have no weight yet
       if (128 * t + row < left) *w = a.accumulate && key < fresh ? *w + total : total;
-      g0 += tiles;
       release_item(i);
     }
   }
@@ -457,7 +489,7 @@ __global__ void __launch_bounds__(384, 1) prompt_weights_kernel(const __grid_con
 template <int D, bool PAGED>
 cudaError_t launch_d(const PromptWeightArgs& a, cudaStream_t st) {
   using C = WCfg<D>;
-  static_assert(C::ALLOC <= 227 * 1024, "shared memory budget");
+  static_assert(C::BYTES <= C::MOST, "shared memory budget");
   const long long ctas = a.max_units * a.Hkv;
   if (a.max_units < 1 || ctas > 0x7fffffffll) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(prompt_weights_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ALLOC);
