@@ -102,8 +102,8 @@ struct PromptCfg : FwdCfg<D> {
   static constexpr int ITEM_INTS = 12;
   static constexpr int OFF_BARS = OFF_STAT + 2 * 2 * 128 * 8;
   // q_full[2], q_empty[2], k_full, v_full, k_empty, v_empty [STAGES each], s_full[2], p_full[2],
-  // o_done[2], s_free[2], o_free[2], l_full[2 tiles][2 blocks], item_full, item_empty [IRING each], cancel, drain
-  static constexpr int NBARS = 4 + 4 * F::STAGES + 14 + 2 * IRING + 2;
+  // o_done[2], s_free[2], o_free[2], l_full[2 tiles][2 blocks], item_full, item_empty [IRING each], cancel, near, drain
+  static constexpr int NBARS = 4 + 4 * F::STAGES + 14 + 2 * IRING + 3;
   static constexpr int OFF_ITEMS = (OFF_BARS + NBARS * 8 + 15) / 16 * 16;
   static constexpr int OFF_CANCEL = OFF_ITEMS + IRING * ITEM_INTS * 4;  // 16 bytes: the next CTA index
   static constexpr int OFF_MISC = OFF_CANCEL + 16;                      // TMEM base, abort flag
@@ -133,7 +133,8 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
   const int B_QFULL = 0, B_QEMPTY = 2, B_KFULL = 4, B_VFULL = B_KFULL + C::STAGES, B_KEMPTY = B_VFULL + C::STAGES,
             B_VEMPTY = B_KEMPTY + C::STAGES, B_SFULL = B_VEMPTY + C::STAGES, B_PFULL = B_SFULL + 2,
             B_ODONE = B_PFULL + 2, B_SFREE = B_ODONE + 2, B_OFREE = B_SFREE + 2, B_LFULL = B_OFREE + 2,
-            B_ITF = B_LFULL + 4, B_ITE = B_ITF + C::IRING, B_CANCEL = B_ITE + C::IRING, B_DRAIN = B_CANCEL + 1;
+            B_ITF = B_LFULL + 4, B_ITE = B_ITF + C::IRING, B_CANCEL = B_ITE + C::IRING, B_NEAR = B_CANCEL + 1,
+            B_DRAIN = B_NEAR + 1;
   volatile int* items = reinterpret_cast<volatile int*>(smem + C::OFF_ITEMS);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
@@ -164,6 +165,7 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
       mbar_init(BAR(B_ITE + s), 14);  // one arrival per consuming warp: producer, MMA, 8 softmax, 4 output
     }
     mbar_init(BAR(B_CANCEL), 1);
+    mbar_init(BAR(B_NEAR), 1);
     mbar_init(BAR(B_DRAIN), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -199,6 +201,9 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
       for (int i = 0; ok && u >= 0; ++i) {
         const int s = i % C::IRING;
         if (i >= C::IRING) ok = wait(B_ITE + s, ((i / C::IRING) - 1) & 1);
+        // Not before the block in work is near its end: a CTA with a long one would
+        // hold the next back from those that run dry.
+        if (ok && i > 0) ok = wait(B_NEAR, (i - 1) & 1);
         if (ok && i > 0) {
           // the CTA that would begin next gives its index to this one, if any is left
           if (lane == 0) {
@@ -326,8 +331,10 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
           last_v = g;
           page = next_page;
           row = next_row;
+          if (j == max(0, n_max - 3) && lane == 0) mbar_arrive(BAR(B_NEAR));
         }
         if (!ok) break;
+        if (n_max == 0 && lane == 0) mbar_arrive(BAR(B_NEAR));
         g0 += n_max;
         release_item(i);
       }

@@ -49,8 +49,8 @@ struct WCfg {
   static constexpr int OFF_PART = OFF_STAT + QS * 512;  // [2 tiles][128] sums of the second column halves
   static constexpr int OFF_BARS = OFF_PART + 2 * 512;
   // k_full[2], k_empty[2], q_full[QS], q_empty[QS], st_full[QS], st_empty[QS], s_full[2][2], s_free[2][2],
-  // part_full[2], part_free[2], item_full[2], item_empty[2], cancel, drain
-  static constexpr int NBARS = 4 + 4 * QS + 12 + 2 * IRING + 2;
+  // part_full[2], part_free[2], item_full[2], item_empty[2], cancel, near, drain
+  static constexpr int NBARS = 4 + 4 * QS + 12 + 2 * IRING + 3;
   static constexpr int OFF_ITEMS = (OFF_BARS + NBARS * 8 + 15) / 16 * 16;
   static constexpr int OFF_CANCEL = OFF_ITEMS + IRING * ITEM_INTS * 4;
   static constexpr int OFF_MISC = OFF_CANCEL + 16;
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
   auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   const int B_KFULL = 0, B_KEMPTY = 2, B_QFULL = 4, B_QEMPTY = B_QFULL + C::QS, B_STFULL = B_QEMPTY + C::QS,
             B_STEMPTY = B_STFULL + C::QS, B_SFULL = B_STEMPTY + C::QS, B_SFREE = B_SFULL + 4, B_PART = B_SFREE + 4, B_ITF = B_PART + 4,
-            B_ITE = B_ITF + C::IRING, B_CANCEL = B_ITE + C::IRING, B_DRAIN = B_CANCEL + 1;
+            B_ITE = B_ITF + C::IRING, B_CANCEL = B_ITE + C::IRING, B_NEAR = B_CANCEL + 1, B_DRAIN = B_NEAR + 1;
   volatile int* items = reinterpret_cast<volatile int*>(smem + C::OFF_ITEMS);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
@@ -161,6 +161,7 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
       mbar_init(BAR(B_ITE + s), 19);  // producer, MMA, statistics, 16 weights warps
     }
     mbar_init(BAR(B_CANCEL), 1);
+    mbar_init(BAR(B_NEAR), 1);
     mbar_init(BAR(B_DRAIN), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -198,6 +199,9 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
     for (int i = 0; ok && u >= 0; ++i) {
       const int s = i % C::IRING;
       if (i >= C::IRING) ok = wait(B_ITE + s, ((i / C::IRING) - 1) & 1);
+      // not before the unit in work is near its end: a CTA with a long one would
+      // hold the next back from those that run dry
+      if (ok && i > 0) ok = wait(B_NEAR, (i - 1) & 1);
       if (ok && i > 0) {
         if (lane == 0) {
           mbar_arrive_expect_tx(BAR(B_CANCEL), 16);
@@ -283,6 +287,7 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
           skipped = g;
         }
         last_q = g;
+        if (j == max(0, tiles - 4) && lane == 0) mbar_arrive(BAR(B_NEAR));
       }
       if (!ok) break;
       g0 += tiles;
