@@ -280,7 +280,7 @@ constexpr int kPromptMaxTokens = 1 << 30;
 inline int prompt_tile_tokens(int G) { return 128 / G; }
 
 struct PromptFwdArgs {
-  CUtensorMap tmQ;       // 4-D (d, head of the group, token, K/V head), boxes 64 x G x TP x 1
+  CUtensorMap tmQ, tmO;  // 4-D (d, head of the group, token, K/V head), boxes 64 x G x TP x 1
   CUtensorMap tmK, tmV;  // packed: 3-D (d, token, head), boxes 64 x 128 x 1; paged: the pool (encode_pool_bf16)
   PromptSeqs seqs;
   PagedPool pool;            // paged only

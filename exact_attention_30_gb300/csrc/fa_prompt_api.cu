@@ -135,7 +135,8 @@ fa_status fwd_launch(PromptFwdArgs& a, const void* Q, long long q_stride, void* 
     a.Opart = static_cast<float*>(workspace);
     a.Lpart = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.lpart);
   }
-  if (!encode_grouped(&a.tmQ, Q, token_stride(q_stride, total_q, Hq, d), G, a.Hkv, total_q, a.tile_tokens, d))
+  if (!encode_grouped(&a.tmQ, Q, token_stride(q_stride, total_q, Hq, d), G, a.Hkv, total_q, a.tile_tokens, d) ||
+      !encode_grouped(&a.tmO, O, a.o_stride, G, a.Hkv, total_q, a.tile_tokens, d))
     return FA_ERR_CUDA;
   return launch_prompt_fwd(a, d, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

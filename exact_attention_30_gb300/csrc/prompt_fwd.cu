@@ -89,29 +89,31 @@ __device__ __forceinline__ bool prompt_block(const PromptFwdArgs& a, long long u
 
 // Warps 0-3: producer, MMA issuer, scheduler, none; 4-7 and 8-11: softmax of
 // query tiles 0 and 1; 12-15: output. Shared memory: that of the two-tile
-// forward, a 4 KB staging buffer for each output warp, the rows' statistics on
-// their way to the output warps and a ring of published blocks.
+// forward, a tile of O on its way out, the rows' sums on their way to the output
+// warps and a ring of published blocks.
 template <int D>
 struct PromptCfg : FwdCfg<D> {
   using F = FwdCfg<D>;
   static constexpr int NTHREADS = 512;
-  static constexpr int STAGE_BYTES = 32 * 128;
-  static constexpr int OFF_STAGE = F::OFF_BAR;  // behind the K/V ring
-  static constexpr int OFF_STAT = OFF_STAGE + 4 * STAGE_BYTES;  // float2 [2 blocks][2 tiles][128 rows]: maximum, sum
+  static constexpr int OFF_STAGE = F::OFF_BAR;  // behind the K/V ring: 128 rows of O, as the query tiles are laid out
+  static constexpr int OFF_STAT = OFF_STAGE + F::TILE_BYTES;  // float [2 blocks][2 tiles][128 rows]: sums of weights
   static constexpr int IRING = 2;  // blocks published: the one in work and the next
   static constexpr int ITEM_INTS = 12;
-  static constexpr int OFF_BARS = OFF_STAT + 2 * 2 * 128 * 8;
-  // q_full[2], q_empty[2], k_full, v_full, k_empty, v_empty [STAGES each], s_full[2], p_full[2],
-  // o_done[2], s_free[2], o_free[2], l_full[2 tiles][2 blocks], item_full, item_empty [IRING each], cancel, near, drain
-  static constexpr int NBARS = 4 + 4 * F::STAGES + 14 + 2 * IRING + 3;
+  static constexpr int OFF_BARS = OFF_STAT + 2 * 2 * 128 * 4;
+  // q_full[2], q_empty[2], k_full, v_full, k_empty, v_empty [STAGES each], s_full[2], p_full[2], o_done[2],
+  // s_free[2], o_free[2], l_full[2 tiles][2 blocks], stage_full, stage_free, item_full, item_empty [IRING each],
+  // cancel, near, drain
+  static constexpr int NBARS = 4 + 4 * F::STAGES + 16 + 2 * IRING + 3;
   static constexpr int OFF_ITEMS = (OFF_BARS + NBARS * 8 + 15) / 16 * 16;
   static constexpr int OFF_CANCEL = OFF_ITEMS + IRING * ITEM_INTS * 4;  // 16 bytes: the next CTA index
   static constexpr int OFF_MISC = OFF_CANCEL + 16;                      // TMEM base, abort flag
   static constexpr int BYTES = OFF_MISC + 8;
-  static constexpr int ALLOC = BYTES + 1024;  // slack for 1024-byte alignment
-  // Registers per thread of the control, softmax and output warps: with the
-  // launch's 128 each, 128 * (56 + 2 * 176 + 104) = 512 * 128.
-  static constexpr int R_CONTROL = 56, R_SOFTMAX = 176, R_OUT = 104;
+  static constexpr int MOST = 227 * 1024;
+  // 1 KB of alignment slack where it fits; the kernel checks the alignment
+  static constexpr int ALLOC = BYTES + 1024 <= MOST ? BYTES + 1024 : MOST;
+  // Registers per thread of the control, softmax and output warps, out of the
+  // launch's 128 each: control + 2 softmax + out = 512.
+  static constexpr int R_CONTROL = D == 128 ? 64 : 72, R_SOFTMAX = D == 128 ? 176 : 168, R_OUT = D == 128 ? 96 : 104;
   static_assert(128 * (R_CONTROL + 2 * R_SOFTMAX + R_OUT) <= NTHREADS * 128, "register split");
 };
 
@@ -125,15 +127,21 @@ enum : int { kItQ0, kItN, kItHead, kItTok0, kItKt0, kItN0, kItN1, kItPart, kItK0
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constant__ PromptFwdArgs a) {
   using C = PromptCfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t pad = ((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + pad;
   const uint32_t sbase = smem_u32(smem);
+  if (pad + C::BYTES > (uint32_t)C::ALLOC) {
+    // cannot place the swizzled tiles: report and leave before touching anything
+    if (threadIdx.x == 0) report_status(a.status, kStatusTimeout);
+    return;
+  }
   const uint32_t bar0 = sbase + C::OFF_BARS;
   auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   const int B_QFULL = 0, B_QEMPTY = 2, B_KFULL = 4, B_VFULL = B_KFULL + C::STAGES, B_KEMPTY = B_VFULL + C::STAGES,
             B_VEMPTY = B_KEMPTY + C::STAGES, B_SFULL = B_VEMPTY + C::STAGES, B_PFULL = B_SFULL + 2,
             B_ODONE = B_PFULL + 2, B_SFREE = B_ODONE + 2, B_OFREE = B_SFREE + 2, B_LFULL = B_OFREE + 2,
-            B_ITF = B_LFULL + 4, B_ITE = B_ITF + C::IRING, B_CANCEL = B_ITE + C::IRING, B_NEAR = B_CANCEL + 1,
+            B_STAGE = B_LFULL + 4, B_ITF = B_STAGE + 2, B_ITE = B_ITF + C::IRING, B_CANCEL = B_ITE + C::IRING, B_NEAR = B_CANCEL + 1,
             B_DRAIN = B_NEAR + 1;
   volatile int* items = reinterpret_cast<volatile int*>(smem + C::OFF_ITEMS);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
@@ -164,6 +172,8 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
       mbar_init(BAR(B_ITF + s), 1);   // the scheduler
       mbar_init(BAR(B_ITE + s), 14);  // one arrival per consuming warp: producer, MMA, 8 softmax, 4 output
     }
+    mbar_init(BAR(B_STAGE), 4);      // stage_full: one arrival per output warp
+    mbar_init(BAR(B_STAGE + 1), 1);  // stage_free
     mbar_init(BAR(B_CANCEL), 1);
     mbar_init(BAR(B_NEAR), 1);
     mbar_init(BAR(B_DRAIN), 1);
@@ -435,11 +445,11 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
         for (int t = 0; ok && t < C::QT; ++t) ok = first_s(t, t == 0 ? n0 : n1, g0, t == 0 ? c0 : c1, false);
         if (!ok) break;
         s_done = 0;
-        // the accumulators have left tensor memory (the block's first P V is at
-        // least a softmax away)
-        if (n0 > 0 && q0_used > 1) ok = wait(B_OFREE + 0, q0_used & 1);
-        if (n1 > 0 && q1_used > 1) ok = ok && wait(B_OFREE + 1, q1_used & 1);
-        if (!ok) break;
+        // before the block's first P V: the accumulator has left tensor memory
+        auto o_free = [&](int t, int j) {
+          const int used = t == 0 ? q0_used : q1_used;
+          return j > 0 || used <= 1 || wait(B_OFREE + t, used & 1);
+        };
         if (n_max > 0) mma_commit(BAR(B_KEMPTY + g0 % C::STAGES), leader);
         // The tiles that neither query tile ends near: whole keys, a next S for
         // both. The loop is kept short (a wait and sixteen products per tile):
@@ -464,13 +474,13 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
               if (!ok) break;
               tc_fence_after();
               issue_s(t, s1, false);
-              ok = wait(B_PFULL + t, pt);
+              ok = wait(B_PFULL + t, pt) && o_free(t, j);
               if (t == 0) ok = ok && wait(B_VFULL + s, (g / C::STAGES) & 1);
               if (!ok) break;
               tc_fence_after();
               issue_pv(t, s, j > 0);
             } else {
-              ok = ok && wait(B_PFULL + t, pt);
+              ok = ok && wait(B_PFULL + t, pt) && o_free(t, j);
               if (!ok) break;
               tc_fence_after();
               issue_pv(t, s, j > 0);
@@ -518,12 +528,12 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
               if constexpr (C::P_OWN) {
                 // P has its own columns: S_{j+1} goes first, P_j V_j follows
                 if (more && !(wait(B_SFREE + t, pt) && next_s(t))) { ok = false; break; }
-                if (!wait(B_PFULL + t, pt) || !need_v()) { ok = false; break; }
+                if (!wait(B_PFULL + t, pt) || !o_free(t, j) || !need_v()) { ok = false; break; }
                 tc_fence_after();
                 issue_pv_keys(t, s, j > 0, keys);
               } else {
                 // P overwrites S: P_j V_j must be issued before S_{j+1}
-                if (!need_v() || !wait(B_PFULL + t, pt)) { ok = false; break; }
+                if (!need_v() || !wait(B_PFULL + t, pt) || !o_free(t, j)) { ok = false; break; }
                 tc_fence_after();
                 issue_pv_keys(t, s, j > 0, keys);
                 if (more && !next_s(t)) { ok = false; break; }
@@ -685,10 +695,19 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
       tmem_st_wait();  // no TMEM store may be in flight when the loop is left early
       if (!ok) break;
       c += n_own;
-      // the row's statistics, for the output warps
-      reinterpret_cast<float2*>(smem + C::OFF_STAT)[((i & 1) * 2 + t) * 128 + row] = make_float2(m_ref, l);
+      // the row's sum goes to the output warps, its log-sum-exp out from here
+      reinterpret_cast<float*>(smem + C::OFF_STAT)[((i & 1) * 2 + t) * 128 + row] = l;
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(B_LFULL + 2 * t + (i & 1)));
+      const float lse2 = m_ref + __log2f(l);  // -inf for a row without keys
+      const int n = item(i, kItN), tok0 = item(i, kItTok0) + t * TP, tok_in = a.g_div(row);
+      if (a.splits > 1) {
+        if (tok0 < n) a.Lpart[((long long)item(i, kItPart) * 2 + t) * C::BM + row] = lse2;
+      } else {
+        const int q0 = item(i, kItQ0), hq0 = item(i, kItHead) * a.G;
+        if (row < RT && tok0 + tok_in < n)
+          a.LSE[(size_t)(hq0 + row - tok_in * a.G) * a.seqs.total_q + q0 + tok0 + tok_in] = lse2 * 0.69314718055994531f;
+      }
       release_item(i);
     }
     if (!ok) *abort_flag = 1;
@@ -696,14 +715,17 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
     set_max_registers_dec<C::R_OUT>();
     // -------------------------------------------------------------- output
     // O of both tiles leaves tensor memory here, so that the softmax warps go on
-    // to the next block at once.
+    // to the next block at once, whose first P V follows two microseconds later:
+    // by then the accumulators have to be free. So a tile is staged as fast as
+    // it can be read, and a TMA store takes it out of the staging buffer.
     const int wq = warp & 3;
     const uint32_t lane_addr = tmem + ((uint32_t)(wq * 32) << 16);
     const int row = wq * 32 + lane;
-    uint8_t* stage = smem + C::OFF_STAGE + wq * C::STAGE_BYTES;  // [32 rows][128 bytes]
     const int rsub = lane >> 3, unit = lane & 7;
     bool ok = true;
     int c0 = 0, c1 = 0;  // key tiles of query tiles 0 and 1 before the block
+    int staged = 0;      // tiles staged so far
+    if (lane == 0 && wq == 0) tma_prefetch_desc(&a.tmO);
     for (int i = 0; ok; ++i) {
       if (!get_item(i)) { ok = false; break; }
       const int n0 = item(i, kItN0), n1 = item(i, kItN1);
@@ -714,33 +736,40 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {
         const int n_own = t == 0 ? n0 : n1, tok0 = item(i, kItTok0) + t * TP;
-        // the row's statistics, then its last P V (in this order: the barrier
-        // of the latter can be a phase behind until the former are there)
+        // the row's sum, then its last P V (in this order: the barrier of the
+        // latter can be a phase behind until the former is there)
         if (!wait(B_LFULL + 2 * t + (i & 1), (i >> 1) & 1)) { ok = false; break; }
-        const float2 ml = reinterpret_cast<const float2*>(smem + C::OFF_STAT)[((i & 1) * 2 + t) * 128 + row];
-        if (n_own > 0 && !wait(B_ODONE + t, ((t == 0 ? c0 : c1) - 1) & 1)) { ok = false; break; }
-        tc_fence_after();
-        const float l = ml.y, inv_l = l == 0.f ? 0.f : 1.f / l;
-        const float lse2 = ml.x + __log2f(l);  // -inf for a row without keys
+        const float l = reinterpret_cast<const float*>(smem + C::OFF_STAT)[((i & 1) * 2 + t) * 128 + row];
+        if (tok0 >= n) continue;  // no such tile
         const bool any = n_own > 0, some = any && l != 0.f;
+        const float inv_l = some ? 1.f / l : 0.f;
         const uint32_t o_addr = lane_addr + C::O_COL(t);
+        // 32 columns of the row, normalised (zeros for a row without keys)
+        auto read_o = [&](int q, uint32_t (&r)[32]) {
+          if (any) {
+            tmem_ld32(o_addr + 32 * q, r);
+            tmem_ld_wait();
+          }
+#pragma unroll
+          for (int u = 0; u < 32; ++u) r[u] = some ? __float_as_uint(__uint_as_float(r[u]) * inv_l) : 0u;
+        };
         auto free_o = [&]() {  // the tensor memory has been read
           tc_fence_before();
           __syncwarp();
           if (any && lane == 0) mbar_arrive(BAR(B_OFREE + t));
         };
+        if (any && !wait(B_ODONE + t, ((t == 0 ? c0 : c1) - 1) & 1)) { ok = false; break; }
+        tc_fence_after();
         if (a.splits > 1) {
-          // fp32 rows of this key range; a range without keys leaves only its log-sum-exp
-          const long long prow0 = (long long)item(i, kItPart) * (2 * C::BM) + t * C::BM + wq * 32;
-          if (tok0 < n) a.Lpart[prow0 + lane] = lse2;
+          // fp32 rows of this key range (one without keys leaves only its
+          // log-sum-exp), 128 bytes of each row of the warp at a time
+          const long long prow0 = ((long long)item(i, kItPart) * 2 + t) * C::BM + wq * 32;
+          uint8_t* stage = smem + C::OFF_STAGE + wq * (32 * 128);
           if (any) {
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
               uint32_t r[32];
-              tmem_ld32(o_addr + 32 * q, r);
-              tmem_ld_wait();
-#pragma unroll
-              for (int u = 0; u < 32; ++u) r[u] = some ? __float_as_uint(__uint_as_float(r[u]) * inv_l) : 0u;
+              read_o(q, r);
 #pragma unroll
               for (int u = 0; u < 8; ++u)
                 *reinterpret_cast<uint4*>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) =
@@ -758,47 +787,58 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
           free_o();
           continue;
         }
-        // 64 columns of a row as bf16 at a time; out through the staging buffer,
-        // 128 bytes of each of the warp's 32 rows in the swizzle that spreads
-        // them over the banks, read back so that a store instruction writes
-        // whole 128-byte rows.
+        // the tile before has left the staging buffer
+        if (staged > 0 && !wait(B_STAGE + 1, (staged - 1) & 1)) { ok = false; break; }
+        uint8_t* stage = smem + C::OFF_STAGE;
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t r[32];
+          read_o(q, r);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            *reinterpret_cast<uint4*>(stage + (q >> 1) * C::CHUNK_BYTES + row * 128 + (((4 * (q & 1) + u) ^ (row & 7)) << 4)) =
+                make_uint4(pack_bf16x2(__uint_as_float(r[8 * u]), __uint_as_float(r[8 * u + 1])),
+                           pack_bf16x2(__uint_as_float(r[8 * u + 2]), __uint_as_float(r[8 * u + 3])),
+                           pack_bf16x2(__uint_as_float(r[8 * u + 4]), __uint_as_float(r[8 * u + 5])),
+                           pack_bf16x2(__uint_as_float(r[8 * u + 6]), __uint_as_float(r[8 * u + 7])));
+        }
+        free_o();
         const long long tok_q = item(i, kItQ0) + tok0;
-        const int hq0 = item(i, kItHead) * a.G;
+        const int head = item(i, kItHead);
+        const bool whole = tok0 + TP <= n;
+        if (whole) {
+          fence_proxy_async_smem();
+        } else {
+          // a sequence's last, partial tile: the warp's rows, 16 lanes to one
+          constexpr int LPR = D / 8;
+          const int x = lane % LPR;
 #pragma unroll 1
-        for (int h = 0; h < D / 64; ++h) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t r[32];
-            if (any) {
-              tmem_ld32(o_addr + 64 * h + 32 * q, r);
-              tmem_ld_wait();
-            }
-#pragma unroll
-            for (int u = 0; u < 16; ++u)
-              pk[16 * q + u] =
-                  some ? pack_bf16x2(__uint_as_float(r[2 * u]) * inv_l, __uint_as_float(r[2 * u + 1]) * inv_l) : 0u;
-          }
-          if (h + 1 == D / 64) free_o();
-          if (tok0 >= n) continue;  // no such tile
-#pragma unroll
-          for (int u = 0; u < 8; ++u)
-            *reinterpret_cast<uint4*>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) =
-                make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
-          __syncwarp();
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int rr = 4 * u + rsub, tr = wq * 32 + rr, tk = a.g_div(tr);
-            const uint4 y = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((unit ^ (rr & 7)) << 4));
+          for (int k = 0; k < 32; k += 32 / LPR) {
+            const int tr = wq * 32 + k + lane / LPR, tk = a.g_div(tr);
+            const uint4 y = *reinterpret_cast<const uint4*>(stage + (x >> 3) * C::CHUNK_BYTES + tr * 128 +
+                                                            (((x & 7) ^ (tr & 7)) << 4));
             if (tr < RT && tok0 + tk < n)
               *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.O) + (tok_q + tk) * a.o_stride +
-                                        (long long)(hq0 + tr - tk * a.G) * D + 64 * h + 8 * unit) = y;
+                                        (long long)(head * a.G + tr - tk * a.G) * D + 8 * x) = y;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_STAGE));
+        if (wq == 0) {
+          if (!wait(B_STAGE, staged & 1)) { ok = false; break; }
+          if (lane == 0) {
+            if (whole) {
+#pragma unroll
+              for (int c = 0; c < C::CH; ++c)
+                tma_store_4d(&a.tmO, sbase + C::OFF_STAGE + c * C::CHUNK_BYTES, c * 64, 0, (int)tok_q, head);
+              bulk_commit_group();
+              bulk_wait_group_read<0>();
+            }
+            mbar_arrive(BAR(B_STAGE + 1));
           }
           __syncwarp();
         }
-        const int tok_in = a.g_div(row);
-        if (row < RT && tok0 + tok_in < n)
-          a.LSE[(size_t)(hq0 + row - tok_in * a.G) * a.seqs.total_q + tok_q + tok_in] = lse2 * 0.69314718055994531f;
+        ++staged;
       }
       if (ok) release_item(i);
     }
@@ -872,7 +912,7 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const __grid_constant
 template <int D, bool PAGED>
 cudaError_t launch_d(const PromptFwdArgs& a, cudaStream_t st) {
   using C = PromptCfg<D>;
-  static_assert(C::ALLOC <= 227 * 1024, "shared memory budget");
+  static_assert(C::BYTES <= C::MOST, "shared memory budget");
   const long long ctas = a.max_blocks * a.Hkv * a.splits;
   if (a.splits < 1 || a.max_blocks < 1 || ctas > 0x7fffffffll || (a.splits > 1 && (!a.Opart || !a.Lpart)))
     return cudaErrorInvalidValue;
