@@ -381,12 +381,12 @@ struct EvictArgs {
   long long w_batch, w_head, wout_batch, wout_head;
   int* kept;                 // [B, Hkv, budget]
   int B, Hkv, d, max_pages, new_pages, w_keys, most_keys, budget, recent;
-  int pieces;                // column pieces of a row in the move
+  int pieces, shares;        // of the move: column pieces of a row, shares of the rows
   FastDiv page_div;
   int* status;
 };
 cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t st);
-int evict_pieces(int B, int Hkv, int d, int sms);
+void evict_split(int B, int Hkv, int d, int budget, bool in_place, int sms, int* pieces, int* shares);
 
 struct PagedDecodeArgs {
   CUtensorMap tmK, tmV;

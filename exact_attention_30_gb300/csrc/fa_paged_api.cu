@@ -429,7 +429,7 @@ fa_status fa_kv_evict(const fa_paged_kv* cache, const int* block_tables, int max
   a.status = device_status_ptr();
   const int sms = fwd_slots();
   if (!a.status || sms < 1) return FA_ERR_CUDA;
-  a.pieces = evict_pieces(B, a.Hkv, a.d, sms);
+  evict_split(B, a.Hkv, a.d, keep, new_tables == block_tables, sms, &a.pieces, &a.shares);
   return launch_kv_evict(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -8,16 +8,19 @@
 //    key that stays by a radix selection over 11, 11 and 10 bits of the weights'
 //    order (a histogram in shared memory, its suffix sums, the digit that holds
 //    the rank), then one pass over the weights in order that counts and lists.
-//    Bound by its passes over the weights (4 bytes a key and pass, from L2) and
-//    by latency: a few barriers per pass.
+//    Up to 49152 weights are held in shared memory, read once. Bound by latency
+//    (some 20 barriers) and the histogram's atomics.
 // 2. evict_move_kernel copies the rows. Bound by memory: each row that stays is
 //    read and written once; in place, rows that do not move are left alone. In
 //    place a row may only be written when the row it held has been read: since
 //    those that stay keep their order, row i's new content comes from a row >= i,
 //    so a CTA that goes through the rows in order, reading a batch before it
 //    writes it, never loses one. Rows of one head cannot be shared out among
-//    CTAs, therefore, but their columns can: keys and values, and pieces of 32 to
-//    128 bytes of a row, are CTAs of their own.
+//    CTAs, therefore, but their columns can: keys and values, and pieces of 64 or
+//    128 bytes of a row, are CTAs of their own. Into other pages, rows are shared
+//    out instead, and whole (a warp's load of 32-byte pieces touches 16 lines:
+//    8 x 8 x 2048 rows of 256 bytes took 41 us so). The next batch's indices and
+//    pages are looked up while this one's rows are on their way.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -27,7 +30,6 @@
 namespace fa {
 namespace {
 
-constexpr int kSelectThreads = 1024;
 constexpr int kBins = 2048;
 constexpr int kPerThread = 4;  // neighbouring weights of a thread in the listing pass
 
@@ -39,33 +41,46 @@ __device__ __forceinline__ unsigned order_of(float w) {
 }
 
 // Exclusive sum over the block's threads of `x`, and the total. `part`: 32 ints.
-__device__ __forceinline__ int block_scan(int x, int* part, int& total) {
+template <int THREADS>
+__device__ __forceinline__ int block_scan(int value, int* part, int& total) {
+  constexpr int WARPS = THREADS / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int sum = x;
+  const unsigned x = (unsigned)value;  // two counts in one word may pass 31 bits in the total
+  unsigned sum = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, sum, o);
+    const unsigned y = __shfl_up_sync(0xffffffffu, sum, o);
     if (lane >= o) sum += y;
   }
-  if (lane == 31) part[warp] = sum;
+  if (lane == 31) part[warp] = (int)sum;
   __syncthreads();
-  int p = part[lane];
+  unsigned p = lane < WARPS ? (unsigned)part[lane] : 0u;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, p, o);
+  for (int o = 1; o < WARPS; o <<= 1) {
+    const unsigned y = __shfl_up_sync(0xffffffffu, p, o);
     if (lane >= o) p += y;
   }
-  total = __shfl_sync(0xffffffffu, p, 31);
-  const int before = warp > 0 ? __shfl_sync(0xffffffffu, p, warp - 1) : 0;
+  total = (int)__shfl_sync(0xffffffffu, p, WARPS - 1);
+  const unsigned before = warp > 0 ? __shfl_sync(0xffffffffu, p, warp - 1) : 0u;
   __syncthreads();
-  return before + sum - x;
+  return (int)(before + sum - x);
 }
 
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __grid_constant__ EvictArgs a) {
-  __shared__ int hist[kBins];
+// Bin i of the histogram, one word in 33 left out: a thread's eight neighbouring
+// bins then fall on banks of their own.
+__device__ __forceinline__ int bin_at(int i) { return i + (i >> 5); }
+
+// HELD: the weights are copied to (dynamic) shared memory first and read there;
+// else from memory in each pass.
+template <int THREADS, bool HELD>
+__global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_constant__ EvictArgs a) {
+  constexpr int BPT = kBins / THREADS;  // bins of a thread
+  extern __shared__ __align__(16) float held[];
+  __shared__ int hist[kBins + kBins / 32];
   __shared__ int part[32];
   __shared__ int found_bin, found_above;
   const int h = blockIdx.x, b = blockIdx.y, t = threadIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the move's CTAs may come; they wait for this grid
   int len = a.seq_lens[b];
   if (len < 0 || len > a.most_keys || len > a.w_keys) {
     if (h == 0 && t == 0) report_status(a.status, kStatusBadSeqlens);
@@ -77,7 +92,16 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
   const int count = min(len, a.budget), recent = min(a.recent, len);
   const int old = len - recent;   // keys that the weights decide on
   const int need = count - recent;  // how many of them stay
-  for (int i = count + t; i < a.budget; i += kSelectThreads) kept[i] = -1;
+  for (int i = count + t; i < a.budget; i += THREADS) kept[i] = -1;
+  for (int i = t; i < kBins + kBins / 32; i += THREADS) hist[i] = 0;
+  if constexpr (HELD) {
+    const int whole = (reinterpret_cast<uintptr_t>(w) & 15) == 0 ? len / 4 : 0;
+#pragma unroll 4
+    for (int j = t; j < whole; j += THREADS) reinterpret_cast<float4*>(held)[j] = reinterpret_cast<const float4*>(w)[j];
+    for (int j = 4 * whole + t; j < len; j += THREADS) held[j] = w[j];
+  }
+  __syncthreads();
+  auto weight = [&](int j) { return HELD ? held[j] : w[j]; };
 
   unsigned least = 0;   // order of the last weight that stays
   int ties = 0;         // how many of that order stay
@@ -88,30 +112,36 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const unsigned digits = pass == 2 ? 1023u : 2047u;
-      for (int i = t; i < kBins; i += kSelectThreads) hist[i] = 0;
-      __syncthreads();
 #pragma unroll 4
-      for (int j = t; j < old; j += kSelectThreads) {
-        const unsigned x = order_of(w[j]);
-        if ((x & mask) == prefix) atomicAdd(&hist[(x >> shift) & digits], 1);
+      for (int j = t; j < old; j += THREADS) {
+        const unsigned u = order_of(weight(j));
+        if ((u & mask) == prefix) atomicAdd(&hist[bin_at((u >> shift) & digits)], 1);
       }
       __syncthreads();
-      // bins from the top: thread t has bins 2047 - 2 t and 2046 - 2 t
-      const int x0 = hist[kBins - 1 - 2 * t], x1 = hist[kBins - 2 - 2 * t];
-      int total;
-      const int above = block_scan(x0 + x1, part, total);
-      if (above < rank && rank <= above + x0) {
-        found_bin = kBins - 1 - 2 * t;
-        found_above = above;
-      } else if (above + x0 < rank && rank <= above + x0 + x1) {
-        found_bin = kBins - 2 - 2 * t;
-        found_above = above + x0;
+      // bins from the top: thread t has the BPT bins below kBins - t BPT, and
+      // clears them for the next pass
+      int n[BPT], mine = 0, total;
+#pragma unroll
+      for (int e = 0; e < BPT; ++e) {
+        int* bin = &hist[bin_at(kBins - 1 - t * BPT - e)];
+        mine += n[e] = *bin;
+        *bin = 0;
+      }
+      int above = block_scan<THREADS>(mine, part, total);
+      if (above < rank && rank <= above + mine) {
+#pragma unroll
+        for (int e = 0; e < BPT; ++e) {
+          if (above < rank && rank <= above + n[e]) {
+            found_bin = kBins - 1 - t * BPT - e;
+            found_above = above;
+          }
+          above += n[e];
+        }
       }
       __syncthreads();
       prefix |= (unsigned)found_bin << shift;
       mask |= digits << shift;
       rank -= found_above;
-      __syncthreads();
     }
     least = prefix;
     ties = rank;
@@ -122,24 +152,23 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
   int larger = 0, equal = 0;  // before this chunk
   if (need > 0) {
 #pragma unroll 1
-    for (int j0 = 0; j0 < old; j0 += kSelectThreads * kPerThread) {
+    for (int j0 = 0; j0 < old; j0 += THREADS * kPerThread) {
       const int j = j0 + t * kPerThread;
-      float x[kPerThread];
-      int mine = 0;  // larger ones in the low half, equal ones in the high half
+      float y[kPerThread];
       unsigned gt = 0, eq = 0;
 #pragma unroll
       for (int e = 0; e < kPerThread; ++e) {
-        x[e] = 0.f;
+        y[e] = 0.f;
         if (j + e < old) {
-          x[e] = w[j + e];
-          const unsigned u = order_of(x[e]);
+          y[e] = weight(j + e);
+          const unsigned u = order_of(y[e]);
           if (all || u > least) gt |= 1u << e;
           else if (u == least) eq |= 1u << e;
         }
       }
-      mine = __popc(gt) | __popc(eq) << 16;
+      // larger ones in the low half, equal ones in the high half
       int total;
-      const int before = block_scan(mine, part, total);  // also: the chunk is read before it is written
+      const int before = block_scan<THREADS>(__popc(gt) | __popc(eq) << 16, part, total);  // also: the chunk is read before it is written
       int ng = larger + (before & 0xffff), ne = equal + (before >> 16);
 #pragma unroll
       for (int e = 0; e < kPerThread; ++e) {
@@ -147,37 +176,41 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
         if ((gt >> e & 1u) || (is_eq && ne < ties)) {
           const int pos = ng + min(ne, ties);
           kept[pos] = j + e;
-          out_w[pos] = x[e];
+          out_w[pos] = y[e];
         }
         ng += gt >> e & 1u;
         ne += is_eq;
       }
       larger += total & 0xffff;
       equal += total >> 16;
-      __syncthreads();
     }
   }
-  // the newest ones
+  // the newest ones (in place, and not held: their weights may lie where the
+  // list's last ones went only if they are read a batch ahead)
 #pragma unroll 1
-  for (int j0 = 0; j0 < recent; j0 += kSelectThreads) {
+  for (int j0 = 0; j0 < recent; j0 += THREADS) {
     const int j = j0 + t;
-    const float x = j < recent ? w[old + j] : 0.f;
+    const float y = j < recent ? weight(old + j) : 0.f;
     __syncthreads();
     if (j < recent) {
       kept[need + j] = old + j;
-      out_w[need + j] = x;
+      out_w[need + j] = y;
     }
   }
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveLoads = 8;  // 16-byte loads of a thread in flight
+constexpr int kMoveLoads = 4;  // 16-byte loads of a thread in flight
 
-// CTA (piece, head, sequence); pieces: keys, then values, a.pieces columns each.
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a) {
+// CTA (part, head, sequence): parts are pieces of a row's columns (in place) or
+// shares of the rows, of the keys first, then of the values.
+__global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __grid_constant__ EvictArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the lists are there
   const int h = blockIdx.y, b = blockIdx.z, t = threadIdx.x;
-  const bool values = (int)blockIdx.x >= a.pieces;
-  const int piece = (int)blockIdx.x - (values ? a.pieces : 0);
+  const int parts = a.pieces * a.shares;
+  const bool values = (int)blockIdx.x >= parts;
+  const int part = (int)blockIdx.x - (values ? parts : 0);
+  const int piece = part % a.pieces, share = part / a.pieces;
   if (blockIdx.x == 0 && h == 0 && t == 0) {
     const int len = a.seq_lens[b];
     a.new_lens[b] = len < 0 || len > a.most_keys || len > a.w_keys ? len : min(len, a.budget);
@@ -188,62 +221,110 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   __nv_bfloat16* pool = static_cast<__nv_bfloat16*>(values ? a.pool.v : a.pool.k);
   const long long s_page = values ? a.pool.v_page : a.pool.k_page, s_head = values ? a.pool.v_head : a.pool.k_head,
                   s_row = values ? a.pool.v_row : a.pool.k_row;
-  pool += h * s_head + piece * (a.d / a.pieces);
   const int units = a.d / a.pieces / 8;       // 16-byte units of a row here (a power of two)
   const int rows = kMoveThreads / units;      // rows of one load of the block
-  const int u = t & (units - 1), r = t / units;
-  for (int i0 = 0; i0 < a.budget; i0 += rows * kMoveLoads) {
-    uint4 x[kMoveLoads];
-    __nv_bfloat16* dst[kMoveLoads];
-    int src[kMoveLoads];
+  pool += h * s_head + piece * (a.d / a.pieces) + 8 * (t & (units - 1));
+  const int r = t / units;
+  const int batch = rows * kMoveLoads;
+  // offsets of source and destination of this thread's row e of the batch at
+  // i0, source -1: nothing to copy; whether any key of the batch stays
+  long long src[kMoveLoads], dst[kMoveLoads];
+  auto look_up = [&](int i0) {
+    int j[kMoveLoads];
     bool more = false;
 #pragma unroll
     for (int e = 0; e < kMoveLoads; ++e) {
       const int i = i0 + e * rows + r;
-      src[e] = i < a.budget ? __ldg(kept + i) : -1;
-      more = more || src[e] >= 0;
+      j[e] = i < a.budget ? __ldcg(kept + i) : -1;
+      more = more || j[e] >= 0;
     }
 #pragma unroll
     for (int e = 0; e < kMoveLoads; ++e) {
-      dst[e] = nullptr;
-      if (src[e] < 0) continue;
+      src[e] = -1;
+      if (j[e] < 0) continue;
       const int i = i0 + e * rows + r;
-      const int pf = a.page_div(src[e]), pt = a.page_div(i);
+      const int pf = a.page_div(j[e]), pt = a.page_div(i);
       const int page_f = __ldg(from + pf), page_t = __ldg(to + pt);
       if (page_f < 0 || page_f >= a.pool.num_pages || page_t < 0 || page_t >= a.pool.num_pages) {
         report_status(a.status, kStatusBadSeqlens);
         continue;
       }
-      const int row_f = src[e] - pf * a.pool.page_size, row_t = i - pt * a.pool.page_size;
-      if (page_f == page_t && row_f == row_t) continue;  // it stays where it is
-      dst[e] = pool + page_t * s_page + row_t * s_row + 8 * u;
-      x[e] = *reinterpret_cast<const uint4*>(pool + page_f * s_page + row_f * s_row + 8 * u);
+      const long long x = page_f * s_page + (j[e] - pf * a.pool.page_size) * s_row;
+      dst[e] = page_t * s_page + (i - pt * a.pool.page_size) * s_row;
+      if (x != dst[e]) src[e] = x;  // else it stays where it is
     }
-    // the batch has been read before any of it is written (and all threads
-    // leave together, behind the last key that stays)
+    return more;
+  };
+  const int stride = a.shares * batch;
+  int i0 = share * batch;
+  if (i0 >= a.budget) return;
+  bool more = look_up(i0);
+  while (true) {
+    // the block leaves together, behind the last key that stays
     if (!__syncthreads_or(more)) break;
+    uint4 x[kMoveLoads];
+    __nv_bfloat16* out[kMoveLoads];
+#pragma unroll
+    for (int e = 0; e < kMoveLoads; ++e) {
+      out[e] = src[e] >= 0 ? pool + dst[e] : nullptr;
+      if (src[e] >= 0) x[e] = *reinterpret_cast<const uint4*>(pool + src[e]);
+    }
+    i0 += stride;
+    more = i0 < a.budget && look_up(i0);
+    __syncthreads();  // the batch has been read before any of it is written
 #pragma unroll
     for (int e = 0; e < kMoveLoads; ++e)
-      if (dst[e] != nullptr) *reinterpret_cast<uint4*>(dst[e]) = x[e];
+      if (out[e] != nullptr) *reinterpret_cast<uint4*>(out[e]) = x[e];
   }
+}
+
+template <int THREADS, bool HELD>
+cudaError_t launch_select(const EvictArgs& a, int most, cudaStream_t st) {
+  const size_t bytes = HELD ? ((size_t)most * 4 + 15) / 16 * 16 : 0;
+  if (bytes > 32 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<THREADS, HELD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+  }
+  evict_select_kernel<THREADS, HELD><<<dim3((unsigned)a.Hkv, (unsigned)a.B), THREADS, bytes, st>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-int evict_pieces(int B, int Hkv, int d, int sms) {
-  // pieces of at least 32 bytes (a sector) of a row, as many as give every SM
-  // eight blocks to run at once
-  int pieces = 1;
-  while (pieces * 32 < d * 2 && (long long)B * Hkv * 2 * pieces < 8ll * sms) pieces *= 2;
-  return pieces;
+void evict_split(int B, int Hkv, int d, int budget, bool in_place, int sms, int* pieces, int* shares) {
+  // eight blocks for each SM, of whole rows; fewer where a share would be less than a batch of rows
+  *pieces = *shares = 1;
+  const long long ctas = 2ll * B * Hkv, want = 8ll * sms;
+  if (in_place) {
+    while (*pieces * 64 < d * 2 && ctas * *pieces < want) *pieces *= 2;
+    return;
+  }
+  const int batch = kMoveThreads / (d / 8) * kMoveLoads;
+  const long long most = ((long long)budget + batch - 1) / batch;
+  long long s = (want + ctas - 1) / ctas;
+  if (s > most) s = most;
+  *shares = s < 1 ? 1 : (int)s;
 }
 
 cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t st) {
-  evict_select_kernel<<<dim3((unsigned)a.Hkv, (unsigned)a.B), kSelectThreads, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+  // threads by the longest sequence that the rows can hold: 4 to 32 weights each
+  const int most = a.most_keys < a.w_keys ? a.most_keys : a.w_keys;
+  cudaError_t e;
+  if (most <= 4096) e = launch_select<256, true>(a, most, st);
+  else if (most <= 49152) e = launch_select<1024, true>(a, most, st);
+  else e = launch_select<1024, false>(a, most, st);
   if (e != cudaSuccess) return e;
-  evict_move_kernel<<<dim3((unsigned)(2 * a.pieces), (unsigned)a.Hkv, (unsigned)a.B), kMoveThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  // the move's CTAs come while the selection ends, and wait for it
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * a.pieces * a.shares), (unsigned)a.Hkv, (unsigned)a.B);
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, evict_move_kernel, a);
 }
 
 }  // namespace fa

@@ -855,57 +855,72 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
 
 // Combines the key ranges of a block: row r gets O = sum_p w_p O_p / sum_p w_p
 // with w_p = 2^(L_p - max L), LSE = (max L + log2 sum_p w_p) ln 2. One CTA per
-// 32 rows of a block, a warp per row (lanes along d), ranges without keys (L =
-// -inf) not read.
+// 64 rows of a block, eight rows to a warp (lanes along d, their loads in flight
+// together), ranges without keys (L = -inf) not read.
 template <int D>
 __global__ void __launch_bounds__(256) prompt_merge_kernel(const __grid_constant__ PromptFwdArgs a) {
-  constexpr int PER = D / 32;
+  constexpr int PER = D / 32, ROWS = 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   PromptBlock k;
   int part;
-  if (!prompt_block(a, (long long)blockIdx.x / 8 * a.splits, lane, false, k, part)) return;
+  if (!prompt_block(a, (long long)blockIdx.x / 4 * a.splits, lane, false, k, part)) return;
   const int RT = a.tile_tokens * a.G;
-#pragma unroll 1
-  for (int i = 0; i < 4; ++i) {
-    const int br = (int)(blockIdx.x & 7) * 32 + warp * 4 + i;  // row of the block
-    const int t = br >> 7, row = br & 127;
-    const int tk = a.g_div(row), tok = k.tok0 + t * a.tile_tokens + tk;
-    if (row >= RT || tok >= k.v.n) continue;
-    const long long p0 = (long long)k.unit * a.splits * 256 + br;
-    float L = -INFINITY;
-    for (int p = lane; p < a.splits; p += 32) L = fmaxf(L, a.Lpart[p0 + 256ll * p]);
+  const int br0 = (int)(blockIdx.x & 3) * 64 + warp * ROWS;  // rows of the block, of one query tile
+  const int t = br0 >> 7, row0 = br0 & 127, tok0 = k.tok0 + t * a.tile_tokens;
+  const long long p0 = (long long)k.unit * a.splits * 256 + br0;
+  // the rows that there are begin the eight: rows of a sequence's end lack the last ones
+  const int live = min(ROWS, min(RT, (k.v.n - tok0) * a.G) - row0);
+  if (live <= 0) return;
+  float L[ROWS], acc[ROWS][PER], sum[ROWS];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L = fmaxf(L, __shfl_xor_sync(0xffffffffu, L, o));
-    float acc[PER], sum = 0.f;
+  for (int i = 0; i < ROWS; ++i) {
+    L[i] = -INFINITY;
+    sum[i] = 0.f;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-    for (int p = 0; p < a.splits; ++p) {
-      const float lp = a.Lpart[p0 + 256ll * p];
-      if (lp == -INFINITY) continue;
-      const float w = exp2f(lp - L);
-      sum += w;
-      const float* src = a.Opart + (p0 + 256ll * p) * D + lane * PER;
-      if constexpr (PER == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(src);
-        acc[0] = fmaf(w, x.x, acc[0]);
-        acc[1] = fmaf(w, x.y, acc[1]);
-        acc[2] = fmaf(w, x.z, acc[2]);
-        acc[3] = fmaf(w, x.w, acc[3]);
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(src);
-        acc[0] = fmaf(w, x.x, acc[0]);
-        acc[1] = fmaf(w, x.y, acc[1]);
+    for (int e = 0; e < PER; ++e) acc[i][e] = 0.f;
+  }
+  for (int p = 0; p < a.splits; ++p) {
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) L[i] = fmaxf(L[i], a.Lpart[p0 + 256ll * p + i]);  // rows past `live`: any value
+  }
+  for (int p = 0; p < a.splits; ++p) {
+    float lp[ROWS], x[ROWS][PER];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      lp[i] = i < live ? a.Lpart[p0 + 256ll * p + i] : -INFINITY;
+      const float* src = a.Opart + (p0 + 256ll * p + i) * D + lane * PER;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) x[i][e] = 0.f;
+      if (lp[i] != -INFINITY) {
+        if constexpr (PER == 4) {
+          const float4 y = *reinterpret_cast<const float4*>(src);
+          x[i][0] = y.x, x[i][1] = y.y, x[i][2] = y.z, x[i][3] = y.w;
+        } else {
+          const float2 y = *reinterpret_cast<const float2*>(src);
+          x[i][0] = y.x, x[i][1] = y.y;
+        }
       }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int hq = k.head * a.G + row - tk * a.G;
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.O) + (long long)(k.v.q0 + tok) * a.o_stride + (long long)hq * D + lane * PER;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const float w = lp[i] == -INFINITY ? 0.f : exp2f(lp[i] - L[i]);
+      sum[i] += w;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[i][e] = w > 0.f ? fmaf(w, x[i][e], acc[i][e]) : acc[i][e];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    if (i >= live) break;
+    const int row = row0 + i, tk = a.g_div(row), hq = k.head * a.G + row - tk * a.G;
+    const long long tok = k.v.q0 + tok0 + tk;
+    const float inv = sum[i] == 0.f ? 0.f : 1.f / sum[i];
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.O) + tok * a.o_stride + (long long)hq * D + lane * PER;
     if constexpr (PER == 4)
-      *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+      *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(acc[i][0] * inv, acc[i][1] * inv), pack_bf16x2(acc[i][2] * inv, acc[i][3] * inv));
     else
-      *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-    if (lane == 0)
-      a.LSE[(size_t)hq * a.seqs.total_q + k.v.q0 + tok] = (L + __log2f(sum)) * 0.69314718055994531f;
+      *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(acc[i][0] * inv, acc[i][1] * inv);
+    if (lane == 0) a.LSE[(size_t)hq * a.seqs.total_q + tok] = (L[i] + __log2f(sum[i])) * 0.69314718055994531f;
   }
 }
 
@@ -922,7 +937,7 @@ cudaError_t launch_d(const PromptFwdArgs& a, cudaStream_t st) {
   prompt_fwd_kernel<D, PAGED><<<(unsigned)ctas, C::NTHREADS, C::ALLOC, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.splits == 1) return e;
-  prompt_merge_kernel<D><<<(unsigned)(a.max_blocks * a.Hkv * 8), 256, 0, st>>>(a);
+  prompt_merge_kernel<D><<<(unsigned)(a.max_blocks * a.Hkv * 4), 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -45,11 +45,11 @@ struct WCfg {
   static constexpr int OFF_K = 0;          // [2 units][2 tiles]
   static constexpr int OFF_Q = OFF_K + 4 * TILE;
   static constexpr int OFF_STAT = OFF_Q + QS * TILE;  // [QS][128] -LSE * log2(e)
-  static constexpr int IRING = 2, ITEM_INTS = 12;
+  static constexpr int IRING = 3, ITEM_INTS = 12;  // units published ahead (short ones: many)
   static constexpr int OFF_PART = OFF_STAT + QS * 512;  // [2 tiles][128] sums of the second column halves
   static constexpr int OFF_BARS = OFF_PART + 2 * 512;
   // k_full[2], k_empty[2], q_full[QS], q_empty[QS], st_full[QS], st_empty[QS], s_full[2][2], s_free[2][2],
-  // part_full[2], part_free[2], item_full[2], item_empty[2], cancel, near, drain
+  // part_full[2], part_free[2], item_full, item_empty [IRING each], cancel, near, drain
   static constexpr int NBARS = 4 + 4 * QS + 12 + 2 * IRING + 3;
   static constexpr int OFF_ITEMS = (OFF_BARS + NBARS * 8 + 15) / 16 * 16;
   static constexpr int OFF_CANCEL = OFF_ITEMS + IRING * ITEM_INTS * 4;
