@@ -33,12 +33,15 @@ namespace {
 constexpr int kBins = 2048;
 constexpr int kPerThread = 4;  // neighbouring weights of a thread in the listing pass
 
-// Weights as unsigned numbers in the same order: NaN above all, -0 equal to 0.
+// Weights as unsigned numbers in the same order (NaN above all, -0 equal to 0),
+// and back.
 __device__ __forceinline__ unsigned order_of(float w) {
   if (w != w) return 0xffffffffu;
   const unsigned x = __float_as_uint(w + 0.f);
   return x & 0x80000000u ? ~x : x | 0x80000000u;
 }
+
+__device__ __forceinline__ float weight_of(unsigned u) { return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u); }
 
 // Exclusive sum over the block's threads of `x`, and the total. `part`: 32 ints.
 template <int THREADS>
@@ -70,12 +73,12 @@ __device__ __forceinline__ int block_scan(int value, int* part, int& total) {
 // bins then fall on banks of their own.
 __device__ __forceinline__ int bin_at(int i) { return i + (i >> 5); }
 
-// HELD: the weights are copied to (dynamic) shared memory first and read there;
-// else from memory in each pass.
+// HELD: the weights' orders are put into (dynamic) shared memory first and read
+// there; else they are found from memory in each pass.
 template <int THREADS, bool HELD>
 __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_constant__ EvictArgs a) {
   constexpr int BPT = kBins / THREADS;  // bins of a thread
-  extern __shared__ __align__(16) float held[];
+  extern __shared__ __align__(16) unsigned held[];
   __shared__ int hist[kBins + kBins / 32];
   __shared__ int part[32];
   __shared__ int found_bin, found_above;
@@ -97,11 +100,14 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_cons
   if constexpr (HELD) {
     const int whole = (reinterpret_cast<uintptr_t>(w) & 15) == 0 ? len / 4 : 0;
 #pragma unroll 4
-    for (int j = t; j < whole; j += THREADS) reinterpret_cast<float4*>(held)[j] = reinterpret_cast<const float4*>(w)[j];
-    for (int j = 4 * whole + t; j < len; j += THREADS) held[j] = w[j];
+    for (int j = t; j < whole; j += THREADS) {
+      const float4 y = reinterpret_cast<const float4*>(w)[j];
+      reinterpret_cast<uint4*>(held)[j] = make_uint4(order_of(y.x), order_of(y.y), order_of(y.z), order_of(y.w));
+    }
+    for (int j = 4 * whole + t; j < len; j += THREADS) held[j] = order_of(w[j]);
   }
   __syncthreads();
-  auto weight = [&](int j) { return HELD ? held[j] : w[j]; };
+  auto order = [&](int j) { return HELD ? held[j] : order_of(w[j]); };
 
   unsigned least = 0;   // order of the last weight that stays
   int ties = 0;         // how many of that order stay
@@ -114,7 +120,7 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_cons
       const unsigned digits = pass == 2 ? 1023u : 2047u;
 #pragma unroll 4
       for (int j = t; j < old; j += THREADS) {
-        const unsigned u = order_of(weight(j));
+        const unsigned u = order(j);
         if ((u & mask) == prefix) atomicAdd(&hist[bin_at((u >> shift) & digits)], 1);
       }
       __syncthreads();
@@ -149,52 +155,99 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_cons
   // The list, in order. Before key j stay the larger weights before it and at
   // most `ties` of those equal to the last.
   const bool all = need >= old;
-  int larger = 0, equal = 0;  // before this chunk
-  if (need > 0) {
-#pragma unroll 1
-    for (int j0 = 0; j0 < old; j0 += THREADS * kPerThread) {
-      const int j = j0 + t * kPerThread;
-      float y[kPerThread];
-      unsigned gt = 0, eq = 0;
-#pragma unroll
-      for (int e = 0; e < kPerThread; ++e) {
-        y[e] = 0.f;
-        if (j + e < old) {
-          y[e] = weight(j + e);
-          const unsigned u = order_of(y[e]);
-          if (all || u > least) gt |= 1u << e;
-          else if (u == least) eq |= 1u << e;
-        }
-      }
-      // larger ones in the low half, equal ones in the high half
-      int total;
-      const int before = block_scan<THREADS>(__popc(gt) | __popc(eq) << 16, part, total);  // also: the chunk is read before it is written
-      int ng = larger + (before & 0xffff), ne = equal + (before >> 16);
-#pragma unroll
-      for (int e = 0; e < kPerThread; ++e) {
-        const bool is_eq = eq >> e & 1u;
-        if ((gt >> e & 1u) || (is_eq && ne < ties)) {
-          const int pos = ng + min(ne, ties);
-          kept[pos] = j + e;
-          out_w[pos] = y[e];
-        }
-        ng += gt >> e & 1u;
-        ne += is_eq;
-      }
-      larger += total & 0xffff;
-      equal += total >> 16;
+  if constexpr (HELD) {
+    // A run of keys to each warp: counted, then listed 32 at a time behind what
+    // the warps before it list.
+    __shared__ int before_gt[32], before_eq[32];
+    constexpr int WARPS = THREADS / 32;
+    const int warp = t >> 5, lane = t & 31;
+    const int run = ((old + WARPS - 1) / WARPS + 31) & ~31;
+    const int first = warp * run, last = need > 0 ? min(old, first + run) : 0;
+    int ng = 0, ne = 0;
+#pragma unroll 4
+    for (int j = first + lane; j < last; j += 32) {
+      const unsigned u = held[j];
+      ng += all || u > least;
+      ne += !all && u == least;
     }
-  }
-  // the newest ones (in place, and not held: their weights may lie where the
-  // list's last ones went only if they are read a batch ahead)
-#pragma unroll 1
-  for (int j0 = 0; j0 < recent; j0 += THREADS) {
-    const int j = j0 + t;
-    const float y = j < recent ? weight(old + j) : 0.f;
+    ng = __reduce_add_sync(0xffffffffu, ng);
+    ne = __reduce_add_sync(0xffffffffu, ne);
+    if (lane == 0) {
+      before_gt[warp] = ng;
+      before_eq[warp] = ne;
+    }
     __syncthreads();
-    if (j < recent) {
+    ng = __reduce_add_sync(0xffffffffu, lane < warp ? before_gt[lane] : 0);
+    ne = __reduce_add_sync(0xffffffffu, lane < warp ? before_eq[lane] : 0);
+    const unsigned below = (1u << lane) - 1u;
+#pragma unroll 2
+    for (int j0 = first; j0 < last; j0 += 32) {
+      const int j = j0 + lane;
+      const unsigned u = j < last ? held[j] : 0u;
+      const bool gt = j < last && (all || u > least), eq = j < last && !all && u == least;
+      const unsigned vg = __ballot_sync(0xffffffffu, gt), ve = __ballot_sync(0xffffffffu, eq);
+      if ((vg | ve) == 0u) continue;
+      const int eq_before = ne + __popc(ve & below);
+      if (gt || (eq && eq_before < ties)) {
+        const int pos = ng + __popc(vg & below) + min(eq_before, ties);
+        kept[pos] = j;
+        out_w[pos] = weight_of(u);
+      }
+      ng += __popc(vg);
+      ne += __popc(ve);
+    }
+    for (int j = t; j < recent; j += THREADS) {  // the newest ones
       kept[need + j] = old + j;
-      out_w[need + j] = y;
+      out_w[need + j] = weight_of(held[old + j]);
+    }
+  } else {
+    int larger = 0, equal = 0;  // before this chunk
+    if (need > 0) {
+#pragma unroll 1
+      for (int j0 = 0; j0 < old; j0 += THREADS * kPerThread) {
+        const int j = j0 + t * kPerThread;
+        float y[kPerThread];
+        unsigned gt = 0, eq = 0;
+#pragma unroll
+        for (int e = 0; e < kPerThread; ++e) {
+          y[e] = 0.f;
+          if (j + e < old) {
+            y[e] = w[j + e];
+            const unsigned u = order_of(y[e]);
+            if (all || u > least) gt |= 1u << e;
+            else if (u == least) eq |= 1u << e;
+          }
+        }
+        // larger ones in the low half, equal ones in the high half
+        int total;
+        const int before = block_scan<THREADS>(__popc(gt) | __popc(eq) << 16, part, total);  // also: the chunk is read before it is written
+        int ng = larger + (before & 0xffff), ne = equal + (before >> 16);
+#pragma unroll
+        for (int e = 0; e < kPerThread; ++e) {
+          const bool is_eq = eq >> e & 1u;
+          if ((gt >> e & 1u) || (is_eq && ne < ties)) {
+            const int pos = ng + min(ne, ties);
+            kept[pos] = j + e;
+            out_w[pos] = y[e];
+          }
+          ng += gt >> e & 1u;
+          ne += is_eq;
+        }
+        larger += total & 0xffff;
+        equal += total >> 16;
+      }
+    }
+    // the newest ones
+#pragma unroll 1
+    for (int j0 = 0; j0 < recent; j0 += THREADS) {
+      const int j = j0 + t;
+      __syncthreads();  // what the batch before wrote lies before what this one reads
+      const float y = j < recent ? w[old + j] : 0.f;
+      __syncthreads();
+      if (j < recent) {
+        kept[need + j] = old + j;
+        out_w[need + j] = y;
+      }
     }
   }
 }
