@@ -744,10 +744,25 @@ def _prompt_outputs(q, out, lse, total: int, hq: int, d: int, dev: int):
     return out, stride, lse
 
 
-def _scratch(workspace, need, device, dev: int):
-    """(pointer, bytes, tensor) of the caller's scratch, or of a new one of need() bytes (None for 0)."""
+_prompt_ws_bytes: dict = {}  # (entry point, device, sizes) -> bytes: what the library answered
+
+
+def _prompt_workspace_size(key) -> int:
+    fn, dev, *sizes = key
+    with torch.cuda.device(dev):
+        n = int(getattr(load_library(), fn)(*sizes, FA_BF16))
+    if len(_prompt_ws_bytes) >= 4096:
+        _prompt_ws_bytes.clear()
+    _prompt_ws_bytes[key] = n
+    return n
+
+
+def _scratch(workspace, key, device, dev: int):
+    """(pointer, bytes, tensor) of the caller's scratch, or of a new one of as many bytes as ``key`` asks for (None for 0)."""
     if workspace is None:
-        n = need()
+        n = _prompt_ws_bytes.get(key)
+        if n is None:
+            n = _prompt_workspace_size(key)
         if n == 0:
             return None, 0, None
         workspace = torch.empty(n, dtype=torch.uint8, device=device)
@@ -806,14 +821,13 @@ def fa_prompt_fwd(q, k, v, cu_seqlens_q, max_seqlen_q: int, cu_seqlens_k=None, m
     if total_k == 0:  # no sequence has a key; a tensor map wants one row
         k = v = torch.zeros((1, hkv, d), dtype=_BF16, device=q.device)
         total_k = mk = 1
-    lib = load_library()
-    with torch.cuda.device(dev):
-        ws, n, workspace = _scratch(
-            workspace, lambda: lib.fa_prompt_fwd_workspace_bytes(B, hq, hkv, total, mq, mk, d, FA_BF16), q.device, dev)
-        rc = lib.fa_prompt_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, out.data_ptr(), os_, lse.data_ptr(),
-                               cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, hq, hkv, total, total_k, mq, mk, ws,
-                               n, d, scale, FA_BF16, _raw_stream(dev))
-    _raise(rc, "fa_prompt_fwd")
+    ws, n, workspace = _scratch(workspace, ("fa_prompt_fwd_workspace_bytes", dev, B, hq, hkv, total, mq, mk, d), q.device,
+                                dev)
+    rc = _on_device(dev, load_library().fa_prompt_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, out.data_ptr(),
+                    os_, lse.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, hq, hkv, total, total_k, mq,
+                    mk, ws, n, d, scale, FA_BF16)
+    if rc != FA_OK:
+        _raise(rc, "fa_prompt_fwd")
     return out, lse
 
 
@@ -856,15 +870,13 @@ def fa_prompt_bwd(q, k, v, o, do, lse, cu_seqlens_q, max_seqlen_q: int, cu_seqle
         k = v = torch.zeros((1, hkv, d), dtype=_BF16, device=q.device)
         dk = dv = torch.empty_like(k)
         total_k = mk = 1
-    lib = load_library()
-    with torch.cuda.device(dev):
-        ws, n, workspace = _scratch(
-            workspace, lambda: lib.fa_prompt_bwd_workspace_bytes(B, hq, hkv, total, d, FA_BF16), q.device, dev)
-        rc = lib.fa_prompt_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), qs, ks, vs, os_, dos,
-                               lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *strides,
-                               cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), ws, n, B, hq, hkv, total, total_k, mq,
-                               mk, d, scale, FA_BF16, _raw_stream(dev))
-    _raise(rc, "fa_prompt_bwd")
+    ws, n, workspace = _scratch(workspace, ("fa_prompt_bwd_workspace_bytes", dev, B, hq, hkv, total, d), q.device, dev)
+    rc = _on_device(dev, load_library().fa_prompt_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
+                    qs, ks, vs, os_, dos, lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *strides,
+                    cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), ws, n, B, hq, hkv, total, total_k, mq, mk, d, scale,
+                    FA_BF16)
+    if rc != FA_OK:
+        _raise(rc, "fa_prompt_bwd")
     return tuple(outs)
 
 
@@ -884,15 +896,14 @@ def fa_prompt_paged(q, k_pages, v_pages, block_tables, seq_lens, cu_seqlens_q, m
     out, os_, lse = _prompt_outputs(q, out, lse, total, hq, d, dev)
     if total == 0:
         return out, lse
-    lib = load_library()
     most = min(max_pages * page, 1 << 30)
-    with torch.cuda.device(dev):
-        ws, n, workspace = _scratch(
-            workspace, lambda: lib.fa_prompt_fwd_workspace_bytes(B, hq, hkv, total, mq, most, d, FA_BF16), q.device, dev)
-        rc = lib.fa_prompt_paged(q.data_ptr(), qs, pool, block_tables.data_ptr(), max_pages, seq_lens.data_ptr(),
-                                 out.data_ptr(), os_, lse.data_ptr(), cu_seqlens_q.data_ptr(), B, hq, total, mq, ws, n,
-                                 scale, FA_BF16, _raw_stream(dev))
-    _raise(rc, "fa_prompt_paged")
+    ws, n, workspace = _scratch(workspace, ("fa_prompt_fwd_workspace_bytes", dev, B, hq, hkv, total, mq, most, d), q.device,
+                                dev)
+    rc = _on_device(dev, load_library().fa_prompt_paged, q.data_ptr(), qs, pool, block_tables.data_ptr(), max_pages,
+                    seq_lens.data_ptr(), out.data_ptr(), os_, lse.data_ptr(), cu_seqlens_q.data_ptr(), B, hq, total, mq, ws,
+                    n, scale, FA_BF16)
+    if rc != FA_OK:
+        _raise(rc, "fa_prompt_paged")
     return out, lse
 
 
@@ -1018,7 +1029,8 @@ def fa_kv_evict(k_pages, v_pages, block_tables, seq_lens, weights, budget: int, 
     rc = _on_device(dev, load_library().fa_kv_evict, pool, block_tables.data_ptr(), max_pages, seq_lens.data_ptr(),
                     new_tables.data_ptr(), new_tables.shape[1], new_lens.data_ptr(), weights.data_ptr(), wb, wh, wk,
                     new_weights.data_ptr(), nb, nh, kept.data_ptr(), B, budget, recent, FA_BF16)
-    _raise(rc, "fa_kv_evict")
+    if rc != FA_OK:
+        _raise(rc, "fa_kv_evict")
     return new_lens, kept
 
 

@@ -1738,7 +1738,8 @@ cudaError_t launch_prompt_d(const PromptBwdArgs& a, cudaStream_t st) {
   prompt_bwd_pre_kernel<D><<<dim3((unsigned)(a.slots + 1 + kPromptZeroBlocks), (unsigned)a.Hkv), 256, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(bwd_main_kernel<D, true, PromptBwdArgs>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
+  static std::atomic<unsigned char> asked[kMaxSharedMemoryDevices];
+  e = ask_shared_memory(reinterpret_cast<const void*>(bwd_main_kernel<D, true, PromptBwdArgs>), C::SMEM_ALLOC, asked);
   if (e != cudaSuccess) return e;
   const int sms = fwd_slots();
   bwd_main_kernel<D, true, PromptBwdArgs>

@@ -4,6 +4,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -260,6 +261,20 @@ bool encode_part_f32(CUtensorMap* m, void* ptr, long long rows, int d);
 // boxes of 64 columns x box_rows rows of one page, 128-byte swizzle.
 bool encode_pool_bf16(CUtensorMap* m, const PagedPool& pool, bool values, int d, int box_rows);
 
+constexpr int kMaxSharedMemoryDevices = 16;
+// Asks once per device for a kernel's dynamic shared memory (a call of 1 us);
+// `done` is the kernel's own: one byte per device, zero at first.
+inline cudaError_t ask_shared_memory(const void* kernel, int bytes, std::atomic<unsigned char>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < kMaxSharedMemoryDevices;
+  if (known && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && known) done[dev].store(1, std::memory_order_release);
+  return e;
+}
+
 // ---- causal attention of packed prompts with grouped heads (prompt_*.cu) ----
 // B sequences; sequence b has the packed query tokens cu_q[b] .. cu_q[b + 1] - 1
 // and the keys cu_k[b] .. cu_k[b + 1] - 1 (packed) or the first seq_lens[b] keys
@@ -382,6 +397,7 @@ struct EvictArgs {
   int* kept;                 // [B, Hkv, budget]
   int B, Hkv, d, max_pages, new_pages, w_keys, most_keys, budget, recent;
   int pieces, shares;        // of the move: column pieces of a row, shares of the rows
+  int held_words;            // of the selection: words of shared memory before its list
   FastDiv page_div;
   int* status;
 };

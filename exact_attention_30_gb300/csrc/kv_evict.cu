@@ -8,8 +8,8 @@
 //    key that stays by a radix selection over 11, 11 and 10 bits of the weights'
 //    order (a histogram in shared memory, its suffix sums, the digit that holds
 //    the rank), then one pass over the weights in order that counts and lists.
-//    Up to 49152 weights are held in shared memory, read once. Bound by latency
-//    (some 20 barriers) and the histogram's atomics.
+//    What fits is held in shared memory, weights and list, and read and written
+//    once. Bound by latency (some 20 barriers) and the histogram's atomics.
 // 2. evict_move_kernel copies the rows. Bound by memory: each row that stays is
 //    read and written once; in place, rows that do not move are left alone. In
 //    place a row may only be written when the row it held has been read: since
@@ -31,6 +31,7 @@ namespace fa {
 namespace {
 
 constexpr int kBins = 2048;
+constexpr size_t kSelectMostBytes = 208 * 1024;  // of weights and list (counts in 16 bits: at most 53248 keys)
 constexpr int kPerThread = 4;  // neighbouring weights of a thread in the listing pass
 
 // Weights as unsigned numbers in the same order (NaN above all, -0 equal to 0),
@@ -107,7 +108,6 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_cons
     for (int j = 4 * whole + t; j < len; j += THREADS) held[j] = order_of(w[j]);
   }
   __syncthreads();
-  auto order = [&](int j) { return HELD ? held[j] : order_of(w[j]); };
 
   unsigned least = 0;   // order of the last weight that stays
   int ties = 0;         // how many of that order stay
@@ -118,10 +118,21 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_cons
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const unsigned digits = pass == 2 ? 1023u : 2047u;
-#pragma unroll 4
-      for (int j = t; j < old; j += THREADS) {
-        const unsigned u = order(j);
+      auto count_one = [&](unsigned u) {
         if ((u & mask) == prefix) atomicAdd(&hist[bin_at((u >> shift) & digits)], 1);
+      };
+      if constexpr (HELD) {
+#pragma unroll 2
+        for (int j = 4 * t; j < old; j += 4 * THREADS) {
+          const uint4 u = *reinterpret_cast<const uint4*>(held + j);
+          count_one(u.x);
+          if (j + 1 < old) count_one(u.y);
+          if (j + 2 < old) count_one(u.z);
+          if (j + 3 < old) count_one(u.w);
+        }
+      } else {
+#pragma unroll 4
+        for (int j = t; j < old; j += THREADS) count_one(order_of(w[j]));
       }
       __syncthreads();
       // bins from the top: thread t has the BPT bins below kBins - t BPT, and
@@ -156,49 +167,66 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_cons
   // most `ties` of those equal to the last.
   const bool all = need >= old;
   if constexpr (HELD) {
-    // A run of keys to each warp: counted, then listed 32 at a time behind what
-    // the warps before it list.
-    __shared__ int before_gt[32], before_eq[32];
+    // A run of keys to each warp: counted, then listed 128 at a time, four to a
+    // lane, behind what the warps before it list. Larger ones are counted in the
+    // low half of a word, equal ones in the high half.
+    __shared__ unsigned counts[32];
     constexpr int WARPS = THREADS / 32;
     const int warp = t >> 5, lane = t & 31;
-    const int run = ((old + WARPS - 1) / WARPS + 31) & ~31;
+    int* list = reinterpret_cast<int*>(held + a.held_words);
+    const int run = ((old + WARPS - 1) / WARPS + 127) & ~127;
     const int first = warp * run, last = need > 0 ? min(old, first + run) : 0;
-    int ng = 0, ne = 0;
-#pragma unroll 4
-    for (int j = first + lane; j < last; j += 32) {
-      const unsigned u = held[j];
-      ng += all || u > least;
-      ne += !all && u == least;
-    }
-    ng = __reduce_add_sync(0xffffffffu, ng);
-    ne = __reduce_add_sync(0xffffffffu, ne);
-    if (lane == 0) {
-      before_gt[warp] = ng;
-      before_eq[warp] = ne;
-    }
-    __syncthreads();
-    ng = __reduce_add_sync(0xffffffffu, lane < warp ? before_gt[lane] : 0);
-    ne = __reduce_add_sync(0xffffffffu, lane < warp ? before_eq[lane] : 0);
-    const unsigned below = (1u << lane) - 1u;
-#pragma unroll 2
-    for (int j0 = first; j0 < last; j0 += 32) {
-      const int j = j0 + lane;
-      const unsigned u = j < last ? held[j] : 0u;
-      const bool gt = j < last && (all || u > least), eq = j < last && !all && u == least;
-      const unsigned vg = __ballot_sync(0xffffffffu, gt), ve = __ballot_sync(0xffffffffu, eq);
-      if ((vg | ve) == 0u) continue;
-      const int eq_before = ne + __popc(ve & below);
-      if (gt || (eq && eq_before < ties)) {
-        const int pos = ng + __popc(vg & below) + min(eq_before, ties);
-        kept[pos] = j;
-        out_w[pos] = weight_of(u);
+    // bits 0-3: which of the four keys from j on are larger, bits 16-19: equal
+    auto classes = [&](int j, const uint4& u) {
+      unsigned c = 0;
+      const unsigned k[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (j + e < last && (all || k[e] > least)) c |= 1u << e;
+        if (j + e < last && !all && k[e] == least) c |= 0x10000u << e;
       }
-      ng += __popc(vg);
-      ne += __popc(ve);
+      return c;
+    };
+    auto count_of = [](unsigned c) { return (unsigned)__popc(c & 15u) | (unsigned)__popc(c >> 16) << 16; };
+    unsigned n = 0;
+#pragma unroll 2
+    for (int j = first + 4 * lane; j < last; j += 128) n += count_of(classes(j, *reinterpret_cast<const uint4*>(held + j)));
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) counts[warp] = n;
+    __syncthreads();
+    n = __reduce_add_sync(0xffffffffu, lane < warp ? counts[lane] : 0u);
+#pragma unroll 1
+    for (int j0 = first; j0 < last; j0 += 128) {
+      const int j = j0 + 4 * lane;
+      uint4 u = make_uint4(0u, 0u, 0u, 0u);
+      if (j < last) u = *reinterpret_cast<const uint4*>(held + j);
+      const unsigned c = classes(j, u), mine = count_of(c);
+      unsigned sum = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+      }
+      const unsigned here = n + sum - mine;
+      int ng = (int)(here & 0xffffu), ne = (int)(here >> 16);
+      if (c != 0u) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool eq = c >> (16 + e) & 1u;
+          if ((c >> e & 1u) || (eq && ne < ties)) list[ng + min(ne, ties)] = j + e;
+          ng += c >> e & 1u;
+          ne += eq;
+        }
+      }
+      n += __shfl_sync(0xffffffffu, sum, 31);
     }
-    for (int j = t; j < recent; j += THREADS) {  // the newest ones
-      kept[need + j] = old + j;
-      out_w[need + j] = weight_of(held[old + j]);
+    // and out in order, the newest ones behind (stored as they were found, a few
+    // lanes of a warp at a time, the lists of 2048 out of 30000 took 6 us)
+    __syncthreads();
+    for (int i = t; i < count; i += THREADS) {
+      const int j = i < need ? list[i] : old + i - need;
+      kept[i] = j;
+      out_w[i] = weight_of(held[j]);
     }
   } else {
     int larger = 0, equal = 0;  // before this chunk
@@ -332,8 +360,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __gri
 }
 
 template <int THREADS, bool HELD>
-cudaError_t launch_select(const EvictArgs& a, int most, cudaStream_t st) {
-  const size_t bytes = HELD ? ((size_t)most * 4 + 15) / 16 * 16 : 0;
+cudaError_t launch_select(const EvictArgs& a, size_t bytes, cudaStream_t st) {
   if (bytes > 32 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<THREADS, HELD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
@@ -359,13 +386,16 @@ void evict_split(int B, int Hkv, int d, int budget, bool in_place, int sms, int*
   *shares = s < 1 ? 1 : (int)s;
 }
 
-cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t st) {
-  // threads by the longest sequence that the rows can hold: 4 to 32 weights each
+cudaError_t launch_kv_evict(const EvictArgs& args, cudaStream_t st) {
+  // threads by the longest sequence that the rows can hold: up to 32 weights each
+  EvictArgs a = args;
   const int most = a.most_keys < a.w_keys ? a.most_keys : a.w_keys;
+  a.held_words = (most + 3) / 4 * 4;
+  const size_t bytes = ((size_t)a.held_words + (most < a.budget ? most : a.budget)) * 4;
   cudaError_t e;
-  if (most <= 4096) e = launch_select<256, true>(a, most, st);
-  else if (most <= 49152) e = launch_select<1024, true>(a, most, st);
-  else e = launch_select<1024, false>(a, most, st);
+  if (bytes > kSelectMostBytes) e = launch_select<1024, false>(a, 0, st);
+  else if (most <= 4096) e = launch_select<256, true>(a, bytes, st);
+  else e = launch_select<1024, true>(a, bytes, st);
   if (e != cudaSuccess) return e;
   // the move's CTAs come while the selection ends, and wait for it
   cudaLaunchAttribute attr;

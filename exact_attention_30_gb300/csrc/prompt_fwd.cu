@@ -931,8 +931,8 @@ cudaError_t launch_d(const PromptFwdArgs& a, cudaStream_t st) {
   const long long ctas = a.max_blocks * a.Hkv * a.splits;
   if (a.splits < 1 || a.max_blocks < 1 || ctas > 0x7fffffffll || (a.splits > 1 && (!a.Opart || !a.Lpart)))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(prompt_fwd_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       C::ALLOC);
+  static std::atomic<unsigned char> asked[kMaxSharedMemoryDevices];
+  cudaError_t e = ask_shared_memory(reinterpret_cast<const void*>(prompt_fwd_kernel<D, PAGED>), C::ALLOC, asked);
   if (e != cudaSuccess) return e;
   prompt_fwd_kernel<D, PAGED><<<(unsigned)ctas, C::NTHREADS, C::ALLOC, st>>>(a);
   e = cudaGetLastError();

@@ -497,7 +497,8 @@ cudaError_t launch_d(const PromptWeightArgs& a, cudaStream_t st) {
   static_assert(C::BYTES <= C::MOST, "shared memory budget");
   const long long ctas = a.max_units * a.Hkv;
   if (a.max_units < 1 || ctas > 0x7fffffffll) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(prompt_weights_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ALLOC);
+  static std::atomic<unsigned char> asked[kMaxSharedMemoryDevices];
+  cudaError_t e = ask_shared_memory(reinterpret_cast<const void*>(prompt_weights_kernel<D, PAGED>), C::ALLOC, asked);
   if (e != cudaSuccess) return e;
   prompt_weights_kernel<D, PAGED><<<(unsigned)ctas, C::THREADS, C::ALLOC, st>>>(a);
   return cudaGetLastError();
