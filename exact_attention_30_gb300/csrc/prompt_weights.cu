@@ -7,8 +7,11 @@
 // and nothing else: P is summed where it is computed.
 //
 // Keys are the rows of the products (S^T = K Q^T, a TMEM lane per key), so that
-// a thread adds up its own key's weights over the query tiles and no thread
-// needs another's. A unit is 256 keys (two tiles) of a sequence and K/V head,
+// a thread adds up its own keys' weights over the query tiles: four keys over a
+// quarter of the columns, the four threads of a key joined at the end. (With a
+// key to a thread each needs the statistics of all columns: broadcasts of 16
+// bytes took 3.5 cycles of shared memory each, 900 of a tile's 2280, beside the
+// products' operands: 8 prompts of 361 to 6925 tokens 521 us.) A unit is 256 keys (two tiles) of a sequence and K/V head,
 // which stay in shared memory while the query tiles (128 rows: all heads of the
 // group, prompt_fwd.cu) that see them stream through a ring; the next unit's
 // keys load meanwhile. Two tiles of keys per query tile, because one product of
@@ -17,8 +20,9 @@
 // Bound by the products and the exponentials alike: 1024 cycles a unit and query
 // tile each (8192 FLOP and 32 exponentials per cycle and SM).
 //
-// Sums: 64 weights of a query tile in eight fp32 accumulators, the tiles' sums
-// with a compensation term (Kahan's), in a fixed order.
+// Sums: 16 weights of a query tile and key to a thread, 64 of eight tiles in each
+// of two fp32 accumulators, and their sums with a compensation term (Kahan's), in
+// a fixed order.
 //
 // Warps 0: producer, 1: MMA issuer, 2: scheduler, 3: statistics, 4-19: weights,
 // four warps to the first and to the second 64 queries of each key tile (with
@@ -347,38 +351,55 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
     // ---------------------------------------------------------- statistics
     // -LSE * log2(e) of a query tile's rows, lane l: rows 4 l .. 4 l + 3; -inf
     // (weight zero) for rows past the sequence, and where the row saw no key
-    int g0 = 0;
+    // One warp does this for all: few instructions a tile (a division for each
+    // row and tile made it the kernel's bound), loads three tiles ahead.
+    int tk[4];             // token of the row within its tile; past every tile: no such row
+    long long at[4];       // offset of its statistic from that of the group's first head and the tile's first token
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = 4 * lane + e, x = a.g_div(r);
+      tk[e] = r < RT ? x : 0x7fffffff;
+      at[e] = (long long)(r - x * a.G) * a.seqs.total_q + x;
+    }
+    uint32_t slot = 0, slot_phase = 1;
     for (int i = 0; ok; ++i) {
       if (!get_item(i)) { ok = false; break; }
       const int tiles = item(i, kWTiles);
       if (tiles < 0) break;
-      const int tok = item(i, kWTok), tokens = item(i, kWTokens), hq0 = item(i, kWHead) * a.G;
-      auto row_stat = [&](int j, int r) {
-        const int tk = a.g_div(r), t = j * TP + tk;
-        if (r >= RT || t >= tokens) return -INFINITY;
-        const float x = __ldg(a.LSE + (size_t)(hq0 + r - tk * a.G) * a.seqs.total_q + tok + t);
-        return x == -INFINITY ? x : -x * 1.4426950408889634f;
+      const int tokens = item(i, kWTokens);
+      const float* base = a.LSE + (long long)item(i, kWHead) * a.G * a.seqs.total_q + item(i, kWTok);
+      float ahead[3][4];
+      auto fetch = [&](int j, float (&x)[4]) {
+        const int left = tokens - j * TP;  // not positive past the last tile: nothing is read
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = tk[e] < left ? __ldg(base + (long long)j * TP + at[e]) : -INFINITY;
       };
-      auto tile_stat = [&](int j) {
-        return j < tiles ? make_float4(row_stat(j, 4 * lane), row_stat(j, 4 * lane + 1), row_stat(j, 4 * lane + 2),
-                                       row_stat(j, 4 * lane + 3))
-                         : make_float4(0.f, 0.f, 0.f, 0.f);
-      };
-      float4 ahead[3] = {tile_stat(0), tile_stat(1), tile_stat(2)};  // loads of three tiles in flight
+      fetch(0, ahead[0]);
+      fetch(1, ahead[1]);
+      fetch(2, ahead[2]);
+#pragma unroll 1
       for (int j = 0; j < tiles; ++j) {
-        if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
-        const int g = g0 + j, s = g % C::QS;
-        const float4 x = ahead[0];
-        ahead[0] = ahead[1];
-        ahead[1] = ahead[2];
-        ahead[2] = tile_stat(j + 3);
-        if (g >= C::QS && !wait(B_STEMPTY + s, ((g / C::QS) - 1) & 1)) { ok = false; break; }
-        reinterpret_cast<float4*>(smem + C::OFF_STAT + s * 512)[lane] = x;
+        float4 x;
+        x.x = ahead[0][0] == -INFINITY ? -INFINITY : -ahead[0][0] * 1.4426950408889634f;
+        x.y = ahead[0][1] == -INFINITY ? -INFINITY : -ahead[0][1] * 1.4426950408889634f;
+        x.z = ahead[0][2] == -INFINITY ? -INFINITY : -ahead[0][2] * 1.4426950408889634f;
+        x.w = ahead[0][3] == -INFINITY ? -INFINITY : -ahead[0][3] * 1.4426950408889634f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          ahead[0][e] = ahead[1][e];
+          ahead[1][e] = ahead[2][e];
+        }
+        fetch(j + 3, ahead[2]);
+        if (!wait(B_STEMPTY + slot, slot_phase)) { ok = false; break; }
+        reinterpret_cast<float4*>(smem + C::OFF_STAT + slot * 512)[lane] = x;
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(B_STFULL + s));
+        if (lane == 0) mbar_arrive(BAR(B_STFULL) + 8 * slot);
+        if (++slot == C::QS) {
+          slot = 0;
+          slot_phase ^= 1u;
+        }
       }
       if (!ok) break;
-      g0 += tiles;
       release_item(i);
     }
   } else {
@@ -387,34 +408,48 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
     const int row = wq * 32 + lane;                                       // key of the tile
     const uint32_t lane_addr = tmem + ((uint32_t)(wq * 32) << 16) + C::S_COL(t, 0) + 64u * half;
     const uint64_t c22 = f2_pack(a.scale_log2, a.scale_log2);
-    int g0 = 0, c = 0;
+    // The loop over query tiles is bound by the instructions it issues: 140 for
+    // 64 columns of 32 keys, and what comes on top (317 in all once, 521 us for 8
+    // prompts of 361 to 6925 tokens). So ring positions are counted, not divided
+    // out, masks are rare, and sums are joined only every eighth tile.
+    uint32_t slot = 0, slot_phase = 0;  // ring position of the next query tile
+    int c = 0;                          // S tiles of this key tile so far
+    const uint32_t bar_stat = BAR(B_STFULL), bar_s = BAR(B_SFULL + 2 * t);
     for (int i = 0; ok; ++i) {
       if (!get_item(i)) { ok = false; break; }
       const int tiles = item(i, kWTiles);
       if (tiles < 0) break;
       const int skip = t == 0 ? 0 : item(i, kWSkip1);
-      const int diag0 = item(i, kWDiag) + 128 * t;  // the token (from the first tile's on) whose diagonal is the tile's first key
-      const int tokens = item(i, kWTokens);
-      float total = 0.f, lost = 0.f;
+      // the token (from the unit's first tile's on) whose diagonal is the key tile's first key
+      int first = item(i, kWDiag) + 128 * t;
+      int tokens = item(i, kWTokens);  // from the next query tile on
+      // of the rows l / 4 + 8 e of the warp's quarter, over this thread's columns
+      uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+      float total[4] = {0.f, 0.f, 0.f, 0.f}, lost[4] = {0.f, 0.f, 0.f, 0.f};
+      auto join = [&]() {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 sa = f2_unpack(sum[e]);
+          sum[e] = 0ull;
+          const float y = __fsub_rn(__fadd_rn(sa.x, sa.y), lost[e]), z = __fadd_rn(total[e], y);
+          lost[e] = __fsub_rn(__fsub_rn(z, total[e]), y);
+          total[e] = z;
+        }
+      };
+#pragma unroll 1
       for (int j = 0; j < tiles; ++j) {
-        if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
-        const int g = g0 + j, s = g % C::QS;
-        if (!wait(B_STFULL + s, (g / C::QS) & 1)) { ok = false; break; }
+        if (!wait_warp(bar_stat + 8 * slot, slot_phase, a.status, a.wait_limit_ns)) { ok = false; break; }
         if (j >= skip) {
-          const int b = c & 1;
-          if (!wait(B_SFULL + 2 * t + b, (c >> 1) & 1)) { ok = false; break; }
+          const uint32_t b = c & 1;
+          if (!wait_warp(bar_s + 8 * b, (c >> 1) & 1, a.status, a.wait_limit_ns)) { ok = false; break; }
           tc_fence_after();
-          const float* nl = reinterpret_cast<const float*>(smem + C::OFF_STAT + s * 512) + 64 * half;
-          // columns that this key's weight has a part in: from its diagonal on,
-          // up to the sequence's end (the others may hold anything)
-          const int first = diag0 - j * TP;
-          const int lo = a.G * max(first + row, 0), hi = a.G * min(tokens - j * TP, 128);
-          const bool masked = first + 127 > 0 || hi < 128;
-          uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
-          const uint32_t s_addr = lane_addr + 128u * (uint32_t)b;
-          if (masked) {
-            // a few tiles to a unit: the others' scores become -inf where they
-            // stand, and no mask is in the pass below
+          const float* nl = reinterpret_cast<const float*>(smem + C::OFF_STAT + slot * 512) + 64 * half + 2 * (lane & 3);
+          const uint32_t s_addr = lane_addr + 128u * b;
+          if (first + 127 > 0 || tokens * a.G < 128) {
+            // Columns that a key's weight has no part in (before its diagonal,
+            // behind the sequence's end: they may hold anything) become -inf
+            // where they stand: a few tiles to a unit, and no mask below.
+            const int lo = a.G * max(first + row, 0), hi = a.G * min(tokens, 128);
 #pragma unroll 1
             for (int q = 0; q < 2; ++q) {
               uint32_t r[32];
@@ -427,57 +462,69 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
             }
             tmem_st_wait();
           }
-          auto add = [&](const uint32_t (&r)[32], int q) {
-#pragma unroll
-            for (int k4 = 0; k4 < 8; ++k4) {
-              const float4 n4 = *reinterpret_cast<const float4*>(nl + 32 * q + 4 * k4);
-              const float2 xa = f2_unpack(ffma2(f2_pack(__uint_as_float(r[4 * k4]), __uint_as_float(r[4 * k4 + 1])), c22, f2_pack(n4.x, n4.y)));
-              const float2 xb = f2_unpack(ffma2(f2_pack(__uint_as_float(r[4 * k4 + 2]), __uint_as_float(r[4 * k4 + 3])), c22, f2_pack(n4.z, n4.w)));
-              const float p0 = ex2_approx(xa.x), p1 = ex2_approx(xa.y), p2 = ex2_approx(xb.x), p3 = ex2_approx(xb.y);
-              sum[k4 & 1] = fadd2(sum[k4 & 1], f2_pack(p0, p1));
-              sum[2 + (k4 & 1)] = fadd2(sum[2 + (k4 & 1)], f2_pack(p2, p3));
-            }
-          };
-          uint32_t ra[32], rb[32];
-          tmem_ld32(s_addr, ra);
+          uint32_t ra[32], rb[32];  // lanes 0-15 and 16-31 of the warp's quarter
+          tmem_ld_16x256(s_addr, ra);
+          tmem_ld_16x256(s_addr + (16u << 16), rb);
           tmem_ld_wait_dep(ra);
-          tmem_ld32(s_addr + 32, rb);
-          add(ra, 0);
           tmem_ld_wait_dep(rb);
           // all of S is in registers: its buffer takes the tile after next
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(BAR(B_SFREE + 2 * t + b));
-          add(rb, 1);
+          if (lane == 0) mbar_arrive(BAR(B_SFREE + 2 * t) + 8 * b);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float2 n2 = *reinterpret_cast<const float2*>(nl + 8 * k);
+            const uint64_t n22 = f2_pack(n2.x, n2.y);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t(&r)[32] = e < 2 ? ra : rb;
+              const int u = 4 * k + 2 * (e & 1);
+              const float2 x = f2_unpack(ffma2(f2_pack(__uint_as_float(r[u]), __uint_as_float(r[u + 1])), c22, n22));
+              sum[e] = fadd2(sum[e], f2_pack(ex2_approx(x.x), ex2_approx(x.y)));
+            }
+          }
           ++c;
-          const float2 sa = f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])));
-          const float y = __fsub_rn(__fadd_rn(sa.x, sa.y), lost), z = __fadd_rn(total, y);
-          lost = __fsub_rn(__fsub_rn(z, total), y);
-          total = z;
+          if ((c & 7) == 0) join();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(B_STEMPTY + s));
+        if (lane == 0) mbar_arrive(BAR(B_STEMPTY) + 8 * slot);
+        first -= TP;
+        tokens -= TP;
+        if (++slot == C::QS) {
+          slot = 0;
+          slot_phase ^= 1u;
+        }
       }
       if (!ok) break;
+      join();
+      // a row's four threads add up; thread l keeps row l / 4 + 8 (l % 4)
+      float mine = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float x = total[e];
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        mine = (lane & 3) == e ? x : mine;
+      }
+      const int row_out = wq * 32 + (lane >> 2) + 8 * (lane & 3);
       // the second half's sums go to the first's warps
-      volatile float* part = reinterpret_cast<float*>(smem + C::OFF_PART + t * 512) + row;
-      g0 += tiles;
+      volatile float* part = reinterpret_cast<float*>(smem + C::OFF_PART + t * 512) + row_out;
       if (half) {
         if (i > 0 && !wait(B_PART + 2 + t, (i - 1) & 1)) { ok = false; break; }
-        *part = total;
+        *part = mine;
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(B_PART + t));
         release_item(i);
         continue;
       }
       if (!wait(B_PART + t, i & 1)) { ok = false; break; }
-      total += *part;
+      mine += *part;
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(B_PART + 2 + t));
-      const int left = item(i, kWLeft), key = item(i, kWKey0) + 128 * t + row, fresh = item(i, kWNew);
+      const int left = item(i, kWLeft), key = item(i, kWKey0) + 128 * t + row_out, fresh = item(i, kWNew);
       float* w = a.W + (long long)item(i, kWSeq) * a.w_batch + (long long)item(i, kWHead) * a.w_head + key;
       // keys that are new with these tokens have no weight yet
-      if (128 * t + row < left) *w = a.accumulate && key < fresh ? *w + total : total;
+      if (128 * t + row_out < left) *w = a.accumulate && key < fresh ? *w + mine : mine;
       release_item(i);
     }
   }
