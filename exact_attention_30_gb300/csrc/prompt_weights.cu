@@ -7,22 +7,24 @@
 // and nothing else: P is summed where it is computed.
 //
 // Keys are the rows of the products (S^T = K Q^T, a TMEM lane per key), so that
-// a thread adds up its own keys' weights over the query tiles: four keys over a
-// quarter of the columns, the four threads of a key joined at the end. (With a
-// key to a thread each needs the statistics of all columns: broadcasts of 16
-// bytes took 3.5 cycles of shared memory each, 900 of a tile's 2280, beside the
-// products' operands: 8 prompts of 361 to 6925 tokens 521 us.) A unit is 256 keys (two tiles) of a sequence and K/V head,
+// a thread adds up its own key's weights over the query tiles and no thread
+// needs another's. A unit is 256 keys (two tiles) of a sequence and K/V head,
 // which stay in shared memory while the query tiles (128 rows: all heads of the
 // group, prompt_fwd.cu) that see them stream through a ring; the next unit's
 // keys load meanwhile. Two tiles of keys per query tile, because one product of
 // 512 cycles per 32 KB of queries would ask the L2 for 18 TB/s. S is double
 // buffered in tensor memory for each key tile (four buffers of 128 columns).
-// Bound by the products and the exponentials alike: 1024 cycles a unit and query
-// tile each (8192 FLOP and 32 exponentials per cycle and SM).
 //
-// Sums: 16 weights of a query tile and key to a thread, 64 of eight tiles in each
-// of two fp32 accumulators, and their sums with a compensation term (Kahan's), in
-// a fixed order.
+// Products and exponentials need 1024 cycles a unit and query tile each (8192
+// FLOP and 32 exponentials per cycle and SM). Measured: 2000, of which the
+// products alone take 1530 (both operands come from shared memory, 128 bytes a
+// cycle) and the weights' warps alone 1850 (their waits and loads 950). Other
+// ways that were slower: keys as first operands in tensor memory, which leaves
+// three S buffers for both tiles (2400); four keys to a thread, by loads of 16
+// lanes, which need a quarter of the statistics (2150).
+//
+// Sums: 64 weights of eight query tiles in each of eight fp32 accumulators, and
+// their sums with a compensation term (Kahan's), in a fixed order.
 //
 // Warps 0: producer, 1: MMA issuer, 2: scheduler, 3: statistics, 4-19: weights,
 // four warps to the first and to the second 64 queries of each key tile (with
@@ -423,18 +425,15 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
       // the token (from the unit's first tile's on) whose diagonal is the key tile's first key
       int first = item(i, kWDiag) + 128 * t;
       int tokens = item(i, kWTokens);  // from the next query tile on
-      // of the rows l / 4 + 8 e of the warp's quarter, over this thread's columns
       uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
-      float total[4] = {0.f, 0.f, 0.f, 0.f}, lost[4] = {0.f, 0.f, 0.f, 0.f};
+      float total = 0.f, lost = 0.f;
       auto join = [&]() {
+        const float2 sa = f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 sa = f2_unpack(sum[e]);
-          sum[e] = 0ull;
-          const float y = __fsub_rn(__fadd_rn(sa.x, sa.y), lost[e]), z = __fadd_rn(total[e], y);
-          lost[e] = __fsub_rn(__fsub_rn(z, total[e]), y);
-          total[e] = z;
-        }
+        for (int e = 0; e < 4; ++e) sum[e] = 0ull;
+        const float y = __fsub_rn(__fadd_rn(sa.x, sa.y), lost), z = __fadd_rn(total, y);
+        lost = __fsub_rn(__fsub_rn(z, total), y);
+        total = z;
       };
 #pragma unroll 1
       for (int j = 0; j < tiles; ++j) {
@@ -443,7 +442,7 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
           const uint32_t b = c & 1;
           if (!wait_warp(bar_s + 8 * b, (c >> 1) & 1, a.status, a.wait_limit_ns)) { ok = false; break; }
           tc_fence_after();
-          const float* nl = reinterpret_cast<const float*>(smem + C::OFF_STAT + slot * 512) + 64 * half + 2 * (lane & 3);
+          const float* nl = reinterpret_cast<const float*>(smem + C::OFF_STAT + slot * 512) + 64 * half;
           const uint32_t s_addr = lane_addr + 128u * b;
           if (first + 127 > 0 || tokens * a.G < 128) {
             // Columns that a key's weight has no part in (before its diagonal,
@@ -462,27 +461,29 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
             }
             tmem_st_wait();
           }
-          uint32_t ra[32], rb[32];  // lanes 0-15 and 16-31 of the warp's quarter
-          tmem_ld_16x256(s_addr, ra);
-          tmem_ld_16x256(s_addr + (16u << 16), rb);
+          auto add = [&](const uint32_t (&r)[32], int q) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float4 n4 = *reinterpret_cast<const float4*>(nl + 32 * q + 4 * k);
+              const float2 x = f2_unpack(ffma2(f2_pack(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1])), c22, f2_pack(n4.x, n4.y)));
+              const float2 y = f2_unpack(ffma2(f2_pack(__uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3])), c22, f2_pack(n4.z, n4.w)));
+              sum[2 * (k & 1)] = fadd2(sum[2 * (k & 1)], f2_pack(ex2_approx(x.x), ex2_approx(x.y)));
+              sum[2 * (k & 1) + 1] = fadd2(sum[2 * (k & 1) + 1], f2_pack(ex2_approx(y.x), ex2_approx(y.y)));
+            }
+          };
+          // the second load is under way while the first is exponentiated (both
+          // awaited first: 611 us instead of 521 for 8 prompts of 361 to 6925 tokens)
+          uint32_t ra[32], rb[32];
+          tmem_ld32(s_addr, ra);
           tmem_ld_wait_dep(ra);
+          tmem_ld32(s_addr + 32, rb);
+          add(ra, 0);
           tmem_ld_wait_dep(rb);
           // all of S is in registers: its buffer takes the tile after next
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(BAR(B_SFREE + 2 * t) + 8 * b);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float2 n2 = *reinterpret_cast<const float2*>(nl + 8 * k);
-            const uint64_t n22 = f2_pack(n2.x, n2.y);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t(&r)[32] = e < 2 ? ra : rb;
-              const int u = 4 * k + 2 * (e & 1);
-              const float2 x = f2_unpack(ffma2(f2_pack(__uint_as_float(r[u]), __uint_as_float(r[u + 1])), c22, n22));
-              sum[e] = fadd2(sum[e], f2_pack(ex2_approx(x.x), ex2_approx(x.y)));
-            }
-          }
+          add(rb, 1);
           ++c;
           if ((c & 7) == 0) join();
         }
@@ -497,34 +498,24 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
       }
       if (!ok) break;
       join();
-      // a row's four threads add up; thread l keeps row l / 4 + 8 (l % 4)
-      float mine = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float x = total[e];
-        x += __shfl_xor_sync(0xffffffffu, x, 1);
-        x += __shfl_xor_sync(0xffffffffu, x, 2);
-        mine = (lane & 3) == e ? x : mine;
-      }
-      const int row_out = wq * 32 + (lane >> 2) + 8 * (lane & 3);
       // the second half's sums go to the first's warps
-      volatile float* part = reinterpret_cast<float*>(smem + C::OFF_PART + t * 512) + row_out;
+      volatile float* part = reinterpret_cast<float*>(smem + C::OFF_PART + t * 512) + row;
       if (half) {
         if (i > 0 && !wait(B_PART + 2 + t, (i - 1) & 1)) { ok = false; break; }
-        *part = mine;
+        *part = total;
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(B_PART + t));
         release_item(i);
         continue;
       }
       if (!wait(B_PART + t, i & 1)) { ok = false; break; }
-      mine += *part;
+      total += *part;
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(B_PART + 2 + t));
-      const int left = item(i, kWLeft), key = item(i, kWKey0) + 128 * t + row_out, fresh = item(i, kWNew);
+      const int left = item(i, kWLeft), key = item(i, kWKey0) + 128 * t + row, fresh = item(i, kWNew);
       float* w = a.W + (long long)item(i, kWSeq) * a.w_batch + (long long)item(i, kWHead) * a.w_head + key;
       // keys that are new with these tokens have no weight yet
-      if (128 * t + row_out < left) *w = a.accumulate && key < fresh ? *w + mine : mine;
+      if (128 * t + row < left) *w = a.accumulate && key < fresh ? *w + total : total;
       release_item(i);
     }
   }
