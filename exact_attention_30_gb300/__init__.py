@@ -103,7 +103,7 @@ _SIGNATURES = {
     "fa_prompt_fwd_workspace_bytes": (_sz, [_ci] * 8),
     "fa_prompt_bwd": (_ci, [_vp] * 5 + [_ll] * 5 + [_vp] * 4 + [_ll] * 3 + [_vp] * 3 + [_sz] + [_ci] * 8 +
                       [_cf, _ci, _vp]),
-    "fa_prompt_bwd_workspace_bytes": (_sz, [_ci] * 6),
+    "fa_prompt_bwd_workspace_bytes": (_sz, [_ci] * 9),
     "fa_prompt_key_weights": (_ci, [_vp, _vp, _ll, _ll, _vp, _vp, _ll, _ll, _ci, _vp, _vp] + [_ci] * 9 +
                               [_cf, _ci, _ci, _vp]),
     "fa_prompt_key_weights_paged": (_ci, [_vp, _ll, _vp, _vp, _ci, _vp, _vp, _vp, _ll, _ll, _ci, _vp] + [_ci] * 5 +
@@ -831,9 +831,11 @@ def fa_prompt_fwd(q, k, v, cu_seqlens_q, max_seqlen_q: int, cu_seqlens_k=None, m
     return out, lse
 
 
-def fa_prompt_bwd_workspace_bytes(B: int, Hq: int, Hkv: int, total_q: int, d: int) -> int:
-    """Scratch bytes fa_prompt_bwd needs."""
-    return int(load_library().fa_prompt_bwd_workspace_bytes(B, Hq, Hkv, total_q, d, FA_BF16))
+def fa_prompt_bwd_workspace_bytes(B: int, Hq: int, Hkv: int, total_q: int, total_k: int, max_seqlen_q: int,
+                                  max_seqlen_k: int, d: int) -> int:
+    """Scratch bytes fa_prompt_bwd needs on the current device."""
+    return int(load_library().fa_prompt_bwd_workspace_bytes(B, Hq, Hkv, total_q, total_k, max_seqlen_q, max_seqlen_k, d,
+                                                            FA_BF16))
 
 
 def fa_prompt_bwd(q, k, v, o, do, lse, cu_seqlens_q, max_seqlen_q: int, cu_seqlens_k=None,
@@ -870,7 +872,8 @@ def fa_prompt_bwd(q, k, v, o, do, lse, cu_seqlens_q, max_seqlen_q: int, cu_seqle
         k = v = torch.zeros((1, hkv, d), dtype=_BF16, device=q.device)
         dk = dv = torch.empty_like(k)
         total_k = mk = 1
-    ws, n, workspace = _scratch(workspace, ("fa_prompt_bwd_workspace_bytes", dev, B, hq, hkv, total, d), q.device, dev)
+    ws, n, workspace = _scratch(workspace, ("fa_prompt_bwd_workspace_bytes", dev, B, hq, hkv, total, total_k, mq, mk, d), q.device,
+                                dev)
     rc = _on_device(dev, load_library().fa_prompt_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
                     qs, ks, vs, os_, dos, lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *strides,
                     cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), ws, n, B, hq, hkv, total, total_k, mq, mk, d, scale,

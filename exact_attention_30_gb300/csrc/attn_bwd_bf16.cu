@@ -407,40 +407,68 @@ __device__ __noinline__ bool bwd_item(const BwdArgs& a, bool list, int w, BwdIte
   return it.n_it > 0;
 }
 
-// The same for prompts: the preprocess's list has (sequence, K/V head, key
-// tile), sequences with the most keys first; a sequence without queries has no
-// items.
-template <int BK>
-__device__ __noinline__ bool prompt_bwd_item(const PromptBwdArgs& a, int w, BwdItem& it) {
+// Where a prompt's key tile kb has its queries: query tiles from that of the
+// first token that sees the tile's first key on; of them part `part` of `splits`.
+struct PromptRange {
+  int first, count;
+};
+__device__ __forceinline__ PromptRange prompt_range(const PromptView& v, int kb, int TP, int part, int splits) {
+  const int t0 = kb * 128 - (v.m - v.n), i0 = t0 > 0 ? t0 / TP : 0;
+  const int n = (v.n + TP - 1) / TP - i0;
+  if (splits == 1) return PromptRange{i0, n};
+  const unsigned s = (unsigned)min(splits, n);  // a range has a tile at least; there are eight at most, n < 2^28
+  if ((unsigned)part >= s) return PromptRange{i0, 0};
+  const int from = (int)((unsigned)part * (unsigned)n / s);
+  return PromptRange{i0 + from, (int)((unsigned)(part + 1) * (unsigned)n / s) - from};
+}
+
+// Unit u (sequence, K/V head, key tile) of the preprocess's list: sequences with
+// the most keys first; a sequence without queries has none.
+struct PromptUnit {
+  PromptView v;
+  int seq, head, kb;
+};
+__device__ __forceinline__ bool prompt_unit(const PromptBwdArgs& a, int u, PromptUnit& k) {
   const int* order = a.item_counter + 2;
   const int* prefix = order + a.nseq;
-  int lo = 0, hi = a.nseq;  // prefix[lo] <= w < prefix[hi]
-  if (w < 0 || w >= prefix[hi]) return false;
+  int lo = 0, hi = a.nseq;  // prefix[lo] <= u < prefix[hi]
+  if (u < 0 || u >= prefix[hi]) return false;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (prefix[mid] <= w) lo = mid;
+    if (prefix[mid] <= u) lo = mid;
     else hi = mid;
   }
-  const int b = order[lo], local = w - prefix[lo];
+  k.seq = order[lo];
+  const int local = u - prefix[lo];
   bool bad = false;
-  const PromptView v = prompt_view(a.seqs, b, bad);
-  const int kblocks = (v.m + BK - 1) / BK;
-  if (kblocks < 1 || v.n < 1) return false;
-  const int head = local / kblocks, TP = a.tile_tokens, past = v.m - v.n;
-  it.kb = local - head * kblocks;
-  it.sv.plane = head;
-  it.sv.start = v.k0;
-  it.sv.len = v.m;
-  // query tiles from that of the first token that sees the key tile's first key
-  const int t0 = it.kb * BK - past, i0 = t0 > 0 ? t0 / TP : 0;
+  k.v = prompt_view(a.seqs, k.seq, bad);
+  const int kblocks = (k.v.m + 127) / 128;
+  if (kblocks < 1 || k.v.n < 1) return false;
+  k.head = local / kblocks;
+  k.kb = local - k.head * kblocks;
+  return true;
+}
+
+// Item w: a unit, or (splits > 1: few units) one range of its query tiles, which
+// leaves fp32 partial sums as a split unit of the fixed-length schedule does.
+template <int BK>
+__device__ __noinline__ bool prompt_bwd_item(const PromptBwdArgs& a, int w, BwdItem& it) {
+  PromptUnit k;
+  const int u = a.splits == 1 ? w : w / a.splits, part = w - u * a.splits, TP = a.tile_tokens;
+  if (w < 0 || !prompt_unit(a, u, k)) return false;
+  const PromptRange r = prompt_range(k.v, k.kb, TP, part, a.splits);
+  it.kb = k.kb;
+  it.sv.plane = k.head;
+  it.sv.start = k.v.k0;
+  it.sv.len = k.v.m;
   it.i_begin = 0;
-  it.n_it = (v.n + TP - 1) / TP - i0;
-  it.tail_unit = -1;
-  it.part = 0;
-  it.q_tok = v.q0 + i0 * TP;
-  it.q_left = v.n - i0 * TP;
-  it.diag0 = t0 - i0 * TP;
-  it.ws_row = (head * a.slots + prompt_slot(v.q0, b, TP) + i0) * 128;
+  it.n_it = r.count;
+  it.tail_unit = a.splits > 1 ? u : -1;
+  it.part = part;
+  it.q_tok = k.v.q0 + r.first * TP;
+  it.q_left = k.v.n - r.first * TP;
+  it.diag0 = k.kb * BK - (k.v.m - k.v.n) - r.first * TP;
+  it.ws_row = (k.head * a.slots + prompt_slot(k.v.q0, k.seq, TP) + r.first) * 128;
   return it.n_it > 0;
 }
 template <int BK, int BQ>
@@ -513,12 +541,12 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
       it.kb = f(3);
       it.i_begin = 0;
       it.n_it = f(5);
-      it.tail_unit = -1;
-      it.part = 0;
       it.q_tok = f(6);
       it.q_left = f(7);
       it.diag0 = f(8);
       it.ws_row = f(9);
+      it.tail_unit = f(10);
+      it.part = f(11);
       return it;
     }
     it.sv.plane = p[0];
@@ -536,8 +564,13 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool causal = a.seq.causal != 0;
   const bool list = a.items > 0;
+  if constexpr (PROMPT) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the convert's CTAs may come; they wait for this grid
+    asm volatile("griddepcontrol.wait;" ::: "memory");               // the preprocess's schedule and statistics are there
+  }
   // item indices >= n_items end the walk (a packed batch's total is in its schedule)
-  const int n_items = !list ? 1 : (PROMPT || a.seq.cu_seqlens != nullptr ? a.item_counter[1] : a.items);
+  int n_items = !list ? 1 : (PROMPT || a.seq.cu_seqlens != nullptr ? a.item_counter[1] : a.items);
+  if constexpr (PROMPT) n_items *= a.splits;
   if (list && (int)blockIdx.x >= n_items) return;
   if (!list) {
     BwdItem it0;
@@ -695,6 +728,8 @@ __global__ void __launch_bounds__(512, 1) bwd_main_kernel(const __grid_constant_
             p[7] = it.q_left;
             p[8] = it.diag0;
             p[9] = it.ws_row;
+            p[10] = it.tail_unit;
+            p[11] = it.part;
           } else {
             p[6] = it.tail_unit;
             p[7] = it.part;
@@ -1609,13 +1644,15 @@ __device__ void prompt_sched_block(const PromptBwdArgs& a) {
   __syncthreads();
   if (t == 0) {
     int acc = 0;
-    for (int i = 0; i < 256; ++i) {
+    for (int i = 0; i < min(256, B); ++i) {  // the threads with sequences are the first ones
       const int x = part[i];
       part[i] = acc;
       acc += x;
     }
     sched[0] = 0;
-    sched[1] = acc;
+    // offsets that run back and forth can give more units than there is room for
+    if (acc > a.items / a.splits) bad = true;
+    sched[1] = min(acc, a.items / a.splits);
     prefix[B] = acc;
   }
   __syncthreads();
@@ -1659,9 +1696,11 @@ __device__ void prompt_zero_block(const PromptBwdArgs& a, int block, int blocks)
 }
 
 constexpr int kPromptZeroBlocks = 32;
+constexpr int kPromptBwdSplits = 8;
 
 template <int D>
 __global__ void __launch_bounds__(256) prompt_bwd_pre_kernel(const __grid_constant__ PromptBwdArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the main kernel's CTAs may come; they wait for this grid
   const int extra = (int)blockIdx.x - a.slots;
   if (extra >= 0) {
     if (blockIdx.y != 0) return;
@@ -1708,8 +1747,46 @@ __global__ void __launch_bounds__(256) prompt_bwd_pre_kernel(const __grid_consta
   }
 }
 
+// The query ranges of split units added up, in order: rows 16 j .. of unit u for
+// block (8 u + j) of these; dK times the softmax scale.
+template <int D>
+__device__ void prompt_merge_rows(const PromptBwdArgs& a, int block) {
+  constexpr int LPR = D / 4, LOADS = 2 * 16 * LPR / 256;
+  const int u = block >> 3;
+  PromptUnit k;
+  if (!prompt_unit(a, u, k)) return;
+  const int t0 = k.kb * 128 - (k.v.m - k.v.n);
+  const int tiles = (k.v.n + a.tile_tokens - 1) / a.tile_tokens - (t0 > 0 ? t0 / a.tile_tokens : 0);
+  const int parts = min(a.splits, tiles);  // as prompt_range
+  const float* base = a.dKVpart + (size_t)u * a.splits * 2 * 128 * D;
+#pragma unroll
+  for (int i = 0; i < LOADS; ++i) {
+    const int x = threadIdx.x + 256 * i, l = x % LPR, which = x / (16 * LPR);  // 0: dV, 1: dK
+    const int r = (block & 7) * 16 + x / LPR % 16, key = k.kb * 128 + r;
+    const float* src = base + (size_t)which * 128 * D + (size_t)r * D + 4 * l;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (key < k.v.m) {
+#pragma unroll
+      for (int p = 0; p < kPromptBwdSplits; ++p) {
+        if (p >= parts) continue;
+        const float4 y = *reinterpret_cast<const float4*>(src + (size_t)p * 2 * 128 * D);
+        sum.x += y.x, sum.y += y.y, sum.z += y.z, sum.w += y.w;
+      }
+      const float f = which ? a.scale : 1.f;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(which ? a.dK : a.dV) +
+                           (long long)(k.v.k0 + key) * (which ? a.dk_stride : a.dv_stride) + (long long)k.head * D + 4 * l;
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(f * sum.x, f * sum.y), pack_bf16x2(f * sum.z, f * sum.w));
+    }
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(256) prompt_bwd_convert_kernel(const __grid_constant__ PromptBwdArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the accumulators and partial sums are there
+  if ((int)blockIdx.x >= a.slots) {
+    prompt_merge_rows<D>(a, ((int)blockIdx.x - a.slots) * a.Hkv + (int)blockIdx.y);
+    return;
+  }
   constexpr int LPR = D / 8, RPB = 256 / LPR;
   const int head = blockIdx.y, slot = blockIdx.x;
   PromptView v;
@@ -1733,7 +1810,8 @@ __global__ void __launch_bounds__(256) prompt_bwd_convert_kernel(const __grid_co
 template <int D>
 cudaError_t launch_prompt_d(const PromptBwdArgs& a, cudaStream_t st) {
   using C = BwdCfg<D>;
-  if (a.slots < 1 || a.nseq < 1 || a.items < 1 || a.splits != 1 || a.item_counter == nullptr || a.seq.causal != 1)
+  if (a.slots < 1 || a.nseq < 1 || a.items < 1 || a.splits < 1 || a.splits > kPromptBwdSplits || (a.splits > 1 && a.dKVpart == nullptr) ||
+      a.item_counter == nullptr || a.seq.causal != 1)
     return cudaErrorInvalidValue;
   prompt_bwd_pre_kernel<D><<<dim3((unsigned)(a.slots + 1 + kPromptZeroBlocks), (unsigned)a.Hkv), 256, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
@@ -1741,13 +1819,28 @@ cudaError_t launch_prompt_d(const PromptBwdArgs& a, cudaStream_t st) {
   static std::atomic<unsigned char> asked[kMaxSharedMemoryDevices];
   e = ask_shared_memory(reinterpret_cast<const void*>(bwd_main_kernel<D, true, PromptBwdArgs>), C::SMEM_ALLOC, asked);
   if (e != cudaSuccess) return e;
+  // Few units (split ranges): each kernel's CTAs come while the one before ends,
+  // and wait for it (5 examples of 9 to 300 tokens, 14 heads on 2, d = 64: 28 us
+  // with it, 32 without). A batch that fills the GPU is slower so (8 prompts of
+  // 500 to 4096 tokens: 1083 us, 1074 without).
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = a.splits > 1 ? 1 : 0;
   const int sms = fwd_slots();
-  bwd_main_kernel<D, true, PromptBwdArgs>
-      <<<(unsigned)(sms > 0 && sms < a.items ? sms : a.items), C::THREADS, C::SMEM_ALLOC, st>>>(a);
-  e = cudaGetLastError();
+  cfg.gridDim = dim3((unsigned)(sms > 0 && sms < a.items ? sms : a.items));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM_ALLOC;
+  e = cudaLaunchKernelEx(&cfg, bwd_main_kernel<D, true, PromptBwdArgs>, a);
   if (e != cudaSuccess) return e;
-  prompt_bwd_convert_kernel<D><<<dim3((unsigned)a.slots, (unsigned)a.Hkv), 256, 0, st>>>(a);
-  return cudaGetLastError();
+  const int merge_blocks = a.splits > 1 ? 8 * (a.items / a.splits / a.Hkv) : 0;  // units: a multiple of the K/V heads
+  cfg.gridDim = dim3((unsigned)(a.slots + merge_blocks), (unsigned)a.Hkv);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, prompt_bwd_convert_kernel<D>, a);
 }
 
 }  // namespace
@@ -1776,6 +1869,15 @@ cudaError_t launch_bwd_bf16(const BwdArgs& a, int BH, int d, unsigned stages, cu
   if (d == 128) return launch_bwd_d<128>(a, BH, stages, st);
   if (d == 64) return launch_bwd_d<64>(a, BH, stages, st);
   return cudaErrorInvalidValue;
+}
+
+int plan_prompt_bwd_splits(long long units, int query_tiles, int slots) {
+  // fewer units than half the SMs: as many ranges of at least two query tiles as
+  // the SMs take at once, eight at most
+  long long s = units > 0 ? slots / units : 1;
+  if (s > query_tiles / 2) s = query_tiles / 2;
+  if (s > kPromptBwdSplits) s = kPromptBwdSplits;
+  return s < 2 ? 1 : (int)s;
 }
 
 cudaError_t launch_prompt_bwd(const PromptBwdArgs& a, int d, cudaStream_t st) {

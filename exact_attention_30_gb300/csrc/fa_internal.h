@@ -328,7 +328,8 @@ inline int pool_box_rows(int page_size, int most) {
 // The backward of packed prompts with grouped heads (attn_bwd_bf16.cu): the main
 // kernel of the causal backward over rows of all heads of a group. Of BwdArgs:
 // tmQ, tmdO as tmQ above; tmK, tmV 3-D as above; tmDQacc over Hkv * slots * 128
-// rows; dQacc, lse2, Drow [Hkv][slots][128 rows]; the schedule ints, nseq, items.
+// rows; dQacc, lse2, Drow [Hkv][slots][128 rows]; the schedule ints, nseq, items
+// (units * splits at most), splits, dKVpart.
 struct PromptBwdArgs : BwdArgs {
   PromptSeqs seqs;
   int Hkv, G, tile_tokens;
@@ -337,6 +338,9 @@ struct PromptBwdArgs : BwdArgs {
   long long o_stride, do_stride, dq_stride, dk_stride, dv_stride;  // elements between tokens
 };
 cudaError_t launch_prompt_bwd(const PromptBwdArgs& a, int d, cudaStream_t st);
+// Ranges of query tiles per (K/V head, key tile) unit, on a GPU that runs `slots`
+// CTAs at once; their fp32 partial dV and dK lie in dKVpart [units][splits][2][128][d].
+int plan_prompt_bwd_splits(long long units, int query_tiles, int slots);
 // The weight that each key got (prompt_weights.cu): W[seq * w_batch + head *
 // w_head + key], keys below w_keys.
 struct PromptWeightArgs {

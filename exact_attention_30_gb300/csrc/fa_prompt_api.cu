@@ -65,19 +65,25 @@ bool encode_keys(CUtensorMap* m, const void* p, long long stride, int Hkv, int t
   return encode_bf16(m, p, 3, dims, strides, box);
 }
 
-// Scratch of the backward: fp32 dQ accumulator, two statistics per row, and the
-// main kernel's schedule (item counter, total, sequence order, B + 1 prefix sums).
+// Scratch of the backward: fp32 dQ accumulator, two statistics per row, split
+// units' partial dV and dK, and the main kernel's schedule (item counter, total,
+// sequence order, B + 1 prefix sums).
 struct BwdLayout {
   long long slots, rows;  // workspace slots per K/V head, rows of 128 of all heads
-  size_t lse2, drow, sched, total;
+  long long units;        // at least as many (K/V head, key tile) units as there are
+  int splits;
+  size_t lse2, drow, part, sched, total;
 };
-BwdLayout bwd_layout(int B, int G, int Hkv, int total_q, int d) {
+BwdLayout bwd_layout(int B, int G, int Hkv, int total_q, int total_k, int max_q, int max_k, int d) {
   BwdLayout L{};
   L.slots = (long long)total_q / prompt_tile_tokens(G) + B + 1;
   L.rows = L.slots * Hkv * 128;
+  L.units = most_blocks(B, total_k, max_k, 128) * Hkv;
+  L.splits = plan_prompt_bwd_splits(L.units, (max_q + prompt_tile_tokens(G) - 1) / prompt_tile_tokens(G), fwd_slots());
   L.lse2 = align_up((size_t)L.rows * d * sizeof(float), 256);
   L.drow = L.lse2 + align_up((size_t)L.rows * sizeof(float), 256);
-  L.sched = L.drow + align_up((size_t)L.rows * sizeof(float), 256);
+  L.part = L.drow + align_up((size_t)L.rows * sizeof(float), 256);
+  L.sched = L.part + (L.splits > 1 ? (size_t)L.units * L.splits * 2 * 128 * d * sizeof(float) : 0);
   L.total = L.sched + align_up(sizeof(int) * (3 + 2 * (size_t)B), 256);
   return L;
 }
@@ -263,9 +269,10 @@ fa_status fa_prompt_paged(const void* Q, long long q_stride, const fa_paged_kv* 
                     workspace, workspace_bytes, cache->d, scale, stream, -1, kDefaultWaitLimitNs);
 }
 
-size_t fa_prompt_bwd_workspace_bytes(int B, int Hq, int Hkv, int total_q, int d, fa_dtype dt) {
-  if (check_heads(B, Hq, Hkv, d, dt) != FA_OK || total_q < 1 || total_q > kPromptMaxTokens) return 0;
-  const BwdLayout L = bwd_layout(B, Hq / Hkv, Hkv, total_q, d);
+size_t fa_prompt_bwd_workspace_bytes(int B, int Hq, int Hkv, int total_q, int total_k, int max_seqlen_q,
+                                     int max_seqlen_k, int d, fa_dtype dt) {
+  if (check_sizes(B, Hq, Hkv, total_q, total_k, max_seqlen_q, max_seqlen_k, d, 1.f, dt) != FA_OK) return 0;
+  const BwdLayout L = bwd_layout(B, Hq / Hkv, Hkv, total_q, total_k, max_seqlen_q, max_seqlen_k, d);
   return L.rows > 0x7fffffffll ? 0 : L.total;
 }
 
@@ -289,7 +296,7 @@ fa_status fa_prompt_bwd(const void* Q, const void* K, const void* V, const void*
       !token_stride_ok(dk_stride, total_k, Hkv, d) || !token_stride_ok(dv_stride, total_k, Hkv, d))
     return FA_ERR_INVALID_ARG;
   const int G = Hq / Hkv;
-  const BwdLayout L = bwd_layout(B, G, Hkv, total_q, d);
+  const BwdLayout L = bwd_layout(B, G, Hkv, total_q, total_k, max_seqlen_q, max_seqlen_k, d);
   if (Hkv > 65535 || L.rows > 0x7fffffffll) return FA_ERR_UNSUPPORTED;
   if (workspace_bytes < L.total) return FA_ERR_INVALID_ARG;
   PromptBwdArgs a;
@@ -323,8 +330,10 @@ fa_status fa_prompt_bwd(const void* Q, const void* K, const void* V, const void*
   a.Drow = reinterpret_cast<float*>(ws + L.drow);
   a.item_counter = reinterpret_cast<int*>(ws + L.sched);
   a.nseq = B;
-  a.items = (int)std::min<long long>(most_blocks(B, total_k, max_seqlen_k, 128) * Hkv, 1 << 30);
-  a.splits = 1;
+  if (L.units > (1 << 28)) return FA_ERR_UNSUPPORTED;
+  a.items = (int)L.units * L.splits;
+  a.splits = L.splits;
+  a.dKVpart = L.splits > 1 ? reinterpret_cast<float*>(ws + L.part) : nullptr;
   a.seq.causal = 1;
   a.seq.H = Hkv;
   a.scale = scale;

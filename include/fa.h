@@ -532,8 +532,9 @@ fa_status fa_prompt_paged(const void* Q, long long q_stride, const fa_paged_kv* 
                           const int* cu_seqlens_q, int B, int Hq, int total_q, int max_seqlen_q, void* workspace,
                           size_t workspace_bytes, float scale, fa_dtype dt, void* stream);
 
-/* Scratch bytes for fa_prompt_bwd (0 on invalid sizes, or sizes past its limits). */
-size_t fa_prompt_bwd_workspace_bytes(int B, int Hq, int Hkv, int total_q, int d, fa_dtype dt);
+/* Scratch bytes for fa_prompt_bwd on the CURRENT device (0 on invalid sizes, or sizes past its limits). */
+size_t fa_prompt_bwd_workspace_bytes(int B, int Hq, int Hkv, int total_q, int total_k, int max_seqlen_q,
+                                     int max_seqlen_k, int d, fa_dtype dt);
 
 /*
  * Backward pass of fa_prompt_fwd: dQ like Q, dK and dV like K and V, the

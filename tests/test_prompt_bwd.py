@@ -107,7 +107,7 @@ def test_graph_follows_offsets():
     cu = c.cu_q.clone()
     o, lse = torch.zeros_like(c.q), torch.zeros((8, 128), device="cuda")
     out = [torch.zeros_like(t) for t in (c.q, c.k, c.v)]
-    ws = torch.empty(fa.fa_prompt_bwd_workspace_bytes(3, 8, 2, 128, 128), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(fa.fa_prompt_bwd_workspace_bytes(3, 8, 2, 128, 128, 128, 128, 128), dtype=torch.uint8, device="cuda")
 
     def step():
         fa.fa_prompt_fwd(c.q, c.k, c.v, cu, 128, out=o, lse=lse)
@@ -166,3 +166,29 @@ def test_refusals():
     for kw in (dict(max_seqlen_q=0), dict(scale=-1.0), dict(workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))):
         with pytest.raises(fa.FAError):
             call(**kw)
+
+
+def test_offsets_back_and_forth():
+    """Sequences one upon another have more key tiles than the tokens: no partial sum goes past the workspace."""
+    c = Prompts((512,), 4, 4, 64, seed=13)
+    b = 9
+    cu = torch.tensor([0, 512] * (b // 2 + 1), dtype=torch.int32).cuda()
+    o, lse = fa.fa_prompt_fwd(c.q, c.k, c.v, c.cu_q, 512)
+    n = fa.fa_prompt_bwd_workspace_bytes(b, 4, 4, 512, 512, 512, 512, 64)
+    ws = torch.full((n + (1 << 22),), 7, dtype=torch.uint8, device="cuda")
+    fa.fa_prompt_bwd(c.q, c.k, c.v, o, c.do, lse, cu, 512, workspace=ws)
+    assert fa.fa_check_device_status() == fa.FA_ERR_INVALID_ARG
+    assert (ws[n:] == 7).all()
+
+
+def test_workspace_of_its_size_alone():
+    """Few key tiles: their query ranges' partial sums lie inside the bytes asked for."""
+    c = Prompts((300, 9, 77), 14, 2, 64, seed=15)
+    o, lse = fa.fa_prompt_fwd(c.q, c.k, c.v, c.cu_q, 300)
+    n = fa.fa_prompt_bwd_workspace_bytes(3, 14, 2, c.total, c.total, 300, 300, 64)
+    ws = torch.full((n + (1 << 22),), 255, dtype=torch.uint8, device="cuda")  # all NaN where anything were read unwritten
+    g = fa.fa_prompt_bwd(c.q, c.k, c.v, o, c.do, lse, c.cu_q, 300, workspace=ws)
+    check_backward(c, *g, 1 / 8)
+    assert (ws[n:] == 255).all()
+    again = fa.fa_prompt_bwd(c.q, c.k, c.v, o, c.do, lse, c.cu_q, 300, workspace=ws)
+    assert torch.equal(again[1], g[1]) and torch.equal(again[2], g[2])  # a fixed order of sums
