@@ -300,6 +300,7 @@ struct PromptFwdArgs {
   PromptSeqs seqs;
   PagedPool pool;            // paged only
   const int* block_tables;   // paged only: [B, max_pages]
+  FastDiv page_div;          // paged only: by the page size
   int max_pages, box_rows;
   void* O;
   long long o_stride;        // elements between the tokens of O
@@ -314,7 +315,6 @@ struct PromptFwdArgs {
   float scale_log2;
   int* status;
   unsigned long long wait_limit_ns;
-  int debug_skip_kv;
 };
 cudaError_t launch_prompt_fwd(const PromptFwdArgs& a, int d, cudaStream_t st);
 // Key ranges per block for `units` blocks (of all heads) that see up to
@@ -360,7 +360,6 @@ struct PromptWeightArgs {
   float scale_log2;
   int* status;
   unsigned long long wait_limit_ns;
-  int debug_skip_q;
 };
 cudaError_t launch_prompt_weights(const PromptWeightArgs& a, int d, cudaStream_t st);
 bool encode_acc_f32(CUtensorMap* m, void* ptr, long long rows, int d);

@@ -109,8 +109,7 @@ FwdPlan fwd_plan(int B, int G, int Hkv, int total_q, int max_q, int max_k, int d
 // `a` stands.
 fa_status fwd_launch(PromptFwdArgs& a, const void* Q, long long q_stride, void* O, long long o_stride, float* LSE,
                      const int* cu_q, int B, int Hq, int total_q, int max_q, long long key_bytes, void* workspace,
-                     size_t workspace_bytes, int d, float scale, void* stream, int debug_skip,
-                     unsigned long long limit_ns) {
+                     size_t workspace_bytes, int d, float scale, void* stream) {
   const int G = Hq / a.Hkv;
   if (!Q || !O || !LSE || !cu_q) return FA_ERR_INVALID_ARG;
   if (!aligned(Q, 16) || !aligned(O, 16) || !aligned(LSE, 4) || !aligned(cu_q, 4) || !aligned(workspace, 256))
@@ -128,8 +127,7 @@ fa_status fwd_launch(PromptFwdArgs& a, const void* Q, long long q_stride, void* 
   a.g_div = fast_div((unsigned)G);
   a.heads_per_group = causal_heads_per_group(a.Hkv, key_bytes, 96ll << 20);
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.wait_limit_ns = limit_ns;
-  a.debug_skip_kv = debug_skip;
+  a.wait_limit_ns = kDefaultWaitLimitNs;
   a.status = device_status_ptr();
   if (!a.status) return FA_ERR_CUDA;
   const FwdPlan p = fwd_plan(B, G, a.Hkv, total_q, max_q, a.seqs.max_k, d);
@@ -172,7 +170,6 @@ fa_status weights_launch(PromptWeightArgs& a, const void* Q, long long q_stride,
   a.heads_per_group = causal_heads_per_group(a.Hkv, 2ll * total_q * a.G * d, 96ll << 20);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_limit_ns = kDefaultWaitLimitNs;
-  a.debug_skip_q = -1;
   a.status = device_status_ptr();
   if (!a.status) return FA_ERR_CUDA;
   if (a.max_units * a.Hkv > 0x7fffffffll) return FA_ERR_UNSUPPORTED;
@@ -230,7 +227,7 @@ fa_status fa_prompt_fwd(const void* Q, const void* K, const void* V, long long q
       !encode_keys(&a.tmV, V, token_stride(v_stride, total_k, Hkv, d), Hkv, total_k, 128, d))
     return FA_ERR_CUDA;
   return fwd_launch(a, Q, q_stride, O, o_stride, LSE, cu_seqlens_q, B, Hq, total_q, max_seqlen_q, 4ll * total_k * d,
-                    workspace, workspace_bytes, d, scale, stream, -1, kDefaultWaitLimitNs);
+                    workspace, workspace_bytes, d, scale, stream);
 }
 
 size_t fa_prompt_fwd_workspace_bytes(int B, int Hq, int Hkv, int total_q, int max_seqlen_q, int max_seqlen_k, int d,
@@ -260,13 +257,14 @@ fa_status fa_prompt_paged(const void* Q, long long q_stride, const fa_paged_kv* 
   a.seqs.max_k = (int)most;
   a.block_tables = block_tables;
   a.max_pages = max_pages;
+  a.page_div = fast_div((unsigned)cache->page_size);
   a.box_rows = pool_box_rows(cache->page_size, 128);
   if (!encode_pool_bf16(&a.tmK, a.pool, false, cache->d, a.box_rows) ||
       !encode_pool_bf16(&a.tmV, a.pool, true, cache->d, a.box_rows))
     return FA_ERR_CUDA;
   const long long keys = std::min<long long>((long long)cache->num_pages * cache->page_size, B * most);
   return fwd_launch(a, Q, q_stride, O, o_stride, LSE, cu_seqlens_q, B, Hq, total_q, max_seqlen_q, 4 * keys * cache->d,
-                    workspace, workspace_bytes, cache->d, scale, stream, -1, kDefaultWaitLimitNs);
+                    workspace, workspace_bytes, cache->d, scale, stream);
 }
 
 size_t fa_prompt_bwd_workspace_bytes(int B, int Hq, int Hkv, int total_q, int total_k, int max_seqlen_q,

@@ -87,7 +87,7 @@ __device__ __forceinline__ bool prompt_block(const PromptFwdArgs& a, long long u
   return true;
 }
 
-// Warps 0-3: producer, MMA issuer, scheduler, none; 4-7 and 8-11: softmax of
+// Warps 0-3: producer, MMA issuer, scheduler, producer of V from pages; 4-7 and 8-11: softmax of
 // query tiles 0 and 1; 12-15: output. Shared memory: that of the two-tile
 // forward, a tile of O on its way out, the rows' sums on their way to the output
 // warps and a ring of published blocks.
@@ -95,15 +95,25 @@ template <int D>
 struct PromptCfg : FwdCfg<D> {
   using F = FwdCfg<D>;
   static constexpr int NTHREADS = 512;
+  // Scores: with d = 128 a buffer for each query tile, over which its weights P
+  // go. With d = 64 three of them in turn: while one tile's P V and the other's
+  // softmax are at work, the next S is there already.
+  static constexpr bool TURNS = D == 64;
+  static constexpr int SBUF = TURNS ? 3 : 2;
+  // Barriers that tell a query tile's softmax of its next S, in turn: as many as
+  // S can be ahead of it, so that none is a phase ahead of its waiter.
+  static constexpr int SFULLS = TURNS ? 3 : 1;
+  static constexpr uint32_t S_COL(int b) { return 128u * b; }
+  static constexpr uint32_t O_COL(int t) { return 128u * SBUF + (uint32_t)D * t; }
   static constexpr int OFF_STAGE = F::OFF_BAR;  // behind the K/V ring: 128 rows of O, as the query tiles are laid out
   static constexpr int OFF_STAT = OFF_STAGE + F::TILE_BYTES;  // float [2 blocks][2 tiles][128 rows]: sums of weights
   static constexpr int IRING = 2;  // blocks published: the one in work and the next
   static constexpr int ITEM_INTS = 12;
   static constexpr int OFF_BARS = OFF_STAT + 2 * 2 * 128 * 4;
-  // q_full[2], q_empty[2], k_full, v_full, k_empty, v_empty [STAGES each], s_full[2], p_full[2], o_done[2],
-  // s_free[2], o_free[2], l_full[2 tiles][2 blocks], stage_full, stage_free, item_full, item_empty [IRING each],
+  // q_full[2], q_empty[2], k_full, v_full, k_empty, v_empty [STAGES each], s_full[2][SFULLS], p_full, s_done
+  // [SBUF each], o_done[2], o_free[2], l_full[2 tiles][2 blocks], stage_full, stage_free, item_full, item_empty [IRING each],
   // cancel, near, drain
-  static constexpr int NBARS = 4 + 4 * F::STAGES + 16 + 2 * IRING + 3;
+  static constexpr int NBARS = 4 + 4 * F::STAGES + 2 * SFULLS + 2 * SBUF + 10 + 2 * IRING + 3;
   static constexpr int OFF_ITEMS = (OFF_BARS + NBARS * 8 + 15) / 16 * 16;
   static constexpr int OFF_CANCEL = OFF_ITEMS + IRING * ITEM_INTS * 4;  // 16 bytes: the next CTA index
   static constexpr int OFF_MISC = OFF_CANCEL + 16;                      // TMEM base, abort flag
@@ -113,7 +123,7 @@ struct PromptCfg : FwdCfg<D> {
   static constexpr int ALLOC = BYTES + 1024 <= MOST ? BYTES + 1024 : MOST;
   // Registers per thread of the control, softmax and output warps, out of the
   // launch's 128 each: control + 2 softmax + out = 512.
-  static constexpr int R_CONTROL = D == 128 ? 64 : 72, R_SOFTMAX = D == 128 ? 176 : 168, R_OUT = D == 128 ? 96 : 104;
+  static constexpr int R_CONTROL = D == 128 ? 64 : 80, R_SOFTMAX = D == 128 ? 176 : 168, R_OUT = D == 128 ? 96 : 96;
   static_assert(128 * (R_CONTROL + 2 * R_SOFTMAX + R_OUT) <= NTHREADS * 128, "register split");
 };
 
@@ -139,8 +149,8 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
   const uint32_t bar0 = sbase + C::OFF_BARS;
   auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   const int B_QFULL = 0, B_QEMPTY = 2, B_KFULL = 4, B_VFULL = B_KFULL + C::STAGES, B_KEMPTY = B_VFULL + C::STAGES,
-            B_VEMPTY = B_KEMPTY + C::STAGES, B_SFULL = B_VEMPTY + C::STAGES, B_PFULL = B_SFULL + 2,
-            B_ODONE = B_PFULL + 2, B_SFREE = B_ODONE + 2, B_OFREE = B_SFREE + 2, B_LFULL = B_OFREE + 2,
+            B_VEMPTY = B_KEMPTY + C::STAGES, B_SFULL = B_VEMPTY + C::STAGES, B_PFULL = B_SFULL + 2 * C::SFULLS,
+            B_SDONE = B_PFULL + C::SBUF, B_ODONE = B_SDONE + C::SBUF, B_OFREE = B_ODONE + 2, B_LFULL = B_OFREE + 2,
             B_STAGE = B_LFULL + 4, B_ITF = B_STAGE + 2, B_ITE = B_ITF + C::IRING, B_CANCEL = B_ITE + C::IRING, B_NEAR = B_CANCEL + 1,
             B_DRAIN = B_NEAR + 1;
   volatile int* items = reinterpret_cast<volatile int*>(smem + C::OFF_ITEMS);
@@ -154,13 +164,15 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
     for (int t = 0; t < 2; ++t) {
       mbar_init(BAR(B_QFULL + t), 1);
       mbar_init(BAR(B_QEMPTY + t), 1);
-      mbar_init(BAR(B_SFULL + t), 1);
-      mbar_init(BAR(B_PFULL + t), 4);  // one arrival per softmax warp
       mbar_init(BAR(B_ODONE + t), 1);
-      mbar_init(BAR(B_SFREE + t), 4);
+      for (int k = 0; k < C::SFULLS; ++k) mbar_init(BAR(B_SFULL + t * C::SFULLS + k), 1);
       mbar_init(BAR(B_OFREE + t), 4);  // one arrival per output warp
       mbar_init(BAR(B_LFULL + 2 * t), 4);  // a barrier for every other block: a tile without rows
       mbar_init(BAR(B_LFULL + 2 * t + 1), 4);  // is done at once, and its waiter may be a block behind
+    }
+    for (int b = 0; b < C::SBUF; ++b) {
+      mbar_init(BAR(B_PFULL + b), 4);  // one arrival per softmax warp
+      mbar_init(BAR(B_SDONE + b), 1);
     }
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(BAR(B_KFULL + s), 1);
@@ -170,7 +182,7 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
     }
     for (int s = 0; s < C::IRING; ++s) {
       mbar_init(BAR(B_ITF + s), 1);   // the scheduler
-      mbar_init(BAR(B_ITE + s), 14);  // one arrival per consuming warp: producer, MMA, 8 softmax, 4 output
+      mbar_init(BAR(B_ITE + s), PAGED ? 15 : 14);  // one arrival per consuming warp: producers, MMA, 8 softmax, 4 output
     }
     mbar_init(BAR(B_STAGE), 4);      // stage_full: one arrival per output warp
     mbar_init(BAR(B_STAGE + 1), 1);  // stage_free
@@ -189,6 +201,14 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
   // shared memory held: rows are independent, and these are not written out.
 
   auto wait = [&](int b, uint32_t parity) { return wait_warp(BAR(b), parity, a.status, a.wait_limit_ns); };
+  // Both at once (an answer takes a hundred cycles, and the products issued last
+  // some hundreds), and whether any warp has given up.
+  auto wait2 = [&](int b, uint32_t parity, int b2, uint32_t parity2) {
+    const int gone = *abort_flag;
+    const bool here = mbar_try_wait2(BAR(b), parity, BAR(b2), parity2);
+    if (__all_sync(0xffffffffu, here && gone == 0)) return true;
+    return !__any_sync(0xffffffffu, gone != 0) && wait(b, parity) && wait(b2, parity2);
+  };
   // Waits for the i-th block of this CTA (a consuming warp; false if the wait
   // ran out), and reads of it, until release_item(i).
   auto get_item = [&](int i) { return wait(B_ITF + i % C::IRING, (i / C::IRING) & 1); };
@@ -248,21 +268,28 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
         __syncwarp();
       }
       if (!ok) *abort_flag = 1;
-    } else if (warp == 0) {
-      // ---------------------------------------------------------- producer
+    } else if (warp == 0 || (PAGED && warp == 3)) {
+      // ---------------------------------------------------------- producers
+      // Of packed tensors warp 0 loads all. Of pages warp 3 loads V: with pages of
+      // 32 keys a tile takes four boxes of each, whose issue by one warp is longer
+      // than the tile's softmax (six chats' next turns, d = 64: 106 us, 97 with two
+      // warps; of packed tensors two warps are slower, 1160 TFLOP/s to 1197).
       // One lane issues the packed tensors' boxes; a paged cache's boxes have a
       // lane each (box `box` of the 64-column chunk `chunk` of a tile).
       const int nbox = PAGED ? C::BN / a.box_rows : 1;
       const bool mine = PAGED ? lane < nbox * C::CH : lane == 0;
       const int box = PAGED ? lane % nbox : 0, chunk = PAGED ? lane / nbox : 0;
+      const bool of_k = warp == 0;
+      const CUtensorMap* map = of_k ? &a.tmK : &a.tmV;
+      const int ring = of_k ? C::OFF_K : C::OFF_V, full = of_k ? B_KFULL : B_VFULL, empty = of_k ? B_KEMPTY : B_VEMPTY;
       if (lane == 0) {
-        tma_prefetch_desc(&a.tmQ);
-        tma_prefetch_desc(&a.tmK);
-        tma_prefetch_desc(&a.tmV);
+        if (of_k) tma_prefetch_desc(&a.tmQ);
+        tma_prefetch_desc(map);
+        if (!PAGED) tma_prefetch_desc(&a.tmV);
       }
       bool ok = true;
-      int g0 = 0, q0_used = 0, q1_used = 0;        // key tiles, and loads of each Q slot, before this block
-      int last_k = -1, last_v = -1, skipped = -1;  // last tiles whose loads were issued, by ring position
+      int g0 = 0, q0_used = 0, q1_used = 0;  // key tiles, and loads of each Q slot, before this block
+      int last = -1, last_v = -1;            // last tiles whose loads were issued, by ring position
       for (int i = 0; ok; ++i) {
         if (!get_item(i)) { ok = false; break; }
         const int n0 = item(i, kItN0), n1 = item(i, kItN1), n_max = max(n0, n1);
@@ -270,19 +297,16 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
         const int kt0 = item(i, kItKt0), left = item(i, kItLeft), head = item(i, kItHead);
         const int key0 = item(i, kItK0) + kt0 * C::BN, tok = item(i, kItQ0) + item(i, kItTok0);
         const int* table = PAGED ? a.block_tables + (size_t)item(i, kItSeq) * a.max_pages : nullptr;
+        // a lane's page and first row of key tile j; row = -1: it has no box there
         auto look_up = [&](int j, int& page, int& row) {
-          page = -1;
-          row = 0;
+          page = 0;
+          row = -1;
           if constexpr (PAGED) {
             const int key = j * C::BN + box * a.box_rows;  // from kt0 on
             if (mine && key < left) {
-              const int at = kt0 * C::BN + key, pi = at / a.pool.page_size;
+              const int at = kt0 * C::BN + key, pi = a.page_div(at);
               row = at - pi * a.pool.page_size;
-              page = __ldg(table + pi);
-              if (page < 0 || page >= a.pool.num_pages) {
-                report_status(a.status, kStatusBadSeqlens);
-                page = a.pool.num_pages;  // outside the tensor: reads as zeros
-              }
+              page = __ldg(table + pi);  // first used a tile later
             }
           }
         };
@@ -293,15 +317,26 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
           const int boxes = keys >= C::BN ? nbox : (keys + a.box_rows - 1) / a.box_rows;
           return (uint32_t)(boxes * a.box_rows * 128 * C::CH);
         };
-        auto load = [&](const CUtensorMap* map, int off, int bar, int s, int j, int page, int row) {
-          const uint32_t dst = sbase + off + s * C::TILE_BYTES;
+        // tile j of K or V into its ring's slot, once that is free
+        auto load = [&](const CUtensorMap* map, int ring, int full, int empty, int j, int page, int row, int& at) {
+          const int g = g0 + j, s = g % C::STAGES;
+          if (!wait(empty + s, ((g / C::STAGES) & 1) ^ 1)) return false;
+          if (lane == 0) mbar_arrive_expect_tx(BAR(full + s), tile_bytes(j));
+          __syncwarp();
+          const uint32_t dst = sbase + ring + s * C::TILE_BYTES;
           if constexpr (PAGED) {
-            if (page >= 0)
-              tma_load_4d(dst + chunk * C::CHUNK_BYTES + box * a.box_rows * 128, map, BAR(bar + s), chunk * 64, row, head, page);
+            if ((unsigned)page >= (unsigned)a.pool.num_pages) {
+              report_status(a.status, kStatusBadSeqlens);
+              page = a.pool.num_pages;  // outside the tensor: reads as zeros
+            }
+            if (row >= 0)
+              tma_load_4d(dst + chunk * C::CHUNK_BYTES + box * a.box_rows * 128, map, BAR(full + s), chunk * 64, row, head, page);
           } else if (lane == 0) {
             for (int c = 0; c < C::CH; ++c)
-              tma_load_3d(dst + c * C::CHUNK_BYTES, map, BAR(bar + s), c * 64, key0 + j * C::BN, head);
+              tma_load_3d(dst + c * C::CHUNK_BYTES, map, BAR(full + s), c * 64, key0 + j * C::BN, head);
           }
+          at = g;
+          return true;
         };
         auto load_q = [&](int t, int& used) {  // once the block before has read the slot
           if ((t == 0 ? n0 : n1) == 0) return true;
@@ -320,31 +355,18 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
         look_up(0, page, row);
         for (int j = 0; j < n_max; ++j) {
           if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
-          const int g = g0 + j, s = g % C::STAGES;
-          const uint32_t ph = (g / C::STAGES) & 1;
-          int next_page = -1, next_row = 0;
+          int next_page = 0, next_row = -1;
           if (j + 1 < n_max) look_up(j + 1, next_page, next_row);
-          if (!wait(B_KEMPTY + s, ph ^ 1)) { ok = false; break; }
-          if (g != a.debug_skip_kv) {
-            if (lane == 0) mbar_arrive_expect_tx(BAR(B_KFULL + s), tile_bytes(j));
-            __syncwarp();
-            load(&a.tmK, C::OFF_K, B_KFULL, s, j, page, row);
-          } else {
-            skipped = g;
-          }
-          last_k = g;
-          if (j == 0 && !(load_q(0, q0_used) && load_q(1, q1_used))) { ok = false; break; }
-          if (!wait(B_VEMPTY + s, ph ^ 1)) { ok = false; break; }
-          if (lane == 0) mbar_arrive_expect_tx(BAR(B_VFULL + s), tile_bytes(j));
-          __syncwarp();
-          load(&a.tmV, C::OFF_V, B_VFULL, s, j, page, row);
-          last_v = g;
+          ok = load(map, ring, full, empty, j, page, row, last);
+          if (of_k && j == 0) ok = ok && load_q(0, q0_used) && load_q(1, q1_used);
+          if constexpr (!PAGED) ok = ok && load(&a.tmV, C::OFF_V, B_VFULL, B_VEMPTY, j, page, row, last_v);
+          if (!ok) break;
           page = next_page;
           row = next_row;
-          if (j == max(0, n_max - 3) && lane == 0) mbar_arrive(BAR(B_NEAR));
+          if (of_k && j == max(0, n_max - 3) && lane == 0) mbar_arrive(BAR(B_NEAR));
         }
         if (!ok) break;
-        if (n_max == 0 && lane == 0) mbar_arrive(BAR(B_NEAR));
+        if (of_k && n_max == 0 && lane == 0) mbar_arrive(BAR(B_NEAR));
         g0 += n_max;
         release_item(i);
       }
@@ -352,8 +374,7 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
       // drain: what was asked for last must have landed before exit
       if (q0_used > 0) wait(B_QFULL + 0, (q0_used - 1) & 1);
       if (q1_used > 0) wait(B_QFULL + 1, (q1_used - 1) & 1);
-      for (int g = max(0, last_k - C::STAGES + 1); g <= last_k; ++g)
-        if (g != skipped) wait(B_KFULL + g % C::STAGES, (g / C::STAGES) & 1);
+      for (int g = max(0, last - C::STAGES + 1); g <= last; ++g) wait(full + g % C::STAGES, (g / C::STAGES) & 1);
       for (int g = max(0, last_v - C::STAGES + 1); g <= last_v; ++g) wait(B_VFULL + g % C::STAGES, (g / C::STAGES) & 1);
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
@@ -363,36 +384,39 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
       const uint64_t dQ0 = sdesc_sw128(sbase + C::OFF_Q, 16, 1024);
       const uint64_t dK0 = sdesc_sw128(sbase + C::OFF_K, 16, 1024);
       const uint64_t dV0 = sdesc_sw128(sbase + C::OFF_V, C::CHUNK_BYTES, 1024);
-      // S of tile t against the keys in slot s; `last`: the block's last for this tile
-      auto issue_s = [&](int t, int s, bool last) {
+      // S of tile t against the keys in slot s, into buffer b, told by the tile's
+      // barrier f; `last`: the block's last for this tile
+      auto issue_s = [&](int t, int s, int b, int f, bool last) {
         const uint64_t qa = dQ0 + (uint64_t)((t * C::TILE_BYTES) >> 4);
         const uint64_t kb = dK0 + (uint64_t)((s * C::TILE_BYTES) >> 4);
-        const uint32_t dcol = tmem + C::S_COL(t);
+        const uint32_t dcol = tmem + C::S_COL(b);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t off = (uint64_t)(((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32) >> 4);
           mma_ss(dcol, qa + off, kb + off, idesc_s, kk > 0 ? 1u : 0u, leader);
         }
-        mma_commit(BAR(B_SFULL + t), leader);
+        mma_commit(BAR(B_SFULL + t * C::SFULLS + f), leader);
         if (last) mma_commit(BAR(B_QEMPTY + t), leader);
       };
       // P V over a whole tile, and over the first `keys` keys (those that the
-      // tile's last query sees) in steps of 16
-      auto issue_pv = [&](int t, int s, bool acc) {
+      // tile's last query sees) in steps of 16; `last`: the block's last for this
+      // tile, O is whole behind it
+      auto issue_pv = [&](int t, int s, int b, bool acc) {
         const uint64_t vb = dV0 + (uint64_t)((s * C::TILE_BYTES) >> 4);
-        const uint32_t dcol = tmem + C::O_COL(t), acol = tmem + C::P_COL(t);
+        const uint32_t dcol = tmem + C::O_COL(t), acol = tmem + C::S_COL(b);
 #pragma unroll
         for (int kk = 0; kk < C::BN / 16; ++kk)
           mma_ts(dcol, acol + kk * 8, vb + (uint64_t)((kk * 2048) >> 4), idesc_o, (acc || kk > 0) ? 1u : 0u, leader);
-        mma_commit(BAR(B_ODONE + t), leader);
+        if constexpr (C::TURNS) mma_commit(BAR(B_SDONE + b), leader);
       };
-      auto issue_pv_keys = [&](int t, int s, bool acc, int keys) {
+      auto issue_pv_keys = [&](int t, int s, int b, bool acc, int keys, bool last) {
         const uint64_t vb = dV0 + (uint64_t)((s * C::TILE_BYTES) >> 4);
-        const uint32_t dcol = tmem + C::O_COL(t), acol = tmem + C::P_COL(t);
+        const uint32_t dcol = tmem + C::O_COL(t), acol = tmem + C::S_COL(b);
 #pragma unroll 1
         for (int kk = 0; kk < C::BN / 16 && 16 * kk < keys; ++kk)
           mma_ts(dcol, acol + kk * 8, vb + (uint64_t)((kk * 2048) >> 4), idesc_o, (acc || kk > 0) ? 1u : 0u, leader);
-        mma_commit(BAR(B_ODONE + t), leader);
+        if constexpr (C::TURNS) mma_commit(BAR(B_SDONE + b), leader);
+        if (last) mma_commit(BAR(B_ODONE + t), leader);
       };
       // V has landed in slot s with `keys` keys of the sequence: rows behind them
       // that the last step would read become zero.
@@ -408,158 +432,325 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
           __syncwarp();
         }
       };
-      bool ok = get_item(0);
-      int n0 = item(0, kItN0), n1 = item(0, kItN1);  // key tiles of the block's query tiles
-      int g0 = 0;              // key tiles before this block
-      int c0 = 0, c1 = 0;      // key tiles of query tiles 0 and 1 before it
-      int q0_used = 0, q1_used = 0;  // blocks with such a tile before it
-      int s_done = 0;  // bit t: the block's first S of tile t has been issued
-      // The first S of tile t (of nt key tiles) of a block whose keys begin at ring position g
-      // (`now`: only if its operands are there).
-      auto first_s = [&](int t, int nt, int g, int c, bool now) {
-        if (nt == 0 || (s_done >> t & 1)) return true;
-        const int s = g % C::STAGES;
-        const uint32_t pk = (g / C::STAGES) & 1, pq = (t == 0 ? q0_used : q1_used) & 1;
-        if (now && !__all_sync(0xffffffffu, mbar_test(BAR(B_KFULL + s), pk) && mbar_test(BAR(B_QFULL + t), pq)))
+      bool ok = true;
+      if constexpr (C::TURNS) {
+        // The (key tile, query tile) pairs in order, tile 0 before tile 1, block
+        // after block; pair number x has S buffer x % 3. S is issued up to three
+        // pairs ahead of P V.
+        int g0 = 0;                  // key tiles before the block
+        int done = 0, issued = 0;    // pairs whose P V, and whose S, has been issued
+        int o0_used = 0, o1_used = 0, q0_used = 0, q1_used = 0;  // blocks with such a tile before, at P V and at S
+        int hi = 0, hg = 0, h0 = 0, h1 = 0, hj = 0, ht = 0;      // the next S: block, its ring position and key tiles, pair
+        int f0 = 0, f1 = 0;                                      // its barrier, by query tile
+        bool known = false;                                      // h0, h1 are those of block hi
+        // The next S, if its operands are there; `must` (no S is under way, it is
+        // this block's): waits for them.
+        auto next_s = [&](bool must) {
+#pragma unroll 1
+          while (true) {
+            if (known) {
+              if (hj < max(h0, h1)) break;
+              hg += max(h0, h1);
+              ++hi;
+              hj = ht = 0;
+              known = false;
+            }
+            const uint32_t pi = (hi / C::IRING) & 1;
+            if (must ? !wait(B_ITF + hi % C::IRING, pi) : !__all_sync(0xffffffffu, mbar_test(BAR(B_ITF + hi % C::IRING), pi)))
+              return !must;
+            h0 = item(hi, kItN0);
+            h1 = item(hi, kItN1);
+            if (h0 < 0) return true;
+            known = true;
+          }
+          if (ht == 0 && hj >= h0) ht = 1;
+          const int s = (hg + hj) % C::STAGES;
+          const uint32_t pk = ((hg + hj) / C::STAGES) & 1, pq = (ht == 0 ? q0_used : q1_used) & 1;
+          if (must) {
+            if (!wait(B_KFULL + s, pk) || (hj == 0 && !wait(B_QFULL + ht, pq))) return false;
+          } else if (!__all_sync(0xffffffffu, mbar_test(BAR(B_KFULL + s), pk))) {
+            return true;
+          } else if (hj == 0 && !__all_sync(0xffffffffu, mbar_test(BAR(B_QFULL + ht), pq))) {
+            return true;
+          }
+          tc_fence_after();
+          issue_s(ht, s, issued % C::SBUF, ht == 0 ? f0 : f1, hj + 1 == (ht == 0 ? h0 : h1));
+          if (ht == 0) f0 = f0 == C::SFULLS - 1 ? 0 : f0 + 1;
+          else f1 = f1 == C::SFULLS - 1 ? 0 : f1 + 1;
+          if (hj == 0) {
+            if (ht == 0) ++q0_used;
+            else ++q1_used;
+          }
+          ++issued;
+          if (ht == 0 && hj < h1) {
+            ht = 1;
+          } else {
+            mma_commit(BAR(B_KEMPTY + s), leader);
+            ++hj;
+            ht = 0;
+          }
           return true;
-        if (!now && !(wait(B_KFULL + s, pk) && wait(B_QFULL + t, pq))) return false;
-        if (C::P_OWN && c > 0 && !wait(B_SFREE + t, (c - 1) & 1)) return false;
-        tc_fence_after();
-        issue_s(t, s, nt == 1);
-        if (t == 0) ++q0_used;
-        else ++q1_used;
-        s_done |= 1 << t;
-        return true;
-      };
-      for (int i = 0; ok && n0 >= 0; ++i) {
-        const int n_max = max(n0, n1);
-        int next0 = -1, next1 = 0;
-        bool fetched = false;
-        auto fetch = [&]() {
-          if (!fetched && !get_item(i + 1)) return false;
-          next0 = item(i + 1, kItN0);
-          next1 = item(i + 1, kItN1);
-          return fetched = true;
         };
 #pragma unroll 1
-        for (int t = 0; ok && t < C::QT; ++t) ok = first_s(t, t == 0 ? n0 : n1, g0, t == 0 ? c0 : c1, false);
-        if (!ok) break;
-        s_done = 0;
-        // before the block's first P V: the accumulator has left tensor memory
-        auto o_free = [&](int t, int j) {
-          const int used = t == 0 ? q0_used : q1_used;
-          return j > 0 || used <= 1 || wait(B_OFREE + t, used & 1);
-        };
-        if (n_max > 0) mma_commit(BAR(B_KEMPTY + g0 % C::STAGES), leader);
-        // The tiles that neither query tile ends near: whole keys, a next S for
-        // both. The loop is kept short (a wait and sixteen products per tile):
-        // what its warp does between two waits, and what it does to the
-        // instruction cache, is on the path from one softmax to the next
-        // (16384 tokens, 32 heads, d = 128: 1385 TFLOP/s with the last tiles'
-        // cases in it).
-        const int n_lean = min(n0, n1) - 2;
-        int j = 0;
+        for (int i = 0; ok; ++i) {
+          ok = get_item(i);
+          if (!ok) break;
+          const int n0 = item(i, kItN0), n1 = item(i, kItN1), n_max = max(n0, n1);
+          if (n0 < 0) break;
+          if (hi < i) {
+            hi = i;
+            hg = g0;
+            hj = ht = 0;
+            known = false;
+          }
+          const int first = item(i, kItFirst), left = item(i, kItLeft);
+          // A query tile's accumulator has left tensor memory: asked before its first P V.
+          auto o_free = [&](int t) {
+            int& used = t == 0 ? o0_used : o1_used;
+            ++used;
+            return used == 1 || wait(B_OFREE + t, used & 1);
+          };
+          const int n_lean = min(n0, n1) - 2;
+          int j = 0;
+          if (n_lean > 0) {
 #pragma unroll 1
-        for (; j < n_lean; ++j) {
-          if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
-          const int g = g0 + j, s = g % C::STAGES, s1 = (g + 1) % C::STAGES;
-          const uint32_t ph1 = ((g + 1) / C::STAGES) & 1;
-          if constexpr (!C::P_OWN) ok = wait(B_VFULL + s, (g / C::STAGES) & 1);
+            while (ok && issued - done < C::SBUF) ok = next_s(true);
+            ok = ok && o_free(0) && o_free(1);
+          }
+#pragma unroll 1
+          while (ok && j < n_max) {
+            // Tiles that neither query tile ends with, S three pairs ahead: kept
+            // short, as below.
+            if (j < n_lean && hi == i && hj == j + 1 && ht == 1) {
+              int b = done % C::SBUF;
+              uint32_t pb = (uint32_t)(done / C::SBUF) & 1u;
+              const int from = j;
+#pragma unroll 1
+              for (; j < n_lean; ++j) {
+                const int g = g0 + j, s = g % C::STAGES, s1 = (g + 1) % C::STAGES, s2 = (g + 2) % C::STAGES;
+                ok = wait2(B_VFULL + s, (g / C::STAGES) & 1, B_PFULL + b, pb);
+                if (!ok) break;
+                tc_fence_after();
+                issue_pv(0, s, b, j > 0);
+                issue_s(1, s1, b, f1, false);
+                f1 = f1 == C::SFULLS - 1 ? 0 : f1 + 1;
+                mma_commit(BAR(B_KEMPTY + s1), leader);
+                pb ^= b == C::SBUF - 1;
+                b = b == C::SBUF - 1 ? 0 : b + 1;
+                ok = wait2(B_KFULL + s2, ((g + 2) / C::STAGES) & 1, B_PFULL + b, pb);
+                if (!ok) break;
+                tc_fence_after();
+                issue_pv(1, s, b, j > 0);
+                issue_s(0, s2, b, f0, j + 3 == n0);
+                f0 = f0 == C::SFULLS - 1 ? 0 : f0 + 1;
+                mma_commit(BAR(B_VEMPTY + s), leader);
+                pb ^= b == C::SBUF - 1;
+                b = b == C::SBUF - 1 ? 0 : b + 1;
+              }
+              done += 2 * (j - from);
+              issued += 2 * (j - from);
+              hj = j + 1;
+              continue;
+            }
+            // The same where there is one query tile only (the last of a sequence).
+            if (j > 0 && j < n_max - 4 && min(n0, n1) <= j && hi == i && hj == j + 3) {
+              const int t = n0 > n1 ? 0 : 1, from = j;
+              int b = done % C::SBUF, f = t == 0 ? f0 : f1;
+              uint32_t pb = (uint32_t)(done / C::SBUF) & 1u;
+#pragma unroll 1
+              for (; j < n_max - 4; ++j) {
+                const int g = g0 + j, s = g % C::STAGES, s3 = (g + 3) % C::STAGES;
+                ok = wait2(B_VFULL + s, (g / C::STAGES) & 1, B_PFULL + b, pb);
+                if (!ok) break;
+                tc_fence_after();
+                issue_pv(t, s, b, true);
+                mma_commit(BAR(B_VEMPTY + s), leader);
+                ok = wait(B_KFULL + s3, ((g + 3) / C::STAGES) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                issue_s(t, s3, b, f, false);
+                mma_commit(BAR(B_KEMPTY + s3), leader);
+                f = f == C::SFULLS - 1 ? 0 : f + 1;
+                pb ^= b == C::SBUF - 1;
+                b = b == C::SBUF - 1 ? 0 : b + 1;
+              }
+              if (t == 0) f0 = f;
+              else f1 = f;
+              done += j - from;
+              issued += j - from;
+              hj = j + 3;
+              continue;
+            }
+            const int g = g0 + j, s = g % C::STAGES;
+            bool v_here = false;
+#pragma unroll 1
+            for (int t = 0; t < C::QT; ++t) {
+              const int nt = t == 0 ? n0 : n1;
+              if (j >= nt) continue;
+              if (issued == done && !next_s(true)) { ok = false; break; }
+#pragma unroll 1
+              while (issued - done < C::SBUF) {
+                const int before = issued;
+                next_s(false);
+                if (issued == before) break;
+              }
+              if (j == 0 && n_lean <= 0 && !o_free(t)) { ok = false; break; }
+              const int b = done % C::SBUF;
+              const uint32_t pb = (uint32_t)(done / C::SBUF) & 1u;
+              if (!v_here) {
+                ok = wait2(B_VFULL + s, (g / C::STAGES) & 1, B_PFULL + b, pb);
+                if (!ok) break;
+                clean_v(s, left - j * C::BN);
+                v_here = true;
+              } else if (!wait(B_PFULL + b, pb)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              issue_pv_keys(t, s, b, j > 0, min(first - 1 + (t + 1) * TP, left) - j * C::BN, j + 1 == nt);
+              ++done;
+            }
+            if (!ok) break;
+            mma_commit(BAR(B_VEMPTY + s), leader);
+            ++j;
+            if (j < n_max && issued - done < C::SBUF) next_s(false);
+          }
+          if (!ok) break;
+          g0 += n_max;
+          release_item(i);
+        }
+      } else {
+        ok = get_item(0);
+        int n0 = item(0, kItN0), n1 = item(0, kItN1);  // key tiles of the block's query tiles
+        int g0 = 0;              // key tiles before this block
+        int c0 = 0, c1 = 0;      // key tiles of query tiles 0 and 1 before it
+        int q0_used = 0, q1_used = 0;  // blocks with such a tile before it
+        int s_done = 0;  // bit t: the block's first S of tile t has been issued
+        // The first S of tile t (of nt key tiles) of a block whose keys begin at ring position g
+        // (`now`: only if its operands are there).
+        auto first_s = [&](int t, int nt, int g, bool now) {
+          if (nt == 0 || (s_done >> t & 1)) return true;
+          const int s = g % C::STAGES;
+          const uint32_t pk = (g / C::STAGES) & 1, pq = (t == 0 ? q0_used : q1_used) & 1;
+          if (now && !__all_sync(0xffffffffu, mbar_test(BAR(B_KFULL + s), pk) && mbar_test(BAR(B_QFULL + t), pq)))
+            return true;
+          if (!now && !(wait(B_KFULL + s, pk) && wait(B_QFULL + t, pq))) return false;
+          tc_fence_after();
+          issue_s(t, s, t, 0, nt == 1);
+          if (t == 0) ++q0_used;
+          else ++q1_used;
+          s_done |= 1 << t;
+          return true;
+        };
+        for (int i = 0; ok && n0 >= 0; ++i) {
+          const int n_max = max(n0, n1);
+          int next0 = -1, next1 = 0;
+          bool fetched = false;
+          auto fetch = [&]() {
+            if (!fetched && !get_item(i + 1)) return false;
+            next0 = item(i + 1, kItN0);
+            next1 = item(i + 1, kItN1);
+            return fetched = true;
+          };
+#pragma unroll 1
+          for (int t = 0; ok && t < C::QT; ++t) ok = first_s(t, t == 0 ? n0 : n1, g0, false);
+          if (!ok) break;
+          s_done = 0;
+          // before the block's first P V: the accumulator has left tensor memory
+          auto o_free = [&](int t, int j) {
+            const int used = t == 0 ? q0_used : q1_used;
+            return j > 0 || used <= 1 || wait(B_OFREE + t, used & 1);
+          };
+          if (n_max > 0) mma_commit(BAR(B_KEMPTY + g0 % C::STAGES), leader);
+          // The tiles that neither query tile ends near: whole keys, a next S for
+          // both. The loop is kept short (a wait and sixteen products per tile):
+          // what its warp does between two waits, and what it does to the
+          // instruction cache, is on the path from one softmax to the next
+          // (16384 tokens, 32 heads, d = 128: 1385 TFLOP/s with the last tiles'
+          // cases in it).
+          const int n_lean = min(n0, n1) - 2;
+          int j = 0;
+#pragma unroll 1
+          for (; j < n_lean; ++j) {
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
+            const int g = g0 + j, s = g % C::STAGES, s1 = (g + 1) % C::STAGES;
+            const uint32_t ph1 = ((g + 1) / C::STAGES) & 1;
+            ok = wait(B_VFULL + s, (g / C::STAGES) & 1);
 #pragma unroll
-          for (int t = 0; t < C::QT; ++t) {
-            const uint32_t pt = (uint32_t)((t == 0 ? c0 : c1) + j) & 1u;
-            if constexpr (C::P_OWN) {
-              ok = ok && wait(B_SFREE + t, pt);
-              if (t == 0) ok = ok && wait(B_KFULL + s1, ph1);
-              if (!ok) break;
-              tc_fence_after();
-              issue_s(t, s1, false);
-              ok = wait(B_PFULL + t, pt) && o_free(t, j);
-              if (t == 0) ok = ok && wait(B_VFULL + s, (g / C::STAGES) & 1);
-              if (!ok) break;
-              tc_fence_after();
-              issue_pv(t, s, j > 0);
-            } else {
+            for (int t = 0; t < C::QT; ++t) {
+              const uint32_t pt = (uint32_t)((t == 0 ? c0 : c1) + j) & 1u;
               ok = ok && wait(B_PFULL + t, pt) && o_free(t, j);
               if (!ok) break;
               tc_fence_after();
-              issue_pv(t, s, j > 0);
+              issue_pv(t, s, t, j > 0);
               if (t == 0) {
                 ok = wait(B_KFULL + s1, ph1);
                 if (!ok) break;
                 tc_fence_after();
               }
-              issue_s(t, s1, false);
+              issue_s(t, s1, t, 0, false);
             }
+            if (!ok) break;
+            mma_commit(BAR(B_VEMPTY + s), leader);
+            mma_commit(BAR(B_KEMPTY + s1), leader);
           }
           if (!ok) break;
-          mma_commit(BAR(B_VEMPTY + s), leader);
-          mma_commit(BAR(B_KEMPTY + s1), leader);
-        }
-        if (!ok) break;
 #pragma unroll 1
-        for (; j < n_max; ++j) {
-          if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
-          const int g = g0 + j, s = g % C::STAGES, s1 = (g + 1) % C::STAGES;
-          const uint32_t ph = (g / C::STAGES) & 1, ph1 = ((g + 1) / C::STAGES) & 1;
-          bool k_next = false, v_here = false;  // K_{j+1}, V_j have landed
-          auto need_v = [&]() {
-            if (!v_here) {
-              if (!wait(B_VFULL + s, ph)) return false;
-              clean_v(s, item(i, kItLeft) - j * C::BN);
-            }
-            return v_here = true;
-          };
-          auto next_s = [&](int t) {
-            if (!k_next && !wait(B_KFULL + s1, ph1)) return false;
-            k_next = true;
-            tc_fence_after();
-            issue_s(t, s1, j + 2 == (t == 0 ? n0 : n1));
-            return true;
-          };
+          for (; j < n_max; ++j) {
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
+            const int g = g0 + j, s = g % C::STAGES, s1 = (g + 1) % C::STAGES;
+            const uint32_t ph = (g / C::STAGES) & 1, ph1 = ((g + 1) / C::STAGES) & 1;
+            bool k_next = false, v_here = false;  // K_{j+1}, V_j have landed
+            auto need_v = [&]() {
+              if (!v_here) {
+                if (!wait(B_VFULL + s, ph)) return false;
+                clean_v(s, item(i, kItLeft) - j * C::BN);
+              }
+              return v_here = true;
+            };
+            auto next_s = [&](int t) {
+              if (!k_next && !wait(B_KFULL + s1, ph1)) return false;
+              k_next = true;
+              tc_fence_after();
+              issue_s(t, s1, t, 0, j + 2 == (t == 0 ? n0 : n1));
+              return true;
+            };
 #pragma unroll 1
-          for (int t = 0; t < C::QT; ++t) {
-            const uint32_t pt = (uint32_t)((t == 0 ? c0 : c1) + j) & 1u;
-            const int nt = t == 0 ? n0 : n1;
-            if (j < nt) {
-              const bool more = j + 1 < nt;
-              // keys of this tile that the query tile's last query sees
-              const int keys = min(item(i, kItFirst) - 1 + (t + 1) * TP, item(i, kItLeft)) - j * C::BN;
-              if constexpr (C::P_OWN) {
-                // P has its own columns: S_{j+1} goes first, P_j V_j follows
-                if (more && !(wait(B_SFREE + t, pt) && next_s(t))) { ok = false; break; }
-                if (!wait(B_PFULL + t, pt) || !o_free(t, j) || !need_v()) { ok = false; break; }
-                tc_fence_after();
-                issue_pv_keys(t, s, j > 0, keys);
-              } else {
+            for (int t = 0; t < C::QT; ++t) {
+              const uint32_t pt = (uint32_t)((t == 0 ? c0 : c1) + j) & 1u;
+              const int nt = t == 0 ? n0 : n1;
+              if (j < nt) {
+                const bool more = j + 1 < nt;
+                // keys of this tile that the query tile's last query sees
+                const int keys = min(item(i, kItFirst) - 1 + (t + 1) * TP, item(i, kItLeft)) - j * C::BN;
                 // P overwrites S: P_j V_j must be issued before S_{j+1}
                 if (!need_v() || !wait(B_PFULL + t, pt) || !o_free(t, j)) { ok = false; break; }
                 tc_fence_after();
-                issue_pv_keys(t, s, j > 0, keys);
+                issue_pv_keys(t, s, t, j > 0, keys, !more);
                 if (more && !next_s(t)) { ok = false; break; }
               }
-            }
-            if (j + 1 == n_max) {
-              // this tile is done with the block: the next block's first S, if
-              // its operands are there already
-              if (!fetch()) { ok = false; break; }
-              if (next0 >= 0 && !first_s(t, t == 0 ? next0 : next1, g0 + n_max, (t == 0 ? c0 : c1) + nt, true)) {
-                ok = false;
-                break;
+              if (j + 1 == n_max) {
+                // this tile is done with the block: the next block's first S, if
+                // its operands are there already
+                if (!fetch()) { ok = false; break; }
+                if (next0 >= 0 && !first_s(t, t == 0 ? next0 : next1, g0 + n_max, true)) {
+                  ok = false;
+                  break;
+                }
               }
             }
+            if (!ok) break;
+            mma_commit(BAR(B_VEMPTY + s), leader);
+            if (j + 1 < n_max) mma_commit(BAR(B_KEMPTY + s1), leader);
           }
-          if (!ok) break;
-          mma_commit(BAR(B_VEMPTY + s), leader);
-          if (j + 1 < n_max) mma_commit(BAR(B_KEMPTY + s1), leader);
+          if (!ok || !fetch()) { ok = false; break; }
+          release_item(i);
+          g0 += n_max;
+          c0 += n0;
+          c1 += n1;
+          n0 = next0;
+          n1 = next1;
         }
-        if (!ok || !fetch()) { ok = false; break; }
-        release_item(i);
-        g0 += n_max;
-        c0 += n0;
-        c1 += n1;
-        n0 = next0;
-        n1 = next1;
       }
       if (!ok && lane == 0) *abort_flag = 1;
       // drain every MMA issued before TMEM can be released
@@ -573,23 +764,28 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
     const int wq = warp & 3;             // TMEM lane quarter
     const int row = wq * 32 + lane;      // row of the tile
     const uint32_t lane_addr = tmem + ((uint32_t)(wq * 32) << 16);
-    const uint32_t s_addr = lane_addr + C::S_COL(t);
     const uint32_t o_addr = lane_addr + C::O_COL(t);
     const float c2 = a.scale_log2;
     const uint64_t c22 = f2_pack(c2, c2);
     bool ok = true;
-    int c = 0;  // key tiles of this query tile before the block
+    int c = 0, pairs = 0;  // key tiles of this query tile, and of both, before the block
     for (int i = 0; ok; ++i) {
       int n_own, sees, first;  // keys from kt0 on that this row and the tile's first row see
       if (!get_item(i)) { ok = false; break; }
-      if (item(i, kItN0) < 0) break;
-      n_own = item(i, t == 0 ? kItN0 : kItN1);
+      const int n0 = item(i, kItN0), n1 = item(i, kItN1), both = min(n0, n1);
+      if (n0 < 0) break;
+      n_own = t == 0 ? n0 : n1;
+      // TURNS: the place of key tile j among the pairs of key and query tiles
+      auto pair = [&](int j) { return pairs + j + (j < both ? j + t : both); };
       first = item(i, kItFirst) + t * TP;
       sees = min(first + a.g_div(row), item(i, kItLeft));
       float m_ref = -INFINITY, l = 0.f;
       for (int j = 0; j < n_own; ++j) {
         if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
-        const bool w = wait_phase(BAR(B_SFULL + t), (c + j) & 1, a.status, a.wait_limit_ns);
+        const int buf = C::TURNS ? pair(j) % C::SBUF : t;
+        const uint32_t s_addr = lane_addr + C::S_COL(buf);
+        const bool w = wait_phase(BAR(B_SFULL + t * C::SFULLS + (c + j) % C::SFULLS), ((c + j) / C::SFULLS) & 1, a.status,
+                                  a.wait_limit_ns);
         if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
         tc_fence_after();
         // the diagonal of the tile's first query decides whether any row has
@@ -624,33 +820,27 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
         uint64_t sm2[4];
         float alpha = 1.f;
         bool moved = false;
-        uint32_t pk[C::P_OWN ? 1 : 64];
+        uint32_t pk[64];
 #pragma unroll 1
         while (true) {
 #pragma unroll
           for (int u = 0; u < 4; ++u) { mx[u] = -INFINITY; sm2[u] = 0ull; }
           const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
           const uint64_t nm2 = f2_pack(neg, neg);
-          if constexpr (C::P_OWN) {
-            ok = softmax_pass_own_p<true>(s_addr, lane_addr + C::P_COL(t), false, 0, c22, nm2, mx, sm2, c + j > 0 && !moved,
-                                          BAR(B_ODONE + t), (uint32_t)(c + j - 1) & 1u, a.status, a.wait_limit_ns);
-            if (!ok) break;
-          } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t r[64];  // 64 columns of S at a time
-              tmem_ld32(s_addr + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
-              tmem_ld32(s_addr + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
-              tmem_ld_wait();
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r[64];  // 64 columns of S at a time
+            tmem_ld32(s_addr + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+            tmem_ld32(s_addr + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+            tmem_ld_wait();
 #pragma unroll
-              for (int u = 0; u < 32; ++u) {
-                const float x0 = __uint_as_float(r[2 * u]), x1 = __uint_as_float(r[2 * u + 1]);
-                mx[u & 3] = fmax3(mx[u & 3], x0, x1);
-                const float2 x = f2_unpack(ffma2(f2_pack(x0, x1), c22, nm2));
-                const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
-                sm2[u & 3] = fadd2(sm2[u & 3], f2_pack(p0, p1));
-                pk[32 * h + u] = pack_bf16x2(p0, p1);
-              }
+            for (int u = 0; u < 32; ++u) {
+              const float x0 = __uint_as_float(r[2 * u]), x1 = __uint_as_float(r[2 * u + 1]);
+              mx[u & 3] = fmax3(mx[u & 3], x0, x1);
+              const float2 x = f2_unpack(ffma2(f2_pack(x0, x1), c22, nm2));
+              const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+              sm2[u & 3] = fadd2(sm2[u & 3], f2_pack(p0, p1));
+              pk[32 * h + u] = pack_bf16x2(p0, p1);
             }
           }
           const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
@@ -661,22 +851,20 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
             m_ref = mt;
           }
           moved = true;
-          if constexpr (C::P_OWN) tmem_st_wait();  // the speculative P is overwritten
         }
-        if (!ok) break;
-        if constexpr (C::P_OWN) {
-          // S_j has been read: S_{j+1} may be written over it
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(BAR(B_SFREE + t));
-        } else {
-          tmem_st32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-          tmem_st32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
-        }
+        tmem_st32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+        tmem_st32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
         const float2 sa = f2_unpack(fadd2(fadd2(sm2[0], sm2[1]), fadd2(sm2[2], sm2[3])));
         l = l * alpha + (sa.x + sa.y);
-        // P V of the tile before is complete here (attn_fwd_bf16.cu): O can be rescaled
+        // O can be rescaled once P V of the tile before is complete: with a buffer
+        // for each query tile it is, since S has come behind it in the same buffer
         if (j > 0 && moved) {
+          if constexpr (C::TURNS) {
+            const bool d = wait_phase(BAR(B_SDONE + pair(j - 1) % C::SBUF), (pair(j - 1) / C::SBUF) & 1, a.status,
+                                      a.wait_limit_ns);
+            if (!__all_sync(0xffffffffu, d)) { ok = false; break; }
+            tc_fence_after();
+          }
 #pragma unroll
           for (int q = 0; q < D / 32; ++q) {
             uint32_t o[32];
@@ -690,11 +878,12 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(B_PFULL + t));
+        if (lane == 0) mbar_arrive(BAR(B_PFULL + buf));
       }
       tmem_st_wait();  // no TMEM store may be in flight when the loop is left early
       if (!ok) break;
       c += n_own;
+      pairs += n0 + n1;
       // the row's sum goes to the output warps, its log-sum-exp out from here
       reinterpret_cast<float*>(smem + C::OFF_STAT)[((i & 1) * 2 + t) * 128 + row] = l;
       __syncwarp();
@@ -723,21 +912,18 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
     const int row = wq * 32 + lane;
     const int rsub = lane >> 3, unit = lane & 7;
     bool ok = true;
-    int c0 = 0, c1 = 0;  // key tiles of query tiles 0 and 1 before the block
+    int o0_used = 0, o1_used = 0;  // blocks with such a tile before
     int staged = 0;      // tiles staged so far
     if (lane == 0 && wq == 0) tma_prefetch_desc(&a.tmO);
     for (int i = 0; ok; ++i) {
       if (!get_item(i)) { ok = false; break; }
       const int n0 = item(i, kItN0), n1 = item(i, kItN1);
       if (n0 < 0) break;
-      c0 += n0;
-      c1 += n1;
       const int n = item(i, kItN);
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {
         const int n_own = t == 0 ? n0 : n1, tok0 = item(i, kItTok0) + t * TP;
-        // the row's sum, then its last P V (in this order: the barrier of the
-        // latter can be a phase behind until the former is there)
+        // the row's sum, then its last P V
         if (!wait(B_LFULL + 2 * t + (i & 1), (i >> 1) & 1)) { ok = false; break; }
         const float l = reinterpret_cast<const float*>(smem + C::OFF_STAT)[((i & 1) * 2 + t) * 128 + row];
         if (tok0 >= n) continue;  // no such tile
@@ -758,7 +944,11 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
           __syncwarp();
           if (any && lane == 0) mbar_arrive(BAR(B_OFREE + t));
         };
-        if (any && !wait(B_ODONE + t, ((t == 0 ? c0 : c1) - 1) & 1)) { ok = false; break; }
+        if (any) {
+          int& used = t == 0 ? o0_used : o1_used;
+          if (!wait(B_ODONE + t, used & 1)) { ok = false; break; }
+          ++used;
+        }
         tc_fence_after();
         if (a.splits > 1) {
           // fp32 rows of this key range (one without keys leaves only its

@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
       tma_prefetch_desc(&a.tmQ);
       tma_prefetch_desc(&a.tmK);
     }
-    int g0 = 0, units = 0, last_q = -1, skipped = -1;
+    int g0 = 0, units = 0, last_q = -1;
     for (int i = 0; ok; ++i) {
       if (!get_item(i)) { ok = false; break; }
       const int left = item(i, kWLeft);
@@ -281,17 +281,13 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
         if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
         const int g = g0 + j, s = g % C::QS;
         if (g >= C::QS && !wait(B_QEMPTY + s, ((g / C::QS) - 1) & 1)) { ok = false; break; }
-        if (g != a.debug_skip_q) {
-          if (lane == 0) {
-            mbar_arrive_expect_tx(BAR(B_QFULL + s), (uint32_t)(RT * 128 * C::CH));
-            for (int c = 0; c < C::CH; ++c)
-              tma_load_4d(sbase + C::OFF_Q + s * C::TILE + c * C::CHUNK, &a.tmQ, BAR(B_QFULL + s), c * 64, 0, tok + j * TP,
-                          head);
-          }
-          __syncwarp();
-        } else {
-          skipped = g;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(BAR(B_QFULL + s), (uint32_t)(RT * 128 * C::CH));
+          for (int c = 0; c < C::CH; ++c)
+            tma_load_4d(sbase + C::OFF_Q + s * C::TILE + c * C::CHUNK, &a.tmQ, BAR(B_QFULL + s), c * 64, 0, tok + j * TP,
+                        head);
         }
+        __syncwarp();
         last_q = g;
         if (j == max(0, tiles - 4) && lane == 0) mbar_arrive(BAR(B_NEAR));
       }
@@ -303,7 +299,7 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
     // drain: what was asked for last must have landed before exit
     for (int i = max(0, units - 2); i < units; ++i) wait(B_KFULL + (i & 1), (i >> 1) & 1);
     for (int g = max(0, last_q - C::QS + 1); g <= last_q; ++g)
-      if (g != skipped) wait(B_QFULL + g % C::QS, (g / C::QS) & 1);
+      wait(B_QFULL + g % C::QS, (g / C::QS) & 1);
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
     const uint32_t leader = elect_one();

@@ -66,6 +66,29 @@ def test_many_sequences_and_one_long():
     check_forward(c, o, lse, 1 / math.sqrt(128), seqs=range(0, 151, 10))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens", [(20, 60, 64, 1), (33, 70)])
+def test_blocks_of_one_and_of_two_query_tiles_in_turn(lens, d):
+    """More blocks than SMs: every CTA takes several, whose query tiles visit different numbers of key tiles, or
+    none, some of them many in a row."""
+    n = [lens[i % len(lens)] for i in range(150)]
+    m = [(700, 1900, 300, 1100, 40)[i % 5] + n[i] for i in range(150)]
+    c = Prompts(n, 16, 4, d, m=m, seed=d)
+    o, lse = _fwd(c)
+    check_forward(c, o, lse, 1 / math.sqrt(d), seqs=range(0, 150, 17))
+
+
+def test_sums_that_grow_late():
+    """The largest scores come last, by far: what was summed before is scaled down, tile after tile."""
+    for d in (64, 128):
+        c = Prompts((100, 260), 8, 2, d, m=(2000, 900), seed=d)
+        for b, rows, keys, nb, mb in c.seqs():
+            ramp = torch.linspace(0.02, 3.0, mb, device="cuda")[:, None, None]
+            c.k[keys] = (c.k[keys].abs() * ramp).to(torch.bfloat16)
+            c.q[rows] = c.q[rows].abs()
+        _check(c)
+
+
 def test_large_scores_and_scale():
     for scale in (0.5, 1.7):
         _check(Prompts((150, 260), 6, 2, 128, seed=3, big=16), scale)
