@@ -672,14 +672,12 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
           int j = 0;
 #pragma unroll 1
           for (; j < n_lean; ++j) {
-            if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
             const int g = g0 + j, s = g % C::STAGES, s1 = (g + 1) % C::STAGES;
             const uint32_t ph1 = ((g + 1) / C::STAGES) & 1;
-            ok = wait(B_VFULL + s, (g / C::STAGES) & 1);
+            ok = wait2(B_VFULL + s, (g / C::STAGES) & 1, B_PFULL, (uint32_t)(c0 + j) & 1u);
 #pragma unroll
             for (int t = 0; t < C::QT; ++t) {
-              const uint32_t pt = (uint32_t)((t == 0 ? c0 : c1) + j) & 1u;
-              ok = ok && wait(B_PFULL + t, pt) && o_free(t, j);
+              ok = ok && (t == 0 || wait(B_PFULL + 1, (uint32_t)(c1 + j) & 1u)) && o_free(t, j);
               if (!ok) break;
               tc_fence_after();
               issue_pv(t, s, t, j > 0);
