@@ -433,10 +433,14 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
       };
 #pragma unroll 1
       for (int j = 0; j < tiles; ++j) {
-        if (!wait_warp(bar_stat + 8 * slot, slot_phase, a.status, a.wait_limit_ns)) { ok = false; break; }
-        if (j >= skip) {
+        if (j < skip) {
+          if (!wait_warp(bar_stat + 8 * slot, slot_phase, a.status, a.wait_limit_ns)) { ok = false; break; }
+        } else {
           const uint32_t b = c & 1;
-          if (!wait_warp(bar_s + 8 * b, (c >> 1) & 1, a.status, a.wait_limit_ns)) { ok = false; break; }
+          if (!wait_warp2(bar_stat + 8 * slot, slot_phase, bar_s + 8 * b, (c >> 1) & 1, a.status, a.wait_limit_ns)) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
           const float* nl = reinterpret_cast<const float*>(smem + C::OFF_STAT + slot * 512) + 64 * half;
           const uint32_t s_addr = lane_addr + 128u * b;

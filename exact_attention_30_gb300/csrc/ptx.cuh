@@ -130,6 +130,13 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int* st
   return __all_sync(0xffffffffu, wait_phase(bar, parity, status, limit_ns));
 }
 
+// Two phases, asked for at once (an answer takes a hundred cycles).
+__device__ __forceinline__ bool wait_warp2(uint32_t bar, uint32_t parity, uint32_t bar2, uint32_t parity2, int* status,
+                                           unsigned long long limit_ns) {
+  return __all_sync(0xffffffffu, mbar_try_wait2(bar, parity, bar2, parity2)) ||
+         (wait_warp(bar, parity, status, limit_ns) && wait_warp(bar2, parity2, status, limit_ns));
+}
+
 // Make generic-proxy writes to shared memory visible to the async proxy
 // (TMA / tensor core operand reads).
 // Registers per thread of this warpgroup, fewer or more than at launch (all of
