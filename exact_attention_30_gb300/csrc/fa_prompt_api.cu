@@ -1,6 +1,6 @@
 // fa_prompt_api.cu -- the C ABI of the prompt operators (fa_prompt_fwd,
-// fa_prompt_paged, fa_prompt_bwd, fa_prompt_key_weights and its paged form): argument validation, tensor maps, plans and launch. Host
-// code only.
+// fa_prompt_paged, fa_prompt_bwd, fa_prompt_key_weights and its paged form):
+// argument validation, tensor maps, plans and launch. Host code only.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -105,16 +105,21 @@ FwdPlan fwd_plan(int B, int G, int Hkv, int total_q, int max_q, int max_k, int d
   return p;
 }
 
-// What fa_prompt_fwd and fa_prompt_paged have in common, once the keys' part of
-// `a` stands.
-fa_status fwd_launch(PromptFwdArgs& a, const void* Q, long long q_stride, void* O, long long o_stride, float* LSE,
-                     const int* cu_q, int B, int Hq, int total_q, int max_q, long long key_bytes, void* workspace,
-                     size_t workspace_bytes, int d, float scale, void* stream) {
-  const int G = Hq / a.Hkv;
+// What fa_prompt_fwd and fa_prompt_paged check alike.
+fa_status check_fwd(const void* Q, long long q_stride, const void* O, long long o_stride, const float* LSE,
+                    const int* cu_q, int Hq, int total_q, int d, const void* workspace) {
   if (!Q || !O || !LSE || !cu_q) return FA_ERR_INVALID_ARG;
   if (!aligned(Q, 16) || !aligned(O, 16) || !aligned(LSE, 4) || !aligned(cu_q, 4) || !aligned(workspace, 256))
     return FA_ERR_INVALID_ARG;
   if (!token_stride_ok(q_stride, total_q, Hq, d) || !token_stride_ok(o_stride, total_q, Hq, d)) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+// What they do alike, once everything is checked and the keys' part of `a` stands.
+fa_status fwd_launch(PromptFwdArgs& a, const void* Q, long long q_stride, void* O, long long o_stride, float* LSE,
+                     const int* cu_q, int B, int Hq, int total_q, int max_q, long long key_bytes, void* workspace,
+                     size_t workspace_bytes, int d, float scale, void* stream) {
+  const int G = Hq / a.Hkv;
   a.seqs.cu_q = cu_q;
   a.seqs.B = B;
   a.seqs.total_q = total_q;
@@ -145,14 +150,19 @@ fa_status fwd_launch(PromptFwdArgs& a, const void* Q, long long q_stride, void* 
   return launch_prompt_fwd(a, d, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-// What the two entry points of the keys' weights have in common.
+// What the two entry points of the keys' weights check alike, and do alike.
+fa_status check_weights(const void* Q, long long q_stride, const float* LSE, const float* W, long long w_batch,
+                        long long w_head, int w_keys, const int* cu_q, int B, int Hq, int Hkv, int total_q, int window,
+                        int d, int flags) {
+  if (!Q || !LSE || !W || !cu_q || window < 0 || (flags & ~FA_ACCUMULATE)) return FA_ERR_INVALID_ARG;
+  if (!aligned(Q, 16) || !aligned(LSE, 4) || !aligned(W, 4) || !aligned(cu_q, 4)) return FA_ERR_INVALID_ARG;
+  if (!token_stride_ok(q_stride, total_q, Hq, d) || !weight_strides_ok(w_batch, w_head, w_keys, B, Hkv))
+    return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
 fa_status weights_launch(PromptWeightArgs& a, const void* Q, long long q_stride, const float* LSE, float* W,
                          long long w_batch, long long w_head, int w_keys, const int* cu_q, int B, int Hq, int total_q,
                          int max_q, int window, int d, float scale, int flags, void* stream) {
-  if (!Q || !LSE || !W || !cu_q || window < 0 || (flags & ~FA_ACCUMULATE)) return FA_ERR_INVALID_ARG;
-  if (!aligned(Q, 16) || !aligned(LSE, 4) || !aligned(W, 4) || !aligned(cu_q, 4)) return FA_ERR_INVALID_ARG;
-  if (!token_stride_ok(q_stride, total_q, Hq, d) || !weight_strides_ok(w_batch, w_head, w_keys, B, a.Hkv))
-    return FA_ERR_INVALID_ARG;
   a.G = Hq / a.Hkv;
   a.tile_tokens = prompt_tile_tokens(a.G);
   a.g_div = fast_div((unsigned)a.G);
@@ -211,7 +221,9 @@ fa_status fa_prompt_fwd(const void* Q, const void* K, const void* V, long long q
                         const int* cu_seqlens_k, int B, int Hq, int Hkv, int total_q, int total_k, int max_seqlen_q,
                         int max_seqlen_k, void* workspace, size_t workspace_bytes, int d, float scale, fa_dtype dt,
                         void* stream) {
-  const fa_status s = check_sizes(B, Hq, Hkv, total_q, total_k, max_seqlen_q, max_seqlen_k, d, scale, dt);
+  fa_status s = check_sizes(B, Hq, Hkv, total_q, total_k, max_seqlen_q, max_seqlen_k, d, scale, dt);
+  if (s != FA_OK) return s;
+  s = check_fwd(Q, q_stride, O, o_stride, LSE, cu_seqlens_q, Hq, total_q, d, workspace);
   if (s != FA_OK) return s;
   if (!K || !V || !cu_seqlens_k) return FA_ERR_INVALID_ARG;
   if (!aligned(K, 16) || !aligned(V, 16) || !aligned(cu_seqlens_k, 4)) return FA_ERR_INVALID_ARG;
@@ -249,6 +261,8 @@ fa_status fa_prompt_paged(const void* Q, long long q_stride, const fa_paged_kv* 
   if (max_pages < 1) return FA_ERR_INVALID_ARG;
   const long long most = std::min<long long>((long long)max_pages * cache->page_size, kPagedMaxKeys);
   s = check_sizes(B, Hq, cache->kv_heads, total_q, (int)most, max_seqlen_q, (int)most, cache->d, scale, dt);
+  if (s != FA_OK) return s;
+  s = check_fwd(Q, q_stride, O, o_stride, LSE, cu_seqlens_q, Hq, total_q, cache->d, workspace);
   if (s != FA_OK) return s;
   if (!block_tables || !seq_lens || !aligned(block_tables, 4) || !aligned(seq_lens, 4)) return FA_ERR_INVALID_ARG;
   a.Hkv = cache->kv_heads;
@@ -354,7 +368,10 @@ fa_status fa_prompt_key_weights(const void* Q, const void* K, long long q_stride
                                 const int* cu_seqlens_q, const int* cu_seqlens_k, int B, int Hq, int Hkv, int total_q,
                                 int total_k, int max_seqlen_q, int max_seqlen_k, int window, int d, float scale,
                                 int flags, fa_dtype dt, void* stream) {
-  const fa_status s = check_sizes(B, Hq, Hkv, total_q, total_k, max_seqlen_q, max_seqlen_k, d, scale, dt);
+  fa_status s = check_sizes(B, Hq, Hkv, total_q, total_k, max_seqlen_q, max_seqlen_k, d, scale, dt);
+  if (s != FA_OK) return s;
+  s = check_weights(Q, q_stride, LSE, W, w_batch_stride, w_head_stride, w_keys, cu_seqlens_q, B, Hq, Hkv, total_q, window,
+                    d, flags);
   if (s != FA_OK) return s;
   if (!K || !cu_seqlens_k || !aligned(K, 16) || !aligned(cu_seqlens_k, 4) || !token_stride_ok(k_stride, total_k, Hkv, d))
     return FA_ERR_INVALID_ARG;
@@ -382,6 +399,9 @@ fa_status fa_prompt_key_weights_paged(const void* Q, long long q_stride, const f
   if (max_pages < 1) return FA_ERR_INVALID_ARG;
   const long long most = std::min<long long>((long long)max_pages * cache->page_size, kPagedMaxKeys);
   s = check_sizes(B, Hq, cache->kv_heads, total_q, (int)most, max_seqlen_q, (int)most, cache->d, scale, dt);
+  if (s != FA_OK) return s;
+  s = check_weights(Q, q_stride, LSE, W, w_batch_stride, w_head_stride, w_keys, cu_seqlens_q, B, Hq, cache->kv_heads,
+                    total_q, window, cache->d, flags);
   if (s != FA_OK) return s;
   if (!block_tables || !seq_lens || !aligned(block_tables, 4) || !aligned(seq_lens, 4)) return FA_ERR_INVALID_ARG;
   a.Hkv = cache->kv_heads;
