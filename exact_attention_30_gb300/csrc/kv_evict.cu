@@ -361,10 +361,12 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __gri
 
 template <int THREADS, bool HELD>
 cudaError_t launch_select(const EvictArgs& a, size_t bytes, cudaStream_t st) {
-  if (bytes > 32 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<THREADS, HELD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e != cudaSuccess) return e;
-  }
+  // for the most that any call needs: two calls at once ask for the same
+  static std::atomic<unsigned char> asked[kMaxSharedMemoryDevices];
+  const cudaError_t e = HELD ? ask_shared_memory(reinterpret_cast<const void*>(evict_select_kernel<THREADS, HELD>),
+                                                 (int)kSelectMostBytes, asked)
+                             : cudaSuccess;
+  if (e != cudaSuccess) return e;
   evict_select_kernel<THREADS, HELD><<<dim3((unsigned)a.Hkv, (unsigned)a.B), THREADS, bytes, st>>>(a);
   return cudaGetLastError();
 }

@@ -109,6 +109,16 @@ def test_long_sequences_in_place():
     _check(cache, _weights((2, 2, 13000), 4, "plain"), 7001, 50, True)
 
 
+@pytest.mark.parametrize("kind", ["plain", "ties"])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_weights_past_shared_memory(kind, in_place):
+    """65000 weights and indices do not fit: the weights are read again for each step of the selection."""
+    extra = 160
+    cache = Cache((60000, 50001, 17), 1, 64, 64, seed=4, spare=extra)
+    w = _weights((3, 1, 60000), 5, kind)
+    _check(cache, w, 5000, 100, in_place, None if in_place else _spare_tables(cache, 5000, extra))
+
+
 def test_no_row_moves_when_all_stay():
     cache = Cache((100, 40), 1, 16, 64, seed=5)
     _check(cache, _weights((2, 1, 100), 6, "plain"), 100, 0, True)
