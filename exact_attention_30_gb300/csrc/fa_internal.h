@@ -312,6 +312,7 @@ struct PromptFwdArgs {
   int splits;                // key ranges per block
   float* Opart;              // splits > 1: fp32 [Hkv * max_blocks][splits][256][d], normalised
   float* Lpart;              // and base-2 log-sum-exps
+  int4* blocks;              // and of each block: first packed token, tokens from there on, K/V head
   float scale_log2;
   int* status;
   unsigned long long wait_limit_ns;

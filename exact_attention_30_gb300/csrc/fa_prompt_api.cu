@@ -91,7 +91,7 @@ BwdLayout bwd_layout(int B, int G, int Hkv, int total_q, int total_k, int max_q,
 struct FwdPlan {
   long long max_blocks;
   int splits;
-  size_t lpart, total;  // scratch: partial rows, then their log-sum-exps
+  size_t lpart, blocks, total;  // scratch: partial rows, their log-sum-exps, the blocks
 };
 FwdPlan fwd_plan(int B, int G, int Hkv, int total_q, int max_q, int max_k, int d) {
   FwdPlan p{};
@@ -100,7 +100,8 @@ FwdPlan fwd_plan(int B, int G, int Hkv, int total_q, int max_q, int max_k, int d
   if (p.splits > 1) {
     const size_t rows = (size_t)p.max_blocks * Hkv * p.splits * 256;
     p.lpart = align_up(rows * d * sizeof(float), 256);
-    p.total = p.lpart + align_up(rows * sizeof(float), 256);
+    p.blocks = p.lpart + align_up(rows * sizeof(float), 256);
+    p.total = p.blocks + align_up((size_t)p.max_blocks * Hkv * sizeof(int4), 256);
   }
   return p;
 }
@@ -143,6 +144,7 @@ fa_status fwd_launch(PromptFwdArgs& a, const void* Q, long long q_stride, void* 
     if (workspace_bytes < p.total) return FA_ERR_INVALID_ARG;
     a.Opart = static_cast<float*>(workspace);
     a.Lpart = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.lpart);
+    a.blocks = reinterpret_cast<int4*>(static_cast<char*>(workspace) + p.blocks);
   }
   if (!encode_grouped(&a.tmQ, Q, token_stride(q_stride, total_q, Hq, d), G, a.Hkv, total_q, a.tile_tokens, d) ||
       !encode_grouped(&a.tmO, O, a.o_stride, G, a.Hkv, total_q, a.tile_tokens, d))

@@ -248,7 +248,11 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
         if (!ok) break;
         PromptBlock b;
         int part = 0;
+        const long long asked = u;
         if (u >= 0 && !prompt_block(a, u, lane, u == 0, b, part)) u = -1;
+        // for the merge: where the block's rows go (no tokens: there is no such block)
+        if (a.splits > 1 && asked >= 0 && part == 0 && lane == 0)
+          a.blocks[asked / a.splits] = u >= 0 ? make_int4(b.v.q0 + b.tok0, b.v.n - b.tok0, b.head, 0) : make_int4(0, 0, 0, 0);
         if (lane == 0) {
           volatile int* d = items + s * C::ITEM_INTS;
           d[kItQ0] = b.v.q0;
@@ -1049,15 +1053,15 @@ template <int D>
 __global__ void __launch_bounds__(256) prompt_merge_kernel(const __grid_constant__ PromptFwdArgs a) {
   constexpr int PER = D / 32, ROWS = 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  PromptBlock k;
-  int part;
-  if (!prompt_block(a, (long long)blockIdx.x / 4 * a.splits, lane, false, k, part)) return;
-  const int RT = a.tile_tokens * a.G;
+  const int unit = (int)(blockIdx.x >> 2);
+  const int4 k = a.blocks[unit];  // first packed token, tokens of the sequence from there on, K/V head
   const int br0 = (int)(blockIdx.x & 3) * 64 + warp * ROWS;  // rows of the block, of one query tile
-  const int t = br0 >> 7, row0 = br0 & 127, tok0 = k.tok0 + t * a.tile_tokens;
-  const long long p0 = (long long)k.unit * a.splits * 256 + br0;
+  const int t = br0 >> 7, row0 = br0 & 127;
+  const long long p0 = (long long)unit * a.splits * 256 + br0;
+  // what a launch that gave up left unwritten is not followed
+  if (k.x < 0 || k.y > a.seqs.total_q - k.x || (unsigned)k.z >= (unsigned)a.Hkv) return;
   // the rows that there are begin the eight: rows of a sequence's end lack the last ones
-  const int live = min(ROWS, min(RT, (k.v.n - tok0) * a.G) - row0);
+  const int live = min(ROWS, min(a.tile_tokens, k.y - t * a.tile_tokens) * a.G - row0);
   if (live <= 0) return;
   float L[ROWS], acc[ROWS][PER], sum[ROWS];
 #pragma unroll
@@ -1100,8 +1104,8 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const __grid_constant
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
     if (i >= live) break;
-    const int row = row0 + i, tk = a.g_div(row), hq = k.head * a.G + row - tk * a.G;
-    const long long tok = k.v.q0 + tok0 + tk;
+    const int row = row0 + i, tk = a.g_div(row), hq = k.z * a.G + row - tk * a.G;
+    const long long tok = k.x + t * a.tile_tokens + tk;
     const float inv = sum[i] == 0.f ? 0.f : 1.f / sum[i];
     __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.O) + tok * a.o_stride + (long long)hq * D + lane * PER;
     if constexpr (PER == 4)
