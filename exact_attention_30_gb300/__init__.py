@@ -20,6 +20,16 @@ Serving from a paged cache (k_pages, v_pages: [pages, Hkv, page_size, d]):
     q = fa_kv_append(k, v, k_pages, v_pages, block_tables, seq_lens, cu_seqlens, q=q, cos=cos, sin=sin)
     o, lse = fa_decode_paged(q, k_pages, v_pages, block_tables, seq_lens)       # q: [B,Hq,Nq,d]
     o, lse = fa_decode_shared(q, k_pages, v_pages, prefix_pages, prefix_len, block_tables, seq_lens)
+
+Prompts, packed [total, heads, d] with grouped heads, forward and backward; the
+same over the cache; the weight that each key got; keeping the heaviest keys:
+
+    o, lse = fa_prompt_fwd(q, k, v, cu_seqlens, max_seqlen)
+    dq, dk, dv = fa_prompt_bwd(q, k, v, o, do, lse, cu_seqlens, max_seqlen)
+    o, lse = fa_prompt_paged(q, k_pages, v_pages, block_tables, seq_lens, cu_seqlens, max_seqlen)
+    w = fa_prompt_key_weights(q, k, lse, weights, cu_seqlens, max_seqlen, window=64)    # weights: [B,Hkv,keys]
+    w = fa_decode_key_weights(q4, k_pages, block_tables, seq_lens, lse, weights)        # added, step by step
+    new_lens, kept = fa_kv_evict(k_pages, v_pages, block_tables, seq_lens, weights, budget, recent)
 """
 from __future__ import annotations
 

@@ -12,22 +12,40 @@
 // instead of 37 of four, and a CTA's keys and values serve 2 TP tokens of every
 // head.
 //
-// CTA = one block: two query tiles of one sequence and K/V head. Warp roles,
-// products, tensor-memory columns and the online softmax are those of the
-// forward in attn_fwd_bf16.cu (described there). What differs: each tile visits
-// its own number of key tiles (its last query's diagonal), the diagonal of a
-// tile can cross two key tiles, rows may see no key at all, and keys come either
-// packed (one TMA box per 128 keys) or from the pages of a cache (one box per
-// page or part of one, issued by the lanes of the producer warp). What stands
-// behind a sequence's last key (another sequence's rows, old rows of a page, NaN
-// included) has no influence: its scores are replaced, the products over keys
-// end at the last one, and the up to 15 rows of V that their last step still
-// reads are set to zero.
+// A block is two query tiles of one sequence and K/V head, whose key tiles are
+// those of the second one's last query. Products and online softmax are those of
+// the forward in attn_fwd_bf16.cu (described there). What differs: each tile
+// visits its own number of key tiles, the diagonal of a tile can cross two key
+// tiles (masked scores are replaced where they stand, in tensor memory, in a pass
+// of its own: a few tiles to a block, and no mask in the loop), rows may see no
+// key at all, and keys come either packed (one TMA box per 128 keys) or from the
+// pages of a cache (one box per page or part of one, issued by the lanes of a
+// producer warp). What stands behind a sequence's last key (another sequence's
+// rows, old rows of a page, NaN included) has no influence: its scores are
+// replaced, the products over keys end at the last one, and the up to 15 rows of
+// V that their last step still reads are set to zero. P is rounded to bf16 for its
+// product, its sum is not.
 //
-// Blocks are listed longest first (prompt.cuh); each CTA finds its own from the
-// offsets on the device, so a captured graph follows them. Few blocks with many
-// keys are split into key ranges, whose partial results prompt_merge_kernel
-// combines by their maxima and sums.
+// Blocks are listed longest first (prompt.cuh), found from the offsets on the
+// device, so a captured graph follows them. CTAs are persistent: near the end of
+// its block a CTA's scheduler warp takes over the index of one that has not begun
+// (cluster launch control), so that the next block's loads and first products run
+// under the last one's softmax, while four warps of their own take the last one's
+// output away (16384 tokens, 32 heads: one block per CTA 1442 TFLOP/s, blocks taken
+// over 1728, with output warps 1839; taken over earlier, a long block would hold
+// the next one back). Few blocks with many keys are split into key ranges, whose
+// partial results prompt_merge_kernel combines by their maxima and sums.
+//
+// Bound, per pair of query tiles and 128 keys and SM, in cycles: products 2048
+// (d = 128) or 1024 (d = 64), exponentials 1024. Measured on long prompts: 2640
+// (1860 TFLOP/s) and 2170 (1190). What is between is the chain from scores to
+// weights to the next product, whose waits cost a hundred cycles each even when
+// they are over: with d = 128 tensor memory is full with two tiles' S and O, so a
+// tile's next S can only follow its P V; with d = 64 three S buffers in turn take
+// that out of the chain (1000 TFLOP/s without), and what is left is the time in
+// which the issuing warp asks and waits. Times in a batch: 16 prompts of 128 to 7821
+// tokens (32 heads on 8, d = 128) 980 us, one of 32768 tokens 5.1 ms, the next
+// turns of six chats (d = 64, pages of 32 keys) 90 us, one of 37 tokens 12.5 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -1051,68 +1069,65 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
 // together), ranges without keys (L = -inf) not read.
 template <int D>
 __global__ void __launch_bounds__(256) prompt_merge_kernel(const __grid_constant__ PromptFwdArgs a) {
-  constexpr int PER = D / 32, ROWS = 8;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int ROWS = 8, LPR = D / 4, RPW = 32 / LPR, STEPS = ROWS / RPW;  // rows of a warp, lanes to a row, rows at once
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
   const int unit = (int)(blockIdx.x >> 2);
   const int4 k = a.blocks[unit];  // first packed token, tokens of the sequence from there on, K/V head
   const int br0 = (int)(blockIdx.x & 3) * 64 + warp * ROWS;  // rows of the block, of one query tile
   const int t = br0 >> 7, row0 = br0 & 127;
-  const long long p0 = (long long)unit * a.splits * 256 + br0;
   // what a launch that gave up left unwritten is not followed
   if (k.x < 0 || k.y > a.seqs.total_q - k.x || (unsigned)k.z >= (unsigned)a.Hkv) return;
   // the rows that there are begin the eight: rows of a sequence's end lack the last ones
   const int live = min(ROWS, min(a.tile_tokens, k.y - t * a.tile_tokens) * a.G - row0);
   if (live <= 0) return;
-  float L[ROWS], acc[ROWS][PER], sum[ROWS];
+  const long long p0 = (long long)unit * a.splits * 256 + br0 + sub;
+  const float* lpart = a.Lpart + p0;
+  const float4* opart = reinterpret_cast<const float4*>(a.Opart + p0 * D) + l;
+  float top[STEPS], sum[STEPS];
+  float4 acc[STEPS];
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    L[i] = -INFINITY;
+  for (int i = 0; i < STEPS; ++i) {
+    top[i] = -INFINITY;
     sum[i] = 0.f;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) acc[i][e] = 0.f;
+    acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   for (int p = 0; p < a.splits; ++p) {
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) L[i] = fmaxf(L[i], a.Lpart[p0 + 256ll * p + i]);  // rows past `live`: any value
+    for (int i = 0; i < STEPS; ++i) top[i] = fmaxf(top[i], lpart[p * 256 + i * RPW]);  // rows past `live`: any value
   }
   for (int p = 0; p < a.splits; ++p) {
-    float lp[ROWS], x[ROWS][PER];
+    float lp[STEPS];
+    float4 x[STEPS];
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      lp[i] = i < live ? a.Lpart[p0 + 256ll * p + i] : -INFINITY;
-      const float* src = a.Opart + (p0 + 256ll * p + i) * D + lane * PER;
-#pragma unroll
-      for (int e = 0; e < PER; ++e) x[i][e] = 0.f;
-      if (lp[i] != -INFINITY) {
-        if constexpr (PER == 4) {
-          const float4 y = *reinterpret_cast<const float4*>(src);
-          x[i][0] = y.x, x[i][1] = y.y, x[i][2] = y.z, x[i][3] = y.w;
-        } else {
-          const float2 y = *reinterpret_cast<const float2*>(src);
-          x[i][0] = y.x, x[i][1] = y.y;
-        }
-      }
+    for (int i = 0; i < STEPS; ++i) {
+      lp[i] = i * RPW + sub < live ? lpart[i * RPW] : -INFINITY;
+      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (lp[i] != -INFINITY) x[i] = opart[i * RPW * LPR];
     }
+    lpart += 256;
+    opart += 256 * LPR;
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      const float w = lp[i] == -INFINITY ? 0.f : exp2f(lp[i] - L[i]);
+    for (int i = 0; i < STEPS; ++i) {
+      if (lp[i] == -INFINITY) continue;
+      const float w = ex2_approx(lp[i] - top[i]);
       sum[i] += w;
-#pragma unroll
-      for (int e = 0; e < PER; ++e) acc[i][e] = w > 0.f ? fmaf(w, x[i][e], acc[i][e]) : acc[i][e];
+      if (!(w > 0.f)) continue;  // nothing of what is too small, an infinity included
+      acc[i].x = fmaf(w, x[i].x, acc[i].x);
+      acc[i].y = fmaf(w, x[i].y, acc[i].y);
+      acc[i].z = fmaf(w, x[i].z, acc[i].z);
+      acc[i].w = fmaf(w, x[i].w, acc[i].w);
     }
   }
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    if (i >= live) break;
-    const int row = row0 + i, tk = a.g_div(row), hq = k.z * a.G + row - tk * a.G;
+  for (int i = 0; i < STEPS; ++i) {
+    const int r = i * RPW + sub;
+    if (r >= live) break;
+    const int row = row0 + r, tk = a.g_div(row), hq = k.z * a.G + row - tk * a.G;
     const long long tok = k.x + t * a.tile_tokens + tk;
     const float inv = sum[i] == 0.f ? 0.f : 1.f / sum[i];
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.O) + tok * a.o_stride + (long long)hq * D + lane * PER;
-    if constexpr (PER == 4)
-      *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(acc[i][0] * inv, acc[i][1] * inv), pack_bf16x2(acc[i][2] * inv, acc[i][3] * inv));
-    else
-      *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(acc[i][0] * inv, acc[i][1] * inv);
-    if (lane == 0) a.LSE[(size_t)hq * a.seqs.total_q + tok] = (L[i] + __log2f(sum[i])) * 0.69314718055994531f;
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + tok * a.o_stride + (long long)hq * D + 4 * l) =
+        make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv));
+    if (l == 0) a.LSE[(size_t)hq * a.seqs.total_q + tok] = (top[i] + __log2f(sum[i])) * 0.69314718055994531f;
   }
 }
 

@@ -16,12 +16,15 @@
 // buffered in tensor memory for each key tile (four buffers of 128 columns).
 //
 // Products and exponentials need 1024 cycles a unit and query tile each (8192
-// FLOP and 32 exponentials per cycle and SM). Measured: 2000, of which the
-// products alone take 1530 (both operands come from shared memory, 128 bytes a
-// cycle) and the weights' warps alone 1850 (their waits and loads 950). Other
+// FLOP and 32 exponentials per cycle and SM). Measured: 1950 (8 prompts of 361 to
+// 6925 tokens, 32 heads on 8: 492 us; the last 64 tokens of six of 5627 to 18982:
+// 47 us, of which most is the beginning and end of units of two query tiles). The
+// products alone take 1530 and the weights' warps alone 1850, their waits and
+// loads 950 of it: each wait takes a hundred cycles even when it is over, so
+// statistics and scores are awaited at once (503 us one after the other, 492 so). Other
 // ways that were slower: keys as first operands in tensor memory, which leaves
 // three S buffers for both tiles (2400); four keys to a thread, by loads of 16
-// lanes, which need a quarter of the statistics (2150).
+// lanes, which need a quarter of the statistics (2150); loads of 16 columns (2040).
 //
 // Sums: 64 weights of eight query tiles in each of eight fp32 accumulators, and
 // their sums with a compensation term (Kahan's), in a fixed order.
@@ -407,9 +410,9 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
     const uint32_t lane_addr = tmem + ((uint32_t)(wq * 32) << 16) + C::S_COL(t, 0) + 64u * half;
     const uint64_t c22 = f2_pack(a.scale_log2, a.scale_log2);
     // The loop over query tiles is bound by the instructions it issues: 140 for
-    // 64 columns of 32 keys, and what comes on top (317 in all once, 521 us for 8
-    // prompts of 361 to 6925 tokens). So ring positions are counted, not divided
-    // out, masks are rare, and sums are joined only every eighth tile.
+    // 64 columns of 32 keys, and what comes on top (317 in all once: 521 us for 8
+    // prompts of 361 to 6925 tokens, 503 now). So ring positions are counted, not
+    // divided out, masks are rare, and sums are joined only every eighth tile.
     uint32_t slot = 0, slot_phase = 0;  // ring position of the next query tile
     int c = 0;                          // S tiles of this key tile so far
     const uint32_t bar_stat = BAR(B_STFULL), bar_s = BAR(B_SFULL + 2 * t);
