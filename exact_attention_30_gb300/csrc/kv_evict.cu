@@ -105,6 +105,8 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_cons
       const float4 y = reinterpret_cast<const float4*>(w)[j];
       reinterpret_cast<uint4*>(held)[j] = make_uint4(order_of(y.x), order_of(y.y), order_of(y.z), order_of(y.w));
     }
+    // (rows that do not begin on 16 bytes, every second or third of an odd width)
+#pragma unroll 8
     for (int j = 4 * whole + t; j < len; j += THREADS) held[j] = order_of(w[j]);
   }
   __syncthreads();
@@ -167,58 +169,42 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_cons
   // most `ties` of those equal to the last.
   const bool all = need >= old;
   if constexpr (HELD) {
-    // A run of keys to each warp: counted, then listed 128 at a time, four to a
-    // lane, behind what the warps before it list. Larger ones are counted in the
-    // low half of a word, equal ones in the high half.
+    // A run of keys to each warp: counted, then listed 32 at a time behind what
+    // the warps before it list. Larger ones are counted in the low half of a word,
+    // equal ones in the high half. (Four neighbouring keys to a lane, counts summed
+    // over the lanes: 12800 cycles for the list of 32499 weights, 8900 by ballots.)
     __shared__ unsigned counts[32];
     constexpr int WARPS = THREADS / 32;
     const int warp = t >> 5, lane = t & 31;
     int* list = reinterpret_cast<int*>(held + a.held_words);
-    const int run = ((old + WARPS - 1) / WARPS + 127) & ~127;
+    const int run = ((old + WARPS - 1) / WARPS + 31) & ~31;
     const int first = warp * run, last = need > 0 ? min(old, first + run) : 0;
-    // bits 0-3: which of the four keys from j on are larger, bits 16-19: equal
-    auto classes = [&](int j, const uint4& u) {
-      unsigned c = 0;
-      const unsigned k[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (j + e < last && (all || k[e] > least)) c |= 1u << e;
-        if (j + e < last && !all && k[e] == least) c |= 0x10000u << e;
-      }
-      return c;
-    };
-    auto count_of = [](unsigned c) { return (unsigned)__popc(c & 15u) | (unsigned)__popc(c >> 16) << 16; };
     unsigned n = 0;
-#pragma unroll 2
-    for (int j = first + 4 * lane; j < last; j += 128) n += count_of(classes(j, *reinterpret_cast<const uint4*>(held + j)));
+#pragma unroll 4
+    for (int j = first + lane; j < last; j += 32) {
+      const unsigned u = held[j];
+      n += (all || u > least ? 1u : 0u) + (u == least ? 0x10000u : 0u);  // (none equal where all stay: least is 0, no weight's)
+    }
     n = __reduce_add_sync(0xffffffffu, n);
     if (lane == 0) counts[warp] = n;
     __syncthreads();
     n = __reduce_add_sync(0xffffffffu, lane < warp ? counts[lane] : 0u);
-#pragma unroll 1
-    for (int j0 = first; j0 < last; j0 += 128) {
-      const int j = j0 + 4 * lane;
-      uint4 u = make_uint4(0u, 0u, 0u, 0u);
-      if (j < last) u = *reinterpret_cast<const uint4*>(held + j);
-      const unsigned c = classes(j, u), mine = count_of(c);
-      unsigned sum = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned y = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += y;
+    int ng = (int)(n & 0xffffu), ne = (int)(n >> 16);
+    const unsigned before = (1u << lane) - 1u;
+#pragma unroll 4
+    for (int j0 = first; j0 < last; j0 += 32) {
+      const int j = j0 + lane;
+      const unsigned u = j < last ? held[j] : 0u;
+      const bool gt = j < last && (all || u > least), eq = j < last && u == least;
+      const unsigned mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
+      if (me == 0u) {  // nearly always; counting a mask's bits takes a warp eight cycles
+        if (gt) list[ng + __popc(mg & before) + min(ne, ties)] = j;
+      } else {
+        const int e = ne + __popc(me & before);
+        if (gt || (eq && e < ties)) list[ng + __popc(mg & before) + min(e, ties)] = j;
+        ne += __popc(me);
       }
-      const unsigned here = n + sum - mine;
-      int ng = (int)(here & 0xffffu), ne = (int)(here >> 16);
-      if (c != 0u) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool eq = c >> (16 + e) & 1u;
-          if ((c >> e & 1u) || (eq && ne < ties)) list[ng + min(ne, ties)] = j + e;
-          ng += c >> e & 1u;
-          ne += eq;
-        }
-      }
-      n += __shfl_sync(0xffffffffu, sum, 31);
+      ng += __popc(mg);
     }
     // and out in order, the newest ones behind (stored as they were found, a few
     // lanes of a warp at a time, the lists of 2048 out of 30000 took 6 us)
