@@ -141,7 +141,7 @@ struct PromptCfg : FwdCfg<D> {
   static constexpr int ALLOC = BYTES + 1024 <= MOST ? BYTES + 1024 : MOST;
   // Registers per thread of the control, softmax and output warps, out of the
   // launch's 128 each: control + 2 softmax + out = 512.
-  static constexpr int R_CONTROL = D == 128 ? 64 : 80, R_SOFTMAX = D == 128 ? 176 : 168, R_OUT = D == 128 ? 96 : 96;
+  static constexpr int R_CONTROL = D == 128 ? 64 : 88, R_SOFTMAX = D == 128 ? 176 : 160, R_OUT = D == 128 ? 96 : 104;
   static_assert(128 * (R_CONTROL + 2 * R_SOFTMAX + R_OUT) <= NTHREADS * 128, "register split");
 };
 
@@ -200,13 +200,13 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
     }
     for (int s = 0; s < C::IRING; ++s) {
       mbar_init(BAR(B_ITF + s), 1);   // the scheduler
-      mbar_init(BAR(B_ITE + s), PAGED ? 15 : 14);  // one arrival per consuming warp: producers, MMA, 8 softmax, 4 output
+      mbar_init(BAR(B_ITE + s), 14 + (PAGED ? 1 : 0) + (C::TURNS ? 1 : 0));  // the warps that read it: producers, MMA, softmax, output
     }
     mbar_init(BAR(B_STAGE), 4);      // stage_full: one arrival per output warp
     mbar_init(BAR(B_STAGE + 1), 1);  // stage_free
     mbar_init(BAR(B_CANCEL), 1);
     mbar_init(BAR(B_NEAR), 1);
-    mbar_init(BAR(B_DRAIN), 1);
+    mbar_init(BAR(B_DRAIN), C::TURNS ? 2 : 1);  // the issuing warps
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -242,58 +242,63 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
 
   if (warp < 4) {
     set_max_registers_dec<C::R_CONTROL>();
-    if (warp == 2) {
-      // ---------------------------------------------------------- scheduler
-      bool ok = true;
-      long long u = blockIdx.x;
-      for (int i = 0; ok && u >= 0; ++i) {
-        const int s = i % C::IRING;
-        if (i >= C::IRING) ok = wait(B_ITE + s, ((i / C::IRING) - 1) & 1);
-        // Not before the block in work is near its end: a CTA with a long one would
-        // hold the next back from those that run dry.
-        if (ok && i > 0) ok = wait(B_NEAR, (i - 1) & 1);
-        if (ok && i > 0) {
-          // the CTA that would begin next gives its index to this one, if any is left
-          if (lane == 0) {
-            mbar_arrive_expect_tx(BAR(B_CANCEL), 16);
-            clc_try_cancel(sbase + C::OFF_CANCEL, BAR(B_CANCEL));
-          }
-          ok = wait(B_CANCEL, (i - 1) & 1);
-          if (ok) u = clc_next_cta(sbase + C::OFF_CANCEL);
-          fence_proxy_async_smem();  // read before the next answer is written there
-          __syncwarp();
-        }
-        if (!ok) break;
-        PromptBlock b;
-        int part = 0;
-        const long long asked = u;
-        if (u >= 0 && !prompt_block(a, u, lane, u == 0, b, part)) u = -1;
-        // for the merge: where the block's rows go (no tokens: there is no such block)
-        if (a.splits > 1 && asked >= 0 && part == 0 && lane == 0)
-          a.blocks[asked / a.splits] = u >= 0 ? make_int4(b.v.q0 + b.tok0, b.v.n - b.tok0, b.head, 0) : make_int4(0, 0, 0, 0);
+    // The i-th block of this CTA, found and published (warp 2): its own, then what
+    // CTAs that have not begun leave to it. u: its index, -1 behind the last one.
+    long long u = blockIdx.x;
+    auto publish = [&](int i) {
+      const int s = i % C::IRING;
+      if (i >= C::IRING && !wait(B_ITE + s, ((i / C::IRING) - 1) & 1)) return false;
+      if (i > 0) {
+        // the CTA that would begin next gives its index to this one, if any is left
         if (lane == 0) {
-          volatile int* d = items + s * C::ITEM_INTS;
-          d[kItQ0] = b.v.q0;
-          d[kItN] = b.v.n;
-          d[kItHead] = b.head;
-          d[kItTok0] = b.tok0;
-          d[kItKt0] = b.kt0;
-          d[kItN0] = u >= 0 ? b.n0 : -1;
-          d[kItN1] = b.n1;
-          d[kItPart] = b.unit * a.splits + part;
-          d[kItK0] = b.v.k0;
-          d[kItSeq] = b.seq;
-          d[kItFirst] = b.v.m - b.v.n + b.tok0 + 1 - b.kt0 * C::BN;
-          d[kItLeft] = b.v.m - b.kt0 * C::BN;
-          mbar_arrive(BAR(B_ITF + s));
+          mbar_arrive_expect_tx(BAR(B_CANCEL), 16);
+          clc_try_cancel(sbase + C::OFF_CANCEL, BAR(B_CANCEL));
         }
+        if (!wait(B_CANCEL, (i - 1) & 1)) return false;
+        u = clc_next_cta(sbase + C::OFF_CANCEL);
+        fence_proxy_async_smem();  // read before the next answer is written there
         __syncwarp();
       }
+      PromptBlock b;
+      int part = 0;
+      const long long asked = u;
+      if (u >= 0 && !prompt_block(a, u, lane, u == 0, b, part)) u = -1;
+      // for the merge: where the block's rows go (no tokens: there is no such block)
+      if (a.splits > 1 && asked >= 0 && part == 0 && lane == 0)
+        a.blocks[asked / a.splits] = u >= 0 ? make_int4(b.v.q0 + b.tok0, b.v.n - b.tok0, b.head, 0) : make_int4(0, 0, 0, 0);
+      if (lane == 0) {
+        volatile int* d = items + s * C::ITEM_INTS;
+        d[kItQ0] = b.v.q0;
+        d[kItN] = b.v.n;
+        d[kItHead] = b.head;
+        d[kItTok0] = b.tok0;
+        d[kItKt0] = b.kt0;
+        d[kItN0] = u >= 0 ? b.n0 : -1;
+        d[kItN1] = b.n1;
+        d[kItPart] = b.unit * a.splits + part;
+        d[kItK0] = b.v.k0;
+        d[kItSeq] = b.seq;
+        d[kItFirst] = b.v.m - b.v.n + b.tok0 + 1 - b.kt0 * C::BN;
+        d[kItLeft] = b.v.m - b.kt0 * C::BN;
+        mbar_arrive(BAR(B_ITF + s));
+      }
+      __syncwarp();
+      return true;
+    };
+    if (!PAGED && warp == 2) {
+      // ---------------------------------------------------------- scheduler
+      bool ok = true;
+      for (int i = 0; ok && u >= 0; ++i) {
+        // Not before the block in work is near its end: a CTA with a long one would
+        // hold the next back from those that run dry.
+        if (i > 0) ok = wait(B_NEAR, (i - 1) & 1);
+        ok = ok && publish(i);
+      }
       if (!ok) *abort_flag = 1;
-    } else if (warp == 0 || (PAGED && warp == 3)) {
+    } else if (warp == 0 || warp == 2) {
       // ---------------------------------------------------------- producers
-      // Of packed tensors warp 0 loads all. Of pages warp 3 loads V: with pages of
-      // 32 keys a tile takes four boxes of each, whose issue by one warp is longer
+      // Of packed tensors warp 0 loads all. Of pages warp 2 loads V, and publishes
+      // the next block behind a block's last load: with pages of 32 keys a tile takes four boxes of each, whose issue by one warp is longer
       // than the tile's softmax (six chats' next turns, d = 64: 106 us, 97 with two
       // warps; of packed tensors two warps are slower, 1160 TFLOP/s to 1197).
       // One lane issues the packed tensors' boxes; a paged cache's boxes have a
@@ -309,7 +314,7 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
         tma_prefetch_desc(map);
         if (!PAGED) tma_prefetch_desc(&a.tmV);
       }
-      bool ok = true;
+      bool ok = of_k || publish(0);
       int g0 = 0, q0_used = 0, q1_used = 0;  // key tiles, and loads of each Q slot, before this block
       int last = -1, last_v = -1;            // last tiles whose loads were issued, by ring position
       for (int i = 0; ok; ++i) {
@@ -385,10 +390,11 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
           if (!ok) break;
           page = next_page;
           row = next_row;
-          if (of_k && j == max(0, n_max - 3) && lane == 0) mbar_arrive(BAR(B_NEAR));
+          if (!PAGED && j == max(0, n_max - 3) && lane == 0) mbar_arrive(BAR(B_NEAR));
         }
         if (!ok) break;
-        if (of_k && n_max == 0 && lane == 0) mbar_arrive(BAR(B_NEAR));
+        if (!PAGED && n_max == 0 && lane == 0) mbar_arrive(BAR(B_NEAR));
+        if (!of_k && !publish(i + 1)) { ok = false; break; }
         g0 += n_max;
         release_item(i);
       }
@@ -398,8 +404,11 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
       if (q1_used > 0) wait(B_QFULL + 1, (q1_used - 1) & 1);
       for (int g = max(0, last - C::STAGES + 1); g <= last; ++g) wait(full + g % C::STAGES, (g / C::STAGES) & 1);
       for (int g = max(0, last_v - C::STAGES + 1); g <= last_v; ++g) wait(B_VFULL + g % C::STAGES, (g / C::STAGES) & 1);
-    } else if (warp == 1) {
+    } else if (warp == 1 || (C::TURNS && warp == 3)) {
       // ---------------------------------------------------------- MMA issuer
+      // A product is issued as the one three before it ends, so the issuing warp
+      // has some hundred cycles between two waits, each of which takes as long.
+      // With S in turns, warp 1 issues the S products and warp 3 the P V.
       const uint32_t leader = elect_one();
       constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
       constexpr uint32_t idesc_o = idesc_bf16_f32(128, D, false, true);
@@ -421,8 +430,7 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
         if (last) mma_commit(BAR(B_QEMPTY + t), leader);
       };
       // P V over a whole tile, and over the first `keys` keys (those that the
-      // tile's last query sees) in steps of 16; `last`: the block's last for this
-      // tile, O is whole behind it
+      // tile's last query sees) in steps of 16
       auto issue_pv = [&](int t, int s, int b, bool acc) {
         const uint64_t vb = dV0 + (uint64_t)((s * C::TILE_BYTES) >> 4);
         const uint32_t dcol = tmem + C::O_COL(t), acol = tmem + C::S_COL(b);
@@ -431,14 +439,13 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
           mma_ts(dcol, acol + kk * 8, vb + (uint64_t)((kk * 2048) >> 4), idesc_o, (acc || kk > 0) ? 1u : 0u, leader);
         if constexpr (C::TURNS) mma_commit(BAR(B_SDONE + b), leader);
       };
-      auto issue_pv_keys = [&](int t, int s, int b, bool acc, int keys, bool last) {
+      auto issue_pv_keys = [&](int t, int s, int b, bool acc, int keys) {
         const uint64_t vb = dV0 + (uint64_t)((s * C::TILE_BYTES) >> 4);
         const uint32_t dcol = tmem + C::O_COL(t), acol = tmem + C::S_COL(b);
 #pragma unroll 1
         for (int kk = 0; kk < C::BN / 16 && 16 * kk < keys; ++kk)
           mma_ts(dcol, acol + kk * 8, vb + (uint64_t)((kk * 2048) >> 4), idesc_o, (acc || kk > 0) ? 1u : 0u, leader);
         if constexpr (C::TURNS) mma_commit(BAR(B_SDONE + b), leader);
-        if (last) mma_commit(BAR(B_ODONE + t), leader);
       };
       // V has landed in slot s with `keys` keys of the sequence: rows behind them
       // that the last step would read become zero.
@@ -457,61 +464,15 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
       bool ok = true;
       if constexpr (C::TURNS) {
         // The (key tile, query tile) pairs in order, tile 0 before tile 1, block
-        // after block; pair number x has S buffer x % 3. S is issued up to three
-        // pairs ahead of P V.
-        int g0 = 0;                  // key tiles before the block
-        int done = 0, issued = 0;    // pairs whose P V, and whose S, has been issued
-        int o0_used = 0, o1_used = 0, q0_used = 0, q1_used = 0;  // blocks with such a tile before, at P V and at S
-        int hi = 0, hg = 0, h0 = 0, h1 = 0, hj = 0, ht = 0;      // the next S: block, its ring position and key tiles, pair
-        int f0 = 0, f1 = 0;                                      // its barrier, by query tile
-        bool known = false;                                      // h0, h1 are those of block hi
-        // The next S, if its operands are there; `must` (no S is under way, it is
-        // this block's): waits for them.
-        auto next_s = [&](bool must) {
-#pragma unroll 1
-          while (true) {
-            if (known) {
-              if (hj < max(h0, h1)) break;
-              hg += max(h0, h1);
-              ++hi;
-              hj = ht = 0;
-              known = false;
-            }
-            const uint32_t pi = (hi / C::IRING) & 1;
-            if (must ? !wait(B_ITF + hi % C::IRING, pi) : !__all_sync(0xffffffffu, mbar_test(BAR(B_ITF + hi % C::IRING), pi)))
-              return !must;
-            h0 = item(hi, kItN0);
-            h1 = item(hi, kItN1);
-            if (h0 < 0) return true;
-            known = true;
-          }
-          if (ht == 0 && hj >= h0) ht = 1;
-          const int s = (hg + hj) % C::STAGES;
-          const uint32_t pk = ((hg + hj) / C::STAGES) & 1, pq = (ht == 0 ? q0_used : q1_used) & 1;
-          if (must) {
-            if (!wait(B_KFULL + s, pk) || (hj == 0 && !wait(B_QFULL + ht, pq))) return false;
-          } else if (!__all_sync(0xffffffffu, mbar_test(BAR(B_KFULL + s), pk))) {
-            return true;
-          } else if (hj == 0 && !__all_sync(0xffffffffu, mbar_test(BAR(B_QFULL + ht), pq))) {
-            return true;
-          }
-          tc_fence_after();
-          issue_s(ht, s, issued % C::SBUF, ht == 0 ? f0 : f1, hj + 1 == (ht == 0 ? h0 : h1));
-          if (ht == 0) f0 = f0 == C::SFULLS - 1 ? 0 : f0 + 1;
-          else f1 = f1 == C::SFULLS - 1 ? 0 : f1 + 1;
-          if (hj == 0) {
-            if (ht == 0) ++q0_used;
-            else ++q1_used;
-          }
-          ++issued;
-          if (ht == 0 && hj < h1) {
-            ht = 1;
-          } else {
-            mma_commit(BAR(B_KEMPTY + s), leader);
-            ++hj;
-            ht = 0;
-          }
-          return true;
+        // after block: pair x has S buffer x % 3.
+        int g0 = 0;                      // key tiles before the block
+        int used0 = 0, used1 = 0;        // blocks with such a tile before it
+        int buf = 0;                     // the next pair's buffer,
+        uint32_t turn = warp == 1 ? 1u : 0u;  // and the parity that it waits for (S of the first round: for nothing)
+        int f0 = 0, f1 = 0;              // the next S's barrier, by query tile
+        auto next_buffer = [&]() {
+          turn ^= buf == C::SBUF - 1;
+          buf = buf == C::SBUF - 1 ? 0 : buf + 1;
         };
 #pragma unroll 1
         for (int i = 0; ok; ++i) {
@@ -519,125 +480,99 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
           if (!ok) break;
           const int n0 = item(i, kItN0), n1 = item(i, kItN1), n_max = max(n0, n1);
           if (n0 < 0) break;
-          if (hi < i) {
-            hi = i;
-            hg = g0;
-            hj = ht = 0;
-            known = false;
-          }
-          const int first = item(i, kItFirst), left = item(i, kItLeft);
-          // A query tile's accumulator has left tensor memory: asked before its first P V.
-          auto o_free = [&](int t) {
-            int& used = t == 0 ? o0_used : o1_used;
-            ++used;
-            return used == 1 || wait(B_OFREE + t, used & 1);
-          };
-          const int n_lean = min(n0, n1) - 2;
-          int j = 0;
-          if (n_lean > 0) {
+          if (warp == 1) {
+            if (n0 > 0) ok = wait(B_QFULL, used0 & 1);
+            if (n1 > 0) ok = ok && wait(B_QFULL + 1, used1 & 1);
+            int j = 0;
+            // whole tiles of both, in as few instructions as can be: with the
+            // softmax warps beside it each takes this warp ten cycles
 #pragma unroll 1
-            while (ok && issued - done < C::SBUF) ok = next_s(true);
-            ok = ok && o_free(0) && o_free(1);
-          }
-#pragma unroll 1
-          while (ok && j < n_max) {
-            // Tiles that neither query tile ends with, S three pairs ahead: kept
-            // short, as below.
-            if (j < n_lean && hi == i && hj == j + 1 && ht == 1) {
-              int b = done % C::SBUF;
-              uint32_t pb = (uint32_t)(done / C::SBUF) & 1u;
-              const int from = j;
-#pragma unroll 1
-              for (; j < n_lean; ++j) {
-                const int g = g0 + j, s = g % C::STAGES, s1 = (g + 1) % C::STAGES, s2 = (g + 2) % C::STAGES;
-                ok = wait2(B_VFULL + s, (g / C::STAGES) & 1, B_PFULL + b, pb);
-                if (!ok) break;
-                tc_fence_after();
-                issue_pv(0, s, b, j > 0);
-                issue_s(1, s1, b, f1, false);
-                f1 = f1 == C::SFULLS - 1 ? 0 : f1 + 1;
-                mma_commit(BAR(B_KEMPTY + s1), leader);
-                pb ^= b == C::SBUF - 1;
-                b = b == C::SBUF - 1 ? 0 : b + 1;
-                ok = wait2(B_KFULL + s2, ((g + 2) / C::STAGES) & 1, B_PFULL + b, pb);
-                if (!ok) break;
-                tc_fence_after();
-                issue_pv(1, s, b, j > 0);
-                issue_s(0, s2, b, f0, j + 3 == n0);
-                f0 = f0 == C::SFULLS - 1 ? 0 : f0 + 1;
-                mma_commit(BAR(B_VEMPTY + s), leader);
-                pb ^= b == C::SBUF - 1;
-                b = b == C::SBUF - 1 ? 0 : b + 1;
-              }
-              done += 2 * (j - from);
-              issued += 2 * (j - from);
-              hj = j + 1;
-              continue;
-            }
-            // The same where there is one query tile only (the last of a sequence).
-            if (j > 0 && j < n_max - 4 && min(n0, n1) <= j && hi == i && hj == j + 3) {
-              const int t = n0 > n1 ? 0 : 1, from = j;
-              int b = done % C::SBUF, f = t == 0 ? f0 : f1;
-              uint32_t pb = (uint32_t)(done / C::SBUF) & 1u;
-#pragma unroll 1
-              for (; j < n_max - 4; ++j) {
-                const int g = g0 + j, s = g % C::STAGES, s3 = (g + 3) % C::STAGES;
-                ok = wait2(B_VFULL + s, (g / C::STAGES) & 1, B_PFULL + b, pb);
-                if (!ok) break;
-                tc_fence_after();
-                issue_pv(t, s, b, true);
-                mma_commit(BAR(B_VEMPTY + s), leader);
-                ok = wait(B_KFULL + s3, ((g + 3) / C::STAGES) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                issue_s(t, s3, b, f, false);
-                mma_commit(BAR(B_KEMPTY + s3), leader);
-                f = f == C::SFULLS - 1 ? 0 : f + 1;
-                pb ^= b == C::SBUF - 1;
-                b = b == C::SBUF - 1 ? 0 : b + 1;
-              }
-              if (t == 0) f0 = f;
-              else f1 = f;
-              done += j - from;
-              issued += j - from;
-              hj = j + 3;
-              continue;
-            }
-            const int g = g0 + j, s = g % C::STAGES;
-            bool v_here = false;
-#pragma unroll 1
-            for (int t = 0; t < C::QT; ++t) {
-              const int nt = t == 0 ? n0 : n1;
-              if (j >= nt) continue;
-              if (issued == done && !next_s(true)) { ok = false; break; }
-#pragma unroll 1
-              while (issued - done < C::SBUF) {
-                const int before = issued;
-                next_s(false);
-                if (issued == before) break;
-              }
-              if (j == 0 && n_lean <= 0 && !o_free(t)) { ok = false; break; }
-              const int b = done % C::SBUF;
-              const uint32_t pb = (uint32_t)(done / C::SBUF) & 1u;
-              if (!v_here) {
-                ok = wait2(B_VFULL + s, (g / C::STAGES) & 1, B_PFULL + b, pb);
-                if (!ok) break;
-                clean_v(s, left - j * C::BN);
-                v_here = true;
-              } else if (!wait(B_PFULL + b, pb)) {
-                ok = false;
-                break;
-              }
+            for (const int n = min(n0, n1) - 1; ok && j < n; ++j) {
+              const int g = g0 + j, s = g % C::STAGES;
+              ok = wait2(B_KFULL + s, (g / C::STAGES) & 1, B_SDONE + buf, turn);
+              if (!ok) break;
               tc_fence_after();
-              issue_pv_keys(t, s, b, j > 0, min(first - 1 + (t + 1) * TP, left) - j * C::BN, j + 1 == nt);
-              ++done;
+              issue_s(0, s, buf, f0, false);
+              f0 = f0 == C::SFULLS - 1 ? 0 : f0 + 1;
+              next_buffer();
+              ok = wait(B_SDONE + buf, turn);
+              if (!ok) break;
+              tc_fence_after();
+              issue_s(1, s, buf, f1, false);
+              mma_commit(BAR(B_KEMPTY + s), leader);
+              f1 = f1 == C::SFULLS - 1 ? 0 : f1 + 1;
+              next_buffer();
             }
-            if (!ok) break;
-            mma_commit(BAR(B_VEMPTY + s), leader);
-            ++j;
-            if (j < n_max && issued - done < C::SBUF) next_s(false);
+#pragma unroll 1
+            for (; ok && j < n_max; ++j) {
+              const int g = g0 + j, s = g % C::STAGES;
+              const uint32_t pk = (g / C::STAGES) & 1;
+              if (j < n0) {
+                ok = wait2(B_KFULL + s, pk, B_SDONE + buf, turn);
+                if (!ok) break;
+                tc_fence_after();
+                issue_s(0, s, buf, f0, j + 1 == n0);
+                f0 = f0 == C::SFULLS - 1 ? 0 : f0 + 1;
+                next_buffer();
+              }
+              if (j < n1) {
+                ok = wait2(B_KFULL + s, pk, B_SDONE + buf, turn);
+                if (!ok) break;
+                tc_fence_after();
+                issue_s(1, s, buf, f1, j + 1 == n1);
+                f1 = f1 == C::SFULLS - 1 ? 0 : f1 + 1;
+                next_buffer();
+              }
+              mma_commit(BAR(B_KEMPTY + s), leader);
+            }
+          } else {
+            const int first = item(i, kItFirst) - 1, left = item(i, kItLeft);
+            // the accumulators have left tensor memory
+            if (n0 > 0 && used0 > 0) ok = wait(B_OFREE, (used0 - 1) & 1);
+            if (n1 > 0 && used1 > 0) ok = ok && wait(B_OFREE + 1, (used1 - 1) & 1);
+            int j = 0;
+#pragma unroll 1
+            while (ok && j < n_max) {
+              const int g = g0 + j, s = g % C::STAGES;
+              const uint32_t pv = (g / C::STAGES) & 1;
+              if (j > 0 && j + 1 < min(n0, n1)) {  // as above
+                ok = wait2(B_VFULL + s, pv, B_PFULL + buf, turn);
+                if (!ok) break;
+                tc_fence_after();
+                issue_pv(0, s, buf, true);
+                next_buffer();
+                ok = wait(B_PFULL + buf, turn);
+                if (!ok) break;
+                tc_fence_after();
+                issue_pv(1, s, buf, true);
+                mma_commit(BAR(B_VEMPTY + s), leader);
+                next_buffer();
+                ++j;
+                continue;
+              }
+              bool clean = false;
+#pragma unroll 1
+              for (int t = 0; t < C::QT; ++t) {
+                const int nt = t == 0 ? n0 : n1;
+                if (j >= nt) continue;
+                ok = wait2(B_VFULL + s, pv, B_PFULL + buf, turn);
+                if (!ok) break;
+                if (!clean) clean_v(s, left - j * C::BN);
+                clean = true;
+                tc_fence_after();
+                const int keys = min(first + (t + 1) * TP, left) - j * C::BN;
+                if (keys >= C::BN) issue_pv(t, s, buf, j > 0);
+                else issue_pv_keys(t, s, buf, j > 0, keys);
+                if (j + 1 == nt) mma_commit(BAR(B_ODONE + t), leader);
+                next_buffer();
+              }
+              mma_commit(BAR(B_VEMPTY + s), leader);
+              ++j;
+            }
           }
           if (!ok) break;
+          used0 += n0 > 0;
+          used1 += n1 > 0;
           g0 += n_max;
           release_item(i);
         }
@@ -746,7 +681,8 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
                 // P overwrites S: P_j V_j must be issued before S_{j+1}
                 if (!need_v() || !wait(B_PFULL + t, pt) || !o_free(t, j)) { ok = false; break; }
                 tc_fence_after();
-                issue_pv_keys(t, s, t, j > 0, keys, !more);
+                issue_pv_keys(t, s, t, j > 0, keys);
+                if (!more) mma_commit(BAR(B_ODONE + t), leader);
                 if (more && !next_s(t)) { ok = false; break; }
               }
               if (j + 1 == n_max) {
