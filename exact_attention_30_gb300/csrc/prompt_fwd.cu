@@ -38,14 +38,16 @@
 //
 // Bound, per pair of query tiles and 128 keys and SM, in cycles: products 2048
 // (d = 128) or 1024 (d = 64), exponentials 1024. Measured on long prompts: 2640
-// (1860 TFLOP/s) and 2170 (1190). What is between is the chain from scores to
-// weights to the next product, whose waits cost a hundred cycles each even when
-// they are over: with d = 128 tensor memory is full with two tiles' S and O, so a
-// tile's next S can only follow its P V; with d = 64 three S buffers in turn take
-// that out of the chain (1000 TFLOP/s without), and what is left is the time in
-// which the issuing warp asks and waits. Times in a batch: 16 prompts of 128 to 7821
-// tokens (32 heads on 8, d = 128) 980 us, one of 32768 tokens 5.1 ms, the next
-// turns of six chats (d = 64, pages of 32 keys) 90 us, one of 37 tokens 12.5 us.
+// (1860 TFLOP/s) and 1950 (1260). What is between is the chain from scores to
+// weights to the next product. Products are issued hardly ahead of their execution
+// (three at most), an answer from a barrier takes a hundred cycles even when it is
+// over, and beside two softmax warps an instruction takes ten. With d = 128 tensor
+// memory is full with two tiles' S and O, so a tile's next S can only follow its
+// P V; with d = 64 three S buffers in turn take that out of the chain (1000 TFLOP/s
+// without, 1190 with), and S and P V are issued by a warp each (1200, 1260 with
+// loops of few instructions). Times in a batch: 16 prompts of 128 to 7821 tokens (32
+// heads on 8, d = 128) 980 us, one of 32768 tokens 5.1 ms, the next turns of six
+// chats (d = 64, pages of 32 keys) 83 us, one of 37 tokens 12.5 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -105,10 +107,11 @@ __device__ __forceinline__ bool prompt_block(const PromptFwdArgs& a, long long u
   return true;
 }
 
-// Warps 0-3: producer, MMA issuer, scheduler, producer of V from pages; 4-7 and 8-11: softmax of
-// query tiles 0 and 1; 12-15: output. Shared memory: that of the two-tile
-// forward, a tile of O on its way out, the rows' sums on their way to the output
-// warps and a ring of published blocks.
+// Warps 0: producer (of pages: Q and K), 1: MMA issuer (d = 64: the S products),
+// 2: scheduler (and of pages the producer of V), 3: d = 64: the P V products; 4-7
+// and 8-11: softmax of query tiles 0 and 1; 12-15: output. Shared memory: that of
+// the two-tile forward, a tile of O on its way out, the rows' sums on their way to
+// the output warps and a ring of published blocks.
 template <int D>
 struct PromptCfg : FwdCfg<D> {
   using F = FwdCfg<D>;
@@ -298,9 +301,10 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
     } else if (warp == 0 || warp == 2) {
       // ---------------------------------------------------------- producers
       // Of packed tensors warp 0 loads all. Of pages warp 2 loads V, and publishes
-      // the next block behind a block's last load: with pages of 32 keys a tile takes four boxes of each, whose issue by one warp is longer
-      // than the tile's softmax (six chats' next turns, d = 64: 106 us, 97 with two
-      // warps; of packed tensors two warps are slower, 1160 TFLOP/s to 1197).
+      // the next block behind a block's last load: with pages of 32 keys a tile
+      // takes four boxes of each, whose issue by one warp is longer than the tile's
+      // softmax (six chats' next turns, d = 64: 106 us, 97 with two warps; of packed
+      // tensors two warps are slower, 1160 TFLOP/s to 1197).
       // One lane issues the packed tensors' boxes; a paged cache's boxes have a
       // lane each (box `box` of the 64-column chunk `chunk` of a tile).
       const int nbox = PAGED ? C::BN / a.box_rows : 1;
