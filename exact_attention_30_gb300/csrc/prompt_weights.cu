@@ -16,21 +16,23 @@
 // buffered in tensor memory for each key tile (four buffers of 128 columns).
 //
 // Products and exponentials need 1024 cycles a unit and query tile each (8192
-// FLOP and 32 exponentials per cycle and SM). Measured: 1950 (8 prompts of 361 to
-// 6925 tokens, 32 heads on 8: 492 us; the last 64 tokens of six of 5627 to 18982:
-// 47 us, of which most is the beginning and end of units of two query tiles). The
-// products alone take 1530 and the weights' warps alone 1850, their waits and
-// loads 950 of it: each wait takes a hundred cycles even when it is over, so
-// statistics and scores are awaited at once (503 us one after the other, 492 so). Other
-// ways that were slower: keys as first operands in tensor memory, which leaves
-// three S buffers for both tiles (2400); four keys to a thread, by loads of 16
-// lanes, which need a quarter of the statistics (2150); loads of 16 columns (2040).
+// FLOP and 32 exponentials per cycle and SM). Measured: 1790 (8 prompts of 361 to
+// 6925 tokens, 32 heads on 8: 452 us; the last 64 tokens of six of 5627 to 18982:
+// 45 us, of which most is the beginning and end of units of two query tiles). The
+// products alone took 1530, the weights' warps issue 300 instructions for 32 keys
+// and 64 queries where 140 do the sum, each wait takes a hundred cycles even when
+// it is over. So a warp takes whole query tiles in turn with its twin (halves of
+// each: 493 us), and statistics and scores are awaited at once (503 us one after
+// the other). Other ways that were slower: keys as first operands in tensor memory,
+// which leaves three S buffers for both tiles (2400); four keys to a thread, by
+// loads of 16 lanes, which need a quarter of the statistics (2150); loads of 16
+// columns (2040).
 //
-// Sums: 64 weights of eight query tiles in each of eight fp32 accumulators, and
+// Sums: 128 weights of four query tiles in each of eight fp32 accumulators, and
 // their sums with a compensation term (Kahan's), in a fixed order.
 //
 // Warps 0: producer, 1: MMA issuer, 2: scheduler, 3: statistics, 4-19: weights,
-// four warps to the first and to the second 64 queries of each key tile (with
+// four warps to the even and to the odd query tiles of each key tile (with
 // eight warps, two to a scheduler, waits and latencies were not covered: 8192
 // tokens, 32 heads 398 us). Units are listed longest first and taken over
 // from CTAs that have not begun, as in prompt_fwd.cu. Every wait is bounded.
@@ -158,11 +160,11 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
       mbar_init(BAR(B_QFULL + s), 1);
       mbar_init(BAR(B_QEMPTY + s), 1);
       mbar_init(BAR(B_STFULL + s), 1);
-      mbar_init(BAR(B_STEMPTY + s), 16);  // one arrival per weights warp
+      mbar_init(BAR(B_STEMPTY + s), 8);  // one arrival per weights warp of the tile
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(BAR(B_SFULL + i), 1);
-      mbar_init(BAR(B_SFREE + i), 8);
+      mbar_init(BAR(B_SFREE + i), 4);
       mbar_init(BAR(B_PART + i), 4);  // part_full[2], part_free[2]
     }
     for (int s = 0; s < C::IRING; ++s) {
@@ -308,7 +310,9 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
     const uint32_t leader = elect_one();
     constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
     const uint64_t dK0 = sdesc_sw128(sbase + C::OFF_K, 16, 1024), dQ0 = sdesc_sw128(sbase + C::OFF_Q, 16, 1024);
-    int g0 = 0, c0 = 0, c1 = 0;  // query tiles, and S tiles of each key tile, before this unit
+    // query tile g has S buffer g % 2 of each key tile
+    int g0 = 0;              // query tiles before this unit
+    int used0 = 0, used1 = 0;  // S tiles of key tile 1 so far, by buffer (key tile 0 has one for each query tile)
     for (int i = 0; ok; ++i) {
       if (!get_item(i)) { ok = false; break; }
       const int tiles = item(i, kWTiles), skip1 = item(i, kWSkip1);
@@ -316,14 +320,22 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
       if (!wait(B_KFULL + (i & 1), (i >> 1) & 1)) { ok = false; break; }
 #pragma unroll 1
       for (int j = 0; j < tiles; ++j) {
-        if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
+        const int gone = *abort_flag;
         const int g = g0 + j, s = g % C::QS;
-        if (!wait(B_QFULL + s, (g / C::QS) & 1)) { ok = false; break; }
+        // (S of the first two query tiles: a phase before the barrier's first, which is over)
+        ok = wait_warp2(BAR(B_QFULL + s), (g / C::QS) & 1, BAR(B_SFREE + (g & 1)), ((g >> 1) - 1) & 1, a.status,
+                        a.wait_limit_ns) && !__any_sync(0xffffffffu, gone != 0);
+        if (!ok) break;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (t == 1 && j < skip1) continue;
-          const int c = t == 0 ? c0 + j : c1 + j - skip1, b = c & 1;
-          if (c >= 2 && !wait(B_SFREE + 2 * t + b, ((c >> 1) - 1) & 1)) { ok = false; break; }
+          const int b = g & 1;
+          if (t == 1) {
+            const int n = b ? used1 : used0;  // the buffer's S tiles before this one
+            if (!wait(B_SFREE + 2 + b, (n - 1) & 1)) { ok = false; break; }
+            if (b) ++used1;
+            else ++used0;
+          }
           tc_fence_after();
           const uint64_t ka = dK0 + (uint64_t)(((2 * (i & 1) + t) * C::TILE) >> 4);
           const uint64_t qb = dQ0 + (uint64_t)((s * C::TILE) >> 4);
@@ -341,8 +353,6 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
       if (!ok) break;
       mma_commit(BAR(B_KEMPTY + (i & 1)), leader);
       g0 += tiles;
-      c0 += tiles;
-      c1 += tiles - skip1;
       release_item(i);
     }
     if (!ok) *abort_flag = 1;
@@ -405,25 +415,27 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
     }
   } else {
     // ---------------------------------------------------------- weights
-    const int t = (warp >> 2 & 1) ^ 1, half = warp >= 12, wq = warp & 3;  // key tile, columns 64 half ..
+    const int t = (warp >> 2 & 1) ^ 1, odd = warp >= 12, wq = warp & 3;  // key tile, query tiles
     const int row = wq * 32 + lane;                                       // key of the tile
-    const uint32_t lane_addr = tmem + ((uint32_t)(wq * 32) << 16) + C::S_COL(t, 0) + 64u * half;
+    const uint32_t s_addr = tmem + ((uint32_t)(wq * 32) << 16) + C::S_COL(t, odd);
     const uint64_t c22 = f2_pack(a.scale_log2, a.scale_log2);
-    // The loop over query tiles is bound by the instructions it issues: 140 for
-    // 64 columns of 32 keys, and what comes on top (317 in all once: 521 us for 8
-    // prompts of 361 to 6925 tokens, 503 now). So ring positions are counted, not
-    // divided out, masks are rare, and sums are joined only every eighth tile.
-    uint32_t slot = 0, slot_phase = 0;  // ring position of the next query tile
-    int c = 0;                          // S tiles of this key tile so far
-    const uint32_t bar_stat = BAR(B_STFULL), bar_s = BAR(B_SFULL + 2 * t);
+    // The loop over query tiles is bound by the instructions it issues: 280 for
+    // 128 columns of 32 keys, and what comes on top. So ring positions are counted,
+    // not divided out, masks are rare, and sums are joined only every fourth tile.
+    uint32_t slot = odd, slot_phase = 0;  // ring position of this warp's next query tile
+    int g0 = 0;                           // query tiles before the unit
+    int c = 0;                            // S tiles of this warp so far
+    const uint32_t bar_stat = BAR(B_STFULL), bar_s = BAR(B_SFULL + 2 * t + odd);
     for (int i = 0; ok; ++i) {
       if (!get_item(i)) { ok = false; break; }
       const int tiles = item(i, kWTiles);
       if (tiles < 0) break;
       const int skip = t == 0 ? 0 : item(i, kWSkip1);
       // the token (from the unit's first tile's on) whose diagonal is the key tile's first key
-      int first = item(i, kWDiag) + 128 * t;
-      int tokens = item(i, kWTokens);  // from the next query tile on
+      const int j0 = (g0 & 1) ^ odd;  // this warp's first query tile of the unit
+      int first = item(i, kWDiag) + 128 * t - j0 * TP;
+      int tokens = item(i, kWTokens) - j0 * TP;  // from the next query tile on
+      g0 += tiles;
       uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
       float total = 0.f, lost = 0.f;
       auto join = [&]() {
@@ -435,31 +447,26 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
         total = z;
       };
 #pragma unroll 1
-      for (int j = 0; j < tiles; ++j) {
+      for (int j = j0; j < tiles; j += 2) {
         if (j < skip) {
           if (!wait_warp(bar_stat + 8 * slot, slot_phase, a.status, a.wait_limit_ns)) { ok = false; break; }
         } else {
-          const uint32_t b = c & 1;
-          if (!wait_warp2(bar_stat + 8 * slot, slot_phase, bar_s + 8 * b, (c >> 1) & 1, a.status, a.wait_limit_ns)) {
-            ok = false;
-            break;
-          }
+          if (!wait_warp2(bar_stat + 8 * slot, slot_phase, bar_s, c & 1, a.status, a.wait_limit_ns)) { ok = false; break; }
           tc_fence_after();
-          const float* nl = reinterpret_cast<const float*>(smem + C::OFF_STAT + slot * 512) + 64 * half;
-          const uint32_t s_addr = lane_addr + 128u * b;
+          const float* nl = reinterpret_cast<const float*>(smem + C::OFF_STAT + slot * 512);
           if (first + 127 > 0 || tokens * a.G < 128) {
             // Columns that a key's weight has no part in (before its diagonal,
             // behind the sequence's end: they may hold anything) become -inf
             // where they stand: a few tiles to a unit, and no mask below.
             const int lo = a.G * max(first + row, 0), hi = a.G * min(tokens, 128);
 #pragma unroll 1
-            for (int q = 0; q < 2; ++q) {
+            for (int q = 0; q < 4; ++q) {
               uint32_t r[32];
               tmem_ld32(s_addr + 32 * q, r);
               tmem_ld_wait();
 #pragma unroll
               for (int u = 0; u < 32; ++u)
-                r[u] = 64 * half + 32 * q + u < lo || 64 * half + 32 * q + u >= hi ? __float_as_uint(-INFINITY) : r[u];
+                r[u] = 32 * q + u < lo || 32 * q + u >= hi ? __float_as_uint(-INFINITY) : r[u];
               tmem_st32(s_addr + 32 * q, r);
             }
             tmem_st_wait();
@@ -474,7 +481,7 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
               sum[2 * (k & 1) + 1] = fadd2(sum[2 * (k & 1) + 1], f2_pack(ex2_approx(y.x), ex2_approx(y.y)));
             }
           };
-          // the second load is under way while the first is exponentiated (both
+          // each load is under way while the one before is exponentiated (both
           // awaited first: 611 us instead of 521 for 8 prompts of 361 to 6925 tokens)
           uint32_t ra[32], rb[32];
           tmem_ld32(s_addr, ra);
@@ -482,28 +489,35 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
           tmem_ld32(s_addr + 32, rb);
           add(ra, 0);
           tmem_ld_wait_dep(rb);
+          tmem_ld32(s_addr + 64, ra);
+          add(rb, 1);
+          tmem_ld_wait_dep(ra);
+          tmem_ld32(s_addr + 96, rb);
+          add(ra, 2);
+          tmem_ld_wait_dep(rb);
           // all of S is in registers: its buffer takes the tile after next
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(BAR(B_SFREE + 2 * t) + 8 * b);
-          add(rb, 1);
+          if (lane == 0) mbar_arrive(BAR(B_SFREE + 2 * t + odd));
+          add(rb, 3);
           ++c;
-          if ((c & 7) == 0) join();
+          if ((c & 3) == 0) join();
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(B_STEMPTY) + 8 * slot);
-        first -= TP;
-        tokens -= TP;
-        if (++slot == C::QS) {
-          slot = 0;
+        first -= 2 * TP;
+        tokens -= 2 * TP;
+        slot += 2;
+        if (slot >= C::QS) {
+          slot -= C::QS;
           slot_phase ^= 1u;
         }
       }
       if (!ok) break;
       join();
-      // the second half's sums go to the first's warps
+      // the odd query tiles' sums go to the even ones' warps
       volatile float* part = reinterpret_cast<float*>(smem + C::OFF_PART + t * 512) + row;
-      if (half) {
+      if (odd) {
         if (i > 0 && !wait(B_PART + 2 + t, (i - 1) & 1)) { ok = false; break; }
         *part = total;
         __syncwarp();
