@@ -309,7 +309,8 @@ struct PromptFwdArgs {
   FastDiv g_div;             // by G
   int heads_per_group;       // K/V heads whose blocks are listed together (their keys stay in L2)
   long long max_blocks;      // at least as many blocks of 2 * tile_tokens tokens as all sequences have
-  int splits;                // key ranges per block
+  int splits;                // key ranges per block, at most
+  int slots;                 // CTAs that the GPU runs at once
   float* Opart;              // splits > 1: fp32 [Hkv * max_blocks][splits][256][d], normalised
   float* Lpart;              // and base-2 log-sum-exps
   int4* blocks;              // and of each block: first packed token, tokens from there on, K/V head
@@ -318,8 +319,21 @@ struct PromptFwdArgs {
   unsigned long long wait_limit_ns;
 };
 cudaError_t launch_prompt_fwd(const PromptFwdArgs& a, int d, cudaStream_t st);
-// Key ranges per block for `units` blocks (of all heads) that see up to
-// key_tiles 128-key tiles, on a GPU that runs `slots` CTAs at once.
+// What s key ranges per block cost, in key tiles' time, for `units` blocks (of all
+// heads) that see up to key_tiles 128-key tiles, on a GPU that runs `slots` CTAs at
+// once: the longest range, or the blocks' work shared out evenly, whichever is
+// more. Blocks differ (a prompt's first see few keys, sequences are ragged): on
+// average they see half of key_tiles. A range begins and ends in about three
+// tiles' time, the partial results' second kernel takes about four's.
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline float prompt_split_cost(float units, int key_tiles, int slots, int s) {
+  const float share = units / (float)slots * (0.5f * (float)key_tiles + 3.f * (float)s);
+  const float longest = (float)((key_tiles + s - 1) / s + 3);
+  return (share > longest ? share : longest) + (s > 1 ? 4.f : 0.f);
+}
+// The cheapest number of ranges.
 int plan_prompt_splits(long long units, int key_tiles, int slots);
 // Rows of a TMA box of a page: a power of two that divides page_size (a multiple of 8), at most `most`.
 inline int pool_box_rows(int page_size, int most) {

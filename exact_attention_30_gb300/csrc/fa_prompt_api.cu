@@ -139,6 +139,7 @@ fa_status fwd_launch(PromptFwdArgs& a, const void* Q, long long q_stride, void* 
   const FwdPlan p = fwd_plan(B, G, a.Hkv, total_q, max_q, a.seqs.max_k, d);
   a.max_blocks = p.max_blocks;
   a.splits = workspace ? p.splits : 1;
+  a.slots = fwd_slots();
   if (a.max_blocks * a.Hkv * 256 * a.splits > 0x7fffffffll) return FA_ERR_UNSUPPORTED;
   if (a.splits > 1) {
     if (workspace_bytes < p.total) return FA_ERR_INVALID_ARG;
@@ -196,16 +197,10 @@ namespace fa {
 
 int plan_prompt_splits(long long units, int key_tiles, int slots) {
   if (units < 1 || key_tiles < 1 || slots < 1) return 1;
-  // The longest range, or the blocks' work shared out evenly, whichever is
-  // more. Blocks differ (a prompt's first see few keys, sequences are ragged):
-  // on average they see half of key_tiles. A range begins and ends in about
-  // three tiles' time, the partial results' second kernel takes about four's.
   float best = 0.f;
   int splits = 1;
   for (int s = 1; s <= key_tiles && s <= kPrefixMaxSplits; ++s) {
-    const float share = (float)units / (float)slots * (0.5f * (float)key_tiles + 3.f * (float)s);
-    const float longest = (float)((key_tiles + s - 1) / s + 3);
-    const float cost = std::max(share, longest) + (s > 1 ? 4.f : 0.f);
+    const float cost = prompt_split_cost((float)units, key_tiles, slots, s);
     if (s == 1 || cost < best) {
       best = cost;
       splits = s;

@@ -69,6 +69,7 @@ struct PromptBlock {
   int kt0;         // first key tile of this part
   int n0, n1;      // key tiles of the query tiles 0 and 1, from kt0 on
   int unit;        // index of the block in the list
+  int parts;       // key ranges of each block
 };
 
 // Whole warp: the block and key range of CTA `u`; false past the last one.
@@ -81,8 +82,27 @@ __device__ __forceinline__ bool prompt_block(const PromptFwdArgs& a, long long u
   int top;
   const int total = count_blocks(a.seqs.B, lane, span, first, top);
   if (report && bad) report_status(a.status, kStatusBadSeqlens);
-  part = (int)(u % a.splits);
-  const long long w = u / a.splits;
+  // The host's plan may come from a table far wider than its sequences, of fewer
+  // blocks than there can be: the same cost decides here again, for those that
+  // there are, lane by lane (60 tokens after 840 in a table of 131072 keys: 37 us
+  // by the host's plan, 23 so).
+  k.parts = 1;
+  if (a.splits > 1) {
+    const int tiles = (int)min(((long long)(top + 1) * per + 127) / 128, 1ll << 24);
+    const int most_parts = min(a.splits, max(tiles, 1));
+    unsigned best = 0xffffffffu;  // costs are positive: their bits are in their order
+    for (int s = lane + 1; s <= most_parts; s += 32) {
+      const unsigned cost = __float_as_uint(prompt_split_cost((float)total * (float)a.Hkv, tiles, a.slots, s));
+      if (cost < best) {
+        best = cost;
+        k.parts = s;
+      }
+    }
+    const unsigned least = __reduce_min_sync(0xffffffffu, best);
+    k.parts = (int)__reduce_min_sync(0xffffffffu, best == least ? (unsigned)k.parts : 0xffffffffu);
+  }
+  part = (int)(u % k.parts);
+  const long long w = u / k.parts;
   if (w >= (long long)total * a.Hkv) return false;
   const int hpg = a.heads_per_group;
   const int group = (int)(w / ((long long)total * hpg));
@@ -100,8 +120,8 @@ __device__ __forceinline__ bool prompt_block(const PromptFwdArgs& a, long long u
     return t0 < k.v.n && seen > 0 ? (seen + 127) / 128 : 0;
   };
   const int n0 = key_tiles(k.tok0), n1 = key_tiles(k.tok0 + a.tile_tokens), most = max(n0, n1);
-  k.kt0 = (int)((long long)part * most / a.splits);
-  const int end = (int)((long long)(part + 1) * most / a.splits);
+  k.kt0 = (int)((long long)part * most / k.parts);
+  const int end = (int)((long long)(part + 1) * most / k.parts);
   k.n0 = max(0, min(n0, end) - k.kt0);
   k.n1 = max(0, min(n1, end) - k.kt0);
   return true;
@@ -266,9 +286,10 @@ __global__ void __launch_bounds__(512, 1) prompt_fwd_kernel(const __grid_constan
       int part = 0;
       const long long asked = u;
       if (u >= 0 && !prompt_block(a, u, lane, u == 0, b, part)) u = -1;
-      // for the merge: where the block's rows go (no tokens: there is no such block)
-      if (a.splits > 1 && asked >= 0 && part == 0 && lane == 0)
-        a.blocks[asked / a.splits] = u >= 0 ? make_int4(b.v.q0 + b.tok0, b.v.n - b.tok0, b.head, 0) : make_int4(0, 0, 0, 0);
+      // for the merge: where the block's rows go and their ranges (no tokens:
+      // there is no such block; the CTAs are at least as many as the blocks there can be)
+      if (a.splits > 1 && asked >= 0 && part == 0 && lane == 0 && asked / b.parts < a.max_blocks * a.Hkv)
+        a.blocks[asked / b.parts] = u >= 0 ? make_int4(b.v.q0 + b.tok0, b.v.n - b.tok0, b.head, b.parts) : make_int4(0, 0, 0, 0);
       if (lane == 0) {
         volatile int* d = items + s * C::ITEM_INTS;
         d[kItQ0] = b.v.q0;
@@ -1012,11 +1033,11 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const __grid_constant
   constexpr int ROWS = 8, LPR = D / 4, RPW = 32 / LPR, STEPS = ROWS / RPW;  // rows of a warp, lanes to a row, rows at once
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
   const int unit = (int)(blockIdx.x >> 2);
-  const int4 k = a.blocks[unit];  // first packed token, tokens of the sequence from there on, K/V head
+  const int4 k = a.blocks[unit];  // first packed token, tokens of the sequence from there on, K/V head, key ranges
   const int br0 = (int)(blockIdx.x & 3) * 64 + warp * ROWS;  // rows of the block, of one query tile
   const int t = br0 >> 7, row0 = br0 & 127;
   // what a launch that gave up left unwritten is not followed
-  if (k.x < 0 || k.y > a.seqs.total_q - k.x || (unsigned)k.z >= (unsigned)a.Hkv) return;
+  if (k.x < 0 || k.y > a.seqs.total_q - k.x || (unsigned)k.z >= (unsigned)a.Hkv || k.w > a.splits) return;
   // the rows that there are begin the eight: rows of a sequence's end lack the last ones
   const int live = min(ROWS, min(a.tile_tokens, k.y - t * a.tile_tokens) * a.G - row0);
   if (live <= 0) return;
@@ -1031,11 +1052,11 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const __grid_constant
     sum[i] = 0.f;
     acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  for (int p = 0; p < a.splits; ++p) {
+  for (int p = 0; p < k.w; ++p) {
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) top[i] = fmaxf(top[i], lpart[p * 256 + i * RPW]);  // rows past `live`: any value
   }
-  for (int p = 0; p < a.splits; ++p) {
+  for (int p = 0; p < k.w; ++p) {
     float lp[STEPS];
     float4 x[STEPS];
 #pragma unroll

@@ -175,6 +175,21 @@ def test_paged_key_ranges(n, m, d):
     check_forward(c, o, lse, 1 / math.sqrt(d))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_paged_wide_tables(d):
+    """Tables far wider than the sequences: the ranges follow what there is, and nothing is read that no range wrote."""
+    cache = Cache((900, 0, 129, 2500), 4, 64, d, seed=d, width_extra=2000)
+    c = Paged((60, 0, 129, 3), cache, 16, seed=d, pad=(2, 3))
+    most = cache.tables.shape[1] * 64
+    n = fa.fa_prompt_fwd_workspace_bytes(4, 16, 4, c.total, 129, most, d)
+    assert n > 0
+    ws = torch.full((n + (1 << 20),), 255, dtype=torch.uint8, device="cuda")
+    o, lse = fa.fa_prompt_paged(c.q, cache.k, cache.v, cache.tables, cache.seq_lens, c.cu_q, 129, workspace=ws)
+    assert fa.fa_check_device_status() == fa.FA_OK
+    check_forward(c, o, lse, 1 / math.sqrt(d))
+    assert (ws[n:] == 255).all()
+
+
 def test_paged_bad_pages_and_lengths():
     cache = Cache((200, 90), 2, 16, 64, seed=4)
     c = Paged((20, 30), cache, 4)
