@@ -213,7 +213,9 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
       // not before the unit in work is near its end: a CTA with a long one would
       // hold the next back from those that run dry
       if (ok && i > 0) ok = wait(B_NEAR, (i - 1) & 1);
-      if (ok && i > 0) {
+      if (ok && i > 0 && a.stride > 0) {
+        u += a.stride;
+      } else if (ok && i > 0) {
         if (lane == 0) {
           mbar_arrive_expect_tx(BAR(B_CANCEL), 16);
           clc_try_cancel(sbase + C::OFF_CANCEL, BAR(B_CANCEL));
@@ -555,7 +557,15 @@ cudaError_t launch_d(const PromptWeightArgs& a, cudaStream_t st) {
   static std::atomic<unsigned char> asked[kMaxSharedMemoryDevices];
   cudaError_t e = ask_shared_memory(reinterpret_cast<const void*>(prompt_weights_kernel<D, PAGED>), C::ALLOC, asked);
   if (e != cudaSuccess) return e;
-  prompt_weights_kernel<D, PAGED><<<(unsigned)ctas, C::THREADS, C::ALLOC, st>>>(a);
+  // A CTA per unit that there can be, most of them taken over. Where a cache's
+  // tables are far wider than its sequences nearly all would find nothing, which
+  // takes each 2 us (8 sequences of 1500 keys in tables of 131072: 383 us): a CTA
+  // per SM goes through the list in strides instead, longest units first.
+  PromptWeightArgs args = a;
+  const int sms = fwd_slots();
+  const bool strides = PAGED && sms > 0 && ctas > 16ll * sms;
+  args.stride = strides ? sms : 0;
+  prompt_weights_kernel<D, PAGED><<<(unsigned)(strides ? sms : ctas), C::THREADS, C::ALLOC, st>>>(args);
   return cudaGetLastError();
 }
 

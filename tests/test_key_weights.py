@@ -146,3 +146,17 @@ def test_refusals():
     for kw in (dict(window=-1), dict(scale=0.0), dict(weights=w[:1].expand(2, 2, 8)), dict(max_seqlen_q=0)):
         with pytest.raises(fa.FAError):
             call(**kw)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_paged_wide_tables(d):
+    """Tables and rows of weights far wider than the sequences."""
+    cache = Cache((900, 0, 129, 2500, 5000), 4, 64, d, seed=d, width_extra=4000)
+    c = Paged((60, 0, 129, 3, 700), cache, 16, seed=d, pad=(2, 3))
+    o, lse = fa.fa_prompt_paged(c.q, cache.k, cache.v, cache.tables, cache.seq_lens, c.cu_q, 700)
+    for window in (0, 20):
+        w = torch.rand((5, 4, cache.tables.shape[1] * 64), device="cuda")
+        before = w.clone()
+        fa.fa_prompt_key_weights_paged(c.q, cache.k, cache.tables, cache.seq_lens, lse, w, c.cu_q, 700, window=window)
+        assert fa.fa_check_device_status() == fa.FA_OK
+        check_weights(c, w, before, lse, 1 / math.sqrt(d), window)
