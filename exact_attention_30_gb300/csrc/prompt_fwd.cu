@@ -103,7 +103,10 @@ __device__ __forceinline__ bool prompt_block(const PromptFwdArgs& a, long long u
   }
   part = (int)(u % k.parts);
   const long long w = u / k.parts;
-  if (w >= (long long)total * a.Hkv) return false;
+  // Offsets that run back and forth can give more blocks than there is room for
+  // among the partial results; with fewer ranges than the host planned, CTAs
+  // enough to reach them. (A sequence whose offsets run back is reported above.)
+  if (w >= min((long long)total, a.max_blocks) * a.Hkv) return false;
   const int hpg = a.heads_per_group;
   const int group = (int)(w / ((long long)total * hpg));
   const int local = (int)(w - (long long)group * total * hpg);

@@ -501,6 +501,9 @@ fa_status fa_decode_shared_plan(int B, int Hq, int Hkv, int Nq, int prefix_len, 
  * On the device: a sequence whose offsets do not lie within the tensors in
  * order, or whose lengths exceed the given bounds, is left out (nothing of it
  * is read or written) and fa_check_device_status returns FA_ERR_INVALID_ARG.
+ * Where offsets run back, so that sequences lie upon one another, what the
+ * call's sequences get is undefined (and reported); nothing is written past
+ * their rows or the workspace.
  * Limits: bf16, d 64 or 128, Hq / Hkv <= 128, totals <= 2^30, B * Hkv <= 2^24.
  * Errors: FA_ERR_INVALID_ARG (pointers, sizes, strides, scale, small
  * workspace), FA_ERR_UNSUPPORTED (FA_F32, d, the limits), FA_ERR_CUDA.
@@ -549,8 +552,8 @@ size_t fa_prompt_bwd_workspace_bytes(int B, int Hq, int Hkv, int total_q, int to
  *   fused projection's gradient will do: three slices of one tensor) or the
  *   inputs. workspace: >= fa_prompt_bwd_workspace_bytes() bytes, 256-byte
  *   aligned, contents on entry irrelevant, not used by another call in flight.
- * Where offsets are not in order, a sequence that is left out gets no
- * gradients, and gradients of sequences that overlap others are undefined.
+ * A sequence that is left out gets no gradients; where sequences lie upon one
+ * another, gradients are undefined, as the results of fa_prompt_fwd.
  * Limits and errors as fa_prompt_fwd, plus Hkv <= 65535, and the workspace's
  * rows, 128 Hkv (total_q / floor(128 / G) + B + 1), below 2^31.
  */
