@@ -503,7 +503,9 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
           if (lane == 0) mbar_arrive(BAR(B_SFREE + 2 * t + odd));
           add(rb, 3);
           ++c;
-          if ((c & 3) == 0) join();
+          // every fourth of the unit's own tiles: which weights are added up together
+          // must not depend on the units that this CTA had before
+          if ((j & 6) == 6) join();
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(B_STEMPTY) + 8 * slot);
