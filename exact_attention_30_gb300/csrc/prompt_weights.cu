@@ -446,6 +446,7 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
         for (int e = 0; e < 4; ++e) sum[e] = 0ull;
         const float y = __fsub_rn(__fadd_rn(sa.x, sa.y), lost), z = __fadd_rn(total, y);
         lost = __fsub_rn(__fsub_rn(z, total), y);
+        if (!(fabsf(lost) < INFINITY)) lost = 0.f;  // an infinite weight stays infinite (inf - inf is NaN)
         total = z;
       };
 #pragma unroll 1

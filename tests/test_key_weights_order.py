@@ -40,3 +40,33 @@ def test_paged_repeats_itself(width_extra):
     for _ in range(11):
         assert torch.equal(run(), first)
     assert fa.fa_check_device_status() == fa.FA_OK
+
+
+@pytest.mark.parametrize("n", [1, 40, 700, 3000])
+@pytest.mark.parametrize("d", [64, 128])
+def test_infinite_weights_stay_infinite(n, d):
+    """Log-sum-exps that are too small by 200: e^200 is past fp32, for a prompt as for a step; keys that no counted
+    token sees with such a one keep their weight."""
+    c = Prompts((n, 65), 8, 2, d, seed=n)
+    _, lse = fa.fa_prompt_fwd(c.q, c.k, c.v, c.cu_q, c.max_q)
+    ref = fa.fa_prompt_key_weights(c.q, c.k, lse, torch.zeros((2, 2, max(n, 65)), device="cuda"), c.cu_q, c.max_q)
+    tok = n // 2
+    lse[:, tok] -= 200  # one token's: the keys up to it
+    w = fa.fa_prompt_key_weights(c.q, c.k, lse, torch.zeros((2, 2, max(n, 65)), device="cuda"), c.cu_q, c.max_q)
+    assert (w[0, :, :tok + 1] == float("inf")).all()
+    assert torch.equal(w[0, :, tok + 1:], ref[0, :, tok + 1:]) and torch.equal(w[1], ref[1])
+
+
+def test_infinite_weights_of_a_step():
+    cache = Cache((700, 90), 2, 64, 128, seed=3)
+    c = Paged((1, 1), cache, 8, seed=4)
+    q = c.q[:, :, None].contiguous()
+    _, lse = fa.fa_decode_paged(q, cache.k, cache.v, cache.tables, cache.seq_lens)
+    lse[0] -= 200
+    w = torch.zeros((2, 2, 700), device="cuda")
+    fa.fa_decode_key_weights(q, cache.k, cache.tables, cache.seq_lens, lse, w, accumulate=False)
+    v = torch.zeros_like(w)
+    fa.fa_prompt_key_weights_paged(c.q, cache.k, cache.tables, cache.seq_lens, lse[..., 0].T.contiguous(), v, c.cu_q, 1,
+                                   accumulate=False)
+    assert (w[0] == float("inf")).all() and (v[0] == float("inf")).all()
+    assert torch.isfinite(w[1]).all() and torch.isfinite(v[1]).all()
