@@ -399,12 +399,12 @@ fa_status fa_kv_evict(const fa_paged_kv* cache, const int* block_tables, int max
   if (!aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(new_tables, 4) || !aligned(new_lens, 4) ||
       !aligned(W, 4) || !aligned(new_W, 4) || !aligned(kept, 4))
     return FA_ERR_INVALID_ARG;
+  if (B > 65535 || cache->kv_heads > 65535 || budget > kPagedMaxKeys) return FA_ERR_UNSUPPORTED;
   const int most = std::min(most_keys(max_pages, cache->page_size), w_keys), keep = std::min(most, budget);
   if (!weight_strides_ok(w_batch_stride, w_head_stride, w_keys, B, cache->kv_heads) ||
       !weight_strides_ok(new_w_batch_stride, new_w_head_stride, keep, B, cache->kv_heads))
     return FA_ERR_INVALID_ARG;
   if ((long long)new_pages * cache->page_size < keep) return FA_ERR_INVALID_ARG;  // no room for what stays
-  if (B > 65535 || cache->kv_heads > 65535 || budget > kPagedMaxKeys) return FA_ERR_UNSUPPORTED;
   a.block_tables = block_tables;
   a.new_tables = new_tables;
   a.seq_lens = seq_lens;
