@@ -625,7 +625,8 @@ fa_status fa_decode_key_weights(const void* Q, const long long* q_strides, const
  *   new_lens   : DEVICE int32 [B], min(seq_lens[b], budget); may be seq_lens.
  *   W          : float32 weights as above, read. new_W: the weights of what stays,
  *          in its order, from element 0 of each row on (strides likewise, rows
- *          must not overlap; the rest of a row is left as it is); may be W.
+ *          must not overlap; the rest of a row is left as it is); may be W, with
+ *          W's strides, and overlaps it in no other way.
  *   kept       : DEVICE int32 [B, Hkv, budget]: the index that each key that stays
  *          had, -1 behind the last one.
  *   budget     : HOST value >= 1; 0 <= recent <= budget.

@@ -4,7 +4,7 @@ import itertools
 import numpy as np
 import pytest
 
-import exact_attention_30_gb300 as fa
+import test_prompt_cpu
 from test_prompt_cpu import FAKE, INVALID, _cache, _evict, _step, _weights, _weights_paged, lib  # noqa: F401
 
 
@@ -38,6 +38,24 @@ def test_far_apart(lib):
     for s in ((1 << 40) + 1, 1 << 62, -(1 << 62)):
         assert _weights(lib, wb=s, wh=200, wk=200) == INVALID
         assert _weights(lib, wb=400, wh=s, wk=200) == INVALID
-    many = dict(B=65535, kept=FAKE, nwb=1 << 20, nwh=64)
+    many = dict(B=65535, kept=FAKE, nw=FAKE + 4096, nwb=1 << 20, nwh=64)
     assert _evict(lib, _cache(kv_heads=1), wb=64, wh=0, **many) != INVALID
     assert _evict(lib, _cache(kv_heads=3), wb=64, wh=65535 * 64 - 1, **many) == INVALID
+
+
+def test_weights_in_place_keep_their_strides(lib):
+    same = dict(nw=FAKE, wk=64, budget=64, recent=8)
+    assert _evict(lib, wb=128, wh=64, nwb=128, nwh=64, **same) != INVALID
+    for nwb, nwh in ((192, 64), (256, 128), (64, 128)):
+        assert _evict(lib, wb=128, wh=64, nwb=nwb, nwh=nwh, **same) == INVALID
+        assert _evict(lib, wb=128, wh=64, nwb=nwb, nwh=nwh, **{**same, "nw": FAKE + 4096}) != INVALID
+    # an axis of one entry has no stride
+    assert _evict(lib, _cache(kv_heads=1), wb=128, wh=1, nwb=128, nwh=99, **same) != INVALID
+    assert _evict(lib, wb=1, wh=64, nwb=99, nwh=64, B=1, **same) != INVALID
+
+
+def test_evict_refusals_with_weights_elsewhere(lib):
+    """Each of the other refusals by itself: the call is in order but for it."""
+    assert _evict(lib, nw=FAKE + 4096) != INVALID
+    for kw, code in test_prompt_cpu.test_evict_refusals.pytestmark[0].args[1]:
+        assert _evict(lib, **{"nw": FAKE + 4096, **kw}) == code, kw
