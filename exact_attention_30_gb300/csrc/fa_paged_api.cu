@@ -405,6 +405,8 @@ fa_status fa_kv_evict(const fa_paged_kv* cache, const int* block_tables, int max
       !weight_strides_ok(new_w_batch_stride, new_w_head_stride, keep, B, cache->kv_heads))
     return FA_ERR_INVALID_ARG;
   if ((long long)new_pages * cache->page_size < keep) return FA_ERR_INVALID_ARG;  // no room for what stays
+  // tables in place: the same rows of the same width
+  if (new_tables == block_tables && B > 1 && new_pages != max_pages) return FA_ERR_INVALID_ARG;
   // weights in place: a row goes to its own place, not to one that another block still reads
   if (W == new_W && ((B > 1 && w_batch_stride != new_w_batch_stride) ||
                      (cache->kv_heads > 1 && w_head_stride != new_w_head_stride)))

@@ -618,10 +618,11 @@ fa_status fa_decode_key_weights(const void* Q, const long long* q_strides, const
  * moves, with its value, to row i mod page_size of page new_tables[b * new_pages
  * + i / page_size]. Keys keep the rotation they were stored with; give
  * fa_kv_append `positions` afterwards.
- *   new_tables : block_tables itself: in place (no page may then be in two
- *          sequences' tables; the pages behind the last key that stays are free
- *          afterwards). Otherwise pages that no old table holds in use, each once;
- *          the old ones are left as they are, and may be shared.
+ *   new_tables : block_tables itself, of max_pages pages (B = 1: or fewer): in
+ *          place (no page may then be in two sequences' tables; the pages behind
+ *          the last key that stays are free afterwards). Otherwise pages that no
+ *          old table holds in use, each once; the old ones are left as they are,
+ *          and may be shared.
  *   new_lens   : DEVICE int32 [B], min(seq_lens[b], budget); may be seq_lens.
  *   W          : float32 weights as above, read. new_W: the weights of what stays,
  *          in its order, from element 0 of each row on (strides likewise, rows

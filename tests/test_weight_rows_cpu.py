@@ -59,3 +59,12 @@ def test_evict_refusals_with_weights_elsewhere(lib):
     assert _evict(lib, nw=FAKE + 4096) != INVALID
     for kw, code in test_prompt_cpu.test_evict_refusals.pytestmark[0].args[1]:
         assert _evict(lib, **{"nw": FAKE + 4096, **kw}) == code, kw
+
+
+def test_tables_in_place_keep_their_width(lib):
+    """[B, pages] rows of another width would be other sequences' pages."""
+    far = dict(nw=FAKE + 4096)
+    assert _evict(lib, max_pages=5, new_pages=4, **far) == INVALID
+    assert _evict(lib, max_pages=4, new_pages=5, **far) == INVALID
+    assert _evict(lib, max_pages=5, new_pages=4, new=FAKE + 4096, **far) != INVALID
+    assert _evict(lib, max_pages=5, new_pages=4, B=1, **far) != INVALID
