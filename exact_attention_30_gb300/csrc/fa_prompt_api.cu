@@ -108,11 +108,13 @@ FwdPlan fwd_plan(int B, int G, int Hkv, int total_q, int max_q, int max_k, int d
 
 // What fa_prompt_fwd and fa_prompt_paged check alike.
 fa_status check_fwd(const void* Q, long long q_stride, const void* O, long long o_stride, const float* LSE,
-                    const int* cu_q, int Hq, int total_q, int d, const void* workspace) {
+                    const int* cu_q, int B, int Hq, int Hkv, int total_q, int max_q, int d, const void* workspace) {
   if (!Q || !O || !LSE || !cu_q) return FA_ERR_INVALID_ARG;
   if (!aligned(Q, 16) || !aligned(O, 16) || !aligned(LSE, 4) || !aligned(cu_q, 4) || !aligned(workspace, 256))
     return FA_ERR_INVALID_ARG;
   if (!token_stride_ok(q_stride, total_q, Hq, d) || !token_stride_ok(o_stride, total_q, Hq, d)) return FA_ERR_INVALID_ARG;
+  // rows of all blocks (key ranges are planned only where there are few)
+  if (most_blocks(B, total_q, max_q, 2 * prompt_tile_tokens(Hq / Hkv)) * Hkv > 0x7fffffff / 256) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
 
@@ -140,7 +142,6 @@ fa_status fwd_launch(PromptFwdArgs& a, const void* Q, long long q_stride, void* 
   a.max_blocks = p.max_blocks;
   a.splits = workspace ? p.splits : 1;
   a.slots = fwd_slots();
-  if (a.max_blocks * a.Hkv * 256 * a.splits > 0x7fffffffll) return FA_ERR_UNSUPPORTED;
   if (a.splits > 1) {
     if (workspace_bytes < p.total) return FA_ERR_INVALID_ARG;
     a.Opart = static_cast<float*>(workspace);
@@ -220,7 +221,7 @@ fa_status fa_prompt_fwd(const void* Q, const void* K, const void* V, long long q
                         void* stream) {
   fa_status s = check_sizes(B, Hq, Hkv, total_q, total_k, max_seqlen_q, max_seqlen_k, d, scale, dt);
   if (s != FA_OK) return s;
-  s = check_fwd(Q, q_stride, O, o_stride, LSE, cu_seqlens_q, Hq, total_q, d, workspace);
+  s = check_fwd(Q, q_stride, O, o_stride, LSE, cu_seqlens_q, B, Hq, Hkv, total_q, max_seqlen_q, d, workspace);
   if (s != FA_OK) return s;
   if (!K || !V || !cu_seqlens_k) return FA_ERR_INVALID_ARG;
   if (!aligned(K, 16) || !aligned(V, 16) || !aligned(cu_seqlens_k, 4)) return FA_ERR_INVALID_ARG;
@@ -259,7 +260,8 @@ fa_status fa_prompt_paged(const void* Q, long long q_stride, const fa_paged_kv* 
   const long long most = std::min<long long>((long long)max_pages * cache->page_size, kPagedMaxKeys);
   s = check_sizes(B, Hq, cache->kv_heads, total_q, (int)most, max_seqlen_q, (int)most, cache->d, scale, dt);
   if (s != FA_OK) return s;
-  s = check_fwd(Q, q_stride, O, o_stride, LSE, cu_seqlens_q, Hq, total_q, cache->d, workspace);
+  s = check_fwd(Q, q_stride, O, o_stride, LSE, cu_seqlens_q, B, Hq, cache->kv_heads, total_q, max_seqlen_q, cache->d,
+                workspace);
   if (s != FA_OK) return s;
   if (!block_tables || !seq_lens || !aligned(block_tables, 4) || !aligned(seq_lens, 4)) return FA_ERR_INVALID_ARG;
   a.Hkv = cache->kv_heads;

@@ -490,7 +490,8 @@ fa_status fa_decode_shared_plan(int B, int Hq, int Hkv, int Nq, int prefix_len, 
  *          their own sequence whose tile reads them, as in a product with
  *          weight zero.
  *   max_seqlen_q, max_seqlen_k : HOST upper bounds of the sequences' tokens and
- *          keys; with total_q they size the launch.
+ *          keys, at least 1 and at most total_q and total_k; with total_q they
+ *          size the launch.
  *   workspace : device scratch of >= fa_prompt_fwd_workspace_bytes() bytes,
  *          256-byte aligned, contents on entry irrelevant, not used by another
  *          call in flight; it lets few queries with many keys be split into key
@@ -504,7 +505,10 @@ fa_status fa_decode_shared_plan(int B, int Hq, int Hkv, int Nq, int prefix_len, 
  * Where offsets run back, so that sequences lie upon one another, what the
  * call's sequences get is undefined (and reported); nothing is written past
  * their rows or the workspace.
- * Limits: bf16, d 64 or 128, Hq / Hkv <= 128, totals <= 2^30, B * Hkv <= 2^24.
+ * Limits: bf16, d 64 or 128, Hq / Hkv <= 128, totals <= 2^30, B * Hkv <= 2^24,
+ * and the rows of all blocks below 2^31: 256 Hkv times total_q / t + B or B
+ * ceil(max_seqlen_q / t), whichever is less, t = 2 floor(128 / (Hq / Hkv))
+ * tokens to a block (sequences of one token: B * Hkv < 2^23).
  * Errors: FA_ERR_INVALID_ARG (pointers, sizes, strides, scale, small
  * workspace), FA_ERR_UNSUPPORTED (FA_F32, d, the limits), FA_ERR_CUDA.
  */
