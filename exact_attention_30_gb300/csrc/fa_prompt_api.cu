@@ -52,6 +52,14 @@ long long most_blocks(int B, int total, int max_len, int per) {
   return std::min(by_total, by_len);
 }
 
+// The longest that a warp may wait for another one. Some wait for a whole block:
+// the scheduler for its end, the output warps for a query tile's last P V. Its
+// `tiles` steps take 0.7 to 1.4 us each, and finding it among B sequences some
+// 0.2 us for each 32 of them and level of the list (24 at most).
+unsigned long long wait_limit(long long tiles, int B) {
+  return std::max(kDefaultWaitLimitNs, 16000ull * (unsigned long long)tiles + 1000ull * (unsigned long long)B);
+}
+
 // Packed queries (or O, dO, dQ): (d, head of the group, token, K/V head).
 bool encode_grouped(CUtensorMap* m, const void* p, long long stride, int G, int Hkv, int total, int tile_tokens, int d) {
   const long long dims[4] = {d, G, total, Hkv}, strides[3] = {d, stride, (long long)G * d};
@@ -135,7 +143,7 @@ fa_status fwd_launch(PromptFwdArgs& a, const void* Q, long long q_stride, void* 
   a.g_div = fast_div((unsigned)G);
   a.heads_per_group = causal_heads_per_group(a.Hkv, key_bytes, 96ll << 20);
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.wait_limit_ns = kDefaultWaitLimitNs;
+  a.wait_limit_ns = wait_limit((a.seqs.max_k + 127) / 128, B);
   a.status = device_status_ptr();
   if (!a.status) return FA_ERR_CUDA;
   const FwdPlan p = fwd_plan(B, G, a.Hkv, total_q, max_q, a.seqs.max_k, d);
@@ -183,7 +191,7 @@ fa_status weights_launch(PromptWeightArgs& a, const void* Q, long long q_stride,
   a.accumulate = flags & FA_ACCUMULATE ? 1 : 0;
   a.heads_per_group = causal_heads_per_group(a.Hkv, 2ll * total_q * a.G * d, 96ll << 20);
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.wait_limit_ns = kDefaultWaitLimitNs;
+  a.wait_limit_ns = wait_limit((max_q + a.tile_tokens - 1) / a.tile_tokens, B);
   a.status = device_status_ptr();
   if (!a.status) return FA_ERR_CUDA;
   if (a.max_units * a.Hkv > 0x7fffffffll) return FA_ERR_UNSUPPORTED;
