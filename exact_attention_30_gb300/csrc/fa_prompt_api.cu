@@ -253,7 +253,8 @@ size_t fa_prompt_fwd_workspace_bytes(int B, int Hq, int Hkv, int total_q, int ma
   if (check_heads(B, Hq, Hkv, d, dt) != FA_OK || total_q < 1 || max_seqlen_q < 1 || max_seqlen_q > total_q ||
       max_seqlen_k < 1)
     return 0;
-  return fwd_plan(B, Hq / Hkv, Hkv, total_q, max_seqlen_q, max_seqlen_k, d).total;
+  // a table can hold more keys than a sequence may have
+  return fwd_plan(B, Hq / Hkv, Hkv, total_q, max_seqlen_q, std::min(max_seqlen_k, kPagedMaxKeys), d).total;
 }
 
 fa_status fa_prompt_paged(const void* Q, long long q_stride, const fa_paged_kv* cache, const int* block_tables,

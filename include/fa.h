@@ -520,8 +520,8 @@ fa_status fa_prompt_fwd(const void* Q, const void* K, const void* V, long long q
 
 /*
  * Scratch bytes with which fa_prompt_fwd (or fa_prompt_paged, max_seqlen_k =
- * max_pages * page_size) splits this problem on the CURRENT device; 0 when it
- * does not (or on invalid arguments).
+ * max_pages * page_size, or 2^30 where that is more) splits this problem on the
+ * CURRENT device; 0 when it does not (or on invalid arguments).
  */
 size_t fa_prompt_fwd_workspace_bytes(int B, int Hq, int Hkv, int total_q, int max_seqlen_q, int max_seqlen_k, int d,
                                      fa_dtype dt);

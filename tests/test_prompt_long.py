@@ -49,3 +49,12 @@ def test_weights_of_the_first_keys_of_a_long_prompt():
     # rounding -LSE * log2(e) moves the exponent by up to 2^-24 * 20.3, the exponential adds 2^-22, the sums 2^-20
     err = ((w[0, 0].double() - ref).abs() / ref).max().item()
     assert err <= 2.0 ** -18, err
+
+
+def test_workspace_of_tables_past_the_longest_sequence():
+    """max_pages * page_size past 2^30 keys plans as 2^30 do, which is what fa_prompt_paged takes of such a table."""
+    for b, hq, hkv, t, d in ((1, 8, 2, 60, 128), (3, 4, 4, 1, 64)):
+        n = fa.fa_prompt_fwd_workspace_bytes(b, hq, hkv, t, t, 1 << 30, d)
+        assert n > 0
+        for keys in ((1 << 30) + 1, (1 << 31) - 128, (1 << 31) - 1):
+            assert fa.fa_prompt_fwd_workspace_bytes(b, hq, hkv, t, t, keys, d) == n
