@@ -372,7 +372,6 @@ struct PromptWeightArgs {
   FastDiv g_div;
   int heads_per_group;
   long long max_units;       // at least as many blocks of 256 keys as all sequences have
-  int stride;                // > 0: CTA c takes units c, c + stride, ..; 0: one, and others that have not begun
   float scale_log2;
   int* status;
   unsigned long long wait_limit_ns;

@@ -84,8 +84,11 @@ struct WUnit {
   int f[kWInts];
 };
 
-// Whole warp: unit `u` of the list; false past the last one.
-__device__ __forceinline__ bool weight_unit(const PromptWeightArgs& a, long long u, int lane, bool report, WUnit& k) {
+// Whole warp: the units of grid index `u` are `per` neighbours in the list (one,
+// unless the grid is smaller than the list): unit `sub` of them; false past the
+// last one of all.
+__device__ __forceinline__ bool weight_unit(const PromptWeightArgs& a, long long u, int sub, int lane, bool report, int& per,
+                                            WUnit& k) {
   bool bad = false;
   auto span = [&](int b) {
     const PromptView v = prompt_view(a.seqs, b, bad);
@@ -97,7 +100,10 @@ __device__ __forceinline__ bool weight_unit(const PromptWeightArgs& a, long long
   int top;
   const int total = count_blocks(a.seqs.B, lane, span, first, top);
   if (report && bad) report_status(a.status, kStatusBadSeqlens);
-  if (u >= (long long)total * a.Hkv) return false;
+  const long long units = (long long)total * a.Hkv;
+  per = units > gridDim.x ? (int)((units + gridDim.x - 1) / gridDim.x) : 1;
+  u = u * per + sub;
+  if (u >= units) return false;
   const int hpg = a.heads_per_group;
   const int group = (int)(u / ((long long)total * hpg));
   const int local = (int)(u - (long long)group * total * hpg);
@@ -206,28 +212,36 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
 
   if (warp == 2) {
     // ---------------------------------------------------------- scheduler
-    long long u = blockIdx.x;
+    long long u = blockIdx.x;  // grid index in work, -1 past the last unit
+    int sub = 0, per = 1;      // its unit in work, and units
+    int asked = 0;             // questions for a CTA that has not begun
+    auto take_over = [&](int& next) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(BAR(B_CANCEL), 16);
+        clc_try_cancel(sbase + C::OFF_CANCEL, BAR(B_CANCEL));
+      }
+      if (!wait(B_CANCEL, asked & 1)) return false;
+      ++asked;
+      next = clc_next_cta(sbase + C::OFF_CANCEL);
+      fence_proxy_async_smem();
+      __syncwarp();
+      return true;
+    };
+    int next = 0;
     for (int i = 0; ok && u >= 0; ++i) {
       const int s = i % C::IRING;
       if (i >= C::IRING) ok = wait(B_ITE + s, ((i / C::IRING) - 1) & 1);
       // not before the unit in work is near its end: a CTA with a long one would
       // hold the next back from those that run dry
       if (ok && i > 0) ok = wait(B_NEAR, (i - 1) & 1);
-      if (ok && i > 0 && a.stride > 0) {
-        u += a.stride;
-      } else if (ok && i > 0) {
-        if (lane == 0) {
-          mbar_arrive_expect_tx(BAR(B_CANCEL), 16);
-          clc_try_cancel(sbase + C::OFF_CANCEL, BAR(B_CANCEL));
-        }
-        ok = wait(B_CANCEL, (i - 1) & 1);
-        if (ok) u = clc_next_cta(sbase + C::OFF_CANCEL);
-        fence_proxy_async_smem();
-        __syncwarp();
+      if (ok && i > 0 && ++sub == per) {
+        sub = 0;
+        ok = take_over(next);
+        u = next;
       }
       if (!ok) break;
       WUnit k;
-      if (u >= 0 && !weight_unit(a, u, lane, u == 0, k)) u = -1;
+      if (u >= 0 && !weight_unit(a, u, sub, lane, u == 0 && sub == 0, per, k)) u = -1;
       if (lane == 0) {
         volatile int* d = items + s * C::ITEM_INTS;
 #pragma unroll
@@ -236,6 +250,9 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
       }
       __syncwarp();
     }
+    // What has not begun finds nothing either: taken over here, where that takes
+    // a question, rather than begun, which takes 1.3 us on an SM of its own.
+    while (ok && next >= 0) ok = take_over(next);
   } else if (warp == 0) {
     // ---------------------------------------------------------- producer
     const int nbox = PAGED ? 128 / a.box_rows : 1;
@@ -561,14 +578,15 @@ cudaError_t launch_d(const PromptWeightArgs& a, cudaStream_t st) {
   cudaError_t e = ask_shared_memory(reinterpret_cast<const void*>(prompt_weights_kernel<D, PAGED>), C::ALLOC, asked);
   if (e != cudaSuccess) return e;
   // A CTA per unit that there can be, most of them taken over. Where a cache's
-  // tables are far wider than its sequences nearly all would find nothing, which
-  // takes each 2 us (8 sequences of 1500 keys in tables of 131072: 383 us): a CTA
-  // per SM goes through the list in strides instead, longest units first.
-  PromptWeightArgs args = a;
+  // tables are far wider than its sequences nearly all would find nothing: 24 to an
+  // SM then, which share the list out among them in runs of neighbours. 8 sequences
+  // of 1500 keys in tables of 131072, 64 tokens: 24 us, 410 with a CTA for each unit
+  // that there could be. With fewer CTAs the runs of long lists leave a tail: 16
+  // whole prompts of 1000 to 20000 tokens in full tables 2530 us, 2940 with 16 to an
+  // SM, or with one that goes through the list in strides.
   const int sms = fwd_slots();
-  const bool strides = PAGED && sms > 0 && ctas > 16ll * sms;
-  args.stride = strides ? sms : 0;
-  prompt_weights_kernel<D, PAGED><<<(unsigned)(strides ? sms : ctas), C::THREADS, C::ALLOC, st>>>(args);
+  const long long most = PAGED && sms > 0 ? 24ll * sms : ctas;
+  prompt_weights_kernel<D, PAGED><<<(unsigned)(ctas < most ? ctas : most), C::THREADS, C::ALLOC, st>>>(a);
   return cudaGetLastError();
 }
 

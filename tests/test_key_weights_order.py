@@ -4,7 +4,7 @@ import torch
 
 import exact_attention_30_gb300 as fa
 from paged_utils import Cache
-from prompt_utils import Paged, Prompts, offsets
+from prompt_utils import Paged, Prompts, check_weights, offsets
 
 pytestmark = pytest.mark.gpu
 
@@ -40,6 +40,21 @@ def test_paged_repeats_itself(width_extra):
     for _ in range(11):
         assert torch.equal(run(), first)
     assert fa.fa_check_device_status() == fa.FA_OK
+
+
+@pytest.mark.parametrize("width_extra", [0, 100])
+def test_more_units_than_ctas(width_extra):
+    """3712 units of 256 keys in full tables, several to a CTA index; some sequences have none."""
+    lens = [300 if b % 30 else 0 for b in range(120)]
+    cache = Cache(lens, 16, 64, 64, seed=5, width_extra=width_extra)
+    cache.poison()
+    c = Paged([3 if m else 0 for m in lens], cache, 16, seed=6)
+    _, lse = fa.fa_prompt_paged(c.q, cache.k, cache.v, cache.tables, cache.seq_lens, c.cu_q, 3)
+    w = torch.rand((120, 16, cache.tables.shape[1] * 64), device="cuda")
+    before = w.clone()
+    fa.fa_prompt_key_weights_paged(c.q, cache.k, cache.tables, cache.seq_lens, lse, w, c.cu_q, 3)
+    assert fa.fa_check_device_status() == fa.FA_OK
+    check_weights(c, w, before, lse, 1 / 8)
 
 
 @pytest.mark.parametrize("n", [1, 40, 700, 3000])
