@@ -85,8 +85,9 @@ struct WUnit {
 };
 
 // Whole warp: the units of grid index `u` are `per` neighbours in the list (one,
-// unless the grid is smaller than the list): unit `sub` of them; false past the
-// last one of all.
+// unless the grid is smaller than the list, as over pages): unit `sub` of them;
+// false past the last one of all.
+template <bool PAGED>
 __device__ __forceinline__ bool weight_unit(const PromptWeightArgs& a, long long u, int sub, int lane, bool report, int& per,
                                             WUnit& k) {
   bool bad = false;
@@ -101,8 +102,10 @@ __device__ __forceinline__ bool weight_unit(const PromptWeightArgs& a, long long
   const int total = count_blocks(a.seqs.B, lane, span, first, top);
   if (report && bad) report_status(a.status, kStatusBadSeqlens);
   const long long units = (long long)total * a.Hkv;
-  per = units > gridDim.x ? (int)((units + gridDim.x - 1) / gridDim.x) : 1;
-  u = u * per + sub;
+  if constexpr (PAGED) {
+    per = units > gridDim.x ? (int)((units + gridDim.x - 1) / gridDim.x) : 1;
+    u = u * per + sub;
+  }
   if (u >= units) return false;
   const int hpg = a.heads_per_group;
   const int group = (int)(u / ((long long)total * hpg));
@@ -234,14 +237,14 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
       // not before the unit in work is near its end: a CTA with a long one would
       // hold the next back from those that run dry
       if (ok && i > 0) ok = wait(B_NEAR, (i - 1) & 1);
-      if (ok && i > 0 && ++sub == per) {
+      if (ok && i > 0 && (!PAGED || ++sub == per)) {
         sub = 0;
         ok = take_over(next);
         u = next;
       }
       if (!ok) break;
       WUnit k;
-      if (u >= 0 && !weight_unit(a, u, sub, lane, u == 0 && sub == 0, per, k)) u = -1;
+      if (u >= 0 && !weight_unit<PAGED>(a, u, sub, lane, u == 0 && sub == 0, per, k)) u = -1;
       if (lane == 0) {
         volatile int* d = items + s * C::ITEM_INTS;
 #pragma unroll
@@ -252,7 +255,8 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
     }
     // What has not begun finds nothing either: taken over here, where that takes
     // a question, rather than begun, which takes 1.3 us on an SM of its own.
-    while (ok && next >= 0) ok = take_over(next);
+    if constexpr (PAGED)
+      while (ok && next >= 0) ok = take_over(next);
   } else if (warp == 0) {
     // ---------------------------------------------------------- producer
     const int nbox = PAGED ? 128 / a.box_rows : 1;
