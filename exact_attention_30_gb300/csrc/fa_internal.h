@@ -313,7 +313,7 @@ struct PromptFwdArgs {
   int slots;                 // CTAs that the GPU runs at once
   float* Opart;              // splits > 1: fp32 [Hkv * max_blocks][splits][256][d], normalised
   float* Lpart;              // and base-2 log-sum-exps
-  int4* blocks;              // and of each block: first packed token, tokens from there on, K/V head
+  int4* blocks;              // and of each block: first packed token, tokens from there on, K/V head, key ranges
   float scale_log2;
   int* status;
   unsigned long long wait_limit_ns;

@@ -375,7 +375,8 @@ void evict_split(int B, int Hkv, int d, int budget, bool in_place, int sms, int*
 }
 
 cudaError_t launch_kv_evict(const EvictArgs& args, cudaStream_t st) {
-  // threads by the longest sequence that the rows can hold: up to 32 weights each
+  // threads by the longest sequence that the rows can hold: up to 16 weights each
+  // with 256, up to 52 with 1024; past shared memory a form that holds none
   EvictArgs a = args;
   const int most = a.most_keys < a.w_keys ? a.most_keys : a.w_keys;
   a.held_words = (most + 3) / 4 * 4;

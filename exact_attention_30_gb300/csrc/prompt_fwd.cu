@@ -46,7 +46,7 @@
 // P V; with d = 64 three S buffers in turn take that out of the chain (1000 TFLOP/s
 // without, 1190 with), and S and P V are issued by a warp each (1200, 1260 with
 // loops of few instructions). Times in a batch: 16 prompts of 128 to 7821 tokens (32
-// heads on 8, d = 128) 980 us, one of 32768 tokens 5.1 ms, the next turns of six
+// heads on 8, d = 128) 960 to 1020 us by the box, one of 32768 tokens 4.95 to 5.2 ms, the next turns of six
 // chats (d = 64, pages of 32 keys) 83 us, one of 37 tokens 12.5 us.
 #include <cuda.h>
 #include <cuda_bf16.h>

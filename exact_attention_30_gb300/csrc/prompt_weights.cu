@@ -16,20 +16,21 @@
 // buffered in tensor memory for each key tile (four buffers of 128 columns).
 //
 // Products and exponentials need 1024 cycles a unit and query tile each (8192
-// FLOP and 32 exponentials per cycle and SM). Measured: 1790 (8 prompts of 361 to
-// 6925 tokens, 32 heads on 8: 452 us; the last 64 tokens of six of 5627 to 18982:
-// 45 us, of which most is the beginning and end of units of two query tiles). The
-// products alone took 1530, the weights' warps issue 300 instructions for 32 keys
-// and 64 queries where 140 do the sum, each wait takes a hundred cycles even when
-// it is over. So a warp takes whole query tiles in turn with its twin (halves of
+// FLOP and 32 exponentials per cycle and SM). Measured: 1900 by the tensor pipe's
+// share (8 prompts of 361 to 6925 tokens, 32 heads on 8: 452 us; the last 64 tokens
+// of six of 5627 to 18982: 44 us, of which most is the beginning and end of units of
+// two query tiles). The products alone took 1530, an SM's warps issue 470
+// instructions for 32 keys and 128 query rows where 280 do the sum, each wait takes
+// a hundred cycles even when it is over. So a warp takes whole query tiles in turn with its twin (halves of
 // each: 493 us), and statistics and scores are awaited at once (503 us one after
 // the other). Other ways that were slower: keys as first operands in tensor memory,
 // which leaves three S buffers for both tiles (2400); four keys to a thread, by
 // loads of 16 lanes, which need a quarter of the statistics (2150); loads of 16
 // columns (2040).
 //
-// Sums: 128 weights of four query tiles in each of eight fp32 accumulators, and
-// their sums with a compensation term (Kahan's), in a fixed order.
+// Sums: 64 weights, 16 of each of four query tiles, in each of eight fp32
+// accumulators, and their sums with a compensation term (Kahan's), in an order that
+// a unit's own tiles decide.
 //
 // Warps 0: producer, 1: MMA issuer, 2: scheduler, 3: statistics, 4-19: weights,
 // four warps to the even and to the odd query tiles of each key tile (with
@@ -57,7 +58,7 @@ struct WCfg {
   static constexpr int OFF_Q = OFF_K + 4 * TILE;
   static constexpr int OFF_STAT = OFF_Q + QS * TILE;  // [QS][128] -LSE * log2(e)
   static constexpr int IRING = 3, ITEM_INTS = 12;  // units published ahead (short ones: many)
-  static constexpr int OFF_PART = OFF_STAT + QS * 512;  // [2 tiles][128] sums of the second column halves
+  static constexpr int OFF_PART = OFF_STAT + QS * 512;  // [2 tiles][128] sums over the odd query tiles
   static constexpr int OFF_BARS = OFF_PART + 2 * 512;
   // k_full[2], k_empty[2], q_full[QS], q_empty[QS], st_full[QS], st_empty[QS], s_full[2][2], s_free[2][2],
   // part_full[2], part_free[2], item_full, item_empty [IRING each], cancel, near, drain
@@ -443,7 +444,7 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
     const uint32_t s_addr = tmem + ((uint32_t)(wq * 32) << 16) + C::S_COL(t, odd);
     const uint64_t c22 = f2_pack(a.scale_log2, a.scale_log2);
     // The loop over query tiles is bound by the instructions it issues: 280 for
-    // 128 columns of 32 keys, and what comes on top. So ring positions are counted,
+    // the sum over 128 columns of 32 keys, and what comes on top. So ring positions are counted,
     // not divided out, masks are rare, and sums are joined only every fourth tile.
     uint32_t slot = odd, slot_phase = 0;  // ring position of this warp's next query tile
     int g0 = 0;                           // query tiles before the unit

@@ -137,8 +137,6 @@ __device__ __forceinline__ bool wait_warp2(uint32_t bar, uint32_t parity, uint32
          (wait_warp(bar, parity, status, limit_ns) && wait_warp(bar2, parity2, status, limit_ns));
 }
 
-// Make generic-proxy writes to shared memory visible to the async proxy
-// (TMA / tensor core operand reads).
 // Registers per thread of this warpgroup, fewer or more than at launch (all of
 // its warps; what the block's warpgroups ask for must add up to the launch's).
 template <int N>
@@ -170,6 +168,8 @@ __device__ __forceinline__ bool named_bar_and(int count, bool pred) {
       : "memory");
   return r != 0;
 }
+// Make generic-proxy writes to shared memory visible to the async proxy
+// (TMA / tensor core operand reads).
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }

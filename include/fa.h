@@ -635,11 +635,12 @@ fa_status fa_decode_key_weights(const void* Q, const long long* q_strides, const
  *   kept       : DEVICE int32 [B, Hkv, budget]: the index that each key that stays
  *          had, -1 behind the last one.
  *   budget     : HOST value >= 1; 0 <= recent <= budget.
- * new_pages pages must hold min(budget, w_keys, max_pages pages) keys. B <= 65535. On
+ * new_pages pages must hold min(budget, w_keys, max_pages pages) keys. On
  * the device: a sequence whose length is negative, past max_pages pages or past
  * w_keys is left as it is (kept -1, new_lens as seq_lens), and, like a page outside
  * the pool (whose rows are not moved), reported by fa_check_device_status.
- * Errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED (FA_F32, d, page_size, B), FA_ERR_CUDA.
+ * Errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED (FA_F32, d, page_size; B or
+ * kv_heads > 65535, budget > 2^30), FA_ERR_CUDA.
  */
 fa_status fa_kv_evict(const fa_paged_kv* cache, const int* block_tables, int max_pages, const int* seq_lens,
                       const int* new_tables, int new_pages, int* new_lens, const float* W, long long w_batch_stride,
