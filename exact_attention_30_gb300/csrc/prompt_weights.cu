@@ -21,12 +21,12 @@
 // of six of 5627 to 18982: 44 us, of which most is the beginning and end of units of
 // two query tiles). The products alone took 1530, an SM's warps issue 470
 // instructions for 32 keys and 128 query rows where 280 do the sum, each wait takes
-// a hundred cycles even when it is over. So a warp takes whole query tiles in turn with its twin (halves of
-// each: 493 us), and statistics and scores are awaited at once (503 us one after
-// the other). Other ways that were slower: keys as first operands in tensor memory,
-// which leaves three S buffers for both tiles (2400); four keys to a thread, by
-// loads of 16 lanes, which need a quarter of the statistics (2150); loads of 16
-// columns (2040).
+// a hundred cycles even when it is over. So a warp takes whole query tiles in turn
+// with its twin (halves of each: 493 us), and statistics and scores are awaited at
+// once (503 us one after the other). Other ways that were slower: keys as first
+// operands in tensor memory, which leaves three S buffers for both tiles (2400);
+// four keys to a thread, by loads of 16 lanes, which need a quarter of the
+// statistics (2150); loads of 16 columns (2040).
 //
 // Sums: 64 weights, 16 of each of four query tiles, in each of eight fp32
 // accumulators, and their sums with a compensation term (Kahan's), in an order that
@@ -444,8 +444,8 @@ __global__ void __launch_bounds__(640, 1) prompt_weights_kernel(const __grid_con
     const uint32_t s_addr = tmem + ((uint32_t)(wq * 32) << 16) + C::S_COL(t, odd);
     const uint64_t c22 = f2_pack(a.scale_log2, a.scale_log2);
     // The loop over query tiles is bound by the instructions it issues: 280 for
-    // the sum over 128 columns of 32 keys, and what comes on top. So ring positions are counted,
-    // not divided out, masks are rare, and sums are joined only every fourth tile.
+    // the sum over 128 columns of 32 keys, and what comes on top. So ring positions are
+    // counted, not divided out, masks are rare, and sums are joined only every fourth tile.
     uint32_t slot = odd, slot_phase = 0;  // ring position of this warp's next query tile
     int g0 = 0;                           // query tiles before the unit
     int c = 0;                            // S tiles of this warp so far
